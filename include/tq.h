@@ -302,6 +302,97 @@ TQ_API tq_status tq_multi_token_attention(const tq_cache *cache, const void *q, 
 TQ_API int tq_attention_supported(int32_t head_dim, int32_t k_bits, int32_t v_bits, int32_t group_size);
 
 /*
+ * Paged caches.  A pool is an ordinary tq_cache whose `batch` is the number of
+ * pages and whose `capacity` is the page size P (rows per page, a multiple of
+ * 16): page p of kv-head h is rows [0, P) of (p, h) in every plane, so the row
+ * calls (tq_cache_copy_rows, tq_cache_clear_rows, on a view of one page) move
+ * pages as well.  A page table says where the rows of the sequences of one
+ * batch are: row t of sequence s is row t % P of page pages[s][t / P].
+ *
+ * New tokens are ragged: the tokens of sequence s are rows [starts[s],
+ * starts[s + 1]) of the token tensors, and they are the last starts[s + 1] -
+ * starts[s] rows of the sequence, i.e. token row t stands at position
+ *   seq_lens[s] - (starts[s + 1] - starts[s]) + (t - starts[s]).
+ * A sequence may have no new tokens, and no rows at all.  Token rows from
+ * starts[num_seqs] on belong to no sequence (a batch padded to a fixed size):
+ * they are not read, and outputs there are left as they were.
+ *
+ * The table, the lengths and the starts are device memory, so one captured
+ * graph serves changing batches; the host sees only the bounds max_len,
+ * max_new and total.  The kernels check what they read: a page number outside
+ * the pool ORs TQ_DEVICE_ERR_PAGE into the device error word, a length outside
+ * [0, max_len], starts out of order or outside [0, total], or more new tokens
+ * than max_new ORs TQ_DEVICE_ERR_LENGTH, and results of the sequences
+ * concerned are unspecified; nothing outside the pool and the outputs is ever
+ * touched.  A token that stands before its sequence's first row (more new
+ * tokens than rows) is not appended, reads back as zeros and attends to
+ * nothing (zeros).  Two sequences may share pages that neither appends to;
+ * rows appended by one call must not share a place.
+ */
+typedef struct tq_page_table {
+    const int32_t *pages;     /* device [num_seqs][stride] */
+    const int32_t *seq_lens;  /* device [num_seqs]: rows, the new tokens included */
+    int64_t stride;           /* pages between table rows; stride * P >= max_len */
+    int64_t max_len;          /* bound of seq_lens, 1 .. 2^31 - 1 */
+    int32_t num_seqs;         /* >= 1 */
+    int32_t reserved;         /* must be 0 */
+} tq_page_table;
+
+/*
+ * Paged append: quantise the new tokens' K and V (as tq_encode_append does,
+ * bit for bit) into their rows; no other row is written.
+ *  starts    device int32 [num_seqs + 1]; total = rows of k and v.
+ *  k, v      device bf16, element [token][h][j] at token * s[0] + h * s[1] + j
+ *            (strides in elements); pointers 16-byte aligned, strides
+ *            multiples of 8.
+ * total = 0 is a no-op.
+ */
+TQ_API tq_status tq_paged_append(const tq_cache *pool, const tq_page_table *table, const int32_t *starts, int64_t total,
+                                 const void *k, const int64_t k_strides[2], const void *v, const int64_t v_strides[2],
+                                 tq_stream_t stream);
+
+/*
+ * Paged fetch: the last starts[s + 1] - starts[s] rows of every sequence back
+ * as K and V (as tq_decode gives them, bit for bit), [total][H][d]
+ * contiguous, bf16 or fp32; starts of the new tokens give the rows just
+ * appended, running sums of the lengths whole windows.  Either output may be
+ * NULL.  Outputs 32-byte aligned.  total = 0 is a no-op.
+ */
+TQ_API tq_status tq_paged_decode(const tq_cache *pool, const tq_page_table *table, const int32_t *starts, int64_t total,
+                                 tq_dtype out_dtype, void *k_out, void *v_out, tq_stream_t stream);
+
+/* Workspace bytes tq_paged_attention needs for these bounds (0 if invalid);
+ * the table's device arrays are not read. */
+TQ_API size_t tq_paged_attention_workspace_bytes(const tq_cache *pool, const tq_page_table *table, int32_t q_heads,
+                                                 int64_t total, int64_t max_new);
+
+/*
+ * Paged attention: causal attention of the new tokens over the rows of their
+ * sequences, appended first (tq_paged_append with the same starts):
+ *   out[t][h] = sum_{j <= pos(t)} softmax_j(q[t][h] . k_hat[j][h/G] * softmax_scale) v_hat[j][h/G]
+ * One token per sequence is a decode step, a few are verification, many a
+ * prefill chunk; one call takes any mix.
+ *  starts    device int32 [num_seqs + 1]; total = rows of q and out; no
+ *            sequence has more than max_new new tokens.
+ *  q         device bf16, element [token][head][j] at token * s[0] + head *
+ *            s[1] + j; 16-byte aligned, strides multiples of 8.
+ *  out       device bf16 [total][q_heads][d] contiguous, 16-byte aligned:
+ *            rounded once, from fp32 sums.
+ *  workspace device scratch of at least tq_paged_attention_workspace_bytes()
+ *            for these bounds, 256-byte aligned, not initialised.  Calls that
+ *            may run at the same time (other streams, graphs replayed
+ *            together) need one each.
+ * Scores and sums are fp32; keys, values and probabilities enter the tensor
+ * cores as f16 (11 bits), which costs less than the output's rounding.  A
+ * row of the cache that a token does not see never reaches its output,
+ * whatever it holds (NaN and infinities included).  total = 0 is a no-op.
+ */
+TQ_API tq_status tq_paged_attention(const tq_cache *pool, const tq_page_table *table, const int32_t *starts,
+                                    int64_t total, int64_t max_new, const void *q, const int64_t q_strides[2],
+                                    int32_t q_heads, float softmax_scale, void *out, void *workspace,
+                                    size_t workspace_bytes, tq_stream_t stream);
+
+/*
  * Device-side error word.  Kernels that wait on asynchronous copies give up
  * after a bounded number of polls and record a non-zero code here instead of
  * hanging.  tq_device_error() synchronises the device, copies the word into
@@ -311,6 +402,10 @@ TQ_API tq_status tq_device_error(uint32_t *host_code);
 
 /* Code a bounded wait that gave up ORs into the device error word. */
 #define TQ_DEVICE_ERR_WAIT_TIMEOUT 1u
+
+/* Codes of the paged calls: a page number outside the pool; a length or a start out of range. */
+#define TQ_DEVICE_ERR_PAGE 2u
+#define TQ_DEVICE_ERR_LENGTH 4u
 
 /*
  * Failure-path check (no counterpart in the pages): launches one warp that

@@ -26,6 +26,8 @@ __all__ = [
     "tq_decode_values_rotated", "tq_unrotate", "tq_cache_copy_rows", "tq_cache_clear_rows",
     "tq_multi_token_workspace_bytes", "tq_multi_token_attention", "tq_check_wait_timeout",
     "TQ_DEVICE_ERR_WAIT_TIMEOUT", "TQ_DEFAULT_SIGN_SEED",
+    "PageTable", "tq_paged_append", "tq_paged_decode", "tq_paged_attention", "tq_paged_attention_workspace_bytes",
+    "TQ_DEVICE_ERR_PAGE", "TQ_DEVICE_ERR_LENGTH",
 ]
 
 HEAD_DIMS = (64, 128, 256, 512)
@@ -33,6 +35,8 @@ K_BITS = (2, 4, 5, 8)
 V_BITS = (2, 3, 4, 5, 8)
 TQ_BF16, TQ_F32 = 0, 1
 TQ_DEVICE_ERR_WAIT_TIMEOUT = 1  # device error word: a bounded wait gave up
+TQ_DEVICE_ERR_PAGE = 2  # a paged call met a page number outside the pool
+TQ_DEVICE_ERR_LENGTH = 4  # ... a length, or starts, out of range
 TQ_DEFAULT_SIGN_SEED = 42  # the codec's sign-vector seed unless a cache states another
 
 EXPORTS = (
@@ -40,7 +44,8 @@ EXPORTS = (
     "tq_encode_append", "tq_decode", "tq_attention_workspace_bytes", "tq_decode_attention",
     "tq_attention_supported", "tq_device_error", "tq_decode_attention_noalloc", "tq_decode_values_rotated",
     "tq_unrotate", "tq_cache_copy_rows", "tq_cache_clear_rows", "tq_multi_token_workspace_bytes",
-    "tq_multi_token_attention", "tq_check_wait_timeout",
+    "tq_multi_token_attention", "tq_check_wait_timeout", "tq_paged_append", "tq_paged_decode",
+    "tq_paged_attention_workspace_bytes", "tq_paged_attention",
 )
 
 
@@ -60,8 +65,16 @@ class _CacheStruct(ctypes.Structure):
     ]
 
 
+class _PageTableStruct(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("stride", ctypes.c_int64),
+        ("max_len", ctypes.c_int64), ("num_seqs", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _CP = ctypes.POINTER(_CacheStruct)
+_TP = ctypes.POINTER(_PageTableStruct)
 
 
 def library_path() -> str:
@@ -97,9 +110,15 @@ def lib() -> ctypes.CDLL:
     so.tq_multi_token_workspace_bytes.restype = _SZ
     so.tq_multi_token_workspace_bytes.argtypes = [_CP, _I32, _I64, _I64]
     so.tq_multi_token_attention.argtypes = [_CP, _P, _I32, _I64, _I64, ctypes.c_float, _P, _P, _SZ, _P]
+    two = ctypes.POINTER(_I64)
+    so.tq_paged_append.argtypes = [_CP, _TP, _P, _I64, _P, two, _P, two, _P]
+    so.tq_paged_decode.argtypes = [_CP, _TP, _P, _I64, ctypes.c_int, _P, _P, _P]
+    so.tq_paged_attention_workspace_bytes.restype = _SZ
+    so.tq_paged_attention_workspace_bytes.argtypes = [_CP, _TP, _I32, _I64, _I64]
+    so.tq_paged_attention.argtypes = [_CP, _TP, _P, _I64, _I64, _P, two, _I32, ctypes.c_float, _P, _P, _SZ, _P]
     for name in EXPORTS:
         if name not in ("tq_status_string", "tq_bytes_per_token_head", "tq_attention_workspace_bytes",
-                        "tq_attention_supported", "tq_multi_token_workspace_bytes"):
+                        "tq_attention_supported", "tq_multi_token_workspace_bytes", "tq_paged_attention_workspace_bytes"):
             getattr(so, name).restype = ctypes.c_int
     so.tq_attention_supported.restype = ctypes.c_int
     return so
@@ -145,6 +164,25 @@ class Cache:
         self.v_codes = torch.zeros(*shape, head_dim * v_bits // 8, dtype=torch.uint8, **kw)
         self.v_scale = torch.zeros(*shape, g, dtype=torch.int16, **kw)
 
+    @classmethod
+    def from_planes(cls, k_codes, k_scale, k_zero, v_codes, v_scale, head_dim: int, k_bits: int = 8, v_bits: int = 3,
+                    sign_seed: int = TQ_DEFAULT_SIGN_SEED) -> "Cache":
+        """A cache over planes that the caller owns, [batch][H][capacity][row] contiguous each
+        (codes uint8, scales and zeros any 16-bit type); capacity a multiple of 16."""
+        d, g = int(head_dim), int(head_dim) // 32
+        lead = tuple(k_codes.shape[:3])
+        rows = dict(k_codes=(k_codes, d * k_bits // 8, 1), k_scale=(k_scale, g, 2), k_zero=(k_zero, g, 2),
+                    v_codes=(v_codes, d * v_bits // 8, 1), v_scale=(v_scale, g, 2))
+        c = cls.__new__(cls)
+        for name, (t, row, size) in rows.items():
+            if tuple(t.shape) != lead + (row,) or t.element_size() != size or not t.is_contiguous() or \
+                    t.device != k_codes.device:
+                raise ValueError(f"{name} must be contiguous [batch][H][capacity][{row}] of {size}-byte elements on one device")
+            setattr(c, name, t)
+        c.batch, c.num_kv_heads, c.capacity = (int(x) for x in lead)
+        c.head_dim, c.k_bits, c.v_bits, c.sign_seed = d, int(k_bits), int(v_bits), int(sign_seed)
+        return c
+
     def planes(self):
         return self.k_codes, self.k_scale, self.k_zero, self.v_codes, self.v_scale
 
@@ -163,6 +201,36 @@ class Cache:
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in self.planes())
+
+
+class PageTable:
+    """Where the rows of a batch's sequences are in a pool (a Cache whose batch counts pages and
+    whose capacity is the page size): pages int32 [num_seqs][max pages], seq_lens int32
+    [num_seqs] (rows, new tokens included), both on the pool's device, and the host's bound
+    max_len of the lengths (default: all that the table's pages hold).  The tensors are read by
+    every call, so writing to them changes the batch, captured graphs included."""
+
+    def __init__(self, pages: torch.Tensor, seq_lens: torch.Tensor, max_len: int | None = None,
+                 page_size: int | None = None):
+        if pages.dtype != torch.int32 or pages.dim() != 2 or (pages.shape[1] > 1 and pages.stride(1) != 1):
+            raise ValueError("pages must be int32 [num_seqs][pages], a sequence's pages contiguous")
+        if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (pages.shape[0],) or not seq_lens.is_contiguous():
+            raise ValueError("seq_lens must be contiguous int32 [num_seqs]")
+        if max_len is None and page_size is None:
+            raise ValueError("give max_len, or page_size to bound the lengths by the table's pages")
+        _require_cuda(pages, seq_lens)
+        self.pages, self.seq_lens = pages, seq_lens
+        self.num_seqs = int(pages.shape[0])
+        self.max_len = int(pages.shape[1]) * int(page_size) if max_len is None else int(max_len)
+
+    def struct(self, pool: "Cache") -> _PageTableStruct:
+        if self.pages.shape[1] * pool.capacity < self.max_len:
+            raise ValueError(f"{self.pages.shape[1]} pages of {pool.capacity} rows do not hold max_len = {self.max_len}")
+        # a table of one sequence has no row to step to: its stride is its pages
+        stride = self.pages.stride(0) if self.num_seqs > 1 else self.pages.shape[1]
+        if stride < self.pages.shape[1]:
+            raise ValueError("the rows of the page table overlap")
+        return _PageTableStruct(self.pages.data_ptr(), self.seq_lens.data_ptr(), stride, self.max_len, self.num_seqs, 0)
 
 
 # ------------------------------------------------------------------ host-side queries
@@ -365,6 +433,100 @@ def tq_multi_token_attention(cache: Cache, q: torch.Tensor, seq_len: int, softma
     _check(lib().tq_multi_token_attention(ctypes.byref(s), q.data_ptr(), int(QH), int(M), int(seq_len), scale,
                                           out.data_ptr(), ws_ptr, ws_bytes, _stream(stream)),
            "tq_multi_token_attention")
+    return out
+
+
+def _empty_on(stream, shape, dtype, device):
+    """Memory for a call on `stream`, taken from that stream's share of the allocator, so that it is
+    not handed on before the call's kernels are through with it."""
+    if stream is None or int(_stream(stream)) == torch.cuda.current_stream().cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _paged_args(pool: Cache, table: PageTable, starts: torch.Tensor, *tensors):
+    """Checks shared by the paged calls: the starts' form, and one device, the current one, for all."""
+    if starts.dtype != torch.int32 or tuple(starts.shape) != (table.num_seqs + 1,) or not starts.is_contiguous():
+        raise ValueError("starts must be contiguous int32 [num_seqs + 1]")
+    _require_cuda(pool.k_codes, starts, *tensors)
+    dev = pool.k_codes.device
+    if any(t is not None and t.device != dev for t in (table.pages, table.seq_lens, starts, *tensors)):
+        raise ValueError("the pool, the page table and the tensors must be on one device")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError("the tensors are on another device than the current one")
+    return pool.struct(), table.struct(pool)
+
+
+def _ragged_strides(x: torch.Tensor, heads: int | None, d: int, what: str):
+    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[2] != d or (heads is not None and x.shape[1] != heads) or \
+            (d > 1 and x.stride(2) != 1):
+        raise ValueError(f"{what} must be bfloat16 [tokens][heads][head_dim] with head_dim contiguous, matching the pool")
+    return (_I64 * 2)(x.stride(0), x.stride(1))
+
+
+def tq_paged_append(pool: Cache, table: PageTable, starts: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    stream=None) -> None:
+    """Quantise the new tokens' K, V (bf16 [tokens][H][d], any token and head strides) into the pages
+    of their sequences; sequence s owns token rows [starts[s], starts[s + 1]), its last rows."""
+    s, t = _paged_args(pool, table, starts, k, v)
+    if k.shape != v.shape:
+        raise ValueError("K and V must have the same shape")
+    ks, vs = (_ragged_strides(x, pool.num_kv_heads, pool.head_dim, "K and V") for x in (k, v))
+    _check(lib().tq_paged_append(ctypes.byref(s), ctypes.byref(t), starts.data_ptr(), int(k.shape[0]), k.data_ptr(), ks,
+                                 v.data_ptr(), vs, _stream(stream)), "tq_paged_append")
+
+
+def tq_paged_decode(pool: Cache, table: PageTable, starts: torch.Tensor, total: int, dtype=torch.bfloat16,
+                    want_k: bool = True, want_v: bool = True, k_out: torch.Tensor | None = None,
+                    v_out: torch.Tensor | None = None, stream=None):
+    """The last starts[s + 1] - starts[s] rows of every sequence as (K, V), [total][H][d] of `dtype`."""
+    code = _dtype_code(dtype)
+    shape = (int(total), pool.num_kv_heads, pool.head_dim)
+    dev = pool.k_codes.device
+    if want_k and k_out is None:
+        k_out = _empty_on(stream, shape, dtype, dev)
+    if want_v and v_out is None:
+        v_out = _empty_on(stream, shape, dtype, dev)
+    k_out, v_out = (k_out if want_k else None), (v_out if want_v else None)
+    for x in (k_out, v_out):
+        if x is not None and (x.dtype != dtype or tuple(x.shape) != shape or not x.is_contiguous()):
+            raise ValueError("decode outputs must be contiguous [total][H][d] of the requested dtype")
+    s, t = _paged_args(pool, table, starts, k_out, v_out)
+    _check(lib().tq_paged_decode(ctypes.byref(s), ctypes.byref(t), starts.data_ptr(), int(total), code,
+                                 k_out.data_ptr() if want_k else None, v_out.data_ptr() if want_v else None,
+                                 _stream(stream)), "tq_paged_decode")
+    return k_out, v_out
+
+
+def tq_paged_attention_workspace_bytes(pool: Cache, table: PageTable, q_heads: int, total: int, max_new: int) -> int:
+    s, t = pool.struct(), table.struct(pool)
+    return int(lib().tq_paged_attention_workspace_bytes(ctypes.byref(s), ctypes.byref(t), int(q_heads), int(total),
+                                                        int(max_new)))
+
+
+def tq_paged_attention(pool: Cache, table: PageTable, starts: torch.Tensor, q: torch.Tensor, max_new: int,
+                       softmax_scale: float | None = None, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of the new tokens (q bf16 [tokens][QH][d], any token and head strides; at most
+    max_new of one sequence) over their sequences' rows -> bf16 [tokens][QH][d]."""
+    qs = _ragged_strides(q, None, pool.head_dim, "q")
+    total, QH, d = q.shape
+    if out is None:
+        out = _empty_on(stream, (total, QH, d), torch.bfloat16, q.device)
+    if out.dtype != torch.bfloat16 or tuple(out.shape) != (total, QH, d) or not out.is_contiguous():
+        raise ValueError("out must be contiguous bfloat16, shaped like q")
+    if workspace is None and total > 0:
+        need = tq_paged_attention_workspace_bytes(pool, table, QH, total, max_new)
+        workspace = _empty_on(stream, need, torch.uint8, q.device)
+    s, t = _paged_args(pool, table, starts, q, out, workspace)
+    scale = (1.0 / d ** 0.5) if softmax_scale is None else float(softmax_scale)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().tq_paged_attention(ctypes.byref(s), ctypes.byref(t), starts.data_ptr(), int(total), int(max_new),
+                                    q.data_ptr(), qs, int(QH), scale, out.data_ptr(),
+                                    workspace.data_ptr() if workspace is not None else None, ws_bytes,
+                                    _stream(stream)), "tq_paged_attention")
     return out
 
 

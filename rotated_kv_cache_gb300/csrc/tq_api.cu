@@ -385,6 +385,117 @@ tq_status tq_decode_attention_noalloc(const tq_cache *c, const void *q, int32_t 
                                                     scale, out, (cudaStream_t)stream));
 }
 
+namespace {
+tq_status check_table(const tq_cache *c, const tq_page_table *t)
+{
+    if (!t || !t->pages || !t->seq_lens) return TQ_ERR_NULL;
+    if (t->num_seqs < 1 || t->num_seqs >= (1 << 30) || t->reserved != 0) return TQ_ERR_SHAPE;
+    if (t->max_len < 1 || t->max_len > INT32_MAX || t->stride < 1) return TQ_ERR_SHAPE;
+    if (t->stride < (t->max_len + c->capacity - 1) / c->capacity) return TQ_ERR_CAPACITY;
+    return TQ_OK;
+}
+
+tq_status check_paged(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total)
+{
+    tq_status st = check_cache(c);
+    if (st != TQ_OK) return st;
+    st = check_table(c, t);
+    if (st != TQ_OK) return st;
+    if (!starts) return TQ_ERR_NULL;
+    return total < 0 || total > INT32_MAX ? TQ_ERR_SHAPE : TQ_OK;
+}
+
+// strides of a ragged [token][head][d] tensor
+tq_status check_ragged(const void *x, const int64_t s[2])
+{
+    if (!x || !s) return TQ_ERR_NULL;
+    if (s[0] < 0 || s[1] < 0) return TQ_ERR_SHAPE;
+    return !aligned16(x) || s[0] % 8 != 0 || s[1] % 8 != 0 ? TQ_ERR_ALIGN : TQ_OK;
+}
+
+tq_status check_paged_attention(const tq_cache *c, const tq_page_table *t, int32_t q_heads, int64_t total, int64_t max_new)
+{
+    if (q_heads < 1 || q_heads % c->num_kv_heads != 0 || max_new < 1 || total < 0) return TQ_ERR_SHAPE;
+    // rows of out, and units of work, fit the kernels' indices
+    if (total > (int64_t(1) << 30) / q_heads) return TQ_ERR_SHAPE;
+    return (int64_t)t->num_seqs * c->num_kv_heads > (int64_t(1) << 30) ? TQ_ERR_SHAPE : TQ_OK;
+}
+
+tq::PagedView paged_view(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total)
+{
+    tq::PagedView v{};
+    v.pages = t->pages;
+    v.lens = t->seq_lens;
+    v.starts = starts;
+    v.stride = t->stride;
+    v.max_len = t->max_len;
+    v.total = total;
+    v.seqs = t->num_seqs;
+    v.num_pages = c->batch;
+    v.page = (uint32_t)c->capacity;
+    v.div_page = tq::make_fastdiv(v.page);
+    v.err = tq::device_error_word();
+    return v;
+}
+}  // namespace
+
+tq_status tq_paged_append(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total, const void *k,
+                          const int64_t ks[2], const void *v, const int64_t vs[2], tq_stream_t stream)
+{
+    tq_status st = check_paged(c, t, starts, total);
+    if (st != TQ_OK || total == 0) return st;
+    if ((st = check_ragged(k, ks)) != TQ_OK || (st = check_ragged(v, vs)) != TQ_OK) return st;
+    const tq::PagedView pv = paged_view(c, t, starts, total);
+    if (!pv.err) return TQ_ERR_CUDA;
+    return cuda_status(tq::launch_paged_append(view(c), pv, static_cast<const uint16_t *>(k), ks,
+                                               static_cast<const uint16_t *>(v), vs, (cudaStream_t)stream));
+}
+
+tq_status tq_paged_decode(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total, tq_dtype dt,
+                          void *k_out, void *v_out, tq_stream_t stream)
+{
+    tq_status st = check_paged(c, t, starts, total);
+    if (st != TQ_OK) return st;
+    if (dt != TQ_BF16 && dt != TQ_F32) return TQ_ERR_SHAPE;
+    if (total == 0 || (!k_out && !v_out)) return TQ_OK;
+    if ((k_out && !aligned32(k_out)) || (v_out && !aligned32(v_out))) return TQ_ERR_ALIGN;
+    const tq::PagedView pv = paged_view(c, t, starts, total);
+    if (!pv.err) return TQ_ERR_CUDA;
+    return cuda_status(tq::launch_paged_decode(view(c), pv, dt == TQ_F32, k_out, v_out, (cudaStream_t)stream));
+}
+
+size_t tq_paged_attention_workspace_bytes(const tq_cache *c, const tq_page_table *t, int32_t q_heads, int64_t total,
+                                          int64_t max_new)
+{
+    if (check_cache(c) != TQ_OK || check_table(c, t) != TQ_OK) return 0;
+    if (check_paged_attention(c, t, q_heads, total, max_new) != TQ_OK) return 0;
+    if (max_new > total) max_new = total > 0 ? total : 1;
+    return tq::paged_attention_workspace_bytes(view(c), t->num_seqs, t->max_len, total, max_new, q_heads);
+}
+
+tq_status tq_paged_attention(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total,
+                             int64_t max_new, const void *q, const int64_t qs[2], int32_t q_heads, float scale, void *out,
+                             void *ws, size_t ws_bytes, tq_stream_t stream)
+{
+    tq_status st = check_paged(c, t, starts, total);
+    if (st != TQ_OK) return st;
+    if ((st = check_paged_attention(c, t, q_heads, total, max_new)) != TQ_OK) return st;
+    if (total == 0) return TQ_OK;
+    if ((st = check_ragged(q, qs)) != TQ_OK) return st;
+    if (!out) return TQ_ERR_NULL;
+    if (!aligned16(out)) return TQ_ERR_ALIGN;
+    if (max_new > total) max_new = total;
+    const tq::CacheView cv = view(c);
+    const size_t need = tq::paged_attention_workspace_bytes(cv, t->num_seqs, t->max_len, total, max_new, q_heads);
+    if (need == 0) return TQ_ERR_CUDA;  // the occupancy query failed
+    if (!ws || ws_bytes < need) return TQ_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return TQ_ERR_ALIGN;
+    const tq::PagedView pv = paged_view(c, t, starts, total);
+    if (!pv.err) return TQ_ERR_CUDA;
+    return cuda_status(tq::launch_paged_attention(cv, pv, static_cast<const uint16_t *>(q), qs, q_heads, max_new, scale,
+                                                  static_cast<uint16_t *>(out), ws, ws_bytes, (cudaStream_t)stream));
+}
+
 tq_status tq_check_wait_timeout(tq_stream_t stream)
 {
     uint32_t *err = tq::device_error_word();

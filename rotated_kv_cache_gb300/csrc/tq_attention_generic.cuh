@@ -37,6 +37,7 @@
 
 #include "tq_common.cuh"
 #include "tq_kernels.h"
+#include "tq_paged.cuh"
 
 namespace tq {
 namespace {
@@ -62,6 +63,7 @@ struct GenParams {
     int off_ks, off_kz, off_vs, off_v, stage_bytes, key_bytes;
     float scale_log2, koff;                        // softmax scale * log2(e); f16 offset of a key code
     uint16_t cen[256];                             // value centroids as f16 bits
+    PagedSplit pg;                                 // paged launches (partials [slot][CB][D], [slot][CB][2])
 };
 
 __device__ __forceinline__ void g_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -248,12 +250,16 @@ struct GGeo {
     static constexpr int MIN_BLOCKS = D >= 512 ? 1 : (D * NB / 4 <= 32 ? 6 : 4);
 };
 
+// PAGED: the CTA runs the segments of its share of a paged batch one after
+// another (tq_paged.cuh) instead of the grid's (split, column block, sequence);
+// stages arrive chunk by chunk, a chunk lying within a page, each lane of the
+// refilling warp copying one.
 // VLUT: how value codes become f16 centroids.  0: a shared-memory table; 3 or
 // 2: 3- or 2-bit values looked up with byte permutes in registers.  KEY: how
 // key codes are cut (key_pairs).  Separate instantiations: the same choices made
 // at run time inside one kernel cost more than they saved (the larger unrolled
 // body).
-template <int D, int NB, int VLUT, int KEY>
+template <int D, int NB, int VLUT, int KEY, bool PAGED = false>
 __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     attn_generic_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ GenParams p)
 {
@@ -278,18 +284,55 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     const uint32_t full0 = smem_addr(bars);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = blockIdx.x, h = blockIdx.y / p.HB, hb = blockIdx.y - h * p.HB, b = blockIdx.z;
+    PagedWalk walk;
+    if constexpr (PAGED) {
+        if (!walk.start(p.pg, gT, CB, p.H, p.G, lane)) return;
+    }
+    bool ok = true;
+    int it0 = 0;  // stages this CTA has been through before this segment (ring slots and parities run on)
+    bool more = false;
+    do {
+    if constexpr (PAGED) walk.segment(p.pg);
+    const int split = blockIdx.x, h = PAGED ? walk.h : blockIdx.y / p.HB, hb = PAGED ? walk.hb : blockIdx.y - h * p.HB,
+              b = blockIdx.z;
     const int64_t bh = (int64_t)b * p.H + h;
+    const int M = PAGED ? (int)walk.n : p.M, cols = PAGED ? (int)walk.n * p.G : p.cols;
+    const int64_t base0 = PAGED ? walk.len - walk.n + 1 : p.base0;
     // columns col0 .. col0 + CB - 1; column col is query row col / G, q-head
     // h G + col % G; query row i sees cache rows [0, base0 + i)
     const int col0 = hb * CB;
-    const int col_last = (p.cols < col0 + CB ? p.cols : col0 + CB) - 1;
-    const int64_t lim_lo = p.base0 + col0 / p.G, lim_hi = p.base0 + col_last / p.G;
-    const int64_t t_begin = (int64_t)split * p.tokens_per_split;
-    const int64_t t_end = imin64(lim_hi, t_begin + p.tokens_per_split);
-    const int n_stages = t_end > t_begin ? (int)((t_end - t_begin + gT - 1) / gT) : 0;
+    const int col_last = (cols < col0 + CB ? cols : col0 + CB) - 1;
+    const int64_t lim_lo = base0 + col0 / p.G, lim_hi = base0 + col_last / p.G;
+    const int64_t t_begin = PAGED ? (int64_t)walk.first * gT : (int64_t)split * p.tokens_per_split;
+    const int64_t t_end = imin64(lim_hi, t_begin + (PAGED ? (int64_t)walk.count * gT : p.tokens_per_split));
+    const int n_stages = t_end > t_begin && ok ? (int)((t_end - t_begin + gT - 1) / gT) : 0;
     const int NG = D / 32;
+    PagedPages<gT> pages;
 
+    // paged: every lane of the warp calls, with the plane row of its chunk
+    auto issue_paged = [&](int s, int64_t row) {
+        const int slot = (it0 + s) % p.stages, ru = gT / pages.nch;
+        const int live = (int)((imin64(gT, t_end - (t_begin + (int64_t)s * gT)) + ru - 1) / ru);  // chunks with rows to read
+        const uint32_t kst = smem_addr(stages + slot * p.key_bytes), bar = full0 + 8 * slot;
+        const uint32_t st = smem_addr(stages + p.stages * p.key_bytes + slot * p.stage_bytes);
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(live * ru * (p.rbk + p.rbv + 3 * NG * 2)));
+        __syncwarp();
+        if (lane < live) {
+            const int at = lane * ru;
+            if constexpr (KEY != 0) {
+                using K = KSwz<D, KEY>;
+#pragma unroll
+                for (int j = 0; j < K::NBOX; ++j)
+                    g_tma_2d(kst + j * gT * K::BOXB + at * K::BOXB, &kmap, j * K::BOXB, (int)row, bar);
+            } else {
+                bulk_g2s(kst + at * p.rbk, p.k_codes + row * p.rbk, ru * p.rbk, bar);
+            }
+            bulk_g2s(st + p.off_ks + at * (NG * 2), p.k_scale + row * NG, ru * NG * 2, bar);
+            bulk_g2s(st + p.off_kz + at * (NG * 2), p.k_zero + row * NG, ru * NG * 2, bar);
+            bulk_g2s(st + p.off_vs + at * (NG * 2), p.v_scale + row * NG, ru * NG * 2, bar);
+            bulk_g2s(st + p.off_v + at * p.rbv, p.v_codes + row * p.rbv, ru * p.rbv, bar);
+        }
+    };
     auto issue = [&](int s) {
         const int slot = s % p.stages;
         const int64_t t = t_begin + (int64_t)s * gT;
@@ -313,13 +356,22 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
         bulk_g2s(st + p.off_vs, p.v_scale + row0 * NG, rows * NG * 2, bar);
         bulk_g2s(st + p.off_v, p.v_codes + row0 * p.rbv, rows * p.rbv, bar);
     };
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && (!PAGED || !more)) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full0 + 8 * s, 1);
             done[s] = 0;
         }
         fence_mbar_init();
-        for (int s = 0; s < p.stages && s < n_stages; ++s) issue(s);
+        if constexpr (!PAGED)
+            for (int s = 0; s < p.stages && s < n_stages; ++s) issue(s);
+    }
+    if constexpr (PAGED) {
+        pages.start(p.pg, walk, p.H, walk.first, lane);
+        __syncwarp();
+        for (int s = 0; s < p.stages && s < n_stages; ++s) {
+            const int64_t row = pages.rows(p.pg, walk, p.H, walk.first + s, lane);
+            if (warp == 0) issue_paged(s, row);
+        }
     }
     if constexpr (VLUT == 0)
         for (int i = threadIdx.x; i < (1 << p.vb); i += blockDim.x) lut[i] = p.cen[i];
@@ -333,9 +385,10 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     for (int u = warp; u < NB * (gN / 2); u += A::W) {
         const int n = (u / (gN / 2)) * gN + 2 * (u % (gN / 2)) + (lane >> 4), l16 = lane & 15;
         const int col = col0 + n;
-        const bool real = col < p.cols;
+        const bool real = col < cols;
         const int qi = real ? col / p.G : 0, qw = real ? col - qi * p.G : 0;
-        const uint16_t *qrow = p.q + (((int64_t)b * p.M + qi) * p.QH + (int64_t)h * p.G + qw) * D;
+        const uint16_t *qrow = PAGED ? p.q + (walk.s0 + qi) * p.pg.q_token + ((int64_t)h * p.G + qw) * p.pg.q_head
+                                     : p.q + (((int64_t)b * M + qi) * p.QH + (int64_t)h * p.G + qw) * D;
         float qv[D / 64][4];
         float mx = 0.0f;
 #pragma unroll
@@ -432,10 +485,10 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     constexpr int QF_NB = gN * A::QCOL;  // bytes of q fragments per block of 8 columns
     const uint32_t qf_lane = smem_addr(qf) + g * A::QCOL + c * 8, lut_a = smem_addr(lut);
 
-    bool ok = true;
-    for (int s = 0; s < n_stages; ++s) {
-        const int slot = s % p.stages;
-        if (!mbar_wait_bounded(full0 + 8 * slot, (s / p.stages) & 1, p.err)) {
+    int s = 0;
+    for (; s < n_stages; ++s) {
+        const int slot = (it0 + s) % p.stages;
+        if (!mbar_wait_bounded(full0 + 8 * slot, ((it0 + s) / p.stages) & 1, p.err)) {
             ok = false;
             break;
         }
@@ -524,13 +577,13 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
         for (int t2 = 0; t2 < A::TILES; ++t2) {
             const int64_t tt0 = tile_t0 + TR * t2;
             if (tt0 + 16 > lim_lo) {
-                const int64_t ta = tt0 + g - p.base0, tb = ta + 8;
+                const int64_t ta = tt0 + g - base0, tb = ta + 8;
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int col = col0 + nb * gN + 2 * c + j;
-                        const int64_t qi = col < p.cols ? col / p.G : p.M - 1;
+                        const int64_t qi = col < cols ? col / p.G : M - 1;
                         if (ta >= qi) S[t2][nb][0][j] = -INFINITY;
                         if (tb >= qi) S[t2][nb][1][j] = -INFINITY;
                     }
@@ -603,6 +656,23 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) vlive[t2][q] = tile_t0 + TR * t2 + (vr[q] - 16 * warp) < t_end;
+        }
+        // paged: the rows that the lane's column (g of each block) sees, as masks of the
+        // f16 weights of tokens vr[0], vr[1] and vr[2], vr[3]
+        uint32_t seen[A::TILES][NB][2];
+        if constexpr (PAGED) {
+#pragma unroll
+            for (int t2 = 0; t2 < A::TILES; ++t2)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    seen[t2][nb][0] = seen[t2][nb][1] = 0xFFFFFFFFu;
+                    if (M > 1 && tile_t0 + TR * t2 + 16 > lim_lo) {
+                        const int col = col0 + nb * gN + g;
+                        const int64_t lim = base0 + (col < cols ? col / p.G : M - 1) - (tile_t0 + TR * t2 - 16 * warp);
+                        seen[t2][nb][0] = (vr[0] < lim ? 0xFFFFu : 0u) | (vr[1] < lim ? 0xFFFF0000u : 0u);
+                        seen[t2][nb][1] = (vr[2] < lim ? 0xFFFFu : 0u) | (vr[3] < lim ? 0xFFFF0000u : 0u);
+                    }
+                }
         }
         // ---------------- O^T += V^T (P * rms)^T, group by group, both tiles; the
         // value fragments serve every block of columns
@@ -680,7 +750,11 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
                 }
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    const uint32_t b0 = g_hmul2(pt0[t2][nb], sv01), b1 = g_hmul2(pt1[t2][nb], sv23);
+                    uint32_t b0 = g_hmul2(pt0[t2][nb], sv01), b1 = g_hmul2(pt1[t2][nb], sv23);
+                    if constexpr (PAGED) {  // a hidden row's rms may be anything, its weight stays zero
+                        b0 &= seen[t2][nb][0];
+                        b1 &= seen[t2][nb][1];
+                    }
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
                         g_mma(o[nb][2 * G + half], a[half][0], a[half][1], a[half][2], a[half][3], b0, b1);
@@ -688,7 +762,16 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
             }
         }
         __syncwarp();
-        if (lane == 0) {
+        if constexpr (PAGED) {
+            const int64_t row = pages.rows(p.pg, walk, p.H, walk.first + s + p.stages, lane);
+            uint32_t last = 0;
+            if (lane == 0) {
+                __threadfence_block();
+                last = atomicAdd(&done[slot], 1u) == A::W - 1;
+                if (last) done[slot] = 0;
+            }
+            if (__shfl_sync(0xffffffffu, last, 0) && s + p.stages < n_stages) issue_paged(s + p.stages, row);
+        } else if (lane == 0) {
             __threadfence_block();
             if (atomicAdd(&done[slot], 1u) == A::W - 1) {
                 done[slot] = 0;
@@ -696,7 +779,15 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
             }
         }
     }
-    __syncthreads();
+    if constexpr (PAGED) {
+        // after a wait that gave up: the copies still in flight (bounded), and no further stage
+        if (!ok)
+            for (int r = s + 1; r < s + p.stages && r < n_stages; ++r)
+                mbar_wait_bounded(full0 + 8 * ((it0 + r) % p.stages), ((it0 + r) / p.stages) & 1, p.err);
+        ok = __syncthreads_and(ok);
+    } else {
+        __syncthreads();
+    }
 
     // ---------------------------------------------------------------- merge the warps
     float *mw = merge + warp * CB * (D + 2);  // [column][D] o, then [column] m, [column] l
@@ -732,6 +823,7 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     const int d0 = (threadIdx.x & 15) * PER;
 #pragma unroll 1
     for (int hh = threadIdx.x >> 4; hh < CB; hh += A::THREADS / 16) {
+        if (PAGED && walk.slot >= p.pg.slots) break;  // starts out of order make more units than there can be
         float mmax = -INFINITY;
 #pragma unroll
         for (int w = 0; w < A::W; ++w) mmax = fmaxf(mmax, merge[w * CB * (D + 2) + CB * D + hh]);
@@ -747,7 +839,7 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
 #pragma unroll
             for (int i = 0; i < PER; ++i) ov[i] += m2[hh * D + d0 + i] * wt;
         }
-        const int64_t pidx = ((bh * p.HB + hb) * p.splits + split) * CB + hh;
+        const int64_t pidx = (PAGED ? walk.slot : (bh * p.HB + hb) * p.splits + split) * CB + hh;
         float4 *dst = reinterpret_cast<float4 *>(p.part_o + pidx * D + d0);
 #pragma unroll
         for (int i = 0; i < PER / 4; ++i) dst[i] = make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
@@ -756,6 +848,15 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
             p.part_ml[2 * pidx + 1] = lsum;
         }
     }
+    if constexpr (PAGED) {
+        more = walk.next(p.pg, gT, CB, p.H, p.G);
+        it0 += n_stages;
+        if (more) {  // the next segment's copies land where the merge was read and written
+            fence_proxy_async_smem();
+            __syncthreads();
+        }
+    }
+    } while (PAGED && more);
 }
 
 // ---------------------------------------------------------------- combine + deferred un-rotation
@@ -939,24 +1040,25 @@ inline int gen_nb(int d, int64_t cols)
 }
 
 // Calls f with the kernel instantiation the plan's VLUT and KEY name.
-template <int D, int NB, int VLUT, typename F>
+template <int D, int NB, int VLUT, bool PAGED, typename F>
 auto gen_dispatch_key(const GenPlan &pl, F &&f)
 {
-    return pl.key == 8 ? f(attn_generic_kernel<D, NB, VLUT, 8>)
-           : pl.key == 4 ? f(attn_generic_kernel<D, NB, VLUT, 4>)
-                         : f(attn_generic_kernel<D, NB, VLUT, 0>);
+    return pl.key == 8 ? f(attn_generic_kernel<D, NB, VLUT, 8, PAGED>)
+           : pl.key == 4 ? f(attn_generic_kernel<D, NB, VLUT, 4, PAGED>)
+                         : f(attn_generic_kernel<D, NB, VLUT, 0, PAGED>);
 }
 
-template <int D, int NB, typename F>
+template <int D, int NB, bool PAGED = false, typename F>
 auto gen_dispatch(const GenPlan &pl, F &&f)
 {
-    return pl.vlut == 3   ? gen_dispatch_key<D, NB, 3>(pl, f)
-           : pl.vlut == 2 ? gen_dispatch_key<D, NB, 2>(pl, f)
-                          : gen_dispatch_key<D, NB, 0>(pl, f);
+    return pl.vlut == 3   ? gen_dispatch_key<D, NB, 3, PAGED>(pl, f)
+           : pl.vlut == 2 ? gen_dispatch_key<D, NB, 2, PAGED>(pl, f)
+                          : gen_dispatch_key<D, NB, 0, PAGED>(pl, f);
 }
 
-template <int D, int NB>
-bool gen_plan_nb(const CacheView &c, int q_heads, int64_t m, int64_t seq_len, GenPlan &pl)
+// Stage layout, instantiation and shared memory of a plan; resident CTAs per SM (0 on failure).
+template <int D, int NB, bool PAGED>
+int gen_layout(const CacheView &c, GenPlan &pl)
 {
     using A = GGeo<D, NB>;
     const int NG = D / 32, rbk = D * c.kb / 8, rbv = D * c.vb / 8;
@@ -976,13 +1078,20 @@ bool gen_plan_nb(const CacheView &c, int q_heads, int64_t m, int64_t seq_len, Ge
                                                                            : A::MERGE;
     pl.smem = 1024 /*align slack*/ + ring + A::QF + A::QS + (pl.vlut == 0 ? 512 : 0) /*lut*/ +
               gMaxStages * 12 /*barriers, counters*/;
-    const int per_sm = gen_dispatch<D, NB>(pl, [&](auto kern) {
+    return gen_dispatch<D, NB, PAGED>(pl, [&](auto kern) {
         int n = 0;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem) != cudaSuccess) return 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, GGeo<D, NB>::THREADS, pl.smem) != cudaSuccess)
             return 0;
         return n;
     });
+}
+
+template <int D, int NB>
+bool gen_plan_nb(const CacheView &c, int q_heads, int64_t m, int64_t seq_len, GenPlan &pl)
+{
+    using A = GGeo<D, NB>;
+    const int per_sm = gen_layout<D, NB, false>(c, pl);
     if (per_sm < 1) return false;
     const int64_t cols = (int64_t)(q_heads / c.H) * m;
     pl.hb = (int)((cols + A::CB - 1) / A::CB);
@@ -1018,24 +1127,24 @@ bool gen_plan(const CacheView &c, int q_heads, int64_t m, int64_t seq_len, GenPl
     return false;
 }
 
-template <int D, int NB>
+template <int D, int NB, bool PAGED = false>
 cudaError_t gen_launch(const GenPlan &pl, dim3 grid, const CUtensorMap &kmap, const GenParams &p, cudaStream_t s)
 {
-    return gen_dispatch<D, NB>(
+    return gen_dispatch<D, NB, PAGED>(
         pl, [&](auto kern) { return launch_dependent(kern, grid, dim3(GGeo<D, NB>::THREADS), (size_t)pl.smem, s, kmap, p); });
 }
 
 // Tensor map over the key plane for the swizzled key tiles of 8- and 4-bit
-// keys: [B H cap rows][row bytes], boxes of BOXB bytes x gT rows.
+// keys: [B H cap rows][row bytes], boxes of BOXB bytes x box_rows rows.
 template <int D>
-bool gen_key_map(const CacheView &c, CUtensorMap *map)
+bool gen_key_map(const CacheView &c, CUtensorMap *map, int box_rows = gT)
 {
     auto fn = tensor_map_encoder();
     if (!fn) return false;
     const int rb = D * c.kb / 8, boxb = rb < 128 ? rb : 128;
     const cuuint64_t gdim[2] = {(cuuint64_t)rb, (cuuint64_t)c.B * c.H * c.cap};
     const cuuint64_t gstride[1] = {(cuuint64_t)rb};
-    const cuuint32_t box[2] = {(cuuint32_t)boxb, (cuuint32_t)gT};
+    const cuuint32_t box[2] = {(cuuint32_t)boxb, (cuuint32_t)box_rows};
     const cuuint32_t estride[2] = {1, 1};
     const CUtensorMapSwizzle sw = boxb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                   : boxb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
@@ -1052,41 +1161,24 @@ size_t gen_workspace(const CacheView &c, int q_heads, int64_t m, int64_t seq_len
     return (size_t)c.B * c.H * pl.hb * pl.splits * gN * pl.nb * (D + 2) * 4;
 }
 
+// The parameters that go by the cache and the plan alone.
 template <int D>
-cudaError_t gen_run(const CacheView &c, const uint16_t *q, int QH, int64_t m, int64_t seq_len, float scale, float *out,
-                    void *ws, size_t ws_bytes, cudaStream_t s)
+bool gen_params(const CacheView &c, const GenPlan &pl, const uint16_t *q, int QH, float scale, GenParams &p)
 {
-    GenPlan pl;
-    if (!gen_plan<D>(c, QH, m, seq_len, pl)) return cudaErrorInvalidConfiguration;
-    const int G = QH / c.H, CB = gN * pl.nb;
-    const size_t parts = (size_t)c.B * c.H * pl.hb * pl.splits * CB;
-    const size_t need_o = parts * D * 4;
-    if (ws_bytes < need_o + parts * 2 * 4) return cudaErrorInvalidValue;
-    GenParams p{};
     p.k_codes = c.k_codes;
     p.v_codes = c.v_codes;
     p.k_scale = c.k_scale;
     p.k_zero = c.k_zero;
     p.v_scale = c.v_scale;
     p.q = q;
-    p.part_o = static_cast<float *>(ws);
-    p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + need_o);
     p.err = device_error_word();
-    if (!p.err) return cudaErrorInvalidDevice;
     p.H = c.H;
     p.QH = QH;
-    p.G = G;
-    p.M = (int)m;
-    p.cols = G * (int)m;
-    p.HB = pl.hb;
-    p.splits = pl.splits;
+    p.G = QH / c.H;
     p.kb = c.kb;
     p.vb = c.vb;
     p.stages = pl.stages;
     p.cap = c.cap;
-    p.seq_len = seq_len;
-    p.tokens_per_split = pl.tokens_per_split;
-    p.base0 = seq_len - m + 1;
     p.rbk = D * c.kb / 8;
     p.rbv = D * c.vb / 8;
     p.off_ks = pl.off_ks;
@@ -1099,6 +1191,30 @@ cudaError_t gen_run(const CacheView &c, const uint16_t *q, int QH, int64_t m, in
     p.koff = c.kb == 8 ? 1152.0f : 1024.0f;
     const Tables &tab = codebook_tables(c.vb);
     for (int i = 0; i < (1 << c.vb); ++i) p.cen[i] = __half_as_ushort(__float2half_rn(tab.centroids[i]));
+    return p.err != nullptr;
+}
+
+template <int D>
+cudaError_t gen_run(const CacheView &c, const uint16_t *q, int QH, int64_t m, int64_t seq_len, float scale, float *out,
+                    void *ws, size_t ws_bytes, cudaStream_t s)
+{
+    GenPlan pl;
+    if (!gen_plan<D>(c, QH, m, seq_len, pl)) return cudaErrorInvalidConfiguration;
+    const int G = QH / c.H, CB = gN * pl.nb;
+    const size_t parts = (size_t)c.B * c.H * pl.hb * pl.splits * CB;
+    const size_t need_o = parts * D * 4;
+    if (ws_bytes < need_o + parts * 2 * 4) return cudaErrorInvalidValue;
+    GenParams p{};
+    if (!gen_params<D>(c, pl, q, QH, scale, p)) return cudaErrorInvalidDevice;
+    p.part_o = static_cast<float *>(ws);
+    p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + need_o);
+    p.M = (int)m;
+    p.cols = G * (int)m;
+    p.HB = pl.hb;
+    p.splits = pl.splits;
+    p.seq_len = seq_len;
+    p.tokens_per_split = pl.tokens_per_split;
+    p.base0 = seq_len - m + 1;
     if ((int64_t)c.H * pl.hb > 65535 || c.B > 65535) return cudaErrorInvalidValue;
     CUtensorMap kmap{};
     if (pl.key != 0 && !gen_key_map<D>(c, &kmap)) return cudaErrorInvalidValue;
@@ -1114,6 +1230,51 @@ cudaError_t gen_run(const CacheView &c, const uint16_t *q, int QH, int64_t m, in
     GenCombineParams cp{p.part_o, p.part_ml, out, c.H, QH, G, (int)m, pl.hb, CB, pl.splits, rows,
                         inv_sqrt_head_dim(D), c.signs};
     return launch_generic_combine<D>(cp, s);
+}
+
+// ---------------------------------------------------------------- paged launches
+// Resident CTAs (one wave) and geometry of the paged kernel for blocks that
+// take up to `cols` columns of a sequence's kv-head.
+template <int D, int NB>
+bool gen_paged_plan_nb(const CacheView &c, GenPlan &pl, PagedShape &sh)
+{
+    const int per_sm = gen_layout<D, NB, true>(c, pl);
+    sh = PagedShape{gT, gN * NB, per_sm * num_sms()};
+    return per_sm >= 1;
+}
+
+template <int D>
+bool gen_paged_plan(const CacheView &c, int64_t cols, GenPlan &pl, PagedShape &sh)
+{
+    switch (gen_nb(D, cols)) {
+    case 1: return gen_paged_plan_nb<D, 1>(c, pl, sh);
+    case 2: if constexpr (D <= 256) return gen_paged_plan_nb<D, 2>(c, pl, sh); break;
+    case 4: if constexpr (D <= 128) return gen_paged_plan_nb<D, 4>(c, pl, sh); break;
+    }
+    return false;
+}
+
+template <int D>
+cudaError_t gen_paged_run(const CacheView &c, const PagedSplit &pg, int64_t cols, const uint16_t *q, int QH, float scale,
+                          float *part_o, float *part_ml, cudaStream_t s)
+{
+    GenPlan pl;
+    PagedShape sh;
+    if (!gen_paged_plan<D>(c, cols, pl, sh)) return cudaErrorInvalidConfiguration;
+    GenParams p{};
+    if (!gen_params<D>(c, pl, q, QH, scale, p)) return cudaErrorInvalidDevice;
+    p.part_o = part_o;
+    p.part_ml = part_ml;
+    p.pg = pg;
+    CUtensorMap kmap{};
+    if (pl.key != 0 && !gen_key_map<D>(c, &kmap, gcd_int(gT, (int)c.cap))) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)sh.ctas);
+    switch (pl.nb) {
+    case 1: return gen_launch<D, 1, true>(pl, grid, kmap, p, s);
+    case 2: if constexpr (D <= 256) return gen_launch<D, 2, true>(pl, grid, kmap, p, s); break;
+    case 4: if constexpr (D <= 128) return gen_launch<D, 4, true>(pl, grid, kmap, p, s); break;
+    }
+    return cudaErrorInvalidValue;
 }
 
 template <int D>
@@ -1146,5 +1307,15 @@ cudaError_t combine_parts(const float *part_o, const float *part_ml, float *out,
                                                     const SignBits &sg, cudaStream_t s)                                \
     {                                                                                                                    \
         return combine_parts<D>(part_o, part_ml, out, B, H, QH, m, hb, cb, splits, sg, s);                               \
+    }                                                                                                                    \
+    bool paged_generic_shape_d##D(const CacheView &c, int64_t cols, PagedShape &sh)                                      \
+    {                                                                                                                    \
+        GenPlan pl;                                                                                                      \
+        return gen_paged_plan<D>(c, cols, pl, sh);                                                                       \
+    }                                                                                                                    \
+    cudaError_t launch_paged_generic_d##D(const CacheView &c, const PagedSplit &pg, int64_t cols, const uint16_t *q,    \
+                                          int QH, float scale, float *part_o, float *part_ml, cudaStream_t s)           \
+    {                                                                                                                    \
+        return gen_paged_run<D>(c, pg, cols, q, QH, scale, part_o, part_ml, s);                                          \
     }                                                                                                                    \
     }

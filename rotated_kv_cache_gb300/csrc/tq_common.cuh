@@ -246,21 +246,7 @@ __device__ __forceinline__ void ld_global_v8(const void *p, uint32_t (&v)[8])
 
 __host__ __device__ constexpr int64_t imin64(int64_t a, int64_t b) { return a < b ? a : b; }
 
-// Division by a run-time constant d >= 1 for dividends x < 2^31: q = (x * m) >> sh
-// with sh = 31 + ceil(log2 d), m = ceil(2^sh / d) < 2^32 (Granlund & Montgomery,
-// "Division by invariant integers using multiplication", PLDI 1994, Thm 4.2).
-struct FastDiv {
-    uint32_t m, sh;
-};
-
-inline FastDiv make_fastdiv(uint32_t d)
-{
-    uint32_t l = 0;
-    while ((1ull << l) < d) ++l;
-    const uint32_t sh = 31 + l;
-    return FastDiv{(uint32_t)(((1ull << sh) + d - 1) / d), sh};
-}
-
+// x / d for the constant's divisor d and x < 2^31 (see FastDiv)
 __device__ __forceinline__ uint32_t fast_div(uint32_t x, FastDiv f) { return (uint32_t)(((uint64_t)x * f.m) >> f.sh); }
 
 // Largest power of two (<= 16) dividing x.
@@ -337,6 +323,32 @@ __device__ __forceinline__ void fwht_pairs_d128(float2 (&P)[32], int part)
     for (int j = 0; j < 32; ++j) {  // stride 64 across the row's two lanes
         const float o = __shfl_xor_sync(0xffffffffu, P[j].y, ROWS), a = P[j].x;
         P[j] = make_float2(__fadd_rn(a, o), __fsub_rn(a, o));
+    }
+}
+
+// Unnormalised Sylvester transform of a row held by a warp, dims PER lane ..
+// PER lane + PER - 1 on each lane: log2(PER) stages in the lane, 5 across lanes.
+template <int PER>
+__device__ __forceinline__ void fwht_warp(float (&x)[PER], int lane)
+{
+#pragma unroll
+    for (int hs = 1; hs < PER; hs <<= 1)
+#pragma unroll
+        for (int k = 0; k < PER; k += 2 * hs)
+#pragma unroll
+            for (int j = k; j < k + hs; ++j) {
+                const float a = x[j], b = x[j + hs];
+                x[j] = a + b;
+                x[j + hs] = a - b;
+            }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const bool upper = (lane & m) != 0;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const float other = __shfl_xor_sync(0xffffffffu, x[k], m);
+            x[k] = upper ? other - x[k] : x[k] + other;
+        }
     }
 }
 

@@ -20,4 +20,17 @@ cudaError_t launch_decode(const CacheView &c, int64_t t0, int64_t n, bool f32, v
     return cudaErrorInvalidValue;
 }
 
+cudaError_t launch_paged_decode(const CacheView &c, const PagedView &v, bool f32, void *k_out, void *v_out,
+                                cudaStream_t s)
+{
+    if (!v_out) return f32 ? paged_key_dispatch<true>(c, v, k_out, s) : paged_key_dispatch<false>(c, v, k_out, s);
+    switch (c.d) {
+    case 64: return launch_paged_decode_values_d64(c, v, f32, v_out, k_out, s);
+    case 128: return launch_paged_decode_values_d128(c, v, f32, v_out, k_out, s);
+    case 256: return launch_paged_decode_values_d256(c, v, f32, v_out, k_out, s);
+    case 512: return launch_paged_decode_values_d512(c, v, f32, v_out, k_out, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
 }  // namespace tq

@@ -20,6 +20,7 @@
 #pragma once
 #include "tq_common.cuh"
 #include "tq_kernels.h"
+#include "tq_paged.cuh"
 
 namespace tq {
 namespace {
@@ -31,6 +32,7 @@ struct KeyDecodeParams {
     void *out;
     int64_t cap, t0, n, groups_per_bh, BH;
     int d;
+    PagedView pv;  // paged launches: where the rows of the n ragged tokens are
 };
 
 // 32 codes of one group -> the float bit patterns of 1.5*2^23 + u with u = code
@@ -87,7 +89,7 @@ __device__ __forceinline__ void key_group_out(const uint32_t (&w)[KB], float s, 
     }
 }
 
-template <int KB, bool F32>
+template <int KB, bool F32, bool PAGED>
 __global__ void __launch_bounds__(256) decode_key_kernel(const __grid_constant__ KeyDecodeParams p)
 {
     pdl_wait_primary();  // whatever the previous kernel on the stream writes or reads is settled
@@ -95,6 +97,23 @@ __global__ void __launch_bounds__(256) decode_key_kernel(const __grid_constant__
     const int64_t gi = (int64_t)blockIdx.x * 256 + threadIdx.x;  // group within the (sequence, kv-head)'s n rows
     if (gi >= p.groups_per_bh) return;
     constexpr int A = align_of_bytes(4 * KB);
+    if constexpr (PAGED) {  // group gi % (d / 32) of token gi / (d / 32), every kv-head
+        const int gpr = p.d / 32, g = (int)(gi % gpr);
+        const int64_t t = gi / gpr, row0 = paged_row(p.pv, t, (int)p.BH);
+        if (t >= p.pv.starts[p.pv.seqs]) return;  // behind the last sequence: left as it was
+        for (int64_t h = blockIdx.y; h < p.BH; h += gridDim.y) {
+            uint32_t w[KB] = {};
+            float s = 0.0f, z = 0.0f;  // a token without a row reads as zeros
+            if (row0 >= 0) {
+                const int64_t mi = (row0 + h * p.pv.page) * gpr + g;
+                load_words<KB, A>(p.codes + mi * (4 * KB), w);
+                s = f16_bits_to_f32(p.scale[mi]);
+                z = f16_bits_to_f32(p.zero[mi]);
+            }
+            key_group_out<KB, F32>(w, s, z, static_cast<uint8_t *>(p.out) + ((t * p.BH + h) * p.d + 32 * g) * (F32 ? 4 : 2));
+        }
+        return;
+    }
     for (int64_t bh = blockIdx.y; bh < p.BH; bh += gridDim.y) {
         // rows t0 .. t0+n-1 of one (sequence, kv-head) are contiguous in every plane
         const int64_t row0 = bh * p.cap + p.t0;
@@ -131,6 +150,8 @@ struct ValueDecodeParams {
     FastDiv div_tiles;
     float inv_sqrt_d;
     SignBits sg;  // value signs
+    PagedView pv;   // paged launches: where the rows of the n ragged tokens are (outputs [n][H][d])
+    FastDiv div_h;  // ... x / H
     float cen[256];
 };
 
@@ -183,17 +204,30 @@ __device__ __forceinline__ void key_words_load(const uint8_t *src, uint32_t (&w)
     }
 }
 
-template <int D>
-__device__ __forceinline__ void key_tile_load(const ValueDecodeParams &p, uint32_t bh, int64_t t_first, int lane,
-                                              KeyTile &k)
+// Paged: row r of the tile is at cache row `crow` of lane r (-1: none, its
+// groups read as zeros).
+template <int D, bool PAGED>
+__device__ __forceinline__ void key_tile_load(const ValueDecodeParams &p, uint32_t bh, int64_t t_first, int64_t crow,
+                                              int lane, KeyTile &k)
 {
     constexpr int GPR = D / 32;  // groups per row
     const int64_t g0 = ((int64_t)bh * p.cap + p.t0 + t_first) * GPR;  // first group of the tile in the planes
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int g = lane + 32 * i;
-        if (t_first + g / GPR >= p.n) continue;
-        const int64_t gi = g0 + g;
+        int64_t gi = g0 + g;
+        if constexpr (PAGED) {
+            const int64_t row = __shfl_sync(0xffffffffu, crow, g / GPR);
+            gi = row * GPR + g % GPR;
+            if (row < 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) k.w[i][j] = 0u;
+                k.s[i] = k.z[i] = 0u;
+                continue;
+            }
+        } else if (t_first + g / GPR >= p.n) {
+            continue;
+        }
         switch (p.kb) {
         case 8: key_words_load<8>(p.k_codes + gi * 32, k.w[i]); break;
         case 4: key_words_load<4>(p.k_codes + gi * 16, k.w[i]); break;
@@ -214,17 +248,18 @@ __device__ __forceinline__ void key_group_from_tile(const uint32_t (&w8)[8], uin
     key_group_out<KB, F32>(w, f16_bits_to_f32((uint16_t)s), f16_bits_to_f32((uint16_t)z), dst);
 }
 
-template <int D, bool F32>
-__device__ __forceinline__ void key_tile_store(const ValueDecodeParams &p, uint32_t bh, int64_t t_first, int lane,
-                                               const KeyTile &k)
+template <int D, bool F32, bool PAGED>
+__device__ __forceinline__ void key_tile_store(const ValueDecodeParams &p, uint32_t bh, int64_t t_first, int64_t n,
+                                               int lane, const KeyTile &k)
 {
     constexpr int GPR = D / 32;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int g = lane + 32 * i;
-        if (t_first + g / GPR >= p.n) continue;
-        // output [bh][t][D]: group g of the tile starts at element (bh n + t_first) D + 32 g
-        void *dst = static_cast<uint8_t *>(p.k_out) + (((int64_t)bh * p.n + t_first) * D + 32 * g) * (F32 ? 4 : 2);
+        if (t_first + g / GPR >= n) continue;
+        // output [bh][t][D] (paged [t][h][D]): group g of the tile starts at element (bh n + t_first) D + 32 g
+        const int64_t e = PAGED ? ((t_first + g / GPR) * p.H + bh) * D + 32 * (g % GPR) : ((int64_t)bh * n + t_first) * D + 32 * g;
+        void *dst = static_cast<uint8_t *>(p.k_out) + e * (F32 ? 4 : 2);
         switch (p.kb) {
         case 8: key_group_from_tile<8, F32>(k.w[i], k.s[i], k.z[i], dst); break;
         case 4: key_group_from_tile<4, F32>(k.w[i], k.s[i], k.z[i], dst); break;
@@ -234,7 +269,10 @@ __device__ __forceinline__ void key_tile_store(const ValueDecodeParams &p, uint3
     }
 }
 
-template <int D, int VB, bool F32>
+// A warp takes every (grid kVWarps)-th tile of rows; in paged launches a run
+// of consecutive items, the kv-heads of one token tile after another, so that
+// it looks a tile's rows up once for all its heads.
+template <int D, int VB, bool F32, bool PAGED>
 __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __grid_constant__ ValueDecodeParams p)
 {
     using G = VGeo<D>;
@@ -256,22 +294,45 @@ __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __g
     const int r = lane % G::ROWS, part = lane / G::ROWS;
     const char *cen = reinterpret_cast<const char *>(scen);
 
-    const uint32_t W = gridDim.x * kVWarps;
-    uint32_t item = blockIdx.x * kVWarps + warp;
+    const uint32_t W = PAGED ? 1u : gridDim.x * kVWarps;
+    uint32_t item = blockIdx.x * kVWarps + warp, end = p.items;
+    int64_t n = p.n;
+    if constexpr (PAGED) {
+        const uint64_t w = item, all = (uint64_t)gridDim.x * kVWarps;
+        item = (uint32_t)(w * p.items / all);
+        end = (uint32_t)((w + 1) * p.items / all);
+        n = imin64(n, p.pv.starts[p.pv.seqs]);  // tokens behind the last sequence are left as they were
+    }
     // the next tile's codes are loaded while this one is transformed
     uint32_t nw[2 * VB], nsc = 0;
+    int64_t prow = -1, prow_t = -1;  // paged: this lane's row for kv-head 0, of the token tile at prow_t
     auto locate = [&](uint32_t it, int64_t &t, int64_t &crow, uint32_t &bh) {
-        bh = fast_div(it, p.div_tiles);
-        t = (int64_t)(it - bh * p.tiles_per_bh) * G::ROWS + r;
-        crow = (int64_t)bh * p.cap + p.t0 + t;
+        if constexpr (PAGED) {
+            const uint32_t tile = fast_div(it, p.div_h);
+            bh = it - tile * (uint32_t)p.H;
+            t = (int64_t)tile * G::ROWS + r;
+        } else {
+            bh = fast_div(it, p.div_tiles);
+            t = (int64_t)(it - bh * p.tiles_per_bh) * G::ROWS + r;
+            crow = (int64_t)bh * p.cap + p.t0 + t;
+        }
     };
-    if (item < p.items) {
+    int64_t ahead = -1;  // paged: cache row of this lane in the tile loaded ahead (-1: none)
+    auto load_tile = [&](uint32_t it) {
         int64_t t, crow;
         uint32_t bh;
-        locate(item, t, crow, bh);
-        if (t < p.n) load_value_lane<D, VB>(p, crow, part, nw, nsc);
-    }
-    for (; item < p.items; item += W) {
+        locate(it, t, crow, bh);
+        if constexpr (PAGED) {
+            if (t != prow_t) {
+                prow_t = t;
+                prow = paged_row(p.pv, t, p.H);
+            }
+            crow = ahead = prow < 0 ? -1 : prow + (int64_t)bh * p.pv.page;
+        }
+        if (PAGED ? crow >= 0 : t < p.n) load_value_lane<D, VB>(p, crow, part, nw, nsc);
+    };
+    if (item < end) load_tile(item);
+    for (; item < end; item += W) {
         uint32_t w[2 * VB], sc = nsc;
 #pragma unroll
         for (int k = 0; k < 2 * VB; ++k) w[k] = nw[k];
@@ -289,18 +350,14 @@ __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __g
         int64_t t, crow;
         uint32_t bh;
         locate(item, t, crow, bh);
-        const bool valid = t < p.n;
+        if constexpr (PAGED) crow = ahead;
+        const bool valid = t < n;
         KeyTile kt;
         const bool keys = p.k_out != nullptr;
-        if (keys) key_tile_load<D>(p, bh, t - r, lane, kt);
-        if (item + W < p.items) {
-            int64_t t1, crow1;
-            uint32_t bh1;
-            locate(item + W, t1, crow1, bh1);
-            if (t1 < p.n) load_value_lane<D, VB>(p, crow1, part, nw, nsc);
-        }
+        if (keys) key_tile_load<D, PAGED>(p, bh, t - r, crow, lane, kt);
+        if (item + W < end) load_tile(item + W);
         float2 P[32];
-        if (valid) {
+        if (PAGED ? crow >= 0 : valid) {
             const float s0 = f16_bits_to_f32((uint16_t)(sc & 0xFFFFu)), s1 = f16_bits_to_f32((uint16_t)(sc >> 16));
             const float2 s2 = make_float2(s0, s1);
 #pragma unroll
@@ -326,7 +383,7 @@ __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __g
             }
             // P[j].x, P[j].y: elements X0 + j, Y0 + j of the row (whole 32-byte sectors per store)
             constexpr int XS = D == 128 ? 32 : 64, Y0 = D == 128 ? 64 : 32;
-            const int64_t o = ((int64_t)bh * p.n + t) * D + XS * part;
+            const int64_t o = (PAGED ? t * p.H + bh : (int64_t)bh * p.n + t) * D + XS * part;
             if constexpr (F32) {
                 float *dst = static_cast<float *>(p.out) + o;
 #pragma unroll
@@ -353,7 +410,7 @@ __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __g
                 }
             }
         }
-        if (keys) key_tile_store<D, F32>(p, bh, t - r, lane, kt);
+        if (keys) key_tile_store<D, F32, PAGED>(p, bh, t - r, n, lane, kt);
     }
 }
 
@@ -374,11 +431,31 @@ cudaError_t run_key(const CacheView &c, int64_t t0, int64_t n, void *out, cudaSt
     const int64_t bx = (p.groups_per_bh + 255) / 256;
     if (bx >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)bx, (unsigned)imin64(p.BH, 65535));
-    return launch_dependent(decode_key_kernel<KB, F32>, grid, dim3(256), 0, s, p);
+    return launch_dependent(decode_key_kernel<KB, F32, false>, grid, dim3(256), 0, s, p);
 }
 
-template <int D, int VB, bool F32>
-cudaError_t run_value(const CacheView &c, int64_t t0, int64_t n, void *out, void *k_out, cudaStream_t s)
+template <int KB, bool F32>
+cudaError_t run_paged_key(const CacheView &c, const PagedView &v, void *out, cudaStream_t s)
+{
+    KeyDecodeParams p{};
+    p.codes = c.k_codes;
+    p.scale = c.k_scale;
+    p.zero = c.k_zero;
+    p.out = out;
+    p.d = c.d;
+    p.groups_per_bh = v.total * (c.d / 32);
+    p.BH = c.H;
+    p.pv = v;
+    const int64_t bx = (p.groups_per_bh + 255) / 256;
+    if (bx >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)bx, (unsigned)imin64(p.BH, 65535));
+    return launch_dependent(decode_key_kernel<KB, F32, true>, grid, dim3(256), 0, s, p);
+}
+
+// pv: the ragged tokens of a paged launch (n = pv->total), else null.
+template <int D, int VB, bool F32, bool PAGED>
+cudaError_t run_value(const CacheView &c, const PagedView *pv, int64_t t0, int64_t n, void *out, void *k_out,
+                      cudaStream_t s)
 {
     using G = VGeo<D>;
     ValueDecodeParams p{};
@@ -394,16 +471,18 @@ cudaError_t run_value(const CacheView &c, int64_t t0, int64_t n, void *out, void
     p.cap = c.cap;
     p.t0 = t0;
     p.n = n;
-    const int64_t tiles = (n + G::ROWS - 1) / G::ROWS, items = tiles * (int64_t)c.B * c.H;
+    const int64_t tiles = (n + G::ROWS - 1) / G::ROWS, items = tiles * (int64_t)(PAGED ? 1 : c.B) * c.H;
     if (items >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     p.tiles_per_bh = (uint32_t)tiles;
     p.items = (uint32_t)items;
     p.div_tiles = make_fastdiv(tiles > 0 ? (uint32_t)tiles : 1u);
     p.inv_sqrt_d = inv_sqrt_head_dim(D);
     p.sg = c.signs;
+    p.div_h = make_fastdiv((uint32_t)c.H);
+    if (PAGED) p.pv = *pv;
     const Tables &tab = codebook_tables(VB);
     for (int i = 0; i < (1 << VB); ++i) p.cen[i] = tab.centroids[i];
-    auto kern = decode_value_kernel<D, VB, F32>;
+    auto kern = decode_value_kernel<D, VB, F32, PAGED>;
     static int per_sm = 0;  // same on every GB300; only a successful query is kept
     if (!per_sm) {
         int k = 0;
@@ -428,16 +507,29 @@ cudaError_t key_dispatch(const CacheView &c, int64_t t0, int64_t n, void *out, c
     return cudaErrorInvalidValue;
 }
 
+template <bool F32>
+cudaError_t paged_key_dispatch(const CacheView &c, const PagedView &v, void *out, cudaStream_t s)
+{
+    switch (c.kb) {
+    case 2: return run_paged_key<2, F32>(c, v, out, s);
+    case 4: return run_paged_key<4, F32>(c, v, out, s);
+    case 5: return run_paged_key<5, F32>(c, v, out, s);
+    case 8: return run_paged_key<8, F32>(c, v, out, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
 // Values, and the keys of the same rows when k_out is not null (one launch).
-template <int D, bool F32>
-cudaError_t value_dispatch_vb(const CacheView &c, int64_t t0, int64_t n, void *out, void *k_out, cudaStream_t s)
+template <int D, bool F32, bool PAGED = false>
+cudaError_t value_dispatch_vb(const CacheView &c, int64_t t0, int64_t n, void *out, void *k_out, cudaStream_t s,
+                              const PagedView *pv = nullptr)
 {
     switch (c.vb) {
-    case 2: return run_value<D, 2, F32>(c, t0, n, out, k_out, s);
-    case 3: return run_value<D, 3, F32>(c, t0, n, out, k_out, s);
-    case 4: return run_value<D, 4, F32>(c, t0, n, out, k_out, s);
-    case 5: return run_value<D, 5, F32>(c, t0, n, out, k_out, s);
-    case 8: return run_value<D, 8, F32>(c, t0, n, out, k_out, s);
+    case 2: return run_value<D, 2, F32, PAGED>(c, pv, t0, n, out, k_out, s);
+    case 3: return run_value<D, 3, F32, PAGED>(c, pv, t0, n, out, k_out, s);
+    case 4: return run_value<D, 4, F32, PAGED>(c, pv, t0, n, out, k_out, s);
+    case 5: return run_value<D, 5, F32, PAGED>(c, pv, t0, n, out, k_out, s);
+    case 8: return run_value<D, 8, F32, PAGED>(c, pv, t0, n, out, k_out, s);
     }
     return cudaErrorInvalidValue;
 }

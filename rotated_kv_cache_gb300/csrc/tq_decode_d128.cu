@@ -8,4 +8,11 @@ cudaError_t launch_decode_values_d128(const CacheView &c, int64_t t0, int64_t n,
     return f32 ? value_dispatch_vb<128, true>(c, t0, n, out, k_out, s)
                : value_dispatch_vb<128, false>(c, t0, n, out, k_out, s);
 }
+
+cudaError_t launch_paged_decode_values_d128(const CacheView &c, const PagedView &v, bool f32, void *out, void *k_out,
+                                           cudaStream_t s)
+{
+    return f32 ? value_dispatch_vb<128, true, true>(c, 0, v.total, out, k_out, s, &v)
+               : value_dispatch_vb<128, false, true>(c, 0, v.total, out, k_out, s, &v);
+}
 }  // namespace tq

@@ -16,4 +16,16 @@ cudaError_t launch_encode(const CacheView &c, const uint16_t *k, const int64_t k
     return cudaErrorInvalidValue;
 }
 
+cudaError_t launch_paged_append(const CacheView &c, const PagedView &v, const uint16_t *k, const int64_t ks[2],
+                                const uint16_t *vv, const int64_t vs[2], cudaStream_t s)
+{
+    switch (c.d) {
+    case 64: return launch_paged_append_d64(c, v, k, ks, vv, vs, s);
+    case 128: return launch_paged_append_d128(c, v, k, ks, vv, vs, s);
+    case 256: return launch_paged_append_d256(c, v, k, ks, vv, vs, s);
+    case 512: return launch_paged_append_d512(c, v, k, ks, vv, vs, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
 }  // namespace tq

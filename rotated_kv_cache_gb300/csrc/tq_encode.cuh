@@ -27,6 +27,7 @@
 #pragma once
 #include "tq_common.cuh"
 #include "tq_kernels.h"
+#include "tq_paged.cuh"
 
 namespace tq {
 namespace {
@@ -72,31 +73,48 @@ struct EncodeParams {
     SignBits sg;  // value signs
     uint32_t *err;
     int use_tma;     // tiles arrive by tensor copies of the map (else one bulk copy per row)
+    PagedView pv;    // paged launches: where the token rows go (the source is [n][H][d] ragged tokens)
     float bnd[255];  // value boundaries (ascending)
 };
 
+// Item -> first token of its tile and (sequence, kv-head) index.  Paged items
+// run over the kv-heads of a token tile first, so a warp looks a tile's rows
+// up once for all its heads.
+template <int TROWS, bool PAGED>
+__device__ __forceinline__ int64_t locate_tile(const EncodeParams &p, uint32_t item, uint32_t &bh)
+{
+    if constexpr (PAGED) {
+        const uint32_t tile = fast_div(item, p.div_h);
+        bh = item - tile * (uint32_t)p.H;
+        return (int64_t)tile * TROWS;
+    } else {
+        bh = fast_div(item, p.div_tiles);
+        return (int64_t)(item - bh * p.tiles_per_bh) * TROWS;
+    }
+}
+
 // Bytes a tile's copies bring into shared memory.
-template <int D, bool KEY, int KR = kKeyRows>
+template <int D, bool KEY, bool PAGED, int KR = kKeyRows>
 __device__ __forceinline__ uint32_t tile_bytes(const EncodeParams &p, uint32_t item)
 {
     using G = EGeo<D, KEY, KR>;
     if (p.use_tma) return (uint32_t)((D / 64) * G::TROWS * 128);  // rows past n arrive as zeros
-    const uint32_t bh = fast_div(item, p.div_tiles);
-    const int64_t t_first = (int64_t)(item - bh * p.tiles_per_bh) * G::TROWS;
+    uint32_t bh;
+    const int64_t t_first = locate_tile<G::TROWS, PAGED>(p, item, bh);
     return (uint32_t)(imin64(G::TROWS, p.n - t_first) * D * 2);
 }
 
 // The copies of a tile, completing on `bar` (whose expected bytes the caller
 // has already raised by tile_bytes): one tensor copy per 64-column box, or
 // one bulk copy per row.  Call from every lane of the warp.
-template <int D, bool KEY, int KR = kKeyRows>
+template <int D, bool KEY, bool PAGED, int KR = kKeyRows>
 __device__ __forceinline__ void issue_copies(const EncodeParams &p, const CUtensorMap &map, uint32_t item,
                                              uint32_t buf, uint32_t bar, int lane)
 {
     using G = EGeo<D, KEY, KR>;
-    const uint32_t bh = fast_div(item, p.div_tiles);
-    const int64_t t_first = (int64_t)(item - bh * p.tiles_per_bh) * G::TROWS;
-    const uint32_t b = fast_div(bh, p.div_h), h = bh - b * (uint32_t)p.H;
+    uint32_t bh;
+    const int64_t t_first = locate_tile<G::TROWS, PAGED>(p, item, bh);
+    const uint32_t b = PAGED ? 0u : fast_div(bh, p.div_h), h = bh - b * (uint32_t)p.H;
     if (p.use_tma) {
         if (lane == 0) {
 #pragma unroll
@@ -111,13 +129,13 @@ __device__ __forceinline__ void issue_copies(const EncodeParams &p, const CUtens
     }
 }
 
-template <int D, bool KEY, int KR = kKeyRows>
+template <int D, bool KEY, bool PAGED, int KR = kKeyRows>
 __device__ __forceinline__ void issue_tile(const EncodeParams &p, const CUtensorMap &map, uint32_t item, uint32_t buf,
                                            uint32_t bar, int lane)
 {
-    if (lane == 0) mbar_arrive_expect_tx(bar, tile_bytes<D, KEY, KR>(p, item));
+    if (lane == 0) mbar_arrive_expect_tx(bar, tile_bytes<D, KEY, PAGED, KR>(p, item));
     __syncwarp();
-    issue_copies<D, KEY, KR>(p, map, item, buf, bar, lane);
+    issue_copies<D, KEY, PAGED, KR>(p, map, item, buf, bar, lane);
 }
 
 // Shared-memory base of a row's 64-column box c and the chunk xor for it.
@@ -170,7 +188,7 @@ __device__ __forceinline__ float pow2_scale_for(float den)
     return __uint_as_float((294u - e) << 23);
 }
 
-// ------------------------------------------------------------------ keys// ------------------------------------------------------------------ keys
+// ------------------------------------------------------------------ keys
 // Pack codes given as 0x4B400000 + code (code < 2^BITS) into the BITS-bit
 // little-endian stream: accumulate the sums, then subtract what the constant
 // 0x4B400000 part contributed (fields do not overlap, so adding is or-ing).
@@ -322,13 +340,16 @@ __device__ __forceinline__ void key_codes_fast(const uint32_t (&w)[16], const Ke
 }
 
 // A lane's RPL key groups (rows r, r + ROWS, ...): parameters for all first,
-// then the element passes, so the groups' dependency chains interleave.
-template <int D, int BITS, int KR = kKeyRows>
+// then the element passes, so the groups' dependency chains interleave.  The
+// rows' cache rows are crow, crow + ROWS, ... for the first nvalid of them, or
+// in paged launches rows[0], rows[1], ... where not negative.
+template <int D, int BITS, bool PAGED, int KR = kKeyRows>
 __device__ __forceinline__ void encode_key_lane(const EncodeParams &p, uint32_t buf, int r, int64_t crow, int part,
-                                                int nvalid)
+                                                int nvalid, const int64_t (&rows)[EGeo<D, true, KR>::RPL])
 {
     using G = EGeo<D, true, KR>;
     constexpr int R = G::RPL;
+    auto present = [&](int g) { return PAGED ? rows[g] >= 0 : g < nvalid; };
     const uint32_t lo = 4 * (part & 1);  // first 16-byte chunk of this lane's 32 keys in the 64-column box
     uint32_t base[R], xr[R];
 #pragma unroll
@@ -336,7 +357,7 @@ __device__ __forceinline__ void encode_key_lane(const EncodeParams &p, uint32_t 
     uint32_t w[R][16];
 #pragma unroll
     for (int g = 0; g < R; ++g) {
-        if (g < nvalid) {
+        if (present(g)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint4 v = lds128(base[g] + 16 * ((lo + i) ^ xr[g]));
@@ -352,13 +373,16 @@ __device__ __forceinline__ void encode_key_lane(const EncodeParams &p, uint32_t 
 #pragma unroll
     for (int g = 0; g < R; ++g) {
         kp[g] = key_params<BITS>(w[g]);
-        all &= kp[g].ok | (g >= nvalid);
+        all &= kp[g].ok | !present(g);
     }
     constexpr int RB = D * BITS / 8, LB = 4 * BITS;
 #pragma unroll
     for (int g = 0; g < R; ++g) {
-        if (g >= nvalid) break;
-        const int64_t row = crow + g * G::ROWS;
+        if (!present(g)) {
+            if constexpr (PAGED) continue;
+            break;
+        }
+        const int64_t row = PAGED ? rows[g] : crow + g * G::ROWS;
         if (!all && !kp[g].ok) {
             key_group_exact<BITS>(base[g], lo, xr[g], p.codes + row * RB + part * LB, p.scale + row * (D / 32) + part,
                                   p.zero + row * (D / 32) + part);
@@ -612,8 +636,9 @@ __device__ __forceinline__ void encode_value_lane(const EncodeParams &p, const f
 }
 
 // ------------------------------------------------------------------ kernels
-// The work of CTA `cta` of `ncta` encoding keys (KEY) or values.
-template <int D, int BITS, bool KEY>
+// The work of CTA `cta` of `ncta` encoding keys (KEY) or values.  A warp takes
+// every (ncta kWarps)-th item; in paged launches a run of consecutive ones.
+template <int D, int BITS, bool KEY, bool PAGED>
 __device__ __forceinline__ void encode_body(const EncodeParams &p, const CUtensorMap &map, uint8_t *smem_raw,
                                             uint32_t cta, uint32_t ncta)
 {
@@ -655,27 +680,44 @@ __device__ __forceinline__ void encode_body(const EncodeParams &p, const CUtenso
 
     const int r = lane % G::ROWS, part = lane / G::ROWS;
     const uint32_t my_mtab = smem_addr(mtab) + part * 272;
-    const uint32_t W = ncta * kWarps;
-    uint32_t item = cta * kWarps + warp;
-    if (item < p.items) issue_tile<D, KEY>(p, map, item, buf0, bar0, lane);
-    for (uint32_t k = 0; item < p.items; item += W, ++k) {
+    const uint32_t W = PAGED ? 1u : ncta * kWarps;
+    uint32_t item = cta * kWarps + warp, end = p.items;
+    int64_t prow[G::RPL];  // paged: rows of this lane's tokens for kv-head 0 (-1: none)
+    int64_t prow_t = -1;   // ... of the tile that starts at this token
+    if constexpr (PAGED) {
+        const uint64_t w = item, n = (uint64_t)ncta * kWarps;
+        item = (uint32_t)(w * p.items / n);
+        end = (uint32_t)((w + 1) * p.items / n);
+    }
+    if (item < end) issue_tile<D, KEY, PAGED>(p, map, item, buf0, bar0, lane);
+    for (uint32_t k = 0; item < end; item += W, ++k) {
         const uint32_t next = item + W;
         const uint32_t buf = (k & 1) ? buf1 : buf0, bar = (k & 1) ? bar1 : bar0;
-        if (next < p.items) issue_tile<D, KEY>(p, map, next, (k & 1) ? buf0 : buf1, (k & 1) ? bar0 : bar1, lane);
+        if (next < end) issue_tile<D, KEY, PAGED>(p, map, next, (k & 1) ? buf0 : buf1, (k & 1) ? bar0 : bar1, lane);
+        uint32_t bh;
+        const int64_t t_first = locate_tile<G::TROWS, PAGED>(p, item, bh);
+        if constexpr (PAGED) {
+            if (t_first != prow_t) {  // looked up while the tile is on its way
+                prow_t = t_first;
+#pragma unroll
+                for (int g = 0; g < G::RPL; ++g) prow[g] = paged_row(p.pv, t_first + r + g * G::ROWS, p.H);
+            }
+        }
         if (!mbar_wait_bounded(bar, (k >> 1) & 1, p.err)) {
             // give the other copy a bounded chance to land before leaving
-            if (next < p.items) mbar_wait_bounded((k & 1) ? bar0 : bar1, ((k + 1) >> 1) & 1, p.err);
+            if (next < end) mbar_wait_bounded((k & 1) ? bar0 : bar1, ((k + 1) >> 1) & 1, p.err);
             if (!KEY && lane == 0) bulk_wait0();
             return;
         }
-        const uint32_t bh = fast_div(item, p.div_tiles);
-        const int64_t t_first = (int64_t)(item - bh * p.tiles_per_bh) * G::TROWS;
-        const bool valid = t_first + r < p.n;
-        const int64_t crow = (int64_t)bh * p.cap + p.t0 + t_first + r;
+        int64_t rows[G::RPL];
+#pragma unroll
+        for (int g = 0; g < G::RPL; ++g) rows[g] = PAGED && prow[g] >= 0 ? prow[g] + (int64_t)bh * p.pv.page : -1;
+        const bool valid = PAGED ? rows[0] >= 0 : t_first + r < p.n;
+        const int64_t crow = PAGED ? rows[0] : (int64_t)bh * p.cap + p.t0 + t_first + r;
         if constexpr (KEY) {
             // rows r, r + ROWS, ... of the tile that exist
             const int nvalid = (int)imin64(G::RPL, (p.n - t_first - r + G::ROWS - 1) / G::ROWS);
-            if (valid) encode_key_lane<D, BITS>(p, buf, r, crow, part, nvalid);
+            if (PAGED || valid) encode_key_lane<D, BITS, PAGED>(p, buf, r, crow, part, nvalid, rows);
         } else {
             constexpr int RB = VStage<D, BITS>::RB;
             const uint32_t stage = smem_addr(stages + warp * STG);
@@ -688,16 +730,33 @@ __device__ __forceinline__ void encode_body(const EncodeParams &p, const CUtenso
             encode_value_lane<D, BITS>(p, sbnd, a, xr, my_mtab, stage, crow, r, part, valid);
             fence_proxy_async_smem();
             __syncwarp();
-            const int rows = (int)imin64(G::TROWS, p.n - t_first);
-            uint8_t *dst = p.codes + (crow - r) * RB;
-            if (((uintptr_t)dst & 15) == 0 && (rows * RB) % 16 == 0) {
+            const int nrows = (int)imin64(G::TROWS, p.n - t_first);
+            int64_t row0 = crow - r;
+            bool whole = true;  // the tile's rows follow one another in the cache
+            if constexpr (PAGED) {
+                row0 = __shfl_sync(0xffffffffu, crow, 0);
+                whole = __all_sync(0xffffffffu, r >= nrows || (valid && crow == row0 + r)) && row0 >= 0;
+            }
+            uint8_t *dst = p.codes + row0 * RB;
+            if (PAGED && !whole) {
+                // row by row, 8 bytes a lane (row bytes are a multiple of 8)
+                constexpr int WORDS = G::ROWS * RB / 8;
+#pragma unroll 1
+                for (int i0 = 0; i0 < WORDS; i0 += 32) {
+                    const int i = i0 + lane, row = i < WORDS ? i / (RB / 8) : 0;
+                    const int64_t to = __shfl_sync(0xffffffffu, crow, row);  // lane = row for part 0
+                    if (i < WORDS && to >= 0)
+                        *reinterpret_cast<uint2 *>(p.codes + to * RB + 8 * (i - row * (RB / 8))) =
+                            *reinterpret_cast<const uint2 *>(stages + warp * STG + 8 * i);
+                }
+            } else if (((uintptr_t)dst & 15) == 0 && (nrows * RB) % 16 == 0) {
                 if (lane == 0) {
-                    bulk_s2g(dst, stage, (uint32_t)(rows * RB));
+                    bulk_s2g(dst, stage, (uint32_t)(nrows * RB));
                     bulk_commit();
                 }
             } else {
                 // destination or size not a multiple of 16 bytes (row bytes are a multiple of 8): plain stores
-                for (int i = 8 * lane; i < rows * RB; i += 256)
+                for (int i = 8 * lane; i < nrows * RB; i += 256)
                     *reinterpret_cast<uint2 *>(dst + i) = *reinterpret_cast<const uint2 *>(stages + warp * STG + i);
             }
         }
@@ -714,20 +773,20 @@ __device__ __forceinline__ void encode_body(const EncodeParams &p, const CUtenso
 // the key kernel has started and takes the SMs that key CTAs leave in their
 // last round; it waits for the key grid only before it ends, which keeps
 // stream order for whatever is queued after the append.
-template <int D, int BITS, bool KEY>
+template <int D, int BITS, bool KEY, bool PAGED>
 __global__ void __launch_bounds__(kWarps * 32)
     encode_kernel(const __grid_constant__ EncodeParams p, const __grid_constant__ CUtensorMap map)
 {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     if constexpr (KEY) pdl_wait_primary();  // whatever the previous kernel on the stream writes or reads is settled
     pdl_allow_dependents();
-    encode_body<D, BITS, KEY>(p, map, smem_raw, blockIdx.x, gridDim.x);
+    encode_body<D, BITS, KEY, PAGED>(p, map, smem_raw, blockIdx.x, gridDim.x);
     if constexpr (!KEY) pdl_wait_primary();
 }
 
 // Keys and values in one launch: CTAs [0, key_ctas) encode the keys, the
 // others the values (see run_kv for how the CTAs are shared out).
-template <int D, int KB, int VB>
+template <int D, int KB, int VB, bool PAGED>
 __global__ void __launch_bounds__(kWarps * 32)
     encode_kv_kernel(const __grid_constant__ EncodeParams pk, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ EncodeParams pv, const __grid_constant__ CUtensorMap mv, uint32_t key_ctas)
@@ -736,9 +795,9 @@ __global__ void __launch_bounds__(kWarps * 32)
     pdl_wait_primary();  // whatever the previous kernel on the stream writes or reads is settled
     pdl_allow_dependents();
     if (blockIdx.x < key_ctas)
-        encode_body<D, KB, true>(pk, mk, smem_raw, blockIdx.x, key_ctas);
+        encode_body<D, KB, true, PAGED>(pk, mk, smem_raw, blockIdx.x, key_ctas);
     else
-        encode_body<D, VB, false>(pv, mv, smem_raw, blockIdx.x - key_ctas, gridDim.x - key_ctas);
+        encode_body<D, VB, false, PAGED>(pv, mv, smem_raw, blockIdx.x - key_ctas, gridDim.x - key_ctas);
 }
 
 // dynamic shared memory of encode_body<D, BITS, KEY>
@@ -751,11 +810,11 @@ constexpr size_t encode_smem()
 }
 
 // A value launch must directly follow the key launch of the same append.
-template <int D, int BITS, bool KEY>
+template <int D, int BITS, bool KEY, bool PAGED>
 cudaError_t run(const EncodeParams &p, const CUtensorMap &map, cudaStream_t s)
 {
     const size_t smem = encode_smem<D, BITS, KEY>();
-    auto kern = encode_kernel<D, BITS, KEY>;
+    auto kern = encode_kernel<D, BITS, KEY, PAGED>;
     static int per_sm = 0;  // same on every GB300; only a successful query is kept
     if (!per_sm) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -772,13 +831,13 @@ cudaError_t run(const EncodeParams &p, const CUtensorMap &map, cudaStream_t s)
 
 // Keys and values of a small append in one launch (encode_kv_kernel), every
 // CTA resident at once.
-template <int D, int KB, int VB>
+template <int D, int KB, int VB, bool PAGED>
 cudaError_t run_kv(const EncodeParams &pk, const CUtensorMap &mk, const EncodeParams &pv, const CUtensorMap &mv,
                    uint32_t key_ctas, uint32_t value_ctas, cudaStream_t s)
 {
     constexpr size_t sk = encode_smem<D, KB, true>(), sv = encode_smem<D, VB, false>();
     constexpr size_t smem = sk > sv ? sk : sv;
-    auto kern = encode_kv_kernel<D, KB, VB>;
+    auto kern = encode_kv_kernel<D, KB, VB, PAGED>;
     static bool attr = false;  // same on every GB300; only a successful call is kept
     if (!attr) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -788,27 +847,27 @@ cudaError_t run_kv(const EncodeParams &pk, const CUtensorMap &mk, const EncodePa
     return launch_dependent(kern, dim3(key_ctas + value_ctas), dim3(kWarps * 32), smem, s, pk, mk, pv, mv, key_ctas);
 }
 
-template <int D>
+template <int D, bool PAGED>
 cudaError_t dispatch_key(int kb, const EncodeParams &p, const CUtensorMap &map, cudaStream_t s)
 {
     switch (kb) {
-    case 2: return run<D, 2, true>(p, map, s);
-    case 4: return run<D, 4, true>(p, map, s);
-    case 5: return run<D, 5, true>(p, map, s);
-    case 8: return run<D, 8, true>(p, map, s);
+    case 2: return run<D, 2, true, PAGED>(p, map, s);
+    case 4: return run<D, 4, true, PAGED>(p, map, s);
+    case 5: return run<D, 5, true, PAGED>(p, map, s);
+    case 8: return run<D, 8, true, PAGED>(p, map, s);
     }
     return cudaErrorInvalidValue;
 }
 
-template <int D>
+template <int D, bool PAGED>
 cudaError_t dispatch_value(int vb, const EncodeParams &p, const CUtensorMap &map, cudaStream_t s)
 {
     switch (vb) {
-    case 2: return run<D, 2, false>(p, map, s);
-    case 3: return run<D, 3, false>(p, map, s);
-    case 4: return run<D, 4, false>(p, map, s);
-    case 5: return run<D, 5, false>(p, map, s);
-    case 8: return run<D, 8, false>(p, map, s);
+    case 2: return run<D, 2, false, PAGED>(p, map, s);
+    case 3: return run<D, 3, false, PAGED>(p, map, s);
+    case 4: return run<D, 4, false, PAGED>(p, map, s);
+    case 5: return run<D, 5, false, PAGED>(p, map, s);
+    case 8: return run<D, 8, false, PAGED>(p, map, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -832,9 +891,9 @@ inline bool input_map(CUtensorMap *map, const uint16_t *src, int D, int64_t n, i
 
 // Tiles of `rows` token rows per (sequence, kv-head); false if the count
 // does not fit the kernels' 31-bit item index.
-inline bool set_items(EncodeParams &p, int64_t n, int rows, const CacheView &c)
+inline bool set_items(EncodeParams &p, int64_t n, int rows, int B, int H)
 {
-    const int64_t tiles = (n + rows - 1) / rows, items = tiles * (int64_t)c.B * c.H;
+    const int64_t tiles = (n + rows - 1) / rows, items = tiles * (int64_t)B * H;
     if (items >= (int64_t(1) << 31)) return false;
     p.tiles_per_bh = (uint32_t)tiles;
     p.items = (uint32_t)items;
@@ -842,23 +901,12 @@ inline bool set_items(EncodeParams &p, int64_t n, int rows, const CacheView &c)
     return true;
 }
 
-template <int D>
-cudaError_t encode_d(const CacheView &c, const uint16_t *k, const int64_t ks[3], const uint16_t *v,
-                     const int64_t vs[3], int64_t t0, int64_t n, cudaStream_t s)
+// Keys and values of one append: source strides {b, h, t} (elements); the tiles
+// of pk and pv are set by the caller.
+template <int D, bool PAGED>
+cudaError_t encode_launch(const CacheView &c, EncodeParams &pk, EncodeParams &pv, const uint16_t *k,
+                          const int64_t ks[3], const uint16_t *v, const int64_t vs[3], int64_t n, int B, cudaStream_t s)
 {
-    EncodeParams p{};
-    p.H = c.H;
-    p.cap = c.cap;
-    p.t0 = t0;
-    p.n = n;
-    p.inv_sqrt_d = inv_sqrt_head_dim(D);
-    p.sg = c.signs;
-    p.err = device_error_word();
-    if (!p.err) return cudaErrorInvalidDevice;
-    const Tables &tab = codebook_tables(c.vb);
-    for (int i = 0; i < (1 << c.vb) - 1; ++i) p.bnd[i] = tab.boundaries[i];
-
-    EncodeParams pk = p, pv = p;
     CUtensorMap mk{}, mv{};
     pk.src = k;
     pk.sb = ks[0]; pk.sh = ks[1]; pk.st = ks[2];
@@ -866,8 +914,8 @@ cudaError_t encode_d(const CacheView &c, const uint16_t *k, const int64_t ks[3],
     pk.scale = c.k_scale;
     pk.zero = c.k_zero;
     pk.div_h = make_fastdiv((uint32_t)c.H);
-    if (!set_items(pk, n, EGeo<D, true>::TROWS, c)) return cudaErrorInvalidValue;
-    pk.use_tma = input_map(&mk, k, D, n, c.H, c.B, ks, EGeo<D, true>::TROWS) ? 1 : 0;
+    if (!set_items(pk, n, EGeo<D, true>::TROWS, B, c.H)) return cudaErrorInvalidValue;
+    pk.use_tma = input_map(&mk, k, D, n, c.H, B, ks, EGeo<D, true>::TROWS) ? 1 : 0;
 
     pv.src = v;
     pv.sb = vs[0]; pv.sh = vs[1]; pv.st = vs[2];
@@ -875,20 +923,58 @@ cudaError_t encode_d(const CacheView &c, const uint16_t *k, const int64_t ks[3],
     pv.scale = c.v_scale;
     pv.zero = nullptr;
     pv.div_h = make_fastdiv((uint32_t)c.H);
-    if (!set_items(pv, n, EGeo<D, false>::TROWS, c)) return cudaErrorInvalidValue;
-    pv.use_tma = input_map(&mv, v, D, n, c.H, c.B, vs, EGeo<D, false>::TROWS) ? 1 : 0;
+    if (!set_items(pv, n, EGeo<D, false>::TROWS, B, c.H)) return cudaErrorInvalidValue;
+    pv.use_tma = input_map(&mv, v, D, n, c.H, B, vs, EGeo<D, false>::TROWS) ? 1 : 0;
 
     // a small append (a few rows per sequence-head, as in a decode step) runs
     // keys and values in one launch when both grids fit one CTA per SM; a
     // larger one as two launches (keys, then values)
     const uint32_t gk = (pk.items + kWarps - 1) / kWarps, gv = (pv.items + kWarps - 1) / kWarps;
     if ((int64_t)gk + gv <= num_sms() && c.vb == 3 && (c.kb == 8 || c.kb == 4)) {
-        if (c.kb == 8) return run_kv<D, 8, 3>(pk, mk, pv, mv, gk, gv, s);
-        return run_kv<D, 4, 3>(pk, mk, pv, mv, gk, gv, s);
+        if (c.kb == 8) return run_kv<D, 8, 3, PAGED>(pk, mk, pv, mv, gk, gv, s);
+        return run_kv<D, 4, 3, PAGED>(pk, mk, pv, mv, gk, gv, s);
     }
-    cudaError_t e = dispatch_key<D>(c.kb, pk, mk, s);
+    cudaError_t e = dispatch_key<D, PAGED>(c.kb, pk, mk, s);
     if (e != cudaSuccess) return e;
-    return dispatch_value<D>(c.vb, pv, mv, s);
+    return dispatch_value<D, PAGED>(c.vb, pv, mv, s);
+}
+
+inline bool encode_common(EncodeParams &p, const CacheView &c, int64_t n)
+{
+    p.H = c.H;
+    p.cap = c.cap;
+    p.n = n;
+    p.inv_sqrt_d = inv_sqrt_head_dim(c.d);
+    p.sg = c.signs;
+    p.err = device_error_word();
+    const Tables &tab = codebook_tables(c.vb);
+    for (int i = 0; i < (1 << c.vb) - 1; ++i) p.bnd[i] = tab.boundaries[i];
+    return p.err != nullptr;
+}
+
+template <int D>
+cudaError_t encode_d(const CacheView &c, const uint16_t *k, const int64_t ks[3], const uint16_t *v,
+                     const int64_t vs[3], int64_t t0, int64_t n, cudaStream_t s)
+{
+    EncodeParams pk{};
+    if (!encode_common(pk, c, n)) return cudaErrorInvalidDevice;
+    pk.t0 = t0;
+    EncodeParams pv = pk;
+    return encode_launch<D, false>(c, pk, pv, k, ks, v, vs, n, c.B, s);
+}
+
+// Ragged tokens (element strides {token, head}) into the pages of their sequences.
+template <int D>
+cudaError_t paged_encode_d(const CacheView &c, const PagedView &view, const uint16_t *k, const int64_t ks[2],
+                           const uint16_t *v, const int64_t vs[2], cudaStream_t s)
+{
+    EncodeParams pk{};
+    if (!encode_common(pk, c, view.total)) return cudaErrorInvalidDevice;
+    pk.pv = view;
+    EncodeParams pv = pk;
+    // one "sequence" of total tokens; its stride is never stepped over
+    const int64_t k3[3] = {ks[1], ks[1], ks[0]}, v3[3] = {vs[1], vs[1], vs[0]};
+    return encode_launch<D, true>(c, pk, pv, k, k3, v, v3, view.total, 1, s);
 }
 
 }  // namespace

@@ -7,4 +7,10 @@ cudaError_t launch_encode_d128(const CacheView &c, const uint16_t *k, const int6
 {
     return encode_d<128>(c, k, ks, v, vs, t0, n, s);
 }
+
+cudaError_t launch_paged_append_d128(const CacheView &c, const PagedView &v, const uint16_t *k, const int64_t ks[2],
+                                    const uint16_t *vv, const int64_t vs[2], cudaStream_t s)
+{
+    return paged_encode_d<128>(c, v, k, ks, vv, vs, s);
+}
 }  // namespace tq

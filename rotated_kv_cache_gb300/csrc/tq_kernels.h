@@ -44,6 +44,52 @@ struct CacheView {
     SignBits signs;  // the cache's value sign vector
 };
 
+// Division by a run-time constant d >= 1 for dividends x < 2^31: q = (x * m) >> sh
+// with sh = 31 + ceil(log2 d), m = ceil(2^sh / d) < 2^32 (Granlund & Montgomery,
+// "Division by invariant integers using multiplication", PLDI 1994, Thm 4.2).
+struct FastDiv {
+    uint32_t m, sh;
+};
+
+inline FastDiv make_fastdiv(uint32_t d)
+{
+    uint32_t l = 0;
+    while ((1ull << l) < d) ++l;
+    const uint32_t sh = 31 + l;
+    return FastDiv{(uint32_t)(((1ull << sh) + d - 1) / d), sh};
+}
+
+// A page table and the ragged tokens of one call (tq_paged.cuh reads it).
+struct PagedView {
+    const int32_t *pages;   // [seqs][stride]
+    const int32_t *lens;    // [seqs]
+    const int32_t *starts;  // [seqs + 1]
+    int64_t stride, max_len, total;
+    int seqs, num_pages;
+    uint32_t page;          // rows per page
+    FastDiv div_page;
+    uint32_t *err;
+};
+
+// A paged attention call, for the split kernels (tq_paged.cuh).
+struct PagedSplit {
+    PagedView v;
+    int64_t q_token, q_head;  // element strides of q
+    int64_t *plan;            // [seqs + 1] stages before a sequence, [seqs + 1] units before it, per
+    int64_t slots;            // partial slots of the workspace
+    int64_t wide;             // sequences with more new tokens than this are another kernel's
+};
+
+__host__ __device__ constexpr int64_t paged_plan_words(int64_t seqs) { return 2 * (seqs + 1) + 1; }
+
+__host__ __device__ constexpr int gcd_int(int a, int b) { return b == 0 ? a : gcd_int(b, a % b); }
+
+// A split kernel's geometry for a paged batch: rows per stage, columns per
+// block, CTAs of the launch.
+struct PagedShape {
+    int stage, block, ctas;
+};
+
 struct Tables {
     float centroids[256];
     float boundaries[255];
@@ -65,7 +111,12 @@ cudaError_t launch_encode(const CacheView &c, const uint16_t *k, const int64_t k
     cudaError_t launch_encode_d##D(const CacheView &c, const uint16_t *k, const int64_t ks[3], const uint16_t *v, \
                                    const int64_t vs[3], int64_t t0, int64_t n, cudaStream_t s);                  \
     cudaError_t launch_decode_values_d##D(const CacheView &c, int64_t t0, int64_t n, bool f32, void *out,        \
-                                          void *k_out, cudaStream_t s);
+                                          void *k_out, cudaStream_t s);                                          \
+    cudaError_t launch_paged_append_d##D(const CacheView &c, const PagedView &v, const uint16_t *k,               \
+                                         const int64_t ks[2], const uint16_t *vv, const int64_t vs[2],           \
+                                         cudaStream_t s);                                                        \
+    cudaError_t launch_paged_decode_values_d##D(const CacheView &c, const PagedView &v, bool f32, void *out,     \
+                                                void *k_out, cudaStream_t s);
 TQ_DECLARE_PER_D(64)
 TQ_DECLARE_PER_D(128)
 TQ_DECLARE_PER_D(256)
@@ -109,6 +160,19 @@ cudaError_t launch_attention(const CacheView &c, const uint16_t *q, int q_heads,
                              float *out, void *ws, size_t ws_bytes, cudaStream_t s);
 
 int num_sms();
+
+// Paged caches: the view's pool is `c` (batch = pages, capacity = page size).
+// K, V of ragged tokens -> their rows, and back ([total][H][d]; either output may be null).
+cudaError_t launch_paged_append(const CacheView &c, const PagedView &v, const uint16_t *k, const int64_t ks[2],
+                                const uint16_t *vv, const int64_t vs[2], cudaStream_t s);
+cudaError_t launch_paged_decode(const CacheView &c, const PagedView &v, bool f32, void *k_out, void *v_out,
+                                cudaStream_t s);
+// Causal attention of ragged tokens q (strides {token, head}) -> out bf16 [total][QH][d];
+// no sequence has more than max_new of them.  0 bytes: an occupancy query failed.
+size_t paged_attention_workspace_bytes(const CacheView &c, int seqs, int64_t max_len, int64_t total, int64_t max_new, int QH);
+cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const uint16_t *q, const int64_t qs[2], int QH,
+                                   int64_t max_new, float scale, uint16_t *out, void *ws, size_t ws_bytes,
+                                   cudaStream_t s);
 
 // Allocation-free decode attention: partials in a library-owned device array.
 size_t noalloc_scratch_bytes();

@@ -1,0 +1,241 @@
+// tq_paged_attention.cu -- causal attention of ragged new tokens over a paged
+// cache: the choice of kernels, the workspace, and the merge of the partials.
+//
+//   o_i = sum_{t <= pos_i} softmax_t(q_i . k_t scale) v_t
+//
+// for every new token i at position pos_i of its sequence; the values stay in
+// the rotated domain and the sum is un-rotated once per (token, q-head), as in
+// the contiguous calls.  A token that sees no row gives zeros.
+#include "tq_common.cuh"
+#include "tq_kernels.h"
+#include "tq_paged.cuh"
+
+namespace tq {
+
+#define TQ_DECLARE_PAGED_GENERIC(D)                                                                                    \
+    bool paged_generic_shape_d##D(const CacheView &c, int64_t cols, PagedShape &sh);                                   \
+    cudaError_t launch_paged_generic_d##D(const CacheView &c, const PagedSplit &pg, int64_t cols, const uint16_t *q,  \
+                                          int QH, float scale, float *part_o, float *part_ml, cudaStream_t s);
+TQ_DECLARE_PAGED_GENERIC(64)
+TQ_DECLARE_PAGED_GENERIC(128)
+TQ_DECLARE_PAGED_GENERIC(256)
+TQ_DECLARE_PAGED_GENERIC(512)
+#undef TQ_DECLARE_PAGED_GENERIC
+
+namespace {
+
+// ---------------------------------------------------------------- merge of the segments
+struct PagedCombineParams {
+    const float *part_o, *part_ml;
+    uint16_t *out;  // bf16 [total][QH][D]
+    PagedSplit pg;
+    int H, QH, G, ST, CB;
+    int64_t rows;  // total * QH
+    float inv_sqrt_d;
+    SignBits sg;
+};
+
+__device__ __forceinline__ float pc_ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// W warps per (token, q-head) row; lane holds dims PER lane .. + PER - 1.
+// Warp w of a row takes its unit's segments w, w + W, ...: their (max, sum)
+// pairs one a lane, 32 at a time, then their output rows with independent
+// loads; the row's first warp merges the warps' results, divides, un-rotates
+// (log2 d butterfly stages) and rounds once to bf16.  It moves one partial row
+// per segment and does nothing else of size: bound by the latency of two
+// dependent loads, so few rows take many warps (host rule below).
+template <int D, int W>
+__global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(const __grid_constant__ PagedCombineParams p)
+{
+    constexpr int PER = D / 32, CW = W > 4 ? W : 4;
+    __shared__ float wo[W > 1 ? CW : 1][PER][32];
+    __shared__ float wm[CW], wl[CW];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wid = warp % W, lead = warp - wid;
+    const int64_t row = (int64_t)blockIdx.x * (CW / W) + warp / W;
+    pdl_wait_primary();
+    pdl_allow_dependents();
+    bool live = row < p.rows;
+    const int64_t t = live ? row / p.QH : 0;
+    const int qh = (int)(row - t * p.QH);
+    int s = 0;
+    int64_t n = 0, len = 0, s0 = 0;
+    if (live) {
+        int lo = 0, hi = p.pg.v.seqs + 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (p.pg.v.starts[mid] <= t) lo = mid + 1;
+            else hi = mid;
+        }
+        s = lo - 1;
+        live = s >= 0 && s < p.pg.v.seqs;  // else behind the last sequence: left as it was
+        if (live) {
+            s0 = paged_start(p.pg.v, s);
+            n = paged_new(p.pg.v, s);
+            len = paged_len(p.pg.v, s);
+            live = n <= p.pg.wide && t < s0 + n;
+        }
+    }
+    if (W == 1 && !live) return;  // no barrier below when W = 1
+    int64_t first = 0;            // slots of the unit's segments: first .. first + segs - 1
+    int segs = 0, col = 0;
+    if (live && len > 0) {
+        const int64_t stages = (len + p.ST - 1) / p.ST, blocks = (n * p.G + p.CB - 1) / p.CB;
+        const int64_t per = p.pg.plan[2 * p.pg.v.seqs + 2], up = p.pg.plan[p.pg.v.seqs + 1 + s];
+        const int h = qh / p.G;
+        col = (int)((t - s0) * p.G + (qh - h * p.G));
+        const int64_t u = h * blocks + col / p.CB, a = p.pg.plan[s] + u * stages;
+        const int64_t c0 = a / per, c1 = (a + stages - 1) / per;
+        first = c0 + up + u;
+        segs = (int)(c1 - c0 + 1);
+        col %= p.CB;
+        if (first + segs > p.pg.slots) segs = 0;  // starts out of order
+    }
+    const int mine = segs > wid ? (segs - wid + W - 1) / W : 0;
+    auto part = [&](int j) { return (first + wid + (int64_t)W * j) * p.CB + col; };
+    float m = -INFINITY, l = 0.0f, x[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) x[k] = 0.0f;
+    for (int j0 = 0; j0 < mine; j0 += 32) {
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (j0 + lane < mine) ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * part(j0 + lane));
+        float mx = ml.x;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = fmaxf(m, mx);
+        const float mu = mx == -INFINITY ? 0.0f : mx, keep = pc_ex2(m - mu), wt = pc_ex2(ml.x - mu);
+        m = mx;
+        l = l * keep + ml.y * wt;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) x[k] *= keep;
+        const int cnt = mine - j0 < 32 ? mine - j0 : 32;
+#pragma unroll 4
+        for (int j = 0; j < cnt; ++j) {
+            const float w = __shfl_sync(0xffffffffu, wt, j);
+            const float *src = p.part_o + part(j0 + j) * D + PER * lane;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) x[k] += src[k] * w;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) wo[warp][k][lane] = x[k];
+        if (lane == 0) {
+            wm[warp] = m;
+            wl[warp] = l;
+        }
+        __syncthreads();
+        if (wid != 0 || !live) return;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < W; ++w) mx = fmaxf(mx, wm[lead + w]);
+        const float mu = mx == -INFINITY ? 0.0f : mx;
+        l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) x[k] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float wt = pc_ex2(wm[lead + w] - mu);
+            l += wl[lead + w] * wt;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) x[k] += wo[lead + w][k][lane] * wt;
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : p.inv_sqrt_d / l;  // nothing seen: zeros
+    fwht_warp<PER>(x, lane);
+    uint32_t w[PER / 2];
+#pragma unroll
+    for (int k = 0; k < PER; k += 2)
+        w[k / 2] = pack_bf16x2(x[k] * (sign_negative(p.sg, PER * lane + k) ? -inv : inv),
+                               x[k + 1] * (sign_negative(p.sg, PER * lane + k + 1) ? -inv : inv));
+    store_words<PER / 2, PER * 2 < 16 ? PER * 2 : 16>(p.out + row * D + PER * lane, w);
+}
+
+template <int D>
+cudaError_t run_combine(const PagedCombineParams &p, cudaStream_t s)
+{
+    // fewer rows, more warps to each: enough warps to fill the SMs' issue slots
+    // either way, and a row's partials in as few dependent loads as they allow
+    if (p.rows >= 4096)
+        return launch_dependent(paged_combine_kernel<D, 1>, dim3((unsigned)((p.rows + 3) / 4)), dim3(128), 0, s, p);
+    if (p.rows >= 512) return launch_dependent(paged_combine_kernel<D, 4>, dim3((unsigned)p.rows), dim3(128), 0, s, p);
+    return launch_dependent(paged_combine_kernel<D, 16>, dim3((unsigned)p.rows), dim3(512), 0, s, p);
+}
+
+// ---------------------------------------------------------------- plan and workspace
+bool generic_shape(const CacheView &c, int64_t cols, PagedShape &sh)
+{
+    switch (c.d) {
+    case 64: return paged_generic_shape_d64(c, cols, sh);
+    case 128: return paged_generic_shape_d128(c, cols, sh);
+    case 256: return paged_generic_shape_d256(c, cols, sh);
+    case 512: return paged_generic_shape_d512(c, cols, sh);
+    }
+    return false;
+}
+
+struct PagedPlan {
+    PagedShape split;
+    int64_t slots;
+    size_t off_ml, off_o, bytes;  // workspace: plan words, partial (max, sum), partial outputs
+};
+
+bool paged_plan(const CacheView &c, int seqs, int64_t total, int64_t max_new, int QH, PagedPlan &pl)
+{
+    const int64_t G = QH / c.H;
+    if (!generic_shape(c, max_new * G, pl.split)) return false;
+    // a sequence of n new tokens has ceil(n G / block) blocks: at most this many units in all
+    const int64_t units = c.H * (total * G / pl.split.block + seqs), slots = pl.slots = pl.split.ctas + units;
+    auto r256 = [](size_t x) { return (x + 255) / 256 * 256; };
+    pl.off_ml = r256((size_t)paged_plan_words(seqs) * 8);
+    pl.off_o = pl.off_ml + r256((size_t)slots * pl.split.block * 8);
+    pl.bytes = pl.off_o + (size_t)slots * pl.split.block * c.d * 4;
+    return true;
+}
+
+}  // namespace
+
+size_t paged_attention_workspace_bytes(const CacheView &c, int seqs, int64_t max_len, int64_t total, int64_t max_new, int QH)
+{
+    (void)max_len;
+    PagedPlan pl;
+    return paged_plan(c, seqs, total, max_new, QH, pl) ? pl.bytes : 0;
+}
+
+cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const uint16_t *q, const int64_t qs[2], int QH,
+                                   int64_t max_new, float scale, uint16_t *out, void *ws, size_t ws_bytes,
+                                   cudaStream_t s)
+{
+    PagedPlan pl;
+    if (!paged_plan(c, v.seqs, v.total, max_new, QH, pl)) return cudaErrorInvalidConfiguration;
+    if (ws_bytes < pl.bytes) return cudaErrorInvalidValue;
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<int64_t *>(base), pl.slots, INT32_MAX};
+    float *part_ml = reinterpret_cast<float *>(base + pl.off_ml), *part_o = reinterpret_cast<float *>(base + pl.off_o);
+    const int64_t cols = max_new * (QH / c.H);
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (c.d) {
+    case 64: e = launch_paged_generic_d64(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
+    case 128: e = launch_paged_generic_d128(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
+    case 256: e = launch_paged_generic_d256(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
+    case 512: e = launch_paged_generic_d512(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
+    }
+    if (e != cudaSuccess) return e;
+    PagedCombineParams cp{part_o, part_ml, out, pg, c.H, QH, QH / c.H, pl.split.stage, pl.split.block, v.total * QH,
+                          inv_sqrt_head_dim(c.d), c.signs};
+    switch (c.d) {
+    case 64: return run_combine<64>(cp, s);
+    case 128: return run_combine<128>(cp, s);
+    case 256: return run_combine<256>(cp, s);
+    case 512: return run_combine<512>(cp, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace tq

@@ -1,0 +1,353 @@
+"""Paged cache on the GPU: append and fetch against the contiguous calls (bit
+for bit) and the oracle, attention against a plain binary64 implementation."""
+import numpy as np
+import pytest
+import torch
+
+from pagedtest import Batch, check_attention, rows_of
+
+pytestmark = pytest.mark.gpu
+
+
+def _contiguous(tq, b, s, n=None):
+    """Sequence s appended through tq_encode_append into a cache of its own."""
+    n = b.lens[s] if n is None else n
+    c = tq.Cache(1, b.H, b.d, max(n, 1), k_bits=b.kb, v_bits=b.vb)
+    x = [t[s][:n].transpose(0, 1).contiguous()[None].cuda() for t in (b.k, b.v)]
+    tq.tq_encode_append(c, x[0], x[1], 0)
+    return c
+
+
+APPENDS = [(128, 8, 3, 64), (128, 4, 3, 16), (128, 5, 8, 48), (64, 8, 4, 32), (64, 4, 2, 16), (64, 2, 3, 80),
+           (256, 4, 2, 48), (256, 8, 5, 128), (512, 8, 3, 16), (512, 2, 4, 256)]
+
+
+@pytest.mark.parametrize("d,kb,vb,page", APPENDS)
+def test_append_matches_the_contiguous_append(cuda, d, kb, vb, page):
+    """Chunks on top of chunks, ragged, some of one row and some empty: the rows' bytes are those of
+    tq_encode_append, and no other row of the pool is written."""
+    b = Batch([70, 0, 1, 257, 33, 16], [0] * 6, H=3, d=d, kb=kb, vb=vb, page=page, seed=d + kb)
+    pool = b.pool(cuda)
+    for t in pool.planes():
+        t.fill_(0x5A)
+    lens = [0] * 6
+    for step in ([1, 0, 1, 100, 16, 15], [69, 0, 0, 156, 17, 0], [0, 0, 0, 1, 0, 1]):
+        lens = [a + c for a, c in zip(lens, step)]
+        part = lambda rows: torch.cat([x[n - c:n] for x, n, c in zip(rows, lens, step)]).cuda()  # noqa: E731
+        starts = b.dev(np.concatenate([[0], np.cumsum(step)]).astype(np.int32))
+        cuda.tq_paged_append(pool, b.pages(cuda, lens), starts, part(b.k), part(b.v))
+    assert lens == b.lens
+    for s, n in enumerate(lens):
+        if n:
+            want = _contiguous(cuda, b, s)
+            for got, ref in zip(rows_of(pool, b.table[s], n), want.planes()):
+                assert np.array_equal(got, ref[0, :, :n].cpu().numpy()), s
+    written = torch.zeros(b.num_pages, page, dtype=torch.bool)
+    for s, n in enumerate(lens):
+        for t in range(n):
+            written[b.table[s, t // page], t % page] = True
+    for t in pool.planes():
+        rest = t.transpose(1, 2)[~written.cuda()]
+        fill = 0x5A if t.dtype == torch.uint8 else 0x5A
+        assert bool((rest == fill).all())
+    assert cuda.tq_device_error() == 0
+
+
+def test_append_strided_views_and_padding(cuda):
+    """K and V as slices of one fused projection; tokens behind the last sequence are not read into any page."""
+    H, d = 4, 128
+    b = Batch([40, 25], [40, 25], H=H, d=d, kb=8, vb=3, page=32, pad_rows=7)
+    k, v = b.tokens(b.k, b.new), b.tokens(b.v, b.new)
+    k[b.total:] = float("nan")
+    fused = torch.cat([k, v], 1).cuda()
+    plain, strided = b.pool(cuda), b.pool(cuda)
+    starts = b.dev(b.starts)
+    cuda.tq_paged_append(plain, b.pages(cuda), starts, k[:b.total].cuda(), v[:b.total].cuda())
+    cuda.tq_paged_append(strided, b.pages(cuda), starts, fused[:, :H], fused[:, H:])
+    for x, y in zip(plain.planes(), strided.planes()):
+        assert torch.equal(x, y)
+    # heads before tokens
+    hk, hv = (x.transpose(0, 1).contiguous().transpose(0, 1).cuda() for x in (k, v))
+    other = b.pool(cuda)
+    cuda.tq_paged_append(other, b.pages(cuda), starts, hk, hv)
+    for x, y in zip(plain.planes(), other.planes()):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,kb,vb,page", APPENDS)
+def test_fetch_matches_the_contiguous_fetch(cuda, d, kb, vb, page, dtype):
+    b = Batch([70, 0, 1, 257, 33], [33, 0, 1, 257, 2], H=3, d=d, kb=kb, vb=vb, page=page, seed=d + vb, pad_rows=5)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    n = b.total + b.pad_rows
+    outs = [torch.full((n, b.H, d), 7.0, dtype=dtype, device="cuda") for _ in range(2)]
+    args = (pool, b.pages(cuda), b.dev(b.starts), n)
+    k, v = cuda.tq_paged_decode(*args, dtype=dtype, k_out=outs[0], v_out=outs[1])
+    at = 0
+    for s, (n_s, m) in enumerate(zip(b.lens, b.new)):
+        if m:
+            ck, cv = cuda.tq_decode(_contiguous(cuda, b, s), n_s - m, m, dtype=dtype)
+            assert torch.equal(k[at:at + m], ck[0].transpose(0, 1)) and torch.equal(v[at:at + m], cv[0].transpose(0, 1))
+        at += m
+    assert bool((k[b.total:] == 7).all()) and bool((v[b.total:] == 7).all())  # behind the last sequence
+    only_k, none = cuda.tq_paged_decode(pool, b.pages(cuda), b.dev(b.starts), b.total, dtype=dtype, want_v=False)
+    none2, only_v = cuda.tq_paged_decode(pool, b.pages(cuda), b.dev(b.starts), b.total, dtype=dtype, want_k=False)
+    assert none is None and none2 is None
+    assert torch.equal(only_k, k[:b.total]) and torch.equal(only_v, v[:b.total])
+    assert cuda.tq_device_error() == 0
+
+
+def _attend(tq, b, QH, seed=1, scale=None, **kw):
+    pool = b.pool(tq)
+    b.fill(tq, pool)
+    q = b.queries(QH, seed)
+    out = tq.tq_paged_attention(pool, b.pages(tq), b.dev(b.starts), q.cuda(), max(max(b.new), 1), softmax_scale=scale, **kw)
+    check_attention(b, pool, q, out, scale=scale)
+    assert tq.tq_device_error() == 0
+    return pool, q, out
+
+
+# decode: lengths around the stages and pages of every kernel, empty slots among them
+@pytest.mark.parametrize("d,kb,vb,G,page", [
+    (128, 8, 3, 8, 64), (128, 4, 3, 8, 16), (128, 4, 2, 4, 48), (128, 8, 4, 1, 32), (128, 8, 2, 16, 128),
+    (128, 4, 4, 12, 96), (128, 5, 3, 8, 32), (128, 2, 8, 3, 16), (64, 8, 3, 8, 64), (64, 4, 4, 5, 16), (64, 8, 2, 16, 80),
+    (64, 2, 5, 2, 48), (256, 8, 4, 4, 128), (256, 4, 3, 8, 16), (256, 5, 2, 12, 32), (512, 8, 3, 8, 64), (512, 4, 5, 2, 16),
+])
+def test_decode_shapes(cuda, d, kb, vb, G, page):
+    lens = [1, 0, 15, 16, 17, 63, 64, 65, 96, 97, 128, 129, 300, 1000]
+    b = Batch(lens, [min(n, 1) for n in lens], H=2, d=d, kb=kb, vb=vb, page=page, seed=d + G)
+    _attend(cuda, b, 2 * G)
+
+
+@pytest.mark.parametrize("d,kb,vb,G,page,new", [
+    (128, 8, 3, 8, 64, 4), (128, 4, 3, 8, 32, 3), (128, 8, 4, 5, 16, 7), (128, 4, 2, 16, 128, 2), (64, 8, 4, 4, 16, 5),
+    (64, 4, 3, 8, 48, 9), (256, 8, 3, 4, 32, 4), (256, 4, 4, 16, 64, 3), (512, 8, 3, 2, 16, 6), (128, 5, 5, 3, 80, 8),
+])
+def test_verification_shapes(cuda, d, kb, vb, G, page, new):
+    """Up to `new` new tokens a sequence: fewer in some, as many as rows in others."""
+    lens = [1, 2, new, new + 1, 64, 65, 0, 200, 777]
+    b = Batch(lens, [min(n, 1 + (i * 3 + new) % new) for i, n in enumerate(lens)], H=2, d=d, kb=kb, vb=vb, page=page, seed=new)
+    _attend(cuda, b, 2 * G)
+
+
+@pytest.mark.parametrize("d,kb,vb,G,page,lens,new", [
+    (128, 8, 3, 8, 64, [300], [300]), (128, 4, 3, 8, 16, [1000, 5, 200], [130, 1, 200]),
+    (128, 8, 4, 4, 32, [129, 700, 1, 0, 513], [129, 1, 1, 0, 257]), (64, 8, 4, 4, 32, [640, 90, 1000], [512, 1, 77]),
+    (64, 4, 2, 1, 48, [515], [388]), (64, 8, 3, 16, 64, [100, 129], [40, 129]), (128, 5, 2, 3, 16, [444, 100], [150, 99]),
+    (128, 2, 5, 8, 256, [300], [100]), (256, 8, 3, 4, 64, [400, 33], [140, 33]), (512, 4, 4, 2, 32, [200], [90]),
+    (128, 8, 3, 7, 64, [391], [255]), (128, 8, 8, 8, 64, [257], [256]),
+])
+def test_chunk_shapes(cuda, d, kb, vb, G, page, lens, new):
+    b = Batch(lens, new, H=2, d=d, kb=kb, vb=vb, page=page, seed=sum(lens))
+    _attend(cuda, b, 2 * G)
+
+
+@pytest.mark.parametrize("d,kb,vb", [(128, 8, 3), (128, 4, 3), (64, 8, 4), (256, 8, 3)])
+def test_long_contexts(cuda, d, kb, vb):
+    """Many segments a unit, beside sequences far shorter than a segment."""
+    lens = [9000, 3, 64, 4097, 1, 2000]
+    b = Batch(lens, [1, 1, 2, 1, 1, 4], H=2, d=d, kb=kb, vb=vb, page=64, seed=5)
+    _attend(cuda, b, 16)
+    b = Batch([5000], [90], H=1, d=d, kb=kb, vb=vb, page=32, seed=6)
+    _attend(cuda, b, 8)
+
+
+def test_many_short_sequences(cuda):
+    """More sequences than a warp scans at once, most of a page or less."""
+    lens = [(i * 7) % 40 for i in range(200)]
+    b = Batch(lens, [min(n, 1 + i % 2) for i, n in enumerate(lens)], H=2, d=128, kb=8, vb=3, page=16, seed=9)
+    _attend(cuda, b, 8)
+
+
+def test_one_step_matches_the_contiguous_attention(cuda):
+    """Same rows, same kernels' arithmetic: within one bf16 rounding of tq_decode_attention."""
+    b = Batch([777], [1], H=2, d=128, kb=8, vb=3, page=64)
+    _, q, out = _attend(cuda, b, 16)
+    c = _contiguous(cuda, b, 0)
+    want = cuda.tq_decode_attention(c, q.cuda(), 777)
+    assert ((out.float() - want).abs() <= 2.0 ** -8 * want.abs() + 2e-3).all()
+
+
+def test_strided_queries_padding_and_scale(cuda):
+    """q as a slice of a fused projection; outputs behind the last sequence stay as they were."""
+    b = Batch([100, 30, 200], [5, 1, 130], H=2, d=128, kb=8, vb=3, page=32, pad_rows=6)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = b.queries(8)
+    q[b.total:] = float("nan")
+    fused = torch.zeros(len(q), 12, 128, dtype=torch.bfloat16)
+    fused[:, 2:10] = q
+    out = torch.full((len(q), 8, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), fused.cuda()[:, 2:10], 130, softmax_scale=0.031, out=out)
+    assert bool((out[b.total:] == 3).all())
+    check_attention(b, pool, q[:b.total], out[:b.total], scale=0.031)
+
+
+@pytest.mark.parametrize("d,kb,new", [(128, 8, 4), (64, 4, 3), (128, 8, 150), (64, 8, 300), (256, 8, 20)])
+def test_hidden_rows_may_hold_anything(cuda, d, kb, new):
+    """NaN and infinities in later rows of the chunk reach only the tokens that see them; rows of a page behind
+    the sequence's end reach nobody."""
+    b = Batch([new + 50, 77], [new, 1], H=2, d=d, kb=kb, vb=3, page=64, seed=3)
+    # one NaN in a key is quantised to the lowest code and leaves its group finite (the codec's clip);
+    # the scale written below is what makes a key of kv-head 0 NaN
+    b.k[0][50 + new * 3 // 4, 0, 3] = float("nan")
+    b.v[0][50 + new // 2, 1, 5] = float("inf")      # a value of kv-head 1
+    pool = b.pool(cuda)
+    for t in pool.planes():  # what no sequence holds: codes of any kind, scales NaN
+        t.fill_(0x7F if t.dtype == torch.uint8 else 0x7FFF)
+    b.fill(cuda, pool)
+    t = 50 + new * 3 // 4
+    pool.k_scale[int(b.table[0, t // 64]), 0, t % 64, 1] = 0x7E00
+    q = b.queries(8)
+    out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q.cuda(), new)
+    check_attention(b, pool, q, out)
+    nan = out.float().isnan().any(-1).cpu()  # [token][head]
+    assert bool(nan[new * 3 // 4:new, :4].all()) and not bool(nan[:new * 3 // 4, :4].any())
+    assert bool(nan[new // 2:new, 4:].all()) and not bool(nan[:new // 2, 4:].any())
+    assert not bool(nan[new:].any())
+
+
+def test_more_new_tokens_than_rows(cuda):
+    """Tokens before their sequence's first row: not appended, zeros back, zeros out."""
+    b = Batch([3, 0, 40], [3, 0, 4], H=2, d=128, kb=8, vb=3, page=16)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    before = [t.clone() for t in pool.planes()]
+    starts = b.dev(np.array([0, 5, 7, 11], np.int32))  # 5 new tokens of 3 rows, 2 of none
+    k = torch.cat([torch.ones(2, 2, 128), b.k[0], torch.ones(2, 2, 128), b.k[2][36:]]).to(torch.bfloat16).cuda()
+    v = torch.cat([torch.ones(2, 2, 128), b.v[0], torch.ones(2, 2, 128), b.v[2][36:]]).to(torch.bfloat16).cuda()
+    cuda.tq_paged_append(pool, b.pages(cuda), starts, k, v)
+    for x, y in zip(before, pool.planes()):
+        assert torch.equal(x, y)
+    rk, rv = cuda.tq_paged_decode(pool, b.pages(cuda), starts, 11)
+    q = b.queries(4, total=11)
+    out = cuda.tq_paged_attention(pool, b.pages(cuda), starts, q.cuda(), 5)
+    for x in (rk, rv, out):
+        assert not bool(x[:2].any()) and not bool(x[5:7].any()) and bool(x[2:5].any())
+    check_attention(b, pool, torch.cat([q[2:5], q[7:]]), torch.cat([out[2:5], out[7:]]))
+
+
+def test_shared_pages(cuda):
+    """Two sequences over one prefix: the same page numbers in both rows of the table."""
+    b = Batch([160, 130], [1, 1], H=2, d=128, kb=8, vb=3, page=64)
+    b.table[1, :2] = b.table[0, :2]
+    for x in (b.k, b.v):
+        x[1][:128] = x[0][:128]
+    _attend(cuda, b, 8)
+
+
+def test_a_run_as_a_server_makes_it(cuda):
+    """Prompts, then decode steps, a sequence that ends, one that takes over its pages, a verification step:
+    every output against the plain implementation, every append read back."""
+    H, QH, d, page = 2, 8, 128, 16
+    b = Batch([400, 300, 120], [0, 0, 0], H=H, d=d, kb=8, vb=3, page=page, seed=11, spare=4)
+    pool = b.pool(cuda)
+    lens = [0, 0, 0]
+
+    def step(new):
+        nonlocal lens
+        lens = [n + m for n, m in zip(lens, new)]
+        part = lambda rows: torch.cat([x[n - m:n] for x, n, m in zip(rows, lens, new)]).cuda()  # noqa: E731
+        starts, pages = b.dev(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)), b.pages(cuda, lens)
+        cuda.tq_paged_append(pool, pages, starts, part(b.k), part(b.v))
+        q = b.queries(QH, seed=sum(lens), total=sum(new))
+        out = cuda.tq_paged_attention(pool, pages, starts, q.cuda(), max(new))
+        rk, rv = cuda.tq_paged_decode(pool, pages, starts, sum(new), dtype=torch.float32)
+        check_attention(b, pool, q, out, lens=lens, new=new)
+        at = 0
+        for s, m in enumerate(new):
+            if m:
+                ck, cv = cuda.tq_decode(_contiguous(cuda, b, s, lens[s]), lens[s] - m, m, dtype=torch.float32)
+                assert torch.equal(rk[at:at + m], ck[0].transpose(0, 1)) and torch.equal(rv[at:at + m], cv[0].transpose(0, 1))
+            at += m
+
+    step([150, 37, 120])
+    step([1, 1, 0])
+    step([1, 1, 0])
+    b.table[2, :4] = b.table[2, :4][::-1].copy()  # sequence 2 ended: another takes its pages, in another order
+    b.k[2], b.v[2] = (x[torch.randperm(len(x))] for x in (b.k[2], b.v[2]))
+    lens[2] = 0
+    step([1, 1, 60])
+    step([4, 3, 2])
+    assert cuda.tq_device_error() == 0
+
+
+def test_streams_and_graph_replay(cuda):
+    """The same batch through a side stream, and captured once and replayed after the lengths, the table and
+    the tokens changed under it."""
+    b = Batch([90, 33, 0, 200], [1, 1, 0, 1], H=2, d=128, kb=8, vb=3, page=32, seed=21)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = b.queries(8).cuda()
+    pages, starts = b.pages(cuda, max_len=224), b.dev(b.starts)
+    want = cuda.tq_paged_attention(pool, pages, starts, q, 1)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = cuda.tq_paged_attention(pool, pages, starts, q, 1, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    ws = torch.empty(cuda.tq_paged_attention_workspace_bytes(pool, pages, 8, 3, 1), dtype=torch.uint8, device="cuda")
+    knew = torch.zeros(3, 2, 128, dtype=torch.bfloat16, device="cuda")
+    vnew, out = knew.clone(), torch.empty_like(want)
+    back = [torch.empty(3, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+
+    def step():
+        cuda.tq_paged_append(pool, pages, starts, knew, vnew)
+        cuda.tq_paged_attention(pool, pages, starts, q, 1, out=out, workspace=ws)
+        cuda.tq_paged_decode(pool, pages, starts, 3, k_out=back[0], v_out=back[1])
+
+    take = lambda rows, lens: torch.stack([x[n - 1] for x, n in zip(rows, lens) if n]).cuda()  # noqa: E731
+    lens = [90, 33, 0, 200]
+    knew.copy_(take(b.k, lens)), vnew.copy_(take(b.v, lens))
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for lens in ([90, 33, 0, 200], [50, 20, 0, 131], [64, 1, 0, 17]):
+        pages.seq_lens.copy_(b.dev(np.array(lens, np.int32)))
+        knew.copy_(take(b.k, lens)), vnew.copy_(take(b.v, lens))
+        g.replay()
+        torch.cuda.synchronize()
+        check_attention(b, pool, q, out, lens=lens, new=b.new)
+    assert cuda.tq_device_error() == 0
+
+
+def test_bad_pages_and_lengths_are_reported(cuda):
+    """A page number outside the pool and a length above the bound: recorded, nothing outside touched, and the
+    other sequences' results stand."""
+    b = Batch([70, 40], [1, 1], H=2, d=128, kb=8, vb=3, page=32)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = b.queries(8)
+    good = b.table.copy()
+    for bad in (b.num_pages, -1, 2 ** 31 - 1):
+        b.table = good.copy()
+        b.table[0, 2] = bad  # holds the new token's row
+        pages, starts = b.pages(cuda), b.dev(b.starts)
+        before = [t.clone() for t in pool.planes()]
+        assert cuda.tq_device_error() == 0
+        out = cuda.tq_paged_attention(pool, pages, starts, q.cuda(), 1)
+        assert cuda.tq_device_error() == cuda.TQ_DEVICE_ERR_PAGE
+        rk, _ = cuda.tq_paged_decode(pool, pages, starts, 2)
+        assert cuda.tq_device_error() == cuda.TQ_DEVICE_ERR_PAGE
+        new = [torch.stack([x[0][69], x[1][39]]).cuda() for x in (b.k, b.v)]
+        cuda.tq_paged_append(pool, pages, starts, *new)
+        assert cuda.tq_device_error() == cuda.TQ_DEVICE_ERR_PAGE
+        assert not bool(rk[0].any()) and bool(rk[1].any())
+        for x, y in zip(before, pool.planes()):
+            assert torch.equal(x, y)
+        b.table = good
+        k1, v1 = b.lens, b.new
+        assert k1 == [70, 40] and v1 == [1, 1]
+        from pagedtest import ATOL, RTOL, attention64, dequantised
+        k, v = dequantised(pool, good[1], 40)
+        want = attention64(q[1:2], k, v, 39)
+        assert ((out[1:2].cpu().double() - want).abs() <= RTOL * want.abs() + ATOL).all()
+    pages = b.pages(cuda, lens=[200, 40], max_len=96)
+    cuda.tq_paged_attention(pool, pages, b.dev(b.starts), q.cuda(), 1)
+    assert cuda.tq_device_error() & cuda.TQ_DEVICE_ERR_LENGTH
+    # starts out of order: more segments than there can be, none of them written outside the workspace
+    cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(np.array([0, 2, 0], np.int32)), q.cuda(), 2)
+    assert cuda.tq_device_error() & cuda.TQ_DEVICE_ERR_LENGTH
