@@ -321,10 +321,10 @@ TQ_API int tq_attention_supported(int32_t head_dim, int32_t k_bits, int32_t v_bi
  * graph serves changing batches; the host sees only the bounds max_len,
  * max_new and total.  The kernels check what they read: a page number outside
  * the pool ORs TQ_DEVICE_ERR_PAGE into the device error word, a length outside
- * [0, max_len], starts out of order or outside [0, total], or more new tokens
- * than max_new ORs TQ_DEVICE_ERR_LENGTH, and results of the sequences
- * concerned are unspecified; nothing outside the pool and the outputs is ever
- * touched.  A token that stands before its sequence's first row (more new
+ * [0, max_len], starts out of order, or lengths of more than total_len in all
+ * OR TQ_DEVICE_ERR_LENGTH; results are then unspecified (for a bad page, those
+ * of its sequences), but nothing outside the pool, the outputs and the
+ * workspace is ever touched.  A token that stands before its sequence's first row (more new
  * tokens than rows) is not appended, reads back as zeros and attends to
  * nothing (zeros).  Two sequences may share pages that neither appends to;
  * rows appended by one call must not share a place.
@@ -334,6 +334,8 @@ typedef struct tq_page_table {
     const int32_t *seq_lens;  /* device [num_seqs]: rows, the new tokens included */
     int64_t stride;           /* pages between table rows; stride * P >= max_len */
     int64_t max_len;          /* bound of seq_lens, 1 .. 2^31 - 1 */
+    int64_t total_len;        /* bound of the sum of seq_lens (0: num_seqs * max_len); attention of long
+                                 chunks sizes its workspace by it */
     int32_t num_seqs;         /* >= 1 */
     int32_t reserved;         /* must be 0 */
 } tq_page_table;
@@ -385,7 +387,9 @@ TQ_API size_t tq_paged_attention_workspace_bytes(const tq_cache *pool, const tq_
  * Scores and sums are fp32; keys, values and probabilities enter the tensor
  * cores as f16 (11 bits), which costs less than the output's rounding.  A
  * row of the cache that a token does not see never reaches its output,
- * whatever it holds (NaN and infinities included).  total = 0 is a no-op.
+ * whatever it holds (NaN and infinities included); a row that it sees whose
+ * value scale is not finite makes its output not finite (NaN, or infinite in
+ * single dims).  total = 0 is a no-op.
  */
 TQ_API tq_status tq_paged_attention(const tq_cache *pool, const tq_page_table *table, const int32_t *starts,
                                     int64_t total, int64_t max_new, const void *q, const int64_t q_strides[2],

@@ -68,7 +68,7 @@ class _CacheStruct(ctypes.Structure):
 class _PageTableStruct(ctypes.Structure):
     _fields_ = [
         ("pages", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("stride", ctypes.c_int64),
-        ("max_len", ctypes.c_int64), ("num_seqs", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("max_len", ctypes.c_int64), ("total_len", ctypes.c_int64), ("num_seqs", ctypes.c_int32), ("reserved", ctypes.c_int32),
     ]
 
 
@@ -207,11 +207,12 @@ class PageTable:
     """Where the rows of a batch's sequences are in a pool (a Cache whose batch counts pages and
     whose capacity is the page size): pages int32 [num_seqs][max pages], seq_lens int32
     [num_seqs] (rows, new tokens included), both on the pool's device, and the host's bound
-    max_len of the lengths (default: all that the table's pages hold).  The tensors are read by
+    max_len of the lengths (default: all that the table's pages hold) and total_len of their sum (0:
+    num_seqs * max_len; long chunks size their workspace by it).  The tensors are read by
     every call, so writing to them changes the batch, captured graphs included."""
 
     def __init__(self, pages: torch.Tensor, seq_lens: torch.Tensor, max_len: int | None = None,
-                 page_size: int | None = None):
+                 page_size: int | None = None, total_len: int = 0):
         if pages.dtype != torch.int32 or pages.dim() != 2 or (pages.shape[1] > 1 and pages.stride(1) != 1):
             raise ValueError("pages must be int32 [num_seqs][pages], a sequence's pages contiguous")
         if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (pages.shape[0],) or not seq_lens.is_contiguous():
@@ -222,6 +223,7 @@ class PageTable:
         self.pages, self.seq_lens = pages, seq_lens
         self.num_seqs = int(pages.shape[0])
         self.max_len = int(pages.shape[1]) * int(page_size) if max_len is None else int(max_len)
+        self.total_len = int(total_len)
 
     def struct(self, pool: "Cache") -> _PageTableStruct:
         if self.pages.shape[1] * pool.capacity < self.max_len:
@@ -230,7 +232,8 @@ class PageTable:
         stride = self.pages.stride(0) if self.num_seqs > 1 else self.pages.shape[1]
         if stride < self.pages.shape[1]:
             raise ValueError("the rows of the page table overlap")
-        return _PageTableStruct(self.pages.data_ptr(), self.seq_lens.data_ptr(), stride, self.max_len, self.num_seqs, 0)
+        return _PageTableStruct(self.pages.data_ptr(), self.seq_lens.data_ptr(), stride, self.max_len, self.total_len,
+                                self.num_seqs, 0)
 
 
 # ------------------------------------------------------------------ host-side queries

@@ -391,6 +391,7 @@ tq_status check_table(const tq_cache *c, const tq_page_table *t)
     if (!t || !t->pages || !t->seq_lens) return TQ_ERR_NULL;
     if (t->num_seqs < 1 || t->num_seqs >= (1 << 30) || t->reserved != 0) return TQ_ERR_SHAPE;
     if (t->max_len < 1 || t->max_len > INT32_MAX || t->stride < 1) return TQ_ERR_SHAPE;
+    if (t->total_len < 0) return TQ_ERR_SHAPE;
     if (t->stride < (t->max_len + c->capacity - 1) / c->capacity) return TQ_ERR_CAPACITY;
     return TQ_OK;
 }
@@ -419,6 +420,13 @@ tq_status check_paged_attention(const tq_cache *c, const tq_page_table *t, int32
     // rows of out, and units of work, fit the kernels' indices
     if (total > (int64_t(1) << 30) / q_heads) return TQ_ERR_SHAPE;
     return (int64_t)t->num_seqs * c->num_kv_heads > (int64_t(1) << 30) ? TQ_ERR_SHAPE : TQ_OK;
+}
+
+tq::PagedBounds paged_bounds(const tq_page_table *t, int64_t total, int64_t max_new)
+{
+    const int64_t all = t->num_seqs * t->max_len;
+    return tq::PagedBounds{t->num_seqs, total, max_new < total ? max_new : total, t->max_len,
+                           t->total_len > 0 && t->total_len < all ? t->total_len : all, INT32_MAX};
 }
 
 tq::PagedView paged_view(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total)
@@ -469,8 +477,7 @@ size_t tq_paged_attention_workspace_bytes(const tq_cache *c, const tq_page_table
 {
     if (check_cache(c) != TQ_OK || check_table(c, t) != TQ_OK) return 0;
     if (check_paged_attention(c, t, q_heads, total, max_new) != TQ_OK) return 0;
-    if (max_new > total) max_new = total > 0 ? total : 1;
-    return tq::paged_attention_workspace_bytes(view(c), t->num_seqs, t->max_len, total, max_new, q_heads);
+    return tq::paged_attention_workspace_bytes(view(c), paged_bounds(t, total > 0 ? total : 1, max_new), q_heads);
 }
 
 tq_status tq_paged_attention(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total,
@@ -484,15 +491,15 @@ tq_status tq_paged_attention(const tq_cache *c, const tq_page_table *t, const in
     if ((st = check_ragged(q, qs)) != TQ_OK) return st;
     if (!out) return TQ_ERR_NULL;
     if (!aligned16(out)) return TQ_ERR_ALIGN;
-    if (max_new > total) max_new = total;
     const tq::CacheView cv = view(c);
-    const size_t need = tq::paged_attention_workspace_bytes(cv, t->num_seqs, t->max_len, total, max_new, q_heads);
+    const tq::PagedBounds b = paged_bounds(t, total, max_new);
+    const size_t need = tq::paged_attention_workspace_bytes(cv, b, q_heads);
     if (need == 0) return TQ_ERR_CUDA;  // the occupancy query failed
     if (!ws || ws_bytes < need) return TQ_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return TQ_ERR_ALIGN;
     const tq::PagedView pv = paged_view(c, t, starts, total);
     if (!pv.err) return TQ_ERR_CUDA;
-    return cuda_status(tq::launch_paged_attention(cv, pv, static_cast<const uint16_t *>(q), qs, q_heads, max_new, scale,
+    return cuda_status(tq::launch_paged_attention(cv, pv, b, static_cast<const uint16_t *>(q), qs, q_heads, scale,
                                                   static_cast<uint16_t *>(out), ws, ws_bytes, (cudaStream_t)stream));
 }
 

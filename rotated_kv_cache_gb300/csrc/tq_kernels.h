@@ -84,6 +84,13 @@ __host__ __device__ constexpr int64_t paged_plan_words(int64_t seqs) { return 2 
 
 __host__ __device__ constexpr int gcd_int(int a, int b) { return b == 0 ? a : gcd_int(b, a % b); }
 
+// What the host knows of a paged attention call.
+struct PagedBounds {
+    int seqs;
+    int64_t total, max_new, max_len, total_len;
+    int64_t wide;  // more new tokens than this make a sequence wide (tq_paged_wide.cu); INT32_MAX: none is
+};
+
 // A split kernel's geometry for a paged batch: rows per stage, columns per
 // block, CTAs of the launch.
 struct PagedShape {
@@ -169,10 +176,15 @@ cudaError_t launch_paged_decode(const CacheView &c, const PagedView &v, bool f32
                                 cudaStream_t s);
 // Causal attention of ragged tokens q (strides {token, head}) -> out bf16 [total][QH][d];
 // no sequence has more than max_new of them.  0 bytes: an occupancy query failed.
-size_t paged_attention_workspace_bytes(const CacheView &c, int seqs, int64_t max_len, int64_t total, int64_t max_new, int QH);
-cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const uint16_t *q, const int64_t qs[2], int QH,
-                                   int64_t max_new, float scale, uint16_t *out, void *ws, size_t ws_bytes,
+size_t paged_attention_workspace_bytes(const CacheView &c, const PagedBounds &b, int QH);
+cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const PagedBounds &b, const uint16_t *q,
+                                   const int64_t qs[2], int QH, float scale, uint16_t *out, void *ws, size_t ws_bytes,
                                    cudaStream_t s);
+// ... of the wide sequences, by tcgen05 (head_dim 64 and 128).
+bool paged_wide_applies(const CacheView &c);
+size_t paged_wide_workspace_bytes(const CacheView &c, const PagedBounds &b, int QH);
+cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const PagedBounds &b, const uint16_t *q, int QH,
+                              float scale, uint16_t *out, void *ws, cudaStream_t s);
 
 // Allocation-free decode attention: partials in a library-owned device array.
 size_t noalloc_scratch_bytes();

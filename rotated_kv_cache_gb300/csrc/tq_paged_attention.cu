@@ -182,49 +182,62 @@ bool generic_shape(const CacheView &c, int64_t cols, PagedShape &sh)
 
 struct PagedPlan {
     PagedShape split;
+    PagedBounds b;
     int64_t slots;
-    size_t off_ml, off_o, bytes;  // workspace: plan words, partial (max, sum), partial outputs
+    size_t off_ml, off_o, off_wide, bytes;  // workspace: plan words, partial (max, sum), partial outputs, the wide kernels'
 };
 
-bool paged_plan(const CacheView &c, int seqs, int64_t total, int64_t max_new, int QH, PagedPlan &pl)
+// A sequence with at least this many columns (new tokens x q-heads of a
+// kv-head) is wide.
+constexpr int64_t kWideColumns = 128;
+
+bool paged_plan(const CacheView &c, const PagedBounds &bounds, int QH, PagedPlan &pl)
 {
     const int64_t G = QH / c.H;
-    if (!generic_shape(c, max_new * G, pl.split)) return false;
+    pl.b = bounds;
+    pl.b.wide = paged_wide_applies(c) && pl.b.max_new * G >= kWideColumns ? (kWideColumns - 1) / G : INT32_MAX;
+    const bool wide = pl.b.wide != INT32_MAX;
+    const int64_t narrow = wide ? (pl.b.wide > 0 ? pl.b.wide : 1) : pl.b.max_new;  // new tokens of a sequence for the split kernels
+    if (!generic_shape(c, narrow * G, pl.split)) return false;
     // a sequence of n new tokens has ceil(n G / block) blocks: at most this many units in all
-    const int64_t units = c.H * (total * G / pl.split.block + seqs), slots = pl.slots = pl.split.ctas + units;
+    const int64_t units = c.H * (pl.b.total * G / pl.split.block + pl.b.seqs);
+    pl.slots = pl.split.ctas + units;
     auto r256 = [](size_t x) { return (x + 255) / 256 * 256; };
-    pl.off_ml = r256((size_t)paged_plan_words(seqs) * 8);
-    pl.off_o = pl.off_ml + r256((size_t)slots * pl.split.block * 8);
-    pl.bytes = pl.off_o + (size_t)slots * pl.split.block * c.d * 4;
+    pl.off_ml = r256((size_t)paged_plan_words(pl.b.seqs) * 8);
+    pl.off_o = pl.off_ml + r256((size_t)pl.slots * pl.split.block * 8);
+    pl.off_wide = pl.off_o + r256((size_t)pl.slots * pl.split.block * c.d * 4);
+    pl.bytes = pl.off_wide + (wide ? paged_wide_workspace_bytes(c, pl.b, QH) : 0);
     return true;
 }
 
 }  // namespace
 
-size_t paged_attention_workspace_bytes(const CacheView &c, int seqs, int64_t max_len, int64_t total, int64_t max_new, int QH)
+size_t paged_attention_workspace_bytes(const CacheView &c, const PagedBounds &b, int QH)
 {
-    (void)max_len;
     PagedPlan pl;
-    return paged_plan(c, seqs, total, max_new, QH, pl) ? pl.bytes : 0;
+    return paged_plan(c, b, QH, pl) ? pl.bytes : 0;
 }
 
-cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const uint16_t *q, const int64_t qs[2], int QH,
-                                   int64_t max_new, float scale, uint16_t *out, void *ws, size_t ws_bytes,
+cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const PagedBounds &b, const uint16_t *q,
+                                   const int64_t qs[2], int QH, float scale, uint16_t *out, void *ws, size_t ws_bytes,
                                    cudaStream_t s)
 {
     PagedPlan pl;
-    if (!paged_plan(c, v.seqs, v.total, max_new, QH, pl)) return cudaErrorInvalidConfiguration;
+    if (!paged_plan(c, b, QH, pl)) return cudaErrorInvalidConfiguration;
     if (ws_bytes < pl.bytes) return cudaErrorInvalidValue;
     uint8_t *base = static_cast<uint8_t *>(ws);
-    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<int64_t *>(base), pl.slots, INT32_MAX};
+    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<int64_t *>(base), pl.slots, pl.b.wide};
     float *part_ml = reinterpret_cast<float *>(base + pl.off_ml), *part_o = reinterpret_cast<float *>(base + pl.off_o);
-    const int64_t cols = max_new * (QH / c.H);
-    cudaError_t e = cudaErrorInvalidValue;
+    cudaError_t e = cudaSuccess;
+    if (pl.b.wide != INT32_MAX) e = launch_paged_wide(c, pg, pl.b, q, QH, scale, out, base + pl.off_wide, s);
+    if (e != cudaSuccess) return e;
+    const int64_t narrow = pl.b.wide != INT32_MAX ? (pl.b.wide > 0 ? pl.b.wide : 1) : pl.b.max_new, cols = narrow * (QH / c.H);
     switch (c.d) {
     case 64: e = launch_paged_generic_d64(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
     case 128: e = launch_paged_generic_d128(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
     case 256: e = launch_paged_generic_d256(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
     case 512: e = launch_paged_generic_d512(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
+    default: e = cudaErrorInvalidValue;
     }
     if (e != cudaSuccess) return e;
     PagedCombineParams cp{part_o, part_ml, out, pg, c.H, QH, QH / c.H, pl.split.stage, pl.split.block, v.total * QH,

@@ -1,0 +1,807 @@
+// tq_paged_wide.cu -- paged attention of long chunks (prefill) on the
+// fifth-generation tensor cores, head_dims 64 and 128.
+//
+// The split kernels dequantise every cached row once per 32 columns (a column
+// being one (new token, q-head) of a kv-head), which is what a chunk of
+// hundreds of columns spends its time on.  Here the rows are expanded once:
+//
+//  1. plan     which sequences are wide (more new tokens than `wide`), their
+//              128-row tiles and 256-column blocks, as prefix sums;
+//  2. expand   every (128-row tile, kv-head) becomes two f16 operand tiles in
+//              the workspace, laid out as the images that the tensor cores
+//              read from shared memory (128-byte swizzle; keys K-major, values
+//              MN-major), so that a tile is one linear copy;
+//  3. attend   persistent CTAs of two 128-column groups: one warp copies
+//              tiles, one issues the MMAs, two warpgroups run the softmax (a
+//              thread per column);
+//  4. merge    of the few blocks that two or more CTAs shared.
+//
+// Range.  f16 has 11 bits and a narrow exponent, so every key tile is scaled
+// by a power of two that puts its largest finite |k| in [2^13, 2^14) (undone on
+// the scores) and every value tile likewise; the value exponent e of a tile is
+// added to the base-2 scores, so that one accumulator holds
+//   O = sum_t 2^(s_t + e - R + 6) (v_t 2^-e),   l = sum_t 2^(s_t + e - R + 6) 2^-e
+// for any mixture of tiles, and O / l needs no correction.  The roundings are
+// those of k, v and p to f16 (2^-11 each), below the bf16 output's 2^-8.
+// The reference R follows the running maximum of s + e lazily: it is raised
+// (and O rescaled) only when the maximum has grown by more than 2^8, so that
+// the weights stay within [0, 2^14] and keep 11 bits down to 2^-20 of the
+// largest.
+//
+// A value row with an infinity or NaN would spoil the sums of columns that do
+// not see it (0 * inf), so expand writes zeros there and a bit mask; a column
+// that sees a marked row gets NaN through l.
+#include "tq_common.cuh"
+#include "tq_kernels.h"
+#include "tq_paged.cuh"
+#include "tq_tcgen05.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int wT = 128;    // rows per tile
+constexpr int wC = 256;    // columns per block (two groups of the MMA's 128)
+constexpr int wThreads = 320;
+constexpr float wTau = 8.0f, wUp = 6.0f;  // lazy raise of R; weights are 2^(s - R + wUp)
+
+// What expand says about a tile.
+struct __align__(16) TileMeta {
+    float kf;       // 2^-ek: scores are (q k~) kf
+    float e;        // the value tile's exponent: v = v~ 2^e
+    float lf;       // 2^-e
+    uint32_t any;   // some value row is not finite
+    uint32_t bad[4];
+};
+
+struct WidePlan {        // device arrays, written by plan
+    int32_t *tile0;      // [seqs + 1] scratch tiles before a sequence
+    int32_t *entry0;     // [seqs + 1] blocks before it
+    int64_t *before;     // [entries + 1] tiles of the blocks before an entry (one kv-head's)
+    int64_t *line;       // total stages of the line, stages per CTA
+};
+
+struct WideParams {
+    PagedSplit pg;
+    WidePlan pl;
+    int64_t max_tiles, max_entries;  // room in the workspace
+    const uint8_t *k_codes, *v_codes;
+    const uint16_t *k_scale, *k_zero, *v_scale;
+    const uint16_t *q;
+    uint16_t *out;
+    TileMeta *meta;      // [tile][H]
+    uint8_t *tiles;      // [tile][H][keys, values]
+    float *part_o, *part_ml;  // [2 CTAs][256][D], [..][256][2]
+    uint32_t *err;
+    int H, QH, G, kb, vb, ctas;
+    float scale_log2;    // |softmax scale| * log2(e); its sign goes into q
+    float qsign, kcmax, cmax, inv_sqrt_d;
+    SignBits sg;
+    float cen[256];
+};
+
+template <int D>
+struct WideGeo {
+    static constexpr int KT = wT * D * 2;  // bytes of one operand tile
+    static constexpr int NK = D == 128 ? 2 : 4, NV = NK;  // tiles in flight
+    static constexpr int OFF_K = 2 * KT, OFF_V = OFF_K + NK * KT, OFF_BAR = OFF_V + NV * KT;
+    static constexpr int SMEM = 1024 + OFF_BAR + 256;
+    static constexpr int O_COL = 2 * wT;   // tensor memory: S (then P) of both groups, then O of both
+};
+
+// ---------------------------------------------------------------- plan
+__device__ __forceinline__ int64_t block_exclusive_sum(int64_t x, int64_t &total, int64_t *sh)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int64_t in = warp_inclusive_sum(x, lane);
+    __syncthreads();  // the previous call's readers are done with sh
+    if (lane == 31) sh[warp] = in;
+    __syncthreads();
+    int64_t base = 0;
+    total = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w < warp) base += sh[w];
+        total += sh[w];
+    }
+    return base + in - x;
+}
+
+// Tiles that block b of a sequence reads: up to its last column's limit (one
+// at least, so that a column that sees nothing is written too).
+__device__ __forceinline__ int64_t block_tiles(int64_t len, int64_t n, int G, int64_t b)
+{
+    const int64_t cols = n * G, last = (cols < (b + 1) * wC ? cols : (b + 1) * wC) - 1;
+    const int64_t lim = len - n + 1 + last / G, t = (lim + wT - 1) / wT;
+    return t < 1 ? 1 : t;
+}
+
+__global__ void __launch_bounds__(1024) wide_plan_kernel(const __grid_constant__ WideParams p)
+{
+    __shared__ int64_t sh[32];
+    pdl_wait_primary();
+    pdl_allow_dependents();
+    const int S = p.pg.v.seqs;
+    int64_t tiles = 0, entries = 0;
+    for (int s0 = 0; s0 < S; s0 += blockDim.x) {
+        const int s = s0 + threadIdx.x;
+        int64_t t = 0, e = 0, all;
+        if (s < S) {
+            const int64_t n = paged_new(p.pg.v, s);
+            if (n > p.pg.wide) {
+                const int64_t len = paged_len(p.pg.v, s);
+                t = len > 0 ? (len + wT - 1) / wT : 1;
+                e = (n * p.G + wC - 1) / wC;
+            }
+        }
+        const int64_t at = tiles + block_exclusive_sum(t, all, sh);
+        tiles += all;
+        const int64_t ae = entries + block_exclusive_sum(e, all, sh);
+        entries += all;
+        // sequences for which the bounds that the workspace was sized by left no room get nothing
+        if (s < S) {
+            if (e > 0 && (at + t > p.max_tiles || ae + e > p.max_entries)) atomicOr(p.err, kErrLength);
+            p.pl.tile0[s] = (int32_t)imin64(at, p.max_tiles);
+            p.pl.entry0[s] = (int32_t)imin64(ae, p.max_entries);
+        }
+    }
+    const bool room = tiles <= p.max_tiles && entries <= p.max_entries;
+    if (!room) tiles = entries = 0;
+    if (threadIdx.x == 0) {
+        p.pl.tile0[S] = (int32_t)tiles;
+        p.pl.entry0[S] = (int32_t)entries;
+    }
+    __syncthreads();  // tile0, entry0 are read back below (same block)
+    int64_t line = 0;
+    for (int64_t e0 = 0; e0 < entries; e0 += blockDim.x) {
+        const int64_t e = e0 + threadIdx.x;
+        int64_t t = 0, all;
+        if (e < entries) {
+            int lo = 0, hi = S;  // the last sequence with entry0 <= e
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (p.pl.entry0[mid] <= e) lo = mid;
+                else hi = mid - 1;
+            }
+            t = block_tiles(paged_len(p.pg.v, lo), paged_new(p.pg.v, lo), p.G, e - p.pl.entry0[lo]);
+        }
+        const int64_t at = line + block_exclusive_sum(t, all, sh);
+        line += all;
+        if (e < entries) p.pl.before[e] = at;
+    }
+    if (threadIdx.x == 0) {
+        p.pl.before[entries] = line;
+        const int64_t total = line * p.H;
+        int64_t per = (total + p.ctas - 1) / p.ctas;
+        p.pl.line[0] = total;
+        p.pl.line[1] = per < 1 ? 1 : per;
+    }
+}
+
+// A place on the line: sequence after sequence, in a sequence kv-head after
+// kv-head (CTAs of one head are neighbours, and share its tiles in L2), then
+// block after block, then tile after tile.
+struct WidePlace {
+    int s, h, e, tile, tiles;  // entry (block) and tile in it; tiles of the block
+    int64_t at;                // line position of the block's first tile
+};
+
+__device__ __forceinline__ WidePlace wide_locate(const WideParams &p, int64_t x)
+{
+    WidePlace w;
+    int lo = 0, hi = p.pg.v.seqs - 1;  // the last sequence that starts at or before x
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.pl.before[p.pl.entry0[mid]] * p.H <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    w.s = lo;
+    const int e0 = p.pl.entry0[lo], e1 = p.pl.entry0[lo + 1];
+    const int64_t b0 = p.pl.before[e0], sum = p.pl.before[e1] - b0, y = x - b0 * p.H;
+    w.h = (int)(y / sum);
+    const int64_t z = y - w.h * sum + b0;  // within one head's blocks
+    int a = e0, b = e1 - 1;
+    while (a < b) {
+        const int mid = (a + b + 1) >> 1;
+        if (p.pl.before[mid] <= z) a = mid;
+        else b = mid - 1;
+    }
+    w.e = a;
+    w.tile = (int)(z - p.pl.before[a]);
+    w.tiles = (int)(p.pl.before[a + 1] - p.pl.before[a]);
+    w.at = x - w.tile;
+    return w;
+}
+
+// ---------------------------------------------------------------- expand
+template <int D>
+__global__ void __launch_bounds__(256) wide_expand_kernel(const __grid_constant__ WideParams p)
+{
+    constexpr int NG = D / 32, C8 = D / 8, KT = WideGeo<D>::KT;
+    __shared__ float lut[256];
+    __shared__ int64_t rows[wT];   // plane row of each tile row (-1: none)
+    __shared__ float red[2][8];
+    __shared__ uint32_t bad[4];
+    pdl_wait_primary();
+    pdl_allow_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < (1 << p.vb); i += 256) lut[i] = p.cen[i];
+    const int S = p.pg.v.seqs, rbk = D * p.kb / 8, rbv = D * p.vb / 8;
+    const int64_t items = (int64_t)p.pl.tile0[S] * p.H;
+    const float magic = p.kb == 8 ? 8388736.0f : 8388608.0f;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int tile = (int)(item / p.H), h = (int)(item - (int64_t)tile * p.H);
+        int lo = 0, hi = S - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.pl.tile0[mid] <= tile) lo = mid;
+            else hi = mid - 1;
+        }
+        const int64_t t0 = (int64_t)(tile - p.pl.tile0[lo]) * wT, len = paged_len(p.pg.v, lo);
+        __syncthreads();  // the previous item is done with rows, red and bad
+        if (tid < 4) bad[tid] = 0;
+        if (tid < wT) {
+            int64_t r = -1;
+            if (t0 + tid < len) {
+                uint32_t slot;
+                const int pg = paged_page(p.pg.v, lo, (uint32_t)(t0 + tid), slot);
+                if (pg >= 0) r = ((int64_t)pg * p.H + h) * p.pg.v.page + slot;
+            }
+            rows[tid] = r;
+        }
+        __syncthreads();
+        // bounds of the finite groups, and the value rows that are not finite
+        float bk = 0.0f, bv = 0.0f;
+        for (int i = tid; i < wT * NG; i += 256) {
+            const int64_t r = rows[i / NG];
+            if (r < 0) continue;
+            const int64_t mi = r * NG + i % NG;
+            const float b = fabsf(f16_bits_to_f32(p.k_scale[mi])) * (fabsf(f16_bits_to_f32(p.k_zero[mi])) + p.kcmax);
+            const float v = fabsf(f16_bits_to_f32(p.v_scale[mi]));
+            if (b < INFINITY) bk = fmaxf(bk, b);
+            if (v < INFINITY) bv = fmaxf(bv, v);
+            else atomicOr(&bad[(i / NG) >> 5], 1u << ((i / NG) & 31));
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            bk = fmaxf(bk, __shfl_xor_sync(0xffffffffu, bk, o));
+            bv = fmaxf(bv, __shfl_xor_sync(0xffffffffu, bv, o));
+        }
+        if (lane == 0) {
+            red[0][warp] = bk;
+            red[1][warp] = bv;
+        }
+        __syncthreads();
+        bk = bv = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            bk = fmaxf(bk, red[0][w]);
+            bv = fmaxf(bv, red[1][w]);
+        }
+        // a tile of zeros takes the exponent of one whose largest value is 1
+        const int ek = tile_exponent(bk), ev = tile_exponent(bv > 0.0f ? bv * p.cmax : 1.0f);
+        const float sk = ldexpf(1.0f, ek), sv2 = ldexpf(1.0f, ev);
+        uint8_t *dst = p.tiles + item * (2 * KT);
+        if (tid == 0) {
+            TileMeta m;
+            m.kf = ldexpf(1.0f, -ek);
+            m.e = (float)-ev;
+            m.lf = sv2;
+            m.any = bad[0] | bad[1] | bad[2] | bad[3];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m.bad[i] = bad[i];
+            p.meta[item] = m;
+        }
+        for (int it = tid; it < wT * C8; it += 256) {
+            const int t = it / C8, c8 = it - t * C8, g = c8 >> 2;
+            const int64_t r = rows[t];
+            uint4 k4 = make_uint4(0u, 0u, 0u, 0u), v4 = k4;
+            if (r >= 0) {
+                const float sc = f16_bits_to_f32(p.k_scale[r * NG + g]) * sk;
+                const float cz = magic - f16_bits_to_f32(p.k_zero[r * NG + g]);
+                const int kbyte = c8 * p.kb;
+                const uint32_t *ka = reinterpret_cast<const uint32_t *>(p.k_codes + r * rbk + (kbyte & ~3));
+                const uint32_t k0 = ka[0], k1 = (kbyte & 3) + p.kb > 4 ? ka[1] : 0u;
+                float x[8];
+                key_values<0>(k0, k1, (kbyte & 3) * 8, p.kb, sc, cz, x);
+                k4 = make_uint4(tc_pack_f16(x[0], x[1]), tc_pack_f16(x[2], x[3]), tc_pack_f16(x[4], x[5]), tc_pack_f16(x[6], x[7]));
+                const float sv = f16_bits_to_f32(p.v_scale[r * NG + g]) * sv2;
+                if (!((bad[t >> 5] >> (t & 31)) & 1u)) {
+                    const int vbit = 8 * c8 * p.vb;
+                    const uint32_t *va = reinterpret_cast<const uint32_t *>(p.v_codes + r * rbv) + (vbit >> 5);
+                    const uint32_t v0 = va[0], v1 = (vbit & 31) + 8 * p.vb > 32 ? va[1] : 0u;
+                    value_values<0>(v0, v1, vbit & 31, p.vb, sv, smem_addr(lut), x);
+                    v4 = make_uint4(tc_pack_f16(x[0], x[1]), tc_pack_f16(x[2], x[3]), tc_pack_f16(x[4], x[5]), tc_pack_f16(x[6], x[7]));
+                }
+            }
+            *reinterpret_cast<uint4 *>(dst + kmaj_off(wT, t, 8 * c8)) = k4;
+            *reinterpret_cast<uint4 *>(dst + KT + mnmaj_off<D>(t, 8 * c8)) = v4;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- attend
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Tensor memory holds S of both groups (128 columns each; P, f16, overwrites
+// its first half) and O of both.  In one pass over a tile the issuing warp
+// queues O_a += P_a V, S_a = Q_a K(next), then the same for the other group, so
+// that one group's softmax runs under the other's products.  MMAs of one
+// thread execute in order: S(t) complete says that P V(t - 1) is complete, so
+// the softmax threads may rescale O between reading S(t) and handing over P(t)
+// without a barrier of its own.
+template <int D>
+__global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_constant__ WideParams p)
+{
+    using A = WideGeo<D>;
+    constexpr int KT = A::KT, NK = A::NK, NV = A::NV;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + A::OFF_BAR);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 2 * NK + 2 * NV + 9);
+    const uint32_t sb = smem_addr(smem), b0 = smem_addr(bars);
+    const uint32_t kfull = b0, kempty = kfull + 8 * NK, vfull = kempty + 8 * NK, vempty = vfull + 8 * NV;
+    const uint32_t qfull = vempty + 8 * NV, sfull = qfull + 16, pfull = sfull + 16, ofull = pfull + 16, drained = ofull + 16;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    pdl_wait_primary();
+    pdl_allow_dependents();
+    const int64_t total = p.pl.line[0], per = p.pl.line[1];
+    const int64_t x0 = blockIdx.x * per, x1 = imin64(total, x0 + per);
+    if (x0 >= x1) return;
+    if (tid == 0) {
+        for (int i = 0; i < 2 * NK + 2 * NV; ++i) mbar_init(b0 + 8 * i, 1);
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(qfull + 8 * g, 128);
+            mbar_init(sfull + 8 * g, 1);
+            mbar_init(pfull + 8 * g, 128);
+            mbar_init(ofull + 8 * g, 1);
+        }
+        mbar_init(drained, 1);
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tslot)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+
+    if (warp == 9) {
+        // ------------------------------------------------------------ tiles in
+        if (lane == 0) {
+            bool ok = true;
+            uint32_t it = 0;
+            for (int64_t x = x0; x < x1 && ok;) {
+                const WidePlace w = wide_locate(p, x);
+                const int n = (int)imin64(w.tiles - w.tile, x1 - x);
+                const int64_t scratch = p.pl.tile0[w.s] + w.tile;
+                for (int t = 0; t < n && ok; ++t, ++it) {
+                    const uint8_t *src = p.tiles + ((scratch + t) * p.H + w.h) * (2 * KT);
+                    const uint32_t ks = it % NK, vs = it % NV;
+                    if (it >= NK) ok = mbar_wait_bounded(kempty + 8 * ks, (it / NK - 1) & 1, p.err);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(kfull + 8 * ks, KT);
+                    bulk_g2s(sb + A::OFF_K + ks * KT, src, KT, kfull + 8 * ks);
+                    if (it >= NV) ok = mbar_wait_bounded(vempty + 8 * vs, (it / NV - 1) & 1, p.err);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(vfull + 8 * vs, KT);
+                    bulk_g2s(sb + A::OFF_V + vs * KT, src + KT, KT, vfull + 8 * vs);
+                }
+                x += n;
+            }
+            if (!ok) {  // copies still in flight land before the CTA ends (bounded)
+                for (uint32_t i = it > (uint32_t)NK ? it - NK : 0; i <= it; ++i) {
+                    mbar_wait_bounded(kfull + 8 * (i % NK), (i / NK) & 1, p.err);
+                    if (i < it) mbar_wait_bounded(vfull + 8 * (i % NV), (i / NV) & 1, p.err);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ MMAs
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = tc_idesc(128, wT, 0), idesc_pv = tc_idesc(128, D, 1), SBO = (D / 64) * 1024;
+            auto qk = [&](int g, uint32_t ks) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = (kk / 4) * (wT * 128) + (kk % 4) * 32;
+                    tc_mma(tmem + g * wT, tc_desc(sb + g * KT + o, 16, 1024), tc_desc(sb + A::OFF_K + ks * KT + o, 16, 1024),
+                           idesc_qk, kk > 0);
+                }
+                tc_commit(sfull + 8 * g);
+            };
+            auto pv = [&](int g, uint32_t vs, bool acc) {
+#pragma unroll
+                for (int kk = 0; kk < wT / 16; ++kk)
+                    tc_mma_ts(tmem + A::O_COL + g * D, tmem + g * wT + kk * 8,
+                              tc_desc(sb + A::OFF_V + vs * KT + kk * 2 * SBO, 1024, SBO), idesc_pv, acc || kk > 0);
+            };
+            bool ok = true;
+            uint32_t it = 0, seg = 0;
+            for (int64_t x = x0; x < x1 && ok; ++seg) {
+                const WidePlace w = wide_locate(p, x);
+                const int n = (int)imin64(w.tiles - w.tile, x1 - x);
+                const int64_t cols = paged_new(p.pg.v, w.s) * p.G - (int64_t)(w.e - p.pl.entry0[w.s]) * wC;
+                const int groups = cols > 128 ? 2 : 1;
+                ok = mbar_wait_bounded(kfull + 8 * (it % NK), (it / NK) & 1, p.err);
+                for (int g = 0; g < groups && ok; ++g) {
+                    ok = mbar_wait_bounded(qfull + 8 * g, seg & 1, p.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    qk(g, it % NK);
+                }
+                if (groups == 1 && ok) {  // the idle group's threads keep step through the same barriers
+                    ok = mbar_wait_bounded(qfull + 8, seg & 1, p.err);
+                    tc_commit(sfull + 8);
+                }
+                if (!ok) break;
+                tc_commit(kempty + 8 * (it % NK));
+                for (int t = 0; t < n && ok; ++t, ++it) {
+                    const bool more = t + 1 < n;
+                    const uint32_t vs = it % NV, nk = (it + 1) % NK;
+                    ok = mbar_wait_bounded(vfull + 8 * vs, (it / NV) & 1, p.err);
+                    for (int g = 0; g < groups && ok; ++g) {
+                        ok = mbar_wait_bounded(pfull + 8 * g, it & 1, p.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        pv(g, vs, t > 0);
+                        if (g == groups - 1) tc_commit(vempty + 8 * vs);
+                        if (more) {
+                            if (g == 0) ok = mbar_wait_bounded(kfull + 8 * nk, ((it + 1) / NK) & 1, p.err);
+                            if (!ok) break;
+                            qk(g, nk);
+                        } else {
+                            tc_commit(ofull + 8 * g);
+                        }
+                    }
+                    if (groups == 1 && ok) {
+                        ok = mbar_wait_bounded(pfull + 8, it & 1, p.err);
+                        if (more) tc_commit(sfull + 8);
+                        else tc_commit(ofull + 8);
+                    }
+                    if (more && ok) tc_commit(kempty + 8 * nk);
+                }
+                x += n;
+            }
+            if (!ok) {  // whatever was issued is through before tensor memory is given back (bounded)
+                tc_commit(drained);
+                mbar_wait_bounded(drained, 0, p.err);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax, one column a thread
+        const int g = warp >> 2, ltid = tid & 127;
+        const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t t_s = tmem + g * wT + lane_at, t_o = tmem + A::O_COL + g * D + lane_at;
+        const uint32_t bar_s = sfull + 8 * g, bar_p = pfull + 8 * g;
+        bool ok = true;
+        uint32_t it = 0, seg = 0;
+        for (int64_t x = x0; x < x1 && ok; ++seg) {
+            const WidePlace w = wide_locate(p, x);
+            const int n = (int)imin64(w.tiles - w.tile, x1 - x);
+            const int64_t nn = paged_new(p.pg.v, w.s), len = paged_len(p.pg.v, w.s);
+            const int64_t col = (int64_t)(w.e - p.pl.entry0[w.s]) * wC + 128 * g + ltid;
+            const bool real = col < nn * p.G;
+            const int64_t tok = real ? col / p.G : nn - 1, row = paged_start(p.pg.v, w.s) + tok;
+            const int hq = real ? (int)(col - tok * p.G) : 0;
+            const int64_t lim = len - nn + 1 + tok;  // rows that this column sees
+            // q, scaled by a power of two that puts its largest |q| in [2^14, 2^15): exact in f16
+            float ie;
+            {
+                const uint16_t *qrow = p.q + row * p.pg.q_token + ((int64_t)w.h * p.G + hq) * p.pg.q_head;
+                float mx = 0.0f;
+                if (real)
+                    for (int c8 = 0; c8 < D / 8; ++c8) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(qrow + 8 * c8);
+                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx = max3(mx, fabsf(bf16_lo(uu[i])), fabsf(bf16_hi(uu[i])));
+                    }
+                int e = 0;
+                if (mx > 0.0f && mx < INFINITY) e = 14 - (((int)(__float_as_uint(mx) >> 23) & 0xFF) - 127);
+                e = e < -100 ? -100 : (e > 100 ? 100 : e);
+                const float qs = ldexpf(p.qsign, e);
+                ie = ldexpf(1.0f, -e) * p.scale_log2;
+                for (int c8 = 0; c8 < D / 8; ++c8) {
+                    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                    if (real) u = *reinterpret_cast<const uint4 *>(qrow + 8 * c8);
+                    sts128(sb + g * KT + kmaj_off(128, ltid, 8 * c8),
+                           make_uint4(tc_pack_f16(bf16_lo(u.x) * qs, bf16_hi(u.x) * qs),
+                                      tc_pack_f16(bf16_lo(u.y) * qs, bf16_hi(u.y) * qs),
+                                      tc_pack_f16(bf16_lo(u.z) * qs, bf16_hi(u.z) * qs),
+                                      tc_pack_f16(bf16_lo(u.w) * qs, bf16_hi(u.w) * qs)));
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(qfull + 8 * g);
+
+            const TileMeta *meta = p.meta + ((int64_t)(p.pl.tile0[w.s] + w.tile) * p.H + w.h);
+            float R = -INFINITY, l = 0.0f;
+            for (int t = 0; t < n; ++t, ++it) {
+                const TileMeta *mt = meta + (int64_t)t * p.H;
+                const float f = ie * mt->kf, e = mt->e, lf = mt->lf;
+                const uint32_t any = mt->any;
+                const int64_t left = lim - (int64_t)(w.tile + t) * wT;
+                const int vis = left < 0 ? 0 : (left > wT ? wT : (int)left);
+                if (!mbar_wait_bounded(bar_s, it & 1, p.err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t sr[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc_ld32(t_s + 32 * c, sr[c]);
+                tc_wait_ld();
+                const bool cut = __any_sync(0xffffffffu, vis < wT);
+                if (cut)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (32 * c + j >= vis) sr[c][j] = 0xFF800000u;
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) m4[c] = max3(m4[c], __uint_as_float(sr[c][j]), __uint_as_float(sr[c][j + 1]));
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                const float top = mx == -INFINITY ? -INFINITY : fmaf(mx, f, e);
+                if (t == 0) {
+                    R = top;
+                } else if (__any_sync(0xffffffffu, top > R + wTau)) {
+                    const float Rn = top > R + wTau ? top : R;
+                    const float a = R == -INFINITY ? 0.0f : tc_ex2(R - Rn);  // nothing was summed before the first row seen
+                    R = Rn;
+                    l *= a;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tc_ld32(t_o + 32 * c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
+                        uint32_t lo[16], hi[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            lo[j] = o[j];
+                            hi[j] = o[16 + j];
+                        }
+                        tc_st16(t_o + 32 * c, lo);
+                        tc_st16(t_o + 32 * c + 16, hi);
+                    }
+                }
+                const float add = R == -INFINITY ? 0.0f : e - R + wUp;
+                const float2 f2 = make_float2(f, f), a2 = make_float2(add, add);
+                float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pp[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[c][j]), __uint_as_float(sr[c][j + 1])), f2, a2);
+                        float p0 = tc_ex2(y.x), p1 = tc_ex2(y.y);
+                        if (cut) {
+                            if (32 * c + j >= vis) p0 = 0.0f;
+                            if (32 * c + j + 1 >= vis) p1 = 0.0f;
+                        }
+                        ls[(j >> 1) & 1] = __fadd2_rn(ls[(j >> 1) & 1], make_float2(p0, p1));
+                        pp[j / 2] = tc_pack_f16(p0, p1);
+                    }
+                    tc_st16(t_s + 16 * c, pp);
+                }
+                l = fmaf((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y), lf, l);
+                if (any) {
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        const int rows = vis - 32 * i;
+                        const uint32_t seen = rows >= 32 ? 0xFFFFFFFFu : (rows <= 0 ? 0u : (1u << rows) - 1u);
+                        if (mt->bad[i] & seen) l = NAN;
+                    }
+                }
+                tc_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar_p);
+            }
+            if (ok) ok = mbar_wait_bounded(ofull + 8 * g, seg & 1, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            float o[D];
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) tc_ld32(t_o + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&o[32 * c]));
+            tc_wait_ld();
+            tc_fence_before();
+            if (n == w.tiles) {
+                // the whole block: un-rotate (Sylvester stages 1, 2, 4, ...), divide, round
+#pragma unroll
+                for (int hs = 1; hs < D; hs <<= 1)
+#pragma unroll
+                    for (int k = 0; k < D; k += 2 * hs)
+#pragma unroll
+                        for (int j = k; j < k + hs; ++j) {
+                            const float u = o[j], v = o[j + hs];
+                            o[j] = u + v;
+                            o[j + hs] = u - v;
+                        }
+                if (real) {
+                    const float inv = l == 0.0f ? 0.0f : p.inv_sqrt_d / l;
+                    uint16_t *dst = p.out + (row * p.QH + (int64_t)w.h * p.G + hq) * D;
+#pragma unroll
+                    for (int j = 0; j < D; j += 8) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            u[i] = pack_bf16x2(o[j + 2 * i] * (sign_negative(p.sg, j + 2 * i) ? -inv : inv),
+                                               o[j + 2 * i + 1] * (sign_negative(p.sg, j + 2 * i + 1) ? -inv : inv));
+                        *reinterpret_cast<uint4 *>(dst + j) = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                }
+            } else {
+                // a share of a block: slot 2 c of a CTA when the block began in an earlier one, else 2 c + 1
+                const int64_t at = ((int64_t)2 * blockIdx.x + (w.tile == 0 ? 1 : 0)) * wC + 128 * g + ltid;
+                float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D);
+#pragma unroll
+                for (int j = 0; j < D; j += 4) dst[j / 4] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                p.part_ml[2 * at] = R - wUp;  // R = -inf (nothing seen): weight 0
+                p.part_ml[2 * at + 1] = l;
+            }
+            x += n;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ---------------------------------------------------------------- merge
+// Block c merges the shares of the block that CTA c began and did not finish,
+// a warp per column (256 columns over gridDim.y x 8 warps).
+template <int D>
+__global__ void __launch_bounds__(256) wide_merge_kernel(const __grid_constant__ WideParams p)
+{
+    constexpr int PER = D / 32;
+    pdl_wait_primary();
+    pdl_allow_dependents();
+    const int64_t total = p.pl.line[0], per = p.pl.line[1], c = blockIdx.x, x1 = (c + 1) * per;
+    if (x1 >= total) return;
+    const WidePlace w = wide_locate(p, x1);
+    if (w.tile == 0 || w.at < c * per) return;  // nothing runs on past CTA c, or it began before c
+    const int64_t last = (w.at + w.tiles - 1) / per, nn = paged_new(p.pg.v, w.s);
+    const int lane = threadIdx.x & 31;
+    for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < wC; i += gridDim.y * 8) {
+        const int64_t col = (int64_t)(w.e - p.pl.entry0[w.s]) * wC + i;
+        if (col >= nn * p.G) break;
+        auto slot = [&](int64_t k) { return (k == c ? 2 * c + 1 : 2 * k) * wC + i; };
+        float m = -INFINITY;
+        for (int64_t k = c + lane; k <= last; k += 32) m = fmaxf(m, p.part_ml[2 * slot(k)]);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float mu = m == -INFINITY ? 0.0f : m;
+        float l = 0.0f, x[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) x[k] = 0.0f;
+#pragma unroll 4
+        for (int64_t k = c; k <= last; ++k) {
+            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(k));
+            const float wt = tc_ex2(ml.x - mu);
+            l += ml.y * wt;
+            const float *src = p.part_o + slot(k) * D + PER * lane;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) x[j] += src[j] * wt;
+        }
+        fwht_warp<PER>(x, lane);
+        const float inv = l == 0.0f ? 0.0f : p.inv_sqrt_d / l;
+        const int64_t tok = col / p.G, row = paged_start(p.pg.v, w.s) + tok;
+        uint32_t u[PER / 2];
+#pragma unroll
+        for (int k = 0; k < PER; k += 2)
+            u[k / 2] = pack_bf16x2(x[k] * (sign_negative(p.sg, PER * lane + k) ? -inv : inv),
+                                   x[k + 1] * (sign_negative(p.sg, PER * lane + k + 1) ? -inv : inv));
+        store_words<PER / 2, 2 * PER>(p.out + (row * p.QH + (int64_t)w.h * p.G + (col - tok * p.G)) * D + PER * lane, u);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+struct WideSizes {
+    int64_t tiles, entries;
+    size_t off_tile0, off_entry0, off_before, off_line, off_meta, off_ml, off_o, off_tiles, bytes;
+};
+
+WideSizes wide_sizes(const CacheView &c, const PagedBounds &b, int QH)
+{
+    WideSizes z{};
+    const int64_t G = QH / c.H;
+    const int64_t most = imin64(b.seqs, b.total / (b.wide + 1));  // sequences that can be wide
+    z.tiles = imin64(most * ((b.max_len + wT - 1) / wT), b.total_len / wT + most);
+    z.entries = b.total * G / wC + most;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t o = at;
+        at += (n + 255) / 256 * 256;
+        return o;
+    };
+    const size_t slots = 2 * (size_t)num_sms() * wC;
+    z.off_tile0 = take((size_t)(b.seqs + 1) * 4);
+    z.off_entry0 = take((size_t)(b.seqs + 1) * 4);
+    z.off_before = take((size_t)(z.entries + 1) * 8);
+    z.off_line = take(16);
+    z.off_meta = take((size_t)z.tiles * c.H * sizeof(TileMeta));
+    z.off_ml = take(slots * 8);
+    z.off_o = take(slots * c.d * 4);
+    z.off_tiles = take((size_t)z.tiles * c.H * 2 * wT * c.d * 2);
+    z.bytes = at;
+    return z;
+}
+
+template <int D>
+cudaError_t wide_run(WideParams &p, cudaStream_t s)
+{
+    using A = WideGeo<D>;
+    cudaError_t e = cudaFuncSetAttribute(wide_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(wide_plan_kernel, dim3(1), dim3(1024), 0, s, p);
+    if (e != cudaSuccess) return e;
+    const int64_t items = p.max_tiles * p.H;
+    e = launch_dependent(wide_expand_kernel<D>, dim3((unsigned)imin64(items, (int64_t)num_sms() * 8)), dim3(256), 0, s, p);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(wide_attend_kernel<D>, dim3((unsigned)p.ctas), dim3(wThreads), A::SMEM, s, p);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(wide_merge_kernel<D>, dim3((unsigned)p.ctas, 4), dim3(256), 0, s, p);
+}
+
+}  // namespace
+
+bool paged_wide_applies(const CacheView &c) { return c.d == 64 || c.d == 128; }
+
+size_t paged_wide_workspace_bytes(const CacheView &c, const PagedBounds &b, int QH) { return wide_sizes(c, b, QH).bytes; }
+
+cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const PagedBounds &b, const uint16_t *q, int QH,
+                              float scale, uint16_t *out, void *ws, cudaStream_t s)
+{
+    const WideSizes z = wide_sizes(c, b, QH);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    WideParams p{};
+    p.pg = pg;
+    p.pl = WidePlan{reinterpret_cast<int32_t *>(w + z.off_tile0), reinterpret_cast<int32_t *>(w + z.off_entry0),
+                    reinterpret_cast<int64_t *>(w + z.off_before), reinterpret_cast<int64_t *>(w + z.off_line)};
+    p.max_tiles = z.tiles;
+    p.max_entries = z.entries;
+    p.k_codes = c.k_codes;
+    p.v_codes = c.v_codes;
+    p.k_scale = c.k_scale;
+    p.k_zero = c.k_zero;
+    p.v_scale = c.v_scale;
+    p.q = q;
+    p.out = out;
+    p.meta = reinterpret_cast<TileMeta *>(w + z.off_meta);
+    p.tiles = w + z.off_tiles;
+    p.part_o = reinterpret_cast<float *>(w + z.off_o);
+    p.part_ml = reinterpret_cast<float *>(w + z.off_ml);
+    p.err = pg.v.err;
+    p.H = c.H;
+    p.QH = QH;
+    p.G = QH / c.H;
+    p.kb = c.kb;
+    p.vb = c.vb;
+    p.ctas = num_sms();
+    p.scale_log2 = fabsf(scale) * 1.4426950408889634f;
+    p.qsign = scale < 0.0f ? -1.0f : 1.0f;
+    p.kcmax = c.kb == 8 ? 127.0f : (float)((1 << c.kb) - 1);
+    p.inv_sqrt_d = inv_sqrt_head_dim(c.d);
+    p.sg = c.signs;
+    const Tables &tab = codebook_tables(c.vb);
+    for (int i = 0; i < (1 << c.vb); ++i) {
+        p.cen[i] = tab.centroids[i];
+        p.cmax = p.cmax > fabsf(tab.centroids[i]) ? p.cmax : fabsf(tab.centroids[i]);
+    }
+    return c.d == 64 ? wide_run<64>(p, s) : wide_run<128>(p, s);
+}
+
+}  // namespace tq

@@ -133,7 +133,10 @@ def check_attention(batch, pool, q, out, lens=None, new=None, scale=None, sign_s
         else:
             want = torch.zeros(m, q.shape[1], q.shape[2], dtype=torch.float64)
         got = out[at:at + m]
-        assert torch.equal(torch.isnan(got), torch.isnan(want)), f"sequence {s}: NaN elsewhere"
+        # Not finite together.  A value row with an infinite rms is +-inf in every rotated dim, and its
+        # un-rotation is inf - inf = NaN except in a dim whose signs happen to agree with all of them;
+        # chunks on the wide kernel give NaN there as well (the header says so).
+        assert torch.equal(torch.isfinite(got), torch.isfinite(want)), f"sequence {s}: not finite elsewhere"
         err = (got - want).abs() - RTOL * want.abs()
         worst = max(worst, float(err.nan_to_num(0.0).max()))
         at += m

@@ -11,7 +11,7 @@ NULL, SHAPE, CAPACITY, ALIGN, WORKSPACE = 1, 4, 5, 6, 7
 
 
 def _table(tqlib, **kw):
-    f = dict(pages=0x100000, seq_lens=0x200000, stride=4, max_len=128, num_seqs=3, reserved=0)
+    f = dict(pages=0x100000, seq_lens=0x200000, stride=4, max_len=128, total_len=0, num_seqs=3, reserved=0)
     f.update(kw)
     return tqlib._PageTableStruct(*[f[n] for n, _ in tqlib._PageTableStruct._fields_])
 
@@ -42,6 +42,7 @@ def test_shared_refusals(tqlib):
     assert calls(pool, _table(tqlib, num_seqs=0)) == {SHAPE}
     assert calls(pool, _table(tqlib, reserved=1)) == {SHAPE}
     assert calls(pool, _table(tqlib, max_len=0)) == {SHAPE}
+    assert calls(pool, _table(tqlib, total_len=-1)) == {SHAPE}
     assert calls(pool, _table(tqlib, max_len=1 << 31, stride=1 << 30)) == {SHAPE}
     assert calls(pool, _table(tqlib, max_len=129)) == {CAPACITY}  # 4 pages of 32 rows hold 128
     assert calls(pool, table, total=-1) == {SHAPE}
