@@ -131,7 +131,7 @@ def _check(status: int, what: str) -> None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -186,14 +186,24 @@ class Cache:
     def planes(self):
         return self.k_codes, self.k_scale, self.k_zero, self.v_codes, self.v_scale
 
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__.pop("_struct", None)  # built again from the new attributes
+
     def struct(self) -> _CacheStruct:
-        return _CacheStruct(self.head_dim, self.k_bits, self.v_bits, self.num_kv_heads, self.batch, 0,
-                            self.capacity, *[t.data_ptr() for t in self.planes()], self.sign_seed)
+        """The C ABI's view of this cache (built once, and again after an attribute is set)."""
+        s = self.__dict__.get("_struct")
+        if s is None:
+            s = _CacheStruct(self.head_dim, self.k_bits, self.v_bits, self.num_kv_heads, self.batch, 0,
+                             self.capacity, *[t.data_ptr() for t in self.planes()], self.sign_seed)
+            self.__dict__["_struct"] = s
+        return s
 
     def batch_slice(self, b0: int, nb: int) -> "Cache":
         """A view of sequences [b0, b0+nb) sharing this cache's storage."""
         v = Cache.__new__(Cache)
         v.__dict__.update(self.__dict__)
+        v.__dict__.pop("_struct", None)
         for name in ("k_codes", "k_scale", "k_zero", "v_codes", "v_scale"):
             setattr(v, name, getattr(self, name)[b0:b0 + nb])
         v.batch = int(nb)
@@ -220,20 +230,32 @@ class PageTable:
         if max_len is None and page_size is None:
             raise ValueError("give max_len, or page_size to bound the lengths by the table's pages")
         _require_cuda(pages, seq_lens)
-        self.pages, self.seq_lens = pages, seq_lens
-        self.num_seqs = int(pages.shape[0])
-        self.max_len = int(pages.shape[1]) * int(page_size) if max_len is None else int(max_len)
+        if pages.device != seq_lens.device:
+            raise ValueError("pages and seq_lens must be on one device")
+        self._pages, self._seq_lens = pages, seq_lens
+        self.num_seqs, self.width = (int(x) for x in pages.shape)
+        self.max_len = self.width * int(page_size) if max_len is None else int(max_len)
         self.total_len = int(total_len)
+        # a table of one sequence has no row to step to: its stride is its pages
+        stride = pages.stride(0) if self.num_seqs > 1 else self.width
+        if stride < self.width:
+            raise ValueError("the rows of the page table overlap")
+        self._struct = _PageTableStruct(pages.data_ptr(), seq_lens.data_ptr(), stride, self.max_len, self.total_len,
+                                        self.num_seqs, 0)
+
+    @property
+    def pages(self) -> torch.Tensor:
+        return self._pages
+
+    @property
+    def seq_lens(self) -> torch.Tensor:
+        return self._seq_lens
 
     def struct(self, pool: "Cache") -> _PageTableStruct:
-        if self.pages.shape[1] * pool.capacity < self.max_len:
-            raise ValueError(f"{self.pages.shape[1]} pages of {pool.capacity} rows do not hold max_len = {self.max_len}")
-        # a table of one sequence has no row to step to: its stride is its pages
-        stride = self.pages.stride(0) if self.num_seqs > 1 else self.pages.shape[1]
-        if stride < self.pages.shape[1]:
-            raise ValueError("the rows of the page table overlap")
-        return _PageTableStruct(self.pages.data_ptr(), self.seq_lens.data_ptr(), stride, self.max_len, self.total_len,
-                                self.num_seqs, 0)
+        """The C ABI's view of the table, for a pool whose pages hold max_len rows."""
+        if self.width * pool.capacity < self.max_len:
+            raise ValueError(f"{self.width} pages of {pool.capacity} rows do not hold max_len = {self.max_len}")
+        return self._struct
 
 
 # ------------------------------------------------------------------ host-side queries
@@ -451,13 +473,16 @@ def _empty_on(stream, shape, dtype, device):
 
 def _paged_args(pool: Cache, table: PageTable, starts: torch.Tensor, *tensors):
     """Checks shared by the paged calls: the starts' form, and one device, the current one, for all."""
-    if starts.dtype != torch.int32 or tuple(starts.shape) != (table.num_seqs + 1,) or not starts.is_contiguous():
+    if starts.dtype != torch.int32 or starts.dim() != 1 or starts.shape[0] != table.num_seqs + 1 or \
+            not starts.is_contiguous():
         raise ValueError("starts must be contiguous int32 [num_seqs + 1]")
-    _require_cuda(pool.k_codes, starts, *tensors)
-    dev = pool.k_codes.device
-    if any(t is not None and t.device != dev for t in (table.pages, table.seq_lens, starts, *tensors)):
-        raise ValueError("the pool, the page table and the tensors must be on one device")
-    if dev.index != torch.cuda.current_device():
+    dev = pool.k_codes.get_device()
+    if dev < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    for t in (table._pages, starts, *tensors):
+        if t is not None and t.get_device() != dev:
+            raise ValueError("the pool, the page table and the tensors must be on one device")
+    if dev != torch.cuda.current_device():
         raise ValueError("the tensors are on another device than the current one")
     return pool.struct(), table.struct(pool)
 

@@ -35,6 +35,8 @@
 #pragma once
 #include <cuda.h>
 
+#include <atomic>
+
 #include "tq_common.cuh"
 #include "tq_kernels.h"
 #include "tq_paged.cuh"
@@ -45,6 +47,7 @@ namespace {
 constexpr int gT = 64;              // tokens per stage
 constexpr int gN = 8;               // q-heads per CTA (the MMA's N)
 constexpr int gMaxStages = 3;
+constexpr int kMaxDynamicSmem = 226 * 1024;  // the opt-in asked for: leaves room for a kernel's static shared memory
 
 struct GenParams {
     const uint8_t *k_codes, *v_codes;
@@ -284,34 +287,37 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     const uint32_t full0 = smem_addr(bars);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    PagedWalk walk;
+    __shared__ PagedWalk walk;  // PAGED only
     if constexpr (PAGED) {
-        if (!walk.start(p.pg, gT, CB, p.H, p.G, lane)) return;
+        if (warp == 0) paged_walk_start(p.pg, walk, gT, CB, p.H, p.G, lane);
+        __syncthreads();
+        if (walk.x >= walk.end) return;
     }
     bool ok = true;
-    int it0 = 0;  // stages this CTA has been through before this segment (ring slots and parities run on)
-    bool more = false;
+    int it0 = 0;        // stages this CTA has been through before this segment (ring slots and parities run on)
+    int nseg = 0;       // segments before it
+    bool more = false;  // another one follows
     do {
-    if constexpr (PAGED) walk.segment(p.pg);
-    const int split = blockIdx.x, h = PAGED ? walk.h : blockIdx.y / p.HB, hb = PAGED ? walk.hb : blockIdx.y - h * p.HB,
+    const PagedSegment &seg = walk.seg[nseg & 1];
+    const int split = blockIdx.x, h = PAGED ? seg.h : blockIdx.y / p.HB, hb = PAGED ? seg.hb : blockIdx.y - h * p.HB,
               b = blockIdx.z;
     const int64_t bh = (int64_t)b * p.H + h;
-    const int M = PAGED ? (int)walk.n : p.M, cols = PAGED ? (int)walk.n * p.G : p.cols;
-    const int64_t base0 = PAGED ? walk.len - walk.n + 1 : p.base0;
+    const int M = PAGED ? seg.n : p.M, cols = PAGED ? seg.n * p.G : p.cols;
+    const int64_t base0 = PAGED ? seg.len - seg.n + 1 : p.base0;
     // columns col0 .. col0 + CB - 1; column col is query row col / G, q-head
     // h G + col % G; query row i sees cache rows [0, base0 + i)
     const int col0 = hb * CB;
     const int col_last = (cols < col0 + CB ? cols : col0 + CB) - 1;
     const int64_t lim_lo = base0 + col0 / p.G, lim_hi = base0 + col_last / p.G;
-    const int64_t t_begin = PAGED ? (int64_t)walk.first * gT : (int64_t)split * p.tokens_per_split;
-    const int64_t t_end = imin64(lim_hi, t_begin + (PAGED ? (int64_t)walk.count * gT : p.tokens_per_split));
+    const int64_t t_begin = PAGED ? (int64_t)seg.first * gT : (int64_t)split * p.tokens_per_split;
+    const int64_t t_end = imin64(lim_hi, t_begin + (PAGED ? (int64_t)seg.count * gT : p.tokens_per_split));
     const int n_stages = t_end > t_begin && ok ? (int)((t_end - t_begin + gT - 1) / gT) : 0;
     const int NG = D / 32;
-    PagedPages<gT> pages;
+    PagedPages pages;
 
-    // paged: every lane of the warp calls, with the plane row of its chunk
-    auto issue_paged = [&](int s, int64_t row) {
-        const int slot = (it0 + s) % p.stages, ru = gT / pages.nch;
+    // paged: every lane of the warp calls, with the page of its chunk
+    auto issue_paged = [&](int s, int page) {
+        const int slot = (it0 + s) % p.stages, ru = p.pg.ru;
         const int live = (int)((imin64(gT, t_end - (t_begin + (int64_t)s * gT)) + ru - 1) / ru);  // chunks with rows to read
         const uint32_t kst = smem_addr(stages + slot * p.key_bytes), bar = full0 + 8 * slot;
         const uint32_t st = smem_addr(stages + p.stages * p.key_bytes + slot * p.stage_bytes);
@@ -319,6 +325,7 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
         __syncwarp();
         if (lane < live) {
             const int at = lane * ru;
+            const int64_t row = paged_chunk_plane_row(p.pg, seg, p.H, page, seg.first + s, lane);
             if constexpr (KEY != 0) {
                 using K = KSwz<D, KEY>;
 #pragma unroll
@@ -356,7 +363,7 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
         bulk_g2s(st + p.off_vs, p.v_scale + row0 * NG, rows * NG * 2, bar);
         bulk_g2s(st + p.off_v, p.v_codes + row0 * p.rbv, rows * p.rbv, bar);
     };
-    if (threadIdx.x == 0 && (!PAGED || !more)) {
+    if (threadIdx.x == 0 && (!PAGED || nseg == 0)) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(full0 + 8 * s, 1);
             done[s] = 0;
@@ -366,11 +373,11 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
             for (int s = 0; s < p.stages && s < n_stages; ++s) issue(s);
     }
     if constexpr (PAGED) {
-        pages.start(p.pg, walk, p.H, walk.first, lane);
+        paged_pages_start(p.pg, seg, pages, lane);
         __syncwarp();
         for (int s = 0; s < p.stages && s < n_stages; ++s) {
-            const int64_t row = pages.rows(p.pg, walk, p.H, walk.first + s, lane);
-            if (warp == 0) issue_paged(s, row);
+            const int page = paged_pages_at(p.pg, seg, pages, seg.first + s, lane);
+            if (warp == 0) issue_paged(s, page);
         }
     }
     if constexpr (VLUT == 0)
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
         const int col = col0 + n;
         const bool real = col < cols;
         const int qi = real ? col / p.G : 0, qw = real ? col - qi * p.G : 0;
-        const uint16_t *qrow = PAGED ? p.q + (walk.s0 + qi) * p.pg.q_token + ((int64_t)h * p.G + qw) * p.pg.q_head
+        const uint16_t *qrow = PAGED ? p.q + (seg.s0 + qi) * p.pg.q_token + ((int64_t)h * p.G + qw) * p.pg.q_head
                                      : p.q + (((int64_t)b * M + qi) * p.QH + (int64_t)h * p.G + qw) * D;
         float qv[D / 64][4];
         float mx = 0.0f;
@@ -763,14 +770,14 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
         }
         __syncwarp();
         if constexpr (PAGED) {
-            const int64_t row = pages.rows(p.pg, walk, p.H, walk.first + s + p.stages, lane);
+            const int page = paged_pages_at(p.pg, seg, pages, seg.first + s + p.stages, lane);
             uint32_t last = 0;
             if (lane == 0) {
                 __threadfence_block();
                 last = atomicAdd(&done[slot], 1u) == A::W - 1;
                 if (last) done[slot] = 0;
             }
-            if (__shfl_sync(0xffffffffu, last, 0) && s + p.stages < n_stages) issue_paged(s + p.stages, row);
+            if (__shfl_sync(0xffffffffu, last, 0) && s + p.stages < n_stages) issue_paged(s + p.stages, page);
         } else if (lane == 0) {
             __threadfence_block();
             if (atomicAdd(&done[slot], 1u) == A::W - 1) {
@@ -823,7 +830,7 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     const int d0 = (threadIdx.x & 15) * PER;
 #pragma unroll 1
     for (int hh = threadIdx.x >> 4; hh < CB; hh += A::THREADS / 16) {
-        if (PAGED && walk.slot >= p.pg.slots) break;  // starts out of order make more units than there can be
+        if (PAGED && seg.slot >= p.pg.slots) break;  // starts out of order make more units than there can be
         float mmax = -INFINITY;
 #pragma unroll
         for (int w = 0; w < A::W; ++w) mmax = fmaxf(mmax, merge[w * CB * (D + 2) + CB * D + hh]);
@@ -839,7 +846,7 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
 #pragma unroll
             for (int i = 0; i < PER; ++i) ov[i] += m2[hh * D + d0 + i] * wt;
         }
-        const int64_t pidx = (PAGED ? walk.slot : (bh * p.HB + hb) * p.splits + split) * CB + hh;
+        const int64_t pidx = (PAGED ? seg.slot : (bh * p.HB + hb) * p.splits + split) * CB + hh;
         float4 *dst = reinterpret_cast<float4 *>(p.part_o + pidx * D + d0);
 #pragma unroll
         for (int i = 0; i < PER / 4; ++i) dst[i] = make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
@@ -849,12 +856,12 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
         }
     }
     if constexpr (PAGED) {
-        more = walk.next(p.pg, gT, CB, p.H, p.G);
+        if (threadIdx.x == 0) paged_walk_next(p.pg, walk, seg, walk.seg[(nseg + 1) & 1], gT, CB, p.H, p.G);
         it0 += n_stages;
-        if (more) {  // the next segment's copies land where the merge was read and written
-            fence_proxy_async_smem();
-            __syncthreads();
-        }
+        ++nseg;
+        fence_proxy_async_smem();  // the next segment's copies land where the merge was read and written
+        __syncthreads();
+        more = walk.x < walk.end;
     }
     } while (PAGED && more);
 }
@@ -1043,7 +1050,10 @@ inline int gen_nb(int d, int64_t cols)
 template <int D, int NB, int VLUT, bool PAGED, typename F>
 auto gen_dispatch_key(const GenPlan &pl, F &&f)
 {
-    return pl.key == 8 ? f(attn_generic_kernel<D, NB, VLUT, 8, PAGED>)
+    // paged, 8- or 4-bit keys with 2- or 3-bit values: the specialised kernel's up
+    // to head_dim 256, but for pools whose rows pass 2^31, which take KEY 0
+    if constexpr (PAGED && D <= 256 && VLUT != 0) return f(attn_generic_kernel<D, NB, VLUT, 0, PAGED>);
+    else return pl.key == 8 ? f(attn_generic_kernel<D, NB, VLUT, 8, PAGED>)
            : pl.key == 4 ? f(attn_generic_kernel<D, NB, VLUT, 4, PAGED>)
                          : f(attn_generic_kernel<D, NB, VLUT, 0, PAGED>);
 }
@@ -1078,11 +1088,16 @@ int gen_layout(const CacheView &c, GenPlan &pl)
                                                                            : A::MERGE;
     pl.smem = 1024 /*align slack*/ + ring + A::QF + A::QS + (pl.vlut == 0 ? 512 : 0) /*lut*/ +
               gMaxStages * 12 /*barriers, counters*/;
+    // the opt-in and the occupancy of an instantiation are looked up once per shared-memory size
     return gen_dispatch<D, NB, PAGED>(pl, [&](auto kern) {
+        static std::atomic<uint64_t> known{0};  // smem << 32 | CTAs; same on every GB300
+        const uint64_t k = known.load(std::memory_order_relaxed);
+        if (k >> 32 == (uint64_t)pl.smem) return (int)(uint32_t)k;
         int n = 0;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pl.smem) != cudaSuccess) return 0;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem) != cudaSuccess) return 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, GGeo<D, NB>::THREADS, pl.smem) != cudaSuccess)
             return 0;
+        known.store((uint64_t)pl.smem << 32 | (uint32_t)n, std::memory_order_relaxed);
         return n;
     });
 }
@@ -1266,6 +1281,7 @@ cudaError_t gen_paged_run(const CacheView &c, const PagedSplit &pg, int64_t cols
     p.part_o = part_o;
     p.part_ml = part_ml;
     p.pg = pg;
+    set_paged_chunks(p.pg, gT, (int)c.cap);
     CUtensorMap kmap{};
     if (pl.key != 0 && !gen_key_map<D>(c, &kmap, gcd_int(gT, (int)c.cap))) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)sh.ctas);

@@ -87,7 +87,7 @@ __device__ __forceinline__ int64_t paged_row(const PagedView &v, int64_t t, int 
 // along the line c or u grows by one at every new segment, so slots are
 // distinct, and at most CTAs + units of them are used.
 //
-// Every warp works the line out for itself from the lengths (two passes of 32
+// A CTA's first warp works the line out from the lengths (two passes of 32
 // sequences at a time); the first CTA leaves the prefix sums for the combine.
 // Stages and units of sequence s (none where it has no rows, no new tokens, or too many).
 __device__ __forceinline__ void paged_shape(const PagedSplit &ps, int s, int ST, int CB, int H, int G, int64_t &stages,
@@ -111,133 +111,150 @@ __device__ __forceinline__ int64_t warp_inclusive_sum(int64_t x, int lane)
     return x;
 }
 
+// A segment, as the CTA's threads read it from shared memory.
+struct PagedSegment {
+    int64_t s0, slot;              // first ragged row of the sequence; partial slot
+    int s, n, len;                 // sequence, its new tokens, its rows
+    int h, hb, first, count;       // kv-head, column block, first stage, stages
+};
+
+// The CTA's place on the line and its current segment (two, so that the next
+// one can be written while the current one is still read).
 struct PagedWalk {
-    int64_t x, end;        // stages of the line still to do
-    int s;                 // sequence of x
-    int64_t sp, up;        // stages, units before it
-    int64_t stages, blocks;
-    // the segment at x
-    int64_t s0, n, len;    // first ragged row, new tokens, rows
-    int h, hb, first, count;
-    int64_t slot;
+    int64_t x, end;         // stages of the line still to do
+    int64_t sp, up;         // stages, units before sequence s
+    int64_t stages, blocks; // of sequence s
+    int s;
+    PagedSegment seg[2];
+};
 
-    // Call from whole warps.  False: nothing for this CTA.
-    __device__ __forceinline__ bool start(const PagedSplit &ps, int ST, int CB, int H, int G, int lane)
-    {
-        int64_t total = 0;
-        for (int b = 0; b < ps.v.seqs; b += 32) {
-            int64_t st, bl;
-            paged_shape(ps, b + lane, ST, CB, H, G, st, bl);
-            total += st * bl * H;
-        }
+// The segment at w.x, by one thread.
+__device__ __forceinline__ void paged_segment(const PagedSplit &ps, PagedWalk &w, PagedSegment &g)
+{
+    const int64_t y = w.x - w.sp, u = y / w.stages;
+    g.first = (int)(y - u * w.stages);
+    g.count = (int)imin64(w.stages - g.first, w.end - w.x);
+    g.h = (int)(u / w.blocks);
+    g.hb = (int)(u - g.h * w.blocks);
+    g.slot = blockIdx.x + w.up + u;
+    g.s = w.s;
+    g.s0 = paged_start(ps.v, w.s);
+    g.n = (int)paged_new(ps.v, w.s);
+    g.len = (int)paged_len(ps.v, w.s);
+}
+
+// The CTA's first segment, by the first warp (whole): into w.seg[0], w.x < w.end
+// saying that there is one.  The first CTA leaves the prefix sums for the
+// combine.  The caller synchronises the CTA before w is read.
+__device__ __forceinline__ void paged_walk_start(const PagedSplit &ps, PagedWalk &w, int ST, int CB, int H, int G, int lane)
+{
+    int64_t total = 0;
+    for (int b = 0; b < ps.v.seqs; b += 32) {
+        int64_t st, bl;
+        paged_shape(ps, b + lane, ST, CB, H, G, st, bl);
+        total += st * bl * H;
+    }
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        int64_t per = (total + gridDim.x - 1) / gridDim.x;
-        if (per < 1) per = 1;
-        x = blockIdx.x * per;
-        end = imin64(total, x + per);
-        const bool writer = blockIdx.x == 0 && threadIdx.x < 32;
-        if (x >= end && !writer) return false;
-        int64_t sbase = 0, ubase = 0;
-        bool found = false;
-        for (int b = 0; b < ps.v.seqs && (writer || !found); b += 32) {
-            int64_t st, bl;
-            paged_shape(ps, b + lane, ST, CB, H, G, st, bl);
-            const int64_t w = st * bl * H, u = bl * H;
-            const int64_t ws = warp_inclusive_sum(w, lane), us = warp_inclusive_sum(u, lane);
-            const int64_t s_at = sbase + ws - w, u_at = ubase + us - u;
-            if (writer && b + lane <= ps.v.seqs) {
-                ps.plan[b + lane] = s_at;
-                ps.plan[ps.v.seqs + 1 + b + lane] = u_at;
-            }
-            const uint32_t hit = __ballot_sync(0xffffffffu, w > 0 && s_at <= x && x < s_at + w);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                s = b + l;
-                sp = __shfl_sync(0xffffffffu, s_at, l);
-                up = __shfl_sync(0xffffffffu, u_at, l);
-                stages = __shfl_sync(0xffffffffu, st, l);
-                blocks = __shfl_sync(0xffffffffu, bl, l);
-                found = true;
-            }
-            sbase += __shfl_sync(0xffffffffu, ws, 31);
-            ubase += __shfl_sync(0xffffffffu, us, 31);
-        }
-        if (writer && lane == 0) {
-            ps.plan[ps.v.seqs] = sbase;
-            ps.plan[2 * ps.v.seqs + 1] = ubase;
-            ps.plan[2 * ps.v.seqs + 2] = per;
-        }
-        return x < end;
+    for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < 1) per = 1;
+    const int64_t x = blockIdx.x * per, end = imin64(total, x + per);
+    const bool writer = blockIdx.x == 0;
+    if (lane == 0) {
+        w.x = x;
+        w.end = end;
     }
-
-    // The segment at x.
-    __device__ __forceinline__ void segment(const PagedSplit &ps)
-    {
-        const int64_t y = x - sp, u = y / stages;
-        first = (int)(y - u * stages);
-        count = (int)imin64(stages - first, end - x);
-        h = (int)(u / blocks);
-        hb = (int)(u - h * blocks);
-        slot = blockIdx.x + up + u;
-        s0 = paged_start(ps.v, s);
-        n = paged_new(ps.v, s);
-        len = paged_len(ps.v, s);
-    }
-
-    // To the segment after this one.  False: the CTA's run is done.
-    __device__ __forceinline__ bool next(const PagedSplit &ps, int ST, int CB, int H, int G)
-    {
-        x += count;
-        if (x >= end) return false;
-        while (x >= sp + stages * blocks * H) {  // to the next sequence with work: x < end says that there is one
-            sp += stages * blocks * H;
-            up += blocks * H;
-            ++s;
-            paged_shape(ps, s, ST, CB, H, G, stages, blocks);
+    int64_t sbase = 0, ubase = 0;
+    bool found = x >= end;
+    for (int b = 0; b < ps.v.seqs && (writer || !found); b += 32) {
+        int64_t st, bl;
+        paged_shape(ps, b + lane, ST, CB, H, G, st, bl);
+        const int64_t c = st * bl * H, u = bl * H;
+        const int64_t ws = warp_inclusive_sum(c, lane), us = warp_inclusive_sum(u, lane);
+        const int64_t s_at = sbase + ws - c, u_at = ubase + us - u;
+        if (writer && b + lane < ps.v.seqs) {
+            ps.plan[b + lane] = s_at;
+            ps.plan[ps.v.seqs + 1 + b + lane] = u_at;
         }
-        return true;
+        const bool mine = c > 0 && s_at <= x && x < s_at + c;
+        if (mine) {
+            w.s = b + lane;
+            w.sp = s_at;
+            w.up = u_at;
+            w.stages = st;
+            w.blocks = bl;
+            paged_segment(ps, w, w.seg[0]);
+        }
+        found |= __any_sync(0xffffffffu, mine);
+        sbase += __shfl_sync(0xffffffffu, ws, 31);
+        ubase += __shfl_sync(0xffffffffu, us, 31);
     }
-};
+    if (writer && lane == 0) ps.plan[2 * ps.v.seqs + 2] = per;
+}
 
-// The pages of a segment's chunks (RU = gcd(stage rows, page rows) rows each,
-// so that no chunk crosses a page), 32 / NCH stages ahead at a time, one
-// chunk a lane: a refill finds its pages in registers.
-template <int ST>
+// On to the segment after `cur`, by one thread, into `nxt`; w.x < w.end says
+// that there is one.
+__device__ __forceinline__ void paged_walk_next(const PagedSplit &ps, PagedWalk &w, const PagedSegment &cur,
+                                                PagedSegment &nxt, int ST, int CB, int H, int G)
+{
+    w.x += cur.count;
+    if (w.x >= w.end) return;
+    while (w.x >= w.sp + w.stages * w.blocks * H) {  // to the next sequence with work: x < end says that there is one
+        w.sp += w.stages * w.blocks * H;
+        w.up += w.blocks * H;
+        ++w.s;
+        paged_shape(ps, w.s, ST, CB, H, G, w.stages, w.blocks);
+    }
+    paged_segment(ps, w, nxt);
+}
+
+// The page numbers of a segment's chunks (ru = gcd(stage rows, page rows) rows
+// each, so that no chunk crosses a page), ps.spl stages ahead at a time, one
+// chunk a lane: a refill finds its pages in a register.
 struct PagedPages {
-    int nch = 1, spl = 32;     // chunks per stage, stages per warp load
-    int base = 0;              // first stage of `cur`
-    int64_t cur = 0, nxt = 0;  // plane row of the lane's chunk for kv-head 0 (+ h page)
-
-    __device__ __forceinline__ int64_t load(const PagedSplit &ps, const PagedWalk &w, int H, int stage0, int lane) const
-    {
-        const int st = stage0 + lane / nch, ch = lane - (lane / nch) * nch;
-        const int64_t row = (int64_t)st * ST + ch * (ST / nch);
-        if (lane >= spl * nch || row >= w.len) return 0;
-        uint32_t slot;
-        const int pg = paged_page(ps.v, w.s, (uint32_t)row, slot);
-        return ((int64_t)(pg < 0 ? 0 : pg) * H + w.h) * ps.v.page + slot;
-    }
-
-    __device__ __forceinline__ void start(const PagedSplit &ps, const PagedWalk &w, int H, int stage, int lane)
-    {
-        nch = ST / gcd_int(ST, (int)ps.v.page);
-        spl = 32 / nch;
-        base = stage;
-        cur = load(ps, w, H, base, lane);
-        nxt = load(ps, w, H, base + spl, lane);
-    }
-
-    // Plane row of chunk (lane) of `stage`, which is base or later and at most a load ahead.
-    __device__ __forceinline__ int64_t rows(const PagedSplit &ps, const PagedWalk &w, int H, int stage, int lane)
-    {
-        while (stage >= base + spl) {
-            base += spl;
-            cur = nxt;
-            nxt = load(ps, w, H, base + spl, lane);
-        }
-        return __shfl_sync(0xffffffffu, cur, (stage - base) * nch + (lane < nch ? lane : 0));
-    }
+    int base = 0, cur = 0, nxt = 0;  // first stage of `cur`; the lane's page numbers, and of the next load
 };
+
+// Row of the sequence where chunk `lane` of `stage` starts.
+__device__ __forceinline__ uint32_t paged_chunk_row(const PagedSplit &ps, int stage, int chunk)
+{
+    return (uint32_t)((stage * ps.nch + chunk) * ps.ru);
+}
+
+__device__ __forceinline__ int paged_pages_load(const PagedSplit &ps, const PagedSegment &g, int stage0, int lane)
+{
+    const int st = stage0 + lane / ps.nch, ch = lane % ps.nch;
+    const uint32_t row = paged_chunk_row(ps, st, ch);
+    if (lane >= ps.spl * ps.nch || row >= (uint32_t)g.len) return 0;
+    uint32_t slot;
+    const int pg = paged_page(ps.v, g.s, row, slot);
+    return pg < 0 ? 0 : pg;
+}
+
+__device__ __forceinline__ void paged_pages_start(const PagedSplit &ps, const PagedSegment &g, PagedPages &pp, int lane)
+{
+    pp.base = g.first;
+    pp.cur = paged_pages_load(ps, g, pp.base, lane);
+    pp.nxt = paged_pages_load(ps, g, pp.base + ps.spl, lane);
+}
+
+// Page of chunk (lane) of `stage`, which is base or later; whole warps call it in stage order.
+__device__ __forceinline__ int paged_pages_at(const PagedSplit &ps, const PagedSegment &g, PagedPages &pp, int stage, int lane)
+{
+    while (stage >= pp.base + ps.spl) {
+        pp.base += ps.spl;
+        pp.cur = pp.nxt;
+        pp.nxt = paged_pages_load(ps, g, pp.base + ps.spl, lane);
+    }
+    return __shfl_sync(0xffffffffu, pp.cur, (stage - pp.base) * ps.nch + (lane < ps.nch ? lane : 0));
+}
+
+// Plane row of that chunk for the segment's kv-head.
+__device__ __forceinline__ int64_t paged_chunk_plane_row(const PagedSplit &ps, const PagedSegment &g, int H, int page,
+                                                         int stage, int chunk)
+{
+    const uint32_t row = paged_chunk_row(ps, stage, chunk);
+    return ((int64_t)page * H + g.h) * ps.v.page + (row - fast_div(row, ps.v.div_page) * ps.v.page);
+}
 
 }  // namespace tq

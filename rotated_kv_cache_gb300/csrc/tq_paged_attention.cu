@@ -21,6 +21,14 @@ TQ_DECLARE_PAGED_GENERIC(128)
 TQ_DECLARE_PAGED_GENERIC(256)
 TQ_DECLARE_PAGED_GENERIC(512)
 #undef TQ_DECLARE_PAGED_GENERIC
+#define TQ_DECLARE_PAGED_SPLIT(D)                                                                                      \
+    PagedShape paged_split_shape_d##D(const CacheView &c, int64_t cols);                                              \
+    cudaError_t launch_paged_split_d##D(const CacheView &c, const PagedSplit &pg, const PagedShape &sh, const uint16_t *q, \
+                                        int QH, float scale, float *part_o, float *part_ml, cudaStream_t s);
+TQ_DECLARE_PAGED_SPLIT(64)
+TQ_DECLARE_PAGED_SPLIT(128)
+TQ_DECLARE_PAGED_SPLIT(256)
+#undef TQ_DECLARE_PAGED_SPLIT
 
 namespace {
 
@@ -182,6 +190,8 @@ bool generic_shape(const CacheView &c, int64_t cols, PagedShape &sh)
 
 struct PagedPlan {
     PagedShape split;
+    bool special;   // the specialised split kernel, else the generic one
+    int64_t cols;   // most columns of a kv-head that the split kernels see
     PagedBounds b;
     int64_t slots;
     size_t off_ml, off_o, off_wide, bytes;  // workspace: plan words, partial (max, sum), partial outputs, the wide kernels'
@@ -197,8 +207,15 @@ bool paged_plan(const CacheView &c, const PagedBounds &bounds, int QH, PagedPlan
     pl.b = bounds;
     pl.b.wide = paged_wide_applies(c) && pl.b.max_new * G >= kWideColumns ? (kWideColumns - 1) / G : INT32_MAX;
     const bool wide = pl.b.wide != INT32_MAX;
-    const int64_t narrow = wide ? (pl.b.wide > 0 ? pl.b.wide : 1) : pl.b.max_new;  // new tokens of a sequence for the split kernels
-    if (!generic_shape(c, narrow * G, pl.split)) return false;
+    pl.cols = (wide ? (pl.b.wide > 0 ? pl.b.wide : 1) : pl.b.max_new) * G;
+    // the specialised kernel where it has the widths (its tensor copies count rows in 32 bits)
+    pl.special = attention_supported(c.d, c.kb, c.vb, (int)G) && (int64_t)c.B * c.H * c.cap < (int64_t(1) << 31);
+    if (pl.special)
+        pl.split = c.d == 64    ? paged_split_shape_d64(c, pl.cols)
+                   : c.d == 128 ? paged_split_shape_d128(c, pl.cols)
+                                : paged_split_shape_d256(c, pl.cols);
+    else if (!generic_shape(c, pl.cols, pl.split))
+        return false;
     // a sequence of n new tokens has ceil(n G / block) blocks: at most this many units in all
     const int64_t units = c.H * (pl.b.total * G / pl.split.block + pl.b.seqs);
     pl.slots = pl.split.ctas + units;
@@ -226,13 +243,17 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
     if (!paged_plan(c, b, QH, pl)) return cudaErrorInvalidConfiguration;
     if (ws_bytes < pl.bytes) return cudaErrorInvalidValue;
     uint8_t *base = static_cast<uint8_t *>(ws);
-    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<int64_t *>(base), pl.slots, pl.b.wide};
+    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<int64_t *>(base), pl.slots, pl.b.wide, 1, 32, 1};
     float *part_ml = reinterpret_cast<float *>(base + pl.off_ml), *part_o = reinterpret_cast<float *>(base + pl.off_o);
     cudaError_t e = cudaSuccess;
     if (pl.b.wide != INT32_MAX) e = launch_paged_wide(c, pg, pl.b, q, QH, scale, out, base + pl.off_wide, s);
     if (e != cudaSuccess) return e;
-    const int64_t narrow = pl.b.wide != INT32_MAX ? (pl.b.wide > 0 ? pl.b.wide : 1) : pl.b.max_new, cols = narrow * (QH / c.H);
-    switch (c.d) {
+    const int64_t cols = pl.cols;
+    if (pl.special)
+        e = c.d == 64    ? launch_paged_split_d64(c, pg, pl.split, q, QH, scale, part_o, part_ml, s)
+            : c.d == 128 ? launch_paged_split_d128(c, pg, pl.split, q, QH, scale, part_o, part_ml, s)
+                         : launch_paged_split_d256(c, pg, pl.split, q, QH, scale, part_o, part_ml, s);
+    else switch (c.d) {
     case 64: e = launch_paged_generic_d64(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
     case 128: e = launch_paged_generic_d128(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
     case 256: e = launch_paged_generic_d256(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;

@@ -1,0 +1,4 @@
+// tq_paged_split_d256.cu -- paged launches of the specialised split kernel at head_dim 256.
+#include "tq_paged_split.cuh"
+
+TQ_PAGED_SPLIT_ENTRIES(256)
