@@ -38,7 +38,8 @@ struct PagedCombineParams {
     uint16_t *out;  // bf16 [total][QH][D]
     PagedSplit pg;
     int H, QH, G, ST, CB;
-    int64_t rows;  // total * QH
+    int64_t rows;     // rows gone through: total * QH, or seqs * per_seq * QH
+    int per_seq;      // > 0: that many places for tokens per sequence; 0: token by token
     float inv_sqrt_d;
     SignBits sg;
 };
@@ -68,11 +69,18 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
     pdl_wait_primary();
     pdl_allow_dependents();
     bool live = row < p.rows;
-    const int64_t t = live ? row / p.QH : 0;
+    int64_t t = live ? row / p.QH : 0;
     const int qh = (int)(row - t * p.QH);
     int s = 0;
     int64_t n = 0, len = 0, s0 = 0;
-    if (live) {
+    if (live && p.per_seq > 0) {
+        s = (int)(t / p.per_seq);
+        s0 = paged_start(p.pg.v, s);
+        n = paged_new(p.pg.v, s);
+        len = paged_len(p.pg.v, s);
+        t += s0 - (int64_t)s * p.per_seq;
+        live = n <= p.pg.wide && t < s0 + n;
+    } else if (live) {
         int lo = 0, hi = p.pg.v.seqs + 1;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
@@ -162,7 +170,7 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
     for (int k = 0; k < PER; k += 2)
         w[k / 2] = pack_bf16x2(x[k] * (sign_negative(p.sg, PER * lane + k) ? -inv : inv),
                                x[k + 1] * (sign_negative(p.sg, PER * lane + k + 1) ? -inv : inv));
-    store_words<PER / 2, PER * 2 < 16 ? PER * 2 : 16>(p.out + row * D + PER * lane, w);
+    store_words<PER / 2, PER * 2 < 16 ? PER * 2 : 16>(p.out + (t * p.QH + qh) * D + PER * lane, w);
 }
 
 template <int D>
@@ -261,8 +269,13 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
     default: e = cudaErrorInvalidValue;
     }
     if (e != cudaSuccess) return e;
-    PagedCombineParams cp{part_o, part_ml, out, pg, c.H, QH, QH / c.H, pl.split.stage, pl.split.block, v.total * QH,
-                          inv_sqrt_head_dim(c.d), c.signs};
+    // by places per sequence where that goes through fewer rows (a decode step: no
+    // search for a token's sequence; a long chunk: none of its tokens)
+    const int64_t per_seq = pl.b.max_new < pl.b.wide ? pl.b.max_new : (pl.b.wide > 0 ? pl.b.wide : 1);
+    const bool by_seq = v.seqs * per_seq <= v.total;
+    PagedCombineParams cp{part_o, part_ml, out, pg, c.H, QH, QH / c.H, pl.split.stage, pl.split.block,
+                          (by_seq ? v.seqs * per_seq : v.total) * QH, by_seq ? (int)per_seq : 0, inv_sqrt_head_dim(c.d),
+                          c.signs};
     switch (c.d) {
     case 64: return run_combine<64>(cp, s);
     case 128: return run_combine<128>(cp, s);

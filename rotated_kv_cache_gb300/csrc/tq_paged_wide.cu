@@ -31,6 +31,8 @@
 // A value row with an infinity or NaN would spoil the sums of columns that do
 // not see it (0 * inf), so expand writes zeros there and a bit mask; a column
 // that sees a marked row gets NaN through l.
+#include <type_traits>
+
 #include "tq_common.cuh"
 #include "tq_kernels.h"
 #include "tq_paged.cuh"
@@ -41,7 +43,8 @@ namespace {
 
 constexpr int wT = 128;    // rows per tile
 constexpr int wC = 256;    // columns per block (two groups of the MMA's 128)
-constexpr int wThreads = 320;
+constexpr int wThreads = 384;  // two softmax warpgroups; MMA warp, tile warp (and two idle ones)
+constexpr int wPlanThreads = 256;
 constexpr float wTau = 8.0f, wUp = 6.0f;  // lazy raise of R; weights are 2^(s - R + wUp)
 
 // What expand says about a tile.
@@ -57,7 +60,13 @@ struct WidePlan {        // device arrays, written by plan
     int32_t *tile0;      // [seqs + 1] scratch tiles before a sequence
     int32_t *entry0;     // [seqs + 1] blocks before it
     int64_t *before;     // [entries + 1] tiles of the blocks before an entry (one kv-head's)
-    int64_t *line;       // total stages of the line, stages per CTA
+    int64_t *line;       // total tiles of the line, tiles per CTA
+    struct WideShare *share;  // [CTAs] the block that a CTA began and did not finish
+};
+
+struct WideShare {
+    int s, h, block;     // block of the sequence
+    int last;            // the last CTA that has a share of it, or -1: nothing is shared
 };
 
 struct WideParams {
@@ -114,7 +123,7 @@ __device__ __forceinline__ int64_t block_tiles(int64_t len, int64_t n, int G, in
     return t < 1 ? 1 : t;
 }
 
-__global__ void __launch_bounds__(1024) wide_plan_kernel(const __grid_constant__ WideParams p)
+__global__ void __launch_bounds__(wPlanThreads) wide_plan_kernel(const __grid_constant__ WideParams p)
 {
     __shared__ int64_t sh[32];
     pdl_wait_primary();
@@ -181,7 +190,7 @@ __global__ void __launch_bounds__(1024) wide_plan_kernel(const __grid_constant__
 // block after block, then tile after tile.
 struct WidePlace {
     int s, h, e, tile, tiles;  // entry (block) and tile in it; tiles of the block
-    int64_t at;                // line position of the block's first tile
+    int e0, e1;                // entries of the sequence
 };
 
 __device__ __forceinline__ WidePlace wide_locate(const WideParams &p, int64_t x)
@@ -194,7 +203,7 @@ __device__ __forceinline__ WidePlace wide_locate(const WideParams &p, int64_t x)
         else hi = mid - 1;
     }
     w.s = lo;
-    const int e0 = p.pl.entry0[lo], e1 = p.pl.entry0[lo + 1];
+    const int e0 = w.e0 = p.pl.entry0[lo], e1 = w.e1 = p.pl.entry0[lo + 1];
     const int64_t b0 = p.pl.before[e0], sum = p.pl.before[e1] - b0, y = x - b0 * p.H;
     w.h = (int)(y / sum);
     const int64_t z = y - w.h * sum + b0;  // within one head's blocks
@@ -207,8 +216,25 @@ __device__ __forceinline__ WidePlace wide_locate(const WideParams &p, int64_t x)
     w.e = a;
     w.tile = (int)(z - p.pl.before[a]);
     w.tiles = (int)(p.pl.before[a + 1] - p.pl.before[a]);
-    w.at = x - w.tile;
     return w;
+}
+
+// From the end of a block to the next one's first tile (there is one).
+__device__ __forceinline__ void wide_next(const WideParams &p, WidePlace &w)
+{
+    w.tile = 0;
+    if (++w.e == w.e1) {
+        w.e = w.e0;
+        if (++w.h == p.H) {
+            w.h = 0;
+            w.e = w.e0 = w.e1;
+            do {
+                ++w.s;
+                w.e1 = p.pl.entry0[w.s + 1];
+            } while (w.e1 == w.e0);
+        }
+    }
+    w.tiles = (int)(p.pl.before[w.e + 1] - p.pl.before[w.e]);
 }
 
 // ---------------------------------------------------------------- expand
@@ -372,13 +398,17 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
     tc_fence_after();
     const uint32_t tmem = *tslot;
 
+    // registers: the softmax threads hold a row of scores each; 256 x 216 + 128 x 72 is what the launch has
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 9) {
         // ------------------------------------------------------------ tiles in
         if (lane == 0) {
             bool ok = true;
             uint32_t it = 0;
+            WidePlace w = wide_locate(p, x0);
             for (int64_t x = x0; x < x1 && ok;) {
-                const WidePlace w = wide_locate(p, x);
+                if (x > x0) wide_next(p, w);
                 const int n = (int)imin64(w.tiles - w.tile, x1 - x);
                 const int64_t scratch = p.pl.tile0[w.s] + w.tile;
                 for (int t = 0; t < n && ok; ++t, ++it) {
@@ -424,10 +454,11 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
             };
             bool ok = true;
             uint32_t it = 0, seg = 0;
+            WidePlace w = wide_locate(p, x0);
             for (int64_t x = x0; x < x1 && ok; ++seg) {
-                const WidePlace w = wide_locate(p, x);
+                if (x > x0) wide_next(p, w);
                 const int n = (int)imin64(w.tiles - w.tile, x1 - x);
-                const int64_t cols = paged_new(p.pg.v, w.s) * p.G - (int64_t)(w.e - p.pl.entry0[w.s]) * wC;
+                const int64_t cols = paged_new(p.pg.v, w.s) * p.G - (int64_t)(w.e - w.e0) * wC;
                 const int groups = cols > 128 ? 2 : 1;
                 ok = mbar_wait_bounded(kfull + 8 * (it % NK), (it / NK) & 1, p.err);
                 for (int g = 0; g < groups && ok; ++g) {
@@ -475,7 +506,9 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
             }
         }
         __syncwarp();
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ------------------------------------------------------------ softmax, one column a thread
         const int g = warp >> 2, ltid = tid & 127;
         const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
@@ -483,11 +516,13 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
         const uint32_t bar_s = sfull + 8 * g, bar_p = pfull + 8 * g;
         bool ok = true;
         uint32_t it = 0, seg = 0;
+        int shared_from = -1;  // thread 0: the block of the last segment, if it is begun here and not finished
+        WidePlace w = wide_locate(p, x0);
         for (int64_t x = x0; x < x1 && ok; ++seg) {
-            const WidePlace w = wide_locate(p, x);
+            if (x > x0) wide_next(p, w);
             const int n = (int)imin64(w.tiles - w.tile, x1 - x);
             const int64_t nn = paged_new(p.pg.v, w.s), len = paged_len(p.pg.v, w.s);
-            const int64_t col = (int64_t)(w.e - p.pl.entry0[w.s]) * wC + 128 * g + ltid;
+            const int64_t col = (int64_t)(w.e - w.e0) * wC + 128 * g + ltid;
             const bool real = col < nn * p.G;
             const int64_t tok = real ? col / p.G : nn - 1, row = paged_start(p.pg.v, w.s) + tok;
             const int hq = real ? (int)(col - tok * p.G) : 0;
@@ -497,21 +532,24 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
             {
                 const uint16_t *qrow = p.q + row * p.pg.q_token + ((int64_t)w.h * p.G + hq) * p.pg.q_head;
                 float mx = 0.0f;
-                if (real)
-                    for (int c8 = 0; c8 < D / 8; ++c8) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(qrow + 8 * c8);
-                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+                uint4 qv[D / 8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mx = max3(mx, fabsf(bf16_lo(uu[i])), fabsf(bf16_hi(uu[i])));
-                    }
+                for (int c8 = 0; c8 < D / 8; ++c8)
+                    qv[c8] = real ? *reinterpret_cast<const uint4 *>(qrow + 8 * c8) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int c8 = 0; c8 < D / 8; ++c8) {
+                    const uint32_t uu[4] = {qv[c8].x, qv[c8].y, qv[c8].z, qv[c8].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx = max3(mx, fabsf(bf16_lo(uu[i])), fabsf(bf16_hi(uu[i])));
+                }
                 int e = 0;
                 if (mx > 0.0f && mx < INFINITY) e = 14 - (((int)(__float_as_uint(mx) >> 23) & 0xFF) - 127);
                 e = e < -100 ? -100 : (e > 100 ? 100 : e);
                 const float qs = ldexpf(p.qsign, e);
                 ie = ldexpf(1.0f, -e) * p.scale_log2;
+#pragma unroll
                 for (int c8 = 0; c8 < D / 8; ++c8) {
-                    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                    if (real) u = *reinterpret_cast<const uint4 *>(qrow + 8 * c8);
+                    const uint4 u = qv[c8];
                     sts128(sb + g * KT + kmaj_off(128, ltid, 8 * c8),
                            make_uint4(tc_pack_f16(bf16_lo(u.x) * qs, bf16_hi(u.x) * qs),
                                       tc_pack_f16(bf16_lo(u.y) * qs, bf16_hi(u.y) * qs),
@@ -539,8 +577,10 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc_ld32(t_s + 32 * c, sr[c]);
                 tc_wait_ld();
-                const bool cut = __any_sync(0xffffffffu, vis < wT);
-                if (cut)
+                // CUT: some column of the warp does not see the whole tile (the last ones only)
+                auto step = [&](auto cut_) __attribute__((always_inline)) {
+                constexpr bool CUT = decltype(cut_)::value;
+                if constexpr (CUT)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -587,7 +627,7 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                     for (int j = 0; j < 32; j += 2) {
                         const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[c][j]), __uint_as_float(sr[c][j + 1])), f2, a2);
                         float p0 = tc_ex2(y.x), p1 = tc_ex2(y.y);
-                        if (cut) {
+                        if constexpr (CUT) {
                             if (32 * c + j >= vis) p0 = 0.0f;
                             if (32 * c + j + 1 >= vis) p1 = 0.0f;
                         }
@@ -597,6 +637,9 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                     tc_st16(t_s + 16 * c, pp);
                 }
                 l = fmaf((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y), lf, l);
+                };
+                if (__any_sync(0xffffffffu, vis < wT)) step(std::true_type{});
+                else step(std::false_type{});
                 if (any) {
 #pragma unroll 1
                     for (int i = 0; i < 4; ++i) {
@@ -650,9 +693,14 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 for (int j = 0; j < D; j += 4) dst[j / 4] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                 p.part_ml[2 * at] = R - wUp;  // R = -inf (nothing seen): weight 0
                 p.part_ml[2 * at + 1] = l;
+                if (tid == 0 && w.tile == 0) {
+                    shared_from = w.e - w.e0;
+                    p.pl.share[blockIdx.x] = WideShare{w.s, w.h, shared_from, (int)((x + w.tiles - 1) / per)};
+                }
             }
             x += n;
         }
+        if (tid == 0 && shared_from < 0) p.pl.share[blockIdx.x].last = -1;
     }
     tc_fence_before();
     __syncthreads();
@@ -669,14 +717,14 @@ __global__ void __launch_bounds__(256) wide_merge_kernel(const __grid_constant__
     constexpr int PER = D / 32;
     pdl_wait_primary();
     pdl_allow_dependents();
-    const int64_t total = p.pl.line[0], per = p.pl.line[1], c = blockIdx.x, x1 = (c + 1) * per;
-    if (x1 >= total) return;
-    const WidePlace w = wide_locate(p, x1);
-    if (w.tile == 0 || w.at < c * per) return;  // nothing runs on past CTA c, or it began before c
-    const int64_t last = (w.at + w.tiles - 1) / per, nn = paged_new(p.pg.v, w.s);
+    const int64_t total = p.pl.line[0], per = p.pl.line[1], c = blockIdx.x;
+    if (c * per >= total) return;  // a CTA without work left no word
+    const WideShare w = p.pl.share[c];
+    if (w.last < 0) return;
+    const int64_t last = w.last, nn = paged_new(p.pg.v, w.s);
     const int lane = threadIdx.x & 31;
     for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < wC; i += gridDim.y * 8) {
-        const int64_t col = (int64_t)(w.e - p.pl.entry0[w.s]) * wC + i;
+        const int64_t col = (int64_t)w.block * wC + i;
         if (col >= nn * p.G) break;
         auto slot = [&](int64_t k) { return (k == c ? 2 * c + 1 : 2 * k) * wC + i; };
         float m = -INFINITY;
@@ -711,7 +759,7 @@ __global__ void __launch_bounds__(256) wide_merge_kernel(const __grid_constant__
 // ---------------------------------------------------------------- host side
 struct WideSizes {
     int64_t tiles, entries;
-    size_t off_tile0, off_entry0, off_before, off_line, off_meta, off_ml, off_o, off_tiles, bytes;
+    size_t off_tile0, off_entry0, off_before, off_line, off_share, off_meta, off_ml, off_o, off_tiles, bytes;
 };
 
 WideSizes wide_sizes(const CacheView &c, const PagedBounds &b, int QH)
@@ -732,6 +780,7 @@ WideSizes wide_sizes(const CacheView &c, const PagedBounds &b, int QH)
     z.off_entry0 = take((size_t)(b.seqs + 1) * 4);
     z.off_before = take((size_t)(z.entries + 1) * 8);
     z.off_line = take(16);
+    z.off_share = take((size_t)num_sms() * sizeof(WideShare));
     z.off_meta = take((size_t)z.tiles * c.H * sizeof(TileMeta));
     z.off_ml = take(slots * 8);
     z.off_o = take(slots * c.d * 4);
@@ -746,14 +795,14 @@ cudaError_t wide_run(WideParams &p, cudaStream_t s)
     using A = WideGeo<D>;
     cudaError_t e = cudaFuncSetAttribute(wide_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(wide_plan_kernel, dim3(1), dim3(1024), 0, s, p);
+    e = launch_dependent(wide_plan_kernel, dim3(1), dim3(wPlanThreads), 0, s, p);
     if (e != cudaSuccess) return e;
     const int64_t items = p.max_tiles * p.H;
     e = launch_dependent(wide_expand_kernel<D>, dim3((unsigned)imin64(items, (int64_t)num_sms() * 8)), dim3(256), 0, s, p);
     if (e != cudaSuccess) return e;
     e = launch_dependent(wide_attend_kernel<D>, dim3((unsigned)p.ctas), dim3(wThreads), A::SMEM, s, p);
     if (e != cudaSuccess) return e;
-    return launch_dependent(wide_merge_kernel<D>, dim3((unsigned)p.ctas, 4), dim3(256), 0, s, p);
+    return launch_dependent(wide_merge_kernel<D>, dim3((unsigned)p.ctas, 8), dim3(256), 0, s, p);
 }
 
 }  // namespace
@@ -770,7 +819,7 @@ cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const Pa
     WideParams p{};
     p.pg = pg;
     p.pl = WidePlan{reinterpret_cast<int32_t *>(w + z.off_tile0), reinterpret_cast<int32_t *>(w + z.off_entry0),
-                    reinterpret_cast<int64_t *>(w + z.off_before), reinterpret_cast<int64_t *>(w + z.off_line)};
+                    reinterpret_cast<int64_t *>(w + z.off_before), reinterpret_cast<int64_t *>(w + z.off_line), reinterpret_cast<WideShare *>(w + z.off_share)};
     p.max_tiles = z.tiles;
     p.max_entries = z.entries;
     p.k_codes = c.k_codes;
