@@ -378,7 +378,7 @@ TQ_API size_t tq_paged_attention_workspace_bytes(const tq_cache *pool, const tq_
  *            sequence has more than max_new new tokens.
  *  q         device bf16, element [token][head][j] at token * s[0] + head *
  *            s[1] + j; 16-byte aligned, strides multiples of 8.
- *  out       device bf16 [total][q_heads][d] contiguous, 16-byte aligned:
+ *  out       device bf16 [total][q_heads][d] contiguous, 32-byte aligned:
  *            rounded once, from fp32 sums.
  *  workspace device scratch of at least tq_paged_attention_workspace_bytes()
  *            for these bounds, 256-byte aligned, not initialised.  Calls that

@@ -490,7 +490,7 @@ tq_status tq_paged_attention(const tq_cache *c, const tq_page_table *t, const in
     if (total == 0) return TQ_OK;
     if ((st = check_ragged(q, qs)) != TQ_OK) return st;
     if (!out) return TQ_ERR_NULL;
-    if (!aligned16(out)) return TQ_ERR_ALIGN;
+    if (!aligned32(out)) return TQ_ERR_ALIGN;
     const tq::CacheView cv = view(c);
     const tq::PagedBounds b = paged_bounds(t, total, max_new);
     const size_t need = tq::paged_attention_workspace_bytes(cv, b, q_heads);

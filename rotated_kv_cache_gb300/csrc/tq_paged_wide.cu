@@ -45,6 +45,7 @@ constexpr int wT = 128;    // rows per tile
 constexpr int wC = 256;    // columns per block (two groups of the MMA's 128)
 constexpr int wThreads = 384;  // two softmax warpgroups; MMA warp, tile warp (and two idle ones)
 constexpr int wPlanThreads = 256;
+constexpr int wStart = 6;  // what a block costs besides its tiles (q in, out of tensor memory, un-rotation), in tiles
 constexpr float wTau = 8.0f, wUp = 6.0f;  // lazy raise of R; weights are 2^(s - R + wUp)
 
 // What expand says about a tile.
@@ -59,8 +60,8 @@ struct __align__(16) TileMeta {
 struct WidePlan {        // device arrays, written by plan
     int32_t *tile0;      // [seqs + 1] scratch tiles before a sequence
     int32_t *entry0;     // [seqs + 1] blocks before it
-    int64_t *before;     // [entries + 1] tiles of the blocks before an entry (one kv-head's)
-    int64_t *line;       // total tiles of the line, tiles per CTA
+    int64_t *before;     // [entries + 1] cost (tiles + wStart each) of the blocks before an entry (one kv-head's)
+    int64_t *line;       // total cost of the line, cost per CTA
     struct WideShare *share;  // [CTAs] the block that a CTA began and did not finish
 };
 
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(wPlanThreads) wide_plan_kernel(const __grid_co
                 if (p.pl.entry0[mid] <= e) lo = mid;
                 else hi = mid - 1;
             }
-            t = block_tiles(paged_len(p.pg.v, lo), paged_new(p.pg.v, lo), p.G, e - p.pl.entry0[lo]);
+            t = wStart + block_tiles(paged_len(p.pg.v, lo), paged_new(p.pg.v, lo), p.G, e - p.pl.entry0[lo]);
         }
         const int64_t at = line + block_exclusive_sum(t, all, sh);
         line += all;
@@ -181,17 +182,37 @@ __global__ void __launch_bounds__(wPlanThreads) wide_plan_kernel(const __grid_co
         const int64_t total = line * p.H;
         int64_t per = (total + p.ctas - 1) / p.ctas;
         p.pl.line[0] = total;
-        p.pl.line[1] = per < 1 ? 1 : per;
+        p.pl.line[1] = per < 2 * wStart ? 2 * wStart : per;  // no run of little more than a start
     }
 }
 
-// A place on the line: sequence after sequence, in a sequence kv-head after
+// A place on the line (its unit is the cost of a tile): sequence after sequence, in a sequence kv-head after
 // kv-head (CTAs of one head are neighbours, and share its tiles in L2), then
-// block after block, then tile after tile.
+// block after block, in a block its start, then its tiles.  A CTA whose run
+// ends within a start leaves the block to the next one.
 struct WidePlace {
     int s, h, e, tile, tiles;  // entry (block) and tile in it; tiles of the block
     int e0, e1;                // entries of the sequence
+    int tile0;                 // its first scratch tile
+    int64_t s0, n, len;        // its first ragged row, new tokens, rows
+    int64_t at;                // line position of the block's first tile
+
+    // tiles of the block from `tile` on that a run up to x1 takes
+    __device__ __forceinline__ int count(int64_t x1) const
+    {
+        const int64_t m = x1 - at;
+        return (int)(m < tiles ? m : tiles) - tile;
+    }
+    __device__ __forceinline__ bool ends(int64_t x1) const { return at + tiles >= x1; }  // the run ends with this block, or in it
 };
+
+__device__ __forceinline__ void wide_sequence(const WideParams &p, WidePlace &w)
+{
+    w.tile0 = p.pl.tile0[w.s];
+    w.s0 = paged_start(p.pg.v, w.s);
+    w.n = paged_new(p.pg.v, w.s);
+    w.len = paged_len(p.pg.v, w.s);
+}
 
 __device__ __forceinline__ WidePlace wide_locate(const WideParams &p, int64_t x)
 {
@@ -214,8 +235,11 @@ __device__ __forceinline__ WidePlace wide_locate(const WideParams &p, int64_t x)
         else b = mid - 1;
     }
     w.e = a;
-    w.tile = (int)(z - p.pl.before[a]);
-    w.tiles = (int)(p.pl.before[a + 1] - p.pl.before[a]);
+    const int off = (int)(z - p.pl.before[a]) - wStart;
+    w.tile = off > 0 ? off : 0;
+    w.tiles = (int)(p.pl.before[a + 1] - p.pl.before[a]) - wStart;
+    w.at = x - off;
+    wide_sequence(p, w);
     return w;
 }
 
@@ -223,6 +247,7 @@ __device__ __forceinline__ WidePlace wide_locate(const WideParams &p, int64_t x)
 __device__ __forceinline__ void wide_next(const WideParams &p, WidePlace &w)
 {
     w.tile = 0;
+    w.at += w.tiles + wStart;
     if (++w.e == w.e1) {
         w.e = w.e0;
         if (++w.h == p.H) {
@@ -232,9 +257,10 @@ __device__ __forceinline__ void wide_next(const WideParams &p, WidePlace &w)
                 ++w.s;
                 w.e1 = p.pl.entry0[w.s + 1];
             } while (w.e1 == w.e0);
+            wide_sequence(p, w);
         }
     }
-    w.tiles = (int)(p.pl.before[w.e + 1] - p.pl.before[w.e]);
+    w.tiles = (int)(p.pl.before[w.e + 1] - p.pl.before[w.e]) - wStart;
 }
 
 // ---------------------------------------------------------------- expand
@@ -407,10 +433,8 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
             bool ok = true;
             uint32_t it = 0;
             WidePlace w = wide_locate(p, x0);
-            for (int64_t x = x0; x < x1 && ok;) {
-                if (x > x0) wide_next(p, w);
-                const int n = (int)imin64(w.tiles - w.tile, x1 - x);
-                const int64_t scratch = p.pl.tile0[w.s] + w.tile;
+            for (int n; ok && (n = w.count(x1)) > 0; wide_next(p, w)) {
+                const int64_t scratch = w.tile0 + w.tile;
                 for (int t = 0; t < n && ok; ++t, ++it) {
                     const uint8_t *src = p.tiles + ((scratch + t) * p.H + w.h) * (2 * KT);
                     const uint32_t ks = it % NK, vs = it % NV;
@@ -423,7 +447,7 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                     mbar_arrive_expect_tx(vfull + 8 * vs, KT);
                     bulk_g2s(sb + A::OFF_V + vs * KT, src + KT, KT, vfull + 8 * vs);
                 }
-                x += n;
+                if (w.ends(x1)) break;
             }
             if (!ok) {  // copies still in flight land before the CTA ends (bounded)
                 for (uint32_t i = it > (uint32_t)NK ? it - NK : 0; i <= it; ++i) {
@@ -455,10 +479,8 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
             bool ok = true;
             uint32_t it = 0, seg = 0;
             WidePlace w = wide_locate(p, x0);
-            for (int64_t x = x0; x < x1 && ok; ++seg) {
-                if (x > x0) wide_next(p, w);
-                const int n = (int)imin64(w.tiles - w.tile, x1 - x);
-                const int64_t cols = paged_new(p.pg.v, w.s) * p.G - (int64_t)(w.e - w.e0) * wC;
+            for (int n; ok && (n = w.count(x1)) > 0; wide_next(p, w), ++seg) {
+                const int64_t cols = w.n * p.G - (int64_t)(w.e - w.e0) * wC;
                 const int groups = cols > 128 ? 2 : 1;
                 ok = mbar_wait_bounded(kfull + 8 * (it % NK), (it / NK) & 1, p.err);
                 for (int g = 0; g < groups && ok; ++g) {
@@ -498,7 +520,7 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                     }
                     if (more && ok) tc_commit(kempty + 8 * nk);
                 }
-                x += n;
+                if (w.ends(x1)) break;
             }
             if (!ok) {  // whatever was issued is through before tensor memory is given back (bounded)
                 tc_commit(drained);
@@ -518,13 +540,11 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
         uint32_t it = 0, seg = 0;
         int shared_from = -1;  // thread 0: the block of the last segment, if it is begun here and not finished
         WidePlace w = wide_locate(p, x0);
-        for (int64_t x = x0; x < x1 && ok; ++seg) {
-            if (x > x0) wide_next(p, w);
-            const int n = (int)imin64(w.tiles - w.tile, x1 - x);
-            const int64_t nn = paged_new(p.pg.v, w.s), len = paged_len(p.pg.v, w.s);
+        for (int n; ok && (n = w.count(x1)) > 0; wide_next(p, w), ++seg) {
+            const int64_t nn = w.n, len = w.len;
             const int64_t col = (int64_t)(w.e - w.e0) * wC + 128 * g + ltid;
             const bool real = col < nn * p.G;
-            const int64_t tok = real ? col / p.G : nn - 1, row = paged_start(p.pg.v, w.s) + tok;
+            const int64_t tok = real ? col / p.G : nn - 1, row = w.s0 + tok;
             const int hq = real ? (int)(col - tok * p.G) : 0;
             const int64_t lim = len - nn + 1 + tok;  // rows that this column sees
             // q, scaled by a power of two that puts its largest |q| in [2^14, 2^15): exact in f16
@@ -559,8 +579,16 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
             }
             fence_proxy_async_smem();
             mbar_arrive(qfull + 8 * g);
+            {  // the next block's q on its way to L2
+                const int64_t nc = col + wC, nt = nc / p.G;
+                if (nc < nn * p.G) {
+                    const uint16_t *a = p.q + (w.s0 + nt) * p.pg.q_token + ((int64_t)w.h * p.G + (nc - nt * p.G)) * p.pg.q_head;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+                    if constexpr (D > 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + 64));
+                }
+            }
 
-            const TileMeta *meta = p.meta + ((int64_t)(p.pl.tile0[w.s] + w.tile) * p.H + w.h);
+            const TileMeta *meta = p.meta + ((int64_t)(w.tile0 + w.tile) * p.H + w.h);
             float R = -INFINITY, l = 0.0f;
             for (int t = 0; t < n; ++t, ++it) {
                 const TileMeta *mt = meta + (int64_t)t * p.H;
@@ -676,13 +704,13 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                     const float inv = l == 0.0f ? 0.0f : p.inv_sqrt_d / l;
                     uint16_t *dst = p.out + (row * p.QH + (int64_t)w.h * p.G + hq) * D;
 #pragma unroll
-                    for (int j = 0; j < D; j += 8) {
-                        uint32_t u[4];
+                    for (int j = 0; j < D; j += 16) {
+                        uint32_t u[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < 8; ++i)
                             u[i] = pack_bf16x2(o[j + 2 * i] * (sign_negative(p.sg, j + 2 * i) ? -inv : inv),
                                                o[j + 2 * i + 1] * (sign_negative(p.sg, j + 2 * i + 1) ? -inv : inv));
-                        *reinterpret_cast<uint4 *>(dst + j) = make_uint4(u[0], u[1], u[2], u[3]);
+                        st_global_v8(dst + j, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
                     }
                 }
             } else {
@@ -695,10 +723,10 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 p.part_ml[2 * at + 1] = l;
                 if (tid == 0 && w.tile == 0) {
                     shared_from = w.e - w.e0;
-                    p.pl.share[blockIdx.x] = WideShare{w.s, w.h, shared_from, (int)((x + w.tiles - 1) / per)};
+                    p.pl.share[blockIdx.x] = WideShare{w.s, w.h, shared_from, (int)((w.at + w.tiles - 1) / per)};
                 }
             }
-            x += n;
+            if (w.ends(x1)) break;
         }
         if (tid == 0 && shared_from < 0) p.pl.share[blockIdx.x].last = -1;
     }
