@@ -385,6 +385,12 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 // thread execute in order: S(t) complete says that P V(t - 1) is complete, so
 // the softmax threads may rescale O between reading S(t) and handing over P(t)
 // without a barrier of its own.
+//
+// The issuing warp runs as a whole with warp-uniform operands, one elected lane
+// issuing (a lone thread with operands in ordinary registers took over 100
+// cycles per MMA, more than the 64 that one of 128 x 128 x 16 takes to run).
+// What runs once per block (q in, masks of the last tiles, un-rotation) is in
+// short loops: unrolled over a row it was 10 us of instruction fetch a block.
 template <int D>
 __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_constant__ WideParams p)
 {
@@ -393,11 +399,13 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + A::OFF_BAR);
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 2 * NK + 2 * NV + 9);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 2 * NK + 2 * NV + 11);
     const uint32_t sb = smem_addr(smem), b0 = smem_addr(bars);
     const uint32_t kfull = b0, kempty = kfull + 8 * NK, vfull = kempty + 8 * NK, vempty = vfull + 8 * NV;
-    const uint32_t qfull = vempty + 8 * NV, sfull = qfull + 16, pfull = sfull + 16, ofull = pfull + 16, drained = ofull + 16;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t qfull = vempty + 8 * NV, sfull = qfull + 16, pfull = sfull + 16, ofull = pfull + 32,
+                   drained = ofull + 16;  // pfull: first halves, then second halves
+    __shared__ WidePlace place[2];
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     pdl_wait_primary();
     pdl_allow_dependents();
@@ -407,9 +415,10 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
     if (tid == 0) {
         for (int i = 0; i < 2 * NK + 2 * NV; ++i) mbar_init(b0 + 8 * i, 1);
         for (int g = 0; g < 2; ++g) {
-            mbar_init(qfull + 8 * g, 128);
+            mbar_init(qfull + 8 * g, 4);  // a warp each
             mbar_init(sfull + 8 * g, 1);
-            mbar_init(pfull + 8 * g, 128);
+            mbar_init(pfull + 8 * g, 4);
+            mbar_init(pfull + 16 + 8 * g, 4);
             mbar_init(ofull + 8 * g, 1);
         }
         mbar_init(drained, 1);
@@ -422,115 +431,131 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tslot;
+    const uint32_t tmem = __reduce_max_sync(0xffffffffu, *tslot);  // (uniform)
 
-    // registers: the softmax threads hold a row of scores each; 256 x 216 + 128 x 72 is what the launch has
+    // registers: the softmax threads hold a row of scores each; 256 x 224 + 128 x 56 is what the launch has
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 9) {
-        // ------------------------------------------------------------ tiles in
-        if (lane == 0) {
-            bool ok = true;
-            uint32_t it = 0;
-            WidePlace w = wide_locate(p, x0);
-            for (int n; ok && (n = w.count(x1)) > 0; wide_next(p, w)) {
-                const int64_t scratch = w.tile0 + w.tile;
-                for (int t = 0; t < n && ok; ++t, ++it) {
-                    const uint8_t *src = p.tiles + ((scratch + t) * p.H + w.h) * (2 * KT);
-                    const uint32_t ks = it % NK, vs = it % NV;
-                    if (it >= NK) ok = mbar_wait_bounded(kempty + 8 * ks, (it / NK - 1) & 1, p.err);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(kfull + 8 * ks, KT);
-                    bulk_g2s(sb + A::OFF_K + ks * KT, src, KT, kfull + 8 * ks);
-                    if (it >= NV) ok = mbar_wait_bounded(vempty + 8 * vs, (it / NV - 1) & 1, p.err);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(vfull + 8 * vs, KT);
-                    bulk_g2s(sb + A::OFF_V + vs * KT, src + KT, KT, vfull + 8 * vs);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 9) {
+            // ------------------------------------------------------------ tiles in
+            if (lane == 0) {
+                bool ok = true;
+                uint32_t it = 0;
+                WidePlace w = wide_locate(p, x0);
+                for (int n; ok && (n = w.count(x1)) > 0; wide_next(p, w)) {
+                    const uint8_t *src = p.tiles + ((int64_t)(w.tile0 + w.tile) * p.H + w.h) * (2 * KT);
+                    for (int t = 0; t < n && ok; ++t, ++it, src += (int64_t)p.H * (2 * KT)) {
+                        const uint32_t ks = it % NK, vs = it % NV;
+                        if (it >= NK) ok = mbar_wait_bounded(kempty + 8 * ks, (it / NK - 1) & 1, p.err);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(kfull + 8 * ks, KT);
+                        bulk_g2s(sb + A::OFF_K + ks * KT, src, KT, kfull + 8 * ks);
+                        if (it >= NV) ok = mbar_wait_bounded(vempty + 8 * vs, (it / NV - 1) & 1, p.err);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(vfull + 8 * vs, KT);
+                        bulk_g2s(sb + A::OFF_V + vs * KT, src + KT, KT, vfull + 8 * vs);
+                    }
+                    if (w.ends(x1)) break;
                 }
-                if (w.ends(x1)) break;
-            }
-            if (!ok) {  // copies still in flight land before the CTA ends (bounded)
-                for (uint32_t i = it > (uint32_t)NK ? it - NK : 0; i <= it; ++i) {
-                    mbar_wait_bounded(kfull + 8 * (i % NK), (i / NK) & 1, p.err);
-                    if (i < it) mbar_wait_bounded(vfull + 8 * (i % NV), (i / NV) & 1, p.err);
+                if (!ok) {  // copies still in flight land before the CTA ends (bounded)
+                    for (uint32_t i = it > (uint32_t)NK ? it - NK : 0; i <= it; ++i) {
+                        mbar_wait_bounded(kfull + 8 * (i % NK), (i / NK) & 1, p.err);
+                        if (i < it) mbar_wait_bounded(vfull + 8 * (i % NV), (i / NV) & 1, p.err);
+                    }
                 }
             }
-        }
-        __syncwarp();
-    } else if (warp == 8) {
-        // ------------------------------------------------------------ MMAs
-        if (lane == 0) {
+            __syncwarp();
+        } else if (warp == 8) {
+            // ------------------------------------------------------------ MMAs
             constexpr uint32_t idesc_qk = tc_idesc(128, wT, 0), idesc_pv = tc_idesc(128, D, 1), SBO = (D / 64) * 1024;
+            const uint32_t leader = tc_elect();
+            // descriptors of the first q, key and value tile; 16-byte units are added to them
+            const uint64_t dq = tc_desc(sb, 16, 1024), dk = tc_desc(sb + A::OFF_K, 16, 1024),
+                           dv = tc_desc(sb + A::OFF_V, 1024, SBO);
+            auto wait = [&](uint32_t bar, uint32_t parity) {  // the same answer in every lane
+                return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.err)) != 0;
+            };
             auto qk = [&](int g, uint32_t ks) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t o = (kk / 4) * (wT * 128) + (kk % 4) * 32;
-                    tc_mma(tmem + g * wT, tc_desc(sb + g * KT + o, 16, 1024), tc_desc(sb + A::OFF_K + ks * KT + o, 16, 1024),
-                           idesc_qk, kk > 0);
+                    const uint32_t o = ((kk / 4) * (wT * 128) + (kk % 4) * 32) >> 4;
+                    tc_mma_elected(leader, tmem + g * wT, dq + (g * KT >> 4) + o, dk + (ks * KT >> 4) + o, idesc_qk, kk > 0);
                 }
-                tc_commit(sfull + 8 * g);
+                tc_commit_elected(leader, sfull + 8 * g);
             };
-            auto pv = [&](int g, uint32_t vs, bool acc) {
+            auto pv = [&](int g, uint32_t vs, int half, uint32_t acc) {
 #pragma unroll
-                for (int kk = 0; kk < wT / 16; ++kk)
-                    tc_mma_ts(tmem + A::O_COL + g * D, tmem + g * wT + kk * 8,
-                              tc_desc(sb + A::OFF_V + vs * KT + kk * 2 * SBO, 1024, SBO), idesc_pv, acc || kk > 0);
+                for (int kk = 0; kk < wT / 32; ++kk) {
+                    const int k = half * (wT / 32) + kk;
+                    tc_mma_ts_elected(leader, tmem + A::O_COL + g * D, tmem + g * wT + k * 8, dv + (vs * KT >> 4) + (k * 2 * SBO >> 4),
+                                      idesc_pv, kk > 0 ? 1u : acc);
+                }
             };
             bool ok = true;
             uint32_t it = 0, seg = 0;
             WidePlace w = wide_locate(p, x0);
-            for (int n; ok && (n = w.count(x1)) > 0; wide_next(p, w), ++seg) {
-                const int64_t cols = w.n * p.G - (int64_t)(w.e - w.e0) * wC;
-                const int groups = cols > 128 ? 2 : 1;
-                ok = mbar_wait_bounded(kfull + 8 * (it % NK), (it / NK) & 1, p.err);
-                for (int g = 0; g < groups && ok; ++g) {
-                    ok = mbar_wait_bounded(qfull + 8 * g, seg & 1, p.err);
-                    if (!ok) break;
-                    tc_fence_after();
-                    qk(g, it % NK);
-                }
-                if (groups == 1 && ok) {  // the idle group's threads keep step through the same barriers
-                    ok = mbar_wait_bounded(qfull + 8, seg & 1, p.err);
-                    tc_commit(sfull + 8);
-                }
+            for (;;) {
+                const int left = w.count(x1);
+                const int n = (int)__reduce_max_sync(0xffffffffu, left > 0 ? (unsigned)left : 0u);
+                if (n == 0) break;
+                const bool two = __any_sync(0xffffffffu, w.n * p.G - (int64_t)(w.e - w.e0) * wC > 128) != 0;  // both groups have columns
+                // the idle group's threads keep step through the same barriers
+                ok = wait(kfull + 8 * (it % NK), (it / NK) & 1) && wait(qfull, seg & 1);
                 if (!ok) break;
-                tc_commit(kempty + 8 * (it % NK));
-                for (int t = 0; t < n && ok; ++t, ++it) {
+                tc_fence_after();
+                qk(0, it % NK);
+                ok = wait(qfull + 8, seg & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (two) qk(1, it % NK);
+                else tc_commit_elected(leader, sfull + 8);
+                tc_commit_elected(leader, kempty + 8 * (it % NK));
+                for (int t = 0; t < n; ++t, ++it) {
                     const bool more = t + 1 < n;
                     const uint32_t vs = it % NV, nk = (it + 1) % NK;
-                    ok = mbar_wait_bounded(vfull + 8 * vs, (it / NV) & 1, p.err);
-                    for (int g = 0; g < groups && ok; ++g) {
-                        ok = mbar_wait_bounded(pfull + 8 * g, it & 1, p.err);
+                    ok = wait(vfull + 8 * vs, (it / NV) & 1) && wait(pfull, it & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    pv(0, vs, 0, t > 0);
+                    ok = wait(pfull + 16, it & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    pv(0, vs, 1, 1);
+                    if (more) {
+                        ok = wait(kfull + 8 * nk, ((it + 1) / NK) & 1);
                         if (!ok) break;
-                        tc_fence_after();
-                        pv(g, vs, t > 0);
-                        if (g == groups - 1) tc_commit(vempty + 8 * vs);
-                        if (more) {
-                            if (g == 0) ok = mbar_wait_bounded(kfull + 8 * nk, ((it + 1) / NK) & 1, p.err);
-                            if (!ok) break;
-                            qk(g, nk);
-                        } else {
-                            tc_commit(ofull + 8 * g);
-                        }
+                        qk(0, nk);
+                    } else {
+                        tc_commit_elected(leader, ofull);
                     }
-                    if (groups == 1 && ok) {
-                        ok = mbar_wait_bounded(pfull + 8, it & 1, p.err);
-                        if (more) tc_commit(sfull + 8);
-                        else tc_commit(ofull + 8);
+                    ok = wait(pfull + 8, it & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (two) pv(1, vs, 0, t > 0);
+                    ok = wait(pfull + 24, it & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (two) pv(1, vs, 1, 1);
+                    tc_commit_elected(leader, vempty + 8 * vs);
+                    if (more) {
+                        if (two) qk(1, nk);
+                        else tc_commit_elected(leader, sfull + 8);
+                        tc_commit_elected(leader, kempty + 8 * nk);
+                    } else {
+                        tc_commit_elected(leader, ofull + 8);
                     }
-                    if (more && ok) tc_commit(kempty + 8 * nk);
                 }
-                if (w.ends(x1)) break;
+                if (!ok || __any_sync(0xffffffffu, w.ends(x1))) break;
+                wide_next(p, w);
+                ++seg;
             }
             if (!ok) {  // whatever was issued is through before tensor memory is given back (bounded)
-                tc_commit(drained);
+                tc_commit_elected(leader, drained);
                 mbar_wait_bounded(drained, 0, p.err);
             }
         }
-        __syncwarp();
-    }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         // ------------------------------------------------------------ softmax, one column a thread
         const int g = warp >> 2, ltid = tid & 127;
         const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
@@ -539,26 +564,28 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
         bool ok = true;
         uint32_t it = 0, seg = 0;
         int shared_from = -1;  // thread 0: the block of the last segment, if it is begun here and not finished
-        WidePlace w = wide_locate(p, x0);
-        for (int n; ok && (n = w.count(x1)) > 0; wide_next(p, w), ++seg) {
-            const int64_t nn = w.n, len = w.len;
-            const int64_t col = (int64_t)(w.e - w.e0) * wC + 128 * g + ltid;
-            const bool real = col < nn * p.G;
-            const int64_t tok = real ? col / p.G : nn - 1, row = w.s0 + tok;
-            const int hq = real ? (int)(col - tok * p.G) : 0;
-            const int64_t lim = len - nn + 1 + tok;  // rows that this column sees
+        // the place is kept in shared memory, out of the registers that hold scores: the group's
+        // first thread moves it on
+        WidePlace &w = place[g];
+        if (ltid == 0) w = wide_locate(p, x0);
+        for (;; ++seg) {
+            // the place is written, and no wait of the group has given up: all leave together
+            if (!named_and(1 + g, 128, ok)) break;
+            const int n = w.count(x1);
+            if (n <= 0) break;
+            const int cols = (int)w.n * p.G, col = (w.e - w.e0) * wC + 128 * g + ltid;  // total * QH < 2^30
+            const bool real = col < cols;
+            const int tok = real ? col / p.G : (int)w.n - 1, hq = real ? col - tok * p.G : 0;
+            int left = (int)(w.len - w.n) + 1 + tok - w.tile * wT;  // rows that this column sees, from the tile's first on
             // q, scaled by a power of two that puts its largest |q| in [2^14, 2^15): exact in f16
             float ie;
             {
-                const uint16_t *qrow = p.q + row * p.pg.q_token + ((int64_t)w.h * p.G + hq) * p.pg.q_head;
+                const uint16_t *qrow = p.q + (w.s0 + tok) * p.pg.q_token + ((int64_t)w.h * p.G + hq) * p.pg.q_head;
                 float mx = 0.0f;
-                uint4 qv[D / 8];
-#pragma unroll
-                for (int c8 = 0; c8 < D / 8; ++c8)
-                    qv[c8] = real ? *reinterpret_cast<const uint4 *>(qrow + 8 * c8) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
+#pragma unroll 4
                 for (int c8 = 0; c8 < D / 8; ++c8) {
-                    const uint32_t uu[4] = {qv[c8].x, qv[c8].y, qv[c8].z, qv[c8].w};
+                    const uint4 u = *reinterpret_cast<const uint4 *>(qrow + 8 * c8);
+                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) mx = max3(mx, fabsf(bf16_lo(uu[i])), fabsf(bf16_hi(uu[i])));
                 }
@@ -567,10 +594,10 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 e = e < -100 ? -100 : (e > 100 ? 100 : e);
                 const float qs = ldexpf(p.qsign, e);
                 ie = ldexpf(1.0f, -e) * p.scale_log2;
-#pragma unroll
+#pragma unroll 4
                 for (int c8 = 0; c8 < D / 8; ++c8) {
-                    const uint4 u = qv[c8];
-                    sts128(sb + g * KT + kmaj_off(128, ltid, 8 * c8),
+                    const uint4 u = *reinterpret_cast<const uint4 *>(qrow + 8 * c8);
+                    sts128(sb + g * KT + (c8 / 8) * (128 * 128) + (ltid / 8) * 1024 + (ltid % 8) * 128 + (((c8 % 8) ^ (ltid % 8)) * 16),
                            make_uint4(tc_pack_f16(bf16_lo(u.x) * qs, bf16_hi(u.x) * qs),
                                       tc_pack_f16(bf16_lo(u.y) * qs, bf16_hi(u.y) * qs),
                                       tc_pack_f16(bf16_lo(u.z) * qs, bf16_hi(u.z) * qs),
@@ -578,96 +605,121 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(qfull + 8 * g);
-            {  // the next block's q on its way to L2
-                const int64_t nc = col + wC, nt = nc / p.G;
-                if (nc < nn * p.G) {
-                    const uint16_t *a = p.q + (w.s0 + nt) * p.pg.q_token + ((int64_t)w.h * p.G + (nc - nt * p.G)) * p.pg.q_head;
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
-                    if constexpr (D > 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + 64));
-                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfull + 8 * g);
+            if (col + wC < cols) {  // the next block's q on its way to L2
+                const int nt = (col + wC) / p.G;
+                const uint16_t *a = p.q + (w.s0 + nt) * p.pg.q_token + ((int64_t)w.h * p.G + (col + wC - nt * p.G)) * p.pg.q_head;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+                if constexpr (D > 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + 64));
             }
 
-            const TileMeta *meta = p.meta + ((int64_t)(w.tile0 + w.tile) * p.H + w.h);
+            const TileMeta *mt = p.meta + ((int64_t)(w.tile0 + w.tile) * p.H + w.h);
             float R = -INFINITY, l = 0.0f;
-            for (int t = 0; t < n; ++t, ++it) {
-                const TileMeta *mt = meta + (int64_t)t * p.H;
-                const float f = ie * mt->kf, e = mt->e, lf = mt->lf;
+            for (int t = 0; t < n; ++t, ++it, mt += p.H, left -= wT) {
+                const float e = mt->e, lf = mt->lf;
+                // (a scale of zero: the smallest normal, so that hidden scores stay -inf)
+                const float f = fmaxf(ie * mt->kf, 1.17549435e-38f);
                 const uint32_t any = mt->any;
-                const int64_t left = lim - (int64_t)(w.tile + t) * wT;
-                const int vis = left < 0 ? 0 : (left > wT ? wT : (int)left);
-                if (!mbar_wait_bounded(bar_s, it & 1, p.err)) {
-                    ok = false;
-                    break;
-                }
+                const int vis = left < 0 ? 0 : (left > wT ? wT : left);
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar_s, it & 1, p.err));
+                if (!ok) break;
                 tc_fence_after();
-                uint32_t sr[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tc_ld32(t_s + 32 * c, sr[c]);
-                tc_wait_ld();
-                // CUT: some column of the warp does not see the whole tile (the last ones only)
-                auto step = [&](auto cut_) __attribute__((always_inline)) {
-                constexpr bool CUT = decltype(cut_)::value;
-                if constexpr (CUT)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (32 * c + j >= vis) sr[c][j] = 0xFF800000u;
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int j = 0; j < 32; j += 2)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) m4[c] = max3(m4[c], __uint_as_float(sr[c][j]), __uint_as_float(sr[c][j + 1]));
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                const float top = mx == -INFINITY ? -INFINITY : fmaf(mx, f, e);
-                if (t == 0) {
-                    R = top;
-                } else if (__any_sync(0xffffffffu, top > R + wTau)) {
-                    const float Rn = top > R + wTau ? top : R;
-                    const float a = R == -INFINITY ? 0.0f : tc_ex2(R - Rn);  // nothing was summed before the first row seen
-                    R = Rn;
-                    l *= a;
+                if (__any_sync(0xffffffffu, vis < wT)) {  // some column does not see the whole tile: its hidden scores become -inf
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tc_ld32(t_o + 32 * c, o);
+                    for (int c = 0; c < wT; c += 16) {
+                        uint32_t x[16];
+                        tc_ld16(t_s + c, x);
                         tc_wait_ld();
+                        tc_pin(x);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
-                        uint32_t lo[16], hi[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            lo[j] = o[j];
-                            hi[j] = o[16 + j];
-                        }
-                        tc_st16(t_o + 32 * c, lo);
-                        tc_st16(t_o + 32 * c + 16, hi);
+                        for (int j = 0; j < 16; ++j)
+                            if (c + j >= vis) x[j] = 0xFF800000u;
+                        tc_st16(t_s + c, x);
                     }
+                    tc_wait_st();
                 }
-                const float add = R == -INFINITY ? 0.0f : e - R + wUp;
-                const float2 f2 = make_float2(f, f), a2 = make_float2(add, add);
-                float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                uint32_t sr[4][32];
+                float2 ls[2];
+                const float2 f2 = make_float2(f, f);
+                // weights of 32 rows at the reference R, into tensor memory over the scores
+                auto weights = [&](int c, float add) __attribute__((always_inline)) {
+                    const float2 a2 = make_float2(add, add);
                     uint32_t pp[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[c][j]), __uint_as_float(sr[c][j + 1])), f2, a2);
-                        float p0 = tc_ex2(y.x), p1 = tc_ex2(y.y);
-                        if constexpr (CUT) {
-                            if (32 * c + j >= vis) p0 = 0.0f;
-                            if (32 * c + j + 1 >= vis) p1 = 0.0f;
-                        }
+                        const float p0 = tc_ex2(y.x), p1 = tc_ex2(y.y);
                         ls[(j >> 1) & 1] = __fadd2_rn(ls[(j >> 1) & 1], make_float2(p0, p1));
                         pp[j / 2] = tc_pack_f16(p0, p1);
                     }
                     tc_st16(t_s + 16 * c, pp);
-                }
-                l = fmaf((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y), lf, l);
                 };
-                if (__any_sync(0xffffffffu, vis < wT)) step(std::true_type{});
-                else step(std::false_type{});
+                auto largest = [&](int c0) __attribute__((always_inline)) {  // of 64 scores
+                    float a = -INFINITY, b = -INFINITY, d = -INFINITY, h = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        a = max3(a, __uint_as_float(sr[c0][j]), __uint_as_float(sr[c0][j + 1]));
+                        b = max3(b, __uint_as_float(sr[c0][j + 2]), __uint_as_float(sr[c0][j + 3]));
+                        d = max3(d, __uint_as_float(sr[c0 + 1][j]), __uint_as_float(sr[c0 + 1][j + 1]));
+                        h = max3(h, __uint_as_float(sr[c0 + 1][j + 2]), __uint_as_float(sr[c0 + 1][j + 3]));
+                    }
+                    return fmaxf(fmaxf(a, b), fmaxf(d, h));
+                };
+                // the first half of P is handed over while the second is still worked on
+                auto hand = [&](uint32_t bar) __attribute__((always_inline)) {
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar);
+                };
+                tc_ld32(t_s, sr[0]);
+                tc_ld32(t_s + 32, sr[1]);
+                tc_wait_ld();
+                tc_pin(sr[0]);
+                tc_pin(sr[1]);
+                tc_ld32(t_s + 64, sr[2]);
+                tc_ld32(t_s + 96, sr[3]);
+                const float m0 = largest(0);
+                // the weights of the first half are taken at the R there is, and again where the
+                // maximum has outgrown it (on a block's first tile, and seldom after)
+                float add = R == -INFINITY ? 0.0f : e - R + wUp;
+                bool checked = false;
+#pragma unroll 1
+                for (;;) {
+                    ls[0] = ls[1] = make_float2(0.0f, 0.0f);
+                    weights(0, add);
+                    weights(1, add);
+                    if (checked) break;
+                    checked = true;
+                    tc_wait_ld();
+                    tc_pin(sr[2]);
+                    tc_pin(sr[3]);
+                    const float mx = fmaxf(m0, largest(2));
+                    const float top = mx == -INFINITY ? -INFINITY : fmaf(mx, f, e);
+                    if (!__any_sync(0xffffffffu, top > R + wTau)) break;
+                    const float Rn = top > R + wTau ? top : R;
+                    const float a = R == -INFINITY ? 0.0f : tc_ex2(R - Rn);  // nothing was summed before the first row seen
+                    R = Rn;
+                    l *= a;
+                    if (t > 0)
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tc_ld16(t_o + c, o);
+                            tc_wait_ld();
+                            tc_pin(o);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
+                            tc_st16(t_o + c, o);
+                        }
+                    add = R == -INFINITY ? 0.0f : e - R + wUp;
+                }
+                hand(bar_p);
+                weights(2, add);
+                weights(3, add);
+                hand(bar_p + 16);
+                l = fmaf((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y), lf, l);
                 if (any) {
 #pragma unroll 1
                     for (int i = 0; i < 4; ++i) {
@@ -676,49 +728,81 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                         if (mt->bad[i] & seen) l = NAN;
                     }
                 }
-                tc_wait_st();
-                tc_fence_before();
-                mbar_arrive(bar_p);
             }
-            if (ok) ok = mbar_wait_bounded(ofull + 8 * g, seg & 1, p.err);
-            if (!ok) break;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(ofull + 8 * g, seg & 1, p.err));
             tc_fence_after();
-            float o[D];
+            if (ok && n == w.tiles) {
+                // the whole block: un-rotate, divide, round.  The Sylvester transform of D
+                // values is one of D / 16 over stride 16, then one of 16: in tensor memory
+                // between the two, 16 values of the row at a time
+                constexpr int NS = D / 16;
+#pragma unroll 1
+                for (int j = 0; j < 16; j += 2) {
+                    uint32_t x[NS][2];
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) tc_ld32(t_o + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&o[32 * c]));
-            tc_wait_ld();
-            tc_fence_before();
-            if (n == w.tiles) {
-                // the whole block: un-rotate (Sylvester stages 1, 2, 4, ...), divide, round
+                    for (int k = 0; k < NS; ++k) tc_ld2(t_o + 16 * k + j, x[k]);
+                    tc_wait_ld();
 #pragma unroll
-                for (int hs = 1; hs < D; hs <<= 1)
+                    for (int k = 0; k < NS; ++k) tc_pin(x[k]);
 #pragma unroll
-                    for (int k = 0; k < D; k += 2 * hs)
+                    for (int hs = 1; hs < NS; hs <<= 1)
 #pragma unroll
-                        for (int j = k; j < k + hs; ++j) {
-                            const float u = o[j], v = o[j + hs];
-                            o[j] = u + v;
-                            o[j + hs] = u - v;
-                        }
-                if (real) {
-                    const float inv = l == 0.0f ? 0.0f : p.inv_sqrt_d / l;
-                    uint16_t *dst = p.out + (row * p.QH + (int64_t)w.h * p.G + hq) * D;
+                        for (int k = 0; k < NS; k += 2 * hs)
 #pragma unroll
-                    for (int j = 0; j < D; j += 16) {
-                        uint32_t u[8];
+                            for (int m = k; m < k + hs; ++m)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            u[i] = pack_bf16x2(o[j + 2 * i] * (sign_negative(p.sg, j + 2 * i) ? -inv : inv),
-                                               o[j + 2 * i + 1] * (sign_negative(p.sg, j + 2 * i + 1) ? -inv : inv));
-                        st_global_v8(dst + j, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
-                    }
+                                for (int q = 0; q < 2; ++q) {
+                                    const float u = __uint_as_float(x[m][q]), v = __uint_as_float(x[m + hs][q]);
+                                    x[m][q] = __float_as_uint(u + v);
+                                    x[m + hs][q] = __float_as_uint(u - v);
+                                }
+#pragma unroll
+                    for (int k = 0; k < NS; ++k) tc_st2(t_o + 16 * k + j, x[k]);
                 }
-            } else {
+                tc_wait_st();
+                const float inv = l == 0.0f ? 0.0f : p.inv_sqrt_d / l;
+                const int tk = real ? col / p.G : 0;
+                uint16_t *dst = p.out + ((w.s0 + tk) * p.QH + (int64_t)w.h * p.G + (real ? col - tk * p.G : 0)) * D;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t x[16];
+                    tc_ld16(t_o + c, x);
+                    tc_wait_ld();
+                    tc_pin(x);
+                    float y[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(x[j]);
+#pragma unroll
+                    for (int hs = 1; hs < 16; hs <<= 1)
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2 * hs)
+#pragma unroll
+                            for (int m = k; m < k + hs; ++m) {
+                                const float u = y[m], v = y[m + hs];
+                                y[m] = u + v;
+                                y[m + hs] = u - v;
+                            }
+                    const uint32_t sg = p.sg.w[c >> 5] >> (c & 16);
+                    uint32_t u[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        u[i] = pack_bf16x2(__uint_as_float(__float_as_uint(y[2 * i] * inv) ^ (sg << (31 - 2 * i) & 0x80000000u)),
+                                           __uint_as_float(__float_as_uint(y[2 * i + 1] * inv) ^ (sg << (30 - 2 * i) & 0x80000000u)));
+                    if (real) st_global_v8(dst + c, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
+                }
+            } else if (ok) {
                 // a share of a block: slot 2 c of a CTA when the block began in an earlier one, else 2 c + 1
                 const int64_t at = ((int64_t)2 * blockIdx.x + (w.tile == 0 ? 1 : 0)) * wC + 128 * g + ltid;
-                float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D);
-#pragma unroll
-                for (int j = 0; j < D; j += 4) dst[j / 4] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t x[16];
+                    tc_ld16(t_o + c, x);
+                    tc_wait_ld();
+                    tc_pin(x);
+                    float *dst = p.part_o + at * D + c;
+                    st_global_v8(dst, x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
+                    st_global_v8(dst + 8, x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15]);
+                }
                 p.part_ml[2 * at] = R - wUp;  // R = -inf (nothing seen): weight 0
                 p.part_ml[2 * at + 1] = l;
                 if (tid == 0 && w.tile == 0) {
@@ -726,7 +810,10 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                     p.pl.share[blockIdx.x] = WideShare{w.s, w.h, shared_from, (int)((w.at + w.tiles - 1) / per)};
                 }
             }
+            tc_fence_before();
             if (w.ends(x1)) break;
+            named_and(1 + g, 128, true);  // all have read the place
+            if (ltid == 0) wide_next(p, w);
         }
         if (tid == 0 && shared_from < 0) p.pl.share[blockIdx.x].last = -1;
     }
