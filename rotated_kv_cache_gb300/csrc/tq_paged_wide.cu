@@ -45,7 +45,7 @@ constexpr int wT = 128;    // rows per tile
 constexpr int wC = 256;    // columns per block (two groups of the MMA's 128)
 constexpr int wThreads = 384;  // two softmax warpgroups; MMA warp, tile warp (and two idle ones)
 constexpr int wPlanThreads = 256;
-constexpr int wStart = 6;  // what a block costs besides its tiles (q in, out of tensor memory, un-rotation), in tiles
+constexpr int wStart = 7;  // what a block costs besides its tiles (q in, out of tensor memory, un-rotation), in tiles
 constexpr float wTau = 8.0f, wUp = 6.0f;  // lazy raise of R; weights are 2^(s - R + wUp)
 
 // What expand says about a tile.
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(wPlanThreads) wide_plan_kernel(const __grid_co
         const int64_t total = line * p.H;
         int64_t per = (total + p.ctas - 1) / p.ctas;
         p.pl.line[0] = total;
-        p.pl.line[1] = per < 2 * wStart ? 2 * wStart : per;  // no run of little more than a start
+        p.pl.line[1] = per < wStart ? wStart : per;  // no run of less than a start
     }
 }
 
@@ -375,6 +375,13 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
 
@@ -577,31 +584,38 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
             const bool real = col < cols;
             const int tok = real ? col / p.G : (int)w.n - 1, hq = real ? col - tok * p.G : 0;
             int left = (int)(w.len - w.n) + 1 + tok - w.tile * wT;  // rows that this column sees, from the tile's first on
-            // q, scaled by a power of two that puts its largest |q| in [2^14, 2^15): exact in f16
-            float ie;
+            // q, scaled by a power of two that puts its largest |q| in [2^14, 2^15): exact in f16.
+            // D / 8 lanes read a row of the warp's 32 together, every row under way before the first is used
+            float ie = 0.0f;
             {
-                const uint16_t *qrow = p.q + (w.s0 + tok) * p.pg.q_token + ((int64_t)w.h * p.G + hq) * p.pg.q_head;
-                float mx = 0.0f;
-#pragma unroll 4
-                for (int c8 = 0; c8 < D / 8; ++c8) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(qrow + 8 * c8);
-                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+                constexpr int LR = D / 8, RI = 32 / LR, NI = 32 / RI;  // lanes per row, rows per step, steps
+                const int64_t mine = real ? (w.s0 + tok) * p.pg.q_token + ((int64_t)w.h * p.G + hq) * p.pg.q_head : -1;
+                const int c8 = lane % LR, sub = lane / LR;
+                uint4 u[NI];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mx = max3(mx, fabsf(bf16_lo(uu[i])), fabsf(bf16_hi(uu[i])));
+                for (int i = 0; i < NI; ++i) {
+                    const int64_t at = __shfl_sync(0xffffffffu, mine, i * RI + sub);
+                    u[i] = at >= 0 ? *reinterpret_cast<const uint4 *>(p.q + at + 8 * c8) : make_uint4(0u, 0u, 0u, 0u);
                 }
-                int e = 0;
-                if (mx > 0.0f && mx < INFINITY) e = 14 - (((int)(__float_as_uint(mx) >> 23) & 0xFF) - 127);
-                e = e < -100 ? -100 : (e > 100 ? 100 : e);
-                const float qs = ldexpf(p.qsign, e);
-                ie = ldexpf(1.0f, -e) * p.scale_log2;
-#pragma unroll 4
-                for (int c8 = 0; c8 < D / 8; ++c8) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(qrow + 8 * c8);
-                    sts128(sb + g * KT + (c8 / 8) * (128 * 128) + (ltid / 8) * 1024 + (ltid % 8) * 128 + (((c8 % 8) ^ (ltid % 8)) * 16),
-                           make_uint4(tc_pack_f16(bf16_lo(u.x) * qs, bf16_hi(u.x) * qs),
-                                      tc_pack_f16(bf16_lo(u.y) * qs, bf16_hi(u.y) * qs),
-                                      tc_pack_f16(bf16_lo(u.z) * qs, bf16_hi(u.z) * qs),
-                                      tc_pack_f16(bf16_lo(u.w) * qs, bf16_hi(u.w) * qs)));
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const uint32_t m = 0x7FFF7FFFu;
+                    const uint32_t b = bf16x2_max(bf16x2_max(u[i].x & m, u[i].y & m), bf16x2_max(u[i].z & m, u[i].w & m));
+                    float mx = fmaxf(bf16_lo(b), bf16_hi(b));
+#pragma unroll
+                    for (int o = LR / 2; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    int e = 0;
+                    if (mx > 0.0f && mx < INFINITY) e = 14 - (((int)(__float_as_uint(mx) >> 23) & 0xFF) - 127);
+                    e = e < -100 ? -100 : (e > 100 ? 100 : e);
+                    const float qs = __uint_as_float((uint32_t)(127 + e) << 23) * p.qsign;
+                    const int er = __shfl_sync(0xffffffffu, e, (lane % RI) * LR);  // of row i RI + lane % RI
+                    if (lane / RI == i) ie = __uint_as_float((uint32_t)(127 - er) << 23) * p.scale_log2;
+                    const int r = 32 * (warp & 3) + i * RI + sub;
+                    sts128(sb + g * KT + (c8 / 8) * (128 * 128) + (r / 8) * 1024 + (r % 8) * 128 + (((c8 % 8) ^ (r % 8)) * 16),
+                           make_uint4(tc_pack_f16(bf16_lo(u[i].x) * qs, bf16_hi(u[i].x) * qs),
+                                      tc_pack_f16(bf16_lo(u[i].y) * qs, bf16_hi(u[i].y) * qs),
+                                      tc_pack_f16(bf16_lo(u[i].z) * qs, bf16_hi(u[i].z) * qs),
+                                      tc_pack_f16(bf16_lo(u[i].w) * qs, bf16_hi(u[i].w) * qs)));
                 }
             }
             fence_proxy_async_smem();
@@ -737,10 +751,10 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 // between the two, 16 values of the row at a time
                 constexpr int NS = D / 16;
 #pragma unroll 1
-                for (int j = 0; j < 16; j += 2) {
-                    uint32_t x[NS][2];
+                for (int j = 0; j < 16; j += 4) {
+                    uint32_t x[NS][4];
 #pragma unroll
-                    for (int k = 0; k < NS; ++k) tc_ld2(t_o + 16 * k + j, x[k]);
+                    for (int k = 0; k < NS; ++k) tc_ld4(t_o + 16 * k + j, x[k]);
                     tc_wait_ld();
 #pragma unroll
                     for (int k = 0; k < NS; ++k) tc_pin(x[k]);
@@ -751,19 +765,19 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
 #pragma unroll
                             for (int m = k; m < k + hs; ++m)
 #pragma unroll
-                                for (int q = 0; q < 2; ++q) {
+                                for (int q = 0; q < 4; ++q) {
                                     const float u = __uint_as_float(x[m][q]), v = __uint_as_float(x[m + hs][q]);
                                     x[m][q] = __float_as_uint(u + v);
                                     x[m + hs][q] = __float_as_uint(u - v);
                                 }
 #pragma unroll
-                    for (int k = 0; k < NS; ++k) tc_st2(t_o + 16 * k + j, x[k]);
+                    for (int k = 0; k < NS; ++k) tc_st4(t_o + 16 * k + j, x[k]);
                 }
                 tc_wait_st();
                 const float inv = l == 0.0f ? 0.0f : p.inv_sqrt_d / l;
                 const int tk = real ? col / p.G : 0;
                 uint16_t *dst = p.out + ((w.s0 + tk) * p.QH + (int64_t)w.h * p.G + (real ? col - tk * p.G : 0)) * D;
-#pragma unroll 1
+#pragma unroll 2
                 for (int c = 0; c < D; c += 16) {
                     uint32_t x[16];
                     tc_ld16(t_o + c, x);
