@@ -220,20 +220,21 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
     const int split = blockIdx.x, hv = blockIdx.y, b = blockIdx.z;
     const int h = PAGED ? seg.h : hv / nbp, hb0 = PAGED ? 0 : (hv - h * nbp) * NBC;  // the CTA's first column block
     const int64_t bh = (int64_t)b * p.H + h;
-    const int64_t t_begin = PAGED ? (int64_t)seg.first * A::ST : (int64_t)split * p.tokens_per_split;
-    // paged: column c of the block sees rows [0, base0 + c / G)
-    const int col0 = PAGED ? seg.hb * NH : 0;
-    const int cols = PAGED ? imin_int(seg.n * p.G - col0, NH) : 0;
-    const int base0 = PAGED ? seg.len - seg.n + 1 : 0;
-    const int64_t t_end = PAGED ? imin64(base0 + (col0 + cols - 1) / p.G, t_begin + (int64_t)seg.count * A::ST)
-                                : imin64(p.seq_len, t_begin + p.tokens_per_split);
-    const int n_stages = t_end > t_begin && (!PAGED || ok) ? (int)((t_end - t_begin + A::ST - 1) / A::ST) : 0;
-    PagedPages pages;
+    const int64_t t_begin = PAGED ? 0 : (int64_t)split * p.tokens_per_split;
+    const int64_t t_end = PAGED ? 0 : imin64(p.seq_len, t_begin + p.tokens_per_split);
+    // paged: the block's columns are col0 .. col0 + cols - 1; rows that column c sees, from the
+    // segment's first row on
+    auto block_cols = [&] { return imin_int(seg.n * p.G - seg.hb * NH, NH); };
+    auto column_rows = [&](int c) { return seg.len - seg.n + 1 + (seg.hb * NH + c) / p.G - seg.first * A::ST; };
+    // row offsets within the split fit 32 bits: a split never holds 2^31 rows
+    // (136 B per row at the smallest width would take 292 GB)
+    const int split_rows = PAGED ? imin_int(column_rows(block_cols() - 1), seg.count * A::ST) : (int)(t_end - t_begin);
+    const int n_stages = split_rows > 0 && (!PAGED || ok) ? (split_rows + A::ST - 1) / A::ST : 0;
 
     // paged: every lane of the warp calls, with the page of its chunk
     auto issue_paged = [&](int s, int at_slot, int page) {
         const int ru = p.pg.ru;
-        const int live = (int)((imin64(A::ST, t_end - (t_begin + (int64_t)s * A::ST)) + ru - 1) / ru);  // chunks with rows to read
+        const int live = (imin_int(A::ST, split_rows - s * A::ST) + ru - 1) / ru;  // chunks with rows to read
         const uint32_t st = smem_addr(stages + at_slot * A::STAGE), bar = full0 + 8 * at_slot;
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(live * ru * (A::KROW + 3 * NG * 2 + A::RBV)));
         __syncwarp();
@@ -277,12 +278,10 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
             for (int s = 0; s < kStages && s < n_stages; ++s) issue(s);
     }
     if constexpr (PAGED) {
-        paged_pages_start(p.pg, seg, pages, lane);
         __syncwarp();
-        for (int s = 0; s < kStages && s < n_stages; ++s) {
-            const int page = paged_pages_at(p.pg, seg, pages, seg.first + s, lane);
-            if (warp == 0) issue_paged(s, (slot + s) % kStages, page);
-        }
+        if (warp == 0)
+            for (int s = 0; s < kStages && s < n_stages; ++s)
+                issue_paged(s, (slot + s) % kStages, paged_chunk_page(p.pg, seg, seg.first + s, lane));
     }
     if (!PAGED || nseg == 0) __syncthreads();
 
@@ -302,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
         const int gq = kG * (hb0 + nb) + g;
         const uint16_t *qrow;
         if constexpr (PAGED) {
-            const int col = col0 + (gq < cols ? gq : cols - 1), qi = col / p.G;
+            const int col = seg.hb * NH + imin_int(gq, block_cols() - 1), qi = col / p.G;
             qrow = p.q + (seg.s0 + qi) * p.pg.q_token + ((int64_t)h * p.G + (col - qi * p.G)) * p.pg.q_head;
         } else {
             qrow = p.q + ((int64_t)b * p.QH + (int64_t)h * p.G + (gq < p.G ? gq : p.G - 1)) * D;
@@ -424,13 +423,10 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
     uint32_t voff[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) voff[q] = A::OFF_V + vr[q] * A::RBV + 4 * v_word;
-    // token offsets within the split fit 32 bits: a split never holds 2^31 rows
-    // (136 B per row at the smallest width would take 292 GB)
-    const int split_rows = (int)(t_end - t_begin);
     const uint32_t ring0 = smem_addr(stages);
     // PAGED, several new tokens: rows from here on are hidden from some column
-    const int first_hidden = PAGED ? base0 + col0 / p.G - (int)t_begin : 0;
-    const bool causal = PAGED && seg.n > 1;
+    const int first_hidden = PAGED && seg.n > 1 ? column_rows(0) : INT32_MAX;
+    int next_page = PAGED ? paged_chunk_page(p.pg, seg, seg.first + kStages, lane) : 0;  // of the next refill
     if constexpr (!PAGED) {
         ok = true;
         slot = 0;
@@ -542,13 +538,12 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
                     }
                 }
                 if constexpr (PAGED) {
-                    if (causal && tile_r + 16 > first_hidden) {
+                    if (tile_r + 16 > first_hidden) {
 #pragma unroll
                         for (int nb = 0; nb < NBC; ++nb)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const int col = imin_int(kG * nb + 2 * c + j, cols - 1);
-                                const int lim = base0 + (col0 + col) / p.G - (int)t_begin - tile_r;  // rows of the tile it sees
+                                const int lim = column_rows(imin_int(kG * nb + 2 * c + j, block_cols() - 1)) - tile_r;  // rows of the tile it sees
                                 if (g >= lim) S[nb][t2][0][j] = -INFINITY;
                                 if (g + 8 >= lim) S[nb][t2][1][j] = -INFINITY;
                             }
@@ -641,13 +636,12 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
             // paged: a hidden row's rms may be anything; the weights of the lane's column (g of
             // each block) keep to the rows it sees
             uint32_t seen[NBC][2];
-            const bool masked = causal && tile_r + 16 > first_hidden;
+            const bool masked = PAGED && tile_r + 16 > first_hidden;
             if constexpr (PAGED) {
                 if (masked) {
 #pragma unroll
                     for (int nb = 0; nb < NBC; ++nb) {
-                        const int col = imin_int(kG * nb + g, cols - 1);
-                        const int lim = base0 + (col0 + col) / p.G - (int)t_begin - tile_r + 16 * warp;
+                        const int lim = column_rows(imin_int(kG * nb + g, block_cols() - 1)) - tile_r + 16 * warp;
                         seen[nb][0] = (vr[0] < lim ? 0xFFFFu : 0u) | (vr[1] < lim ? 0xFFFF0000u : 0u);
                         seen[nb][1] = (vr[2] < lim ? 0xFFFFu : 0u) | (vr[3] < lim ? 0xFFFF0000u : 0u);
                     }
@@ -744,14 +738,14 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
         // the last warp to finish this stage refills its slot with stage s + kStages
         __syncwarp();
         if constexpr (PAGED) {
-            const int page = paged_pages_at(p.pg, seg, pages, seg.first + s + kStages, lane);
             uint32_t last = 0;
             if (lane == 0) {
                 __threadfence_block();
                 last = atomicAdd(&done[slot], 1u) == kCW - 1;
                 if (last) done[slot] = 0;
             }
-            if (__shfl_sync(0xffffffffu, last, 0) && s + kStages < n_stages) issue_paged(s + kStages, slot, page);
+            if (__shfl_sync(0xffffffffu, last, 0) && s + kStages < n_stages) issue_paged(s + kStages, slot, next_page);
+            next_page = paged_chunk_page(p.pg, seg, seg.first + s + kStages + 1, lane);
         } else if (lane == 0) {
             __threadfence_block();
             if (atomicAdd(&done[slot], 1u) == kCW - 1) {

@@ -313,7 +313,6 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     const int64_t t_end = imin64(lim_hi, t_begin + (PAGED ? (int64_t)seg.count * gT : p.tokens_per_split));
     const int n_stages = t_end > t_begin && ok ? (int)((t_end - t_begin + gT - 1) / gT) : 0;
     const int NG = D / 32;
-    PagedPages pages;
 
     // paged: every lane of the warp calls, with the page of its chunk
     auto issue_paged = [&](int s, int page) {
@@ -373,12 +372,9 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
             for (int s = 0; s < p.stages && s < n_stages; ++s) issue(s);
     }
     if constexpr (PAGED) {
-        paged_pages_start(p.pg, seg, pages, lane);
         __syncwarp();
-        for (int s = 0; s < p.stages && s < n_stages; ++s) {
-            const int page = paged_pages_at(p.pg, seg, pages, seg.first + s, lane);
-            if (warp == 0) issue_paged(s, page);
-        }
+        if (warp == 0)
+            for (int s = 0; s < p.stages && s < n_stages; ++s) issue_paged(s, paged_chunk_page(p.pg, seg, seg.first + s, lane));
     }
     if constexpr (VLUT == 0)
         for (int i = threadIdx.x; i < (1 << p.vb); i += blockDim.x) lut[i] = p.cen[i];
@@ -492,6 +488,7 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     constexpr int QF_NB = gN * A::QCOL;  // bytes of q fragments per block of 8 columns
     const uint32_t qf_lane = smem_addr(qf) + g * A::QCOL + c * 8, lut_a = smem_addr(lut);
 
+    int next_page = PAGED ? paged_chunk_page(p.pg, seg, seg.first + p.stages, lane) : 0;  // of the next refill
     int s = 0;
     for (; s < n_stages; ++s) {
         const int slot = (it0 + s) % p.stages;
@@ -770,14 +767,14 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
         }
         __syncwarp();
         if constexpr (PAGED) {
-            const int page = paged_pages_at(p.pg, seg, pages, seg.first + s + p.stages, lane);
             uint32_t last = 0;
             if (lane == 0) {
                 __threadfence_block();
                 last = atomicAdd(&done[slot], 1u) == A::W - 1;
                 if (last) done[slot] = 0;
             }
-            if (__shfl_sync(0xffffffffu, last, 0) && s + p.stages < n_stages) issue_paged(s + p.stages, page);
+            if (__shfl_sync(0xffffffffu, last, 0) && s + p.stages < n_stages) issue_paged(s + p.stages, next_page);
+            next_page = paged_chunk_page(p.pg, seg, seg.first + s + p.stages + 1, lane);
         } else if (lane == 0) {
             __threadfence_block();
             if (atomicAdd(&done[slot], 1u) == A::W - 1) {

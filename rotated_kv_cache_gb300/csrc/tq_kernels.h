@@ -78,7 +78,7 @@ struct PagedSplit {
     int64_t *plan;            // [seqs + 1] stages before a sequence, [seqs + 1] units before it, per
     int64_t slots;            // partial slots of the workspace
     int64_t wide;             // sequences with more new tokens than this are another kernel's
-    int nch, spl, ru;         // chunks per stage, stages whose pages a warp loads at once, rows per chunk
+    int nch, ru;              // chunks per stage, rows per chunk
 };
 
 __host__ __device__ constexpr int64_t paged_plan_words(int64_t seqs) { return 2 * (seqs + 1) + 1; }
@@ -97,7 +97,6 @@ inline void set_paged_chunks(PagedSplit &p, int stage, int page)
 {
     p.ru = gcd_int(stage, page);
     p.nch = stage / p.ru;
-    p.spl = 32 / p.nch;
 }
 
 // A split kernel's geometry for a paged batch: rows per stage, columns per

@@ -208,51 +208,33 @@ __device__ __forceinline__ void paged_walk_next(const PagedSplit &ps, PagedWalk 
     paged_segment(ps, w, nxt);
 }
 
-// The page numbers of a segment's chunks (ru = gcd(stage rows, page rows) rows
-// each, so that no chunk crosses a page), ps.spl stages ahead at a time, one
-// chunk a lane: a refill finds its pages in a register.
-struct PagedPages {
-    int base = 0, cur = 0, nxt = 0;  // first stage of `cur`; the lane's page numbers, and of the next load
-};
+// A stage is copied in chunks of ps.ru = gcd(stage rows, page rows) rows, so that
+// no chunk crosses a page; lane c of the refilling warp copies chunk c.
 
-// Row of the sequence where chunk `lane` of `stage` starts.
+// Row of the sequence where chunk `chunk` of `stage` starts.
 __device__ __forceinline__ uint32_t paged_chunk_row(const PagedSplit &ps, int stage, int chunk)
 {
     return (uint32_t)((stage * ps.nch + chunk) * ps.ru);
 }
 
-__device__ __forceinline__ int paged_pages_load(const PagedSplit &ps, const PagedSegment &g, int stage0, int lane)
+// Page number (unchecked) of the lane's chunk of `stage`, 0 where it has no
+// rows.  Loaded a stage before it is used.
+__device__ __forceinline__ int paged_chunk_page(const PagedSplit &ps, const PagedSegment &g, int stage, int lane)
 {
-    const int st = stage0 + lane / ps.nch, ch = lane % ps.nch;
-    const uint32_t row = paged_chunk_row(ps, st, ch);
-    if (lane >= ps.spl * ps.nch || row >= (uint32_t)g.len) return 0;
-    uint32_t slot;
-    const int pg = paged_page(ps.v, g.s, row, slot);
-    return pg < 0 ? 0 : pg;
+    const uint32_t row = paged_chunk_row(ps, stage, lane);
+    if (lane >= ps.nch || row >= (uint32_t)g.len) return 0;
+    return ps.v.pages[g.s * ps.v.stride + fast_div(row, ps.v.div_page)];
 }
 
-__device__ __forceinline__ void paged_pages_start(const PagedSplit &ps, const PagedSegment &g, PagedPages &pp, int lane)
-{
-    pp.base = g.first;
-    pp.cur = paged_pages_load(ps, g, pp.base, lane);
-    pp.nxt = paged_pages_load(ps, g, pp.base + ps.spl, lane);
-}
-
-// Page of chunk (lane) of `stage`, which is base or later; whole warps call it in stage order.
-__device__ __forceinline__ int paged_pages_at(const PagedSplit &ps, const PagedSegment &g, PagedPages &pp, int stage, int lane)
-{
-    while (stage >= pp.base + ps.spl) {
-        pp.base += ps.spl;
-        pp.cur = pp.nxt;
-        pp.nxt = paged_pages_load(ps, g, pp.base + ps.spl, lane);
-    }
-    return __shfl_sync(0xffffffffu, pp.cur, (stage - pp.base) * ps.nch + (lane < ps.nch ? lane : 0));
-}
-
-// Plane row of that chunk for the segment's kv-head.
+// Plane row of that chunk for the segment's kv-head; a bad page number is
+// recorded, and page 0 read in its place.
 __device__ __forceinline__ int64_t paged_chunk_plane_row(const PagedSplit &ps, const PagedSegment &g, int H, int page,
                                                          int stage, int chunk)
 {
+    if ((uint32_t)page >= (uint32_t)ps.v.num_pages) {
+        atomicOr(ps.v.err, kErrPage);
+        page = 0;
+    }
     const uint32_t row = paged_chunk_row(ps, stage, chunk);
     return ((int64_t)page * H + g.h) * ps.v.page + (row - fast_div(row, ps.v.div_page) * ps.v.page);
 }

@@ -251,7 +251,7 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
     if (!paged_plan(c, b, QH, pl)) return cudaErrorInvalidConfiguration;
     if (ws_bytes < pl.bytes) return cudaErrorInvalidValue;
     uint8_t *base = static_cast<uint8_t *>(ws);
-    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<int64_t *>(base), pl.slots, pl.b.wide, 1, 32, 1};
+    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<int64_t *>(base), pl.slots, pl.b.wide, 1, 1};
     float *part_ml = reinterpret_cast<float *>(base + pl.off_ml), *part_o = reinterpret_cast<float *>(base + pl.off_o);
     cudaError_t e = cudaSuccess;
     if (pl.b.wide != INT32_MAX) e = launch_paged_wide(c, pg, pl.b, q, QH, scale, out, base + pl.off_wide, s);
