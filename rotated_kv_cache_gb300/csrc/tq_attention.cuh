@@ -208,13 +208,12 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
     if constexpr (PAGED) {
         if (warp == 0) paged_walk_start(p.pg, walk, A::ST, NH, p.H, p.G, lane);
         __syncthreads();
-        if (walk.x >= walk.end) return;
+        if (walk.seg[0].count <= 0) return;
     }
     bool ok = true;
-    int slot = 0;
-    uint32_t phase = 0;  // ring slot and barrier parity of the next stage
-    int nseg = 0;        // segments done
-    bool more = false;   // another one follows
+    uint32_t turned = 0;  // paged: bit k set when slot k's barrier has been through an odd number of phases
+    int nseg = 0;         // segments done
+    bool more = false;    // another one follows
     do {
     const PagedSegment &seg = walk.seg[nseg & 1];
     const int split = blockIdx.x, hv = blockIdx.y, b = blockIdx.z;
@@ -281,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
         __syncwarp();
         if (warp == 0)
             for (int s = 0; s < kStages && s < n_stages; ++s)
-                issue_paged(s, (slot + s) % kStages, paged_chunk_page(p.pg, seg, seg.first + s, lane));
+                issue_paged(s, s, paged_chunk_page(p.pg, seg, seg.first + s, lane));
     }
     if (!PAGED || nseg == 0) __syncthreads();
 
@@ -427,14 +426,12 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
     // PAGED, several new tokens: rows from here on are hidden from some column
     const int first_hidden = PAGED && seg.n > 1 ? column_rows(0) : INT32_MAX;
     int next_page = PAGED ? paged_chunk_page(p.pg, seg, seg.first + kStages, lane) : 0;  // of the next refill
-    if constexpr (!PAGED) {
-        ok = true;
-        slot = 0;
-        phase = 0;
-    }
+    if constexpr (!PAGED) ok = true;
+    int slot = 0;
+    uint32_t phase = 0;  // ring slot and barrier parity of stage s, from the segment's start
     int s = 0;
     for (; s < n_stages; ++s) {
-        if (!mbar_wait_bounded(full0 + 8 * slot, phase, p.err)) {
+        if (!mbar_wait_bounded(full0 + 8 * slot, PAGED ? phase ^ (turned >> slot & 1u) : phase, p.err)) {
             ok = false;
             break;
         }
@@ -766,9 +763,11 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
                     slot = 0;
                     phase ^= 1u;
                 }
-                mbar_wait_bounded(full0 + 8 * slot, phase, p.err);
+                mbar_wait_bounded(full0 + 8 * slot, phase ^ (turned >> slot & 1u), p.err);
             }
         ok = __syncthreads_and(ok);
+#pragma unroll
+        for (int k = 0; k < kStages; ++k) turned ^= ((uint32_t)(n_stages - k + kStages - 1) / kStages & 1u) << k;
     } else {
         __syncthreads();  // every warp is done with the ring before it holds the merge
     }
@@ -834,11 +833,11 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
         }
     }
     if constexpr (PAGED) {
-        if (threadIdx.x == 0) paged_walk_next(p.pg, walk, seg, walk.seg[(nseg + 1) & 1], A::ST, NH, p.H, p.G);
+        if (threadIdx.x == 0) paged_walk_next(p.pg, walk, walk.seg[(nseg + 1) & 1], A::ST, NH, p.H, p.G);
         ++nseg;
         fence_proxy_async_smem();  // the next segment's copies land where the merge was read and written
         __syncthreads();
-        more = walk.x < walk.end;
+        more = walk.seg[nseg & 1].count > 0;
     }
     } while (PAGED && more);
 }

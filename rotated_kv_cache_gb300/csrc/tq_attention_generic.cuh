@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     if constexpr (PAGED) {
         if (warp == 0) paged_walk_start(p.pg, walk, gT, CB, p.H, p.G, lane);
         __syncthreads();
-        if (walk.x >= walk.end) return;
+        if (walk.seg[0].count <= 0) return;
     }
     bool ok = true;
     int it0 = 0;        // stages this CTA has been through before this segment (ring slots and parities run on)
@@ -853,12 +853,12 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
         }
     }
     if constexpr (PAGED) {
-        if (threadIdx.x == 0) paged_walk_next(p.pg, walk, seg, walk.seg[(nseg + 1) & 1], gT, CB, p.H, p.G);
+        if (threadIdx.x == 0) paged_walk_next(p.pg, walk, walk.seg[(nseg + 1) & 1], gT, CB, p.H, p.G);
         it0 += n_stages;
         ++nseg;
         fence_proxy_async_smem();  // the next segment's copies land where the merge was read and written
         __syncthreads();
-        more = walk.x < walk.end;
+        more = walk.seg[nseg & 1].count > 0;
     }
     } while (PAGED && more);
 }

@@ -78,27 +78,30 @@ __device__ __forceinline__ int64_t paged_row(const PagedView &v, int64_t t, int 
 }
 
 // ------------------------------------------------------------------ split attention over a paged batch
-// The work of a batch is one line of stages (ST rows each): sequence after
-// sequence, in a sequence its units (kv-head, block of CB columns) one after
-// another, in a unit its stages in row order.  CTA c takes the c-th run of
-// `per` stages, whatever lengths the sequences have, so all CTAs finish
-// together; a run's part of one unit is a segment, and a unit's segments are
-// merged by the combine.  Segment (c, unit u) writes partial slot c + u:
-// along the line c or u grows by one at every new segment, so slots are
-// distinct, and at most CTAs + units of them are used.
+// The work of a batch is one line: sequence after sequence, in a sequence its
+// units (kv-head, block of CB columns) one after another, in a unit its start
+// (kSegStart: what a segment costs besides its stages, in stages) and its
+// stages of ST rows in row order.  CTA c takes the c-th run of `per` places,
+// whatever lengths the sequences have, so all CTAs finish together; a run's
+// stages of one unit are a segment (a run that ends within a start leaves the
+// unit to the next CTA), and a unit's segments are merged by the combine.
+// Segment (c, unit u) writes partial slot c + u: along the line c or u grows by
+// one at every new segment, so slots are distinct, and at most CTAs + units of
+// them are used.
 //
-// A CTA's first warp works the line out from the lengths (two passes of 32
-// sequences at a time); the first CTA leaves the prefix sums for the combine.
+// A CTA's first warp works the line out from the lengths (32 sequences at a
+// time); the first CTA leaves the prefix sums for the combine.
+constexpr int kSegStart = 2;
+
 // Stages and units of sequence s (none where it has no rows, no new tokens, or too many).
-__device__ __forceinline__ void paged_shape(const PagedSplit &ps, int s, int ST, int CB, int H, int G, int64_t &stages,
-                                            int64_t &blocks)
+__device__ __forceinline__ void paged_shape(const PagedSplit &ps, int s, int ST, int CB, int H, int G, int &stages, int &units)
 {
-    stages = blocks = 0;
+    stages = units = 0;
     if (s >= ps.v.seqs) return;
     const int64_t n = paged_new(ps.v, s), len = paged_len(ps.v, s);
     if (n == 0 || n > ps.wide || len == 0) return;
-    stages = (len + ST - 1) / ST;
-    blocks = (n * G + CB - 1) / CB;
+    stages = (int)((uint32_t)(len + ST - 1) / (uint32_t)ST);
+    units = (int)((uint32_t)(n * G + CB - 1) / (uint32_t)CB) * H;
 }
 
 __device__ __forceinline__ int64_t warp_inclusive_sum(int64_t x, int lane)
@@ -111,101 +114,113 @@ __device__ __forceinline__ int64_t warp_inclusive_sum(int64_t x, int lane)
     return x;
 }
 
+// a / b for a, b >= 0: in 32 bits where they fit
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b)
+{
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // A segment, as the CTA's threads read it from shared memory.
 struct PagedSegment {
     int64_t s0, slot;              // first ragged row of the sequence; partial slot
     int s, n, len;                 // sequence, its new tokens, its rows
-    int h, hb, first, count;       // kv-head, column block, first stage, stages
+    int h, hb, first, count;       // kv-head, column block, first stage, stages (none: the run is done)
 };
 
 // The CTA's place on the line and its current segment (two, so that the next
 // one can be written while the current one is still read).
 struct PagedWalk {
-    int64_t x, end;         // stages of the line still to do
-    int64_t sp, up;         // stages, units before sequence s
-    int64_t stages, blocks; // of sequence s
-    int s;
+    int64_t end;          // of the CTA's run
+    int64_t at;           // line position of the current unit's first stage
+    int64_t up;           // units before sequence s
+    int s, u, stages, units;  // sequence, unit in it; its stages per unit and its units
     PagedSegment seg[2];
 };
 
-// The segment at w.x, by one thread.
-__device__ __forceinline__ void paged_segment(const PagedSplit &ps, PagedWalk &w, PagedSegment &g)
+// The segment of the current unit from `first` on, by one thread.
+__device__ __forceinline__ void paged_segment(const PagedSplit &ps, const PagedWalk &w, PagedSegment &g, int first, int H)
 {
-    const int64_t y = w.x - w.sp, u = y / w.stages;
-    g.first = (int)(y - u * w.stages);
-    g.count = (int)imin64(w.stages - g.first, w.end - w.x);
-    g.h = (int)(u / w.blocks);
-    g.hb = (int)(u - g.h * w.blocks);
-    g.slot = blockIdx.x + w.up + u;
+    g.first = first;
+    g.count = (int)imin64(w.stages, w.end - w.at) - first;
+    const int blocks = w.units / H;
+    g.h = w.u / blocks;
+    g.hb = w.u - g.h * blocks;
+    g.slot = blockIdx.x + w.up + w.u;
     g.s = w.s;
     g.s0 = paged_start(ps.v, w.s);
     g.n = (int)paged_new(ps.v, w.s);
     g.len = (int)paged_len(ps.v, w.s);
 }
 
-// The CTA's first segment, by the first warp (whole): into w.seg[0], w.x < w.end
-// saying that there is one.  The first CTA leaves the prefix sums for the
-// combine.  The caller synchronises the CTA before w is read.
+// The CTA's first segment into w.seg[0], by the first warp (whole).  The first
+// CTA leaves the prefix sums for the combine.  The caller synchronises the CTA
+// before w is read.
 __device__ __forceinline__ void paged_walk_start(const PagedSplit &ps, PagedWalk &w, int ST, int CB, int H, int G, int lane)
 {
-    int64_t total = 0;
-    for (int b = 0; b < ps.v.seqs; b += 32) {
-        int64_t st, bl;
-        paged_shape(ps, b + lane, ST, CB, H, G, st, bl);
-        total += st * bl * H;
+    const int S = ps.v.seqs;
+    int st, un;
+    paged_shape(ps, lane, ST, CB, H, G, st, un);
+    int64_t total = (int64_t)(st + kSegStart) * un;
+    for (int b = 32; b < S; b += 32) {
+        int st1, un1;
+        paged_shape(ps, b + lane, ST, CB, H, G, st1, un1);
+        total += (int64_t)(st1 + kSegStart) * un1;
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < 1) per = 1;
+    int64_t per = div_small(total + gridDim.x - 1, gridDim.x);
+    if (per < kSegStart + 1) per = kSegStart + 1;
     const int64_t x = blockIdx.x * per, end = imin64(total, x + per);
     const bool writer = blockIdx.x == 0;
     if (lane == 0) {
-        w.x = x;
         w.end = end;
+        w.seg[0].count = 0;
     }
+    __syncwarp();
     int64_t sbase = 0, ubase = 0;
     bool found = x >= end;
-    for (int b = 0; b < ps.v.seqs && (writer || !found); b += 32) {
-        int64_t st, bl;
-        paged_shape(ps, b + lane, ST, CB, H, G, st, bl);
-        const int64_t c = st * bl * H, u = bl * H;
-        const int64_t ws = warp_inclusive_sum(c, lane), us = warp_inclusive_sum(u, lane);
-        const int64_t s_at = sbase + ws - c, u_at = ubase + us - u;
-        if (writer && b + lane < ps.v.seqs) {
+    for (int b = 0; b < S && (writer || !found); b += 32) {
+        if (b > 0) paged_shape(ps, b + lane, ST, CB, H, G, st, un);
+        const int64_t c = (int64_t)(st + kSegStart) * un;
+        const int64_t ws = warp_inclusive_sum(c, lane), us = warp_inclusive_sum(un, lane);
+        const int64_t s_at = sbase + ws - c, u_at = ubase + us - un;
+        if (writer && b + lane < S) {
             ps.plan[b + lane] = s_at;
-            ps.plan[ps.v.seqs + 1 + b + lane] = u_at;
+            ps.plan[S + 1 + b + lane] = u_at;
         }
-        const bool mine = c > 0 && s_at <= x && x < s_at + c;
+        const bool mine = !found && c > 0 && s_at <= x && x < s_at + c;
         if (mine) {
+            const int64_t u = div_small(x - s_at, st + kSegStart);
             w.s = b + lane;
-            w.sp = s_at;
             w.up = u_at;
             w.stages = st;
-            w.blocks = bl;
-            paged_segment(ps, w, w.seg[0]);
+            w.units = un;
+            w.u = (int)u;
+            w.at = s_at + u * (st + kSegStart) + kSegStart;
+            paged_segment(ps, w, w.seg[0], x > w.at ? (int)(x - w.at) : 0, H);
         }
         found |= __any_sync(0xffffffffu, mine);
         sbase += __shfl_sync(0xffffffffu, ws, 31);
         ubase += __shfl_sync(0xffffffffu, us, 31);
     }
-    if (writer && lane == 0) ps.plan[2 * ps.v.seqs + 2] = per;
+    if (writer && lane == 0) ps.plan[2 * S + 2] = per;
 }
 
-// On to the segment after `cur`, by one thread, into `nxt`; w.x < w.end says
-// that there is one.
-__device__ __forceinline__ void paged_walk_next(const PagedSplit &ps, PagedWalk &w, const PagedSegment &cur,
-                                                PagedSegment &nxt, int ST, int CB, int H, int G)
+// On to the next unit's segment, by one thread, into `nxt` (count <= 0: the run is done).
+__device__ __forceinline__ void paged_walk_next(const PagedSplit &ps, PagedWalk &w, PagedSegment &nxt, int ST, int CB, int H, int G)
 {
-    w.x += cur.count;
-    if (w.x >= w.end) return;
-    while (w.x >= w.sp + w.stages * w.blocks * H) {  // to the next sequence with work: x < end says that there is one
-        w.sp += w.stages * w.blocks * H;
-        w.up += w.blocks * H;
-        ++w.s;
-        paged_shape(ps, w.s, ST, CB, H, G, w.stages, w.blocks);
+    nxt.count = 0;
+    w.at += w.stages + kSegStart;  // of the next unit of the same length
+    if (w.at >= w.end) return;
+    if (++w.u == w.units) {  // the next sequence with work (w.at < w.end says that there is one)
+        w.up += w.units;
+        w.u = 0;
+        do {
+            ++w.s;
+            paged_shape(ps, w.s, ST, CB, H, G, w.stages, w.units);
+        } while (w.units == 0);
     }
-    paged_segment(ps, w, nxt);
+    paged_segment(ps, w, nxt, 0, H);
 }
 
 // A stage is copied in chunks of ps.ru = gcd(stage rows, page rows) rows, so that

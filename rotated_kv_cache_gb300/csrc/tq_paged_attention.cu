@@ -100,12 +100,13 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
     int64_t first = 0;            // slots of the unit's segments: first .. first + segs - 1
     int segs = 0, col = 0;
     if (live && len > 0) {
-        const int64_t stages = (len + p.ST - 1) / p.ST, blocks = (n * p.G + p.CB - 1) / p.CB;
+        const int64_t stages = (uint32_t)(len + p.ST - 1) / (uint32_t)p.ST, blocks = (uint32_t)(n * p.G + p.CB - 1) / (uint32_t)p.CB;
         const int64_t per = p.pg.plan[2 * p.pg.v.seqs + 2], up = p.pg.plan[p.pg.v.seqs + 1 + s];
         const int h = qh / p.G;
         col = (int)((t - s0) * p.G + (qh - h * p.G));
-        const int64_t u = h * blocks + col / p.CB, a = p.pg.plan[s] + u * stages;
-        const int64_t c0 = a / per, c1 = (a + stages - 1) / per;
+        // its first stage's place on the line, and the CTAs of its first and last stage
+        const int64_t u = h * blocks + col / p.CB, a = p.pg.plan[s] + u * (stages + kSegStart) + kSegStart;
+        const int64_t c0 = div_small(a, per), c1 = div_small(a + stages - 1, per);
         first = c0 + up + u;
         segs = (int)(c1 - c0 + 1);
         col %= p.CB;
