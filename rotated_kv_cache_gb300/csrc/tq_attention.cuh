@@ -178,16 +178,20 @@ __device__ __forceinline__ uint32_t shr_fma(uint32_t x)
 }
 
 // ---------------------------------------------------------------- the split kernel
-// PAGED: the CTA runs the segments of its share of a paged batch one after
+// MODE: 0 contiguous; 1 paged, one new token a sequence at most; 2 paged, any
+// (masks for the rows that some column does not see: 43 instructions per warp and
+// stage, 4 % of the time of a decode step).
+// Paged: the CTA runs the segments of its share of a paged batch one after
 // another (tq_paged.cuh) instead of the grid's (split, column blocks,
 // sequence).  A column is then one (new token, q-head) of the kv-head, a block
 // NBC * kG of them; a stage arrives chunk by chunk, each lane of the refilling
 // warp copying one (a chunk lies within a page).
-template <int KB, int D, int VB, int NBC, bool PAGED = false>
+template <int KB, int D, int VB, int NBC, int MODE = 0>
 __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
     attn_split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ AttnParams p)
 {
     using A = AGeo<KB, D, VB, NBC>;
+    constexpr bool PAGED = MODE != 0, CAUSAL = MODE == 2;
     constexpr int NG = A::NG;
     constexpr int NH = NBC * kG;  // MMA columns of the CTA
     extern __shared__ uint8_t smem_raw[];
@@ -230,8 +234,9 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
     const int split_rows = PAGED ? imin_int(column_rows(block_cols() - 1), seg.count * A::ST) : (int)(t_end - t_begin);
     const int n_stages = split_rows > 0 && (!PAGED || ok) ? (split_rows + A::ST - 1) / A::ST : 0;
 
-    // paged: every lane of the warp calls, with the page of its chunk
-    auto issue_paged = [&](int s, int at_slot, int page) {
+    // paged: every lane of the warp calls; the page look-up is in the shadow of the stage that the other slot holds
+    auto issue_paged = [&](int s, int at_slot) {
+        const int page = paged_chunk_page(p.pg, seg, seg.first + s, lane);
         const int ru = p.pg.ru;
         const int live = (imin_int(A::ST, split_rows - s * A::ST) + ru - 1) / ru;  // chunks with rows to read
         const uint32_t st = smem_addr(stages + at_slot * A::STAGE), bar = full0 + 8 * at_slot;
@@ -239,14 +244,14 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
         __syncwarp();
         if (lane < live) {
             const int at = lane * ru;
-            const int64_t row = paged_chunk_plane_row(p.pg, seg, p.H, page, seg.first + s, lane);
+            const uint32_t row = (uint32_t)paged_chunk_plane_row(p.pg, seg, p.H, page, seg.first + s, lane);
 #pragma unroll
             for (int j = 0; j < A::NBOX; ++j)
                 tma_load_2d(st + A::OFF_K + j * (A::ST * A::SW) + at * A::SW, &kmap, j * A::SW, (int)row, bar);
-            bulk_g2s(st + A::OFF_KS + at * (NG * 2), p.k_scale + row * NG, ru * NG * 2, bar);
-            bulk_g2s(st + A::OFF_KZ + at * (NG * 2), p.k_zero + row * NG, ru * NG * 2, bar);
-            bulk_g2s(st + A::OFF_VS + at * (NG * 2), p.v_scale + row * NG, ru * NG * 2, bar);
-            bulk_g2s(st + A::OFF_V + at * A::RBV, p.v_codes + row * A::RBV, ru * A::RBV, bar);
+            bulk_g2s(st + A::OFF_KS + at * (NG * 2), p.k_scale + (size_t)row * NG, ru * NG * 2, bar);
+            bulk_g2s(st + A::OFF_KZ + at * (NG * 2), p.k_zero + (size_t)row * NG, ru * NG * 2, bar);
+            bulk_g2s(st + A::OFF_VS + at * (NG * 2), p.v_scale + (size_t)row * NG, ru * NG * 2, bar);
+            bulk_g2s(st + A::OFF_V + at * A::RBV, p.v_codes + (size_t)row * A::RBV, ru * A::RBV, bar);
         }
     };
 
@@ -280,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
         __syncwarp();
         if (warp == 0)
             for (int s = 0; s < kStages && s < n_stages; ++s)
-                issue_paged(s, s, paged_chunk_page(p.pg, seg, seg.first + s, lane));
+                issue_paged(s, s);
     }
     if (!PAGED || nseg == 0) __syncthreads();
 
@@ -424,8 +429,7 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
     for (int q = 0; q < 4; ++q) voff[q] = A::OFF_V + vr[q] * A::RBV + 4 * v_word;
     const uint32_t ring0 = smem_addr(stages);
     // PAGED, several new tokens: rows from here on are hidden from some column
-    const int first_hidden = PAGED && seg.n > 1 ? column_rows(0) : INT32_MAX;
-    int next_page = PAGED ? paged_chunk_page(p.pg, seg, seg.first + kStages, lane) : 0;  // of the next refill
+    const int first_hidden = CAUSAL && seg.n > 1 ? column_rows(0) : INT32_MAX;
     if constexpr (!PAGED) ok = true;
     int slot = 0;
     uint32_t phase = 0;  // ring slot and barrier parity of stage s, from the segment's start
@@ -534,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
                         if (tile_r + g + 8 >= split_rows) S[nb][t2][1][0] = S[nb][t2][1][1] = -INFINITY;
                     }
                 }
-                if constexpr (PAGED) {
+                if constexpr (CAUSAL) {
                     if (tile_r + 16 > first_hidden) {
 #pragma unroll
                         for (int nb = 0; nb < NBC; ++nb)
@@ -633,8 +637,8 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
             // paged: a hidden row's rms may be anything; the weights of the lane's column (g of
             // each block) keep to the rows it sees
             uint32_t seen[NBC][2];
-            const bool masked = PAGED && tile_r + 16 > first_hidden;
-            if constexpr (PAGED) {
+            const bool masked = CAUSAL && tile_r + 16 > first_hidden;
+            if constexpr (CAUSAL) {
                 if (masked) {
 #pragma unroll
                     for (int nb = 0; nb < NBC; ++nb) {
@@ -655,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
                 for (int nb = 0; nb < NBC; ++nb) {
                     b0[nb] = hmul2(pt0[nb], sp0);
                     b1[nb] = hmul2(pt1[nb], sp1);
-                    if constexpr (PAGED) {
+                    if constexpr (CAUSAL) {
                         if (masked) {
                             b0[nb] &= seen[nb][0];
                             b1[nb] &= seen[nb][1];
@@ -741,8 +745,7 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
                 last = atomicAdd(&done[slot], 1u) == kCW - 1;
                 if (last) done[slot] = 0;
             }
-            if (__shfl_sync(0xffffffffu, last, 0) && s + kStages < n_stages) issue_paged(s + kStages, slot, next_page);
-            next_page = paged_chunk_page(p.pg, seg, seg.first + s + kStages + 1, lane);
+            if (__shfl_sync(0xffffffffu, last, 0) && s + kStages < n_stages) issue_paged(s + kStages, slot);
         } else if (lane == 0) {
             __threadfence_block();
             if (atomicAdd(&done[slot], 1u) == kCW - 1) {
@@ -843,15 +846,15 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
 }
 
 // ---------------------------------------------------------------- host side
-template <int KB, int D, int VB, int NBC, bool PAGED = false>
+template <int KB, int D, int VB, int NBC, int MODE = 0>
 int ctas_per_sm_for()
 {
     static int cached = 0;  // same on every GB300; only a successful query is kept
     if (!cached) {
         int n = 0;
-        if (cudaFuncSetAttribute(attn_split_kernel<KB, D, VB, NBC, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(attn_split_kernel<KB, D, VB, NBC, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  AGeo<KB, D, VB, NBC>::SMEM) == cudaSuccess &&
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_split_kernel<KB, D, VB, NBC, PAGED>, kThreads,
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_split_kernel<KB, D, VB, NBC, MODE>, kThreads,
                                                           AGeo<KB, D, VB, NBC>::SMEM) == cudaSuccess &&
             n > 0)
             cached = n;

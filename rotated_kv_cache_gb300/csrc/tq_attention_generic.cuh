@@ -314,8 +314,9 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     const int n_stages = t_end > t_begin && ok ? (int)((t_end - t_begin + gT - 1) / gT) : 0;
     const int NG = D / 32;
 
-    // paged: every lane of the warp calls, with the page of its chunk
-    auto issue_paged = [&](int s, int page) {
+    // paged: every lane of the warp calls; the page look-up is in the shadow of the stage that the other slot holds
+    auto issue_paged = [&](int s) {
+        const int page = paged_chunk_page(p.pg, seg, seg.first + s, lane);
         const int slot = (it0 + s) % p.stages, ru = p.pg.ru;
         const int live = (int)((imin64(gT, t_end - (t_begin + (int64_t)s * gT)) + ru - 1) / ru);  // chunks with rows to read
         const uint32_t kst = smem_addr(stages + slot * p.key_bytes), bar = full0 + 8 * slot;
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     if constexpr (PAGED) {
         __syncwarp();
         if (warp == 0)
-            for (int s = 0; s < p.stages && s < n_stages; ++s) issue_paged(s, paged_chunk_page(p.pg, seg, seg.first + s, lane));
+            for (int s = 0; s < p.stages && s < n_stages; ++s) issue_paged(s);
     }
     if constexpr (VLUT == 0)
         for (int i = threadIdx.x; i < (1 << p.vb); i += blockDim.x) lut[i] = p.cen[i];
@@ -488,7 +489,6 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     constexpr int QF_NB = gN * A::QCOL;  // bytes of q fragments per block of 8 columns
     const uint32_t qf_lane = smem_addr(qf) + g * A::QCOL + c * 8, lut_a = smem_addr(lut);
 
-    int next_page = PAGED ? paged_chunk_page(p.pg, seg, seg.first + p.stages, lane) : 0;  // of the next refill
     int s = 0;
     for (; s < n_stages; ++s) {
         const int slot = (it0 + s) % p.stages;
@@ -773,8 +773,7 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
                 last = atomicAdd(&done[slot], 1u) == A::W - 1;
                 if (last) done[slot] = 0;
             }
-            if (__shfl_sync(0xffffffffu, last, 0) && s + p.stages < n_stages) issue_paged(s + p.stages, next_page);
-            next_page = paged_chunk_page(p.pg, seg, seg.first + s + p.stages + 1, lane);
+            if (__shfl_sync(0xffffffffu, last, 0) && s + p.stages < n_stages) issue_paged(s + p.stages);
         } else if (lane == 0) {
             __threadfence_block();
             if (atomicAdd(&done[slot], 1u) == A::W - 1) {

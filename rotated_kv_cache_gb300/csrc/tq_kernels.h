@@ -71,17 +71,22 @@ struct PagedView {
     uint32_t *err;
 };
 
+// The partials of a unit (sequence, kv-head, column block): slots first ..
+// first + count - 1, written by the CTA of its first segment.
+struct PagedUnit {
+    int first, count;
+};
+
 // A paged attention call, for the split kernels (tq_paged.cuh).
 struct PagedSplit {
     PagedView v;
     int64_t q_token, q_head;  // element strides of q
-    int64_t *plan;            // [seqs + 1] stages before a sequence, [seqs + 1] units before it, per
+    PagedUnit *units;         // [seqs][H][blocks]: where a unit's partials are
     int64_t slots;            // partial slots of the workspace
+    int blocks;               // column blocks of a sequence's kv-head, at most
     int64_t wide;             // sequences with more new tokens than this are another kernel's
     int nch, ru;              // chunks per stage, rows per chunk
 };
-
-__host__ __device__ constexpr int64_t paged_plan_words(int64_t seqs) { return 2 * (seqs + 1) + 1; }
 
 __host__ __device__ constexpr int gcd_int(int a, int b) { return b == 0 ? a : gcd_int(b, a % b); }
 

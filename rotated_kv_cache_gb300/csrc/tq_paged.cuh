@@ -90,7 +90,8 @@ __device__ __forceinline__ int64_t paged_row(const PagedView &v, int64_t t, int 
 // them are used.
 //
 // A CTA's first warp works the line out from the lengths (32 sequences at a
-// time); the first CTA leaves the prefix sums for the combine.
+// time); the CTA of a unit's first segment leaves word of its slots for the
+// combine.
 constexpr int kSegStart = 2;
 
 // Stages and units of sequence s (none where it has no rows, no new tokens, or too many).
@@ -123,14 +124,15 @@ __device__ __forceinline__ int64_t div_small(int64_t a, int64_t b)
 // A segment, as the CTA's threads read it from shared memory.
 struct PagedSegment {
     int64_t s0, slot;              // first ragged row of the sequence; partial slot
-    int s, n, len;                 // sequence, its new tokens, its rows
+    const int32_t *pages;          // the sequence's row of the page table
+    int n, len;                    // new tokens, rows
     int h, hb, first, count;       // kv-head, column block, first stage, stages (none: the run is done)
 };
 
 // The CTA's place on the line and its current segment (two, so that the next
 // one can be written while the current one is still read).
 struct PagedWalk {
-    int64_t end;          // of the CTA's run
+    int64_t end, per;     // of the CTA's run; places per CTA
     int64_t at;           // line position of the current unit's first stage
     int64_t up;           // units before sequence s
     int s, u, stages, units;  // sequence, unit in it; its stages per unit and its units
@@ -146,15 +148,17 @@ __device__ __forceinline__ void paged_segment(const PagedSplit &ps, const PagedW
     g.h = w.u / blocks;
     g.hb = w.u - g.h * blocks;
     g.slot = blockIdx.x + w.up + w.u;
-    g.s = w.s;
+    g.pages = ps.v.pages + w.s * ps.v.stride;
+    if (first == 0 && g.count > 0 && g.hb < ps.blocks)
+        ps.units[((int64_t)w.s * H + g.h) * ps.blocks + g.hb] =
+            PagedUnit{(int)g.slot, (int)(div_small(w.at + w.stages - 1, w.per) - blockIdx.x) + 1};
     g.s0 = paged_start(ps.v, w.s);
     g.n = (int)paged_new(ps.v, w.s);
     g.len = (int)paged_len(ps.v, w.s);
 }
 
-// The CTA's first segment into w.seg[0], by the first warp (whole).  The first
-// CTA leaves the prefix sums for the combine.  The caller synchronises the CTA
-// before w is read.
+// The CTA's first segment into w.seg[0], by the first warp (whole).  The caller
+// synchronises the CTA before w is read.
 __device__ __forceinline__ void paged_walk_start(const PagedSplit &ps, PagedWalk &w, int ST, int CB, int H, int G, int lane)
 {
     const int S = ps.v.seqs;
@@ -171,24 +175,20 @@ __device__ __forceinline__ void paged_walk_start(const PagedSplit &ps, PagedWalk
     int64_t per = div_small(total + gridDim.x - 1, gridDim.x);
     if (per < kSegStart + 1) per = kSegStart + 1;
     const int64_t x = blockIdx.x * per, end = imin64(total, x + per);
-    const bool writer = blockIdx.x == 0;
     if (lane == 0) {
         w.end = end;
+        w.per = per;
         w.seg[0].count = 0;
     }
     __syncwarp();
     int64_t sbase = 0, ubase = 0;
     bool found = x >= end;
-    for (int b = 0; b < S && (writer || !found); b += 32) {
+    for (int b = 0; b < S && !found; b += 32) {
         if (b > 0) paged_shape(ps, b + lane, ST, CB, H, G, st, un);
         const int64_t c = (int64_t)(st + kSegStart) * un;
         const int64_t ws = warp_inclusive_sum(c, lane), us = warp_inclusive_sum(un, lane);
         const int64_t s_at = sbase + ws - c, u_at = ubase + us - un;
-        if (writer && b + lane < S) {
-            ps.plan[b + lane] = s_at;
-            ps.plan[S + 1 + b + lane] = u_at;
-        }
-        const bool mine = !found && c > 0 && s_at <= x && x < s_at + c;
+        const bool mine = c > 0 && s_at <= x && x < s_at + c;
         if (mine) {
             const int64_t u = div_small(x - s_at, st + kSegStart);
             w.s = b + lane;
@@ -203,7 +203,6 @@ __device__ __forceinline__ void paged_walk_start(const PagedSplit &ps, PagedWalk
         sbase += __shfl_sync(0xffffffffu, ws, 31);
         ubase += __shfl_sync(0xffffffffu, us, 31);
     }
-    if (writer && lane == 0) ps.plan[2 * S + 2] = per;
 }
 
 // On to the next unit's segment, by one thread, into `nxt` (count <= 0: the run is done).
@@ -232,13 +231,12 @@ __device__ __forceinline__ uint32_t paged_chunk_row(const PagedSplit &ps, int st
     return (uint32_t)((stage * ps.nch + chunk) * ps.ru);
 }
 
-// Page number (unchecked) of the lane's chunk of `stage`, 0 where it has no
-// rows.  Loaded a stage before it is used.
+// Page number (unchecked) of the lane's chunk of `stage`, 0 where it has no rows.
 __device__ __forceinline__ int paged_chunk_page(const PagedSplit &ps, const PagedSegment &g, int stage, int lane)
 {
     const uint32_t row = paged_chunk_row(ps, stage, lane);
     if (lane >= ps.nch || row >= (uint32_t)g.len) return 0;
-    return ps.v.pages[g.s * ps.v.stride + fast_div(row, ps.v.div_page)];
+    return g.pages[fast_div(row, ps.v.div_page)];
 }
 
 // Plane row of that chunk for the segment's kv-head; a bad page number is

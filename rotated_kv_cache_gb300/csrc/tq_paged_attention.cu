@@ -21,13 +21,17 @@ TQ_DECLARE_PAGED_GENERIC(128)
 TQ_DECLARE_PAGED_GENERIC(256)
 TQ_DECLARE_PAGED_GENERIC(512)
 #undef TQ_DECLARE_PAGED_GENERIC
-#define TQ_DECLARE_PAGED_SPLIT(D)                                                                                      \
-    PagedShape paged_split_shape_d##D(const CacheView &c, int64_t cols);                                              \
-    cudaError_t launch_paged_split_d##D(const CacheView &c, const PagedSplit &pg, const PagedShape &sh, const uint16_t *q, \
-                                        int QH, float scale, float *part_o, float *part_ml, cudaStream_t s);
-TQ_DECLARE_PAGED_SPLIT(64)
-TQ_DECLARE_PAGED_SPLIT(128)
-TQ_DECLARE_PAGED_SPLIT(256)
+#define TQ_DECLARE_PAGED_SPLIT(NAME)                                                                                   \
+    PagedShape paged_split_shape_##NAME(const CacheView &c, int64_t cols);                                             \
+    cudaError_t launch_paged_split_##NAME(const CacheView &c, const PagedSplit &pg, const PagedShape &sh,              \
+                                          const uint16_t *q, int QH, float scale, float *part_o, float *part_ml,       \
+                                          cudaStream_t s);
+TQ_DECLARE_PAGED_SPLIT(d64_one)
+TQ_DECLARE_PAGED_SPLIT(d64_any)
+TQ_DECLARE_PAGED_SPLIT(d128_one)
+TQ_DECLARE_PAGED_SPLIT(d128_any)
+TQ_DECLARE_PAGED_SPLIT(d256_one)
+TQ_DECLARE_PAGED_SPLIT(d256_any)
 #undef TQ_DECLARE_PAGED_SPLIT
 
 namespace {
@@ -37,7 +41,7 @@ struct PagedCombineParams {
     const float *part_o, *part_ml;
     uint16_t *out;  // bf16 [total][QH][D]
     PagedSplit pg;
-    int H, QH, G, ST, CB;
+    int H, QH, G, CB;
     int64_t rows;     // rows gone through: total * QH, or seqs * per_seq * QH
     int per_seq;      // > 0: that many places for tokens per sequence; 0: token by token
     float inv_sqrt_d;
@@ -100,15 +104,14 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
     int64_t first = 0;            // slots of the unit's segments: first .. first + segs - 1
     int segs = 0, col = 0;
     if (live && len > 0) {
-        const int64_t stages = (uint32_t)(len + p.ST - 1) / (uint32_t)p.ST, blocks = (uint32_t)(n * p.G + p.CB - 1) / (uint32_t)p.CB;
-        const int64_t per = p.pg.plan[2 * p.pg.v.seqs + 2], up = p.pg.plan[p.pg.v.seqs + 1 + s];
         const int h = qh / p.G;
         col = (int)((t - s0) * p.G + (qh - h * p.G));
-        // its first stage's place on the line, and the CTAs of its first and last stage
-        const int64_t u = h * blocks + col / p.CB, a = p.pg.plan[s] + u * (stages + kSegStart) + kSegStart;
-        const int64_t c0 = div_small(a, per), c1 = div_small(a + stages - 1, per);
-        first = c0 + up + u;
-        segs = (int)(c1 - c0 + 1);
+        const int hb = col / p.CB;
+        if (hb < p.pg.blocks) {
+            const PagedUnit u = p.pg.units[((int64_t)s * p.H + h) * p.pg.blocks + hb];
+            first = u.first;
+            segs = u.count;
+        }
         col %= p.CB;
         if (first + segs > p.pg.slots) segs = 0;  // starts out of order
     }
@@ -203,7 +206,8 @@ struct PagedPlan {
     int64_t cols;   // most columns of a kv-head that the split kernels see
     PagedBounds b;
     int64_t slots;
-    size_t off_ml, off_o, off_wide, bytes;  // workspace: plan words, partial (max, sum), partial outputs, the wide kernels'
+    int blocks;
+    size_t off_ml, off_o, off_wide, bytes;  // workspace: units, partial (max, sum), partial outputs, the wide kernels'
 };
 
 // A sequence with at least this many columns (new tokens x q-heads of a
@@ -220,16 +224,21 @@ bool paged_plan(const CacheView &c, const PagedBounds &bounds, int QH, PagedPlan
     // the specialised kernel where it has the widths (its tensor copies count rows in 32 bits)
     pl.special = attention_supported(c.d, c.kb, c.vb, (int)G) && (int64_t)c.B * c.H * c.cap < (int64_t(1) << 31);
     if (pl.special)
-        pl.split = c.d == 64    ? paged_split_shape_d64(c, pl.cols)
-                   : c.d == 128 ? paged_split_shape_d128(c, pl.cols)
-                                : paged_split_shape_d256(c, pl.cols);
+        pl.split = pl.b.max_new <= 1
+                       ? (c.d == 64    ? paged_split_shape_d64_one(c, pl.cols)
+                          : c.d == 128 ? paged_split_shape_d128_one(c, pl.cols)
+                                       : paged_split_shape_d256_one(c, pl.cols))
+                       : (c.d == 64    ? paged_split_shape_d64_any(c, pl.cols)
+                          : c.d == 128 ? paged_split_shape_d128_any(c, pl.cols)
+                                       : paged_split_shape_d256_any(c, pl.cols));
     else if (!generic_shape(c, pl.cols, pl.split))
         return false;
     // a sequence of n new tokens has ceil(n G / block) blocks: at most this many units in all
     const int64_t units = c.H * (pl.b.total * G / pl.split.block + pl.b.seqs);
     pl.slots = pl.split.ctas + units;
     auto r256 = [](size_t x) { return (x + 255) / 256 * 256; };
-    pl.off_ml = r256((size_t)paged_plan_words(pl.b.seqs) * 8);
+    pl.blocks = (int)((pl.cols + pl.split.block - 1) / pl.split.block);
+    pl.off_ml = r256((size_t)pl.b.seqs * c.H * pl.blocks * sizeof(PagedUnit));
     pl.off_o = pl.off_ml + r256((size_t)pl.slots * pl.split.block * 8);
     pl.off_wide = pl.off_o + r256((size_t)pl.slots * pl.split.block * c.d * 4);
     pl.bytes = pl.off_wide + (wide ? paged_wide_workspace_bytes(c, pl.b, QH) : 0);
@@ -252,16 +261,18 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
     if (!paged_plan(c, b, QH, pl)) return cudaErrorInvalidConfiguration;
     if (ws_bytes < pl.bytes) return cudaErrorInvalidValue;
     uint8_t *base = static_cast<uint8_t *>(ws);
-    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<int64_t *>(base), pl.slots, pl.b.wide, 1, 1};
+    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<PagedUnit *>(base), pl.slots, pl.blocks, pl.b.wide, 1, 1};
     float *part_ml = reinterpret_cast<float *>(base + pl.off_ml), *part_o = reinterpret_cast<float *>(base + pl.off_o);
     cudaError_t e = cudaSuccess;
     if (pl.b.wide != INT32_MAX) e = launch_paged_wide(c, pg, pl.b, q, QH, scale, out, base + pl.off_wide, s);
     if (e != cudaSuccess) return e;
     const int64_t cols = pl.cols;
-    if (pl.special)
-        e = c.d == 64    ? launch_paged_split_d64(c, pg, pl.split, q, QH, scale, part_o, part_ml, s)
-            : c.d == 128 ? launch_paged_split_d128(c, pg, pl.split, q, QH, scale, part_o, part_ml, s)
-                         : launch_paged_split_d256(c, pg, pl.split, q, QH, scale, part_o, part_ml, s);
+    if (pl.special) {
+        const auto launch = pl.b.max_new <= 1
+                                ? (c.d == 64 ? launch_paged_split_d64_one : c.d == 128 ? launch_paged_split_d128_one : launch_paged_split_d256_one)
+                                : (c.d == 64 ? launch_paged_split_d64_any : c.d == 128 ? launch_paged_split_d128_any : launch_paged_split_d256_any);
+        e = launch(c, pg, pl.split, q, QH, scale, part_o, part_ml, s);
+    }
     else switch (c.d) {
     case 64: e = launch_paged_generic_d64(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
     case 128: e = launch_paged_generic_d128(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
@@ -274,7 +285,7 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
     // search for a token's sequence; a long chunk: none of its tokens)
     const int64_t per_seq = pl.b.max_new < pl.b.wide ? pl.b.max_new : (pl.b.wide > 0 ? pl.b.wide : 1);
     const bool by_seq = v.seqs * per_seq <= v.total;
-    PagedCombineParams cp{part_o, part_ml, out, pg, c.H, QH, QH / c.H, pl.split.stage, pl.split.block,
+    PagedCombineParams cp{part_o, part_ml, out, pg, c.H, QH, QH / c.H, pl.split.block,
                           (by_seq ? v.seqs * per_seq : v.total) * QH, by_seq ? (int)per_seq : 0, inv_sqrt_head_dim(c.d),
                           c.signs};
     switch (c.d) {

@@ -26,16 +26,16 @@ auto paged_split_widths(const CacheView &c, F &&f)
                        : f(integral_constant<int, 4>{}, integral_constant<int, 3>{});
 }
 
-template <int D, int NBC>
+template <int D, int NBC, int MODE>
 PagedShape paged_split_shape_n(const CacheView &c)
 {
     return paged_split_widths<D, NBC>(c, [](auto kb, auto vb) {
         return PagedShape{AGeo<kb.value, D, vb.value, NBC>::ST, kG * NBC,
-                          ctas_per_sm_for<kb.value, D, vb.value, NBC, true>() * num_sms()};
+                          ctas_per_sm_for<kb.value, D, vb.value, NBC, MODE>() * num_sms()};
     });
 }
 
-template <int D, int NBC>
+template <int D, int NBC, int MODE>
 cudaError_t paged_split_run(const CacheView &c, const PagedSplit &pg, const PagedShape &sh, const uint16_t *q, int QH,
                             float scale, float *part_o, float *part_ml, cudaStream_t s)
 {
@@ -49,7 +49,7 @@ cudaError_t paged_split_run(const CacheView &c, const PagedSplit &pg, const Page
         set_paged_chunks(p.pg, A::ST, (int)c.cap);
         CUtensorMap map;
         if (!split_key_map<A>(c, p.pg.ru, &map)) return cudaErrorInvalidValue;
-        return launch_dependent(attn_split_kernel<kb.value, D, vb.value, NBC, true>, dim3((unsigned)sh.ctas), dim3(kThreads),
+        return launch_dependent(attn_split_kernel<kb.value, D, vb.value, NBC, MODE>, dim3((unsigned)sh.ctas), dim3(kThreads),
                                 (size_t)A::SMEM, s, map, p);
     });
 }
@@ -57,20 +57,21 @@ cudaError_t paged_split_run(const CacheView &c, const PagedSplit &pg, const Page
 }  // namespace
 }  // namespace tq
 
-// The entry points of one head_dim's translation unit.
-#define TQ_PAGED_SPLIT_ENTRIES(D)                                                                                      \
+// The entry points of one head_dim's translation unit for MODE 1 or 2 (NAME d<head_dim>_one / _any).
+#define TQ_PAGED_SPLIT_ENTRIES(D, MODE, NAME)                                                                          \
     namespace tq {                                                                                                     \
-    PagedShape paged_split_shape_d##D(const CacheView &c, int64_t cols)                                                \
+    PagedShape paged_split_shape_##NAME(const CacheView &c, int64_t cols)                                              \
     {                                                                                                                  \
         if constexpr (D <= 128)                                                                                        \
-            if (paged_split_nbc<D>(cols) == 2) return paged_split_shape_n<D, 2>(c);                                    \
-        return paged_split_shape_n<D, 1>(c);                                                                           \
+            if (paged_split_nbc<D>(cols) == 2) return paged_split_shape_n<D, 2, MODE>(c);                              \
+        return paged_split_shape_n<D, 1, MODE>(c);                                                                     \
     }                                                                                                                  \
-    cudaError_t launch_paged_split_d##D(const CacheView &c, const PagedSplit &pg, const PagedShape &sh, const uint16_t *q, \
-                                        int QH, float scale, float *part_o, float *part_ml, cudaStream_t s)            \
+    cudaError_t launch_paged_split_##NAME(const CacheView &c, const PagedSplit &pg, const PagedShape &sh,              \
+                                          const uint16_t *q, int QH, float scale, float *part_o, float *part_ml,       \
+                                          cudaStream_t s)                                                              \
     {                                                                                                                  \
         if constexpr (D <= 128)                                                                                        \
-            if (sh.block == 2 * kG) return paged_split_run<D, 2>(c, pg, sh, q, QH, scale, part_o, part_ml, s);         \
-        return paged_split_run<D, 1>(c, pg, sh, q, QH, scale, part_o, part_ml, s);                                     \
+            if (sh.block == 2 * kG) return paged_split_run<D, 2, MODE>(c, pg, sh, q, QH, scale, part_o, part_ml, s);   \
+        return paged_split_run<D, 1, MODE>(c, pg, sh, q, QH, scale, part_o, part_ml, s);                               \
     }                                                                                                                  \
     }
