@@ -75,6 +75,7 @@ class _PageTableStruct(ctypes.Structure):
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _CP = ctypes.POINTER(_CacheStruct)
 _TP = ctypes.POINTER(_PageTableStruct)
+_TWO = _I64 * 2
 
 
 def library_path() -> str:
@@ -464,7 +465,7 @@ def tq_multi_token_attention(cache: Cache, q: torch.Tensor, seq_len: int, softma
 def _empty_on(stream, shape, dtype, device):
     """Memory for a call on `stream`, taken from that stream's share of the allocator, so that it is
     not handed on before the call's kernels are through with it."""
-    if stream is None or int(_stream(stream)) == torch.cuda.current_stream().cuda_stream:
+    if stream is None or int(_stream(stream)) == _stream(None):
         return torch.empty(shape, dtype=dtype, device=device)
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=device)
     with torch.cuda.stream(s):
@@ -491,7 +492,7 @@ def _ragged_strides(x: torch.Tensor, heads: int | None, d: int, what: str):
     if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[2] != d or (heads is not None and x.shape[1] != heads) or \
             (d > 1 and x.stride(2) != 1):
         raise ValueError(f"{what} must be bfloat16 [tokens][heads][head_dim] with head_dim contiguous, matching the pool")
-    return (_I64 * 2)(x.stride(0), x.stride(1))
+    return _TWO(x.stride(0), x.stride(1))
 
 
 def tq_paged_append(pool: Cache, table: PageTable, starts: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -513,15 +514,18 @@ def tq_paged_decode(pool: Cache, table: PageTable, starts: torch.Tensor, total: 
     code = _dtype_code(dtype)
     shape = (int(total), pool.num_kv_heads, pool.head_dim)
     dev = pool.k_codes.device
-    if want_k and k_out is None:
-        k_out = _empty_on(stream, shape, dtype, dev)
-    if want_v and v_out is None:
-        v_out = _empty_on(stream, shape, dtype, dev)
-    k_out, v_out = (k_out if want_k else None), (v_out if want_v else None)
     for x in (k_out, v_out):
         if x is not None and (x.dtype != dtype or tuple(x.shape) != shape or not x.is_contiguous()):
             raise ValueError("decode outputs must be contiguous [total][H][d] of the requested dtype")
     s, t = _paged_args(pool, table, starts, k_out, v_out)
+    if not want_k:
+        k_out = None
+    elif k_out is None:
+        k_out = _empty_on(stream, shape, dtype, dev)
+    if not want_v:
+        v_out = None
+    elif v_out is None:
+        v_out = _empty_on(stream, shape, dtype, dev)
     _check(lib().tq_paged_decode(ctypes.byref(s), ctypes.byref(t), starts.data_ptr(), int(total), code,
                                  k_out.data_ptr() if want_k else None, v_out.data_ptr() if want_v else None,
                                  _stream(stream)), "tq_paged_decode")
@@ -541,14 +545,14 @@ def tq_paged_attention(pool: Cache, table: PageTable, starts: torch.Tensor, q: t
     max_new of one sequence) over their sequences' rows -> bf16 [tokens][QH][d]."""
     qs = _ragged_strides(q, None, pool.head_dim, "q")
     total, QH, d = q.shape
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous()):
+        raise ValueError("out must be contiguous bfloat16, shaped like q")
+    s, t = _paged_args(pool, table, starts, q, out, workspace)
     if out is None:
         out = _empty_on(stream, (total, QH, d), torch.bfloat16, q.device)
-    if out.dtype != torch.bfloat16 or tuple(out.shape) != (total, QH, d) or not out.is_contiguous():
-        raise ValueError("out must be contiguous bfloat16, shaped like q")
     if workspace is None and total > 0:
         need = tq_paged_attention_workspace_bytes(pool, table, QH, total, max_new)
         workspace = _empty_on(stream, need, torch.uint8, q.device)
-    s, t = _paged_args(pool, table, starts, q, out, workspace)
     scale = (1.0 / d ** 0.5) if softmax_scale is None else float(softmax_scale)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().tq_paged_attention(ctypes.byref(s), ctypes.byref(t), starts.data_ptr(), int(total), int(max_new),

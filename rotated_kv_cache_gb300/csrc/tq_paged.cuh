@@ -80,8 +80,9 @@ __device__ __forceinline__ int64_t paged_row(const PagedView &v, int64_t t, int 
 // ------------------------------------------------------------------ split attention over a paged batch
 // The work of a batch is one line: sequence after sequence, in a sequence its
 // units (kv-head, block of CB columns) one after another, in a unit its start
-// (kSegStart: what a segment costs besides its stages, in stages) and its
-// stages of ST rows in row order.  CTA c takes the c-th run of `per` places,
+// (what a segment costs besides its stages, in stages: kSegStart, or nothing
+// where the CTAs are enough for a stage each) and its stages of ST rows in row
+// order.  CTA c takes the c-th run of `per` places,
 // whatever lengths the sequences have, so all CTAs finish together; a run's
 // stages of one unit are a segment (a run that ends within a start leaves the
 // unit to the next CTA), and a unit's segments are merged by the combine.
@@ -136,6 +137,7 @@ struct PagedWalk {
     int64_t at;           // line position of the current unit's first stage
     int64_t up;           // units before sequence s
     int s, u, stages, units;  // sequence, unit in it; its stages per unit and its units
+    int start;            // places of a unit's start
     PagedSegment seg[2];
 };
 
@@ -164,20 +166,27 @@ __device__ __forceinline__ void paged_walk_start(const PagedSplit &ps, PagedWalk
     const int S = ps.v.seqs;
     int st, un;
     paged_shape(ps, lane, ST, CB, H, G, st, un);
-    int64_t total = (int64_t)(st + kSegStart) * un;
+    int64_t total = (int64_t)st * un, units = un;
     for (int b = 32; b < S; b += 32) {
         int st1, un1;
         paged_shape(ps, b + lane, ST, CB, H, G, st1, un1);
-        total += (int64_t)(st1 + kSegStart) * un1;
+        total += (int64_t)st1 * un1;
+        units += un1;
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    for (int o = 16; o >= 1; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        units += __shfl_xor_sync(0xffffffffu, units, o);
+    }
+    const int start = total <= gridDim.x ? 0 : kSegStart;
+    total += start * units;
     int64_t per = div_small(total + gridDim.x - 1, gridDim.x);
-    if (per < kSegStart + 1) per = kSegStart + 1;
+    if (per < start + 1) per = start + 1;
     const int64_t x = blockIdx.x * per, end = imin64(total, x + per);
     if (lane == 0) {
         w.end = end;
         w.per = per;
+        w.start = start;
         w.seg[0].count = 0;
     }
     __syncwarp();
@@ -185,18 +194,18 @@ __device__ __forceinline__ void paged_walk_start(const PagedSplit &ps, PagedWalk
     bool found = x >= end;
     for (int b = 0; b < S && !found; b += 32) {
         if (b > 0) paged_shape(ps, b + lane, ST, CB, H, G, st, un);
-        const int64_t c = (int64_t)(st + kSegStart) * un;
+        const int64_t c = (int64_t)(st + start) * un;
         const int64_t ws = warp_inclusive_sum(c, lane), us = warp_inclusive_sum(un, lane);
         const int64_t s_at = sbase + ws - c, u_at = ubase + us - un;
         const bool mine = c > 0 && s_at <= x && x < s_at + c;
         if (mine) {
-            const int64_t u = div_small(x - s_at, st + kSegStart);
+            const int64_t u = div_small(x - s_at, st + start);
             w.s = b + lane;
             w.up = u_at;
             w.stages = st;
             w.units = un;
             w.u = (int)u;
-            w.at = s_at + u * (st + kSegStart) + kSegStart;
+            w.at = s_at + u * (st + start) + start;
             paged_segment(ps, w, w.seg[0], x > w.at ? (int)(x - w.at) : 0, H);
         }
         found |= __any_sync(0xffffffffu, mine);
@@ -209,7 +218,7 @@ __device__ __forceinline__ void paged_walk_start(const PagedSplit &ps, PagedWalk
 __device__ __forceinline__ void paged_walk_next(const PagedSplit &ps, PagedWalk &w, PagedSegment &nxt, int ST, int CB, int H, int G)
 {
     nxt.count = 0;
-    w.at += w.stages + kSegStart;  // of the next unit of the same length
+    w.at += w.stages + w.start;  // of the next unit
     if (w.at >= w.end) return;
     if (++w.u == w.units) {  // the next sequence with work (w.at < w.end says that there is one)
         w.up += w.units;
