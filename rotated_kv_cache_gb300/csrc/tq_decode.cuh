@@ -95,12 +95,12 @@ __global__ void __launch_bounds__(256) decode_key_kernel(const __grid_constant__
     pdl_wait_primary();  // whatever the previous kernel on the stream writes or reads is settled
     pdl_allow_dependents();
     const int64_t gi = (int64_t)blockIdx.x * 256 + threadIdx.x;  // group within the (sequence, kv-head)'s n rows
-    if (gi >= p.groups_per_bh) return;
+    if (!PAGED && gi >= p.groups_per_bh) return;
     constexpr int A = align_of_bytes(4 * KB);
     if constexpr (PAGED) {  // group gi % (d / 32) of token gi / (d / 32), every kv-head
         const int gpr = p.d / 32, g = (int)(gi % gpr);
-        const int64_t t = gi / gpr, row0 = paged_row(p.pv, t, (int)p.BH);
-        if (t >= p.pv.starts[p.pv.seqs]) return;  // behind the last sequence: left as it was
+        const int64_t t = gi / gpr, row0 = paged_row(p.pv, paged_lanes(p.pv, threadIdx.x & 31), t, (int)p.BH);
+        if (gi >= p.groups_per_bh || t >= p.pv.starts[p.pv.seqs]) return;  // behind the last sequence: left as it was
         for (int64_t h = blockIdx.y; h < p.BH; h += gridDim.y) {
             uint32_t w[KB] = {};
             float s = 0.0f, z = 0.0f;  // a token without a row reads as zeros
@@ -204,30 +204,17 @@ __device__ __forceinline__ void key_words_load(const uint8_t *src, uint32_t (&w)
     }
 }
 
-// Paged: row r of the tile is at cache row `crow` of lane r (-1: none, its
-// groups read as zeros).
-template <int D, bool PAGED>
-__device__ __forceinline__ void key_tile_load(const ValueDecodeParams &p, uint32_t bh, int64_t t_first, int64_t crow,
-                                              int lane, KeyTile &k)
+template <int D>
+__device__ __forceinline__ void key_tile_load(const ValueDecodeParams &p, uint32_t bh, int64_t t_first, int lane,
+                                              KeyTile &k)
 {
     constexpr int GPR = D / 32;  // groups per row
     const int64_t g0 = ((int64_t)bh * p.cap + p.t0 + t_first) * GPR;  // first group of the tile in the planes
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int g = lane + 32 * i;
-        int64_t gi = g0 + g;
-        if constexpr (PAGED) {
-            const int64_t row = __shfl_sync(0xffffffffu, crow, g / GPR);
-            gi = row * GPR + g % GPR;
-            if (row < 0) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) k.w[i][j] = 0u;
-                k.s[i] = k.z[i] = 0u;
-                continue;
-            }
-        } else if (t_first + g / GPR >= p.n) {
-            continue;
-        }
+        if (t_first + g / GPR >= p.n) continue;
+        const int64_t gi = g0 + g;
         switch (p.kb) {
         case 8: key_words_load<8>(p.k_codes + gi * 32, k.w[i]); break;
         case 4: key_words_load<4>(p.k_codes + gi * 16, k.w[i]); break;
@@ -248,18 +235,17 @@ __device__ __forceinline__ void key_group_from_tile(const uint32_t (&w8)[8], uin
     key_group_out<KB, F32>(w, f16_bits_to_f32((uint16_t)s), f16_bits_to_f32((uint16_t)z), dst);
 }
 
-template <int D, bool F32, bool PAGED>
-__device__ __forceinline__ void key_tile_store(const ValueDecodeParams &p, uint32_t bh, int64_t t_first, int64_t n,
-                                               int lane, const KeyTile &k)
+template <int D, bool F32>
+__device__ __forceinline__ void key_tile_store(const ValueDecodeParams &p, uint32_t bh, int64_t t_first, int lane,
+                                               const KeyTile &k)
 {
     constexpr int GPR = D / 32;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int g = lane + 32 * i;
-        if (t_first + g / GPR >= n) continue;
-        // output [bh][t][D] (paged [t][h][D]): group g of the tile starts at element (bh n + t_first) D + 32 g
-        const int64_t e = PAGED ? ((t_first + g / GPR) * p.H + bh) * D + 32 * (g % GPR) : ((int64_t)bh * n + t_first) * D + 32 * g;
-        void *dst = static_cast<uint8_t *>(p.k_out) + e * (F32 ? 4 : 2);
+        if (t_first + g / GPR >= p.n) continue;
+        // output [bh][t][D]: group g of the tile starts at element (bh n + t_first) D + 32 g
+        void *dst = static_cast<uint8_t *>(p.k_out) + (((int64_t)bh * p.n + t_first) * D + 32 * g) * (F32 ? 4 : 2);
         switch (p.kb) {
         case 8: key_group_from_tile<8, F32>(k.w[i], k.s[i], k.z[i], dst); break;
         case 4: key_group_from_tile<4, F32>(k.w[i], k.s[i], k.z[i], dst); break;
@@ -269,14 +255,89 @@ __device__ __forceinline__ void key_tile_store(const ValueDecodeParams &p, uint3
     }
 }
 
-// A warp takes every (grid kVWarps)-th tile of rows; in paged launches a run
-// of consecutive items, the kv-heads of one token tile after another, so that
-// it looks a tile's rows up once for all its heads.
+// The same for a paged tile, whose rows are anywhere: row r at cache row
+// `crow` of lane r (-1: none, its groups read as zeros).  The look-ups cost
+// registers that the key codes would need while the values are worked on, and
+// spilled prefetches wait for their loads; so the codes go to shared memory
+// (asynchronous copies, each lane its own) and only scales and zeros to
+// registers.  Fetch of 4 x 8 x 8192 rows: 48 us with codes in registers.
+constexpr int kKeyWords = 8;  // most 32-bit words of a key group
+
+template <int KB>
+__device__ __forceinline__ void key_words_copy(uint32_t dst, const uint8_t *src)
+{
+    // a lane's words of one group lie 32 lanes apart in pieces of B bytes
+    constexpr int B = KB % 4 == 0 ? 16 : KB == 2 ? 8 : 4;
+#pragma unroll
+    for (int k = 0; k < 4 * KB / B; ++k)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst + k * 32 * B), "l"(src + k * B), "n"(B) : "memory");
+}
+
+template <int D>
+__device__ __forceinline__ void paged_key_load(const ValueDecodeParams &p, uint32_t buf, int64_t crow, int lane,
+                                               uint32_t (&sz)[2])
+{
+    constexpr int GPR = D / 32;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int g = lane + 32 * i;
+        const int64_t row = __shfl_sync(0xffffffffu, crow, g / GPR);
+        sz[i] = 0u;
+        if (row < 0) continue;
+        const int64_t gi = row * GPR + g % GPR;
+        const uint32_t at = buf + i * (kKeyWords * 128);
+        switch (p.kb) {
+        case 8: key_words_copy<8>(at + 16 * lane, p.k_codes + gi * 32); break;
+        case 4: key_words_copy<4>(at + 16 * lane, p.k_codes + gi * 16); break;
+        case 5: key_words_copy<5>(at + 4 * lane, p.k_codes + gi * 20); break;
+        default: key_words_copy<2>(at + 8 * lane, p.k_codes + gi * 8); break;
+        }
+        sz[i] = (uint32_t)p.k_scale[gi] | (uint32_t)p.k_zero[gi] << 16;
+    }
+}
+
+template <int KB, bool F32>
+__device__ __forceinline__ void paged_key_out(const uint32_t *src, int lane, uint32_t sz, void *dst)
+{
+    constexpr int B = KB % 4 == 0 ? 4 : KB == 2 ? 2 : 1;  // words per piece
+    uint32_t w[KB];
+#pragma unroll
+    for (int k = 0; k < KB; ++k) w[k] = src[(k / B) * 32 * B + lane * B + k % B];
+    key_group_out<KB, F32>(w, f16_bits_to_f32((uint16_t)sz), f16_bits_to_f32((uint16_t)(sz >> 16)), dst);
+}
+
+// outputs [token][head][D]; tokens from n on are left as they were
+template <int D, bool F32>
+__device__ __forceinline__ void paged_key_store(const ValueDecodeParams &p, const uint32_t *buf, uint32_t h, int64_t t_first,
+                                                int64_t n, int lane, const uint32_t (&sz)[2])
+{
+    constexpr int GPR = D / 32;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int g = lane + 32 * i;
+        const int64_t t = t_first + g / GPR;
+        if (t >= n) continue;
+        void *dst = static_cast<uint8_t *>(p.k_out) + ((t * p.H + h) * D + 32 * (g % GPR)) * (F32 ? 4 : 2);
+        const uint32_t *src = buf + i * (kKeyWords * 32);
+        switch (p.kb) {
+        case 8: paged_key_out<8, F32>(src, lane, sz[i], dst); break;
+        case 4: paged_key_out<4, F32>(src, lane, sz[i], dst); break;
+        case 5: paged_key_out<5, F32>(src, lane, sz[i], dst); break;
+        default: paged_key_out<2, F32>(src, lane, sz[i], dst); break;
+        }
+    }
+}
+
+// A warp takes every (grid kVWarps)-th tile of rows, so that neighbouring warps
+// read and write neighbouring memory.  Paged items run over the kv-heads of a
+// token tile first (outputs are [token][head][D]).
 template <int D, int VB, bool F32, bool PAGED>
 __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __grid_constant__ ValueDecodeParams p)
 {
     using G = VGeo<D>;
     __shared__ __align__(16) float scen[1 << VB];
+    __shared__ __align__(16) uint32_t kbuf[PAGED ? kVWarps : 1][PAGED ? 2 * kKeyWords * 32 : 1];  // paged: key codes
     __shared__ __align__(16) float2 smul[G::LPR][34];  // (+-1/sqrt d) of elements (j, j+32) of each part, padded
     pdl_wait_primary();  // whatever the previous kernel on the stream writes or reads is settled
     pdl_allow_dependents();
@@ -294,18 +355,20 @@ __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __g
     const int r = lane % G::ROWS, part = lane / G::ROWS;
     const char *cen = reinterpret_cast<const char *>(scen);
 
-    const uint32_t W = PAGED ? 1u : gridDim.x * kVWarps;
-    uint32_t item = blockIdx.x * kVWarps + warp, end = p.items;
+    const uint32_t W = gridDim.x * kVWarps;
+    uint32_t item = blockIdx.x * kVWarps + warp;
     int64_t n = p.n;
     if constexpr (PAGED) {
-        const uint64_t w = item, all = (uint64_t)gridDim.x * kVWarps;
-        item = (uint32_t)(w * p.items / all);
-        end = (uint32_t)((w + 1) * p.items / all);
         n = imin64(n, p.pv.starts[p.pv.seqs]);  // tokens behind the last sequence are left as they were
     }
     // the next tile's codes are loaded while this one is transformed
     uint32_t nw[2 * VB], nsc = 0;
-    int64_t prow = -1, prow_t = -1;  // paged: this lane's row for kv-head 0, of the token tile at prow_t
+    // paged: this lane's place in the tile loaded next, its page number under way meanwhile
+    PagedPlace next{0, kNoRow};
+    auto seek = [&](uint32_t it) {
+        next = paged_seek(p.pv, paged_lanes(p.pv, lane), (int64_t)fast_div(it, p.div_h) * G::ROWS + r);
+    };
+    if constexpr (PAGED) seek(item);
     auto locate = [&](uint32_t it, int64_t &t, int64_t &crow, uint32_t &bh) {
         if constexpr (PAGED) {
             const uint32_t tile = fast_div(it, p.div_h);
@@ -323,16 +386,14 @@ __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __g
         uint32_t bh;
         locate(it, t, crow, bh);
         if constexpr (PAGED) {
-            if (t != prow_t) {
-                prow_t = t;
-                prow = paged_row(p.pv, t, p.H);
-            }
-            crow = ahead = prow < 0 ? -1 : prow + (int64_t)bh * p.pv.page;
+            const int64_t row = paged_place_row(p.pv, next, p.H);
+            seek(it + W);
+            crow = ahead = row < 0 ? -1 : row + (int64_t)bh * p.pv.page;
         }
         if (PAGED ? crow >= 0 : t < p.n) load_value_lane<D, VB>(p, crow, part, nw, nsc);
     };
-    if (item < end) load_tile(item);
-    for (; item < end; item += W) {
+    if (item < p.items) load_tile(item);
+    for (; item < p.items; item += W) {
         uint32_t w[2 * VB], sc = nsc;
 #pragma unroll
         for (int k = 0; k < 2 * VB; ++k) w[k] = nw[k];
@@ -353,9 +414,13 @@ __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __g
         if constexpr (PAGED) crow = ahead;
         const bool valid = t < n;
         KeyTile kt;
+        uint32_t ksz[2];
         const bool keys = p.k_out != nullptr;
-        if (keys) key_tile_load<D, PAGED>(p, bh, t - r, crow, lane, kt);
-        if (item + W < end) load_tile(item + W);
+        if (keys) {
+            if constexpr (PAGED) paged_key_load<D>(p, smem_addr(kbuf[warp]), crow, lane, ksz);
+            else key_tile_load<D>(p, bh, t - r, lane, kt);
+        }
+        if (item + W < p.items) load_tile(item + W);
         float2 P[32];
         if (PAGED ? crow >= 0 : valid) {
             const float s0 = f16_bits_to_f32((uint16_t)(sc & 0xFFFFu)), s1 = f16_bits_to_f32((uint16_t)(sc >> 16));
@@ -410,7 +475,10 @@ __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __g
                 }
             }
         }
-        if (keys) key_tile_store<D, F32, PAGED>(p, bh, t - r, n, lane, kt);
+        if (keys) {
+            if constexpr (PAGED) paged_key_store<D, F32>(p, kbuf[warp], bh, t - r, n, lane, ksz);
+            else key_tile_store<D, F32>(p, bh, t - r, lane, kt);
+        }
     }
 }
 

@@ -699,8 +699,9 @@ __device__ __forceinline__ void encode_body(const EncodeParams &p, const CUtenso
         if constexpr (PAGED) {
             if (t_first != prow_t) {  // looked up while the tile is on its way
                 prow_t = t_first;
+                const PagedLanes lanes = paged_lanes(p.pv, lane);
 #pragma unroll
-                for (int g = 0; g < G::RPL; ++g) prow[g] = paged_row(p.pv, t_first + r + g * G::ROWS, p.H);
+                for (int g = 0; g < G::RPL; ++g) prow[g] = paged_row(p.pv, lanes, t_first + r + g * G::ROWS, p.H);
             }
         }
         if (!mbar_wait_bounded(bar, (k >> 1) & 1, p.err)) {

@@ -55,26 +55,89 @@ __device__ __forceinline__ int paged_page(const PagedView &v, int s, uint32_t po
     return -1;
 }
 
-// Plane row of ragged token t for kv-head 0 (add h * page for kv-head h), or
-// -1: t lies behind the last sequence, before its sequence's first row (more
-// new tokens than rows), or in a bad page.  The sequence is the last one
-// that starts at or before t (empty sequences share a start).
-__device__ __forceinline__ int64_t paged_row(const PagedView &v, int64_t t, int H)
+// The starts and lengths of the first 31 sequences, one a lane (starts[lane],
+// lens[lane]): with no more sequences than that, a token's sequence is found
+// without a load.
+struct PagedLanes {
+    int start, len;
+};
+
+__device__ __forceinline__ PagedLanes paged_lanes(const PagedView &v, int lane)
 {
-    if (t >= v.total) return -1;
-    int lo = 0, hi = v.seqs + 1;  // starts[lo - 1] <= t < starts[hi]
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (v.starts[mid] <= t) lo = mid + 1;
-        else hi = mid;
-    }
-    const int s = lo - 1;
-    if (s < 0 || s >= v.seqs) return -1;
-    const int64_t s0 = paged_start(v, s), n = paged_new(v, s), pos = paged_len(v, s) - n + (t - s0);
-    if (t >= s0 + n || pos < 0) return -1;
+    PagedLanes l;
+    l.start = v.starts[lane < v.seqs ? lane : v.seqs];
+    l.len = v.lens[lane < v.seqs ? lane : v.seqs - 1];
+    return l;
+}
+
+// A token's place: its page number as the table gives it (a load that may still
+// be under way) and its row in the page, kNoRow where it has none.
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+
+struct PagedPlace {
+    int page;
     uint32_t slot;
-    const int p = paged_page(v, s, (uint32_t)pos, slot);
-    return p < 0 ? -1 : (int64_t)p * H * v.page + slot;
+};
+
+// Plane row of a place for kv-head 0 (add h * page for kv-head h), or -1.
+__device__ __forceinline__ int64_t paged_place_row(const PagedView &v, const PagedPlace &a, int H)
+{
+    if (a.slot == kNoRow) return -1;
+    if ((uint32_t)a.page >= (uint32_t)v.num_pages) {
+        atomicOr(v.err, kErrPage);
+        return -1;
+    }
+    return (int64_t)a.page * H * v.page + a.slot;
+}
+
+// Place of ragged token t; none: t lies behind the last sequence, before its sequence's first row (more
+// new tokens than rows), or in a bad page.  The sequence is the last one
+// that starts at or before t (empty sequences share a start).  Whole warps
+// call it, each lane with a token of its own.
+__device__ __forceinline__ PagedPlace paged_seek(const PagedView &v, const PagedLanes &l, int64_t t)
+{
+    const PagedPlace none{0, kNoRow};
+    int s, len;
+    int64_t s0, s1;
+    if (v.seqs < 32) {
+        int lo = 0;  // sequences that start at or before t, found bit by bit
+#pragma unroll
+        for (int step = 16; step >= 1; step >>= 1) {
+            const int x = __shfl_sync(0xffffffffu, l.start, lo + step - 1);
+            if (lo + step - 1 <= v.seqs && x <= t) lo += step;
+        }
+        s = lo - 1;
+        s0 = __shfl_sync(0xffffffffu, l.start, s < 0 ? 0 : s);
+        s1 = __shfl_sync(0xffffffffu, l.start, s < 0 ? 0 : s + 1 > 31 ? 31 : s + 1);
+        len = __shfl_sync(0xffffffffu, l.len, s < 0 ? 0 : s);
+        if (s < 0 || s >= v.seqs) return none;
+    } else {
+        int lo = 0, hi = v.seqs + 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (v.starts[mid] <= t) lo = mid + 1;
+            else hi = mid;
+        }
+        s = lo - 1;
+        if (s < 0 || s >= v.seqs) return none;
+        s0 = v.starts[s];
+        s1 = v.starts[s + 1];
+        len = v.lens[s];
+    }
+    if (t >= v.total) return none;
+    if (len < 0 || len > v.max_len || s0 < 0 || s1 > v.total || s1 < s0) {
+        atomicOr(v.err, kErrLength);
+        return none;
+    }
+    const int64_t pos = len - (s1 - s0) + (t - s0);
+    if (t >= s1 || pos < 0) return none;
+    const uint32_t i = fast_div((uint32_t)pos, v.div_page);
+    return PagedPlace{v.pages[s * v.stride + i], (uint32_t)pos - i * v.page};
+}
+
+__device__ __forceinline__ int64_t paged_row(const PagedView &v, const PagedLanes &l, int64_t t, int H)
+{
+    return paged_place_row(v, paged_seek(v, l, t), H);
 }
 
 // ------------------------------------------------------------------ split attention over a paged batch
