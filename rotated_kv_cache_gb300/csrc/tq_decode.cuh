@@ -257,87 +257,110 @@ __device__ __forceinline__ void key_tile_store(const ValueDecodeParams &p, uint3
 
 // The same for a paged tile, whose rows are anywhere: row r at cache row
 // `crow` of lane r (-1: none, its groups read as zeros).  The look-ups cost
-// registers that the key codes would need while the values are worked on, and
-// spilled prefetches wait for their loads; so the codes go to shared memory
-// (asynchronous copies, each lane its own) and only scales and zeros to
-// registers.  Fetch of 4 x 8 x 8192 rows: 48 us with codes in registers.
-constexpr int kKeyWords = 8;  // most 32-bit words of a key group
+// registers that the keys would need while the values are worked on, and
+// spilled prefetches wait for their loads; so keys, scales and zeros are copied
+// to shared memory a tile ahead.
+template <int D>
+struct KeyBuf {
+    // codes: a lane's words of its two groups in pieces of at most 16 bytes, 32 lanes
+    // apart; then fp16 scales and zeros, row by row
+    static constexpr int GPR = D / 32, ROWS = VGeo<D>::ROWS;
+    static constexpr int CODES = 2 * 32 * 32, META = ROWS * GPR * 2, BYTES = CODES + 2 * META;
+};
+
+template <int B>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B) : "memory");
+}
 
 template <int KB>
-__device__ __forceinline__ void key_words_copy(uint32_t dst, const uint8_t *src)
+__device__ __forceinline__ void key_words_copy(uint32_t dst, int lane, const uint8_t *src)
 {
-    // a lane's words of one group lie 32 lanes apart in pieces of B bytes
     constexpr int B = KB % 4 == 0 ? 16 : KB == 2 ? 8 : 4;
 #pragma unroll
-    for (int k = 0; k < 4 * KB / B; ++k)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst + k * 32 * B), "l"(src + k * B), "n"(B) : "memory");
+    for (int k = 0; k < 4 * KB / B; ++k) copy_async<B>(dst + (k * 32 + lane) * B, src + k * B);
 }
 
 template <int D>
-__device__ __forceinline__ void paged_key_load(const ValueDecodeParams &p, uint32_t buf, int64_t crow, int lane,
-                                               uint32_t (&sz)[2])
+__device__ __forceinline__ void paged_key_load(const ValueDecodeParams &p, uint32_t buf, int64_t crow, int lane)
 {
-    constexpr int GPR = D / 32;
+    using K = KeyBuf<D>;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int g = lane + 32 * i;
-        const int64_t row = __shfl_sync(0xffffffffu, crow, g / GPR);
-        sz[i] = 0u;
+        const int64_t row = __shfl_sync(0xffffffffu, crow, g / K::GPR);
         if (row < 0) continue;
-        const int64_t gi = row * GPR + g % GPR;
-        const uint32_t at = buf + i * (kKeyWords * 128);
+        const int64_t gi = row * K::GPR + g % K::GPR;
+        const uint32_t at = buf + i * (K::CODES / 2);
         switch (p.kb) {
-        case 8: key_words_copy<8>(at + 16 * lane, p.k_codes + gi * 32); break;
-        case 4: key_words_copy<4>(at + 16 * lane, p.k_codes + gi * 16); break;
-        case 5: key_words_copy<5>(at + 4 * lane, p.k_codes + gi * 20); break;
-        default: key_words_copy<2>(at + 8 * lane, p.k_codes + gi * 8); break;
+        case 8: key_words_copy<8>(at, lane, p.k_codes + gi * 32); break;
+        case 4: key_words_copy<4>(at, lane, p.k_codes + gi * 16); break;
+        case 5: key_words_copy<5>(at, lane, p.k_codes + gi * 20); break;
+        default: key_words_copy<2>(at, lane, p.k_codes + gi * 8); break;
         }
-        sz[i] = (uint32_t)p.k_scale[gi] | (uint32_t)p.k_zero[gi] << 16;
+    }
+    // scales by a row's lane of part 0, zeros by its lane of part 1 (at head_dim 64 it is the only one)
+    constexpr int B = K::GPR * 2 < 16 ? K::GPR * 2 : 16;
+    const int r = lane % K::ROWS, part = lane / K::ROWS;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        if (D > 64 && part != m) continue;
+        const uint16_t *plane = m ? p.k_zero : p.k_scale;
+        const uint32_t at = buf + K::CODES + m * K::META + r * (K::GPR * 2);
+#pragma unroll
+        for (int k = 0; k < K::GPR * 2 / B; ++k) {
+            if (crow >= 0) copy_async<B>(at + k * B, reinterpret_cast<const uint8_t *>(plane + crow * K::GPR) + k * B);
+            else
+#pragma unroll
+                for (int q = 0; q < B / 4; ++q) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + k * B + 4 * q), "r"(0u) : "memory");
+        }
     }
 }
 
 template <int KB, bool F32>
-__device__ __forceinline__ void paged_key_out(const uint32_t *src, int lane, uint32_t sz, void *dst)
+__device__ __forceinline__ void paged_key_out(const uint32_t *src, int lane, float s, float z, void *dst)
 {
     constexpr int B = KB % 4 == 0 ? 4 : KB == 2 ? 2 : 1;  // words per piece
     uint32_t w[KB];
 #pragma unroll
     for (int k = 0; k < KB; ++k) w[k] = src[(k / B) * 32 * B + lane * B + k % B];
-    key_group_out<KB, F32>(w, f16_bits_to_f32((uint16_t)sz), f16_bits_to_f32((uint16_t)(sz >> 16)), dst);
+    key_group_out<KB, F32>(w, s, z, dst);
 }
 
 // outputs [token][head][D]; tokens from n on are left as they were
 template <int D, bool F32>
-__device__ __forceinline__ void paged_key_store(const ValueDecodeParams &p, const uint32_t *buf, uint32_t h, int64_t t_first,
-                                                int64_t n, int lane, const uint32_t (&sz)[2])
+__device__ __forceinline__ void paged_key_store(const ValueDecodeParams &p, const uint8_t *buf, uint32_t h, int64_t t_first,
+                                                int64_t n, int lane)
 {
-    constexpr int GPR = D / 32;
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    using K = KeyBuf<D>;
+    const uint16_t *meta = reinterpret_cast<const uint16_t *>(buf + K::CODES);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int g = lane + 32 * i;
-        const int64_t t = t_first + g / GPR;
+        const int64_t t = t_first + g / K::GPR;
         if (t >= n) continue;
-        void *dst = static_cast<uint8_t *>(p.k_out) + ((t * p.H + h) * D + 32 * (g % GPR)) * (F32 ? 4 : 2);
-        const uint32_t *src = buf + i * (kKeyWords * 32);
+        void *dst = static_cast<uint8_t *>(p.k_out) + ((t * p.H + h) * D + 32 * (g % K::GPR)) * (F32 ? 4 : 2);
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(buf + i * (K::CODES / 2));
+        const float s = f16_bits_to_f32(meta[g]), z = f16_bits_to_f32(meta[K::META / 2 + g]);
         switch (p.kb) {
-        case 8: paged_key_out<8, F32>(src, lane, sz[i], dst); break;
-        case 4: paged_key_out<4, F32>(src, lane, sz[i], dst); break;
-        case 5: paged_key_out<5, F32>(src, lane, sz[i], dst); break;
-        default: paged_key_out<2, F32>(src, lane, sz[i], dst); break;
+        case 8: paged_key_out<8, F32>(src, lane, s, z, dst); break;
+        case 4: paged_key_out<4, F32>(src, lane, s, z, dst); break;
+        case 5: paged_key_out<5, F32>(src, lane, s, z, dst); break;
+        default: paged_key_out<2, F32>(src, lane, s, z, dst); break;
         }
     }
 }
 
-// A warp takes every (grid kVWarps)-th tile of rows, so that neighbouring warps
-// read and write neighbouring memory.  Paged items run over the kv-heads of a
-// token tile first (outputs are [token][head][D]).
+// A warp takes every (grid kVWarps)-th tile of rows; in paged launches a run
+// of consecutive items, the kv-heads of one token tile after another (outputs
+// are [token][head][D]), so that it looks a tile's rows up once for its heads.
 template <int D, int VB, bool F32, bool PAGED>
 __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __grid_constant__ ValueDecodeParams p)
 {
     using G = VGeo<D>;
     __shared__ __align__(16) float scen[1 << VB];
-    __shared__ __align__(16) uint32_t kbuf[PAGED ? kVWarps : 1][PAGED ? 2 * kKeyWords * 32 : 1];  // paged: key codes
+    __shared__ __align__(16) uint8_t kbuf[PAGED ? kVWarps : 1][2][PAGED ? KeyBuf<D>::BYTES : 16];  // paged: keys of two tiles
     __shared__ __align__(16) float2 smul[G::LPR][34];  // (+-1/sqrt d) of elements (j, j+32) of each part, padded
     pdl_wait_primary();  // whatever the previous kernel on the stream writes or reads is settled
     pdl_allow_dependents();
@@ -355,20 +378,28 @@ __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __g
     const int r = lane % G::ROWS, part = lane / G::ROWS;
     const char *cen = reinterpret_cast<const char *>(scen);
 
-    const uint32_t W = gridDim.x * kVWarps;
-    uint32_t item = blockIdx.x * kVWarps + warp;
+    const uint32_t W = PAGED ? 1u : gridDim.x * kVWarps;
+    uint32_t item = blockIdx.x * kVWarps + warp, end = p.items;
     int64_t n = p.n;
     if constexpr (PAGED) {
+        const uint64_t w = item, all = (uint64_t)gridDim.x * kVWarps;
+        item = (uint32_t)(w * p.items / all);
+        end = (uint32_t)((w + 1) * p.items / all);
         n = imin64(n, p.pv.starts[p.pv.seqs]);  // tokens behind the last sequence are left as they were
     }
     // the next tile's codes are loaded while this one is transformed
     uint32_t nw[2 * VB], nsc = 0;
-    // paged: this lane's place in the tile loaded next, its page number under way meanwhile
-    PagedPlace next{0, kNoRow};
-    auto seek = [&](uint32_t it) {
-        next = paged_seek(p.pv, paged_lanes(p.pv, lane), (int64_t)fast_div(it, p.div_h) * G::ROWS + r);
-    };
-    if constexpr (PAGED) seek(item);
+    // paged: this lane's place in the token tile `at_tile`, and in the next one, whose page number
+    // is under way meanwhile
+    const bool keys = p.k_out != nullptr;
+    PagedPlace place{0, kNoRow}, next{0, kNoRow};
+    uint32_t at_tile = 0, half = 0;  // (half of kbuf that the tile loaded next takes)
+    auto seek = [&](uint32_t tile) { next = paged_seek(p.pv, paged_lanes(p.pv, lane), (int64_t)tile * G::ROWS + r); };
+    if constexpr (PAGED) {
+        const uint32_t tile = fast_div(item, p.div_h);
+        seek(tile);
+        at_tile = tile - 1;
+    }
     auto locate = [&](uint32_t it, int64_t &t, int64_t &crow, uint32_t &bh) {
         if constexpr (PAGED) {
             const uint32_t tile = fast_div(it, p.div_h);
@@ -380,20 +411,30 @@ __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __g
             crow = (int64_t)bh * p.cap + p.t0 + t;
         }
     };
-    int64_t ahead = -1;  // paged: cache row of this lane in the tile loaded ahead (-1: none)
+    bool ahead = false, here = false;  // paged: this lane has a row in the tile loaded ahead, in this one
     auto load_tile = [&](uint32_t it) {
         int64_t t, crow;
         uint32_t bh;
         locate(it, t, crow, bh);
         if constexpr (PAGED) {
-            const int64_t row = paged_place_row(p.pv, next, p.H);
-            seek(it + W);
-            crow = ahead = row < 0 ? -1 : row + (int64_t)bh * p.pv.page;
+            const uint32_t tile = fast_div(it, p.div_h);
+            if (tile != at_tile) {
+                at_tile = tile;
+                place = next;
+                seek(tile + 1);
+            }
+            const int64_t row = paged_place_row(p.pv, place, p.H);
+            crow = row < 0 ? -1 : row + (int64_t)bh * p.pv.page;
+            here = ahead;
+            ahead = crow >= 0;
+            if (keys) paged_key_load<D>(p, smem_addr(kbuf[warp][half]), crow, lane);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            half ^= 1u;
         }
         if (PAGED ? crow >= 0 : t < p.n) load_value_lane<D, VB>(p, crow, part, nw, nsc);
     };
-    if (item < p.items) load_tile(item);
-    for (; item < p.items; item += W) {
+    if (item < end) load_tile(item);
+    for (; item < end; item += W) {
         uint32_t w[2 * VB], sc = nsc;
 #pragma unroll
         for (int k = 0; k < 2 * VB; ++k) w[k] = nw[k];
@@ -411,18 +452,18 @@ __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __g
         int64_t t, crow;
         uint32_t bh;
         locate(item, t, crow, bh);
-        if constexpr (PAGED) crow = ahead;
         const bool valid = t < n;
         KeyTile kt;
-        uint32_t ksz[2];
-        const bool keys = p.k_out != nullptr;
-        if (keys) {
-            if constexpr (PAGED) paged_key_load<D>(p, smem_addr(kbuf[warp]), crow, lane, ksz);
-            else key_tile_load<D>(p, bh, t - r, lane, kt);
+        if (!PAGED && keys) key_tile_load<D>(p, bh, t - r, lane, kt);
+        if (item + W < end) {
+            load_tile(item + W);
+        } else if constexpr (PAGED) {
+            here = ahead;
+            asm volatile("cp.async.commit_group;" ::: "memory");  // (so that all but the last group is always this tile's)
+            half ^= 1u;
         }
-        if (item + W < p.items) load_tile(item + W);
         float2 P[32];
-        if (PAGED ? crow >= 0 : valid) {
+        if (PAGED ? here : valid) {
             const float s0 = f16_bits_to_f32((uint16_t)(sc & 0xFFFFu)), s1 = f16_bits_to_f32((uint16_t)(sc >> 16));
             const float2 s2 = make_float2(s0, s1);
 #pragma unroll
@@ -476,8 +517,14 @@ __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __g
             }
         }
         if (keys) {
-            if constexpr (PAGED) paged_key_store<D, F32>(p, kbuf[warp], bh, t - r, n, lane, ksz);
-            else key_tile_store<D, F32>(p, bh, t - r, lane, kt);
+            if constexpr (PAGED) {
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                __syncwarp();
+                paged_key_store<D, F32>(p, kbuf[warp][half], bh, t - r, n, lane);
+                __syncwarp();
+            } else {
+                key_tile_store<D, F32>(p, bh, t - r, lane, kt);
+            }
         }
     }
 }
