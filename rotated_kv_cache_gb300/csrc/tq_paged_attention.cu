@@ -57,8 +57,8 @@ __device__ __forceinline__ float pc_ex2(float x)
 
 // W warps per (token, q-head) row; lane holds dims PER lane .. + PER - 1.
 // Warp w of a row takes its unit's segments w, w + W, ...: their (max, sum)
-// pairs one a lane, 32 at a time, then their output rows with independent
-// loads; the row's first warp merges the warps' results, divides, un-rotates
+// pairs one a lane, 32 at a time, and their output rows with independent
+// loads, the first ones under way with the pairs; the row's first warp merges the warps' results, divides, un-rotates
 // (log2 d butterfly stages) and rounds once to bf16.  It moves one partial row
 // per segment and does nothing else of size: bound by the latency of two
 // dependent loads, so few rows take many warps (host rule below).
@@ -74,16 +74,25 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
     pdl_allow_dependents();
     bool live = row < p.rows;
     int64_t t = live ? row / p.QH : 0;
-    const int qh = (int)(row - t * p.QH);
-    int s = 0;
+    const int qh = (int)(row - t * p.QH), h = qh / p.G;
+    int s = 0, col = 0;
     int64_t n = 0, len = 0, s0 = 0;
+    PagedUnit unit{0, 0};  // slots of the row's unit: first .. first + count - 1
+    auto load_unit = [&](int64_t i) {  // of token i of sequence s
+        col = (int)i * p.G + (qh - h * p.G);
+        const int hb = col / p.CB;
+        if (hb < p.pg.blocks) unit = p.pg.units[((int64_t)s * p.H + h) * p.pg.blocks + hb];
+        col -= hb * p.CB;
+    };
     if (live && p.per_seq > 0) {
-        s = (int)(t / p.per_seq);
+        s = (int)((uint32_t)t / (uint32_t)p.per_seq);
+        t -= (int64_t)s * p.per_seq;
+        load_unit(t);  // (under way with the lengths; written only where there are any)
         s0 = paged_start(p.pg.v, s);
         n = paged_new(p.pg.v, s);
         len = paged_len(p.pg.v, s);
-        t += s0 - (int64_t)s * p.per_seq;
-        live = n <= p.pg.wide && t < s0 + n;
+        live = n <= p.pg.wide && t < n;
+        t += s0;
     } else if (live) {
         int lo = 0, hi = p.pg.v.seqs + 1;
         while (lo < hi) {
@@ -98,25 +107,24 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
             n = paged_new(p.pg.v, s);
             len = paged_len(p.pg.v, s);
             live = n <= p.pg.wide && t < s0 + n;
+            if (live) load_unit(t - s0);
         }
     }
     if (W == 1 && !live) return;  // no barrier below when W = 1
-    int64_t first = 0;            // slots of the unit's segments: first .. first + segs - 1
-    int segs = 0, col = 0;
-    if (live && len > 0) {
-        const int h = qh / p.G;
-        col = (int)((t - s0) * p.G + (qh - h * p.G));
-        const int hb = col / p.CB;
-        if (hb < p.pg.blocks) {
-            const PagedUnit u = p.pg.units[((int64_t)s * p.H + h) * p.pg.blocks + hb];
-            first = u.first;
-            segs = u.count;
-        }
-        col %= p.CB;
-        if (first + segs > p.pg.slots) segs = 0;  // starts out of order
-    }
+    const bool some = live && len > 0 && unit.first + unit.count <= p.pg.slots;  // (more: starts out of order)
+    const int64_t first = unit.first;
+    const int segs = some ? unit.count : 0;
     const int mine = segs > wid ? (segs - wid + W - 1) / W : 0;
     auto part = [&](int j) { return (first + wid + (int64_t)W * j) * p.CB + col; };
+    // the first rows are under way with their (max, sum) pairs
+    constexpr int KF = PER <= 4 ? 4 : 2;
+    float v[KF][PER];
+#pragma unroll
+    for (int j = 0; j < KF; ++j) {
+        const float *src = p.part_o + part(j) * D + PER * lane;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) v[j][k] = j < mine ? src[k] : 0.0f;
+    }
     float m = -INFINITY, l = 0.0f, x[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) x[k] = 0.0f;
@@ -133,8 +141,15 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
 #pragma unroll
         for (int k = 0; k < PER; ++k) x[k] *= keep;
         const int cnt = mine - j0 < 32 ? mine - j0 : 32;
+        if (j0 == 0)
+#pragma unroll
+            for (int j = 0; j < KF; ++j) {
+                const float w = __shfl_sync(0xffffffffu, wt, j);  // (0 past the last)
+#pragma unroll
+                for (int k = 0; k < PER; ++k) x[k] += v[j][k] * w;
+            }
 #pragma unroll 4
-        for (int j = 0; j < cnt; ++j) {
+        for (int j = j0 == 0 ? KF : 0; j < cnt; ++j) {
             const float w = __shfl_sync(0xffffffffu, wt, j);
             const float *src = p.part_o + part(j0 + j) * D + PER * lane;
 #pragma unroll

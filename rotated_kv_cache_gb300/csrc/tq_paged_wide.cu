@@ -931,7 +931,7 @@ cudaError_t wide_run(WideParams &p, cudaStream_t s)
     if (e != cudaSuccess) return e;
     e = launch_dependent(wide_attend_kernel<D>, dim3((unsigned)p.ctas), dim3(wThreads), A::SMEM, s, p);
     if (e != cudaSuccess) return e;
-    return launch_dependent(wide_merge_kernel<D>, dim3((unsigned)p.ctas, 8), dim3(256), 0, s, p);
+    return launch_dependent(wide_merge_kernel<D>, dim3((unsigned)p.ctas, wC / 8), dim3(256), 0, s, p);
 }
 
 }  // namespace
