@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
         }
     }
     if (W == 1 && !live) return;  // no barrier below when W = 1
-    const bool some = live && len > 0 && unit.first + unit.count <= p.pg.slots;  // (more: starts out of order)
+    // (a unit without a segment, or beyond the slots: starts out of order)
+    const bool some = live && len > 0 && unit.first >= 0 && unit.count > 0 && unit.count <= p.pg.slots - unit.first;
     const int64_t first = unit.first;
     const int segs = some ? unit.count : 0;
     const int mine = segs > wid ? (segs - wid + W - 1) / W : 0;
