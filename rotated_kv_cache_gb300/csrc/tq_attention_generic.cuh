@@ -1085,8 +1085,9 @@ int gen_layout(const CacheView &c, GenPlan &pl)
     pl.smem = 1024 /*align slack*/ + ring + A::QF + A::QS + (pl.vlut == 0 ? 512 : 0) /*lut*/ +
               gMaxStages * 12 /*barriers, counters*/;
     // the opt-in and the occupancy of an instantiation are looked up once per shared-memory size
+    static std::atomic<uint64_t> table[3][3];  // [VLUT][KEY]: smem << 32 | CTAs; same on every GB300
+    std::atomic<uint64_t> &known = table[pl.vlut == 0 ? 0 : pl.vlut - 1][pl.key / 4];
     return gen_dispatch<D, NB, PAGED>(pl, [&](auto kern) {
-        static std::atomic<uint64_t> known{0};  // smem << 32 | CTAs; same on every GB300
         const uint64_t k = known.load(std::memory_order_relaxed);
         if (k >> 32 == (uint64_t)pl.smem) return (int)(uint32_t)k;
         int n = 0;

@@ -228,6 +228,117 @@ def test_more_new_tokens_than_rows(cuda):
     check_attention(b, pool, torch.cat([q[2:5], q[7:]]), torch.cat([out[2:5], out[7:]]))
 
 
+def test_a_long_chunk_with_more_tokens_than_rows(cuda):
+    """The same on the wide kernel: 200 new tokens of 150 rows, beside a sequence of its own."""
+    b = Batch([150, 90], [150, 1], H=2, d=128, kb=8, vb=3, page=32)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = b.queries(8, total=201)
+    out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(np.array([0, 200, 201], np.int32)), q.cuda(), 200)
+    assert not bool(out[:50].any())
+    check_attention(b, pool, q[50:], out[50:])
+
+
+def test_broadcast_and_reversed_inputs(cuda):
+    """One K, V head expanded over all kv-heads (stride 0), as multi-query models have them."""
+    b = Batch([40, 70], [40, 70], H=4, d=128, kb=4, vb=4, page=16)
+    for x in (b.k, b.v):
+        for s in range(2):
+            x[s] = x[s][:, :1].expand(-1, 4, -1).contiguous()
+    pool, other = b.pool(cuda), b.pool(cuda)
+    k, v = b.tokens(b.k, b.new).cuda(), b.tokens(b.v, b.new).cuda()
+    cuda.tq_paged_append(pool, b.pages(cuda), b.dev(b.starts), k, v)
+    cuda.tq_paged_append(other, b.pages(cuda), b.dev(b.starts), k[:, :1].expand(-1, 4, -1), v[:, :1].expand(-1, 4, -1))
+    for x, y in zip(pool.planes(), other.planes()):
+        assert torch.equal(x, y)
+    # a query head expanded over a group
+    q = b.queries(1)
+    out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q.cuda().expand(-1, 8, -1), 70)
+    check_attention(b, pool, q.expand(-1, 8, -1), out)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.09, 1e-6, 0.7])
+@pytest.mark.parametrize("new", [1, 3, 140])
+def test_softmax_scales(cuda, scale, new):
+    """Zero (equal weights), negative, tiny and large ones; the last concentrates the weights on a few rows."""
+    b = Batch([260, 140], [new, min(new, 140)], H=2, d=128, kb=8, vb=3, page=64, seed=31)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = (b.queries(8).float() * 0.2).to(torch.bfloat16)
+    out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q.cuda(), new, softmax_scale=scale)
+    check_attention(b, pool, q, out, scale=scale)
+
+
+@pytest.mark.parametrize("new", [2, 130])
+def test_sizes_far_from_one(cuda, new):
+    """Values of 2^-10 and of 2^12, one sequence each, a row of zeros among them, keys of 2^9 against queries of
+    2^-9: powers of two, so that outputs are those of ordinary sizes scaled."""
+    ref = Batch([200, 300], [new, new], H=2, d=128, kb=8, vb=3, page=64, seed=41)
+    b = Batch([200, 300], [new, new], H=2, d=128, kb=8, vb=3, page=64, seed=41)
+    size = (2.0 ** -10, 2.0 ** 12)
+    for s in range(2):
+        ref.v[s][7], b.v[s][7] = 0, 0
+        b.k[s] = b.k[s] * 2.0 ** 9
+        b.v[s] = b.v[s] * size[s]
+    outs = []
+    for x, f in ((ref, 1.0), (b, 2.0 ** -9)):
+        pool = x.pool(cuda)
+        x.fill(cuda, pool)
+        q = x.queries(8) * f
+        outs.append(cuda.tq_paged_attention(pool, x.pages(cuda), x.dev(x.starts), q.cuda(), new).float().cpu())
+        if f == 1.0:
+            check_attention(x, pool, q, outs[0].to(torch.bfloat16))
+    # the values' group scales of 2^-10 sizes stay normal fp16 numbers, so their codes are the same; the rms + 1e-8
+    # of the index and the fp16 rounding of scales change nothing at powers of two but a code next to a border
+    for s in range(2):
+        a, c = outs[0][s * new:(s + 1) * new], outs[1][s * new:(s + 1) * new] / size[s]
+        assert ((a - c).abs() <= 2 * 2.0 ** -8 * a.abs() + 2 * 2e-3).all()
+
+
+def test_a_total_that_the_lengths_pass(cuda):
+    """Lengths of more than total_len in all: recorded, and nothing outside the workspace is touched."""
+    b = Batch([700, 800], [200, 300], H=2, d=128, kb=8, vb=3, page=64)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = b.queries(8).cuda()
+    exact = cuda.PageTable(b.dev(b.table), b.dev(np.array(b.lens, np.int32)), 800, total_len=1500)
+    out = cuda.tq_paged_attention(pool, exact, b.dev(b.starts), q, 300)
+    check_attention(b, pool, q.cpu(), out)
+    assert cuda.tq_device_error() == 0
+    small = cuda.PageTable(b.dev(b.table), b.dev(np.array(b.lens, np.int32)), 800, total_len=600)
+    cuda.tq_paged_attention(pool, small, b.dev(b.starts), q, 300)
+    assert cuda.tq_device_error() == cuda.TQ_DEVICE_ERR_LENGTH
+
+
+def test_results_repeat(cuda):
+    """No order of arrival enters a result: the same call gives the same bits."""
+    b = Batch([3000, 17, 900, 2000], [1, 1, 3, 400], H=2, d=128, kb=4, vb=3, page=32, seed=51)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = b.queries(16).cuda()
+    outs = [cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q, 400) for _ in range(5)]
+    assert all(torch.equal(outs[0], x) for x in outs[1:])
+
+
+def test_calls_on_two_streams_at_once(cuda):
+    """Two batches over one pool, each on a stream of its own, its workspace of its own."""
+    b = Batch([900, 500], [1, 200], H=2, d=128, kb=8, vb=3, page=64, seed=61)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = b.queries(8).cuda()
+    want = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q, 200)
+    pages, starts = b.pages(cuda), b.dev(b.starts)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for s, g in zip(streams, got):
+            g.append(cuda.tq_paged_attention(pool, pages, starts, q, 200, stream=s))
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(x, want) for x in g)
+
+
 def test_shared_pages(cuda):
     """Two sequences over one prefix: the same page numbers in both rows of the table."""
     b = Batch([160, 130], [1, 1], H=2, d=128, kb=8, vb=3, page=64)

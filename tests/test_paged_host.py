@@ -113,47 +113,89 @@ def test_binding_refusals_on_the_host(tqlib):
         tqlib.Cache.from_planes(*[torch.zeros(2, 1, 16, 5, dtype=torch.uint8)] * 5, head_dim=64)
 
 
-def _schedule(lens, new, H, G, ST, CB, ctas):
-    """The split kernels' line of stages: per CTA its segments (sequence, kv-head, block, first stage, count, slot)."""
+def _schedule(lens, new, H, G, ST, CB, ctas, seg_start=2):
+    """The split kernels' line: per CTA its segments (sequence, kv-head, block, first stage, count, slot), and per
+    unit the word that its first segment leaves (first slot, segments)."""
     units = []  # (sequence, kv-head, block, stages)
     for s, (n, m) in enumerate(zip(lens, new)):
         if n and m:
             units += [(s, h, b, -(-n // ST)) for h in range(H) for b in range(-(-(m * G) // CB))]
-    total = sum(u[3] for u in units)
-    per = max(1, -(-total // ctas))
-    out, at = {}, 0
-    for i, (s, h, b, stages) in enumerate(units):
+    stages = sum(u[3] for u in units)
+    start = 0 if stages <= ctas else seg_start
+    per = max(start + 1, -(-(stages + start * len(units)) // ctas))
+    out, words, at = {}, [], 0
+    for i, (s, h, b, n) in enumerate(units):
+        at += start  # its first stage
         x = at
-        while x < at + stages:
+        words.append((at // per + i, (at + n - 1) // per - at // per + 1))
+        while x < at + n:
             c = x // per
-            count = min(at + stages, (c + 1) * per) - x
+            count = min(at + n, (c + 1) * per) - x
             out.setdefault(c, []).append((s, h, b, x - at, count, c + i))
             x += count
-        at += stages
-    return out, len(units), per
+        at += n
+    return out, words
 
 
-@pytest.mark.parametrize("seed", range(6))
+@pytest.mark.parametrize("seed", range(8))
 def test_schedule_slots_are_distinct_and_bounded(seed):
     rng = np.random.default_rng(seed)
     S, H, G = int(rng.integers(1, 40)), int(rng.integers(1, 9)), int(rng.integers(1, 17))
-    lens = rng.integers(0, 5000, S) * (rng.random(S) > 0.2)
+    lens = rng.integers(0, 5000 if seed < 6 else 70, S) * (rng.random(S) > 0.2)
     new = np.minimum(lens, rng.integers(0, 6, S))
     ST, CB, ctas = 64, 8, int(rng.integers(1, 1300))
-    segs, units, per = _schedule(lens, new, H, G, ST, CB, ctas)
+    segs, words = _schedule(lens, new, H, G, ST, CB, ctas)
+    units = len(words)
     assert all(c < ctas for c in segs)
     flat = [x for c in sorted(segs) for x in segs[c]]
     slots = [x[5] for x in flat]
     assert slots == sorted(set(slots))                     # distinct, growing along the line
     assert not slots or slots[-1] < ctas + units           # what the workspace has room for
     assert units <= H * (int(new.sum()) * G // CB + S)     # the host's bound of the units
-    # every unit's segments are consecutive slots, as the combine reads them
+    # every unit's segments are consecutive slots, and the word of its first one names them
     seen = {}
     for s, h, b, first, count, slot in flat:
         seen.setdefault((s, h, b), []).append((first, count, slot))
-    for (s, h, b), parts in seen.items():
+    for ((s, h, b), parts), word in zip(seen.items(), words):
         assert parts[0][0] == 0 and sum(p[1] for p in parts) == -(-int(lens[s]) // ST)
-        assert [p[2] for p in parts] == list(range(parts[0][2], parts[0][2] + len(parts)))
+        assert [p[2] for p in parts] == list(range(word[0], word[0] + word[1]))
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_wide_line_covers_every_block_once(seed):
+    """The wide kernel's line: each run's tiles of a block from its first tile on, shares in two slots a CTA, and the
+    CTA that begins a block knowing the last one that has a share."""
+    rng = np.random.default_rng(100 + seed)
+    tiles = [int(x) for x in rng.integers(1, 60, int(rng.integers(1, 200)))]
+    start, ctas = 7, int(rng.integers(1, 160))
+    total = sum(tiles) + start * len(tiles)
+    per = max(start, -(-total // ctas))
+    firsts, at = [], 0
+    for n in tiles:
+        firsts.append(at + start)
+        at += start + n
+    done = [0] * len(tiles)
+    used, shares = set(), {}
+    for c in range(ctas):
+        x0, x1 = c * per, min(total, (c + 1) * per)
+        for b, n in enumerate(tiles):
+            if firsts[b] + n <= x0 or firsts[b] - start >= x1:
+                continue
+            lo, hi = max(0, x0 - firsts[b]), min(n, x1 - firsts[b])
+            if hi <= lo:
+                continue
+            assert done[b] == lo
+            done[b] = hi
+            if hi - lo < n:  # a share: slot 2 c of a CTA that goes on with the block, 2 c + 1 of the one that begins it
+                slot = 2 * c + (lo == 0)
+                assert slot not in used
+                used.add(slot)
+                shares.setdefault(b, []).append(slot)
+    assert done == tiles
+    for b, slots in shares.items():
+        c = slots[0] // 2
+        last = (firsts[b] + tiles[b] - 1) // per
+        assert slots == [2 * c + 1] + [2 * k for k in range(c + 1, last + 1)]
 
 
 @pytest.mark.parametrize("stage", [64, 96, 128])
