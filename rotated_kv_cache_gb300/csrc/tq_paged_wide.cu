@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
     const uint32_t kfull = b0, kempty = kfull + 8 * NK, vfull = kempty + 8 * NK, vempty = vfull + 8 * NV;
     const uint32_t qfull = vempty + 8 * NV, sfull = qfull + 16, pfull = sfull + 16, ofull = pfull + 32,
                    drained = ofull + 16;  // pfull: first halves, then second halves
-    __shared__ WidePlace place[2];
+    __shared__ WidePlace place[2][2];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     pdl_wait_primary();
@@ -571,13 +571,13 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
         bool ok = true;
         uint32_t it = 0, seg = 0;
         int shared_from = -1;  // thread 0: the block of the last segment, if it is begun here and not finished
-        // the place is kept in shared memory, out of the registers that hold scores: the group's
-        // first thread moves it on
-        WidePlace &w = place[g];
-        if (ltid == 0) w = wide_locate(p, x0);
+        // the place is kept in shared memory, out of the registers that hold scores, and the next
+        // one worked out by the group's first thread while the first scores are awaited
+        if (ltid == 0) place[g][0] = wide_locate(p, x0);
         for (;; ++seg) {
             // the place is written, and no wait of the group has given up: all leave together
             if (!named_and(1 + g, 128, ok)) break;
+            const WidePlace &w = place[g][seg & 1];
             const int n = w.count(x1);
             if (n <= 0) break;
             const int cols = (int)w.n * p.G, col = (w.e - w.e0) * wC + 128 * g + ltid;  // total * QH < 2^30
@@ -621,6 +621,11 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull + 8 * g);
+            if (ltid == 0 && !w.ends(x1)) {  // (the other place was last read before this segment's barrier)
+                WidePlace next = w;
+                wide_next(p, next);
+                place[g][(seg + 1) & 1] = next;
+            }
             if (col + wC < cols) {  // the next block's q on its way to L2
                 const int nt = (col + wC) / p.G;
                 const uint16_t *a = p.q + (w.s0 + nt) * p.pg.q_token + ((int64_t)w.h * p.G + (col + wC - nt * p.G)) * p.pg.q_head;
@@ -826,8 +831,6 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
             }
             tc_fence_before();
             if (w.ends(x1)) break;
-            named_and(1 + g, 128, true);  // all have read the place
-            if (ltid == 0) wide_next(p, w);
         }
         if (tid == 0 && shared_from < 0) p.pl.share[blockIdx.x].last = -1;
     }
