@@ -132,7 +132,7 @@ def _check(status: int, what: str) -> None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -241,6 +241,7 @@ class PageTable:
         stride = pages.stride(0) if self.num_seqs > 1 else self.width
         if stride < self.width:
             raise ValueError("the rows of the page table overlap")
+        self._device = pages.get_device()
         self._struct = _PageTableStruct(pages.data_ptr(), seq_lens.data_ptr(), stride, self.max_len, self.total_len,
                                         self.num_seqs, 0)
 
@@ -472,39 +473,44 @@ def _empty_on(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _paged_args(pool: Cache, table: PageTable, starts: torch.Tensor, *tensors):
-    """Checks shared by the paged calls: the starts' form, and one device, the current one, for all."""
-    if starts.dtype != torch.int32 or starts.dim() != 1 or starts.shape[0] != table.num_seqs + 1 or \
+def _paged_check(pool: Cache, table: PageTable, starts: torch.Tensor, *tensors):
+    """Checks shared by the paged calls: the starts' form, one device, the current one, for all; the
+    C ABI's views of pool and table by reference."""
+    if starts.dtype is not torch.int32 or starts.dim() != 1 or starts.shape[0] != table.num_seqs + 1 or \
             not starts.is_contiguous():
         raise ValueError("starts must be contiguous int32 [num_seqs + 1]")
     dev = pool.k_codes.get_device()
     if dev < 0:
         raise ValueError("tensors must live on a CUDA device")
-    for t in (table._pages, starts, *tensors):
+    if table._device != dev or starts.get_device() != dev:
+        raise ValueError("the pool, the page table and the tensors must be on one device")
+    for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError("the pool, the page table and the tensors must be on one device")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError("the tensors are on another device than the current one")
-    return pool.struct(), table.struct(pool)
+    return ctypes.byref(pool.struct()), ctypes.byref(table.struct(pool))
 
 
 def _ragged_strides(x: torch.Tensor, heads: int | None, d: int, what: str):
-    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[2] != d or (heads is not None and x.shape[1] != heads) or \
-            (d > 1 and x.stride(2) != 1):
+    shape, st = x.shape, x.stride()
+    if x.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != d or st[2] != 1 or \
+            (heads is not None and shape[1] != heads):
         raise ValueError(f"{what} must be bfloat16 [tokens][heads][head_dim] with head_dim contiguous, matching the pool")
-    return _TWO(x.stride(0), x.stride(1))
+    return _TWO(st[0], st[1])
 
 
 def tq_paged_append(pool: Cache, table: PageTable, starts: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                     stream=None) -> None:
     """Quantise the new tokens' K, V (bf16 [tokens][H][d], any token and head strides) into the pages
     of their sequences; sequence s owns token rows [starts[s], starts[s + 1]), its last rows."""
-    s, t = _paged_args(pool, table, starts, k, v)
-    if k.shape != v.shape:
+    ks = _ragged_strides(k, pool.num_kv_heads, pool.head_dim, "K and V")
+    vs = _ragged_strides(v, pool.num_kv_heads, pool.head_dim, "K and V")
+    if k.shape[0] != v.shape[0]:
         raise ValueError("K and V must have the same shape")
-    ks, vs = (_ragged_strides(x, pool.num_kv_heads, pool.head_dim, "K and V") for x in (k, v))
-    _check(lib().tq_paged_append(ctypes.byref(s), ctypes.byref(t), starts.data_ptr(), int(k.shape[0]), k.data_ptr(), ks,
-                                 v.data_ptr(), vs, _stream(stream)), "tq_paged_append")
+    s, t = _paged_check(pool, table, starts, k, v)
+    _check(lib().tq_paged_append(s, t, starts.data_ptr(), k.shape[0], k.data_ptr(), ks, v.data_ptr(), vs,
+                                 _stream(stream)), "tq_paged_append")
 
 
 def tq_paged_decode(pool: Cache, table: PageTable, starts: torch.Tensor, total: int, dtype=torch.bfloat16,
@@ -513,22 +519,20 @@ def tq_paged_decode(pool: Cache, table: PageTable, starts: torch.Tensor, total: 
     """The last starts[s + 1] - starts[s] rows of every sequence as (K, V), [total][H][d] of `dtype`."""
     code = _dtype_code(dtype)
     shape = (int(total), pool.num_kv_heads, pool.head_dim)
-    dev = pool.k_codes.device
     for x in (k_out, v_out):
         if x is not None and (x.dtype != dtype or tuple(x.shape) != shape or not x.is_contiguous()):
             raise ValueError("decode outputs must be contiguous [total][H][d] of the requested dtype")
-    s, t = _paged_args(pool, table, starts, k_out, v_out)
+    s, t = _paged_check(pool, table, starts, k_out, v_out)
     if not want_k:
         k_out = None
     elif k_out is None:
-        k_out = _empty_on(stream, shape, dtype, dev)
+        k_out = _empty_on(stream, shape, dtype, pool.k_codes.device)
     if not want_v:
         v_out = None
     elif v_out is None:
-        v_out = _empty_on(stream, shape, dtype, dev)
-    _check(lib().tq_paged_decode(ctypes.byref(s), ctypes.byref(t), starts.data_ptr(), int(total), code,
-                                 k_out.data_ptr() if want_k else None, v_out.data_ptr() if want_v else None,
-                                 _stream(stream)), "tq_paged_decode")
+        v_out = _empty_on(stream, shape, dtype, pool.k_codes.device)
+    _check(lib().tq_paged_decode(s, t, starts.data_ptr(), shape[0], code, k_out.data_ptr() if want_k else None,
+                                 v_out.data_ptr() if want_v else None, _stream(stream)), "tq_paged_decode")
     return k_out, v_out
 
 
@@ -545,20 +549,19 @@ def tq_paged_attention(pool: Cache, table: PageTable, starts: torch.Tensor, q: t
     max_new of one sequence) over their sequences' rows -> bf16 [tokens][QH][d]."""
     qs = _ragged_strides(q, None, pool.head_dim, "q")
     total, QH, d = q.shape
-    if out is not None and (out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous()):
+    if out is not None and (out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous()):
         raise ValueError("out must be contiguous bfloat16, shaped like q")
-    s, t = _paged_args(pool, table, starts, q, out, workspace)
+    s, t = _paged_check(pool, table, starts, q, out, workspace)
     if out is None:
-        out = _empty_on(stream, (total, QH, d), torch.bfloat16, q.device)
+        out = torch.empty_like(q) if stream is None and q.is_contiguous() else \
+            _empty_on(stream, (total, QH, d), torch.bfloat16, q.device)
     if workspace is None and total > 0:
         need = tq_paged_attention_workspace_bytes(pool, table, QH, total, max_new)
         workspace = _empty_on(stream, need, torch.uint8, q.device)
     scale = (1.0 / d ** 0.5) if softmax_scale is None else float(softmax_scale)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().tq_paged_attention(ctypes.byref(s), ctypes.byref(t), starts.data_ptr(), int(total), int(max_new),
-                                    q.data_ptr(), qs, int(QH), scale, out.data_ptr(),
-                                    workspace.data_ptr() if workspace is not None else None, ws_bytes,
-                                    _stream(stream)), "tq_paged_attention")
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    _check(lib().tq_paged_attention(s, t, starts.data_ptr(), total, int(max_new), q.data_ptr(), qs, QH, scale,
+                                    out.data_ptr(), ws_ptr, ws_bytes, _stream(stream)), "tq_paged_attention")
     return out
 
 
