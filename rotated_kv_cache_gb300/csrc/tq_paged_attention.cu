@@ -227,14 +227,24 @@ struct PagedPlan {
 };
 
 // A sequence with at least this many columns (new tokens x q-heads of a
-// kv-head) is wide.
+// kv-head) is wide, unless the whole batch is little work: the split kernel's
+// time grows with rows x columns from nothing, the wide kernels' with rows from
+// about 38 us (three launches more, a tile's first pass through the pipeline).
+// Measured with 8-bit keys, 3-bit values, 8 kv-heads, head_dim 128 (64):
+//   one sequence of 32768 rows   64 columns   split 81.4 us (50.8)  wide 98.9 (71.2)
+//                               128                147.2    (87.1)       98.5 (74.6)
+//   one sequence of 2048 rows   128                 21.1                 38.7
+//                               512                 48.8                 40.5
 constexpr int64_t kWideColumns = 128;
+constexpr int64_t kWideWork = int64_t(1) << 22;  // rows x kv-heads x columns, by the bounds that the host has
 
 bool paged_plan(const CacheView &c, const PagedBounds &bounds, int QH, PagedPlan &pl)
 {
     const int64_t G = QH / c.H;
     pl.b = bounds;
-    pl.b.wide = paged_wide_applies(c) && pl.b.max_new * G >= kWideColumns ? (kWideColumns - 1) / G : INT32_MAX;
+    const int64_t most = pl.b.max_new * G;  // columns of the largest sequence
+    const bool work = most >= kWideColumns && pl.b.total_len >= (kWideWork + c.H * most - 1) / (c.H * most);
+    pl.b.wide = paged_wide_applies(c) && work ? (kWideColumns - 1) / G : INT32_MAX;
     const bool wide = pl.b.wide != INT32_MAX;
     pl.cols = (wide ? (pl.b.wide > 0 ? pl.b.wide : 1) : pl.b.max_new) * G;
     // the specialised kernel where it has the widths (its tensor copies count rows in 32 bits)

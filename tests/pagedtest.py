@@ -24,7 +24,10 @@ class Batch:
         counts = [-(-n // page) for n in lens]
         self.num_pages = sum(counts) + spare
         order = rng.permutation(self.num_pages).astype(np.int32)
-        self.width = width or max(1, max(counts))
+        # a bound of the lengths that lets chunks of 128 columns take the kernels of long chunks (4 Mi rows x kv-heads x
+        # columns in all); a bound given with pages() may be closer
+        self.bound = max(max(lens), 1, -(-(1 << 22) // (128 * H * len(lens))))
+        self.width = width or -(-self.bound // page)
         self.table = np.zeros((len(lens), self.width), np.int32)
         at = 0
         for s, c in enumerate(counts):
@@ -54,7 +57,7 @@ class Batch:
 
     def pages(self, tq, lens=None, max_len=None):
         lens = self.lens if lens is None else lens
-        return tq.PageTable(self.dev(self.table), self.dev(np.array(lens, np.int32)), max_len or max(max(self.lens), 1))
+        return tq.PageTable(self.dev(self.table), self.dev(np.array(lens, np.int32)), max_len or min(self.bound, self.width * self.page))
 
     def fill(self, tq, pool, lens=None):
         """Append every row, as one chunk of each sequence."""

@@ -131,15 +131,26 @@ def test_verification_shapes(cuda, d, kb, vb, G, page, new):
     _attend(cuda, b, 2 * G)
 
 
-@pytest.mark.parametrize("d,kb,vb,G,page,lens,new", [
+CHUNKS = [
     (128, 8, 3, 8, 64, [300], [300]), (128, 4, 3, 8, 16, [1000, 5, 200], [130, 1, 200]),
     (128, 8, 4, 4, 32, [129, 700, 1, 0, 513], [129, 1, 1, 0, 257]), (64, 8, 4, 4, 32, [640, 90, 1000], [512, 1, 77]),
     (64, 4, 2, 1, 48, [515], [388]), (64, 8, 3, 16, 64, [100, 129], [40, 129]), (128, 5, 2, 3, 16, [444, 100], [150, 99]),
     (128, 2, 5, 8, 256, [300], [100]), (256, 8, 3, 4, 64, [400, 33], [140, 33]), (512, 4, 4, 2, 32, [200], [90]),
     (128, 8, 3, 7, 64, [391], [255]), (128, 8, 8, 8, 64, [257], [256]),
-])
+]
+
+
+@pytest.mark.parametrize("d,kb,vb,G,page,lens,new", CHUNKS)
 def test_chunk_shapes(cuda, d, kb, vb, G, page, lens, new):
     b = Batch(lens, new, H=2, d=d, kb=kb, vb=vb, page=page, seed=sum(lens))
+    _attend(cuda, b, 2 * G)
+
+
+@pytest.mark.parametrize("d,kb,vb,G,page,lens,new", CHUNKS)
+def test_short_chunks(cuda, d, kb, vb, G, page, lens, new):
+    """The same under close bounds: little work in all, which the split kernels take however many columns there are."""
+    b = Batch(lens, new, H=2, d=d, kb=kb, vb=vb, page=page, seed=sum(lens))
+    b.bound = max(lens)
     _attend(cuda, b, 2 * G)
 
 
@@ -296,11 +307,12 @@ def test_sizes_far_from_one(cuda, new):
 
 
 def test_a_total_that_the_lengths_pass(cuda):
-    """Lengths of more than total_len in all: recorded, and nothing outside the workspace is touched."""
-    b = Batch([700, 800], [200, 300], H=2, d=128, kb=8, vb=3, page=64)
+    """Lengths of more than total_len in all, where the workspace is sized by it (4 Mi rows x kv-heads x columns and
+    more): recorded, and nothing outside the workspace is touched."""
+    b = Batch([700, 800], [200, 300], H=8, d=128, kb=8, vb=3, page=64)
     pool = b.pool(cuda)
     b.fill(cuda, pool)
-    q = b.queries(8).cuda()
+    q = b.queries(32).cuda()
     exact = cuda.PageTable(b.dev(b.table), b.dev(np.array(b.lens, np.int32)), 800, total_len=1500)
     out = cuda.tq_paged_attention(pool, exact, b.dev(b.starts), q, 300)
     check_attention(b, pool, q.cpu(), out)
@@ -462,3 +474,28 @@ def test_bad_pages_and_lengths_are_reported(cuda):
     # starts out of order: more segments than there can be, none of them written outside the workspace
     cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(np.array([0, 2, 0], np.int32)), q.cuda(), 2)
     assert cuda.tq_device_error() & cuda.TQ_DEVICE_ERR_LENGTH
+
+
+def test_bad_pages_and_lengths_of_long_chunks(cuda):
+    """The same for chunks of more than 128 columns, on the kernels that expand their rows first."""
+    b = Batch([300, 150], [200, 130], H=2, d=128, kb=8, vb=3, page=32, seed=8)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = b.queries(8)
+    good, starts = b.table.copy(), b.dev(b.starts)
+    check = lambda out: check_attention(b, pool, q[200:], out[200:], lens=[0, 150], new=[0, 130])  # noqa: E731
+    assert cuda.tq_device_error() == 0
+    for bad in (b.num_pages, -1, 2 ** 31 - 1):
+        b.table = good.copy()
+        b.table[0, 3] = bad
+        out = cuda.tq_paged_attention(pool, b.pages(cuda), starts, q.cuda(), 200)
+        assert cuda.tq_device_error() == cuda.TQ_DEVICE_ERR_PAGE
+        b.table = good
+        check(out)
+    out = cuda.tq_paged_attention(pool, b.pages(cuda, lens=[b.bound + 1, 150]), starts, q.cuda(), 200)
+    assert cuda.tq_device_error() == cuda.TQ_DEVICE_ERR_LENGTH
+    check(out)
+    # starts out of order: the second sequence has no tokens, the first one's results stand
+    out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(np.array([0, 200, 100], np.int32)), q.cuda(), 200)
+    assert cuda.tq_device_error() == cuda.TQ_DEVICE_ERR_LENGTH
+    check_attention(b, pool, q[:200], out[:200], new=[200, 0])
