@@ -355,6 +355,9 @@ __device__ __forceinline__ void paged_key_store(const ValueDecodeParams &p, cons
 // A warp takes every (grid kVWarps)-th tile of rows; in paged launches a run
 // of consecutive items, the kv-heads of one token tile after another (outputs
 // are [token][head][D]), so that it looks a tile's rows up once for its heads.
+// 4 x 8192 rows of 8 kv-heads, head_dim 128, 8-bit keys and 3-bit values, to
+// bf16: 39 us (a floor of 26; 46 with keys held in registers, whose prefetches
+// the look-ups' registers spilled).
 template <int D, int VB, bool F32, bool PAGED>
 __global__ void __launch_bounds__(kVWarps * 32, 4) decode_value_kernel(const __grid_constant__ ValueDecodeParams p)
 {

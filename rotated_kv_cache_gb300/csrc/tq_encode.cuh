@@ -637,7 +637,10 @@ __device__ __forceinline__ void encode_value_lane(const EncodeParams &p, const f
 
 // ------------------------------------------------------------------ kernels
 // The work of CTA `cta` of `ncta` encoding keys (KEY) or values.  A warp takes
-// every (ncta kWarps)-th item; in paged launches a run of consecutive ones.
+// every (ncta kWarps)-th item; in paged launches a run of consecutive ones, the
+// kv-heads of one token tile after another, so that a tile's rows are looked up
+// once for its heads.  32768 tokens of 8 kv-heads, head_dim 128, 8-bit keys:
+// 25 us, 3-bit values 35 us, each alone; issue-bound as the contiguous kernel is.
 template <int D, int BITS, bool KEY, bool PAGED>
 __device__ __forceinline__ void encode_body(const EncodeParams &p, const CUtensorMap &map, uint8_t *smem_raw,
                                             uint32_t cta, uint32_t ncta)
