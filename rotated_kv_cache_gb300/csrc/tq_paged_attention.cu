@@ -250,7 +250,9 @@ bool paged_plan(const CacheView &c, const PagedBounds &bounds, int QH, PagedPlan
     const int64_t G = QH / c.H;
     pl.b = bounds;
     const int64_t most = pl.b.max_new * G;  // columns of the largest sequence
-    const bool work = most >= kWideColumns && pl.b.total_len >= (kWideWork + c.H * most - 1) / (c.H * most);
+    // (and its tiles are counted in 32 bits, its workspace in 64: bounds far above any memory go to the split kernels)
+    const bool work = most >= kWideColumns && pl.b.total_len >= (kWideWork + c.H * most - 1) / (c.H * most) &&
+                      pl.b.total_len < (int64_t(1) << 37) / c.H;
     pl.b.wide = paged_wide_applies(c) && work ? (kWideColumns - 1) / G : INT32_MAX;
     const bool wide = pl.b.wide != INT32_MAX;
     pl.cols = (wide ? (pl.b.wide > 0 ? pl.b.wide : 1) : pl.b.max_new) * G;

@@ -207,3 +207,25 @@ def test_stage_chunks_never_cross_a_page(stage, page):
         for c in range(stage // ru):
             row = st * stage + c * ru
             assert row // page == (row + ru - 1) // page
+
+
+def test_bounds_above_any_memory(tqlib):
+    """Workspace sizes grow with the bounds and pass no integer's range: above 2^37 rows x kv-heads no expanded tiles
+    (512 bytes a row and kv-head at head_dim 128) are asked for, whose counts are 32-bit."""
+    L, ref = tqlib.lib(), ctypes.byref
+    pool = _struct(tqlib, batch=12)
+    H = pool.num_kv_heads
+
+    def size(seqs, max_len, total):
+        table = _table(tqlib, num_seqs=seqs, max_len=max_len, stride=1 << 32)
+        return L.tq_paged_attention_workspace_bytes(ref(pool), ref(table), 2 * H, total, total)
+
+    rows = 1 << 20
+    assert size(1, rows, 4096) > rows * H * 512
+    last = 0
+    for seqs, max_len in ((64, 1 << 20), (1 << 10, 1 << 24), (1 << 22, 1 << 30), (1 << 26, (1 << 31) - 1)):
+        new = size(seqs, max_len, 1 << 28)
+        assert last < new < 1 << 60
+        if seqs * max_len * H >= 1 << 37:
+            assert new < seqs * max_len * H
+        last = new
