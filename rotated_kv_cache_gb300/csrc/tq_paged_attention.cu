@@ -234,7 +234,7 @@ struct PagedPlan {
 // A sequence with at least this many columns (new tokens x q-heads of a
 // kv-head) is wide, unless the whole batch is little work: the split kernel's
 // time grows with rows x columns from nothing, the wide kernels' with rows from
-// about 38 us (three launches more, a tile's first pass through the pipeline).
+// about 36 us (three launches more, a tile's first pass through the pipeline).
 // Measured with 8-bit keys, 3-bit values, 8 kv-heads, head_dim 128 (64):
 //   one sequence of 32768 rows   64 columns   split 81.4 us (50.8)  wide 98.9 (71.2)
 //                               128                147.2    (87.1)       98.5 (74.6)

@@ -30,9 +30,9 @@
 //
 // Measured: 2048 new tokens over 32768 rows, 64 q-heads, 8 kv-heads, head_dim
 // 128, 4-bit keys, 3-bit values: 1484 us in all, 1.42 PFLOP/s (of 1.87 that a
-// large library product reaches); a prompt of 8191 tokens 412 us, 1.33.  At 1024
+// large library product reaches); a prompt of 8191 tokens 408 us, 1.35.  At 1024
 // tokens over 8192 rows the tensor pipe is busy 69 % of the attend kernel's
-// time (expand 19 us, attend 158, merge 24, cold L2): the rest is the softmax
+// time (expand 14 us, attend 158, merge 18, cold L2): the rest is the softmax
 // of a group where it takes longer than the other group's products, and the
 // starts and ends of blocks.
 //
@@ -274,14 +274,15 @@ __device__ __forceinline__ void wide_next(const WideParams &p, WidePlace &w)
 // ---------------------------------------------------------------- expand
 // A block per (tile, kv-head) item: the rows' places looked up once, the tile's
 // exponents from its scales alone (no pass over the codes), then eight
-// elements a thread to each operand tile in 16-byte words.  It writes 4 d bytes
-// a row and kv-head (32 times a code's 3 bits): 8192 rows of 8 kv-heads, head_dim
-// 128, take 19 us (34 MB written, cold L2), an eighth of what the attend kernel
-// of 1024 tokens spends, which finds the tiles in L2.
+// elements a thread to each operand tile in 16-byte words, the loads of four of
+// them together (with a load and a store at a time, 16 tokens over 4096 rows
+// took 1.4 us more in all).  It writes 4 d bytes a row and kv-head: 8192 rows of
+// 8 kv-heads, head_dim 128, are 34 MB, which the attend kernel finds in L2.
 template <int D>
-__global__ void __launch_bounds__(256) wide_expand_kernel(const __grid_constant__ WideParams p)
+__global__ void __launch_bounds__(256, 4) wide_expand_kernel(const __grid_constant__ WideParams p)
 {
     constexpr int NG = D / 32, C8 = D / 8, KT = WideGeo<D>::KT;
+    static_assert(wT * C8 % 1024 == 0 && wT * NG % 256 == 0);
     __shared__ float lut[256];
     __shared__ int64_t rows[wT];   // plane row of each tile row (-1: none)
     __shared__ float red[2][8];
@@ -316,15 +317,24 @@ __global__ void __launch_bounds__(256) wide_expand_kernel(const __grid_constant_
         __syncthreads();
         // bounds of the finite groups, and the value rows that are not finite
         float bk = 0.0f, bv = 0.0f;
-        for (int i = tid; i < wT * NG; i += 256) {
-            const int64_t r = rows[i / NG];
-            if (r < 0) continue;
-            const int64_t mi = r * NG + i % NG;
-            const float b = fabsf(f16_bits_to_f32(p.k_scale[mi])) * (fabsf(f16_bits_to_f32(p.k_zero[mi])) + p.kcmax);
-            const float v = fabsf(f16_bits_to_f32(p.v_scale[mi]));
+        constexpr int MI = wT * NG / 256;
+        uint16_t ms[MI], mz[MI], mv[MI];
+#pragma unroll
+        for (int j = 0; j < MI; ++j) {
+            const int i = tid + 256 * j;
+            const int64_t r = rows[i / NG], mi = r * NG + i % NG;
+            ms[j] = r < 0 ? 0 : p.k_scale[mi];
+            mz[j] = r < 0 ? 0 : p.k_zero[mi];
+            mv[j] = r < 0 ? 0 : p.v_scale[mi];
+        }
+#pragma unroll
+        for (int j = 0; j < MI; ++j) {
+            const int t = (tid + 256 * j) / NG;
+            const float b = fabsf(f16_bits_to_f32(ms[j])) * (fabsf(f16_bits_to_f32(mz[j])) + p.kcmax);
+            const float v = fabsf(f16_bits_to_f32(mv[j]));
             if (b < INFINITY) bk = fmaxf(bk, b);
             if (v < INFINITY) bv = fmaxf(bv, v);
-            else atomicOr(&bad[(i / NG) >> 5], 1u << ((i / NG) & 31));
+            else atomicOr(&bad[t >> 5], 1u << (t & 31));
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) {
@@ -356,30 +366,55 @@ __global__ void __launch_bounds__(256) wide_expand_kernel(const __grid_constant_
             for (int i = 0; i < 4; ++i) m.bad[i] = bad[i];
             p.meta[item] = m;
         }
-        for (int it = tid; it < wT * C8; it += 256) {
-            const int t = it / C8, c8 = it - t * C8, g = c8 >> 2;
-            const int64_t r = rows[t];
-            uint4 k4 = make_uint4(0u, 0u, 0u, 0u), v4 = k4;
-            if (r >= 0) {
-                const float sc = f16_bits_to_f32(p.k_scale[r * NG + g]) * sk;
-                const float cz = magic - f16_bits_to_f32(p.k_zero[r * NG + g]);
-                const int kbyte = c8 * p.kb;
-                const uint32_t *ka = reinterpret_cast<const uint32_t *>(p.k_codes + r * rbk + (kbyte & ~3));
-                const uint32_t k0 = ka[0], k1 = (kbyte & 3) + p.kb > 4 ? ka[1] : 0u;
-                float x[8];
-                key_values<0>(k0, k1, (kbyte & 3) * 8, p.kb, sc, cz, x);
-                k4 = make_uint4(tc_pack_f16(x[0], x[1]), tc_pack_f16(x[2], x[3]), tc_pack_f16(x[4], x[5]), tc_pack_f16(x[6], x[7]));
-                const float sv = f16_bits_to_f32(p.v_scale[r * NG + g]) * sv2;
-                if (!((bad[t >> 5] >> (t & 31)) & 1u)) {
-                    const int vbit = 8 * c8 * p.vb;
+        // four words of each operand at a time, their loads together
+        constexpr int N = 4;
+        auto pass = [&](auto kb_, auto vb_, int i0) {
+            constexpr int KB = kb_.value, VB = vb_.value;  // 0: as the pool says
+            uint32_t k0[N], k1[N], v0[N], v1[N];
+            uint16_t ks[N], kz[N], vs[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int it = i0 + 256 * j, t = it / C8, c8 = it - t * C8, g = c8 >> 2;
+                const int64_t r = rows[t];
+                k0[j] = k1[j] = v0[j] = v1[j] = 0u;
+                ks[j] = kz[j] = vs[j] = 0;
+                if (r >= 0) {
+                    const int kbyte = c8 * p.kb, vbit = 8 * c8 * p.vb;
+                    const uint32_t *ka = reinterpret_cast<const uint32_t *>(p.k_codes + r * rbk + (kbyte & ~3));
                     const uint32_t *va = reinterpret_cast<const uint32_t *>(p.v_codes + r * rbv) + (vbit >> 5);
-                    const uint32_t v0 = va[0], v1 = (vbit & 31) + 8 * p.vb > 32 ? va[1] : 0u;
-                    value_values<0>(v0, v1, vbit & 31, p.vb, sv, smem_addr(lut), x);
-                    v4 = make_uint4(tc_pack_f16(x[0], x[1]), tc_pack_f16(x[2], x[3]), tc_pack_f16(x[4], x[5]), tc_pack_f16(x[6], x[7]));
+                    k0[j] = ka[0];
+                    if ((kbyte & 3) + p.kb > 4) k1[j] = ka[1];
+                    v0[j] = va[0];
+                    if ((vbit & 31) + 8 * p.vb > 32) v1[j] = va[1];
+                    ks[j] = p.k_scale[r * NG + g];
+                    kz[j] = p.k_zero[r * NG + g];
+                    vs[j] = p.v_scale[r * NG + g];
                 }
             }
-            *reinterpret_cast<uint4 *>(dst + kmaj_off(wT, t, 8 * c8)) = k4;
-            *reinterpret_cast<uint4 *>(dst + KT + mnmaj_off<D>(t, 8 * c8)) = v4;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int it = i0 + 256 * j, t = it / C8, c8 = it - t * C8;
+                uint4 k4 = make_uint4(0u, 0u, 0u, 0u), v4 = k4;
+                if (rows[t] >= 0) {
+                    float x[8];
+                    key_values<KB>(k0[j], k1[j], ((c8 * p.kb) & 3) * 8, p.kb, f16_bits_to_f32(ks[j]) * sk,
+                                  magic - f16_bits_to_f32(kz[j]), x);
+                    k4 = make_uint4(tc_pack_f16(x[0], x[1]), tc_pack_f16(x[2], x[3]), tc_pack_f16(x[4], x[5]), tc_pack_f16(x[6], x[7]));
+                    if (!((bad[t >> 5] >> (t & 31)) & 1u)) {
+                        value_values<VB>(v0[j], v1[j], (8 * c8 * p.vb) & 31, p.vb, f16_bits_to_f32(vs[j]) * sv2, smem_addr(lut), x);
+                        v4 = make_uint4(tc_pack_f16(x[0], x[1]), tc_pack_f16(x[2], x[3]), tc_pack_f16(x[4], x[5]), tc_pack_f16(x[6], x[7]));
+                    }
+                }
+                *reinterpret_cast<uint4 *>(dst + kmaj_off(wT, t, 8 * c8)) = k4;
+                *reinterpret_cast<uint4 *>(dst + KT + mnmaj_off<D>(t, 8 * c8)) = v4;
+            }
+        };
+        using std::integral_constant;
+#pragma unroll 1
+        for (int i0 = tid; i0 < wT * C8; i0 += 256 * N) {
+            if (p.vb == 3 && p.kb == 8) pass(integral_constant<int, 8>{}, integral_constant<int, 3>{}, i0);
+            else if (p.vb == 3 && p.kb == 4) pass(integral_constant<int, 4>{}, integral_constant<int, 3>{}, i0);
+            else pass(integral_constant<int, 0>{}, integral_constant<int, 0>{}, i0);
         }
     }
 }
@@ -855,53 +890,74 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------- merge
-// Block c merges the shares of the block that CTA c began and did not finish,
-// a warp per column (256 columns over gridDim.y x 8 warps).  At most one block
-// per CTA is shared: 36 MB at head_dim 128, 24 us from memory, and less where
-// L2 still holds the shares; bound by the latency of their loads.
+// Blocks (c, y) merge the shares of the block that CTA c began and did not
+// finish, a warp per column (256 columns over 32 y x 8 warps): its (max, sum)
+// pairs one a lane, 32 at a time, the first rows under way with them.  At most
+// one block per CTA is shared, 36 MB of shares at head_dim 128; bound by the
+// latency of three dependent loads (share, pair and row, store).
 template <int D>
 __global__ void __launch_bounds__(256) wide_merge_kernel(const __grid_constant__ WideParams p)
 {
-    constexpr int PER = D / 32;
+    constexpr int PER = D / 32, KF = 4;
     pdl_wait_primary();
     pdl_allow_dependents();
     const int64_t total = p.pl.line[0], per = p.pl.line[1], c = blockIdx.x;
-    if (c * per >= total) return;  // a CTA without work left no word
-    const WideShare w = p.pl.share[c];
-    if (w.last < 0) return;
-    const int64_t last = w.last, nn = paged_new(p.pg.v, w.s);
-    const int lane = threadIdx.x & 31;
-    for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < wC; i += gridDim.y * 8) {
-        const int64_t col = (int64_t)w.block * wC + i;
-        if (col >= nn * p.G) break;
-        auto slot = [&](int64_t k) { return (k == c ? 2 * c + 1 : 2 * k) * wC + i; };
-        float m = -INFINITY;
-        for (int64_t k = c + lane; k <= last; k += 32) m = fmaxf(m, p.part_ml[2 * slot(k)]);
+    const WideShare w = p.pl.share[c];  // (under way with the line's words; one without work left none)
+    if (c * per >= total || w.last < 0) return;
+    const int lane = threadIdx.x & 31, i = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int cnt = w.last - (int)c + 1;
+    auto slot = [&](int k) { return (k == 0 ? 2 * c + 1 : 2 * (c + k)) * wC + i; };  // share k of the block
+    float v[KF][PER];
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float mu = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f, x[PER];
+    for (int k = 0; k < KF; ++k) {
+        const float *src = p.part_o + slot(k) * D + PER * lane;
 #pragma unroll
-        for (int k = 0; k < PER; ++k) x[k] = 0.0f;
-#pragma unroll 4
-        for (int64_t k = c; k <= last; ++k) {
-            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(k));
-            const float wt = tc_ex2(ml.x - mu);
-            l += ml.y * wt;
-            const float *src = p.part_o + slot(k) * D + PER * lane;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) x[j] += src[j] * wt;
-        }
-        fwht_warp<PER>(x, lane);
-        const float inv = l == 0.0f ? 0.0f : p.inv_sqrt_d / l;
-        const int64_t tok = col / p.G, row = paged_start(p.pg.v, w.s) + tok;
-        uint32_t u[PER / 2];
-#pragma unroll
-        for (int k = 0; k < PER; k += 2)
-            u[k / 2] = pack_bf16x2(x[k] * (sign_negative(p.sg, PER * lane + k) ? -inv : inv),
-                                   x[k + 1] * (sign_negative(p.sg, PER * lane + k + 1) ? -inv : inv));
-        store_words<PER / 2, 2 * PER>(p.out + (row * p.QH + (int64_t)w.h * p.G + (col - tok * p.G)) * D + PER * lane, u);
+        for (int j = 0; j < PER; ++j) v[k][j] = k < cnt ? src[j] : 0.0f;
     }
+    const int64_t s0 = paged_start(p.pg.v, w.s), n = paged_new(p.pg.v, w.s), col = (int64_t)w.block * wC + i;
+    float m = -INFINITY, l = 0.0f, x[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) x[j] = 0.0f;
+    for (int k0 = 0; k0 < cnt; k0 += 32) {
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (k0 + lane < cnt) ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(k0 + lane));
+        float mx = ml.x;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mx = fmaxf(m, mx);
+        const float mu = mx == -INFINITY ? 0.0f : mx, keep = tc_ex2(m - mu), wt = tc_ex2(ml.x - mu);
+        m = mx;
+        l = l * keep + ml.y * wt;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) x[j] *= keep;
+        if (k0 == 0)
+#pragma unroll
+            for (int k = 0; k < KF; ++k) {
+                const float f = __shfl_sync(0xffffffffu, wt, k);  // (0 past the last)
+#pragma unroll
+                for (int j = 0; j < PER; ++j) x[j] += v[k][j] * f;
+            }
+        const int end = cnt - k0 < 32 ? cnt - k0 : 32;
+#pragma unroll 4
+        for (int k = k0 == 0 ? KF : 0; k < end; ++k) {
+            const float f = __shfl_sync(0xffffffffu, wt, k);
+            const float *src = p.part_o + slot(k0 + k) * D + PER * lane;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) x[j] += src[j] * f;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    fwht_warp<PER>(x, lane);
+    if (col >= n * p.G) return;  // past the sequence's columns: shares that nothing wrote
+    const float inv = l == 0.0f ? 0.0f : p.inv_sqrt_d / l;
+    const int64_t tok = col / p.G;
+    uint32_t u[PER / 2];
+#pragma unroll
+    for (int k = 0; k < PER; k += 2)
+        u[k / 2] = pack_bf16x2(x[k] * (sign_negative(p.sg, PER * lane + k) ? -inv : inv),
+                               x[k + 1] * (sign_negative(p.sg, PER * lane + k + 1) ? -inv : inv));
+    store_words<PER / 2, 2 * PER>(p.out + ((s0 + tok) * p.QH + (int64_t)w.h * p.G + (col - tok * p.G)) * D + PER * lane, u);
 }
 
 // ---------------------------------------------------------------- host side
