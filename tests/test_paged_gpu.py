@@ -499,3 +499,55 @@ def test_bad_pages_and_lengths_of_long_chunks(cuda):
     out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(np.array([0, 200, 100], np.int32)), q.cuda(), 200)
     assert cuda.tq_device_error() == cuda.TQ_DEVICE_ERR_LENGTH
     check_attention(b, pool, q[:200], out[:200], new=[200, 0])
+
+
+def test_long_chunks_strided_padded_and_replayed(cuda):
+    """Chunks beside single tokens in one captured graph, q cut out of a wider tensor, rows behind the last sequence
+    left as they were; replayed after lengths and starts changed (a chunk for the other sequence, then none)."""
+    b = Batch([500, 333, 0, 260], [150, 1, 0, 60], H=2, d=128, kb=4, vb=3, page=48, seed=31)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    rows, QH = 230, 8
+    whole = torch.zeros(rows, QH + 3, 128, dtype=torch.bfloat16, device="cuda")
+    q = whole[:, 2:2 + QH]
+    pages, starts = b.pages(cuda), b.dev(b.starts)
+    ws = torch.empty(cuda.tq_paged_attention_workspace_bytes(pool, pages, QH, rows, 200), dtype=torch.uint8, device="cuda")
+    out = torch.empty(rows, QH, 128, dtype=torch.bfloat16, device="cuda")
+    step = lambda: cuda.tq_paged_attention(pool, pages, starts, q, 200, out=out, workspace=ws)  # noqa: E731
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i, (lens, new) in enumerate((([500, 333, 0, 260], [150, 1, 0, 60]), ([40, 333, 0, 200], [3, 200, 0, 1]),
+                                     ([500, 1, 0, 129], [2, 1, 0, 31]), ([129, 40, 0, 33], [129, 33, 0, 32]))):
+        total = sum(new)
+        pages.seq_lens.copy_(b.dev(np.array(lens, np.int32)))
+        starts.copy_(b.dev(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)))
+        fresh = b.queries(QH, seed=40 + i, total=rows)
+        whole.fill_(float("nan"))
+        q[:total].copy_(fresh[:total].cuda())
+        out.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert bool((out[total:] == 7.0).all())
+        check_attention(b, pool, fresh[:total], out[:total], lens=lens, new=new)
+    assert cuda.tq_device_error() == 0
+
+
+def test_many_sequences_some_of_them_long(cuda):
+    """More sequences than a warp holds, chunks of every size among them."""
+    lens = [(i * 37) % 290 for i in range(70)]
+    new = [min(n, (1, 0, 5, 140, 32, 31)[i % 6]) for i, n in enumerate(lens)]
+    for d, kb, vb, page in ((128, 8, 3, 32), (64, 4, 4, 16)):
+        b = Batch(lens, new, H=2, d=d, kb=kb, vb=vb, page=page, seed=d)
+        _attend(cuda, b, 8)
+
+
+@pytest.mark.parametrize("G", [128, 160])
+def test_a_group_of_more_q_heads_than_a_column_group(cuda, G):
+    """A single token is a chunk of its own then."""
+    b = Batch([300, 1, 0, 140], [1, 1, 0, 2], H=1, d=128, kb=8, vb=3, page=64, seed=G)
+    _attend(cuda, b, G)
+    b.bound = 300
+    _attend(cuda, b, G)
