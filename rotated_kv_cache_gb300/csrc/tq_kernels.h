@@ -5,6 +5,8 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include <functional>
+
 namespace tq {
 
 // Output i of SplitMix64 started at `seed` (Steele, Lea & Flood, OOPSLA 2014).
@@ -86,6 +88,7 @@ struct PagedSplit {
     int blocks;               // column blocks of a sequence's kv-head, at most
     int64_t wide;             // sequences with more new tokens than this are another kernel's
     int nch, ru;              // chunks per stage, rows per chunk
+    bool late;                // beside the expansion of long chunks' rows: independent of the kernel before
 };
 
 __host__ __device__ constexpr int gcd_int(int a, int b) { return b == 0 ? a : gcd_int(b, a % b); }
@@ -196,8 +199,10 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
 // ... of the wide sequences, by tcgen05 (head_dim 64 and 128).
 bool paged_wide_applies(const CacheView &c);
 size_t paged_wide_workspace_bytes(const CacheView &c, const PagedBounds &b, int QH);
+// `split` launches the other sequences' split kernel, beside the expansion of the rows.
 cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const PagedBounds &b, const uint16_t *q, int QH,
-                              float scale, uint16_t *out, void *ws, cudaStream_t s);
+                              float scale, uint16_t *out, void *ws, cudaStream_t s,
+                              const std::function<cudaError_t()> &split);
 
 // Allocation-free decode attention: partials in a library-owned device array.
 size_t noalloc_scratch_bytes();

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
     __shared__ float wm[CW], wl[CW];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wid = warp % W, lead = warp - wid;
     const int64_t row = (int64_t)blockIdx.x * (CW / W) + warp / W;
-    pdl_wait_primary();
+    const PdlWait order(p.pg.late);  // behind the merge of long chunks: the split kernel is complete before that starts
     pdl_allow_dependents();
     bool live = row < p.rows;
     int64_t t = live ? row / p.QH : 0;
@@ -296,25 +296,28 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
     if (!paged_plan(c, b, QH, pl)) return cudaErrorInvalidConfiguration;
     if (ws_bytes < pl.bytes) return cudaErrorInvalidValue;
     uint8_t *base = static_cast<uint8_t *>(ws);
-    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<PagedUnit *>(base), pl.slots, pl.blocks, pl.b.wide, 1, 1};
+    const bool wide = pl.b.wide != INT32_MAX;
+    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<PagedUnit *>(base), pl.slots, pl.blocks, pl.b.wide, 1, 1, wide};
     float *part_ml = reinterpret_cast<float *>(base + pl.off_ml), *part_o = reinterpret_cast<float *>(base + pl.off_o);
-    cudaError_t e = cudaSuccess;
-    if (pl.b.wide != INT32_MAX) e = launch_paged_wide(c, pg, pl.b, q, QH, scale, out, base + pl.off_wide, s);
-    if (e != cudaSuccess) return e;
-    const int64_t cols = pl.cols;
-    if (pl.special) {
-        const auto launch = pl.b.max_new <= 1
-                                ? (c.d == 64 ? launch_paged_split_d64_one : c.d == 128 ? launch_paged_split_d128_one : launch_paged_split_d256_one)
-                                : (c.d == 64 ? launch_paged_split_d64_any : c.d == 128 ? launch_paged_split_d128_any : launch_paged_split_d256_any);
-        e = launch(c, pg, pl.split, q, QH, scale, part_o, part_ml, s);
-    }
-    else switch (c.d) {
-    case 64: e = launch_paged_generic_d64(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
-    case 128: e = launch_paged_generic_d128(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
-    case 256: e = launch_paged_generic_d256(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
-    case 512: e = launch_paged_generic_d512(c, pg, cols, q, QH, scale, part_o, part_ml, s); break;
-    default: e = cudaErrorInvalidValue;
-    }
+    auto split = [&]() -> cudaError_t {
+        const int64_t cols = pl.cols;
+        if (pl.special) {
+            const auto launch = pl.b.max_new <= 1
+                                    ? (c.d == 64 ? launch_paged_split_d64_one : c.d == 128 ? launch_paged_split_d128_one : launch_paged_split_d256_one)
+                                    : (c.d == 64 ? launch_paged_split_d64_any : c.d == 128 ? launch_paged_split_d128_any : launch_paged_split_d256_any);
+            return launch(c, pg, pl.split, q, QH, scale, part_o, part_ml, s);
+        }
+        switch (c.d) {
+        case 64: return launch_paged_generic_d64(c, pg, cols, q, QH, scale, part_o, part_ml, s);
+        case 128: return launch_paged_generic_d128(c, pg, cols, q, QH, scale, part_o, part_ml, s);
+        case 256: return launch_paged_generic_d256(c, pg, cols, q, QH, scale, part_o, part_ml, s);
+        case 512: return launch_paged_generic_d512(c, pg, cols, q, QH, scale, part_o, part_ml, s);
+        }
+        return cudaErrorInvalidValue;
+    };
+    const cudaError_t e = wide ? launch_paged_wide(c, pg, pl.b, q, QH, scale, out, base + pl.off_wide, s,
+                                                   std::ref(split))  // (a reference: nothing allocated)
+                               : split();
     if (e != cudaSuccess) return e;
     // by places per sequence where that goes through fewer rows (a decode step: no
     // search for a token's sequence; a long chunk: none of its tokens).  32

@@ -993,8 +993,11 @@ WideSizes wide_sizes(const CacheView &c, const PagedBounds &b, int QH)
     return z;
 }
 
+// The split kernel of the other sequences needs nothing of plan and expand: it
+// is launched behind expand and does not wait for it until it ends, so the two
+// run side by side; likewise the combine behind merge.
 template <int D>
-cudaError_t wide_run(WideParams &p, cudaStream_t s)
+cudaError_t wide_run(WideParams &p, cudaStream_t s, const std::function<cudaError_t()> &split)
 {
     using A = WideGeo<D>;
     cudaError_t e = cudaFuncSetAttribute(wide_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
@@ -1004,6 +1007,7 @@ cudaError_t wide_run(WideParams &p, cudaStream_t s)
     const int64_t items = p.max_tiles * p.H;
     e = launch_dependent(wide_expand_kernel<D>, dim3((unsigned)imin64(items, (int64_t)num_sms() * 8)), dim3(256), 0, s, p);
     if (e != cudaSuccess) return e;
+    if ((e = split()) != cudaSuccess) return e;
     e = launch_dependent(wide_attend_kernel<D>, dim3((unsigned)p.ctas), dim3(wThreads), A::SMEM, s, p);
     if (e != cudaSuccess) return e;
     return launch_dependent(wide_merge_kernel<D>, dim3((unsigned)p.ctas, wC / 8), dim3(256), 0, s, p);
@@ -1016,7 +1020,8 @@ bool paged_wide_applies(const CacheView &c) { return c.d == 64 || c.d == 128; }
 size_t paged_wide_workspace_bytes(const CacheView &c, const PagedBounds &b, int QH) { return wide_sizes(c, b, QH).bytes; }
 
 cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const PagedBounds &b, const uint16_t *q, int QH,
-                              float scale, uint16_t *out, void *ws, cudaStream_t s)
+                              float scale, uint16_t *out, void *ws, cudaStream_t s,
+                              const std::function<cudaError_t()> &split)
 {
     const WideSizes z = wide_sizes(c, b, QH);
     uint8_t *w = static_cast<uint8_t *>(ws);
@@ -1054,7 +1059,7 @@ cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const Pa
         p.cen[i] = tab.centroids[i];
         p.cmax = p.cmax > fabsf(tab.centroids[i]) ? p.cmax : fabsf(tab.centroids[i]);
     }
-    return c.d == 64 ? wide_run<64>(p, s) : wide_run<128>(p, s);
+    return c.d == 64 ? wide_run<64>(p, s, split) : wide_run<128>(p, s, split);
 }
 
 }  // namespace tq
