@@ -29,8 +29,8 @@
 // largest.
 //
 // Measured: 2048 new tokens over 32768 rows, 64 q-heads, 8 kv-heads, head_dim
-// 128, 4-bit keys, 3-bit values: 1484 us in all, 1.42 PFLOP/s (of 1.87 that a
-// large library product reaches); a prompt of 8191 tokens 408 us, 1.35.  At 1024
+// 128, 4-bit keys, 3-bit values: 1454 us in all, 1.46 PFLOP/s (of 1.87 that a
+// large library product reaches); a prompt of 8191 tokens 414 us, 1.33 (400 on another board).  At 1024
 // tokens over 8192 rows the tensor pipe is busy 69 % of the attend kernel's
 // time (expand 14 us, attend 158, merge 18, cold L2): the rest is the softmax
 // of a group where it takes longer than the other group's products, and the
