@@ -191,13 +191,21 @@ class Cache:
         self.__dict__[name] = value
         self.__dict__.pop("_struct", None)  # built again from the new attributes
 
+    def __getstate__(self):
+        state = self.__dict__.copy()  # copies and pickles carry the planes, no addresses
+        state.pop("_struct", None)
+        return state
+
     def struct(self) -> _CacheStruct:
-        """The C ABI's view of this cache (built once, and again after an attribute is set)."""
-        s = self.__dict__.get("_struct")
-        if s is None:
-            s = _CacheStruct(self.head_dim, self.k_bits, self.v_bits, self.num_kv_heads, self.batch, 0,
-                             self.capacity, *[t.data_ptr() for t in self.planes()], self.sign_seed)
-            self.__dict__["_struct"] = s
+        """The C ABI's view of this cache, built again after an attribute is set or a plane's storage has moved."""
+        at = (self.k_codes.data_ptr(), self.k_scale.data_ptr(), self.k_zero.data_ptr(), self.v_codes.data_ptr(),
+              self.v_scale.data_ptr())
+        known = self.__dict__.get("_struct")
+        if known is not None and known[0] == at:
+            return known[1]
+        s = _CacheStruct(self.head_dim, self.k_bits, self.v_bits, self.num_kv_heads, self.batch, 0, self.capacity, *at,
+                         self.sign_seed)
+        self.__dict__["_struct"] = at, s
         return s
 
     def batch_slice(self, b0: int, nb: int) -> "Cache":
