@@ -36,11 +36,12 @@ def test_a_cache_follows_its_planes(tqlib):
     c = _cache(tqlib)
     before = _addresses(c)
     assert before == [t.data_ptr() for t in c.planes()]
+    kept = [t.detach() for t in c.planes()]  # (the first storages live on, so that no new one takes their place)
     for name in ("k_codes", "k_scale", "k_zero", "v_codes", "v_scale"):
         t = getattr(c, name)
         t.data = t.clone()
         assert _addresses(c) == [t.data_ptr() for t in c.planes()]
-    assert not set(before) & set(_addresses(c))
+    assert not set(before) & set(_addresses(c)) and [t.data_ptr() for t in kept] == before
     c.v_codes.set_(c.v_codes.clone())
     assert _addresses(c) == [t.data_ptr() for t in c.planes()]
     c.v_scale = c.v_scale.clone()
