@@ -228,30 +228,46 @@ class PageTable:
     [num_seqs] (rows, new tokens included), both on the pool's device, and the host's bound
     max_len of the lengths (default: all that the table's pages hold) and total_len of their sum (0:
     num_seqs * max_len; long chunks size their workspace by it).  The tensors are read by
-    every call, so writing to them changes the batch, captured graphs included."""
+    every call, so writing to them changes the batch, captured graphs included; max_len and
+    total_len may be set again (graphs keep the bounds that they were captured with)."""
 
     def __init__(self, pages: torch.Tensor, seq_lens: torch.Tensor, max_len: int | None = None,
                  page_size: int | None = None, total_len: int = 0):
-        if pages.dtype != torch.int32 or pages.dim() != 2 or (pages.shape[1] > 1 and pages.stride(1) != 1):
-            raise ValueError("pages must be int32 [num_seqs][pages], a sequence's pages contiguous")
-        if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (pages.shape[0],) or not seq_lens.is_contiguous():
-            raise ValueError("seq_lens must be contiguous int32 [num_seqs]")
         if max_len is None and page_size is None:
             raise ValueError("give max_len, or page_size to bound the lengths by the table's pages")
-        _require_cuda(pages, seq_lens)
-        if pages.device != seq_lens.device:
-            raise ValueError("pages and seq_lens must be on one device")
         self._pages, self._seq_lens = pages, seq_lens
-        self.num_seqs, self.width = (int(x) for x in pages.shape)
+        self.total_len, self.max_len = int(total_len), 0
+        self._known = None
+        self._look()
+        _require_cuda(pages, seq_lens)
         self.max_len = self.width * int(page_size) if max_len is None else int(max_len)
-        self.total_len = int(total_len)
+
+    def _look(self) -> _PageTableStruct:
+        """The C ABI's view, made and its tensors checked again after a bound is set or a tensor's storage has moved."""
+        p, n = self._pages, self._seq_lens
+        at = (p.data_ptr(), n.data_ptr(), p.shape, p.stride(), n.shape, n.stride(), self.max_len, self.total_len)
+        if self._known is not None and self._known[0] == at:
+            return self._known[1]
+        if p.dtype != torch.int32 or p.dim() != 2 or (p.shape[1] > 1 and p.stride(1) != 1):
+            raise ValueError("pages must be int32 [num_seqs][pages], a sequence's pages contiguous")
+        if n.dtype != torch.int32 or tuple(n.shape) != (p.shape[0],) or not n.is_contiguous():
+            raise ValueError("seq_lens must be contiguous int32 [num_seqs]")
+        if p.device != n.device:
+            raise ValueError("pages and seq_lens must be on one device")
+        self.num_seqs, self.width = (int(x) for x in p.shape)
         # a table of one sequence has no row to step to: its stride is its pages
-        stride = pages.stride(0) if self.num_seqs > 1 else self.width
+        stride = p.stride(0) if self.num_seqs > 1 else self.width
         if stride < self.width:
             raise ValueError("the rows of the page table overlap")
-        self._device = pages.get_device()
-        self._struct = _PageTableStruct(pages.data_ptr(), seq_lens.data_ptr(), stride, self.max_len, self.total_len,
-                                        self.num_seqs, 0)
+        self._device = p.get_device()
+        s = _PageTableStruct(at[0], at[1], stride, int(self.max_len), int(self.total_len), self.num_seqs, 0)
+        self._known = at, s
+        return s
+
+    def __getstate__(self):
+        state = self.__dict__.copy()  # copies and pickles carry the tensors, no addresses
+        state["_known"] = None
+        return state
 
     @property
     def pages(self) -> torch.Tensor:
@@ -263,9 +279,10 @@ class PageTable:
 
     def struct(self, pool: "Cache") -> _PageTableStruct:
         """The C ABI's view of the table, for a pool whose pages hold max_len rows."""
+        s = self._look()
         if self.width * pool.capacity < self.max_len:
             raise ValueError(f"{self.width} pages of {pool.capacity} rows do not hold max_len = {self.max_len}")
-        return self._struct
+        return s
 
 
 # ------------------------------------------------------------------ host-side queries
@@ -484,6 +501,7 @@ def _empty_on(stream, shape, dtype, device):
 def _paged_check(pool: Cache, table: PageTable, starts: torch.Tensor, *tensors):
     """Checks shared by the paged calls: the starts' form, one device, the current one, for all; the
     C ABI's views of pool and table by reference."""
+    view = table.struct(pool)
     if starts.dtype is not torch.int32 or starts.dim() != 1 or starts.shape[0] != table.num_seqs + 1 or \
             not starts.is_contiguous():
         raise ValueError("starts must be contiguous int32 [num_seqs + 1]")
@@ -497,7 +515,7 @@ def _paged_check(pool: Cache, table: PageTable, starts: torch.Tensor, *tensors):
             raise ValueError("the pool, the page table and the tensors must be on one device")
     if dev != torch._C._cuda_getDevice():
         raise ValueError("the tensors are on another device than the current one")
-    return ctypes.byref(pool.struct()), ctypes.byref(table.struct(pool))
+    return ctypes.byref(pool.struct()), ctypes.byref(view)
 
 
 def _ragged_strides(x: torch.Tensor, heads: int | None, d: int, what: str):

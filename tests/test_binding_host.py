@@ -3,6 +3,7 @@ import copy
 import io
 import pickle
 
+import pytest
 import torch
 
 
@@ -58,3 +59,53 @@ def test_from_planes_takes_the_planes_it_is_given(tqlib):
     s = c.struct()
     assert (s.head_dim, s.k_bits, s.v_bits, s.num_kv_heads, s.batch, s.capacity, s.sign_seed) == (64, 4, 3, 3, 4, 48, 5)
     assert _addresses(c) == [t.data_ptr() for t in planes]
+
+
+def _table(tq, monkeypatch, pages, lens, *a, **kw):
+    monkeypatch.setattr(tq, "_require_cuda", lambda *t: None)
+    return tq.PageTable(pages, lens, *a, **kw)
+
+
+def test_a_page_table_follows_its_tensors_and_bounds(tqlib, monkeypatch):
+    """Bounds set later, and tensors whose storage is replaced in place, reach the library."""
+    pool = _cache(tqlib)  # pages of 32 rows
+    pages, lens = torch.zeros(2, 5, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    t = _table(tqlib, monkeypatch, pages, lens, page_size=32)
+    s = t.struct(pool)
+    assert (s.pages, s.seq_lens, s.stride, s.max_len, s.total_len, s.num_seqs) == (
+        pages.data_ptr(), lens.data_ptr(), 5, 160, 0, 2)
+    t.max_len, t.total_len = 96, 128
+    s = t.struct(pool)
+    assert (s.max_len, s.total_len) == (96, 128)
+    t.max_len = 161
+    with pytest.raises(ValueError):
+        t.struct(pool)
+    t.max_len = 64
+    old = (pages.detach(), lens.detach())
+    pages.data, lens.data = torch.ones(2, 9, dtype=torch.int32)[:, :3], torch.ones(2, dtype=torch.int32)
+    s = t.struct(pool)
+    assert (s.pages, s.seq_lens, s.stride, s.num_seqs, s.max_len) == (pages.data_ptr(), lens.data_ptr(), 9, 2, 64)
+    t.max_len = 97  # three pages of 32 hold 96
+    with pytest.raises(ValueError):
+        t.struct(pool)
+    t.max_len = 96
+    assert t.struct(pool).max_len == 96 and old[0].shape == (2, 5)
+    # what a table is refused for when it is made, it is refused for later
+    lens.data = torch.ones(3, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        t.struct(pool)
+    lens.data = torch.ones(2, dtype=torch.int32)
+    pages.data = torch.zeros(3, 2, dtype=torch.int32).t()
+    with pytest.raises(ValueError):
+        t.struct(pool)
+
+
+def test_a_used_page_table_copies_and_pickles(tqlib, monkeypatch):
+    pool = _cache(tqlib)
+    t = _table(tqlib, monkeypatch, torch.arange(6, dtype=torch.int32).view(2, 3), torch.tensor([7, 9], dtype=torch.int32), 64,
+               total_len=16)
+    t.struct(pool)
+    for x in (copy.deepcopy(t), pickle.loads(pickle.dumps(t)), copy.copy(t)):
+        s = x.struct(pool)
+        assert (s.pages, s.seq_lens, s.max_len, s.total_len) == (x.pages.data_ptr(), x.seq_lens.data_ptr(), 64, 16)
+        assert torch.equal(x.pages, t.pages) and torch.equal(x.seq_lens, t.seq_lens)
