@@ -32,11 +32,9 @@
  *    stream order holds as for ordinary launches; only its start-up overlaps
  *    the previous kernel's end.
  *  - Calls run on the calling thread's current CUDA device, which must hold
- *    every pointer.  The intended use is one process per GPU.  Kernel
- *    shared-memory opt-ins and occupancy figures are set up once per process,
- *    on the first device a kernel runs on; a process that later calls on
- *    another device gets TQ_ERR_CUDA if that device needs its own set-up.
- *    The device error word and the SM count are kept per device.
+ *    every pointer.  The intended use is one process per GPU; kernel
+ *    shared-memory opt-ins, occupancy figures, the device error word and the
+ *    SM count are set up on first use of each device (64 devices at most).
  */
 #ifndef TQ_H
 #define TQ_H

@@ -15,10 +15,10 @@ namespace tq {
 __device__ uint32_t g_device_error;  // see tq_device_error()
 
 namespace {
-constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 uint32_t *g_err_ptr[kMaxDevices];
 int g_sms[kMaxDevices];
+}  // namespace
 
 int current_device()
 {
@@ -26,7 +26,6 @@ int current_device()
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
     return dev;
 }
-}  // namespace
 
 uint32_t *device_error_word()
 {

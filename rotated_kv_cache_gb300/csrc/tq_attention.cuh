@@ -853,19 +853,10 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
 template <int KB, int D, int VB, int NBC, int MODE = 0>
 int ctas_per_sm_for()
 {
-    static int cached = 0;  // same on every GB300; only a successful query is kept
-    if (!cached) {
-        int n = 0;
-        if (cudaFuncSetAttribute(attn_split_kernel<KB, D, VB, NBC, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 AGeo<KB, D, VB, NBC>::SMEM) == cudaSuccess &&
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_split_kernel<KB, D, VB, NBC, MODE>, kThreads,
-                                                          AGeo<KB, D, VB, NBC>::SMEM) == cudaSuccess &&
-            n > 0)
-            cached = n;
-        else
-            return 1;
-    }
-    return cached;
+    static KernelSetup setup;
+    int n;
+    setup.get(attn_split_kernel<KB, D, VB, NBC, MODE>, kThreads, AGeo<KB, D, VB, NBC>::SMEM, AGeo<KB, D, VB, NBC>::SMEM, n);
+    return n > 0 ? n : 1;  // (where the query failed, so will the launch)
 }
 
 // Tensor map over the key plane: rows of KROW bytes, boxes of SW bytes x rows.

@@ -35,8 +35,6 @@
 #pragma once
 #include <cuda.h>
 
-#include <atomic>
-
 #include "tq_common.cuh"
 #include "tq_kernels.h"
 #include "tq_paged.cuh"
@@ -1084,18 +1082,11 @@ int gen_layout(const CacheView &c, GenPlan &pl)
                                                                            : A::MERGE;
     pl.smem = 1024 /*align slack*/ + ring + A::QF + A::QS + (pl.vlut == 0 ? 512 : 0) /*lut*/ +
               gMaxStages * 12 /*barriers, counters*/;
-    // the opt-in and the occupancy of an instantiation are looked up once per shared-memory size
-    static std::atomic<uint64_t> table[3][3];  // [VLUT][KEY]: smem << 32 | CTAs; same on every GB300
-    std::atomic<uint64_t> &known = table[pl.vlut == 0 ? 0 : pl.vlut - 1][pl.key / 4];
+    static KernelSetup table[3][3];  // [VLUT][KEY] of the instantiation
+    KernelSetup &setup = table[pl.vlut == 0 ? 0 : pl.vlut - 1][pl.key / 4];
     return gen_dispatch<D, NB, PAGED>(pl, [&](auto kern) {
-        const uint64_t k = known.load(std::memory_order_relaxed);
-        if (k >> 32 == (uint64_t)pl.smem) return (int)(uint32_t)k;
-        int n = 0;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem) != cudaSuccess) return 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, GGeo<D, NB>::THREADS, pl.smem) != cudaSuccess)
-            return 0;
-        known.store((uint64_t)pl.smem << 32 | (uint32_t)n, std::memory_order_relaxed);
-        return n;
+        int n;
+        return setup.get(kern, GGeo<D, NB>::THREADS, (size_t)pl.smem, kMaxDynamicSmem, n) == cudaSuccess ? n : 0;
     });
 }
 

@@ -601,15 +601,12 @@ cudaError_t run_value(const CacheView &c, const PagedView *pv, int64_t t0, int64
     const Tables &tab = codebook_tables(VB);
     for (int i = 0; i < (1 << VB); ++i) p.cen[i] = tab.centroids[i];
     auto kern = decode_value_kernel<D, VB, F32, PAGED>;
-    static int per_sm = 0;  // same on every GB300; only a successful query is kept
-    if (!per_sm) {
-        int k = 0;
-        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k, kern, kVWarps * 32, 0);
-        if (e != cudaSuccess) return e;
-        per_sm = k > 0 ? k : 1;
-    }
+    static KernelSetup setup;
+    int per_sm;
+    const cudaError_t e = setup.get(kern, kVWarps * 32, 0, 0, per_sm);
+    if (e != cudaSuccess) return e;
     const int64_t want = (items + kVWarps - 1) / kVWarps;
-    const int grid = (int)imin64(want, (int64_t)num_sms() * per_sm);
+    const int grid = (int)imin64(want, (int64_t)num_sms() * (per_sm > 0 ? per_sm : 1));
     return launch_dependent(kern, dim3((unsigned)grid), dim3(kVWarps * 32), 0, s, p);
 }
 

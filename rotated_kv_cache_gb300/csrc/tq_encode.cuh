@@ -819,17 +819,12 @@ cudaError_t run(const EncodeParams &p, const CUtensorMap &map, cudaStream_t s)
 {
     const size_t smem = encode_smem<D, BITS, KEY>();
     auto kern = encode_kernel<D, BITS, KEY, PAGED>;
-    static int per_sm = 0;  // same on every GB300; only a successful query is kept
-    if (!per_sm) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        int n = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kWarps * 32, smem);
-        if (e != cudaSuccess) return e;
-        per_sm = n > 0 ? n : 1;
-    }
+    static KernelSetup setup;
+    int per_sm;
+    const cudaError_t e = setup.get(kern, kWarps * 32, smem, smem, per_sm);
+    if (e != cudaSuccess) return e;
     const int64_t want = ((int64_t)p.items + kWarps - 1) / kWarps;
-    const int grid = (int)imin64(want, (int64_t)num_sms() * per_sm);
+    const int grid = (int)imin64(want, (int64_t)num_sms() * (per_sm > 0 ? per_sm : 1));
     return launch_dependent(kern, dim3((unsigned)grid), dim3(kWarps * 32), smem, s, p, map);
 }
 
@@ -842,12 +837,10 @@ cudaError_t run_kv(const EncodeParams &pk, const CUtensorMap &mk, const EncodePa
     constexpr size_t sk = encode_smem<D, KB, true>(), sv = encode_smem<D, VB, false>();
     constexpr size_t smem = sk > sv ? sk : sv;
     auto kern = encode_kv_kernel<D, KB, VB, PAGED>;
-    static bool attr = false;  // same on every GB300; only a successful call is kept
-    if (!attr) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    static KernelSetup setup;
+    int per_sm;
+    const cudaError_t e = setup.get(kern, kWarps * 32, smem, smem, per_sm);
+    if (e != cudaSuccess) return e;
     return launch_dependent(kern, dim3(key_ctas + value_ctas), dim3(kWarps * 32), smem, s, pk, mk, pv, mv, key_ctas);
 }
 

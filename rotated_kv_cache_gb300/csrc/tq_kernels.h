@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <functional>
 
 namespace tq {
@@ -183,6 +184,40 @@ cudaError_t launch_attention(const CacheView &c, const uint16_t *q, int q_heads,
                              float *out, void *ws, size_t ws_bytes, cudaStream_t s);
 
 int num_sms();
+
+constexpr int kMaxDevices = 64;
+int current_device();  // in [0, kMaxDevices), or -1
+
+// A kernel's shared-memory opt-in, a setting of the current device, and its
+// resident CTAs per SM there (the same whichever thread asks first): once per
+// device and shared-memory size.  A failure is not kept.
+class KernelSetup {
+public:
+    // optin: dynamic shared memory to allow (0: the kernel needs no opt-in); ctas: as the query answers, 0 included
+    template <typename Kernel>
+    cudaError_t get(Kernel kern, int threads, size_t smem, size_t optin, int &ctas)
+    {
+        ctas = 0;
+        const int dev = current_device();
+        if (dev < 0) return cudaErrorInvalidDevice;
+        std::atomic<uint64_t> &known = known_[dev];
+        uint64_t k = known.load(std::memory_order_acquire);
+        if (k == 0 || k >> 32 != (uint64_t)smem) {
+            cudaError_t e = optin ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)optin) : cudaSuccess;
+            if (e != cudaSuccess) return e;
+            int n = 0;
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem);
+            if (e != cudaSuccess) return e;
+            k = (uint64_t)smem << 32 | (uint32_t)(n + 1);
+            known.store(k, std::memory_order_release);
+        }
+        ctas = (int)(uint32_t)k - 1;
+        return cudaSuccess;
+    }
+
+private:
+    std::atomic<uint64_t> known_[kMaxDevices]{};  // smem << 32 | CTAs + 1; 0: not asked yet
+};
 
 // Paged caches: the view's pool is `c` (batch = pages, capacity = page size).
 // K, V of ragged tokens -> their rows, and back ([total][H][d]; either output may be null).

@@ -209,14 +209,11 @@ cudaError_t run_unrotate(const SignBits &sg, const void *x, int64_t rows, void *
     if (items >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     UnrotParams p{x, out, rows, (uint32_t)items, inv_sqrt_head_dim(D), sg};
     auto kern = unrotate_kernel<D, IN_F32, OUT_F32>;
-    static int per_sm = 0;
-    if (!per_sm) {
-        int k = 0;
-        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k, kern, kUWarps * 32, 0);
-        if (e != cudaSuccess) return e;
-        per_sm = k > 0 ? k : 1;
-    }
-    const int grid = (int)imin64((items + kUWarps - 1) / kUWarps, (int64_t)num_sms() * per_sm);
+    static KernelSetup setup;
+    int per_sm;
+    const cudaError_t e = setup.get(kern, kUWarps * 32, 0, 0, per_sm);
+    if (e != cudaSuccess) return e;
+    const int grid = (int)imin64((items + kUWarps - 1) / kUWarps, (int64_t)num_sms() * (per_sm > 0 ? per_sm : 1));
     return launch_dependent(kern, dim3((unsigned)grid), dim3(kUWarps * 32), 0, s, p);
 }
 
