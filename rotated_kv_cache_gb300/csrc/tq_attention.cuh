@@ -205,8 +205,7 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
     uint32_t *done = reinterpret_cast<uint32_t *>(smem + A::RING + kStages * 8);
     const uint32_t full0 = smem_addr(bars);
 
-    // whatever the previous kernel on the stream writes or reads is settled (or, paged, no matter of this one)
-    const PdlWait order(PAGED && p.pg.late);
+    pdl_wait_primary();  // whatever the previous kernel on the stream writes or reads is settled
     pdl_allow_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // blockIdx.y = (kv-head, NBC blocks of kG q-heads); the CTAs of one kv-head

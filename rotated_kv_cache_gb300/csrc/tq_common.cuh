@@ -152,24 +152,6 @@ __device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.p
 __device__ __forceinline__ void pdl_allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// The wait of a kernel that may be independent of the one before it: at the
-// start, or, where `late`, at whichever end of the thread, so that the two run
-// side by side and the kernel after both still finds both complete.  Late is
-// right only where the kernel before lets its dependents start after its own
-// wait (everything older is complete then), and neither reads or overwrites
-// what the other writes.
-struct PdlWait {
-    bool late;
-    __device__ __forceinline__ explicit PdlWait(bool late_) : late(late_)
-    {
-        if (!late) pdl_wait_primary();
-    }
-    __device__ __forceinline__ ~PdlWait()
-    {
-        if (late) pdl_wait_primary();
-    }
-};
-
 // Launch `kern` as a programmatic dependent of the previous kernel on `s`.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args &&...args)

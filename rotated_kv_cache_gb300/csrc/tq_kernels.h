@@ -89,7 +89,6 @@ struct PagedSplit {
     int blocks;               // column blocks of a sequence's kv-head, at most
     int64_t wide;             // sequences with more new tokens than this are another kernel's
     int nch, ru;              // chunks per stage, rows per chunk
-    bool late;                // beside the expansion of long chunks' rows: independent of the kernel before
 };
 
 __host__ __device__ constexpr int gcd_int(int a, int b) { return b == 0 ? a : gcd_int(b, a % b); }
@@ -234,7 +233,7 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
 // ... of the wide sequences, by tcgen05 (head_dim 64 and 128).
 bool paged_wide_applies(const CacheView &c);
 size_t paged_wide_workspace_bytes(const CacheView &c, const PagedBounds &b, int QH);
-// `split` launches the other sequences' split kernel, beside the expansion of the rows.
+// `split` launches the other sequences' split kernel, behind the expansion of the rows.
 cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const PagedBounds &b, const uint16_t *q, int QH,
                               float scale, uint16_t *out, void *ws, cudaStream_t s,
                               const std::function<cudaError_t()> &split);

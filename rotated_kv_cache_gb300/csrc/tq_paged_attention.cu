@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
     __shared__ float wm[CW], wl[CW];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wid = warp % W, lead = warp - wid;
     const int64_t row = (int64_t)blockIdx.x * (CW / W) + warp / W;
-    const PdlWait order(p.pg.late);  // behind the merge of long chunks: the split kernel is complete before that starts
+    pdl_wait_primary();  // the partials are complete and visible
     pdl_allow_dependents();
     bool live = row < p.rows;
     int64_t t = live ? row / p.QH : 0;
@@ -297,7 +297,7 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
     if (ws_bytes < pl.bytes) return cudaErrorInvalidValue;
     uint8_t *base = static_cast<uint8_t *>(ws);
     const bool wide = pl.b.wide != INT32_MAX;
-    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<PagedUnit *>(base), pl.slots, pl.blocks, pl.b.wide, 1, 1, wide};
+    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<PagedUnit *>(base), pl.slots, pl.blocks, pl.b.wide, 1, 1};
     float *part_ml = reinterpret_cast<float *>(base + pl.off_ml), *part_o = reinterpret_cast<float *>(base + pl.off_o);
     auto split = [&]() -> cudaError_t {
         const int64_t cols = pl.cols;

@@ -993,9 +993,11 @@ WideSizes wide_sizes(const CacheView &c, const PagedBounds &b, int QH)
     return z;
 }
 
-// The split kernel of the other sequences needs nothing of plan and expand: it
-// is launched behind expand and does not wait for it until it ends, so the two
-// run side by side; likewise the combine behind merge.
+// The split kernel of the other sequences stands between expand and attend, their
+// combine behind merge: each waits for all of the kernel before it.  (Split
+// beside expand and combine beside merge, waiting at their ends, gained 2 to 10
+// us a call; but then they read pool, lengths and partials without a wait of
+// their own, which the programming model does not cover.)
 template <int D>
 cudaError_t wide_run(WideParams &p, cudaStream_t s, const std::function<cudaError_t()> &split)
 {
