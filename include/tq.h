@@ -319,8 +319,9 @@ TQ_API int tq_attention_supported(int32_t head_dim, int32_t k_bits, int32_t v_bi
  * graph serves changing batches; the host sees only the bounds max_len,
  * max_new and total.  The kernels check what they read: a page number outside
  * the pool ORs TQ_DEVICE_ERR_PAGE into the device error word, a length outside
- * [0, max_len], starts out of order, or lengths of more than total_len in all
- * (where the workspace is sized by it: attention of long chunks) OR
+ * [0, max_len], starts out of order, more new tokens of a sequence than max_new
+ * (attention; that sequence gets no results), or lengths of more than total_len
+ * in all (where the workspace is sized by it: attention of long chunks) OR
  * TQ_DEVICE_ERR_LENGTH; results are then unspecified (for a bad page, those
  * of its sequences), but nothing outside the pool, the outputs and the
  * workspace is ever touched.  A token that stands before its sequence's first row (more new

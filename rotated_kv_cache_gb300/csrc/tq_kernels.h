@@ -87,6 +87,7 @@ struct PagedSplit {
     PagedUnit *units;         // [seqs][H][blocks]: where a unit's partials are
     int64_t slots;            // partial slots of the workspace
     int blocks;               // column blocks of a sequence's kv-head, at most
+    int64_t max_new;          // bound of a sequence's new tokens, which sized the workspace and picked the kernel
     int64_t wide;             // sequences with more new tokens than this are another kernel's
     int nch, ru;              // chunks per stage, rows per chunk
 };

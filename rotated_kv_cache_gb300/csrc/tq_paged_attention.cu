@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
         s0 = paged_start(p.pg.v, s);
         n = paged_new(p.pg.v, s);
         len = paged_len(p.pg.v, s);
-        live = n <= p.pg.wide && t < n;
+        live = n <= p.pg.max_new && n <= p.pg.wide && t < n;
         t += s0;
     } else if (live) {
         int lo = 0, hi = p.pg.v.seqs + 1;
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
             s0 = paged_start(p.pg.v, s);
             n = paged_new(p.pg.v, s);
             len = paged_len(p.pg.v, s);
-            live = n <= p.pg.wide && t < s0 + n;
+            live = n <= p.pg.max_new && n <= p.pg.wide && t < s0 + n;
             if (live) load_unit(t - s0);
         }
     }
@@ -297,7 +297,7 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
     if (ws_bytes < pl.bytes) return cudaErrorInvalidValue;
     uint8_t *base = static_cast<uint8_t *>(ws);
     const bool wide = pl.b.wide != INT32_MAX;
-    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<PagedUnit *>(base), pl.slots, pl.blocks, pl.b.wide, 1, 1};
+    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<PagedUnit *>(base), pl.slots, pl.blocks, pl.b.max_new, pl.b.wide, 1, 1};
     float *part_ml = reinterpret_cast<float *>(base + pl.off_ml), *part_o = reinterpret_cast<float *>(base + pl.off_o);
     auto split = [&]() -> cudaError_t {
         const int64_t cols = pl.cols;

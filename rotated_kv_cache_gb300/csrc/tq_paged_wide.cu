@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(wPlanThreads) wide_plan_kernel(const __grid_co
         int64_t t = 0, e = 0, all;
         if (s < S) {
             const int64_t n = paged_new(p.pg.v, s);
-            if (n > p.pg.wide) {
+            if (n > p.pg.wide && n <= p.pg.max_new) {
                 const int64_t len = paged_len(p.pg.v, s);
                 t = len > 0 ? (len + wT - 1) / wT : 1;
                 e = (n * p.G + wC - 1) / wC;

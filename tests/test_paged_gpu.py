@@ -551,3 +551,33 @@ def test_a_group_of_more_q_heads_than_a_column_group(cuda, G):
     _attend(cuda, b, G)
     b.bound = 300
     _attend(cuda, b, G)
+
+
+@pytest.mark.parametrize("most,new", [(1, 3), (4, 6), (140, 200), (200, 201)])
+def test_more_new_tokens_than_the_bound(cuda, most, new):
+    """Starts that pass max_new when a captured call is replayed (one token a sequence, a few, long chunks): recorded,
+    the other sequences' results stand, and within the bound nothing is recorded."""
+    b = Batch([300, 150, 260], [most, 1, most], H=2, d=128, kb=8, vb=3, page=32, seed=most)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    rows = new + most + 1
+    q = b.queries(8, total=rows)
+    pages, starts = b.pages(cuda), b.dev(b.starts)
+    ws = torch.empty(cuda.tq_paged_attention_workspace_bytes(pool, pages, 8, rows, most), dtype=torch.uint8, device="cuda")
+    ws.fill_(0x11)
+    out = torch.zeros(rows, 8, 128, dtype=torch.bfloat16, device="cuda")
+    qd = q.cuda()
+    step = lambda: cuda.tq_paged_attention(pool, pages, starts, qd, most, out=out, workspace=ws)  # noqa: E731
+    step()
+    torch.cuda.synchronize()
+    assert cuda.tq_device_error() == 0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    g.replay()
+    check_attention(b, pool, q[:b.total], out[:b.total])
+    assert cuda.tq_device_error() == 0
+    starts.copy_(b.dev(np.array([0, new, new + 1, rows], np.int32)))
+    g.replay()
+    assert cuda.tq_device_error() == cuda.TQ_DEVICE_ERR_LENGTH
+    check_attention(b, pool, q[new:], out[new:], lens=[0, 150, 260], new=[0, 1, most])
