@@ -384,8 +384,9 @@ TQ_API size_t tq_paged_attention_workspace_bytes(const tq_cache *pool, const tq_
  *            for these bounds, 256-byte aligned, not initialised.  Calls that
  *            may run at the same time (other streams, graphs replayed
  *            together) need one each.
- * Scores and sums are fp32; keys, values and probabilities enter the tensor
- * cores as f16 (11 bits), which costs less than the output's rounding.  A
+ * Scores and sums are fp32 and keys keep 22 bits or their exact codes; values
+ * (centroid times rms) and probabilities enter the tensor cores as f16 (2^-12 of
+ * them each), less than the output's rounding.  A
  * row of the cache that a token does not see never reaches its output,
  * whatever it holds (NaN and infinities included); a row that it sees whose
  * value scale is not finite makes its output not finite (NaN, or infinite in

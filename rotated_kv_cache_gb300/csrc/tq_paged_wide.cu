@@ -7,10 +7,11 @@
 //
 //  1. plan     which sequences are wide (more new tokens than `wide`), their
 //              128-row tiles and 256-column blocks, as prefix sums;
-//  2. expand   every (128-row tile, kv-head) becomes two f16 operand tiles in
-//              the workspace, laid out as the images that the tensor cores
-//              read from shared memory (128-byte swizzle; keys K-major, values
-//              MN-major), so that a tile is one linear copy;
+//  2. expand   every (128-row tile, kv-head) becomes three f16 operand tiles
+//              in the workspace (keys as two terms, values), laid out as the
+//              images that the tensor cores read from shared memory (128-byte
+//              swizzle; keys K-major, values MN-major), so that a tile is one
+//              linear copy;
 //  3. attend   persistent CTAs of two 128-column groups: one warp copies
 //              tiles, one issues the MMAs, two warpgroups run the softmax (a
 //              thread per column);
@@ -21,20 +22,23 @@
 // the scores) and every value tile likewise; the value exponent e of a tile is
 // added to the base-2 scores, so that one accumulator holds
 //   O = sum_t 2^(s_t + e - R + 6) (v_t 2^-e),   l = sum_t 2^(s_t + e - R + 6) 2^-e
-// for any mixture of tiles, and O / l needs no correction.  The roundings are
-// those of k, v and p to f16 (2^-11 each), below the bf16 output's 2^-8.
+// for any mixture of tiles, and O / l needs no correction.  Values and weights
+// are rounded to f16 (2^-12 of them each), below the bf16 output's 2^-9.  A
+// rounding of a key enters the output times the score, so keys are held as
+// k = hi + lo (hi = f16(k), lo = f16(k - hi): 22 bits), and both terms' products
+// go into one accumulator.  With hi alone heavy-tailed keys, whose scores
+// reach 60, moved outputs of unit values by up to 0.025.
 // The reference R follows the running maximum of s + e lazily: it is raised
 // (and O rescaled) only when the maximum has grown by more than 2^8, so that
 // the weights stay within [0, 2^14] and keep 11 bits down to 2^-20 of the
 // largest.
 //
 // Measured: 2048 new tokens over 32768 rows, 64 q-heads, 8 kv-heads, head_dim
-// 128, 4-bit keys, 3-bit values: 1454 us in all, 1.46 PFLOP/s (of 1.87 that a
-// large library product reaches); a prompt of 8191 tokens 414 us, 1.33 (400 on another board).  At 1024
-// tokens over 8192 rows the tensor pipe is busy 69 % of the attend kernel's
-// time (expand 14 us, attend 158, merge 18, cold L2): the rest is the softmax
-// of a group where it takes longer than the other group's products, and the
-// starts and ends of blocks.
+// 128, 4-bit keys, 3-bit values: 2059 us in all, 1.03 PFLOP/s of the attention's
+// own products and 1.54 with the low terms' (of 1.87 that a large library
+// product reaches); a prompt of 8191 tokens 541 us, 1.02 and 1.53.  With hi alone
+// they took 1493 and 416: the tensor pipe has half as much work again, and
+// bounds the kernel.  The rest is the starts and ends of blocks.
 //
 // A value row with an infinity or NaN would spoil the sums of columns that do
 // not see it (0 * inf), so expand writes zeros there and a bit mask; a column
@@ -87,7 +91,7 @@ struct WideParams {
     const uint16_t *q;
     uint16_t *out;
     TileMeta *meta;      // [tile][H]
-    uint8_t *tiles;      // [tile][H][keys, values]
+    uint8_t *tiles;      // [tile][H][keys hi, keys lo, values]
     float *part_o, *part_ml;  // [2 CTAs][256][D], [..][256][2]
     uint32_t *err;
     int H, QH, G, kb, vb, ctas;
@@ -101,8 +105,12 @@ template <int D>
 struct WideGeo {
     static constexpr int KT = wT * D * 2;  // bytes of one operand tile
     static constexpr int NK = D == 128 ? 2 : 4, NV = NK;  // tiles in flight
-    static constexpr int OFF_K = 2 * KT, OFF_V = OFF_K + NK * KT, OFF_BAR = OFF_V + NV * KT;
-    static constexpr int SMEM = 1024 + OFF_BAR + 256;
+    // the keys' low terms in pieces of 64 dims: a tile's at head_dim 128, where no more fits, four at 64
+    static constexpr int LB = wT * 128, PL = D / 64, NL = D == 128 ? 2 : 4;
+    static constexpr int OFF_K = 2 * KT, OFF_L = OFF_K + NK * KT, OFF_V = OFF_L + NL * LB, OFF_BAR = OFF_V + NV * KT;
+    static constexpr int BARS = 2 * (NK + NL + NV) + 11;
+    static constexpr int SMEM = 1024 + OFF_BAR + (BARS * 8 + 4 + 127) / 128 * 128;
+    static_assert(SMEM + 1024 <= 227 * 1024);
     static constexpr int O_COL = 2 * wT;   // tensor memory: S (then P) of both groups, then O of both
 };
 
@@ -276,8 +284,8 @@ __device__ __forceinline__ void wide_next(const WideParams &p, WidePlace &w)
 // exponents from its scales alone (no pass over the codes), then eight
 // elements a thread to each operand tile in 16-byte words, the loads of four of
 // them together (with a load and a store at a time, 16 tokens over 4096 rows
-// took 1.4 us more in all).  It writes 4 d bytes a row and kv-head: 8192 rows of
-// 8 kv-heads, head_dim 128, are 34 MB, which the attend kernel finds in L2.
+// took 1.4 us more in all).  It writes 6 d bytes a row and kv-head: 8192 rows of
+// 8 kv-heads, head_dim 128, are 50 MB, which the attend kernel finds in L2.
 template <int D>
 __global__ void __launch_bounds__(256, 4) wide_expand_kernel(const __grid_constant__ WideParams p)
 {
@@ -355,7 +363,7 @@ __global__ void __launch_bounds__(256, 4) wide_expand_kernel(const __grid_consta
         // a tile of zeros takes the exponent of one whose largest value is 1
         const int ek = tile_exponent(bk), ev = tile_exponent(bv > 0.0f ? bv * p.cmax : 1.0f);
         const float sk = ldexpf(1.0f, ek), sv2 = ldexpf(1.0f, ev);
-        uint8_t *dst = p.tiles + item * (2 * KT);
+        uint8_t *dst = p.tiles + item * (3 * KT);
         if (tid == 0) {
             TileMeta m;
             m.kf = ldexpf(1.0f, -ek);
@@ -394,19 +402,29 @@ __global__ void __launch_bounds__(256, 4) wide_expand_kernel(const __grid_consta
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const int it = i0 + 256 * j, t = it / C8, c8 = it - t * C8;
-                uint4 k4 = make_uint4(0u, 0u, 0u, 0u), v4 = k4;
+                uint4 k4 = make_uint4(0u, 0u, 0u, 0u), l4 = k4, v4 = k4;
                 if (rows[t] >= 0) {
                     float x[8];
                     key_values<KB>(k0[j], k1[j], ((c8 * p.kb) & 3) * 8, p.kb, f16_bits_to_f32(ks[j]) * sk,
                                   magic - f16_bits_to_f32(kz[j]), x);
-                    k4 = make_uint4(tc_pack_f16(x[0], x[1]), tc_pack_f16(x[2], x[3]), tc_pack_f16(x[4], x[5]), tc_pack_f16(x[6], x[7]));
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        hi[i] = tc_pack_f16(x[2 * i], x[2 * i + 1]);
+                        const float2 h2 = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i]));
+                        const float a = x[2 * i] - h2.x, b = x[2 * i + 1] - h2.y;  // (not finite where k is not: none)
+                        lo[i] = tc_pack_f16(fabsf(a) < 1.0e30f ? a : 0.0f, fabsf(b) < 1.0e30f ? b : 0.0f);
+                    }
+                    k4 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    l4 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     if (!((bad[t >> 5] >> (t & 31)) & 1u)) {
                         value_values<VB>(v0[j], v1[j], (8 * c8 * p.vb) & 31, p.vb, f16_bits_to_f32(vs[j]) * sv2, smem_addr(lut), x);
                         v4 = make_uint4(tc_pack_f16(x[0], x[1]), tc_pack_f16(x[2], x[3]), tc_pack_f16(x[4], x[5]), tc_pack_f16(x[6], x[7]));
                     }
                 }
                 *reinterpret_cast<uint4 *>(dst + kmaj_off(wT, t, 8 * c8)) = k4;
-                *reinterpret_cast<uint4 *>(dst + KT + mnmaj_off<D>(t, 8 * c8)) = v4;
+                *reinterpret_cast<uint4 *>(dst + KT + kmaj_off(wT, t, 8 * c8)) = l4;
+                *reinterpret_cast<uint4 *>(dst + 2 * KT + mnmaj_off<D>(t, 8 * c8)) = v4;
             }
         };
         using std::integral_constant;
@@ -437,7 +455,10 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b)
 // Tensor memory holds S of both groups (128 columns each; P, f16, overwrites
 // its first half) and O of both.  In one pass over a tile the issuing warp
 // queues O_a += P_a V, S_a = Q_a K(next), then the same for the other group, so
-// that one group's softmax runs under the other's products.  MMAs of one
+// that one group's softmax runs under the other's products.  Shared memory has
+// room for two tiles of hi and of values but for one of lo at head_dim 128: group
+// a multiplies by lo last and group b first, so that its copy has the time of
+// group b's hi and of a's next products by values and hi.  MMAs of one
 // thread execute in order: S(t) complete says that P V(t - 1) is complete, so
 // the softmax threads may rescale O between reading S(t) and handing over P(t)
 // without a barrier of its own.
@@ -451,14 +472,15 @@ template <int D>
 __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_constant__ WideParams p)
 {
     using A = WideGeo<D>;
-    constexpr int KT = A::KT, NK = A::NK, NV = A::NV;
+    constexpr int KT = A::KT, NK = A::NK, NV = A::NV, NL = A::NL, PL = A::PL, LB = A::LB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + A::OFF_BAR);
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 2 * NK + 2 * NV + 11);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + A::BARS);
     const uint32_t sb = smem_addr(smem), b0 = smem_addr(bars);
     const uint32_t kfull = b0, kempty = kfull + 8 * NK, vfull = kempty + 8 * NK, vempty = vfull + 8 * NV;
-    const uint32_t qfull = vempty + 8 * NV, sfull = qfull + 16, pfull = sfull + 16, ofull = pfull + 32,
+    const uint32_t lfull = vempty + 8 * NV, lempty = lfull + 8 * NL;
+    const uint32_t qfull = lempty + 8 * NL, sfull = qfull + 16, pfull = sfull + 16, ofull = pfull + 32,
                    drained = ofull + 16;  // pfull: first halves, then second halves
     __shared__ WidePlace place[2][2];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -469,7 +491,7 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
     const int64_t x0 = blockIdx.x * per, x1 = imin64(total, x0 + per);
     if (x0 >= x1) return;
     if (tid == 0) {
-        for (int i = 0; i < 2 * NK + 2 * NV; ++i) mbar_init(b0 + 8 * i, 1);
+        for (int i = 0; i < 2 * (NK + NL + NV); ++i) mbar_init(b0 + 8 * i, 1);
         for (int g = 0; g < 2; ++g) {
             mbar_init(qfull + 8 * g, 4);  // a warp each
             mbar_init(sfull + 8 * g, 1);
@@ -495,29 +517,37 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
         if (warp == 9) {
             // ------------------------------------------------------------ tiles in
             if (lane == 0) {
+                // copy i of a ring of `ring` slots, once what was there has been used
+                auto copy = [&](uint32_t &i, uint32_t ring, uint32_t full, uint32_t empty, uint32_t at, const uint8_t *from,
+                                uint32_t bytes) {
+                    const uint32_t slot = i % ring;
+                    if (i >= ring && !mbar_wait_bounded(empty + 8 * slot, (i / ring - 1) & 1, p.err)) return false;
+                    mbar_arrive_expect_tx(full + 8 * slot, bytes);
+                    bulk_g2s(sb + at + slot * bytes, from, bytes, full + 8 * slot);
+                    ++i;
+                    return true;
+                };
                 bool ok = true;
-                uint32_t it = 0;
+                uint32_t nk = 0, nl = 0, nv = 0;  // copies made
                 WidePlace w = wide_locate(p, x0);
                 for (int n; ok && (n = w.count(x1)) > 0; wide_next(p, w)) {
-                    const uint8_t *src = p.tiles + ((int64_t)(w.tile0 + w.tile) * p.H + w.h) * (2 * KT);
-                    for (int t = 0; t < n && ok; ++t, ++it, src += (int64_t)p.H * (2 * KT)) {
-                        const uint32_t ks = it % NK, vs = it % NV;
-                        if (it >= NK) ok = mbar_wait_bounded(kempty + 8 * ks, (it / NK - 1) & 1, p.err);
-                        if (!ok) break;
-                        mbar_arrive_expect_tx(kfull + 8 * ks, KT);
-                        bulk_g2s(sb + A::OFF_K + ks * KT, src, KT, kfull + 8 * ks);
-                        if (it >= NV) ok = mbar_wait_bounded(vempty + 8 * vs, (it / NV - 1) & 1, p.err);
-                        if (!ok) break;
-                        mbar_arrive_expect_tx(vfull + 8 * vs, KT);
-                        bulk_g2s(sb + A::OFF_V + vs * KT, src + KT, KT, vfull + 8 * vs);
+                    const uint8_t *src = p.tiles + ((int64_t)(w.tile0 + w.tile) * p.H + w.h) * (3 * KT);
+                    for (int t = 0; t < n && ok; ++t, src += (int64_t)p.H * (3 * KT)) {
+                        ok = copy(nk, NK, kfull, kempty, A::OFF_K, src, KT);
+#pragma unroll
+                        for (int i = 0; i < PL; ++i) ok = ok && copy(nl, NL, lfull, lempty, A::OFF_L, src + KT + i * LB, LB);
+                        ok = ok && copy(nv, NV, vfull, vempty, A::OFF_V, src + 2 * KT, KT);
                     }
                     if (w.ends(x1)) break;
                 }
                 if (!ok) {  // copies still in flight land before the CTA ends (bounded)
-                    for (uint32_t i = it > (uint32_t)NK ? it - NK : 0; i <= it; ++i) {
-                        mbar_wait_bounded(kfull + 8 * (i % NK), (i / NK) & 1, p.err);
-                        if (i < it) mbar_wait_bounded(vfull + 8 * (i % NV), (i / NV) & 1, p.err);
-                    }
+                    auto land = [&](uint32_t n, uint32_t ring, uint32_t full) {
+                        for (uint32_t i = n > ring ? n - ring : 0; i < n; ++i)
+                            mbar_wait_bounded(full + 8 * (i % ring), (i / ring) & 1, p.err);
+                    };
+                    land(nk, NK, kfull);
+                    land(nl, NL, lfull);
+                    land(nv, NV, vfull);
                 }
             }
             __syncwarp();
@@ -525,26 +555,60 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
             // ------------------------------------------------------------ MMAs
             constexpr uint32_t idesc_qk = tc_idesc(128, wT, 0), idesc_pv = tc_idesc(128, D, 1), SBO = (D / 64) * 1024;
             const uint32_t leader = tc_elect();
-            // descriptors of the first q, key and value tile; 16-byte units are added to them
-            const uint64_t dq = tc_desc(sb, 16, 1024), dk = tc_desc(sb + A::OFF_K, 16, 1024),
-                           dv = tc_desc(sb + A::OFF_V, 1024, SBO);
+            // descriptors of the first q, key, low-term and value tile, low words (16-byte units are
+            // added to them) and high words (the same for the key side's)
+            const uint64_t d0 = tc_desc(sb, 16, 1024), v0 = tc_desc(sb + A::OFF_V, 1024, SBO);
+            const uint32_t dq = (uint32_t)d0, dk = dq + (A::OFF_K >> 4), dl = dq + (A::OFF_L >> 4), dv = (uint32_t)v0;
+            constexpr uint32_t hk = (uint32_t)(tc_desc_const(16, 1024) >> 32), hv = (uint32_t)(tc_desc_const(1024, SBO) >> 32);
+            auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t)hi << 32 | lo; };
             auto wait = [&](uint32_t bar, uint32_t parity) {  // the same answer in every lane
                 return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.err)) != 0;
             };
-            auto qk = [&](int g, uint32_t ks) {
+            // S_g = Q_g K(tile)^T: the first terms, and the low ones; `acc` where the others came before
+            auto high = [&](int g, uint32_t tile, uint32_t acc) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t o = ((kk / 4) * (wT * 128) + (kk % 4) * 32) >> 4;
-                    tc_mma_elected(leader, tmem + g * wT, dq + (g * KT >> 4) + o, dk + (ks * KT >> 4) + o, idesc_qk, kk > 0);
+                    tc_mma_elected(leader, tmem + g * wT, desc(hk, dq + (g * KT >> 4) + o), desc(hk, dk + (tile % NK * KT >> 4) + o), idesc_qk,
+                                   kk > 0 ? 1u : acc);
                 }
-                tc_commit_elected(leader, sfull + 8 * g);
+            };
+            auto low = [&](int g, uint32_t tile, int i, uint32_t acc) {  // piece i
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_elected(leader, tmem + g * wT, desc(hk, dq + ((g * KT + i * LB + kk * 32) >> 4)),
+                                   desc(hk, dl + (((tile * PL + i) % NL * LB + kk * 32) >> 4)), idesc_qk, kk > 0 ? 1u : acc);
+            };
+            // group a takes the low terms last and group b first: their slots are free for the next
+            // tile's a good way before that needs them
+            auto qk_a = [&](uint32_t tile) {
+                if (!wait(kfull + 8 * (tile % NK), (tile / NK) & 1)) return false;
+                tc_fence_after();
+                high(0, tile, 0);
+#pragma unroll
+                for (int i = 0; i < PL; ++i) {
+                    const uint32_t j = tile * PL + i;
+                    if (!wait(lfull + 8 * (j % NL), (j / NL) & 1)) return false;
+                    low(0, tile, i, 1);
+                }
+                return true;
+            };
+            auto qk_b = [&](uint32_t tile, bool two) {
+#pragma unroll
+                for (int i = 0; i < PL; ++i) {
+                    if (two) low(1, tile, i, i > 0);
+                    tc_commit_elected(leader, lempty + 8 * ((tile * PL + i) % NL));
+                }
+                if (two) high(1, tile, 1);
+                tc_commit_elected(leader, sfull + 8);
+                tc_commit_elected(leader, kempty + 8 * (tile % NK));
             };
             auto pv = [&](int g, uint32_t vs, int half, uint32_t acc) {
 #pragma unroll
                 for (int kk = 0; kk < wT / 32; ++kk) {
                     const int k = half * (wT / 32) + kk;
-                    tc_mma_ts_elected(leader, tmem + A::O_COL + g * D, tmem + g * wT + k * 8, dv + (vs * KT >> 4) + (k * 2 * SBO >> 4),
-                                      idesc_pv, kk > 0 ? 1u : acc);
+                    tc_mma_ts_elected(leader, tmem + A::O_COL + g * D, tmem + g * wT + k * 8,
+                                      desc(hv, dv + (vs * KT >> 4) + (k * 2 * SBO >> 4)), idesc_pv, kk > 0 ? 1u : acc);
                 }
             };
             bool ok = true;
@@ -556,19 +620,16 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 if (n == 0) break;
                 const bool two = __any_sync(0xffffffffu, w.n * p.G - (int64_t)(w.e - w.e0) * wC > 128) != 0;  // both groups have columns
                 // the idle group's threads keep step through the same barriers
-                ok = wait(kfull + 8 * (it % NK), (it / NK) & 1) && wait(qfull, seg & 1);
+                ok = wait(qfull, seg & 1) && qk_a(it);
                 if (!ok) break;
-                tc_fence_after();
-                qk(0, it % NK);
+                tc_commit_elected(leader, sfull);
                 ok = wait(qfull + 8, seg & 1);
                 if (!ok) break;
                 tc_fence_after();
-                if (two) qk(1, it % NK);
-                else tc_commit_elected(leader, sfull + 8);
-                tc_commit_elected(leader, kempty + 8 * (it % NK));
+                qk_b(it, two);
                 for (int t = 0; t < n; ++t, ++it) {
                     const bool more = t + 1 < n;
-                    const uint32_t vs = it % NV, nk = (it + 1) % NK;
+                    const uint32_t vs = it % NV;
                     ok = wait(vfull + 8 * vs, (it / NV) & 1) && wait(pfull, it & 1);
                     if (!ok) break;
                     tc_fence_after();
@@ -578,12 +639,10 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                     tc_fence_after();
                     pv(0, vs, 1, 1);
                     if (more) {
-                        ok = wait(kfull + 8 * nk, ((it + 1) / NK) & 1);
+                        ok = qk_a(it + 1);
                         if (!ok) break;
-                        qk(0, nk);
-                    } else {
-                        tc_commit_elected(leader, ofull);
                     }
+                    tc_commit_elected(leader, more ? sfull : ofull);
                     ok = wait(pfull + 8, it & 1);
                     if (!ok) break;
                     tc_fence_after();
@@ -593,13 +652,8 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                     tc_fence_after();
                     if (two) pv(1, vs, 1, 1);
                     tc_commit_elected(leader, vempty + 8 * vs);
-                    if (more) {
-                        if (two) qk(1, nk);
-                        else tc_commit_elected(leader, sfull + 8);
-                        tc_commit_elected(leader, kempty + 8 * nk);
-                    } else {
-                        tc_commit_elected(leader, ofull + 8);
-                    }
+                    if (more) qk_b(it + 1, two);
+                    else tc_commit_elected(leader, ofull + 8);
                 }
                 if (!ok || __any_sync(0xffffffffu, w.ends(x1))) break;
                 wide_next(p, w);
@@ -988,7 +1042,7 @@ WideSizes wide_sizes(const CacheView &c, const PagedBounds &b, int QH)
     z.off_meta = take((size_t)z.tiles * c.H * sizeof(TileMeta));
     z.off_ml = take(slots * 8);
     z.off_o = take(slots * c.d * 4);
-    z.off_tiles = take((size_t)z.tiles * c.H * 2 * wT * c.d * 2);
+    z.off_tiles = take((size_t)z.tiles * c.H * 3 * wT * c.d * 2);
     z.bytes = at;
     return z;
 }

@@ -12,10 +12,14 @@ namespace {
 // lbo / sbo in bytes (K-major tiles: sbo = 1024 between 8-row groups, lbo
 // unused; MN-major tiles: lbo between 64-element blocks of the M/N extent,
 // sbo between 8-row groups of K).
+__host__ __device__ constexpr uint64_t tc_desc_const(uint32_t lbo, uint32_t sbo)  // all but the address
+{
+    return (uint64_t)((lbo >> 4) & 0x3FFF) << 16 | (uint64_t)((sbo >> 4) & 0x3FFF) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
 __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo)
 {
-    return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 |
-           (uint64_t)((sbo >> 4) & 0x3FFF) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | tc_desc_const(lbo, sbo);
 }
 
 // Instruction descriptor, kind::f16: f16 A and B, f32 accumulator, M x N,

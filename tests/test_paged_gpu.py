@@ -581,3 +581,55 @@ def test_more_new_tokens_than_the_bound(cuda, most, new):
     g.replay()
     assert cuda.tq_device_error() == cuda.TQ_DEVICE_ERR_LENGTH
     check_attention(b, pool, q[new:], out[new:], lens=[0, 150, 260], new=[0, 1, most])
+
+
+def _synth_batch(tq_synth, lens, new, H, d, kb, vb, page, workload="decode"):
+    """A batch whose K and V are a workload's: heavy-tailed key channels (log-sigma 1.5), values of Student's t."""
+    b = Batch(lens, new, H=H, d=d, kb=kb, vb=vb, page=page)
+    bits = lambda x: torch.from_numpy(x.view(np.int16)).view(torch.bfloat16)  # noqa: E731
+    for s, n in enumerate(lens):
+        k, v = tq_synth.host_kv(tq_synth.WORKLOADS[workload], B=1, H=H, d=d, n=max(n, 1), b_offset=s)
+        b.k[s], b.v[s] = (bits(x)[0].transpose(0, 1).contiguous()[:n] for x in (k, v))
+    return b
+
+
+def _synth_queries(tq_synth, total, QH, d):
+    w = tq_synth.WORKLOADS["decode"]
+    return torch.from_numpy(np.stack([tq_synth.host_q(w, i, B=1, QH=QH, d=d)[0] for i in range(total)]).view(np.int16)) \
+        .view(torch.bfloat16)
+
+
+# Scores of these workloads deviate by 12 and reach 60, so a relative error of the keys is an error of the output 60
+# times its size and more: 11 bits of a key (2^-12 of it) would cost 9 times the tolerance.  With keys of two f16 terms
+# (2^-23) or exact codes only fp32 sums remain: 16 products of 16 terms into one accumulator, each rounding 2^-23 of
+# sums below 2^6 / 0.088, less than 2^-9 / 8 of a score; probabilities and values are rounded as in pagedtest.
+@pytest.mark.parametrize("d,kb,vb,page,lens,new", [
+    (128, 8, 3, 64, [4096], [128]), (128, 4, 3, 32, [4096], [128]), (128, 5, 2, 48, [1500, 700], [60, 700]),
+    (64, 8, 4, 64, [4096], [128]), (64, 4, 3, 16, [3000, 300, 1], [200, 17, 1]), (128, 8, 3, 64, [3000, 900], [1, 4]),
+])
+def test_heavy_tailed_keys(cuda, d, kb, vb, page, lens, new):
+    """The codec's own workload: long chunks keep the keys' precision, as the calls for contiguous caches do."""
+    import tq_synth
+
+    b = _synth_batch(tq_synth, lens, new, 2, d, kb, vb, page)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = _synth_queries(tq_synth, b.total, 16, d)
+    out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q.cuda(), max(new))
+    check_attention(b, pool, q, out)
+    assert cuda.tq_device_error() == 0
+
+
+@pytest.mark.parametrize("offset", [64.0, 200.0])
+@pytest.mark.parametrize("d,kb,new", [(128, 8, 130), (64, 8, 140), (128, 4, 150), (128, 8, 3)])
+def test_keys_with_an_offset(cuda, d, kb, new, offset):
+    """One group of 32 key channels far from zero, as keys of trained models have them, against queries of deviation
+    3.  The scores' common part, up to 3 * 200 * 32^.5 / 2^3.5, is exact to fp32 sums' 2^-20 of it: below 2^-11."""
+    b = Batch([900, 333], [new, min(new, 333)], H=2, d=d, kb=kb, vb=3, page=64, seed=71)
+    for s in range(2):
+        b.k[s][:, :, 32:64] = (b.k[s][:, :, 32:64].float() + offset).to(torch.bfloat16)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = (b.queries(8).float() * (3 / 1.3)).to(torch.bfloat16)
+    out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q.cuda(), new)
+    check_attention(b, pool, q, out)
