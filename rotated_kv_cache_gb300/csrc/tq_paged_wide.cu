@@ -28,6 +28,9 @@
 // k = hi + lo (hi = f16(k), lo = f16(k - hi): 22 bits), and both terms' products
 // go into one accumulator.  With hi alone heavy-tailed keys, whose scores
 // reach 60, moved outputs of unit values by up to 0.025.
+// A row may be far larger than others of its tile, and one that a column does
+// not see must not take bits from those that it sees: rows of tiles where sizes
+// spread too far have exponents of their own (RowMeta).
 // The reference R follows the running maximum of s + e lazily: it is raised
 // (and O rescaled) only when the maximum has grown by more than 2^8, so that
 // the weights stay within [0, 2^14] and keep 11 bits down to 2^-20 of the
@@ -65,9 +68,18 @@ struct __align__(16) TileMeta {
     float kf;       // 2^-ek: scores are (q k~) kf
     float e;        // the value tile's exponent: v = v~ 2^e
     float lf;       // 2^-e
-    uint32_t any;   // some value row is not finite
+    uint32_t any;   // bit 0: some value row is not finite; bit 1: every row has exponents of its own (RowMeta)
     uint32_t bad[4];
 };
+
+struct __align__(8) RowMeta {  // of a row of a tile whose rows are of very unlike sizes
+    float kf, e;               // as the tile's
+};
+// A tile gets them where its largest row is larger than its smallest (not zero)
+// by more than this: two f16 terms of a key 2^-16 of the tile's largest still keep
+// 2^-22 of it (the low term's last bit is 2^-38 of the largest), one of a value
+// 2^-24 of it 2^-12.
+constexpr float wSpreadK = 65536.0f, wSpreadV = 16777216.0f;
 
 struct WidePlan {        // device arrays, written by plan
     int32_t *tile0;      // [seqs + 1] scratch tiles before a sequence
@@ -91,6 +103,7 @@ struct WideParams {
     const uint16_t *q;
     uint16_t *out;
     TileMeta *meta;      // [tile][H]
+    RowMeta *row_meta;   // [tile][H][128], of tiles with rows of very unlike sizes
     uint8_t *tiles;      // [tile][H][keys hi, keys lo, values]
     float *part_o, *part_ml;  // [2 CTAs][256][D], [..][256][2]
     uint32_t *err;
@@ -293,7 +306,8 @@ __global__ void __launch_bounds__(256, 4) wide_expand_kernel(const __grid_consta
     static_assert(wT * C8 % 1024 == 0 && wT * NG % 256 == 0);
     __shared__ float lut[256];
     __shared__ int64_t rows[wT];   // plane row of each tile row (-1: none)
-    __shared__ float red[2][8];
+    __shared__ float row_k[wT], row_v[wT];  // bounds of each row, then its powers of two
+    __shared__ float red[4][8];
     __shared__ uint32_t bad[4];
     pdl_wait_primary();
     pdl_allow_dependents();
@@ -323,8 +337,8 @@ __global__ void __launch_bounds__(256, 4) wide_expand_kernel(const __grid_consta
             rows[tid] = r;
         }
         __syncthreads();
-        // bounds of the finite groups, and the value rows that are not finite
-        float bk = 0.0f, bv = 0.0f;
+        // bounds of the finite groups of all rows and of each, and the value rows that are not finite
+        float bk = 0.0f, bv = 0.0f, sk0 = INFINITY, sv0 = INFINITY;  // largest, and smallest of the rows that are not zero
         constexpr int MI = wT * NG / 256;
         uint16_t ms[MI], mz[MI], mv[MI];
 #pragma unroll
@@ -338,30 +352,61 @@ __global__ void __launch_bounds__(256, 4) wide_expand_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < MI; ++j) {
             const int t = (tid + 256 * j) / NG;
-            const float b = fabsf(f16_bits_to_f32(ms[j])) * (fabsf(f16_bits_to_f32(mz[j])) + p.kcmax);
-            const float v = fabsf(f16_bits_to_f32(mv[j]));
-            if (b < INFINITY) bk = fmaxf(bk, b);
-            if (v < INFINITY) bv = fmaxf(bv, v);
-            else atomicOr(&bad[t >> 5], 1u << (t & 31));
+            float b = fabsf(f16_bits_to_f32(ms[j])) * (fabsf(f16_bits_to_f32(mz[j])) + p.kcmax);
+            float v = fabsf(f16_bits_to_f32(mv[j]));
+            if (!(v < INFINITY)) atomicOr(&bad[t >> 5], 1u << (t & 31));
+            b = b < INFINITY ? b : 0.0f;
+            v = v < INFINITY ? v : 0.0f;
+#pragma unroll
+            for (int o = 1; o < NG; o <<= 1) {  // a row's groups are neighbouring lanes
+                b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            }
+            if ((tid & (NG - 1)) == 0) {
+                row_k[t] = b;
+                row_v[t] = v;
+            }
+            bk = fmaxf(bk, b);
+            bv = fmaxf(bv, v);
+            if (b > 0.0f) sk0 = fminf(sk0, b);
+            if (v > 0.0f) sv0 = fminf(sv0, v);
         }
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
+        for (int o = 16; o >= NG; o >>= 1) {
             bk = fmaxf(bk, __shfl_xor_sync(0xffffffffu, bk, o));
             bv = fmaxf(bv, __shfl_xor_sync(0xffffffffu, bv, o));
+            sk0 = fminf(sk0, __shfl_xor_sync(0xffffffffu, sk0, o));
+            sv0 = fminf(sv0, __shfl_xor_sync(0xffffffffu, sv0, o));
         }
         if (lane == 0) {
             red[0][warp] = bk;
             red[1][warp] = bv;
+            red[2][warp] = sk0;
+            red[3][warp] = sv0;
         }
         __syncthreads();
         bk = bv = 0.0f;
+        sk0 = sv0 = INFINITY;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
             bk = fmaxf(bk, red[0][w]);
             bv = fmaxf(bv, red[1][w]);
+            sk0 = fminf(sk0, red[2][w]);
+            sv0 = fminf(sv0, red[3][w]);
         }
         // a tile of zeros takes the exponent of one whose largest value is 1
-        const int ek = tile_exponent(bk), ev = tile_exponent(bv > 0.0f ? bv * p.cmax : 1.0f);
+        auto value_exponent = [&](float x) { return tile_exponent(x > 0.0f ? x * p.cmax : 1.0f); };
+        const int ek = tile_exponent(bk), ev = value_exponent(bv);
+        const bool mixed = bk > sk0 * wSpreadK || bv > sv0 * wSpreadV;  // (the same in every thread)
+        if (mixed) {
+            if (tid < wT) {
+                const int e1 = tile_exponent(row_k[tid]), e2 = value_exponent(row_v[tid]);
+                row_k[tid] = ldexpf(1.0f, e1);
+                row_v[tid] = ldexpf(1.0f, e2);
+                p.row_meta[item * wT + tid] = RowMeta{ldexpf(1.0f, -e1), (float)-e2};
+            }
+            __syncthreads();
+        }
         const float sk = ldexpf(1.0f, ek), sv2 = ldexpf(1.0f, ev);
         uint8_t *dst = p.tiles + item * (3 * KT);
         if (tid == 0) {
@@ -369,7 +414,7 @@ __global__ void __launch_bounds__(256, 4) wide_expand_kernel(const __grid_consta
             m.kf = ldexpf(1.0f, -ek);
             m.e = (float)-ev;
             m.lf = sv2;
-            m.any = bad[0] | bad[1] | bad[2] | bad[3];
+            m.any = ((bad[0] | bad[1] | bad[2] | bad[3]) != 0 ? 1u : 0u) | (mixed ? 2u : 0u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) m.bad[i] = bad[i];
             p.meta[item] = m;
@@ -405,7 +450,7 @@ __global__ void __launch_bounds__(256, 4) wide_expand_kernel(const __grid_consta
                 uint4 k4 = make_uint4(0u, 0u, 0u, 0u), l4 = k4, v4 = k4;
                 if (rows[t] >= 0) {
                     float x[8];
-                    key_values<KB>(k0[j], k1[j], ((c8 * p.kb) & 3) * 8, p.kb, f16_bits_to_f32(ks[j]) * sk,
+                    key_values<KB>(k0[j], k1[j], ((c8 * p.kb) & 3) * 8, p.kb, f16_bits_to_f32(ks[j]) * (mixed ? row_k[t] : sk),
                                   magic - f16_bits_to_f32(kz[j]), x);
                     uint32_t hi[4], lo[4];
 #pragma unroll
@@ -418,7 +463,7 @@ __global__ void __launch_bounds__(256, 4) wide_expand_kernel(const __grid_consta
                     k4 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     l4 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     if (!((bad[t >> 5] >> (t & 31)) & 1u)) {
-                        value_values<VB>(v0[j], v1[j], (8 * c8 * p.vb) & 31, p.vb, f16_bits_to_f32(vs[j]) * sv2, smem_addr(lut), x);
+                        value_values<VB>(v0[j], v1[j], (8 * c8 * p.vb) & 31, p.vb, f16_bits_to_f32(vs[j]) * (mixed ? row_v[t] : sv2), smem_addr(lut), x);
                         v4 = make_uint4(tc_pack_f16(x[0], x[1]), tc_pack_f16(x[2], x[3]), tc_pack_f16(x[4], x[5]), tc_pack_f16(x[6], x[7]));
                     }
                 }
@@ -450,6 +495,46 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b)
     uint32_t d;
     asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
+}
+
+// A tile whose rows have exponents of their own (their sizes are very unlike, so
+// that one exponent would leave some of them too few of f16's bits): this
+// column's true base-2 scores, value exponents added, in place of the products.
+// The thread goes on with those as with any tile's; the weights' sum, whose terms
+// need each row's value exponent, is taken here at the reference R that it will
+// choose.  Out of line: rare, and its registers are not the common path's.
+__device__ __noinline__ float mixed_tile(uint32_t t_s, const RowMeta *rm, float ie, int vis, float R)
+{
+    float mx = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < wT; c += 16) {
+        uint32_t x[16];
+        tc_ld16(t_s + c, x);
+        tc_wait_ld();
+        tc_pin(x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const RowMeta r = rm[c + j];
+            const float y = fmaf(__uint_as_float(x[j]), fmaxf(ie * r.kf, 1.17549435e-38f), r.e);
+            x[j] = c + j < vis ? __float_as_uint(y) : 0xFF800000u;
+            mx = fmaxf(mx, __uint_as_float(x[j]));
+        }
+        tc_st16(t_s + c, x);
+    }
+    tc_wait_st();
+    if (mx > R + wTau) R = mx;
+    const float add = R == -INFINITY ? 0.0f : wUp - R;
+#pragma unroll 1
+    for (int c = 0; c < wT; c += 16) {
+        uint32_t x[16];
+        tc_ld16(t_s + c, x);
+        tc_wait_ld();
+        tc_pin(x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)  // weight times 2^-e, |e| <= 100
+            sum = fmaf(tc_ex2(__uint_as_float(x[j]) + add), __int_as_float((127 - (int)rm[c + j].e) << 23), sum);
+    }
+    return sum;
 }
 
 // Tensor memory holds S of both groups (128 columns each; P, f16, overwrites
@@ -585,7 +670,7 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 if (!wait(kfull + 8 * (tile % NK), (tile / NK) & 1)) return false;
                 tc_fence_after();
                 high(0, tile, 0);
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < PL; ++i) {
                     const uint32_t j = tile * PL + i;
                     if (!wait(lfull + 8 * (j % NL), (j / NL) & 1)) return false;
@@ -594,7 +679,7 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 return true;
             };
             auto qk_b = [&](uint32_t tile, bool two) {
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < PL; ++i) {
                     if (two) low(1, tile, i, i > 0);
                     tc_commit_elected(leader, lempty + 8 * ((tile * PL + i) % NL));
@@ -739,15 +824,21 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
             const TileMeta *mt = p.meta + ((int64_t)(w.tile0 + w.tile) * p.H + w.h);
             float R = -INFINITY, l = 0.0f;
             for (int t = 0; t < n; ++t, ++it, mt += p.H, left -= wT) {
-                const float e = mt->e, lf = mt->lf;
+                float e = mt->e, lf = mt->lf;
                 // (a scale of zero: the smallest normal, so that hidden scores stay -inf)
-                const float f = fmaxf(ie * mt->kf, 1.17549435e-38f);
+                float f = fmaxf(ie * mt->kf, 1.17549435e-38f);
                 const uint32_t any = mt->any;
                 const int vis = left < 0 ? 0 : (left > wT ? wT : left);
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar_s, it & 1, p.err));
                 if (!ok) break;
                 tc_fence_after();
-                if (__any_sync(0xffffffffu, vis < wT)) {  // some column does not see the whole tile: its hidden scores become -inf
+                float extra = 0.0f;
+                if (any & 2u) {
+                    // rows of exponents of their own: true scores now, and the sum of the weights
+                    extra = mixed_tile(t_s, p.row_meta + (mt - p.meta) * wT, ie, vis, R);
+                    f = 1.0f;
+                    e = lf = 0.0f;
+                } else if (__any_sync(0xffffffffu, vis < wT)) {  // some column does not see the whole tile: its hidden scores become -inf
 #pragma unroll 1
                     for (int c = 0; c < wT; c += 16) {
                         uint32_t x[16];
@@ -841,8 +932,8 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 weights(2, add);
                 weights(3, add);
                 hand(bar_p + 16);
-                l = fmaf((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y), lf, l);
-                if (any) {
+                l = fmaf((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y), lf, l + extra);
+                if (any & 1u) {
 #pragma unroll 1
                     for (int i = 0; i < 4; ++i) {
                         const int rows = vis - 32 * i;
@@ -1017,7 +1108,7 @@ __global__ void __launch_bounds__(256) wide_merge_kernel(const __grid_constant__
 // ---------------------------------------------------------------- host side
 struct WideSizes {
     int64_t tiles, entries;
-    size_t off_tile0, off_entry0, off_before, off_line, off_share, off_meta, off_ml, off_o, off_tiles, bytes;
+    size_t off_tile0, off_entry0, off_before, off_line, off_share, off_meta, off_rows, off_ml, off_o, off_tiles, bytes;
 };
 
 WideSizes wide_sizes(const CacheView &c, const PagedBounds &b, int QH)
@@ -1040,6 +1131,7 @@ WideSizes wide_sizes(const CacheView &c, const PagedBounds &b, int QH)
     z.off_line = take(16);
     z.off_share = take((size_t)num_sms() * sizeof(WideShare));
     z.off_meta = take((size_t)z.tiles * c.H * sizeof(TileMeta));
+    z.off_rows = take((size_t)z.tiles * c.H * wT * sizeof(RowMeta));
     z.off_ml = take(slots * 8);
     z.off_o = take(slots * c.d * 4);
     z.off_tiles = take((size_t)z.tiles * c.H * 3 * wT * c.d * 2);
@@ -1095,6 +1187,7 @@ cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const Pa
     p.q = q;
     p.out = out;
     p.meta = reinterpret_cast<TileMeta *>(w + z.off_meta);
+    p.row_meta = reinterpret_cast<RowMeta *>(w + z.off_rows);
     p.tiles = w + z.off_tiles;
     p.part_o = reinterpret_cast<float *>(w + z.off_o);
     p.part_ml = reinterpret_cast<float *>(w + z.off_ml);

@@ -633,3 +633,70 @@ def test_keys_with_an_offset(cuda, d, kb, new, offset):
     q = (b.queries(8).float() * (3 / 1.3)).to(torch.bfloat16)
     out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q.cuda(), new)
     check_attention(b, pool, q, out)
+
+
+@pytest.mark.parametrize("d,kb,new", [(128, 8, 150), (64, 4, 300), (128, 8, 4), (256, 8, 20)])
+def test_hidden_rows_may_be_huge(cuda, d, kb, new):
+    """Finite keys of 2^32 and values of 2^16 in a later row of the chunk change nothing for the tokens before it,
+    rows of ordinary and of tiny keys (2^-20) in the same 128 among them."""
+    b = Batch([new + 50, 77], [new, 1], H=2, d=d, kb=kb, vb=3, page=64, seed=3)
+    for t in range(50, 50 + new, 7):
+        b.k[0][t] = b.k[0][t] * 2.0 ** -20
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    at = 50 + new * 3 // 4
+    row = (int(b.table[0, at // 64]), slice(None), at % 64)
+    q = b.queries(8)
+    args = (pool, b.pages(cuda), b.dev(b.starts), q.cuda(), new)
+    plain = cuda.tq_paged_attention(*args)
+    check_attention(b, pool, q, plain)
+    pool.k_scale[row], pool.k_zero[row], pool.v_scale[row] = 0x7BFF, 0x7BFF, 0x7BFF  # 65504
+    out = cuda.tq_paged_attention(*args)
+    seen = new * 3 // 4
+    keep = torch.ones(len(q), dtype=torch.bool)
+    keep[seen:new] = False
+    # the tokens before the row: as without it, to the tolerance against the plain implementation
+    check_attention(b, pool, q[:seen], out[:seen], lens=[50 + seen, 0], new=[seen, 0])
+    assert torch.equal(out[new:], plain[new:])
+    assert bool(out[seen:new].float().isfinite().all())
+    assert cuda.tq_device_error() == 0
+
+
+@pytest.mark.parametrize("d,kb,vb,new", [(128, 8, 3, 150), (64, 8, 4, 300), (128, 4, 3, 140), (128, 8, 3, 3)])
+def test_far_outliers_that_every_token_sees(cuda, d, kb, vb, new):
+    """Rows with keys of up to 2^20 that all queries point away from: no weight of theirs is left, and the other rows
+    of their 128 keep their precision; rows with values of 2^-14 beside them."""
+    b = Batch([new + 400, 200], [new, min(new, 200)], H=2, d=d, kb=kb, vb=vb, page=64, seed=9)
+    way = np.where(np.arange(d) % 2, 1.0, -1.0).astype(np.float32)
+    q = b.queries(8).float()
+    q = q + torch.from_numpy(way) * (4.0 - (q * torch.from_numpy(way)).mean(-1, keepdim=True))  # mean along `way`: 4
+    q = q.to(torch.bfloat16)
+    for s in range(2):
+        for t, size in ((3, 2.0 ** 20), (64, 2.0 ** 14), (150, 2.0 ** 18)):
+            b.k[s][t] = (torch.from_numpy(-size * way) * (1 + 0.25 * torch.rand(2, 1))).to(torch.bfloat16)
+        b.v[s][8:16] = b.v[s][8:16] * 2.0 ** -14
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q.cuda(), new)
+    check_attention(b, pool, q, out)
+    assert cuda.tq_device_error() == 0
+
+
+def test_values_of_very_unlike_sizes(cuda):
+    """Values of 2^-14 (group rms the smallest normal fp16 numbers) in the rows that tokens of a chunk see, 65504 in a
+    row of the same 128 that they do not: f16 weights and values of exponents of their own keep 2^-12 of each."""
+    new = 150
+    b = Batch([new + 20], [new], H=2, d=128, kb=8, vb=3, page=64, seed=12)
+    size = 2.0 ** -13
+    b.v[0] = (b.v[0].float() * size).to(torch.bfloat16)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    at, seen = 20 + 120, 120
+    pool.v_scale[int(b.table[0, at // 64]), :, at % 64] = 0x7BFF
+    q = b.queries(8)
+    out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q.cuda(), new)
+    from pagedtest import ATOL, RTOL, attention64, dequantised
+    k, v = dequantised(pool, b.table[0], 20 + new)
+    want = attention64(q[:seen], k[:, :20 + seen], v[:, :20 + seen], 20)
+    err = (out[:seen].cpu().double() - want).abs() - RTOL * want.abs()
+    assert float(err.max()) <= ATOL * size, float(err.max()) / size
