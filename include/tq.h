@@ -364,7 +364,13 @@ TQ_API tq_status tq_paged_decode(const tq_cache *pool, const tq_page_table *tabl
                                  tq_dtype out_dtype, void *k_out, void *v_out, tq_stream_t stream);
 
 /* Workspace bytes tq_paged_attention needs for these bounds (0 if invalid);
- * the table's device arrays are not read. */
+ * the table's device arrays are not read.  Partial results take about 520 bytes
+ * per (token, q-head) at head_dim 128; long chunks (128 columns of a kv-head and
+ * more, head_dims 64 and 128) take 6 d bytes per row of their sequences and
+ * kv-head beside them, for as many rows as the bounds allow (total_len, or
+ * num_seqs * max_len), but 8 GiB at most: where a batch's chunks pass that, the
+ * last ones go to the kernels without expanded rows, with the same results and
+ * more time. */
 TQ_API size_t tq_paged_attention_workspace_bytes(const tq_cache *pool, const tq_page_table *table, int32_t q_heads,
                                                  int64_t total, int64_t max_new);
 

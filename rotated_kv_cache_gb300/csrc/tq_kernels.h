@@ -89,6 +89,7 @@ struct PagedSplit {
     int blocks;               // column blocks of a sequence's kv-head, at most
     int64_t max_new;          // bound of a sequence's new tokens, which sized the workspace and picked the kernel
     int64_t wide;             // sequences with more new tokens than this are another kernel's
+    const int32_t *spill;     // [seqs], or null: but for those marked here
     int nch, ru;              // chunks per stage, rows per chunk
 };
 
@@ -234,6 +235,10 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
 // ... of the wide sequences, by tcgen05 (head_dim 64 and 128).
 bool paged_wide_applies(const CacheView &c);
 size_t paged_wide_workspace_bytes(const CacheView &c, const PagedBounds &b, int QH);
+// The workspace holds tiles for a bounded number of rows: whether the bounds allow more, and the
+// sequences whose chunks found no room, which the split kernels take (null: there are none).
+bool paged_wide_spills(const CacheView &c, const PagedBounds &b, int QH);
+int32_t *paged_wide_spill(const CacheView &c, const PagedBounds &b, int QH, void *ws);
 // `split` launches the other sequences' split kernel, behind the expansion of the rows.
 cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const PagedBounds &b, const uint16_t *q, int QH,
                               float scale, uint16_t *out, void *ws, cudaStream_t s,

@@ -162,6 +162,12 @@ __device__ __forceinline__ int64_t paged_row(const PagedView &v, const PagedLane
 // (64 sequences of 2048 rows) 40.8, 40.3 and 43.3.
 constexpr int kSegStart = 2;
 
+// Whether sequence s, of n new tokens, is the split kernels'.
+__device__ __forceinline__ bool paged_split_takes(const PagedSplit &ps, int s, int64_t n)
+{
+    return n <= ps.max_new && (n <= ps.wide || (ps.spill && ps.spill[s]));
+}
+
 // Stages and units of sequence s (none where it has no rows, no new tokens, or too many: those of long chunks are
 // another kernel's, more than the call's bound nobody's).
 __device__ __forceinline__ void paged_shape(const PagedSplit &ps, int s, int ST, int CB, int H, int G, int &stages, int &units)
@@ -170,7 +176,7 @@ __device__ __forceinline__ void paged_shape(const PagedSplit &ps, int s, int ST,
     if (s >= ps.v.seqs) return;
     const int64_t n = paged_new(ps.v, s), len = paged_len(ps.v, s);
     if (n > ps.max_new) atomicOr(ps.v.err, kErrLength);
-    if (n == 0 || n > ps.max_new || n > ps.wide || len == 0) return;
+    if (n == 0 || len == 0 || !paged_split_takes(ps, s, n)) return;
     stages = (int)((uint32_t)(len + ST - 1) / (uint32_t)ST);
     units = (int)((uint32_t)(n * G + CB - 1) / (uint32_t)CB) * H;
 }

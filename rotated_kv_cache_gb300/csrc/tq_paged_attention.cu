@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
         s0 = paged_start(p.pg.v, s);
         n = paged_new(p.pg.v, s);
         len = paged_len(p.pg.v, s);
-        live = n <= p.pg.max_new && n <= p.pg.wide && t < n;
+        live = t < n && paged_split_takes(p.pg, s, n);
         t += s0;
     } else if (live) {
         int lo = 0, hi = p.pg.v.seqs + 1;
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
             s0 = paged_start(p.pg.v, s);
             n = paged_new(p.pg.v, s);
             len = paged_len(p.pg.v, s);
-            live = n <= p.pg.max_new && n <= p.pg.wide && t < s0 + n;
+            live = t < s0 + n && paged_split_takes(p.pg, s, n);
             if (live) load_unit(t - s0);
         }
     }
@@ -224,7 +224,7 @@ bool generic_shape(const CacheView &c, int64_t cols, PagedShape &sh)
 struct PagedPlan {
     PagedShape split;
     bool special;   // the specialised split kernel, else the generic one
-    int64_t cols;   // most columns of a kv-head that the split kernels see
+    int64_t per_seq, cols;  // most new tokens of a sequence, and columns of a kv-head, that the split kernels see
     PagedBounds b;
     int64_t slots;
     int blocks;
@@ -250,12 +250,12 @@ bool paged_plan(const CacheView &c, const PagedBounds &bounds, int QH, PagedPlan
     const int64_t G = QH / c.H;
     pl.b = bounds;
     const int64_t most = pl.b.max_new * G;  // columns of the largest sequence
-    // (and its tiles are counted in 32 bits, its workspace in 64: bounds far above any memory go to the split kernels)
-    const bool work = most >= kWideColumns && pl.b.total_len >= (kWideWork + c.H * most - 1) / (c.H * most) &&
-                      pl.b.total_len < (int64_t(1) << 37) / c.H;
+    const bool work = most >= kWideColumns && pl.b.total_len >= (kWideWork + c.H * most - 1) / (c.H * most);
     pl.b.wide = paged_wide_applies(c) && work ? (kWideColumns - 1) / G : INT32_MAX;
     const bool wide = pl.b.wide != INT32_MAX;
-    pl.cols = (wide ? (pl.b.wide > 0 ? pl.b.wide : 1) : pl.b.max_new) * G;
+    // new tokens of a sequence that the split kernels see, at most
+    pl.per_seq = wide && !paged_wide_spills(c, pl.b, QH) ? (pl.b.wide > 0 ? pl.b.wide : 1) : pl.b.max_new;
+    pl.cols = pl.per_seq * G;
     // the specialised kernel where it has the widths (its tensor copies count rows in 32 bits)
     pl.special = attention_supported(c.d, c.kb, c.vb, (int)G) && (int64_t)c.B * c.H * c.cap < (int64_t(1) << 31);
     if (pl.special)
@@ -297,7 +297,8 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
     if (ws_bytes < pl.bytes) return cudaErrorInvalidValue;
     uint8_t *base = static_cast<uint8_t *>(ws);
     const bool wide = pl.b.wide != INT32_MAX;
-    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<PagedUnit *>(base), pl.slots, pl.blocks, pl.b.max_new, pl.b.wide, 1, 1};
+    PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<PagedUnit *>(base), pl.slots, pl.blocks, pl.b.max_new, pl.b.wide,
+                  wide ? paged_wide_spill(c, pl.b, QH, base + pl.off_wide) : nullptr, 1, 1};
     float *part_ml = reinterpret_cast<float *>(base + pl.off_ml), *part_o = reinterpret_cast<float *>(base + pl.off_o);
     auto split = [&]() -> cudaError_t {
         const int64_t cols = pl.cols;
@@ -322,10 +323,9 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
     // by places per sequence where that goes through fewer rows (a decode step: no
     // search for a token's sequence; a long chunk: none of its tokens).  32
     // sequences of 4096 rows: 61.5 us so, 62.9 token by token
-    const int64_t per_seq = pl.b.max_new < pl.b.wide ? pl.b.max_new : (pl.b.wide > 0 ? pl.b.wide : 1);
-    const bool by_seq = v.seqs * per_seq <= v.total;
+    const bool by_seq = v.seqs * pl.per_seq <= v.total;
     PagedCombineParams cp{part_o, part_ml, out, pg, c.H, QH, QH / c.H, pl.split.block,
-                          (by_seq ? v.seqs * per_seq : v.total) * QH, by_seq ? (int)per_seq : 0, inv_sqrt_head_dim(c.d),
+                          (by_seq ? v.seqs * pl.per_seq : v.total) * QH, by_seq ? (int)pl.per_seq : 0, inv_sqrt_head_dim(c.d),
                           c.signs};
     switch (c.d) {
     case 64: return run_combine<64>(cp, s);

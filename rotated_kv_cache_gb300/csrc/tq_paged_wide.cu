@@ -98,6 +98,7 @@ struct WideParams {
     PagedSplit pg;
     WidePlan pl;
     int64_t max_tiles, max_entries;  // room in the workspace
+    int32_t *spill;      // [seqs]: a long chunk that found no room (null: the bounds leave room for all)
     const uint8_t *k_codes, *v_codes;
     const uint16_t *k_scale, *k_zero, *v_scale;
     const uint16_t *q;
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(wPlanThreads) wide_plan_kernel(const __grid_co
     pdl_wait_primary();
     pdl_allow_dependents();
     const int S = p.pg.v.seqs;
-    int64_t tiles = 0, entries = 0;
+    int64_t want = 0, tiles = 0, entries = 0;  // tiles that all would take; tiles and blocks given
     for (int s0 = 0; s0 < S; s0 += blockDim.x) {
         const int s = s0 + threadIdx.x;
         int64_t t = 0, e = 0, all;
@@ -171,19 +172,26 @@ __global__ void __launch_bounds__(wPlanThreads) wide_plan_kernel(const __grid_co
                 e = (n * p.G + wC - 1) / wC;
             }
         }
+        // the first sequences that fit get tiles; the others are the split kernel's, or where the
+        // bounds that the caller gave left no room, nobody's
+        const bool fits = want + block_exclusive_sum(t, all, sh) + t <= p.max_tiles;
+        want += all;
+        if (s < S) {
+            if (p.spill) p.spill[s] = e > 0 && !fits;
+            else if (e > 0 && !fits) atomicOr(p.err, kErrLength);
+        }
+        if (!fits) t = e = 0;
         const int64_t at = tiles + block_exclusive_sum(t, all, sh);
         tiles += all;
         const int64_t ae = entries + block_exclusive_sum(e, all, sh);
         entries += all;
-        // sequences for which the bounds that the workspace was sized by left no room get nothing
         if (s < S) {
-            if (e > 0 && (at + t > p.max_tiles || ae + e > p.max_entries)) atomicOr(p.err, kErrLength);
-            p.pl.tile0[s] = (int32_t)imin64(at, p.max_tiles);
+            if (ae + e > p.max_entries) atomicOr(p.err, kErrLength);
+            p.pl.tile0[s] = (int32_t)at;
             p.pl.entry0[s] = (int32_t)imin64(ae, p.max_entries);
         }
     }
-    const bool room = tiles <= p.max_tiles && entries <= p.max_entries;
-    if (!room) tiles = entries = 0;
+    if (entries > p.max_entries) tiles = entries = 0;  // (starts out of order)
     if (threadIdx.x == 0) {
         p.pl.tile0[S] = (int32_t)tiles;
         p.pl.entry0[S] = (int32_t)entries;
@@ -1106,9 +1114,16 @@ __global__ void __launch_bounds__(256) wide_merge_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- host side
+// Most bytes of expanded tiles in a workspace.  Bounds that are far above a
+// batch's real lengths (256 slots of up to 131072 rows, 8 kv-heads, head_dim 128)
+// would ask for 200 GB of them; chunks over 1.4 M real rows at a time go by the
+// expanded tiles, and further ones of such a call by the split kernels.
+constexpr int64_t kWideScratch = int64_t(8) << 30;
+
 struct WideSizes {
     int64_t tiles, entries;
-    size_t off_tile0, off_entry0, off_before, off_line, off_share, off_meta, off_rows, off_ml, off_o, off_tiles, bytes;
+    bool spills;  // there may be chunks that find no room
+    size_t off_spill, off_tile0, off_entry0, off_before, off_line, off_share, off_meta, off_rows, off_ml, off_o, off_tiles, bytes;
 };
 
 WideSizes wide_sizes(const CacheView &c, const PagedBounds &b, int QH)
@@ -1116,7 +1131,10 @@ WideSizes wide_sizes(const CacheView &c, const PagedBounds &b, int QH)
     WideSizes z{};
     const int64_t G = QH / c.H;
     const int64_t most = imin64(b.seqs, b.total / (b.wide + 1));  // sequences that can be wide
-    z.tiles = imin64(most * ((b.max_len + wT - 1) / wT), b.total_len / wT + most);
+    const int64_t bound = imin64(most * ((b.max_len + wT - 1) / wT), b.total_len / wT + most);
+    const int64_t tile_bytes = c.H * (3 * wT * c.d * 2 + wT * sizeof(RowMeta) + sizeof(TileMeta));
+    z.tiles = imin64(bound, kWideScratch / tile_bytes);
+    z.spills = z.tiles < bound;
     z.entries = b.total * G / wC + most;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -1125,6 +1143,7 @@ WideSizes wide_sizes(const CacheView &c, const PagedBounds &b, int QH)
         return o;
     };
     const size_t slots = 2 * (size_t)num_sms() * wC;
+    z.off_spill = take((size_t)b.seqs * 4);
     z.off_tile0 = take((size_t)(b.seqs + 1) * 4);
     z.off_entry0 = take((size_t)(b.seqs + 1) * 4);
     z.off_before = take((size_t)(z.entries + 1) * 8);
@@ -1152,7 +1171,7 @@ cudaError_t wide_run(WideParams &p, cudaStream_t s, const std::function<cudaErro
     if (e != cudaSuccess) return e;
     e = launch_dependent(wide_plan_kernel, dim3(1), dim3(wPlanThreads), 0, s, p);
     if (e != cudaSuccess) return e;
-    const int64_t items = p.max_tiles * p.H;
+    const int64_t items = p.max_tiles > 0 ? p.max_tiles * p.H : 1;
     e = launch_dependent(wide_expand_kernel<D>, dim3((unsigned)imin64(items, (int64_t)num_sms() * 8)), dim3(256), 0, s, p);
     if (e != cudaSuccess) return e;
     if ((e = split()) != cudaSuccess) return e;
@@ -1167,6 +1186,14 @@ bool paged_wide_applies(const CacheView &c) { return c.d == 64 || c.d == 128; }
 
 size_t paged_wide_workspace_bytes(const CacheView &c, const PagedBounds &b, int QH) { return wide_sizes(c, b, QH).bytes; }
 
+bool paged_wide_spills(const CacheView &c, const PagedBounds &b, int QH) { return wide_sizes(c, b, QH).spills; }
+
+int32_t *paged_wide_spill(const CacheView &c, const PagedBounds &b, int QH, void *ws)
+{
+    const WideSizes z = wide_sizes(c, b, QH);
+    return z.spills ? reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + z.off_spill) : nullptr;
+}
+
 cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const PagedBounds &b, const uint16_t *q, int QH,
                               float scale, uint16_t *out, void *ws, cudaStream_t s,
                               const std::function<cudaError_t()> &split)
@@ -1179,6 +1206,7 @@ cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const Pa
                     reinterpret_cast<int64_t *>(w + z.off_before), reinterpret_cast<int64_t *>(w + z.off_line), reinterpret_cast<WideShare *>(w + z.off_share)};
     p.max_tiles = z.tiles;
     p.max_entries = z.entries;
+    p.spill = paged_wide_spill(c, b, QH, ws);
     p.k_codes = c.k_codes;
     p.v_codes = c.v_codes;
     p.k_scale = c.k_scale;

@@ -700,3 +700,36 @@ def test_values_of_very_unlike_sizes(cuda):
     want = attention64(q[:seen], k[:, :20 + seen], v[:, :20 + seen], 20)
     err = (out[:seen].cpu().double() - want).abs() - RTOL * want.abs()
     assert float(err.max()) <= ATOL * size, float(err.max()) / size
+
+
+def test_more_long_chunks_than_the_workspace_expands(cuda):
+    """14 chunks over 131072 rows of 8 kv-heads each (one prefix of 512 rows, repeated, so that no memory is needed for
+    them): 11 GiB expanded, of which the workspace holds 8.  All against the plain implementation, whose softmax counts
+    every row of the prefix as often as it is seen."""
+    S, H, d, P, n, new, QH = 14, 8, 128, 128, 131072, 20, 64
+    b = Batch([512], [0], H=H, d=d, kb=4, vb=2, page=P, spare=0, seed=77)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    order = b.table[0, :4]
+    table = b.dev(np.tile(order, (S, n // 512)).astype(np.int32))
+    lens = [n - 37 * s for s in range(S)]
+    pages = cuda.PageTable(table, b.dev(np.array(lens, np.int32)), n)
+    new_of = [new - (s % 3) for s in range(S)]
+    starts = np.concatenate([[0], np.cumsum(new_of)]).astype(np.int32)
+    q = b.queries(QH, total=int(starts[-1]))
+    need = cuda.tq_paged_attention_workspace_bytes(pool, pages, QH, len(q), new)
+    assert 8 << 30 <= need < 9 << 30
+    out = cuda.tq_paged_attention(pool, pages, b.dev(starts), q.cuda(), new).cpu().double()
+    assert cuda.tq_device_error() == 0
+    from pagedtest import ATOL, RTOL, dequantised
+    k, v = (torch.from_numpy(x).double() for x in dequantised(pool, order, 512))
+    worst = 0.0
+    for s in range(S):
+        for i in (0, new_of[s] // 2, new_of[s] - 1):
+            seen = lens[s] - new_of[s] + i + 1
+            times = torch.tensor([(seen - r + 511) // 512 for r in range(512)], dtype=torch.float64)
+            x = q[starts[s] + i].double().view(H, QH // H, d)
+            p = torch.softmax(torch.einsum("hgd,hnd->hgn", x, k) * d ** -0.5 + times.log(), -1)
+            want = torch.einsum("hgn,hnd->hgd", p, v).reshape(QH, d)
+            worst = max(worst, float(((out[starts[s] + i] - want).abs() - RTOL * want.abs()).max()))
+    assert worst <= ATOL, worst

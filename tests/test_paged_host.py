@@ -229,3 +229,21 @@ def test_bounds_above_any_memory(tqlib):
         if seqs * max_len * H >= 1 << 37:
             assert new < seqs * max_len * H
         last = new
+
+
+def test_workspace_of_ordinary_serving_bounds(tqlib):
+    """Slots and lengths as a server states them once and for all, far above what a batch holds: a bounded workspace,
+    and a smaller one where the sum of the lengths is known."""
+    L, ref = tqlib.lib(), ctypes.byref
+    pool = _struct(tqlib, head_dim=128, num_kv_heads=8, batch=20000, capacity=64, v_bits=3)
+
+    def size(seqs, max_len, total, new, total_len=0):
+        table = _table(tqlib, num_seqs=seqs, max_len=max_len, stride=max_len // 64, total_len=total_len)
+        return L.tq_paged_attention_workspace_bytes(ref(pool), ref(table), 64, total, new)
+
+    gib = 1 << 30
+    for seqs, max_len, total, new in ((256, 131072, 8192, 8192), (64, 131072, 2048, 2048), (1024, 1 << 20, 4096, 512)):
+        assert 0 < size(seqs, max_len, total, new) < 9 * gib
+    assert size(64, 131072, 2048, 2048, total_len=262144) < 2 * gib  # 262144 rows x 8 kv-heads x 768 bytes and the rest
+    one = size(1, 131072, 2048, 2048)  # within the limit: room for every row
+    assert one > 131072 * 8 * 6 * 128
