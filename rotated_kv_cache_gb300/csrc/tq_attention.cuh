@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
         // power-of-two scale so the largest |q| of the head lands in [2^14, 2^15)
         int e = 0;
         if (mx > 0.0f && mx < INFINITY) e = 14 - (((int)(__float_as_uint(mx) >> 23) & 0xFF) - 127);
-        e = e < -100 ? -100 : (e > 100 ? 100 : e);
+        e = e > 100 ? 100 : e;  // (-113 at least)
         const float qscale = ldexpf(1.0f, e);
         float qsum[NG];
 #pragma unroll

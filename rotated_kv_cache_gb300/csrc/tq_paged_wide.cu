@@ -62,6 +62,9 @@ constexpr int wThreads = 384;  // two softmax warpgroups; MMA warp, tile warp (a
 constexpr int wPlanThreads = 256;
 constexpr int wStart = 7;  // what a block costs besides its tiles (q in, out of tensor memory, un-rotation), in tiles
 constexpr float wTau = 8.0f, wUp = 6.0f;  // lazy raise of R; weights are 2^(s - R + wUp)
+// A product of the operand tiles is below 2^(15 + 14) D <= 2^36, so with a factor
+// up to this the scores are below 2^24, where R's last bit is 1.
+constexpr float wFar = 1.0f / 4096;
 
 // What expand says about a tile.
 struct __align__(16) TileMeta {
@@ -545,6 +548,24 @@ __device__ __noinline__ float mixed_tile(uint32_t t_s, const RowMeta *rm, float 
     return sum;
 }
 
+// Scores that may be 2^24 and more: s = x f + e in place of the products x,
+// rounded as R is.  (Taken in one step, x f + (e - R) is exact, and its distance
+// from a rounded R of that size no exponent of a weight.)
+__device__ __noinline__ void far_tile(uint32_t t_s, float f, float e)
+{
+#pragma unroll 1
+    for (int c = 0; c < wT; c += 16) {
+        uint32_t x[16];
+        tc_ld16(t_s + c, x);
+        tc_wait_ld();
+        tc_pin(x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), f, e));
+        tc_st16(t_s + c, x);
+    }
+    tc_wait_st();
+}
+
 // Tensor memory holds S of both groups (128 columns each; P, f16, overwrites
 // its first half) and O of both.  In one pass over a tile the issuing warp
 // queues O_a += P_a V, S_a = Q_a K(next), then the same for the other group, so
@@ -802,7 +823,7 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                     for (int o = LR / 2; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                     int e = 0;
                     if (mx > 0.0f && mx < INFINITY) e = 14 - (((int)(__float_as_uint(mx) >> 23) & 0xFF) - 127);
-                    e = e < -100 ? -100 : (e > 100 ? 100 : e);
+                    e = e > 100 ? 100 : e;  // (-113 at least)
                     const float qs = __uint_as_float((uint32_t)(127 + e) << 23) * p.qsign;
                     const int er = __shfl_sync(0xffffffffu, e, (lane % RI) * LR);  // of row i RI + lane % RI
                     if (lane / RI == i) ie = __uint_as_float((uint32_t)(127 - er) << 23) * p.scale_log2;
@@ -841,6 +862,11 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 if (!ok) break;
                 tc_fence_after();
                 float extra = 0.0f;
+                if (!(any & 2u) && __any_sync(0xffffffffu, f > wFar)) {
+                    far_tile(t_s, f, e);
+                    f = 1.0f;
+                    e = 0.0f;
+                }
                 if (any & 2u) {
                     // rows of exponents of their own: true scores now, and the sum of the weights
                     extra = mixed_tile(t_s, p.row_meta + (mt - p.meta) * wT, ie, vis, R);

@@ -733,3 +733,22 @@ def test_more_long_chunks_than_the_workspace_expands(cuda):
             want = torch.einsum("hgn,hnd->hgd", p, v).reshape(QH, d)
             worst = max(worst, float(((out[starts[s] + i] - want).abs() - RTOL * want.abs()).max()))
     assert worst <= ATOL, worst
+
+
+@pytest.mark.parametrize("power", [26, 118])
+@pytest.mark.parametrize("d,kb,new", [(128, 8, 1), (128, 4, 3), (128, 8, 140), (64, 8, 300), (256, 5, 4), (512, 8, 2)])
+def test_scores_of_any_size(cuda, power, d, kb, new):
+    """Queries of 2^26 and 2^118: scores whose last bits are 8 and 2^100, and weights of ones and zeros; finite as long
+    as the scores are."""
+    b = Batch([260, 200], [new, min(new, 200)], H=2, d=d, kb=kb, vb=3, page=64, seed=91)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = (b.queries(8).float() * 2.0 ** power).to(torch.bfloat16)
+    for scale in (None, -0.05):
+        out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q.cuda(), new, softmax_scale=scale)
+        check_attention(b, pool, q, out, scale=scale)
+    c = _contiguous(cuda, b, 0)
+    for s in (None, 0.125):  # and the calls on a contiguous cache
+        one = cuda.tq_decode_attention(c, q[new - 1:new].cuda(), 260, softmax_scale=s)
+        same = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q.cuda(), new, softmax_scale=s)
+        assert ((same[new - 1].float() - one[0]).abs() <= 2.0 ** -8 * one[0].abs() + 2e-3).all()
