@@ -390,9 +390,12 @@ TQ_API size_t tq_paged_attention_workspace_bytes(const tq_cache *pool, const tq_
  *            for these bounds, 256-byte aligned, not initialised.  Calls that
  *            may run at the same time (other streams, graphs replayed
  *            together) need one each.
- * Scores and sums are fp32 and keys keep 22 bits or their exact codes; values
- * (centroid times rms) and probabilities enter the tensor cores as f16 (2^-12 of
- * them each), less than the output's rounding.  A
+ * Scores and sums are fp32 and keys keep 22 bits or their exact codes.  In long
+ * chunks (128 columns and more at head_dims 64 and 128) values and weights enter
+ * the tensor cores as f16 of exponents of their own, 2^-12 of each, less than the
+ * output's rounding; elsewhere as a weight (1 for the largest score) times a
+ * group's rms, which is f16 too and below 2^-14 keeps an absolute 2^-25: values of
+ * 2^-13 and less lose precision there, as in the contiguous calls.  A
  * row of the cache that a token does not see never reaches its output,
  * whatever it holds (NaN and infinities included); a row that it sees whose
  * value scale is not finite makes its output not finite (NaN, or infinite in

@@ -651,7 +651,9 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
                     }
                 }
             }
-            // ---------------- O^T += V^T P'^T, per value group
+            // ---------------- O^T += V^T P'^T, per value group.  P' = weight x rms is f16: 2^-12 of
+            // it, and an absolute 2^-25 below 2^-14, which values of 2^-13 and less notice
+            // (an exponent of their own would take the stage's largest rms before its products)
 #pragma unroll
             for (int G = 0; G < NG; ++G) {
                 const uint32_t sel = (G & 1) ? 0x7632u : 0x5410u;

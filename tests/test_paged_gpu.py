@@ -752,3 +752,26 @@ def test_scores_of_any_size(cuda, power, d, kb, new):
         one = cuda.tq_decode_attention(c, q[new - 1:new].cuda(), 260, softmax_scale=s)
         same = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q.cuda(), new, softmax_scale=s)
         assert ((same[new - 1].float() - one[0]).abs() <= 2.0 ** -8 * one[0].abs() + 2e-3).all()
+
+
+@pytest.mark.parametrize("power", [-12, -14, -16])
+@pytest.mark.parametrize("d,kb,vb,new", [(128, 8, 3, 1), (128, 4, 3, 3), (64, 8, 4, 1), (256, 8, 3, 2), (512, 8, 3, 1), (128, 5, 5, 4)])
+def test_small_values(cuda, power, d, kb, vb, new):
+    """Values of 2^power: a weight times a group's rms is one f16 number, within 2^-12 of it or 2^-25, whichever is
+    more.  Over n rows the second is an independent error of at most 2^-25 |centroid|, |centroid| < 3.3 and 1 in the
+    mean square, uniform: rms 2^-25 / 3^.5 n^.5 of a sum of weights that is 1 at least, and the un-rotation keeps the
+    rms; six deviations are 2^-25 * 3.5 n^.5."""
+    n = 700
+    b = Batch([n, 40], [new, new], H=2, d=d, kb=kb, vb=vb, page=64, seed=55)
+    for s in range(2):
+        b.v[s] = (b.v[s].float() * 2.0 ** power).to(torch.bfloat16)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = b.queries(8)
+    out = cuda.tq_paged_attention(pool, b.pages(cuda), b.dev(b.starts), q.cuda(), new).cpu().double()
+    from pagedtest import ATOL, RTOL, attention64, dequantised
+    for s in range(2):
+        k, v = dequantised(pool, b.table[s], b.lens[s])
+        want = attention64(q[s * new:(s + 1) * new], k, v, b.lens[s] - new)
+        err = (out[s * new:(s + 1) * new] - want).abs() - RTOL * want.abs()
+        assert float(err.max()) <= ATOL * 2.0 ** power + 3.5 * b.lens[s] ** 0.5 * 2.0 ** -25
