@@ -302,7 +302,7 @@ TQ_API int tq_attention_supported(int32_t head_dim, int32_t k_bits, int32_t v_bi
 /*
  * Paged caches.  A pool is an ordinary tq_cache whose `batch` is the number of
  * pages and whose `capacity` is the page size P (rows per page, a multiple of
- * 16): page p of kv-head h is rows [0, P) of (p, h) in every plane, so the row
+ * 16 below 2^31): page p of kv-head h is rows [0, P) of (p, h) in every plane, so the row
  * calls (tq_cache_copy_rows, tq_cache_clear_rows, on a view of one page) move
  * pages as well.  A page table says where the rows of the sequences of one
  * batch are: row t of sequence s is row t % P of page pages[s][t / P].

@@ -390,6 +390,7 @@ tq_status check_table(const tq_cache *c, const tq_page_table *t)
     if (!t || !t->pages || !t->seq_lens) return TQ_ERR_NULL;
     if (t->num_seqs < 1 || t->num_seqs >= (1 << 30) || t->reserved != 0) return TQ_ERR_SHAPE;
     if (t->max_len < 1 || t->max_len > INT32_MAX || t->stride < 1) return TQ_ERR_SHAPE;
+    if (c->capacity > INT32_MAX) return TQ_ERR_SHAPE;  // the page size, 32-bit in the kernels
     if (t->total_len < 0) return TQ_ERR_SHAPE;
     if (t->stride < (t->max_len + c->capacity - 1) / c->capacity) return TQ_ERR_CAPACITY;
     return TQ_OK;

@@ -247,3 +247,16 @@ def test_workspace_of_ordinary_serving_bounds(tqlib):
     assert size(64, 131072, 2048, 2048, total_len=262144) < 2 * gib  # 262144 rows x 8 kv-heads x 768 bytes and the rest
     one = size(1, 131072, 2048, 2048)  # within the limit: room for every row
     assert one > 131072 * 8 * 6 * 128
+
+
+@pytest.mark.parametrize("capacity", [1 << 31, (1 << 32) - 16, 1 << 32, (1 << 32) + 32, 1 << 40])
+def test_pages_of_2_31_rows_are_refused(tqlib, capacity):
+    """Positions and page sizes are 32-bit in the kernels: a larger page is refused before its size is cut off."""
+    L, ref = tqlib.lib(), ctypes.byref
+    pool, table = _struct(tqlib, batch=12, capacity=capacity), _table(tqlib)
+    st = _two(256, 128)
+    assert L.tq_paged_append(ref(pool), ref(table), 0x300000, 4, 0x10000, st, 0x20000, st, None) == SHAPE
+    assert L.tq_paged_decode(ref(pool), ref(table), 0x300000, 4, 0, 0x10000, 0x20000, None) == SHAPE
+    assert L.tq_paged_attention(ref(pool), ref(table), 0x300000, 4, 1, 0x10000, st, 4, 1.0, 0x20000, None, 0, None) == SHAPE
+    assert L.tq_paged_attention_workspace_bytes(ref(pool), ref(table), 4, 4, 1) == 0
+    assert L.tq_paged_attention_workspace_bytes(ref(_struct(tqlib, batch=12, capacity=(1 << 31) - 16)), ref(table), 4, 4, 1) > 0
