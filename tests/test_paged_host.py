@@ -259,4 +259,5 @@ def test_pages_of_2_31_rows_are_refused(tqlib, capacity):
     assert L.tq_paged_decode(ref(pool), ref(table), 0x300000, 4, 0, 0x10000, 0x20000, None) == SHAPE
     assert L.tq_paged_attention(ref(pool), ref(table), 0x300000, 4, 1, 0x10000, st, 4, 1.0, 0x20000, None, 0, None) == SHAPE
     assert L.tq_paged_attention_workspace_bytes(ref(pool), ref(table), 4, 4, 1) == 0
-    assert L.tq_paged_attention_workspace_bytes(ref(_struct(tqlib, batch=12, capacity=(1 << 31) - 16)), ref(table), 4, 4, 1) > 0
+    most = _struct(tqlib, batch=12, capacity=(1 << 31) - 16)
+    assert L.tq_paged_append(ref(most), ref(table), 0x300000, 0, 0x10000, st, 0x20000, st, None) == 0
