@@ -775,3 +775,35 @@ def test_small_values(cuda, power, d, kb, vb, new):
         want = attention64(q[s * new:(s + 1) * new], k, v, b.lens[s] - new)
         err = (out[s * new:(s + 1) * new] - want).abs() - RTOL * want.abs()
         assert float(err.max()) <= ATOL * 2.0 ** power + 3.5 * b.lens[s] ** 0.5 * 2.0 ** -25
+
+
+@pytest.mark.parametrize("d,kb,vb,H,page,rows", [(128, 8, 3, 2, 64, 1 << 26), (64, 4, 2, 1, 16, (1 << 31) + 4096)])
+def test_pages_far_into_a_large_pool(cuda, d, kb, vb, H, page, rows):
+    """Planes of more than 2^32 bytes, and a pool of more than 2^31 rows: append, fetch and attention of every kind at
+    its last pages, the same as in a small pool."""
+    per_row = d * kb // 8 + d * vb // 8 + 3 * (d // 32) * 2
+    if torch.cuda.mem_get_info()[0] < rows * per_row + (8 << 30):
+        torch.cuda.empty_cache()
+        if torch.cuda.mem_get_info()[0] < rows * per_row + (8 << 30):
+            pytest.skip("not enough device memory")
+    lens = [300, 17, 0, 200, 64]
+    small = Batch(lens, [1, 1, 0, 1, 1], H=H, d=d, kb=kb, vb=vb, page=page, seed=13, spare=0)
+    pool = small.pool(cuda)
+    small.fill(cuda, pool)
+    big = Batch(lens, [1, 1, 0, 1, 1], H=H, d=d, kb=kb, vb=vb, page=page, seed=13, spare=0)
+    pages = rows // (H * page)
+    big.table = big.table + (pages - big.num_pages)
+    far = cuda.Cache(pages, H, d, page, k_bits=kb, v_bits=vb)
+    big.fill(cuda, far)
+    for new in ([1, 1, 0, 1, 1], [4, 3, 0, 1, 2], [140, 1, 0, 150, 64]):
+        starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        q = small.queries(8 * H, total=int(starts[-1]))
+        outs = [cuda.tq_paged_attention(p, b.pages(cuda), b.dev(starts), q.cuda(), max(new)) for b, p in ((small, pool), (big, far))]
+        backs = [cuda.tq_paged_decode(p, b.pages(cuda), b.dev(starts), len(q)) for b, p in ((small, pool), (big, far))]
+        check_attention(small, pool, q, outs[0], new=new)
+        check_attention(small, pool, q, outs[1], new=new)
+        for x, y in zip(*backs):
+            assert torch.equal(x, y)
+    assert cuda.tq_device_error() == 0
+    del far
+    torch.cuda.empty_cache()
