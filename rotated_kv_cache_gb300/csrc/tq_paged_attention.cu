@@ -236,12 +236,18 @@ struct PagedPlan {
 // time grows with rows x columns from nothing, the wide kernels' with rows from
 // about 36 us (three launches more, a tile's first pass through the pipeline).
 // Measured with 8-bit keys, 3-bit values, 8 kv-heads, head_dim 128 (64):
-//   one sequence of 32768 rows   64 columns   split 81.4 us (50.8)  wide 98.9 (71.2)
-//                               128                147.2    (87.1)       98.5 (74.6)
-//   one sequence of 2048 rows   128                 21.1                 38.7
-//                               512                 48.8                 40.5
-//   one prompt of 128 tokens   1024                 18.7    (14.0)       32.0 (26.5)
-//                 512 tokens   4096                114.2    (36.9)       38.1 (31.6)
+//   one sequence of 32768 rows   64 columns   split 81.8 us (51.3)  wide 122 (75.6)
+//                               128                147.4    (87.8)       122 (75.2)
+//                               256                280.4   (160.9)       124 (73.7)
+//   one sequence of 2048 rows   128                 21.5    (19.3)       43.4 (36.1)
+//                               512                 49.3    (33.6)       45.0 (35.8)
+//   one prompt of 128 tokens   1024                 19.2    (16.7)       34.1 (27.9)
+//                 256 tokens   2048                 45.7    (27.2)       36.2 (29.7)
+//                 512 tokens   4096                115.7    (66.9)       41.4 (32.9)
+// and at head_dim 128 with fewer kv-heads, whose blocks fill fewer CTAs:
+//   2 kv-heads, 4096 rows       512 columns         29.2                 43.5
+//               2048 rows      4096                 85.4                 45.2
+//   1 kv-head,  2048 rows      4096                 49.7                 43.0
 constexpr int64_t kWideColumns = 128;
 constexpr int64_t kWideWork = int64_t(1) << 22;  // rows x kv-heads x columns, by the bounds that the host has
 

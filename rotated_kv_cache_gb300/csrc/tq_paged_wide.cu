@@ -60,7 +60,10 @@ constexpr int wT = 128;    // rows per tile
 constexpr int wC = 256;    // columns per block (two groups of the MMA's 128)
 constexpr int wThreads = 384;  // two softmax warpgroups; MMA warp, tile warp (and two idle ones)
 constexpr int wPlanThreads = 256;
-constexpr int wStart = 7;  // what a block costs besides its tiles (q in, out of tensor memory, un-rotation), in tiles
+// What a block costs besides its tiles (q in, out of tensor memory, un-rotation), in
+// tiles.  A prompt of 8191 tokens, 32 q-heads, with 3 / 4 / 5 / 7 / 9: 498 / 489 /
+// 493 / 502 / 510 us; of 4096 tokens 178 / 173 / 175 / 180 / 180.
+constexpr int wStart = 4;
 constexpr float wTau = 8.0f, wUp = 6.0f;  // lazy raise of R; weights are 2^(s - R + wUp)
 // A product of the operand tiles is below 2^(15 + 14) D <= 2^36, so with a factor
 // up to this the scores are below 2^24, where R's last bit is 1.
@@ -483,6 +486,8 @@ __global__ void __launch_bounds__(256, 4) wide_expand_kernel(const __grid_consta
                 *reinterpret_cast<uint4 *>(dst + 2 * KT + mnmaj_off<D>(t, 8 * c8)) = v4;
             }
         };
+        // the common widths at compile time: a prompt of 4096 tokens, 4-bit keys, takes 175 us
+        // so and 179 with run-time shifts, 8191 tokens with 8-bit keys 502 and 505
         using std::integral_constant;
 #pragma unroll 1
         for (int i0 = tid; i0 < wT * C8; i0 += 256 * N) {
