@@ -639,8 +639,9 @@ __device__ __forceinline__ void encode_value_lane(const EncodeParams &p, const f
 // The work of CTA `cta` of `ncta` encoding keys (KEY) or values.  A warp takes
 // every (ncta kWarps)-th item; in paged launches a run of consecutive ones, the
 // kv-heads of one token tile after another, so that a tile's rows are looked up
-// once for its heads.  32768 tokens of 8 kv-heads, head_dim 128, 8-bit keys:
-// 25 us, 3-bit values 35 us, each alone; issue-bound as the contiguous kernel is.
+// once for its heads.  32768 tokens of 8 kv-heads, head_dim 128, 8-bit keys and
+// 3-bit values: 53 us, with issue active 49 % and DRAM 40 %: four warps a scheduler
+// (126 registers) wait for the results of their own arithmetic.
 template <int D, int BITS, bool KEY, bool PAGED>
 __device__ __forceinline__ void encode_body(const EncodeParams &p, const CUtensorMap &map, uint8_t *smem_raw,
                                             uint32_t cta, uint32_t ncta)
@@ -886,14 +887,16 @@ template <int D>
 cudaError_t run_kv_any(int kb, int vb, const EncodeParams &pk, const CUtensorMap &mk, const EncodeParams &pv,
                        const CUtensorMap &mv, uint32_t gk, uint32_t gv, cudaStream_t s)
 {
-    auto larger = [](size_t a, size_t b) { return a > b ? a : b; };
-    const size_t k = kb == 2 ? encode_smem<D, 2, true>() : kb == 4 ? encode_smem<D, 4, true>()
-                     : kb == 5 ? encode_smem<D, 5, true>() : encode_smem<D, 8, true>();
-    const size_t v = vb == 2 ? encode_smem<D, 2, false>() : vb == 3 ? encode_smem<D, 3, false>()
-                     : vb == 4 ? encode_smem<D, 4, false>() : vb == 5 ? encode_smem<D, 5, false>() : encode_smem<D, 8, false>();
-    const size_t most = larger(larger(encode_smem<D, 2, true>(), encode_smem<D, 8, true>()), encode_smem<D, 8, false>());
+    // by width; the opt-in allows the largest, whichever comes first
+    constexpr size_t keys[4] = {encode_smem<D, 2, true>(), encode_smem<D, 4, true>(), encode_smem<D, 5, true>(), encode_smem<D, 8, true>()};
+    constexpr size_t values[5] = {encode_smem<D, 2, false>(), encode_smem<D, 3, false>(), encode_smem<D, 4, false>(),
+                                  encode_smem<D, 5, false>(), encode_smem<D, 8, false>()};
+    const size_t k = keys[kb == 2 ? 0 : kb == 4 ? 1 : kb == 5 ? 2 : 3], v = values[vb == 8 ? 4 : vb - 2];
+    size_t most = 0;
+    for (size_t x : keys) most = x > most ? x : most;
+    for (size_t x : values) most = x > most ? x : most;
     static KernelSetup setup;
-    return launch_kv(encode_kv_any_kernel<D>, setup, larger(k, v), larger(most, larger(k, v)), gk, gv, s, pk, mk, pv, mv, kb, vb);
+    return launch_kv(encode_kv_any_kernel<D>, setup, k > v ? k : v, most, gk, gv, s, pk, mk, pv, mv, kb, vb);
 }
 
 template <int D>

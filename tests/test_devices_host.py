@@ -69,3 +69,10 @@ def test_every_call_is_set_up_on_every_device(tqlib, fake, d, kb, vb):
         before = fake.fake_queries()
         _calls(tqlib, fake, d, kb, vb)
         assert fake.fake_queries() - before == each
+
+
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_widths_follow_one_another(tqlib, fake, d):
+    """Kernels that serve several widths keep the opt-in of the largest, whichever was asked for last."""
+    for kb, vb in ((8, 8), (2, 2), (8, 8), (5, 4), (4, 2), (8, 5), (8, 8)):
+        assert set(_calls(tqlib, fake, d, kb, vb).values()) == {0}, (kb, vb)
