@@ -438,9 +438,9 @@ def run_ours(args, rank, world, local_rank):
         "e2e": {"value": round(world * ab["total"] / (e2e_ms * 1e-3) / 1e9, 1), "unit": "GB/s",
                 "h2d_bytes_per_step": h2d, "d2h_bytes_per_step": d2h, "ms_per_step": round(e2e_ms, 3),
                 "pipelined": "copy-in, compute and copy-out streams overlap neighbouring steps (2 buffer sets; one copy in and one copy out per step)"},
-        # per step: prefill append (key and value kernels), fetch (one kernel for keys
-        # and values), single-token append (one kernel), attention (split + combine)
-        "gpu_launches": 6 * K,
+        # per step: prefill append, fetch and single-token append (one kernel each for keys
+        # and values), attention (split + combine)
+        "gpu_launches": 5 * K,
         "clocks": clocks.summary(),
     }
     return line

@@ -771,24 +771,6 @@ __device__ __forceinline__ void encode_body(const EncodeParams &p, const CUtenso
     if (!KEY && lane == 0) bulk_wait0();
 }
 
-// Every launch of this library is a programmatic dependent of the kernel
-// before it on the stream and waits for that kernel before touching memory.
-// The exception is the value launch of a contiguous append made of two launches
-// (keys, then values): it touches none of the key planes, so it starts as soon as
-// the key kernel has started and takes the SMs that key CTAs leave in their
-// last round; it waits for the key grid only before it ends, which keeps
-// stream order for whatever is queued after the append.
-template <int D, int BITS, bool KEY>
-__global__ void __launch_bounds__(kWarps * 32)
-    encode_kernel(const __grid_constant__ EncodeParams p, const __grid_constant__ CUtensorMap map)
-{
-    extern __shared__ __align__(128) uint8_t smem_raw[];
-    if constexpr (KEY) pdl_wait_primary();  // whatever the previous kernel on the stream writes or reads is settled
-    pdl_allow_dependents();
-    encode_body<D, BITS, KEY, false>(p, map, smem_raw, blockIdx.x, gridDim.x);
-    if constexpr (!KEY) pdl_wait_primary();
-}
-
 // Keys and values in one launch: CTAs [0, key_ctas) encode the keys, the
 // others the values (see run_kv for how the CTAs are shared out).
 template <int D, int KB, int VB, bool PAGED>
@@ -805,8 +787,8 @@ __global__ void __launch_bounds__(kWarps * 32)
         encode_body<D, VB, false, PAGED>(pv, mv, smem_raw, blockIdx.x - key_ctas, gridDim.x - key_ctas);
 }
 
-// The same for any widths, of paged appends (the width is one branch per CTA).
-template <int D>
+// The same for any widths (one branch per CTA).
+template <int D, bool PAGED>
 __global__ void __launch_bounds__(kWarps * 32)
     encode_kv_any_kernel(const __grid_constant__ EncodeParams pk, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ EncodeParams pv, const __grid_constant__ CUtensorMap mv, uint32_t key_ctas,
@@ -817,20 +799,20 @@ __global__ void __launch_bounds__(kWarps * 32)
     pdl_allow_dependents();
     if (blockIdx.x < key_ctas) {
         switch (kb) {
-        case 2: encode_body<D, 2, true, true>(pk, mk, smem_raw, blockIdx.x, key_ctas); break;
-        case 4: encode_body<D, 4, true, true>(pk, mk, smem_raw, blockIdx.x, key_ctas); break;
-        case 5: encode_body<D, 5, true, true>(pk, mk, smem_raw, blockIdx.x, key_ctas); break;
-        case 8: encode_body<D, 8, true, true>(pk, mk, smem_raw, blockIdx.x, key_ctas); break;
+        case 2: encode_body<D, 2, true, PAGED>(pk, mk, smem_raw, blockIdx.x, key_ctas); break;
+        case 4: encode_body<D, 4, true, PAGED>(pk, mk, smem_raw, blockIdx.x, key_ctas); break;
+        case 5: encode_body<D, 5, true, PAGED>(pk, mk, smem_raw, blockIdx.x, key_ctas); break;
+        case 8: encode_body<D, 8, true, PAGED>(pk, mk, smem_raw, blockIdx.x, key_ctas); break;
         }
         return;
     }
     const uint32_t cta = blockIdx.x - key_ctas, ctas = gridDim.x - key_ctas;
     switch (vb) {
-    case 2: encode_body<D, 2, false, true>(pv, mv, smem_raw, cta, ctas); break;
-    case 3: encode_body<D, 3, false, true>(pv, mv, smem_raw, cta, ctas); break;
-    case 4: encode_body<D, 4, false, true>(pv, mv, smem_raw, cta, ctas); break;
-    case 5: encode_body<D, 5, false, true>(pv, mv, smem_raw, cta, ctas); break;
-    case 8: encode_body<D, 8, false, true>(pv, mv, smem_raw, cta, ctas); break;
+    case 2: encode_body<D, 2, false, PAGED>(pv, mv, smem_raw, cta, ctas); break;
+    case 3: encode_body<D, 3, false, PAGED>(pv, mv, smem_raw, cta, ctas); break;
+    case 4: encode_body<D, 4, false, PAGED>(pv, mv, smem_raw, cta, ctas); break;
+    case 5: encode_body<D, 5, false, PAGED>(pv, mv, smem_raw, cta, ctas); break;
+    case 8: encode_body<D, 8, false, PAGED>(pv, mv, smem_raw, cta, ctas); break;
     }
 }
 
@@ -841,21 +823,6 @@ constexpr size_t encode_smem()
     using G = EGeo<D, KEY>;
     return 1024 /*alignment slack*/ + (size_t)kWarps * 2 * G::TILE + 16 * kWarps + ((!KEY && BITS > 3) ? 1024 : 0) +
            G::MTAB + (size_t)kWarps * (KEY ? 0 : VStage<D, BITS>::BYTES);
-}
-
-// A contiguous value launch must directly follow the key launch of the same append.
-template <int D, int BITS, bool KEY>
-cudaError_t run(const EncodeParams &p, const CUtensorMap &map, cudaStream_t s)
-{
-    const size_t smem = encode_smem<D, BITS, KEY>();
-    auto kern = encode_kernel<D, BITS, KEY>;
-    static KernelSetup setup;
-    int per_sm;
-    const cudaError_t e = setup.get(kern, kWarps * 32, smem, smem, per_sm);
-    if (e != cudaSuccess) return e;
-    const int64_t want = ((int64_t)p.items + kWarps - 1) / kWarps;
-    const int grid = (int)imin64(want, (int64_t)num_sms() * (per_sm > 0 ? per_sm : 1));
-    return launch_dependent(kern, dim3((unsigned)grid), dim3(kWarps * 32), smem, s, p, map);
 }
 
 // Keys and values in one launch, for up to gk and gv CTAs of each: those of a
@@ -883,7 +850,7 @@ cudaError_t run_kv(const EncodeParams &pk, const CUtensorMap &mk, const EncodePa
     return launch_kv(encode_kv_kernel<D, KB, VB, PAGED>, setup, smem, smem, gk, gv, s, pk, mk, pv, mv);
 }
 
-template <int D>
+template <int D, bool PAGED>
 cudaError_t run_kv_any(int kb, int vb, const EncodeParams &pk, const CUtensorMap &mk, const EncodeParams &pv,
                        const CUtensorMap &mv, uint32_t gk, uint32_t gv, cudaStream_t s)
 {
@@ -896,32 +863,7 @@ cudaError_t run_kv_any(int kb, int vb, const EncodeParams &pk, const CUtensorMap
     for (size_t x : keys) most = x > most ? x : most;
     for (size_t x : values) most = x > most ? x : most;
     static KernelSetup setup;
-    return launch_kv(encode_kv_any_kernel<D>, setup, k > v ? k : v, most, gk, gv, s, pk, mk, pv, mv, kb, vb);
-}
-
-template <int D>
-cudaError_t dispatch_key(int kb, const EncodeParams &p, const CUtensorMap &map, cudaStream_t s)
-{
-    switch (kb) {
-    case 2: return run<D, 2, true>(p, map, s);
-    case 4: return run<D, 4, true>(p, map, s);
-    case 5: return run<D, 5, true>(p, map, s);
-    case 8: return run<D, 8, true>(p, map, s);
-    }
-    return cudaErrorInvalidValue;
-}
-
-template <int D>
-cudaError_t dispatch_value(int vb, const EncodeParams &p, const CUtensorMap &map, cudaStream_t s)
-{
-    switch (vb) {
-    case 2: return run<D, 2, false>(p, map, s);
-    case 3: return run<D, 3, false>(p, map, s);
-    case 4: return run<D, 4, false>(p, map, s);
-    case 5: return run<D, 5, false>(p, map, s);
-    case 8: return run<D, 8, false>(p, map, s);
-    }
-    return cudaErrorInvalidValue;
+    return launch_kv(encode_kv_any_kernel<D, PAGED>, setup, k > v ? k : v, most, gk, gv, s, pk, mk, pv, mv, kb, vb);
 }
 
 // Tensor map over the [B][H][n][D] bf16 input (any strides the API accepts):
@@ -978,24 +920,14 @@ cudaError_t encode_launch(const CacheView &c, EncodeParams &pk, EncodeParams &pv
     if (!set_items(pv, n, EGeo<D, false>::TROWS, B, c.H)) return cudaErrorInvalidValue;
     pv.use_tma = input_map(&mv, v, D, n, c.H, B, vs, EGeo<D, false>::TROWS) ? 1 : 0;
 
-    // a small append (a few rows per sequence-head, as in a decode step) runs
-    // keys and values in one launch when both grids fit one CTA per SM; a larger
-    // one as two launches (keys, then values).  Paged values do not start beside
-    // the keys as a launch of their own (they would read the page table before a
-    // wait of theirs), so paged appends are one launch at every size: 5 x 5500
-    // tokens of 8 kv-heads, head_dim 128, take 47.8 us so and 59.5 in two that wait
+    // Keys and values are one launch.  As two, the values' would have to start
+    // beside the keys' to use the SMs that those leave in their last round, and
+    // read rows and page tables before a wait of its own: 5 x 5500 paged tokens of 8
+    // kv-heads, head_dim 128, take 47.8 us in one launch and 59.5 in two that wait.
     const uint32_t gk = (pk.items + kWarps - 1) / kWarps, gv = (pv.items + kWarps - 1) / kWarps;
-    if ((PAGED || (int64_t)gk + gv <= num_sms()) && c.vb == 3 && (c.kb == 8 || c.kb == 4)) {
-        if (c.kb == 8) return run_kv<D, 8, 3, PAGED>(pk, mk, pv, mv, gk, gv, s);
-        return run_kv<D, 4, 3, PAGED>(pk, mk, pv, mv, gk, gv, s);
-    }
-    if constexpr (PAGED) {
-        return run_kv_any<D>(c.kb, c.vb, pk, mk, pv, mv, gk, gv, s);
-    } else {
-        const cudaError_t e = dispatch_key<D>(c.kb, pk, mk, s);
-        if (e != cudaSuccess) return e;
-        return dispatch_value<D>(c.vb, pv, mv, s);
-    }
+    if (c.vb == 3 && c.kb == 8) return run_kv<D, 8, 3, PAGED>(pk, mk, pv, mv, gk, gv, s);
+    if (c.vb == 3 && c.kb == 4) return run_kv<D, 4, 3, PAGED>(pk, mk, pv, mv, gk, gv, s);
+    return run_kv_any<D, PAGED>(c.kb, c.vb, pk, mk, pv, mv, gk, gv, s);
 }
 
 inline bool encode_common(EncodeParams &p, const CacheView &c, int64_t n)
