@@ -116,9 +116,12 @@ def attention_traffic(kernel_hash: str):
 
 
 def kernel_source_hash() -> str:
-    p = os.path.join(ROOT, "rotated_kv_cache_gb300", "csrc", "tq_attention.cu")
-    with open(p, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()
+    """Of the split kernel and its merge: tq_attention.cuh, then tq_attention.cu."""
+    h = hashlib.sha256()
+    for name in ("tq_attention.cuh", "tq_attention.cu"):
+        with open(os.path.join(ROOT, "rotated_kv_cache_gb300", "csrc", name), "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()
 
 
 class ClockSampler:

@@ -188,7 +188,9 @@ __device__ __forceinline__ uint32_t shr_fma(uint32_t x)
 // warp copying one (a chunk lies within a page).  32 sequences of 24577 .. 32769
 // rows, 64 q-heads, 8-bit keys and 3-bit values: 334 us, 4.5 TB/s (the contiguous
 // call on 32769 rows each 325 us, 5.2): the look-ups and chunks of a stage are 16 %
-// more instructions, and issue is what bounds the kernel there as well.
+// more instructions.  Issue is active 48 % of the time and DRAM 46 %, at 3.2 warps a
+// scheduler (125 registers a thread): each warp's chains of loads and dependent
+// arithmetic take the time, so instructions count although the slots are not full.
 template <int KB, int D, int VB, int NBC, int MODE = 0>
 __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
     attn_split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ AttnParams p)
