@@ -37,11 +37,12 @@
 // largest.
 //
 // Measured: 2048 new tokens over 32768 rows, 64 q-heads, 8 kv-heads, head_dim
-// 128, 4-bit keys, 3-bit values: 2059 us in all, 1.03 PFLOP/s of the attention's
-// own products and 1.54 with the low terms' (of 1.87 that a large library
-// product reaches); a prompt of 8191 tokens 541 us, 1.02 and 1.53.  With hi alone
+// 128, 4-bit keys, 3-bit values: 2020 us in all, 1.05 PFLOP/s of the attention's
+// own products and 1.57 with the low terms' (of 1.88 that a large library
+// product reaches); a prompt of 8191 tokens 535 us, 1.03 and 1.53.  With hi alone
 // they took 1493 and 416: the tensor pipe has half as much work again, and
-// bounds the kernel.  The rest is the starts and ends of blocks.
+// bounds the kernel (77 % busy at 1024 tokens over 8192 rows; expand 18 us, attend
+// 219, merge 20, cold L2).  The rest is the starts and ends of blocks.
 //
 // A value row with an infinity or NaN would spoil the sums of columns that do
 // not see it (0 * inf), so expand writes zeros there and a bit mask; a column
