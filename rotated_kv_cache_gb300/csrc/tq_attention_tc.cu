@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(tcThreads, 1) attn_tc_kernel(const __grid_cons
             }
         int e = 0;
         if (mx > 0.0f && mx < INFINITY) e = 14 - (((int)(__float_as_uint(mx) >> 23) & 0xFF) - 127);
-        e = e < -100 ? -100 : (e > 100 ? 100 : e);
+        e = e > 100 ? 100 : e;  // (-113 at least)
         const float qs = ldexpf(1.0f, e);
         ie = ldexpf(1.0f, -e) * p.scale_log2;
         const uint32_t qt = sbase + A::OFF_Q + wg * A::QT;
@@ -308,17 +308,24 @@ __global__ void __launch_bounds__(tcThreads, 1) attn_tc_kernel(const __grid_cons
         // pass 2: the weights; P (f16, two per column) overwrites the row's first
         // tcT / 2 columns in tensor memory, always behind the columns still to
         // be read, and becomes the A operand of P V
+        // products are below 2^(15 + 14) D <= 2^36; where the scores may pass 2^24 they are
+        // rounded as the maximum is before it is subtracted
+        const bool far = __any_sync(0xffffffffu, f > 1.0f / 4096);
+        const float g = far ? 1.0f : f;
         float2 ls = make_float2(0.0f, 0.0f);
 #pragma unroll 1
         for (int c = 0; c < tcT / 32; ++c) {
             uint32_t sr[32], pp[16];
             tc_ld32(t_s + t_lane + 32 * c, sr);
             tc_wait_ld();
+            if (far)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sr[j] = __float_as_uint(__uint_as_float(sr[j]) * f);
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
                 const float x0 = 32 * c + j < vis ? __uint_as_float(sr[j]) : -INFINITY;
                 const float x1 = 32 * c + j + 1 < vis ? __uint_as_float(sr[j + 1]) : -INFINITY;
-                const float p0 = tc_ex2(fmaf(x0, f, -mu)), p1 = tc_ex2(fmaf(x1, f, -mu));
+                const float p0 = tc_ex2(fmaf(x0, g, -mu)), p1 = tc_ex2(fmaf(x1, g, -mu));
                 ls = __fadd2_rn(ls, make_float2(p0, p1));
                 pp[j / 2] = tc_pack_f16(p0, p1);
             }
