@@ -407,6 +407,172 @@ TQ_API tq_status tq_paged_attention(const tq_cache *pool, const tq_page_table *t
                                     size_t workspace_bytes, tq_stream_t stream);
 
 /*
+ * Attention of trees of drafted tokens: as tq_paged_attention, but the new tokens of
+ * a sequence see one another by masks.  Token t sees every row before the new
+ * ones, and new row j of its sequence (row seq_lens[s] - n + j of n new ones) where
+ * bit j % 32 of masks[t * mask_words + j / 32] is set:
+ *   out[t][h] = sum_{j seen by t} softmax_j(q[t][h] . k_hat[j][h/G] * softmax_scale) v_hat[j][h/G]
+ * For a tree a token's bits are its ancestors' and its own (tq_paged_layout makes
+ * them from the parents); any mask will do, bits from n on are not looked at, and
+ * a token that sees nothing gives zeros.
+ *  masks     device int32 [total][mask_words], mask_words >= ceil(min(max_new, total) / 32).
+ *  The other arguments, the workspace (of tq_paged_tree_attention_workspace_bytes), the
+ *  precision and what is said of rows that a token does not see are tq_paged_attention's.
+ */
+TQ_API size_t tq_paged_tree_attention_workspace_bytes(const tq_cache *pool, const tq_page_table *table, int32_t q_heads,
+                                                      int64_t total, int64_t max_new);
+TQ_API tq_status tq_paged_tree_attention(const tq_cache *pool, const tq_page_table *table, const int32_t *starts,
+                                         int64_t total, int64_t max_new, const void *q, const int64_t q_strides[2],
+                                         int32_t q_heads, float softmax_scale, const int32_t *masks, int64_t mask_words,
+                                         void *out, void *workspace, size_t workspace_bytes, tq_stream_t stream);
+
+/*
+ * Page tables from lengths.  The free pages of a pool are a stack: free_pages[0 ..
+ * free_count - 1], its top the last one.  table->seq_lens says how long the
+ * sequences are before the call, lens how long they are to be; with c(n) =
+ * ceil(n / P), a sequence that shrinks from a to b rows pushes its table entries c(b)
+ * .. c(a) - 1, one that grows from a to b pops pages into entries c(a) .. c(b) - 1.
+ * Pushes come in order of sequences and entries, then pops in that order (so a page
+ * may go from one sequence to another in one call).  Entries given back and
+ * stack places above the new count keep what they held.  A sequence ends with a
+ * length of 0, a new one takes over the row of one that has ended.
+ *  lens        device int32 [num_seqs], in [0, max_len].
+ *  new_tokens  device int32 [num_seqs]: how many of the last rows are new tokens of
+ *              this step (NULL: no starts are wanted), in [0, lens].
+ *  lens_out    device int32 [num_seqs]: becomes lens; may be table->seq_lens (in
+ *              place), or lens.
+ *  starts      device int32 [num_seqs + 1] or NULL: running sums of new_tokens.
+ *  free_pages  device int32 [free_capacity], read and written.
+ *  free_count, free_count_out   device int32; may be the same (in place).
+ * table->pages is written.  Where a value is out of range (TQ_DEVICE_ERR_LENGTH), or
+ * the pool has fewer pages than are lacking, or the stack no room for those given back
+ * or a count out of range (TQ_DEVICE_ERR_FULL), nothing changes: lens_out becomes the
+ * old lengths, free_count_out the old count, starts all 0.  Page numbers given
+ * back that are outside the pool are recorded (TQ_DEVICE_ERR_PAGE) and pushed.
+ */
+TQ_API tq_status tq_page_table_update(const tq_cache *pool, const tq_page_table *table, const int32_t *lens,
+                                      const int32_t *new_tokens, int32_t *lens_out, int32_t *starts, int32_t *free_pages,
+                                      int64_t free_capacity, const int32_t *free_count, int32_t *free_count_out,
+                                      tq_stream_t stream);
+
+/*
+ * Places of the new tokens, each of the outputs or NULL:
+ *  positions   device int32 [total]: the token's row, seq_lens[s] - n + i for token
+ *              i of n; in a tree seq_lens[s] - n + depth, the depth of a root being 0.
+ *  slots       device int64 [total]: page * P + row % P of the token's row (kv-head h's
+ *              plane row is slot + (slot / P * (H - 1) + h) * P).
+ *  masks       device int32 [total][mask_words]: bit j where node j of the sequence is
+ *              the token or an ancestor (tq_paged_tree_attention reads them).
+ *  parents     device int32 [total] or NULL (no trees: the tokens of a sequence
+ *              follow one another, and there are no masks): the parent's index among the sequence's
+ *              new tokens, below the token's own, -1 at a root; a parent out of
+ *              range is taken for -1 and recorded (TQ_DEVICE_ERR_TREE).
+ * With parents no sequence has more than max_new tokens (one that has is recorded as TQ_DEVICE_ERR_LENGTH).
+ * A token behind the last sequence or of a sequence that was recorded has position and slot -1
+ * and an empty mask; one that stands before its sequence's first row or in a bad page slot -1.
+ */
+TQ_API tq_status tq_paged_layout(const tq_cache *pool, const tq_page_table *table, const int32_t *starts, int64_t total,
+                                 const int32_t *parents, int64_t max_new, int32_t *positions, int64_t *slots,
+                                 int32_t *masks, int64_t mask_words, tq_stream_t stream);
+
+/*
+ * Keep the accepted rows of a step: of the n new rows of sequence s, row path[s][k]
+ * moves to place k for k < kept[s] (all planes and kv-heads, byte for byte), and
+ * lens_out[s] becomes seq_lens[s] - n + kept[s].  The rows behind stay as they are.
+ *  path      device int32 [num_seqs][path_stride], its first kept[s] entries growing
+ *            strictly and below n; kept device int32 [num_seqs], 0 .. n; n <= max_new
+ *            <= path_stride.  A sequence where that does not hold keeps its rows and
+ *            its length (TQ_DEVICE_ERR_TREE).
+ *  lens_out  device int32 [num_seqs], not table->seq_lens (tq_page_table_update takes it
+ *            as lens, gives back the pages that are left over and sets the table's).
+ * Sequences must not share pages that hold moved rows.
+ */
+TQ_API tq_status tq_paged_keep(const tq_cache *pool, const tq_page_table *table, const int32_t *starts, int64_t total,
+                               int64_t max_new, const int32_t *path, int64_t path_stride, const int32_t *kept,
+                               int32_t *lens_out, tq_stream_t stream);
+
+/* Most drafted tokens of a sequence that tq_verify_drafts takes (it holds them in shared memory). */
+#define TQ_MAX_DRAFT 1024
+
+/*
+ * Verification of drafted tokens against the target's probabilities.  The new tokens
+ * of sequence s, rows [starts[s], starts[s + 1]), form a tree: node 0 is the token
+ * that is certain already, the parents are those of tq_paged_layout.  Row t of
+ * `target` holds the target's probabilities of the token behind node t, row t of
+ * `draft` those that node t's children were drawn from (independently of one another).
+ * From node 0 on, the children of the last accepted node are tried in index
+ * order: child c of token x is accepted where
+ *   uniforms[c] * r(x) * M < max(p(x) - C r(x), 0)
+ * (p, r: the node's rows; C = 0 and M = 1 at first), else C += M and
+ * M = sum_v max(p(v) - C r(v), 0), which is the rest of the target's distribution
+ * after a rejection, not normalised.  Without draft probabilities (draft NULL: tokens
+ * not drawn at random) the test is uniforms[c] * M < p(x), and a rejected token is
+ * crossed out: M -= p(x), p(x) = 0.  When no child is accepted, the next token is the
+ * first v where the running sum of what is left, max(p - C r, 0) or p without the
+ * crossed-out tokens, is above last[s] times its sum.  The tokens then follow the
+ * target's distribution.
+ *  target, draft   device fp32 or bf16 (dtype), rows of `vocab` probabilities,
+ *            target_stride and draft_stride elements apart, aligned to their elements.
+ *            Values that are negative or not finite count as 0.
+ *  tokens    device int32 [total], in [0, vocab) but for node 0 (one outside is not
+ *            accepted: TQ_DEVICE_ERR_TREE, as for a parent out of range, whose node no
+ *            other reaches).
+ *  uniforms  device fp32 [total] (node 0's is not read), last device fp32 [num_seqs]: in [0, 1).
+ *  path      device int32 [num_seqs][path_stride]: the accepted nodes, node 0 first,
+ *            then -1 up to max_new; kept [num_seqs] their number; next [num_seqs] the next
+ *            token (vocab where nothing is left).  A sequence without tokens: 0 kept, next -1.
+ * max_new <= TQ_MAX_DRAFT, max_new <= path_stride; a sequence of more tokens, or starts out of
+ * range, counts as one without (TQ_DEVICE_ERR_LENGTH).  Sums are kept to about 2^-45,
+ * products and comparisons in 64 bits.
+ */
+TQ_API tq_status tq_verify_drafts(const int32_t *starts, int32_t num_seqs, int64_t total, int64_t max_new,
+                                  const int32_t *parents, const int32_t *tokens, int64_t vocab, tq_dtype dtype,
+                                  const void *target, int64_t target_stride, const void *draft, int64_t draft_stride,
+                                  const float *uniforms, const float *last, int32_t *path, int64_t path_stride,
+                                  int32_t *kept, int32_t *next, tq_stream_t stream);
+
+/* Queries or keys of ragged tokens, [token][head][head_dim] with head_dim contiguous. */
+typedef struct tq_rotary_tensor {
+    const void *x;           /* device, 16-byte aligned */
+    void *out;               /* device, 16-byte aligned; x (in place, with the same strides) or disjoint from it */
+    int64_t x_strides[2];    /* between tokens and heads, in elements; multiples of 16 bytes */
+    int64_t out_strides[2];
+    int32_t heads;           /* >= 1 */
+    int32_t reserved;        /* must be 0 */
+} tq_rotary_tensor;
+
+/*
+ * Rotary positions: each pair (a, b) of the first rot_dim elements of every head becomes
+ *   scale * (a cos t - b sin t, a sin t + b cos t),  t = positions[token] * freqs[pair],
+ * the pairs being elements (2 i, 2 i + 1) when interleaved, else (i, i + rot_dim / 2);
+ * the elements from rot_dim on are copied.  One call turns queries and keys (either
+ * may be NULL).  A token whose position is negative is left as it was.  Angles are
+ * reduced in 64 bits, the rest is fp32, rounded once.
+ *  positions device int32 [tokens] (tq_paged_layout's); freqs device binary64 [rot_dim / 2].
+ *  head_dim  one of the codec's; rot_dim even, 2 .. head_dim.
+ */
+TQ_API tq_status tq_rotary(const int32_t *positions, int64_t tokens, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                           const double *freqs, float scale, tq_dtype dtype, const tq_rotary_tensor *q,
+                           const tq_rotary_tensor *k, tq_stream_t stream);
+
+/* How frequencies are changed for contexts longer than a model was made for. */
+typedef enum tq_rotary_scaling {
+    TQ_ROTARY_PLAIN = 0,  /* w_i = base^(-2 i / rot_dim) */
+    TQ_ROTARY_LINEAR = 1, /* w_i / factor */
+    TQ_ROTARY_NTK = 2,    /* a larger base, which stretches the slowest pair by the factor and leaves the fastest:
+                             base * factor^(rot_dim / (rot_dim - 2)) */
+    TQ_ROTARY_YARN = 3    /* pairs that turn more than `fast` times in original_len positions left, those that turn
+                             less than `slow` times divided by the factor, a linear ramp of the pair's index
+                             between them; vectors grow by 0.1 ln(factor) + 1 */
+} tq_rotary_scaling;
+
+/* The frequencies of rot_dim / 2 pairs (host output) and the scale that goes with them (tq_rotary's).
+ * factor >= 1; original_len, fast and slow for TQ_ROTARY_YARN alone (fast >= slow > 0). */
+TQ_API tq_status tq_rotary_frequencies(int32_t rot_dim, double base, tq_rotary_scaling scaling, double factor,
+                                       int64_t original_len, double fast, double slow, double *host_freqs,
+                                       float *host_scale);
+
+/*
  * Device-side error word.  Kernels that wait on asynchronous copies give up
  * after a bounded number of polls and record a non-zero code here instead of
  * hanging.  tq_device_error() synchronises the device, copies the word into
@@ -420,6 +586,9 @@ TQ_API tq_status tq_device_error(uint32_t *host_code);
 /* Codes of the paged calls: a page number outside the pool; a length or a start out of range. */
 #define TQ_DEVICE_ERR_PAGE 2u
 #define TQ_DEVICE_ERR_LENGTH 4u
+/* Too few free pages, or no room for those given back; a tree, a path or a token out of range. */
+#define TQ_DEVICE_ERR_FULL 8u
+#define TQ_DEVICE_ERR_TREE 16u
 
 /*
  * Failure-path check (no counterpart in the pages): launches one warp that

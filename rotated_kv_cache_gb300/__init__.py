@@ -28,6 +28,9 @@ __all__ = [
     "TQ_DEVICE_ERR_WAIT_TIMEOUT", "TQ_DEFAULT_SIGN_SEED",
     "PageTable", "tq_paged_append", "tq_paged_decode", "tq_paged_attention", "tq_paged_attention_workspace_bytes",
     "TQ_DEVICE_ERR_PAGE", "TQ_DEVICE_ERR_LENGTH",
+    "tq_page_table_update", "tq_paged_layout", "tq_paged_tree_attention", "tq_paged_tree_attention_workspace_bytes",
+    "tq_paged_keep", "tq_verify_drafts", "tq_rotary", "tq_rotary_frequencies", "TQ_DEVICE_ERR_FULL", "TQ_DEVICE_ERR_TREE",
+    "TQ_MAX_DRAFT",
 ]
 
 HEAD_DIMS = (64, 128, 256, 512)
@@ -37,6 +40,10 @@ TQ_BF16, TQ_F32 = 0, 1
 TQ_DEVICE_ERR_WAIT_TIMEOUT = 1  # device error word: a bounded wait gave up
 TQ_DEVICE_ERR_PAGE = 2  # a paged call met a page number outside the pool
 TQ_DEVICE_ERR_LENGTH = 4  # ... a length, or starts, out of range
+TQ_DEVICE_ERR_FULL = 8  # too few free pages, or no room for those given back
+TQ_DEVICE_ERR_TREE = 16  # a tree's parent, a path or a drafted token out of range
+TQ_MAX_DRAFT = 1024  # most drafted tokens of a sequence that tq_verify_drafts takes
+ROTARY_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 TQ_DEFAULT_SIGN_SEED = 42  # the codec's sign-vector seed unless a cache states another
 
 EXPORTS = (
@@ -46,6 +53,8 @@ EXPORTS = (
     "tq_unrotate", "tq_cache_copy_rows", "tq_cache_clear_rows", "tq_multi_token_workspace_bytes",
     "tq_multi_token_attention", "tq_check_wait_timeout", "tq_paged_append", "tq_paged_decode",
     "tq_paged_attention_workspace_bytes", "tq_paged_attention",
+    "tq_paged_tree_attention_workspace_bytes", "tq_paged_tree_attention", "tq_page_table_update", "tq_paged_layout",
+    "tq_paged_keep", "tq_verify_drafts", "tq_rotary", "tq_rotary_frequencies",
 )
 
 
@@ -69,6 +78,13 @@ class _PageTableStruct(ctypes.Structure):
     _fields_ = [
         ("pages", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("stride", ctypes.c_int64),
         ("max_len", ctypes.c_int64), ("total_len", ctypes.c_int64), ("num_seqs", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class _RotaryStruct(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("x_strides", ctypes.c_int64 * 2),
+        ("out_strides", ctypes.c_int64 * 2), ("heads", ctypes.c_int32), ("reserved", ctypes.c_int32),
     ]
 
 
@@ -117,9 +133,22 @@ def lib() -> ctypes.CDLL:
     so.tq_paged_attention_workspace_bytes.restype = _SZ
     so.tq_paged_attention_workspace_bytes.argtypes = [_CP, _TP, _I32, _I64, _I64]
     so.tq_paged_attention.argtypes = [_CP, _TP, _P, _I64, _I64, _P, two, _I32, ctypes.c_float, _P, _P, _SZ, _P]
+    so.tq_paged_tree_attention_workspace_bytes.restype = _SZ
+    so.tq_paged_tree_attention_workspace_bytes.argtypes = [_CP, _TP, _I32, _I64, _I64]
+    so.tq_paged_tree_attention.argtypes = [_CP, _TP, _P, _I64, _I64, _P, two, _I32, ctypes.c_float, _P, _I64, _P, _P, _SZ, _P]
+    so.tq_page_table_update.argtypes = [_CP, _TP, _P, _P, _P, _P, _P, _I64, _P, _P, _P]
+    so.tq_paged_layout.argtypes = [_CP, _TP, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P]
+    so.tq_paged_keep.argtypes = [_CP, _TP, _P, _I64, _I64, _P, _I64, _P, _P, _P]
+    so.tq_verify_drafts.argtypes = [_P, _I32, _I64, _I64, _P, _P, _I64, ctypes.c_int, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P,
+                                    _P, _P]
+    turned = ctypes.POINTER(_RotaryStruct)
+    so.tq_rotary.argtypes = [_P, _I64, _I32, _I32, _I32, _P, ctypes.c_float, ctypes.c_int, turned, turned, _P]
+    f64 = ctypes.c_double
+    so.tq_rotary_frequencies.argtypes = [_I32, f64, ctypes.c_int, f64, _I64, f64, f64, _P, ctypes.POINTER(ctypes.c_float)]
     for name in EXPORTS:
         if name not in ("tq_status_string", "tq_bytes_per_token_head", "tq_attention_workspace_bytes",
-                        "tq_attention_supported", "tq_multi_token_workspace_bytes", "tq_paged_attention_workspace_bytes"):
+                        "tq_attention_supported", "tq_multi_token_workspace_bytes", "tq_paged_attention_workspace_bytes",
+                        "tq_paged_tree_attention_workspace_bytes"):
             getattr(so, name).restype = ctypes.c_int
     so.tq_attention_supported.restype = ctypes.c_int
     return so
@@ -573,22 +602,249 @@ def tq_paged_attention(pool: Cache, table: PageTable, starts: torch.Tensor, q: t
                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Causal attention of the new tokens (q bf16 [tokens][QH][d], any token and head strides; at most
     max_new of one sequence) over their sequences' rows -> bf16 [tokens][QH][d]."""
+    return _attend(pool, table, starts, q, None, max_new, softmax_scale, out, workspace, stream)
+
+
+def _attend(pool, table, starts, q, masks, max_new, softmax_scale, out, workspace, stream) -> torch.Tensor:
+    """Both paged attention calls: causal, or with the masks of trees."""
     qs = _ragged_strides(q, None, pool.head_dim, "q")
     total, QH, d = q.shape
     if out is not None and (out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous()):
         raise ValueError("out must be contiguous bfloat16, shaped like q")
-    s, t = _paged_check(pool, table, starts, q, out, workspace)
+    if masks is not None and (masks.dtype is not torch.int32 or masks.dim() != 2 or masks.shape[0] != total or
+                              not masks.is_contiguous()):
+        raise ValueError("masks must be contiguous int32 [tokens][words]")
+    s, t = _paged_check(pool, table, starts, q, out, workspace, masks)
     if out is None:
         out = torch.empty_like(q) if stream is None and q.is_contiguous() else \
             _empty_on(stream, (total, QH, d), torch.bfloat16, q.device)
     if workspace is None and total > 0:
-        need = tq_paged_attention_workspace_bytes(pool, table, QH, total, max_new)
-        workspace = _empty_on(stream, need, torch.uint8, q.device)
+        size = tq_paged_attention_workspace_bytes if masks is None else tq_paged_tree_attention_workspace_bytes
+        workspace = _empty_on(stream, size(pool, table, QH, total, max_new), torch.uint8, q.device)
     scale = (1.0 / d ** 0.5) if softmax_scale is None else float(softmax_scale)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    if masks is not None:
+        _check(lib().tq_paged_tree_attention(s, t, starts.data_ptr(), total, int(max_new), q.data_ptr(), qs, QH, scale,
+                                             masks.data_ptr(), masks.shape[1], out.data_ptr(), ws_ptr, ws_bytes,
+                                             _stream(stream)), "tq_paged_tree_attention")
+        return out
     _check(lib().tq_paged_attention(s, t, starts.data_ptr(), total, int(max_new), q.data_ptr(), qs, QH, scale,
                                     out.data_ptr(), ws_ptr, ws_bytes, _stream(stream)), "tq_paged_attention")
     return out
+
+
+# ------------------------------------------------------------------ a step of drafted tokens
+def tq_paged_tree_attention_workspace_bytes(pool: Cache, table: PageTable, q_heads: int, total: int, max_new: int) -> int:
+    s, t = pool.struct(), table.struct(pool)
+    return int(lib().tq_paged_tree_attention_workspace_bytes(ctypes.byref(s), ctypes.byref(t), int(q_heads), int(total),
+                                                             int(max_new)))
+
+
+def tq_paged_tree_attention(pool: Cache, table: PageTable, starts: torch.Tensor, q: torch.Tensor, masks: torch.Tensor,
+                            max_new: int, softmax_scale: float | None = None, out: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of drafted tokens (q bf16 [tokens][QH][d]; at most max_new of one sequence) over the rows before
+    the new ones and the new ones that their masks name (int32 [tokens][words], tq_paged_layout's) -> bf16 [tokens][QH][d]."""
+    if masks is None:
+        raise ValueError("masks must be contiguous int32 [tokens][words]")
+    return _attend(pool, table, starts, q, masks, max_new, softmax_scale, out, workspace, stream)
+
+
+def _i32(x: torch.Tensor | None, shape: tuple, what: str) -> int | None:
+    """The address of an int32 tensor of this shape."""
+    if x is None:
+        return None
+    if x.dtype is not torch.int32 or tuple(x.shape) != shape or not x.is_contiguous():
+        raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
+    return x.data_ptr()
+
+
+def _one_device(*tensors) -> torch.device:
+    """The CUDA device that all of them are on, the current one."""
+    dev = -1
+    for t in tensors:
+        if t is None:
+            continue
+        at = t.get_device()
+        if at < 0:
+            raise ValueError("tensors must live on a CUDA device")
+        if dev >= 0 and at != dev:
+            raise ValueError("the tensors must be on one device")
+        dev = at
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError("the tensors are on another device than the current one")
+    return torch.device("cuda", dev)
+
+
+def tq_page_table_update(pool: Cache, table: PageTable, lens: torch.Tensor, free_pages: torch.Tensor,
+                         free_count: torch.Tensor, new_tokens: torch.Tensor | None = None,
+                         lens_out: torch.Tensor | None = None, starts: torch.Tensor | None = None,
+                         free_count_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Give the sequences pages for the wanted lengths (int32 [num_seqs]): those that shrink push theirs onto the stack
+    free_pages[:free_count], those that grow pop theirs; the table's pages are written, its lengths too unless lens_out
+    is given, free_count unless free_count_out is.  With new_tokens (int32 [num_seqs]) their running sums come back as starts."""
+    n = table.num_seqs
+    lens_out = table.seq_lens if lens_out is None else lens_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be contiguous int32 [capacity]")
+    if starts is not None and new_tokens is None:
+        raise ValueError("starts are the running sums of new_tokens: give both")
+    at = (_i32(lens, (n,), "lens"), _i32(new_tokens, (n,), "new_tokens"), _i32(lens_out, (n,), "lens_out"))
+    stack, counts = _i32(free_pages, tuple(free_pages.shape), "free_pages"), (_i32(free_count, (1,), "free_count"),
+                                                                             _i32(free_count_out, (1,), "free_count_out"))
+    dev = _one_device(pool.k_codes, table.pages, table.seq_lens, lens, new_tokens, lens_out, starts, free_pages, free_count,
+                      free_count_out)
+    if starts is None and new_tokens is not None:
+        starts = _empty_on(stream, n + 1, torch.int32, dev)
+    first = _i32(starts, (n + 1,), "starts")
+    s, t = pool.struct(), table.struct(pool)
+    _check(lib().tq_page_table_update(ctypes.byref(s), ctypes.byref(t), at[0], at[1], at[2], first, stack, free_pages.shape[0],
+                                      counts[0], counts[1], _stream(stream)), "tq_page_table_update")
+    return starts
+
+
+def tq_paged_layout(pool: Cache, table: PageTable, starts: torch.Tensor, total: int, parents: torch.Tensor | None = None,
+                    max_new: int | None = None, positions: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                    masks: torch.Tensor | None = None, want_positions: bool = True, want_slots: bool = True,
+                    want_masks: bool = True, stream=None):
+    """(positions int32 [total], slots int64 [total], masks int32 [total][ceil(max_new / 32)]) of the new tokens; with
+    parents (int32 [total], -1 at a root) positions go by the depth in a sequence's tree, without them masks is None."""
+    total = int(total)
+    if parents is not None and max_new is None:
+        raise ValueError("give max_new, the most tokens of a sequence, with parents")
+    if parents is None and masks is not None:
+        raise ValueError("masks are made from parents")
+    up = _i32(parents, (total,), "parents")
+    s, t = _paged_check(pool, table, starts, parents, positions, slots, masks)
+    dev = pool.k_codes.device
+    most = 0 if parents is None else int(max_new)
+    words = masks.shape[1] if masks is not None and masks.dim() == 2 else max(1, (most + 31) // 32)
+    if not want_positions:
+        positions = None
+    elif positions is None:
+        positions = _empty_on(stream, total, torch.int32, dev)
+    if not want_slots:
+        slots = None
+    elif slots is None:
+        slots = _empty_on(stream, total, torch.int64, dev)
+    if slots is not None and (slots.dtype is not torch.int64 or tuple(slots.shape) != (total,) or not slots.is_contiguous()):
+        raise ValueError("slots must be contiguous int64 [total]")
+    if not want_masks or parents is None:
+        masks = None
+    elif masks is None:
+        masks = _empty_on(stream, (total, words), torch.int32, dev)
+    at = _i32(positions, (total,), "positions"), None if slots is None else slots.data_ptr(), _i32(masks, (total, words), "masks")
+    _check(lib().tq_paged_layout(s, t, starts.data_ptr(), total, up, most, *at, words, _stream(stream)), "tq_paged_layout")
+    return positions, slots, masks
+
+
+def tq_paged_keep(pool: Cache, table: PageTable, starts: torch.Tensor, path: torch.Tensor, kept: torch.Tensor,
+                  lens_out: torch.Tensor | None = None, total: int | None = None, stream=None) -> torch.Tensor:
+    """Move the kept new rows of every sequence (path int32 [num_seqs][>= most new tokens], its first kept[s] entries)
+    together behind its other rows; the lengths that are left, int32 [num_seqs], come back (the table keeps its own).
+    total: bound of the new tokens in all (default: of the table's lengths)."""
+    n = table.num_seqs
+    if path.dim() != 2 or path.shape[0] != n or path.shape[1] < 1:
+        raise ValueError("path must be contiguous int32 [num_seqs][most new tokens]")
+    at = _i32(path, tuple(path.shape), "path"), _i32(kept, (n,), "kept")
+    s, t = _paged_check(pool, table, starts, path, kept, lens_out)
+    if lens_out is None:
+        lens_out = _empty_on(stream, n, torch.int32, pool.k_codes.device)
+    total = min(n * table.max_len, 2 ** 31 - 1) if total is None else int(total)
+    _check(lib().tq_paged_keep(s, t, starts.data_ptr(), total, path.shape[1], at[0], path.shape[1], at[1],
+                               _i32(lens_out, (n,), "lens_out"), _stream(stream)), "tq_paged_keep")
+    return lens_out
+
+
+def tq_verify_drafts(starts: torch.Tensor, parents: torch.Tensor, tokens: torch.Tensor, target: torch.Tensor,
+                     draft: torch.Tensor | None, uniforms: torch.Tensor, last: torch.Tensor, max_new: int,
+                     path: torch.Tensor | None = None, kept: torch.Tensor | None = None,
+                     next_tokens: torch.Tensor | None = None, stream=None):
+    """Verify drafted trees (starts int32 [num_seqs + 1]; parents, tokens int32 and uniforms fp32 [total]; target and
+    draft fp32 or bf16 [total][vocab], rows contiguous; last fp32 [num_seqs]) -> (path int32 [num_seqs][max_new] of accepted
+    nodes, kept int32 [num_seqs], the next tokens int32 [num_seqs]).  draft=None: tokens not drawn at random."""
+    if starts.dim() != 1 or starts.shape[0] < 2:
+        raise ValueError("starts must be contiguous int32 [num_seqs + 1]")
+    n, max_new = starts.shape[0] - 1, int(max_new)
+    if target.dim() != 2 or (target.shape[1] > 1 and target.stride(1) != 1):
+        raise ValueError("target must be [total][vocab], rows contiguous")
+    total, vocab = target.shape
+    code = _dtype_code(target.dtype)
+    if draft is not None and (draft.shape != target.shape or draft.dtype != target.dtype or
+                              (vocab > 1 and draft.stride(1) != 1)):
+        raise ValueError("draft must be like target")
+    for x, size, what in ((uniforms, total, "uniforms"), (last, n, "last")):
+        if x.dtype is not torch.float32 or tuple(x.shape) != (size,) or not x.is_contiguous():
+            raise ValueError(f"{what} must be contiguous float32 [{size}]")
+    at = _i32(starts, (n + 1,), "starts"), _i32(parents, (total,), "parents"), _i32(tokens, (total,), "tokens")
+    dev = _one_device(starts, parents, tokens, target, draft, uniforms, last, path, kept, next_tokens)
+    if path is None:
+        path = _empty_on(stream, (n, max_new), torch.int32, dev)
+    if kept is None:
+        kept = _empty_on(stream, n, torch.int32, dev)
+    if next_tokens is None:
+        next_tokens = _empty_on(stream, n, torch.int32, dev)
+    # (a tensor of one row has no row to step to)
+    step = lambda x: max(x.stride(0), vocab) if total < 2 else x.stride(0)  # noqa: E731
+    _check(lib().tq_verify_drafts(at[0], n, total, max_new, at[1], at[2], vocab, code, target.data_ptr(), step(target),
+                                  None if draft is None else draft.data_ptr(), 0 if draft is None else step(draft),
+                                  uniforms.data_ptr(), last.data_ptr(), _i32(path, (n, max_new), "path"), max_new,
+                                  _i32(kept, (n,), "kept"), _i32(next_tokens, (n,), "next_tokens"), _stream(stream)),
+           "tq_verify_drafts")
+    return path, kept, next_tokens
+
+
+def _rotary_tensor(x: torch.Tensor, out: torch.Tensor, what: str) -> _RotaryStruct:
+    if x.dim() != 3 or x.stride(2) != 1 or out.shape != x.shape or out.dtype != x.dtype or out.stride(2) != 1:
+        raise ValueError(f"{what} must be [tokens][heads][head_dim] with head_dim contiguous, its output like it")
+    # (a dimension of one place has no stride to speak of)
+    st = [_TWO(*(t.stride(i) if t.shape[i] > 1 else t.shape[2] for i in (0, 1))) for t in (x, out)]
+    return _RotaryStruct(x.data_ptr(), out.data_ptr(), st[0], st[1], x.shape[1], 0)
+
+
+def tq_rotary(positions: torch.Tensor, freqs: torch.Tensor, q: torch.Tensor | None, k: torch.Tensor | None = None,
+              interleaved: bool = False, scale: float = 1.0, q_out: torch.Tensor | None = None,
+              k_out: torch.Tensor | None = None, stream=None):
+    """(q, k) turned by positions (int32 [tokens], below 0: left as it was) times freqs (float64 [rot_dim / 2]); q and k bf16
+    or fp32 [tokens][heads][d], any token and head strides, either None; q_out=q turns in place."""
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("give q or k")
+    if some.dim() != 3 or (q is not None and k is not None and (k.dim() != 3 or q.shape[0] != k.shape[0] or
+                                                                q.shape[2] != k.shape[2] or q.dtype != k.dtype)):
+        raise ValueError("q and k must be [tokens][heads][head_dim] of one type")
+    if freqs.dtype is not torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be contiguous float64 [rot_dim / 2]")
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("an output without its input")
+    tokens, d = some.shape[0], some.shape[2]
+    code, at = _dtype_code(some.dtype), _i32(positions, (tokens,), "positions")
+    dev = _one_device(positions, freqs, q, k, q_out, k_out)
+    if q is not None and q_out is None:
+        q_out = _empty_on(stream, q.shape, q.dtype, dev)
+    if k is not None and k_out is None:
+        k_out = _empty_on(stream, k.shape, k.dtype, dev)
+    a = None if q is None else ctypes.byref(_rotary_tensor(q, q_out, "q"))
+    b = None if k is None else ctypes.byref(_rotary_tensor(k, k_out, "k"))
+    _check(lib().tq_rotary(at, tokens, d, 2 * freqs.shape[0], int(interleaved), freqs.data_ptr(), float(scale), code, a, b,
+                           _stream(stream)), "tq_rotary")
+    return q_out, k_out
+
+
+def tq_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                          original_len: int = 0, fast: float = 32.0, slow: float = 1.0):
+    """(frequencies float64 [rot_dim / 2], scale) for tq_rotary; scaling "none", "linear", "ntk" or "yarn" (see tq.h)."""
+    import numpy as np
+
+    if scaling not in ROTARY_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALING)}")
+    if int(rot_dim) < 2 or int(rot_dim) > 512:
+        raise ValueError("rot_dim must be even, 2 .. 512")
+    out, scale = np.zeros(max(1, int(rot_dim) // 2), dtype=np.float64), ctypes.c_float(0.0)
+    _check(lib().tq_rotary_frequencies(int(rot_dim), float(base), ROTARY_SCALING[scaling], float(factor), int(original_len),
+                                       float(fast), float(slow), out.ctypes.data, ctypes.byref(scale)), "tq_rotary_frequencies")
+    return out, float(scale.value)
 
 
 def tq_check_wait_timeout(stream=None) -> None:

@@ -422,11 +422,11 @@ tq_status check_paged_attention(const tq_cache *c, const tq_page_table *t, int32
     return (int64_t)t->num_seqs * c->num_kv_heads > (int64_t(1) << 30) ? TQ_ERR_SHAPE : TQ_OK;
 }
 
-tq::PagedBounds paged_bounds(const tq_page_table *t, int64_t total, int64_t max_new)
+tq::PagedBounds paged_bounds(const tq_page_table *t, int64_t total, int64_t max_new, bool tree)
 {
     const int64_t all = t->num_seqs * t->max_len;
     return tq::PagedBounds{t->num_seqs, total, max_new < total ? max_new : total, t->max_len,
-                           t->total_len > 0 && t->total_len < all ? t->total_len : all, INT32_MAX};
+                           t->total_len > 0 && t->total_len < all ? t->total_len : all, INT32_MAX, tree};
 }
 
 tq::PagedView paged_view(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total)
@@ -472,27 +472,30 @@ tq_status tq_paged_decode(const tq_cache *c, const tq_page_table *t, const int32
     return cuda_status(tq::launch_paged_decode(view(c), pv, dt == TQ_F32, k_out, v_out, (cudaStream_t)stream));
 }
 
-size_t tq_paged_attention_workspace_bytes(const tq_cache *c, const tq_page_table *t, int32_t q_heads, int64_t total,
-                                          int64_t max_new)
+namespace {
+size_t paged_workspace(const tq_cache *c, const tq_page_table *t, int32_t q_heads, int64_t total, int64_t max_new, bool tree)
 {
     if (check_cache(c) != TQ_OK || check_table(c, t) != TQ_OK) return 0;
     if (check_paged_attention(c, t, q_heads, total, max_new) != TQ_OK) return 0;
-    return tq::paged_attention_workspace_bytes(view(c), paged_bounds(t, total > 0 ? total : 1, max_new), q_heads);
+    return tq::paged_attention_workspace_bytes(view(c), paged_bounds(t, total > 0 ? total : 1, max_new, tree), q_heads);
 }
 
-tq_status tq_paged_attention(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total,
-                             int64_t max_new, const void *q, const int64_t qs[2], int32_t q_heads, float scale, void *out,
-                             void *ws, size_t ws_bytes, tq_stream_t stream)
+// causal, or with the masks of trees
+tq_status paged_attention(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total, int64_t max_new,
+                          const void *q, const int64_t qs[2], int32_t q_heads, float scale, bool tree, const int32_t *masks,
+                          int64_t mask_words, void *out, void *ws, size_t ws_bytes, tq_stream_t stream)
 {
     tq_status st = check_paged(c, t, starts, total);
     if (st != TQ_OK) return st;
     if ((st = check_paged_attention(c, t, q_heads, total, max_new)) != TQ_OK) return st;
     if (total == 0) return TQ_OK;
     if ((st = check_ragged(q, qs)) != TQ_OK) return st;
+    if (tree && !masks) return TQ_ERR_NULL;
+    if (tree && (mask_words < 1 || mask_words < ((max_new < total ? max_new : total) + 31) / 32)) return TQ_ERR_SHAPE;
     if (!out) return TQ_ERR_NULL;
     if (!aligned32(out)) return TQ_ERR_ALIGN;
     const tq::CacheView cv = view(c);
-    const tq::PagedBounds b = paged_bounds(t, total, max_new);
+    const tq::PagedBounds b = paged_bounds(t, total, max_new, tree);
     const size_t need = tq::paged_attention_workspace_bytes(cv, b, q_heads);
     if (need == 0) return TQ_ERR_CUDA;  // the occupancy query failed
     if (!ws || ws_bytes < need) return TQ_ERR_WORKSPACE;
@@ -500,7 +503,170 @@ tq_status tq_paged_attention(const tq_cache *c, const tq_page_table *t, const in
     const tq::PagedView pv = paged_view(c, t, starts, total);
     if (!pv.err) return TQ_ERR_CUDA;
     return cuda_status(tq::launch_paged_attention(cv, pv, b, static_cast<const uint16_t *>(q), qs, q_heads, scale,
+                                                  reinterpret_cast<const uint32_t *>(masks), mask_words,
                                                   static_cast<uint16_t *>(out), ws, ws_bytes, (cudaStream_t)stream));
+}
+}  // namespace
+
+size_t tq_paged_attention_workspace_bytes(const tq_cache *c, const tq_page_table *t, int32_t q_heads, int64_t total,
+                                          int64_t max_new)
+{
+    return paged_workspace(c, t, q_heads, total, max_new, false);
+}
+
+tq_status tq_paged_attention(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total,
+                             int64_t max_new, const void *q, const int64_t qs[2], int32_t q_heads, float scale, void *out,
+                             void *ws, size_t ws_bytes, tq_stream_t stream)
+{
+    return paged_attention(c, t, starts, total, max_new, q, qs, q_heads, scale, false, nullptr, 0, out, ws, ws_bytes, stream);
+}
+
+size_t tq_paged_tree_attention_workspace_bytes(const tq_cache *c, const tq_page_table *t, int32_t q_heads, int64_t total,
+                                               int64_t max_new)
+{
+    return paged_workspace(c, t, q_heads, total, max_new, true);
+}
+
+tq_status tq_paged_tree_attention(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total,
+                                  int64_t max_new, const void *q, const int64_t qs[2], int32_t q_heads, float scale,
+                                  const int32_t *masks, int64_t mask_words, void *out, void *ws, size_t ws_bytes,
+                                  tq_stream_t stream)
+{
+    return paged_attention(c, t, starts, total, max_new, q, qs, q_heads, scale, true, masks, mask_words, out, ws, ws_bytes,
+                           stream);
+}
+
+tq_status tq_page_table_update(const tq_cache *c, const tq_page_table *t, const int32_t *lens, const int32_t *new_tokens,
+                               int32_t *lens_out, int32_t *starts, int32_t *free_pages, int64_t free_capacity,
+                               const int32_t *free_count, int32_t *free_count_out, tq_stream_t stream)
+{
+    tq_status st = check_cache(c);
+    if (st != TQ_OK) return st;
+    if ((st = check_table(c, t)) != TQ_OK) return st;
+    if (!lens || !lens_out || !free_pages || !free_count || !free_count_out || (starts && !new_tokens)) return TQ_ERR_NULL;
+    if (free_capacity < 1 || free_capacity > INT32_MAX) return TQ_ERR_SHAPE;
+    tq::PagedUpdate u{};
+    u.pages = const_cast<int32_t *>(t->pages);
+    u.lens = t->seq_lens;
+    u.want = lens;
+    u.fresh = new_tokens;
+    u.lens_out = lens_out;
+    u.starts = starts;
+    u.free_pages = free_pages;
+    u.free_count = free_count;
+    u.count_out = free_count_out;
+    u.stride = t->stride;
+    u.max_len = t->max_len;
+    u.free_cap = free_capacity;
+    u.seqs = t->num_seqs;
+    u.num_pages = c->batch;
+    u.div_page = tq::make_fastdiv((uint32_t)c->capacity);
+    u.err = tq::device_error_word();
+    if (!u.err) return TQ_ERR_CUDA;
+    return cuda_status(tq::launch_page_table_update(u, (cudaStream_t)stream));
+}
+
+tq_status tq_paged_layout(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total,
+                          const int32_t *parents, int64_t max_new, int32_t *positions, int64_t *slots, int32_t *masks,
+                          int64_t mask_words, tq_stream_t stream)
+{
+    tq_status st = check_paged(c, t, starts, total);
+    if (st != TQ_OK) return st;
+    if (masks && !parents) return TQ_ERR_NULL;
+    if (parents && max_new < 1) return TQ_ERR_SHAPE;
+    const int64_t most = max_new < total ? max_new : total;
+    if (masks && (mask_words < 1 || mask_words < (most + 31) / 32)) return TQ_ERR_SHAPE;
+    if (total == 0 || (!positions && !slots && !masks)) return TQ_OK;
+    const tq::PagedView pv = paged_view(c, t, starts, total);
+    if (!pv.err) return TQ_ERR_CUDA;
+    return cuda_status(tq::launch_paged_layout(pv, parents, most, positions, slots, reinterpret_cast<uint32_t *>(masks),
+                                               mask_words, (cudaStream_t)stream));
+}
+
+tq_status tq_paged_keep(const tq_cache *c, const tq_page_table *t, const int32_t *starts, int64_t total, int64_t max_new,
+                        const int32_t *path, int64_t path_stride, const int32_t *kept, int32_t *lens_out, tq_stream_t stream)
+{
+    tq_status st = check_paged(c, t, starts, total);
+    if (st != TQ_OK) return st;
+    if (!path || !kept || !lens_out) return TQ_ERR_NULL;
+    if (lens_out == t->seq_lens) return TQ_ERR_SHAPE;  // (read by every CTA of a sequence, written by one)
+    if (max_new < 1 || path_stride < max_new) return TQ_ERR_SHAPE;
+    if ((int64_t)t->num_seqs * c->num_kv_heads > (int64_t(1) << 30)) return TQ_ERR_SHAPE;
+    const tq::PagedView pv = paged_view(c, t, starts, total);
+    if (!pv.err) return TQ_ERR_CUDA;
+    return cuda_status(tq::launch_paged_keep(view(c), pv, max_new, path, path_stride, kept, lens_out, (cudaStream_t)stream));
+}
+
+tq_status tq_verify_drafts(const int32_t *starts, int32_t num_seqs, int64_t total, int64_t max_new, const int32_t *parents,
+                           const int32_t *tokens, int64_t vocab, tq_dtype dt, const void *target, int64_t target_stride,
+                           const void *draft, int64_t draft_stride, const float *uniforms, const float *last, int32_t *path,
+                           int64_t path_stride, int32_t *kept, int32_t *next, tq_stream_t stream)
+{
+    if (!starts || !last || !path || !kept || !next) return TQ_ERR_NULL;
+    if (total > 0 && (!parents || !tokens || !target || !uniforms)) return TQ_ERR_NULL;
+    if (dt != TQ_BF16 && dt != TQ_F32) return TQ_ERR_SHAPE;
+    if (num_seqs < 1 || num_seqs > (1 << 24) || total < 0 || total > INT32_MAX) return TQ_ERR_SHAPE;
+    if (max_new < 1 || max_new > TQ_MAX_DRAFT || path_stride < max_new) return TQ_ERR_SHAPE;
+    if (vocab < 1 || vocab > (int64_t(1) << 30)) return TQ_ERR_SHAPE;
+    if (target_stride < vocab || (draft && draft_stride < vocab)) return TQ_ERR_SHAPE;
+    const uintptr_t size = dt == TQ_F32 ? 4 : 2;
+    if ((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) % size != 0) return TQ_ERR_ALIGN;
+    tq::VerifyCall v{starts, parents, tokens, total, max_new, vocab, num_seqs, target, draft, target_stride, draft_stride,
+                     uniforms, last, path, kept, next, path_stride, dt == TQ_F32, tq::device_error_word()};
+    if (!v.err) return TQ_ERR_CUDA;
+    return cuda_status(tq::launch_verify(v, (cudaStream_t)stream));
+}
+
+tq_status tq_rotary(const int32_t *positions, int64_t tokens, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                    const double *freqs, float scale, tq_dtype dt, const tq_rotary_tensor *q, const tq_rotary_tensor *k,
+                    tq_stream_t stream)
+{
+    if (!positions || !freqs || (!q && !k)) return TQ_ERR_NULL;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256 && head_dim != 512) return TQ_ERR_HEAD_DIM;
+    if (rot_dim < 2 || rot_dim > head_dim || rot_dim % 2 != 0 || tokens < 0 || tokens > INT32_MAX) return TQ_ERR_SHAPE;
+    if (dt != TQ_BF16 && dt != TQ_F32) return TQ_ERR_SHAPE;
+    tq::RotaryCall r{};
+    const int64_t unit = dt == TQ_F32 ? 4 : 8;  // elements of 16 bytes
+    const tq_rotary_tensor *in[2] = {q, k};
+    for (int i = 0; i < 2; ++i) {
+        if (!in[i]) continue;
+        const tq_rotary_tensor &a = *in[i];
+        if (!a.x || !a.out) return TQ_ERR_NULL;
+        if (a.heads < 1 || a.heads > 65535 || a.reserved != 0) return TQ_ERR_SHAPE;
+        const int64_t st[4] = {a.x_strides[0], a.x_strides[1], a.out_strides[0], a.out_strides[1]};
+        for (int64_t x : st) {
+            if (x < 0) return TQ_ERR_SHAPE;
+            if (x % unit != 0) return TQ_ERR_ALIGN;
+        }
+        if (!aligned16(a.x) || !aligned16(a.out)) return TQ_ERR_ALIGN;
+        // outputs apart from one another; in place element for element
+        if ((st[2] < head_dim && tokens > 1) || (st[3] < head_dim && a.heads > 1)) return TQ_ERR_SHAPE;
+        if (a.x == a.out && (st[0] != st[2] || st[1] != st[3])) return TQ_ERR_SHAPE;
+        r.t[i] = tq::RotaryTensor{a.x, a.out, st[0], st[1], st[2], st[3], a.heads};
+    }
+    if (tokens == 0) return TQ_OK;
+    r.pos = positions;
+    r.freqs = freqs;
+    r.tokens = tokens;
+    r.scale = scale;
+    r.d = head_dim;
+    r.rot = rot_dim;
+    r.interleaved = interleaved != 0;
+    r.f32 = dt == TQ_F32;
+    return cuda_status(tq::launch_rotary(r, (cudaStream_t)stream));
+}
+
+tq_status tq_rotary_frequencies(int32_t rot_dim, double base, tq_rotary_scaling scaling, double factor, int64_t original_len,
+                                double fast, double slow, double *host_freqs, float *host_scale)
+{
+    if (!host_freqs || !host_scale) return TQ_ERR_NULL;
+    if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > 512 || !(base > 1.0) || !(base < 1e300)) return TQ_ERR_SHAPE;
+    if (scaling != TQ_ROTARY_PLAIN && scaling != TQ_ROTARY_LINEAR && scaling != TQ_ROTARY_NTK && scaling != TQ_ROTARY_YARN)
+        return TQ_ERR_SHAPE;
+    if (scaling != TQ_ROTARY_PLAIN && !(factor >= 1.0 && factor < 1e9)) return TQ_ERR_SHAPE;
+    if (scaling == TQ_ROTARY_YARN && (original_len < 1 || !(slow > 0.0) || !(fast >= slow) || !(fast < 1e9))) return TQ_ERR_SHAPE;
+    tq::rotary_frequencies(rot_dim, base, (int)scaling, factor, original_len, fast, slow, host_freqs, host_scale);
+    return TQ_OK;
 }
 
 tq_status tq_check_wait_timeout(tq_stream_t stream)

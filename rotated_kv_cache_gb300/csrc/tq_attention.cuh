@@ -180,7 +180,9 @@ __device__ __forceinline__ uint32_t shr_fma(uint32_t x)
 // ---------------------------------------------------------------- the split kernel
 // MODE: 0 contiguous; 1 paged, one new token a sequence at most; 2 paged, any
 // (masks for the rows that some column does not see: 43 instructions per warp and
-// stage, 4 % of the time of a decode step).
+// stage, 4 % of the time of a decode step); 3 paged, the new tokens seeing one
+// another by their mask rows (a column's mask words are read in the tiles that
+// hold new rows alone).
 // Paged: the CTA runs the segments of its share of a paged batch one after
 // another (tq_paged.cuh) instead of the grid's (split, column blocks,
 // sequence).  A column is then one (new token, q-head) of the kv-head, a block
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
     attn_split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ AttnParams p)
 {
     using A = AGeo<KB, D, VB, NBC>;
-    constexpr bool PAGED = MODE != 0, CAUSAL = MODE == 2;
+    constexpr bool PAGED = MODE != 0, CAUSAL = MODE == 2, TREE = MODE == 3;
     constexpr int NG = A::NG;
     constexpr int NH = NBC * kG;  // MMA columns of the CTA
     extern __shared__ uint8_t smem_raw[];
@@ -233,7 +235,14 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
     // paged: the block's columns are col0 .. col0 + cols - 1; rows that column c sees, from the
     // segment's first row on
     auto block_cols = [&] { return imin_int(seg.n * p.G - seg.hb * NH, NH); };
-    auto column_rows = [&](int c) { return seg.len - seg.n + 1 + (seg.hb * NH + c) / p.G - seg.first * A::ST; };
+    auto column_rows = [&](int c) {
+        return (TREE ? seg.len : seg.len - seg.n + 1 + (seg.hb * NH + c) / p.G) - seg.first * A::ST;
+    };
+    // tree: which of the 32 rows from row r of the segment on column c sees
+    [[maybe_unused]] auto tree_rows = [&](int c, int r) {
+        const int64_t tok = seg.s0 + (seg.hb * NH + imin_int(c, block_cols() - 1)) / p.G;
+        return paged_tree_bits(p.pg.masks + tok * p.pg.mask_words, r - (seg.len - seg.n - seg.first * A::ST), seg.n);
+    };
     // row offsets within the split fit 32 bits: a split never holds 2^31 rows
     // (136 B per row at the smallest width would take 292 GB)
     const int split_rows = PAGED ? imin_int(column_rows(block_cols() - 1), seg.count * A::ST) : (int)(t_end - t_begin);
@@ -434,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
     for (int q = 0; q < 4; ++q) voff[q] = A::OFF_V + vr[q] * A::RBV + 4 * v_word;
     const uint32_t ring0 = smem_addr(stages);
     // PAGED, several new tokens: rows from here on are hidden from some column
-    const int first_hidden = CAUSAL && seg.n > 1 ? column_rows(0) : INT32_MAX;
+    const int first_hidden = TREE ? seg.len - seg.n - seg.first * A::ST : CAUSAL && seg.n > 1 ? column_rows(0) : INT32_MAX;
     if constexpr (!PAGED) ok = true;
     int slot = 0;
     uint32_t phase = 0;  // ring slot and barrier parity of stage s, from the segment's start
@@ -555,6 +564,18 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
                             }
                     }
                 }
+                if constexpr (TREE) {
+                    if (tile_r + 16 > first_hidden) {
+#pragma unroll
+                        for (int nb = 0; nb < NBC; ++nb)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t rows = tree_rows(kG * nb + 2 * c + j, tile_r) >> g;
+                                if (!(rows & 1u)) S[nb][t2][0][j] = -INFINITY;
+                                if (!(rows & 0x100u)) S[nb][t2][1][j] = -INFINITY;
+                            }
+                    }
+                }
             }
         }
         // ---------------- online softmax (base 2) over the warp's tiles, heads 2c, 2c+1
@@ -642,7 +663,17 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
             // paged: a hidden row's rms may be anything; the weights of the lane's column (g of
             // each block) keep to the rows it sees
             uint32_t seen[NBC][2];
-            const bool masked = CAUSAL && tile_r + 16 > first_hidden;
+            const bool masked = (CAUSAL || TREE) && tile_r + 16 > first_hidden;
+            if constexpr (TREE) {
+                if (masked) {
+#pragma unroll
+                    for (int nb = 0; nb < NBC; ++nb) {
+                        const uint32_t rows = tree_rows(kG * nb + g, tile_r) >> (2 * c);  // rows 2c, 2c + 1, 2c + 8, 2c + 9
+                        seen[nb][0] = (rows & 1u ? 0xFFFFu : 0u) | (rows & 2u ? 0xFFFF0000u : 0u);
+                        seen[nb][1] = (rows & 0x100u ? 0xFFFFu : 0u) | (rows & 0x200u ? 0xFFFF0000u : 0u);
+                    }
+                }
+            }
             if constexpr (CAUSAL) {
                 if (masked) {
 #pragma unroll
@@ -666,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, AGeo<KB, D, VB, NBC>::MIN_BLOCKS)
                 for (int nb = 0; nb < NBC; ++nb) {
                     b0[nb] = hmul2(pt0[nb], sp0);
                     b1[nb] = hmul2(pt1[nb], sp1);
-                    if constexpr (CAUSAL) {
+                    if constexpr (CAUSAL || TREE) {
                         if (masked) {
                             b0[nb] &= seen[nb][0];
                             b1[nb] &= seen[nb][1];

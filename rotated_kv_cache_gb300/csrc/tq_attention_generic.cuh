@@ -251,6 +251,7 @@ struct GGeo {
     static constexpr int MIN_BLOCKS = D >= 512 ? 1 : (D * NB / 4 <= 32 ? 6 : 4);
 };
 
+// MODE: 0 contiguous, 1 paged, 2 paged with masks among the new tokens (TREE).
 // PAGED: the CTA runs the segments of its share of a paged batch one after
 // another (tq_paged.cuh) instead of the grid's (split, column block, sequence);
 // stages arrive chunk by chunk, a chunk lying within a page, each lane of the
@@ -260,11 +261,12 @@ struct GGeo {
 // key codes are cut (key_pairs).  Separate instantiations: the same choices made
 // at run time inside one kernel cost more than they saved (the larger unrolled
 // body).
-template <int D, int NB, int VLUT, int KEY, bool PAGED = false>
+template <int D, int NB, int VLUT, int KEY, int MODE = 0>
 __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     attn_generic_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ GenParams p)
 {
     using A = GGeo<D, NB>;
+    constexpr bool PAGED = MODE != 0, TREE = MODE == 2;
     constexpr int CB = A::CB;
     pdl_wait_primary();  // whatever the previous kernel on the stream writes or reads is settled
     pdl_allow_dependents();
@@ -306,7 +308,13 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
     // h G + col % G; query row i sees cache rows [0, base0 + i)
     const int col0 = hb * CB;
     const int col_last = (cols < col0 + CB ? cols : col0 + CB) - 1;
-    const int64_t lim_lo = base0 + col0 / p.G, lim_hi = base0 + col_last / p.G;
+    // (TREE: the new ones, from base0 - 1 on, by its mask)
+    const int64_t lim_lo = TREE ? base0 - 1 : base0 + col0 / p.G, lim_hi = TREE ? base0 - 1 + M : base0 + col_last / p.G;
+    // TREE: which of the 32 rows from row t of the sequence on column col sees
+    [[maybe_unused]] auto tree_rows = [&](int col, int64_t t) {
+        const int64_t tok = seg.s0 + (col < cols ? col / p.G : M - 1);
+        return paged_tree_bits(p.pg.masks + tok * p.pg.mask_words, (int)(t - (base0 - 1)), M);
+    };
     const int64_t t_begin = PAGED ? (int64_t)seg.first * gT : (int64_t)split * p.tokens_per_split;
     const int64_t t_end = imin64(lim_hi, t_begin + (PAGED ? (int64_t)seg.count * gT : p.tokens_per_split));
     const int n_stages = t_end > t_begin && ok ? (int)((t_end - t_begin + gT - 1) / gT) : 0;
@@ -578,7 +586,17 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
 #pragma unroll
         for (int t2 = 0; t2 < A::TILES; ++t2) {
             const int64_t tt0 = tile_t0 + TR * t2;
-            if (tt0 + 16 > lim_lo) {
+            if constexpr (TREE) {
+                if (tt0 + 16 > lim_lo)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t rows = tree_rows(col0 + nb * gN + 2 * c + j, tt0) >> g;
+                            if (!(rows & 1u)) S[t2][nb][0][j] = -INFINITY;
+                            if (!(rows & 0x100u)) S[t2][nb][1][j] = -INFINITY;
+                        }
+            } else if (tt0 + 16 > lim_lo) {
                 const int64_t ta = tt0 + g - base0, tb = ta + 8;
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
@@ -668,7 +686,13 @@ __global__ void __launch_bounds__(GGeo<D, NB>::THREADS, GGeo<D, NB>::MIN_BLOCKS)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     seen[t2][nb][0] = seen[t2][nb][1] = 0xFFFFFFFFu;
-                    if (M > 1 && tile_t0 + TR * t2 + 16 > lim_lo) {
+                    if constexpr (TREE) {
+                        if (tile_t0 + TR * t2 + 16 > lim_lo) {
+                            const uint32_t rows = tree_rows(col0 + nb * gN + g, tile_t0 + TR * t2) >> (2 * c);
+                            seen[t2][nb][0] = (rows & 1u ? 0xFFFFu : 0u) | (rows & 2u ? 0xFFFF0000u : 0u);
+                            seen[t2][nb][1] = (rows & 0x100u ? 0xFFFFu : 0u) | (rows & 0x200u ? 0xFFFF0000u : 0u);
+                        }
+                    } else if (M > 1 && tile_t0 + TR * t2 + 16 > lim_lo) {
                         const int col = col0 + nb * gN + g;
                         const int64_t lim = base0 + (col < cols ? col / p.G : M - 1) - (tile_t0 + TR * t2 - 16 * warp);
                         seen[t2][nb][0] = (vr[0] < lim ? 0xFFFFu : 0u) | (vr[1] < lim ? 0xFFFF0000u : 0u);
@@ -1041,27 +1065,27 @@ inline int gen_nb(int d, int64_t cols)
 }
 
 // Calls f with the kernel instantiation the plan's VLUT and KEY name.
-template <int D, int NB, int VLUT, bool PAGED, typename F>
+template <int D, int NB, int VLUT, int MODE, typename F>
 auto gen_dispatch_key(const GenPlan &pl, F &&f)
 {
     // paged, 8- or 4-bit keys with 2- or 3-bit values: the specialised kernel's up
     // to head_dim 256, but for pools whose rows pass 2^31, which take KEY 0
-    if constexpr (PAGED && D <= 256 && VLUT != 0) return f(attn_generic_kernel<D, NB, VLUT, 0, PAGED>);
-    else return pl.key == 8 ? f(attn_generic_kernel<D, NB, VLUT, 8, PAGED>)
-           : pl.key == 4 ? f(attn_generic_kernel<D, NB, VLUT, 4, PAGED>)
-                         : f(attn_generic_kernel<D, NB, VLUT, 0, PAGED>);
+    if constexpr (MODE != 0 && D <= 256 && VLUT != 0) return f(attn_generic_kernel<D, NB, VLUT, 0, MODE>);
+    else return pl.key == 8 ? f(attn_generic_kernel<D, NB, VLUT, 8, MODE>)
+           : pl.key == 4 ? f(attn_generic_kernel<D, NB, VLUT, 4, MODE>)
+                         : f(attn_generic_kernel<D, NB, VLUT, 0, MODE>);
 }
 
-template <int D, int NB, bool PAGED = false, typename F>
+template <int D, int NB, int MODE = 0, typename F>
 auto gen_dispatch(const GenPlan &pl, F &&f)
 {
-    return pl.vlut == 3   ? gen_dispatch_key<D, NB, 3, PAGED>(pl, f)
-           : pl.vlut == 2 ? gen_dispatch_key<D, NB, 2, PAGED>(pl, f)
-                          : gen_dispatch_key<D, NB, 0, PAGED>(pl, f);
+    return pl.vlut == 3   ? gen_dispatch_key<D, NB, 3, MODE>(pl, f)
+           : pl.vlut == 2 ? gen_dispatch_key<D, NB, 2, MODE>(pl, f)
+                          : gen_dispatch_key<D, NB, 0, MODE>(pl, f);
 }
 
 // Stage layout, instantiation and shared memory of a plan; resident CTAs per SM (0 on failure).
-template <int D, int NB, bool PAGED>
+template <int D, int NB, int MODE>
 int gen_layout(const CacheView &c, GenPlan &pl)
 {
     using A = GGeo<D, NB>;
@@ -1084,7 +1108,7 @@ int gen_layout(const CacheView &c, GenPlan &pl)
               gMaxStages * 12 /*barriers, counters*/;
     static KernelSetup table[3][3];  // [VLUT][KEY] of the instantiation
     KernelSetup &setup = table[pl.vlut == 0 ? 0 : pl.vlut - 1][pl.key / 4];
-    return gen_dispatch<D, NB, PAGED>(pl, [&](auto kern) {
+    return gen_dispatch<D, NB, MODE>(pl, [&](auto kern) {
         int n;
         return setup.get(kern, GGeo<D, NB>::THREADS, (size_t)pl.smem, kMaxDynamicSmem, n) == cudaSuccess ? n : 0;
     });
@@ -1094,7 +1118,7 @@ template <int D, int NB>
 bool gen_plan_nb(const CacheView &c, int q_heads, int64_t m, int64_t seq_len, GenPlan &pl)
 {
     using A = GGeo<D, NB>;
-    const int per_sm = gen_layout<D, NB, false>(c, pl);
+    const int per_sm = gen_layout<D, NB, 0>(c, pl);
     if (per_sm < 1) return false;
     const int64_t cols = (int64_t)(q_heads / c.H) * m;
     pl.hb = (int)((cols + A::CB - 1) / A::CB);
@@ -1130,10 +1154,10 @@ bool gen_plan(const CacheView &c, int q_heads, int64_t m, int64_t seq_len, GenPl
     return false;
 }
 
-template <int D, int NB, bool PAGED = false>
+template <int D, int NB, int MODE = 0>
 cudaError_t gen_launch(const GenPlan &pl, dim3 grid, const CUtensorMap &kmap, const GenParams &p, cudaStream_t s)
 {
-    return gen_dispatch<D, NB, PAGED>(
+    return gen_dispatch<D, NB, MODE>(
         pl, [&](auto kern) { return launch_dependent(kern, grid, dim3(GGeo<D, NB>::THREADS), (size_t)pl.smem, s, kmap, p); });
 }
 
@@ -1238,32 +1262,32 @@ cudaError_t gen_run(const CacheView &c, const uint16_t *q, int QH, int64_t m, in
 // ---------------------------------------------------------------- paged launches
 // Resident CTAs (one wave) and geometry of the paged kernel for blocks that
 // take up to `cols` columns of a sequence's kv-head.
-template <int D, int NB>
+template <int D, int NB, int MODE>
 bool gen_paged_plan_nb(const CacheView &c, GenPlan &pl, PagedShape &sh)
 {
-    const int per_sm = gen_layout<D, NB, true>(c, pl);
+    const int per_sm = gen_layout<D, NB, MODE>(c, pl);
     sh = PagedShape{gT, gN * NB, per_sm * num_sms()};
     return per_sm >= 1;
 }
 
-template <int D>
+template <int D, int MODE>
 bool gen_paged_plan(const CacheView &c, int64_t cols, GenPlan &pl, PagedShape &sh)
 {
     switch (gen_nb(D, cols)) {
-    case 1: return gen_paged_plan_nb<D, 1>(c, pl, sh);
-    case 2: if constexpr (D <= 256) return gen_paged_plan_nb<D, 2>(c, pl, sh); break;
-    case 4: if constexpr (D <= 128) return gen_paged_plan_nb<D, 4>(c, pl, sh); break;
+    case 1: return gen_paged_plan_nb<D, 1, MODE>(c, pl, sh);
+    case 2: if constexpr (D <= 256) return gen_paged_plan_nb<D, 2, MODE>(c, pl, sh); break;
+    case 4: if constexpr (D <= 128) return gen_paged_plan_nb<D, 4, MODE>(c, pl, sh); break;
     }
     return false;
 }
 
-template <int D>
+template <int D, int MODE>
 cudaError_t gen_paged_run(const CacheView &c, const PagedSplit &pg, int64_t cols, const uint16_t *q, int QH, float scale,
                           float *part_o, float *part_ml, cudaStream_t s)
 {
     GenPlan pl;
     PagedShape sh;
-    if (!gen_paged_plan<D>(c, cols, pl, sh)) return cudaErrorInvalidConfiguration;
+    if (!gen_paged_plan<D, MODE>(c, cols, pl, sh)) return cudaErrorInvalidConfiguration;
     GenParams p{};
     if (!gen_params<D>(c, pl, q, QH, scale, p)) return cudaErrorInvalidDevice;
     p.part_o = part_o;
@@ -1274,9 +1298,9 @@ cudaError_t gen_paged_run(const CacheView &c, const PagedSplit &pg, int64_t cols
     if (pl.key != 0 && !gen_key_map<D>(c, &kmap, gcd_int(gT, (int)c.cap))) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)sh.ctas);
     switch (pl.nb) {
-    case 1: return gen_launch<D, 1, true>(pl, grid, kmap, p, s);
-    case 2: if constexpr (D <= 256) return gen_launch<D, 2, true>(pl, grid, kmap, p, s); break;
-    case 4: if constexpr (D <= 128) return gen_launch<D, 4, true>(pl, grid, kmap, p, s); break;
+    case 1: return gen_launch<D, 1, MODE>(pl, grid, kmap, p, s);
+    case 2: if constexpr (D <= 256) return gen_launch<D, 2, MODE>(pl, grid, kmap, p, s); break;
+    case 4: if constexpr (D <= 128) return gen_launch<D, 4, MODE>(pl, grid, kmap, p, s); break;
     }
     return cudaErrorInvalidValue;
 }
@@ -1312,14 +1336,19 @@ cudaError_t combine_parts(const float *part_o, const float *part_ml, float *out,
     {                                                                                                                    \
         return combine_parts<D>(part_o, part_ml, out, B, H, QH, m, hb, cb, splits, sg, s);                               \
     }                                                                                                                    \
-    bool paged_generic_shape_d##D(const CacheView &c, int64_t cols, PagedShape &sh)                                      \
+    }
+
+// The paged launches (of the same unit, MODE 1, and of the unit for masks, MODE 2: NAME d<head_dim> / d<head_dim>_tree).
+#define TQ_PAGED_GENERIC_ENTRIES(D, MODE, NAME)                                                                         \
+    namespace tq {                                                                                                       \
+    bool paged_generic_shape_##NAME(const CacheView &c, int64_t cols, PagedShape &sh)                                    \
     {                                                                                                                    \
         GenPlan pl;                                                                                                      \
-        return gen_paged_plan<D>(c, cols, pl, sh);                                                                       \
+        return gen_paged_plan<D, MODE>(c, cols, pl, sh);                                                                 \
     }                                                                                                                    \
-    cudaError_t launch_paged_generic_d##D(const CacheView &c, const PagedSplit &pg, int64_t cols, const uint16_t *q,    \
-                                          int QH, float scale, float *part_o, float *part_ml, cudaStream_t s)           \
+    cudaError_t launch_paged_generic_##NAME(const CacheView &c, const PagedSplit &pg, int64_t cols, const uint16_t *q,  \
+                                            int QH, float scale, float *part_o, float *part_ml, cudaStream_t s)         \
     {                                                                                                                    \
-        return gen_paged_run<D>(c, pg, cols, q, QH, scale, part_o, part_ml, s);                                          \
+        return gen_paged_run<D, MODE>(c, pg, cols, q, QH, scale, part_o, part_ml, s);                                    \
     }                                                                                                                    \
     }

@@ -2,3 +2,4 @@
 #include "tq_attention_generic.cuh"
 
 TQ_ATTENTION_GENERIC_ENTRIES(128)
+TQ_PAGED_GENERIC_ENTRIES(128, 1, d128)

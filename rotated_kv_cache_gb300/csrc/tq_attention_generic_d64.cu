@@ -2,3 +2,4 @@
 #include "tq_attention_generic.cuh"
 
 TQ_ATTENTION_GENERIC_ENTRIES(64)
+TQ_PAGED_GENERIC_ENTRIES(64, 1, d64)

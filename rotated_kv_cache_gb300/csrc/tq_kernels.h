@@ -91,6 +91,8 @@ struct PagedSplit {
     int64_t wide;             // sequences with more new tokens than this are another kernel's
     const int32_t *spill;     // [seqs], or null: but for those marked here
     int nch, ru;              // chunks per stage, rows per chunk
+    const uint32_t *masks;    // null: causal; else bit j of row t: token t sees new row j of its sequence
+    int64_t mask_words;       // words from one token's mask to the next
 };
 
 __host__ __device__ constexpr int gcd_int(int a, int b) { return b == 0 ? a : gcd_int(b, a % b); }
@@ -100,6 +102,7 @@ struct PagedBounds {
     int seqs;
     int64_t total, max_new, max_len, total_len;
     int64_t wide;  // more new tokens than this make a sequence wide (tq_paged_wide.cu); INT32_MAX: none is
+    bool tree;     // the new tokens see one another by masks
 };
 
 // The chunks of a kernel with `stage` rows per stage: a chunk lies within a page.
@@ -226,12 +229,12 @@ cudaError_t launch_paged_append(const CacheView &c, const PagedView &v, const ui
                                 const uint16_t *vv, const int64_t vs[2], cudaStream_t s);
 cudaError_t launch_paged_decode(const CacheView &c, const PagedView &v, bool f32, void *k_out, void *v_out,
                                 cudaStream_t s);
-// Causal attention of ragged tokens q (strides {token, head}) -> out bf16 [total][QH][d];
-// no sequence has more than max_new of them.  0 bytes: an occupancy query failed.
+// Attention of ragged tokens q (strides {token, head}) -> out bf16 [total][QH][d], causal or by masks
+// (b.tree; mask_words apart); no sequence has more than max_new of them.  0 bytes: an occupancy query failed.
 size_t paged_attention_workspace_bytes(const CacheView &c, const PagedBounds &b, int QH);
 cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const PagedBounds &b, const uint16_t *q,
-                                   const int64_t qs[2], int QH, float scale, uint16_t *out, void *ws, size_t ws_bytes,
-                                   cudaStream_t s);
+                                   const int64_t qs[2], int QH, float scale, const uint32_t *masks, int64_t mask_words,
+                                   uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t s);
 // ... of the wide sequences, by tcgen05 (head_dim 64 and 128).
 bool paged_wide_applies(const CacheView &c);
 size_t paged_wide_workspace_bytes(const CacheView &c, const PagedBounds &b, int QH);
@@ -243,6 +246,66 @@ int32_t *paged_wide_spill(const CacheView &c, const PagedBounds &b, int QH, void
 cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const PagedBounds &b, const uint16_t *q, int QH,
                               float scale, uint16_t *out, void *ws, cudaStream_t s,
                               const std::function<cudaError_t()> &split);
+
+// Page tables from lengths (tq_page_table.cu).
+struct PagedUpdate {
+    int32_t *pages;           // [seqs][stride], entries written as sequences grow
+    const int32_t *lens;      // [seqs] before the call
+    const int32_t *want;      // [seqs] after it
+    const int32_t *fresh;     // [seqs] new tokens (null: none)
+    int32_t *lens_out;        // [seqs]
+    int32_t *starts;          // [seqs + 1] or null
+    int32_t *free_pages;      // the stack of free pages
+    const int32_t *free_count;
+    int32_t *count_out;
+    int64_t stride, max_len, free_cap;
+    int seqs, num_pages;
+    FastDiv div_page;
+    uint32_t *err;
+};
+cudaError_t launch_page_table_update(const PagedUpdate &u, cudaStream_t s);
+// Positions, slots and masks of ancestors of the ragged tokens (each may be null; parents null: no trees).
+cudaError_t launch_paged_layout(const PagedView &v, const int32_t *parents, int64_t max_new, int32_t *positions, int64_t *slots,
+                                uint32_t *masks, int64_t mask_words, cudaStream_t s);
+// Kept rows of the new ones moved together (tq_paged_keep.cu).
+cudaError_t launch_paged_keep(const CacheView &c, const PagedView &v, int64_t max_new, const int32_t *path, int64_t path_stride,
+                              const int32_t *kept, int32_t *lens_out, cudaStream_t s);
+
+// Rotary positions (tq_rotary.cu).
+struct RotaryTensor {
+    const void *x;
+    void *out;
+    int64_t x_token, x_head, out_token, out_head;  // strides in elements
+    int heads;                                     // 0: absent
+};
+struct RotaryCall {
+    RotaryTensor t[2];
+    const int32_t *pos;
+    const double *freqs;
+    int64_t tokens;
+    float scale;
+    int d, rot;
+    bool interleaved, f32;
+};
+cudaError_t launch_rotary(const RotaryCall &r, cudaStream_t s);
+// Host (tq_tables.cpp): rot / 2 angles per position, and the size of the turned vectors.
+void rotary_frequencies(int rot, double base, int scaling, double factor, int64_t original_len, double fast, double slow,
+                        double *freqs, float *scale);
+
+// Verification of drafted tokens (tq_verify.cu).
+struct VerifyCall {
+    const int32_t *starts, *parents, *tokens;
+    int64_t total, max_new, vocab;
+    int seqs;
+    const void *target, *draft;                // draft may be null
+    int64_t target_stride, draft_stride;
+    const float *uniforms, *last;
+    int32_t *path, *kept, *next;
+    int64_t path_stride;
+    bool f32;
+    uint32_t *err;
+};
+cudaError_t launch_verify(const VerifyCall &v, cudaStream_t s);
 
 // Allocation-free decode attention: partials in a library-owned device array.
 size_t noalloc_scratch_bytes();

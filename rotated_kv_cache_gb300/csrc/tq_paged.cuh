@@ -17,6 +17,8 @@ namespace tq {
 
 constexpr uint32_t kErrPage = 2u;    // a page number outside the pool
 constexpr uint32_t kErrLength = 4u;  // a length above max_len, or starts out of order
+constexpr uint32_t kErrFull = 8u;    // fewer free pages than sequences lack, or no room for those that they give back
+constexpr uint32_t kErrTree = 16u;   // a parent at or behind its node, a path that does not grow, a token outside the vocabulary
 
 // Rows of sequence s, in [0, max_len].
 __device__ __forceinline__ int64_t paged_len(const PagedView &v, int s)
@@ -138,6 +140,24 @@ __device__ __forceinline__ PagedPlace paged_seek(const PagedView &v, const Paged
 __device__ __forceinline__ int64_t paged_row(const PagedView &v, const PagedLanes &l, int64_t t, int H)
 {
     return paged_place_row(v, paged_seek(v, l, t), H);
+}
+
+// Which of the new rows j0 .. j0 + 31 of a sequence of n new tokens a token with this
+// mask sees (bit r: row j0 + r): those before the new ones (j < 0) all, those
+// from n on none, whatever the mask holds there.
+__device__ __forceinline__ uint32_t paged_tree_bits(const uint32_t *mask, int j0, int n)
+{
+    if (j0 <= -32) return 0xFFFFFFFFu;
+    uint32_t x;
+    if (j0 < 0) {
+        x = mask[0] << -j0 | ((1u << -j0) - 1u);
+    } else {
+        const int w = j0 >> 5, words = (n + 31) >> 5;
+        const uint32_t lo = w < words ? mask[w] : 0u, hi = w + 1 < words ? mask[w + 1] : 0u;
+        x = __funnelshift_r(lo, hi, j0 & 31);
+    }
+    const int live = n - j0;
+    return live >= 32 ? x : live <= 0 ? 0u : x & ((1u << live) - 1u);
 }
 
 // ------------------------------------------------------------------ split attention over a paged batch

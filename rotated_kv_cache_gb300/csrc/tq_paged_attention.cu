@@ -1,9 +1,11 @@
-// tq_paged_attention.cu -- causal attention of ragged new tokens over a paged
+// tq_paged_attention.cu -- attention of ragged new tokens over a paged
 // cache: the choice of kernels, the workspace, and the merge of the partials.
 //
-//   o_i = sum_{t <= pos_i} softmax_t(q_i . k_t scale) v_t
+//   o_i = sum_{t seen by i} softmax_t(q_i . k_t scale) v_t
 //
-// for every new token i at position pos_i of its sequence; the values stay in
+// for every new token i at position pos_i of its sequence, which sees the rows up
+// to its own (causal), or the rows before the new ones and those that its mask
+// names (trees of drafted tokens); the values stay in
 // the rotated domain and the sum is un-rotated once per (token, q-head), as in
 // the contiguous calls.  A token that sees no row gives zeros.
 #include "tq_common.cuh"
@@ -12,14 +14,18 @@
 
 namespace tq {
 
-#define TQ_DECLARE_PAGED_GENERIC(D)                                                                                    \
-    bool paged_generic_shape_d##D(const CacheView &c, int64_t cols, PagedShape &sh);                                   \
-    cudaError_t launch_paged_generic_d##D(const CacheView &c, const PagedSplit &pg, int64_t cols, const uint16_t *q,  \
-                                          int QH, float scale, float *part_o, float *part_ml, cudaStream_t s);
-TQ_DECLARE_PAGED_GENERIC(64)
-TQ_DECLARE_PAGED_GENERIC(128)
-TQ_DECLARE_PAGED_GENERIC(256)
-TQ_DECLARE_PAGED_GENERIC(512)
+#define TQ_DECLARE_PAGED_GENERIC(NAME)                                                                                 \
+    bool paged_generic_shape_##NAME(const CacheView &c, int64_t cols, PagedShape &sh);                                 \
+    cudaError_t launch_paged_generic_##NAME(const CacheView &c, const PagedSplit &pg, int64_t cols, const uint16_t *q, \
+                                            int QH, float scale, float *part_o, float *part_ml, cudaStream_t s);
+TQ_DECLARE_PAGED_GENERIC(d64)
+TQ_DECLARE_PAGED_GENERIC(d128)
+TQ_DECLARE_PAGED_GENERIC(d256)
+TQ_DECLARE_PAGED_GENERIC(d512)
+TQ_DECLARE_PAGED_GENERIC(d64_tree)
+TQ_DECLARE_PAGED_GENERIC(d128_tree)
+TQ_DECLARE_PAGED_GENERIC(d256_tree)
+TQ_DECLARE_PAGED_GENERIC(d512_tree)
 #undef TQ_DECLARE_PAGED_GENERIC
 #define TQ_DECLARE_PAGED_SPLIT(NAME)                                                                                   \
     PagedShape paged_split_shape_##NAME(const CacheView &c, int64_t cols);                                             \
@@ -32,6 +38,9 @@ TQ_DECLARE_PAGED_SPLIT(d128_one)
 TQ_DECLARE_PAGED_SPLIT(d128_any)
 TQ_DECLARE_PAGED_SPLIT(d256_one)
 TQ_DECLARE_PAGED_SPLIT(d256_any)
+TQ_DECLARE_PAGED_SPLIT(d64_tree)
+TQ_DECLARE_PAGED_SPLIT(d128_tree)
+TQ_DECLARE_PAGED_SPLIT(d256_tree)
 #undef TQ_DECLARE_PAGED_SPLIT
 
 namespace {
@@ -210,13 +219,13 @@ cudaError_t run_combine(const PagedCombineParams &p, cudaStream_t s)
 }
 
 // ---------------------------------------------------------------- plan and workspace
-bool generic_shape(const CacheView &c, int64_t cols, PagedShape &sh)
+bool generic_shape(const CacheView &c, int64_t cols, bool tree, PagedShape &sh)
 {
     switch (c.d) {
-    case 64: return paged_generic_shape_d64(c, cols, sh);
-    case 128: return paged_generic_shape_d128(c, cols, sh);
-    case 256: return paged_generic_shape_d256(c, cols, sh);
-    case 512: return paged_generic_shape_d512(c, cols, sh);
+    case 64: return tree ? paged_generic_shape_d64_tree(c, cols, sh) : paged_generic_shape_d64(c, cols, sh);
+    case 128: return tree ? paged_generic_shape_d128_tree(c, cols, sh) : paged_generic_shape_d128(c, cols, sh);
+    case 256: return tree ? paged_generic_shape_d256_tree(c, cols, sh) : paged_generic_shape_d256(c, cols, sh);
+    case 512: return tree ? paged_generic_shape_d512_tree(c, cols, sh) : paged_generic_shape_d512(c, cols, sh);
     }
     return false;
 }
@@ -265,14 +274,18 @@ bool paged_plan(const CacheView &c, const PagedBounds &bounds, int QH, PagedPlan
     // the specialised kernel where it has the widths (its tensor copies count rows in 32 bits)
     pl.special = attention_supported(c.d, c.kb, c.vb, (int)G) && (int64_t)c.B * c.H * c.cap < (int64_t(1) << 31);
     if (pl.special)
-        pl.split = pl.b.max_new <= 1
+        pl.split = pl.b.tree
+                       ? (c.d == 64    ? paged_split_shape_d64_tree(c, pl.cols)
+                          : c.d == 128 ? paged_split_shape_d128_tree(c, pl.cols)
+                                       : paged_split_shape_d256_tree(c, pl.cols))
+                   : pl.b.max_new <= 1
                        ? (c.d == 64    ? paged_split_shape_d64_one(c, pl.cols)
                           : c.d == 128 ? paged_split_shape_d128_one(c, pl.cols)
                                        : paged_split_shape_d256_one(c, pl.cols))
                        : (c.d == 64    ? paged_split_shape_d64_any(c, pl.cols)
                           : c.d == 128 ? paged_split_shape_d128_any(c, pl.cols)
                                        : paged_split_shape_d256_any(c, pl.cols));
-    else if (!generic_shape(c, pl.cols, pl.split))
+    else if (!generic_shape(c, pl.cols, pl.b.tree, pl.split))
         return false;
     // a sequence of n new tokens has ceil(n G / block) blocks: at most this many units in all
     const int64_t units = c.H * (pl.b.total * G / pl.split.block + pl.b.seqs);
@@ -295,8 +308,8 @@ size_t paged_attention_workspace_bytes(const CacheView &c, const PagedBounds &b,
 }
 
 cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const PagedBounds &b, const uint16_t *q,
-                                   const int64_t qs[2], int QH, float scale, uint16_t *out, void *ws, size_t ws_bytes,
-                                   cudaStream_t s)
+                                   const int64_t qs[2], int QH, float scale, const uint32_t *masks, int64_t mask_words,
+                                   uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t s)
 {
     PagedPlan pl;
     if (!paged_plan(c, b, QH, pl)) return cudaErrorInvalidConfiguration;
@@ -304,23 +317,24 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
     uint8_t *base = static_cast<uint8_t *>(ws);
     const bool wide = pl.b.wide != INT32_MAX;
     PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<PagedUnit *>(base), pl.slots, pl.blocks, pl.b.max_new, pl.b.wide,
-                  wide ? paged_wide_spill(c, pl.b, QH, base + pl.off_wide) : nullptr, 1, 1};
+                  wide ? paged_wide_spill(c, pl.b, QH, base + pl.off_wide) : nullptr, 1, 1, masks, mask_words};
     float *part_ml = reinterpret_cast<float *>(base + pl.off_ml), *part_o = reinterpret_cast<float *>(base + pl.off_o);
     auto split = [&]() -> cudaError_t {
         const int64_t cols = pl.cols;
         if (pl.special) {
-            const auto launch = pl.b.max_new <= 1
+            const auto launch = pl.b.tree
+                                    ? (c.d == 64 ? launch_paged_split_d64_tree : c.d == 128 ? launch_paged_split_d128_tree : launch_paged_split_d256_tree)
+                                : pl.b.max_new <= 1
                                     ? (c.d == 64 ? launch_paged_split_d64_one : c.d == 128 ? launch_paged_split_d128_one : launch_paged_split_d256_one)
                                     : (c.d == 64 ? launch_paged_split_d64_any : c.d == 128 ? launch_paged_split_d128_any : launch_paged_split_d256_any);
             return launch(c, pg, pl.split, q, QH, scale, part_o, part_ml, s);
         }
-        switch (c.d) {
-        case 64: return launch_paged_generic_d64(c, pg, cols, q, QH, scale, part_o, part_ml, s);
-        case 128: return launch_paged_generic_d128(c, pg, cols, q, QH, scale, part_o, part_ml, s);
-        case 256: return launch_paged_generic_d256(c, pg, cols, q, QH, scale, part_o, part_ml, s);
-        case 512: return launch_paged_generic_d512(c, pg, cols, q, QH, scale, part_o, part_ml, s);
-        }
-        return cudaErrorInvalidValue;
+        const bool tree = pl.b.tree;
+        const auto launch = c.d == 64    ? (tree ? launch_paged_generic_d64_tree : launch_paged_generic_d64)
+                            : c.d == 128 ? (tree ? launch_paged_generic_d128_tree : launch_paged_generic_d128)
+                            : c.d == 256 ? (tree ? launch_paged_generic_d256_tree : launch_paged_generic_d256)
+                                         : (tree ? launch_paged_generic_d512_tree : launch_paged_generic_d512);
+        return launch(c, pg, cols, q, QH, scale, part_o, part_ml, s);
     };
     const cudaError_t e = wide ? launch_paged_wide(c, pg, pl.b, q, QH, scale, out, base + pl.off_wide, s,
                                                    std::ref(split))  // (a reference: nothing allocated)

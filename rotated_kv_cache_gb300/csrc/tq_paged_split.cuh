@@ -64,7 +64,7 @@ cudaError_t paged_split_run(const CacheView &c, const PagedSplit &pg, const Page
 }  // namespace
 }  // namespace tq
 
-// The entry points of one head_dim's translation unit for MODE 1 or 2 (NAME d<head_dim>_one / _any).
+// The entry points of one head_dim's translation unit for MODE 1, 2 or 3 (NAME d<head_dim>_one / _any / _tree).
 #define TQ_PAGED_SPLIT_ENTRIES(D, MODE, NAME)                                                                          \
     namespace tq {                                                                                                     \
     PagedShape paged_split_shape_##NAME(const CacheView &c, int64_t cols)                                              \

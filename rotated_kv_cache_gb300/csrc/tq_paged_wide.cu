@@ -153,9 +153,10 @@ __device__ __forceinline__ int64_t block_exclusive_sum(int64_t x, int64_t &total
 }
 
 // Tiles that block b of a sequence reads: up to its last column's limit (one
-// at least, so that a column that sees nothing is written too).
-__device__ __forceinline__ int64_t block_tiles(int64_t len, int64_t n, int G, int64_t b)
+// at least, so that a column that sees nothing is written too), with masks all.
+__device__ __forceinline__ int64_t block_tiles(int64_t len, int64_t n, int G, int64_t b, bool tree)
 {
+    if (tree) return len > 0 ? (len + wT - 1) / wT : 1;
     const int64_t cols = n * G, last = (cols < (b + 1) * wC ? cols : (b + 1) * wC) - 1;
     const int64_t lim = len - n + 1 + last / G, t = (lim + wT - 1) / wT;
     return t < 1 ? 1 : t;
@@ -215,7 +216,8 @@ __global__ void __launch_bounds__(wPlanThreads) wide_plan_kernel(const __grid_co
                 if (p.pl.entry0[mid] <= e) lo = mid;
                 else hi = mid - 1;
             }
-            t = wStart + block_tiles(paged_len(p.pg.v, lo), paged_new(p.pg.v, lo), p.G, e - p.pl.entry0[lo]);
+            t = wStart + block_tiles(paged_len(p.pg.v, lo), paged_new(p.pg.v, lo), p.G, e - p.pl.entry0[lo],
+                                     p.pg.masks != nullptr);
         }
         const int64_t at = line + block_exclusive_sum(t, all, sh);
         line += all;
@@ -520,7 +522,24 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b)
 // The thread goes on with those as with any tile's; the weights' sum, whose terms
 // need each row's value exponent, is taken here at the reference R that it will
 // choose.  Out of line: rare, and its registers are not the common path's.
-__device__ __noinline__ float mixed_tile(uint32_t t_s, const RowMeta *rm, float ie, int vis, float R)
+// `rows` says which rows the column sees: the first `vis`, or those of a mask.
+struct CausalRows {
+    int vis;
+    __device__ __forceinline__ uint32_t from(int c) const  // of rows c .. c + 31, as bits
+    {
+        const int n = vis - c;
+        return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+    }
+};
+
+struct TreeRows {
+    const uint32_t *mask;
+    int j0, n;  // the tile's first row among the new ones, new tokens
+    __device__ __forceinline__ uint32_t from(int c) const { return paged_tree_bits(mask, j0 + c, n); }
+};
+
+template <typename Rows>
+__device__ __noinline__ float mixed_tile(uint32_t t_s, const RowMeta *rm, float ie, Rows rows, float R)
 {
     float mx = -INFINITY, sum = 0.0f;
 #pragma unroll 1
@@ -529,11 +548,12 @@ __device__ __noinline__ float mixed_tile(uint32_t t_s, const RowMeta *rm, float 
         tc_ld16(t_s + c, x);
         tc_wait_ld();
         tc_pin(x);
+        const uint32_t seen = rows.from(c);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             const RowMeta r = rm[c + j];
             const float y = fmaf(__uint_as_float(x[j]), fmaxf(ie * r.kf, 1.17549435e-38f), r.e);
-            x[j] = c + j < vis ? __float_as_uint(y) : 0xFF800000u;
+            x[j] = seen >> j & 1u ? __float_as_uint(y) : 0xFF800000u;
             mx = fmaxf(mx, __uint_as_float(x[j]));
         }
         tc_st16(t_s + c, x);
@@ -588,7 +608,10 @@ __device__ __noinline__ void far_tile(uint32_t t_s, float f, float e)
 // cycles per MMA, more than the 64 that one of 128 x 128 x 16 takes to run).
 // What runs once per block (q in, masks of the last tiles, un-rotation) is in
 // short loops: unrolled over a row it was 10 us of instruction fetch a block.
-template <int D>
+//
+// TREE: new rows are seen by the columns' masks; only tiles that hold some are
+// treated apart from the others, as the last tiles are in a causal chunk.
+template <int D, bool TREE>
 __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_constant__ WideParams p)
 {
     using A = WideGeo<D>;
@@ -806,7 +829,9 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
             const int cols = (int)w.n * p.G, col = (w.e - w.e0) * wC + 128 * g + ltid;  // total * QH < 2^30
             const bool real = col < cols;
             const int tok = real ? col / p.G : (int)w.n - 1, hq = real ? col - tok * p.G : 0;
-            int left = (int)(w.len - w.n) + 1 + tok - w.tile * wT;  // rows that this column sees, from the tile's first on
+            // rows that this column sees, from the tile's first on; with masks those before the new ones
+            int left = (int)(w.len - w.n) + (TREE ? 0 : 1 + tok) - w.tile * wT;
+            const uint32_t *mask = TREE ? p.pg.masks + (w.s0 + tok) * p.pg.mask_words : nullptr;
             // q, scaled by a power of two that puts its largest |q| in [2^14, 2^15): exact in f16.
             // D / 8 lanes read a row of the warp's 32 together, every row under way before the first is used
             float ie = 0.0f;
@@ -864,6 +889,10 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 float f = fmaxf(ie * mt->kf, 1.17549435e-38f);
                 const uint32_t any = mt->any;
                 const int vis = left < 0 ? 0 : (left > wT ? wT : left);
+                auto rows = [&] {
+                    if constexpr (TREE) return TreeRows{mask, -left, (int)w.n};
+                    else return CausalRows{vis};
+                };
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar_s, it & 1, p.err));
                 if (!ok) break;
                 tc_fence_after();
@@ -875,7 +904,7 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 }
                 if (any & 2u) {
                     // rows of exponents of their own: true scores now, and the sum of the weights
-                    extra = mixed_tile(t_s, p.row_meta + (mt - p.meta) * wT, ie, vis, R);
+                    extra = mixed_tile(t_s, p.row_meta + (mt - p.meta) * wT, ie, rows(), R);
                     f = 1.0f;
                     e = lf = 0.0f;
                 } else if (__any_sync(0xffffffffu, vis < wT)) {  // some column does not see the whole tile: its hidden scores become -inf
@@ -885,9 +914,16 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                         tc_ld16(t_s + c, x);
                         tc_wait_ld();
                         tc_pin(x);
+                        if constexpr (TREE) {
+                            const uint32_t seen = rows().from(c);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (c + j >= vis) x[j] = 0xFF800000u;
+                            for (int j = 0; j < 16; ++j)
+                                if (!(seen >> j & 1u)) x[j] = 0xFF800000u;
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (c + j >= vis) x[j] = 0xFF800000u;
+                        }
                         tc_st16(t_s + c, x);
                     }
                     tc_wait_st();
@@ -976,9 +1012,7 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 if (any & 1u) {
 #pragma unroll 1
                     for (int i = 0; i < 4; ++i) {
-                        const int rows = vis - 32 * i;
-                        const uint32_t seen = rows >= 32 ? 0xFFFFFFFFu : (rows <= 0 ? 0u : (1u << rows) - 1u);
-                        if (mt->bad[i] & seen) l = NAN;
+                        if (mt->bad[i] & rows().from(32 * i)) l = NAN;
                     }
                 }
             }
@@ -1195,11 +1229,11 @@ WideSizes wide_sizes(const CacheView &c, const PagedBounds &b, int QH)
 // beside expand and combine beside merge, waiting at their ends, gained 2 to 10
 // us a call; but then they read pool, lengths and partials without a wait of
 // their own, which the programming model does not cover.)
-template <int D>
+template <int D, bool TREE>
 cudaError_t wide_run(WideParams &p, cudaStream_t s, const std::function<cudaError_t()> &split)
 {
     using A = WideGeo<D>;
-    cudaError_t e = cudaFuncSetAttribute(wide_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(wide_attend_kernel<D, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
     if (e != cudaSuccess) return e;
     e = launch_dependent(wide_plan_kernel, dim3(1), dim3(wPlanThreads), 0, s, p);
     if (e != cudaSuccess) return e;
@@ -1207,7 +1241,7 @@ cudaError_t wide_run(WideParams &p, cudaStream_t s, const std::function<cudaErro
     e = launch_dependent(wide_expand_kernel<D>, dim3((unsigned)imin64(items, (int64_t)num_sms() * 8)), dim3(256), 0, s, p);
     if (e != cudaSuccess) return e;
     if ((e = split()) != cudaSuccess) return e;
-    e = launch_dependent(wide_attend_kernel<D>, dim3((unsigned)p.ctas), dim3(wThreads), A::SMEM, s, p);
+    e = launch_dependent(wide_attend_kernel<D, TREE>, dim3((unsigned)p.ctas), dim3(wThreads), A::SMEM, s, p);
     if (e != cudaSuccess) return e;
     return launch_dependent(wide_merge_kernel<D>, dim3((unsigned)p.ctas, wC / 8), dim3(256), 0, s, p);
 }
@@ -1268,7 +1302,8 @@ cudaError_t launch_paged_wide(const CacheView &c, const PagedSplit &pg, const Pa
         p.cen[i] = tab.centroids[i];
         p.cmax = p.cmax > fabsf(tab.centroids[i]) ? p.cmax : fabsf(tab.centroids[i]);
     }
-    return c.d == 64 ? wide_run<64>(p, s, split) : wide_run<128>(p, s, split);
+    if (b.tree) return c.d == 64 ? wide_run<64, true>(p, s, split) : wide_run<128, true>(p, s, split);
+    return c.d == 64 ? wide_run<64, false>(p, s, split) : wide_run<128, false>(p, s, split);
 }
 
 }  // namespace tq

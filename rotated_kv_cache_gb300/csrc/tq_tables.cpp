@@ -12,6 +12,10 @@
 // density, so any convergent solver lands on the same table.  Centroids are
 // stored rounded to fp32; boundaries are the binary64 midpoints of the binary64
 // centroids, rounded to fp32.
+//
+// Rotary frequencies: pair i of `rot` / 2 turns by base^(-2 i / rot) a position;
+// for longer contexts than a model was made for they are stretched (see tq.h).
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 #include <vector>
@@ -123,6 +127,32 @@ const Tables &codebook_tables(int vb)
         for (int i = 0; i + 1 < n; ++i) t.boundaries[i] = (float)(0.5 * (c[i] + c[i + 1]));
     });
     return g_tables[vb];
+}
+
+void rotary_frequencies(int rot, double base, int scaling, double factor, int64_t original_len, double fast, double slow,
+                        double *freqs, float *scale)
+{
+    constexpr double kTurn = 6.283185307179586;
+    *scale = 1.0f;
+    // the slowest pair, of exponent (rot - 2) / rot, stretched by the factor, the fastest left
+    if (scaling == 2) base *= std::pow(factor, (double)rot / std::max(rot - 2, 1));
+    // the pair that turns so many times in the original context
+    auto pair = [&](double turns) { return rot * std::log((double)original_len / (turns * kTurn)) / (2.0 * std::log(base)); };
+    double lo = 0.0, hi = 0.0;
+    if (scaling == 3) {
+        lo = std::max(std::floor(pair(fast)), 0.0);
+        hi = std::min(std::ceil(pair(slow)), (double)(rot - 1));
+        *scale = (float)(0.1 * std::log(factor) + 1.0);
+    }
+    for (int i = 0; i < rot / 2; ++i) {
+        const double w = std::pow(base, -2.0 * i / rot);
+        freqs[i] = w;
+        if (scaling == 1) freqs[i] = w / factor;
+        if (scaling == 3) {
+            const double ramp = std::min(std::max((i - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
+            freqs[i] = w / factor * ramp + w * (1.0 - ramp);
+        }
+    }
 }
 
 float inv_sqrt_head_dim(int d) { return (float)(1.0 / std::sqrt((double)d)); }
