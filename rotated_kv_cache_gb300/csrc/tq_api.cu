@@ -621,10 +621,12 @@ tq_status tq_rotary(const int32_t *positions, int64_t tokens, int32_t head_dim, 
                     const double *freqs, float scale, tq_dtype dt, const tq_rotary_tensor *q, const tq_rotary_tensor *k,
                     tq_stream_t stream)
 {
-    if (!positions || !freqs || (!q && !k)) return TQ_ERR_NULL;
+    if (!q && !k) return TQ_ERR_NULL;
     if (head_dim != 64 && head_dim != 128 && head_dim != 256 && head_dim != 512) return TQ_ERR_HEAD_DIM;
     if (rot_dim < 2 || rot_dim > head_dim || rot_dim % 2 != 0 || tokens < 0 || tokens > INT32_MAX) return TQ_ERR_SHAPE;
     if (dt != TQ_BF16 && dt != TQ_F32) return TQ_ERR_SHAPE;
+    if (tokens == 0) return TQ_OK;  // (tensors without tokens may have no address)
+    if (!positions || !freqs) return TQ_ERR_NULL;
     tq::RotaryCall r{};
     const int64_t unit = dt == TQ_F32 ? 4 : 8;  // elements of 16 bytes
     const tq_rotary_tensor *in[2] = {q, k};
@@ -644,7 +646,6 @@ tq_status tq_rotary(const int32_t *positions, int64_t tokens, int32_t head_dim, 
         if (a.x == a.out && (st[0] != st[2] || st[1] != st[3])) return TQ_ERR_SHAPE;
         r.t[i] = tq::RotaryTensor{a.x, a.out, st[0], st[1], st[2], st[3], a.heads};
     }
-    if (tokens == 0) return TQ_OK;
     r.pos = positions;
     r.freqs = freqs;
     r.tokens = tokens;
