@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from functools import lru_cache
 
 import torch
@@ -141,8 +142,7 @@ def lib() -> ctypes.CDLL:
     so.tq_paged_keep.argtypes = [_CP, _TP, _P, _I64, _I64, _P, _I64, _P, _P, _P]
     so.tq_verify_drafts.argtypes = [_P, _I32, _I64, _I64, _P, _P, _I64, ctypes.c_int, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P,
                                     _P, _P]
-    turned = ctypes.POINTER(_RotaryStruct)
-    so.tq_rotary.argtypes = [_P, _I64, _I32, _I32, _I32, _P, ctypes.c_float, ctypes.c_int, turned, turned, _P]
+    so.tq_rotary.argtypes = [_P, _I64, _I32, _I32, _I32, _P, ctypes.c_float, ctypes.c_int, _P, _P, _P]
     f64 = ctypes.c_double
     so.tq_rotary_frequencies.argtypes = [_I32, f64, ctypes.c_int, f64, _I64, f64, f64, _P, ctypes.POINTER(ctypes.c_float)]
     for name in EXPORTS:
@@ -654,26 +654,20 @@ def _i32(x: torch.Tensor | None, shape: tuple, what: str) -> int | None:
     """The address of an int32 tensor of this shape."""
     if x is None:
         return None
-    if x.dtype is not torch.int32 or tuple(x.shape) != shape or not x.is_contiguous():
+    if x.dtype is not torch.int32 or x.shape != shape or not x.is_contiguous():
         raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
     return x.data_ptr()
 
 
-def _one_device(*tensors) -> torch.device:
-    """The CUDA device that all of them are on, the current one."""
-    dev = -1
-    for t in tensors:
-        if t is None:
-            continue
-        at = t.get_device()
-        if at < 0:
-            raise ValueError("tensors must live on a CUDA device")
-        if dev >= 0 and at != dev:
-            raise ValueError("the tensors must be on one device")
-        dev = at
+def _one_device(*tensors) -> int:
+    """The index of the CUDA device that all of them are on, the current one."""
+    at = {t.get_device() for t in tensors if t is not None}
+    dev = at.pop()
+    if at or dev < 0:
+        raise ValueError("the tensors must be on one CUDA device")
     if dev != torch._C._cuda_getDevice():
         raise ValueError("the tensors are on another device than the current one")
-    return torch.device("cuda", dev)
+    return dev
 
 
 def tq_page_table_update(pool: Cache, table: PageTable, lens: torch.Tensor, free_pages: torch.Tensor,
@@ -683,24 +677,25 @@ def tq_page_table_update(pool: Cache, table: PageTable, lens: torch.Tensor, free
     """Give the sequences pages for the wanted lengths (int32 [num_seqs]): those that shrink push theirs onto the stack
     free_pages[:free_count], those that grow pop theirs; the table's pages are written, its lengths too unless lens_out
     is given, free_count unless free_count_out is.  With new_tokens (int32 [num_seqs]) their running sums come back as starts."""
+    t = table.struct(pool)
     n = table.num_seqs
-    lens_out = table.seq_lens if lens_out is None else lens_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    if free_pages.dim() != 1:
-        raise ValueError("free_pages must be contiguous int32 [capacity]")
+    if lens_out is None:
+        lens_out = table.seq_lens
+    if free_count_out is None:
+        free_count_out = free_count
     if starts is not None and new_tokens is None:
         raise ValueError("starts are the running sums of new_tokens: give both")
-    at = (_i32(lens, (n,), "lens"), _i32(new_tokens, (n,), "new_tokens"), _i32(lens_out, (n,), "lens_out"))
-    stack, counts = _i32(free_pages, tuple(free_pages.shape), "free_pages"), (_i32(free_count, (1,), "free_count"),
-                                                                             _i32(free_count_out, (1,), "free_count_out"))
-    dev = _one_device(pool.k_codes, table.pages, table.seq_lens, lens, new_tokens, lens_out, starts, free_pages, free_count,
-                      free_count_out)
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be contiguous int32 [capacity]")
+    dev = _one_device(pool.k_codes, table.pages, lens, new_tokens, lens_out, starts, free_pages, free_count, free_count_out)
     if starts is None and new_tokens is not None:
-        starts = _empty_on(stream, n + 1, torch.int32, dev)
-    first = _i32(starts, (n + 1,), "starts")
-    s, t = pool.struct(), table.struct(pool)
-    _check(lib().tq_page_table_update(ctypes.byref(s), ctypes.byref(t), at[0], at[1], at[2], first, stack, free_pages.shape[0],
-                                      counts[0], counts[1], _stream(stream)), "tq_page_table_update")
+        starts = _empty_on(stream, n + 1, torch.int32, torch.device("cuda", dev))
+    at = (n,)
+    _check(lib().tq_page_table_update(ctypes.byref(pool.struct()), ctypes.byref(t), _i32(lens, at, "lens"),
+                                      _i32(new_tokens, at, "new_tokens"), _i32(lens_out, at, "lens_out"),
+                                      _i32(starts, (n + 1,), "starts"), _i32(free_pages, free_pages.shape, "free_pages"),
+                                      free_pages.shape[0], _i32(free_count, (1,), "free_count"),
+                                      _i32(free_count_out, (1,), "free_count_out"), _stream(stream)), "tq_page_table_update")
     return starts
 
 
@@ -711,15 +706,17 @@ def tq_paged_layout(pool: Cache, table: PageTable, starts: torch.Tensor, total: 
     """(positions int32 [total], slots int64 [total], masks int32 [total][ceil(max_new / 32)]) of the new tokens; with
     parents (int32 [total], -1 at a root) positions go by the depth in a sequence's tree, without them masks is None."""
     total = int(total)
-    if parents is not None and max_new is None:
+    most = words = 0
+    if parents is None:
+        if masks is not None:
+            raise ValueError("masks are made from parents")
+    elif max_new is None:
         raise ValueError("give max_new, the most tokens of a sequence, with parents")
-    if parents is None and masks is not None:
-        raise ValueError("masks are made from parents")
-    up = _i32(parents, (total,), "parents")
+    else:
+        most = int(max_new)
+        words = masks.shape[1] if masks is not None and masks.dim() == 2 else max(1, (most + 31) // 32)
     s, t = _paged_check(pool, table, starts, parents, positions, slots, masks)
-    dev = pool.k_codes.device
-    most = 0 if parents is None else int(max_new)
-    words = masks.shape[1] if masks is not None and masks.dim() == 2 else max(1, (most + 31) // 32)
+    dev = starts.device
     if not want_positions:
         positions = None
     elif positions is None:
@@ -728,14 +725,15 @@ def tq_paged_layout(pool: Cache, table: PageTable, starts: torch.Tensor, total: 
         slots = None
     elif slots is None:
         slots = _empty_on(stream, total, torch.int64, dev)
-    if slots is not None and (slots.dtype is not torch.int64 or tuple(slots.shape) != (total,) or not slots.is_contiguous()):
+    elif slots.dtype is not torch.int64 or slots.shape != (total,) or not slots.is_contiguous():
         raise ValueError("slots must be contiguous int64 [total]")
     if not want_masks or parents is None:
         masks = None
     elif masks is None:
         masks = _empty_on(stream, (total, words), torch.int32, dev)
-    at = _i32(positions, (total,), "positions"), None if slots is None else slots.data_ptr(), _i32(masks, (total, words), "masks")
-    _check(lib().tq_paged_layout(s, t, starts.data_ptr(), total, up, most, *at, words, _stream(stream)), "tq_paged_layout")
+    _check(lib().tq_paged_layout(s, t, starts.data_ptr(), total, _i32(parents, (total,), "parents"), most,
+                                 _i32(positions, (total,), "positions"), None if slots is None else slots.data_ptr(),
+                                 _i32(masks, (total, words), "masks"), words, _stream(stream)), "tq_paged_layout")
     return positions, slots, masks
 
 
@@ -747,13 +745,13 @@ def tq_paged_keep(pool: Cache, table: PageTable, starts: torch.Tensor, path: tor
     n = table.num_seqs
     if path.dim() != 2 or path.shape[0] != n or path.shape[1] < 1:
         raise ValueError("path must be contiguous int32 [num_seqs][most new tokens]")
-    at = _i32(path, tuple(path.shape), "path"), _i32(kept, (n,), "kept")
     s, t = _paged_check(pool, table, starts, path, kept, lens_out)
     if lens_out is None:
-        lens_out = _empty_on(stream, n, torch.int32, pool.k_codes.device)
+        lens_out = _empty_on(stream, n, torch.int32, starts.device)
     total = min(n * table.max_len, 2 ** 31 - 1) if total is None else int(total)
-    _check(lib().tq_paged_keep(s, t, starts.data_ptr(), total, path.shape[1], at[0], path.shape[1], at[1],
-                               _i32(lens_out, (n,), "lens_out"), _stream(stream)), "tq_paged_keep")
+    wide = path.shape[1]
+    _check(lib().tq_paged_keep(s, t, starts.data_ptr(), total, wide, _i32(path, path.shape, "path"), wide,
+                               _i32(kept, (n,), "kept"), _i32(lens_out, (n,), "lens_out"), _stream(stream)), "tq_paged_keep")
     return lens_out
 
 
@@ -767,40 +765,66 @@ def tq_verify_drafts(starts: torch.Tensor, parents: torch.Tensor, tokens: torch.
     if starts.dim() != 1 or starts.shape[0] < 2:
         raise ValueError("starts must be contiguous int32 [num_seqs + 1]")
     n, max_new = starts.shape[0] - 1, int(max_new)
-    if target.dim() != 2 or (target.shape[1] > 1 and target.stride(1) != 1):
+    if target.dim() != 2:
         raise ValueError("target must be [total][vocab], rows contiguous")
     total, vocab = target.shape
+    # (a tensor of one row has no row to step to)
+    step, unit = target.stride()
+    if vocab > 1 and unit != 1:
+        raise ValueError("target must be [total][vocab], rows contiguous")
+    if total < 2:
+        step = vocab
     code = _dtype_code(target.dtype)
-    if draft is not None and (draft.shape != target.shape or draft.dtype != target.dtype or
-                              (vocab > 1 and draft.stride(1) != 1)):
-        raise ValueError("draft must be like target")
+    other, other_step = None, 0
+    if draft is not None:
+        other_step, unit = draft.stride() if draft.dim() == 2 else (0, 0)
+        if draft.shape != target.shape or draft.dtype is not target.dtype or (vocab > 1 and unit != 1):
+            raise ValueError("draft must be like target")
+        if total < 2:
+            other_step = vocab
+        other = draft.data_ptr()
     for x, size, what in ((uniforms, total, "uniforms"), (last, n, "last")):
-        if x.dtype is not torch.float32 or tuple(x.shape) != (size,) or not x.is_contiguous():
+        if x.dtype is not torch.float32 or x.shape != (size,) or not x.is_contiguous():
             raise ValueError(f"{what} must be contiguous float32 [{size}]")
     at = _i32(starts, (n + 1,), "starts"), _i32(parents, (total,), "parents"), _i32(tokens, (total,), "tokens")
     dev = _one_device(starts, parents, tokens, target, draft, uniforms, last, path, kept, next_tokens)
+    if path is None and kept is None and next_tokens is None and max_new > 0:
+        # one piece of memory for the three
+        flat = _empty_on(stream, n * (max_new + 2), torch.int32, torch.device("cuda", dev))
+        path = flat.as_strided((n, max_new), (max_new, 1))
+        kept, next_tokens = flat.as_strided((n,), (1,), n * max_new), flat.as_strided((n,), (1,), n * (max_new + 1))
     if path is None:
-        path = _empty_on(stream, (n, max_new), torch.int32, dev)
+        path = _empty_on(stream, (n, max_new), torch.int32, torch.device("cuda", dev))
     if kept is None:
-        kept = _empty_on(stream, n, torch.int32, dev)
+        kept = _empty_on(stream, n, torch.int32, torch.device("cuda", dev))
     if next_tokens is None:
-        next_tokens = _empty_on(stream, n, torch.int32, dev)
-    # (a tensor of one row has no row to step to)
-    step = lambda x: max(x.stride(0), vocab) if total < 2 else x.stride(0)  # noqa: E731
-    _check(lib().tq_verify_drafts(at[0], n, total, max_new, at[1], at[2], vocab, code, target.data_ptr(), step(target),
-                                  None if draft is None else draft.data_ptr(), 0 if draft is None else step(draft),
+        next_tokens = _empty_on(stream, n, torch.int32, torch.device("cuda", dev))
+    _check(lib().tq_verify_drafts(at[0], n, total, max_new, at[1], at[2], vocab, code, target.data_ptr(), step, other, other_step,
                                   uniforms.data_ptr(), last.data_ptr(), _i32(path, (n, max_new), "path"), max_new,
                                   _i32(kept, (n,), "kept"), _i32(next_tokens, (n,), "next_tokens"), _stream(stream)),
            "tq_verify_drafts")
     return path, kept, next_tokens
 
 
-def _rotary_tensor(x: torch.Tensor, out: torch.Tensor, what: str) -> _RotaryStruct:
-    if x.dim() != 3 or x.stride(2) != 1 or out.shape != x.shape or out.dtype != x.dtype or out.stride(2) != 1:
-        raise ValueError(f"{what} must be [tokens][heads][head_dim] with head_dim contiguous, its output like it")
-    # (a dimension of one place has no stride to speak of)
-    st = [_TWO(*(t.stride(i) if t.shape[i] > 1 else t.shape[2] for i in (0, 1))) for t in (x, out)]
-    return _RotaryStruct(x.data_ptr(), out.data_ptr(), st[0], st[1], x.shape[1], 0)
+_pack_rotary = struct.Struct("PPqqqqii").pack  # tq_rotary_tensor
+
+
+def _rotary_tensor(x: torch.Tensor, out: torch.Tensor | None, tokens: int, d: int, dtype, stream):
+    """A tq_rotary_tensor in bytes, and the output."""
+    shape, st = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != d or x.dtype is not dtype or st[2] != 1:
+        raise ValueError("q and k must be [tokens][heads][head_dim] of one type, head_dim contiguous")
+    if out is None:
+        out = torch.empty_like(x) if stream is None and x.is_contiguous() else _empty_on(stream, shape, dtype, x.device)
+    elif out.shape != shape or out.dtype is not dtype or out.stride(2) != 1:
+        raise ValueError("an output must be like its input, head_dim contiguous")
+    heads, ot = shape[1], out.stride()
+    a, b, e, f = st[0], st[1], ot[0], ot[1]
+    if heads == 1:  # (a dimension of one place has no stride to speak of)
+        b = f = d
+    if tokens == 1:
+        a = e = d
+    return _pack_rotary(x.data_ptr(), out.data_ptr(), a, b, e, f, heads, 0), out
 
 
 def tq_rotary(positions: torch.Tensor, freqs: torch.Tensor, q: torch.Tensor | None, k: torch.Tensor | None = None,
@@ -808,25 +832,24 @@ def tq_rotary(positions: torch.Tensor, freqs: torch.Tensor, q: torch.Tensor | No
               k_out: torch.Tensor | None = None, stream=None):
     """(q, k) turned by positions (int32 [tokens], below 0: left as it was) times freqs (float64 [rot_dim / 2]); q and k bf16
     or fp32 [tokens][heads][d], any token and head strides, either None; q_out=q turns in place."""
-    some = q if q is not None else k
+    some = k if q is None else q
     if some is None:
         raise ValueError("give q or k")
-    if some.dim() != 3 or (q is not None and k is not None and (k.dim() != 3 or q.shape[0] != k.shape[0] or
-                                                                q.shape[2] != k.shape[2] or q.dtype != k.dtype)):
-        raise ValueError("q and k must be [tokens][heads][head_dim] of one type")
+    if some.dim() != 3:
+        raise ValueError("q and k must be [tokens][heads][head_dim] of one type, head_dim contiguous")
     if freqs.dtype is not torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError("freqs must be contiguous float64 [rot_dim / 2]")
     if (q is None and q_out is not None) or (k is None and k_out is not None):
         raise ValueError("an output without its input")
-    tokens, d = some.shape[0], some.shape[2]
-    code, at = _dtype_code(some.dtype), _i32(positions, (tokens,), "positions")
-    dev = _one_device(positions, freqs, q, k, q_out, k_out)
-    if q is not None and q_out is None:
-        q_out = _empty_on(stream, q.shape, q.dtype, dev)
-    if k is not None and k_out is None:
-        k_out = _empty_on(stream, k.shape, k.dtype, dev)
-    a = None if q is None else ctypes.byref(_rotary_tensor(q, q_out, "q"))
-    b = None if k is None else ctypes.byref(_rotary_tensor(k, k_out, "k"))
+    tokens, _, d = some.shape
+    dtype = some.dtype
+    code, at = _dtype_code(dtype), _i32(positions, (tokens,), "positions")
+    _one_device(positions, freqs, q, k, q_out, k_out)
+    a = b = None
+    if q is not None:
+        a, q_out = _rotary_tensor(q, q_out, tokens, d, dtype, stream)
+    if k is not None:
+        b, k_out = _rotary_tensor(k, k_out, tokens, d, dtype, stream)
     _check(lib().tq_rotary(at, tokens, d, 2 * freqs.shape[0], int(interleaved), freqs.data_ptr(), float(scale), code, a, b,
                            _stream(stream)), "tq_rotary")
     return q_out, k_out
