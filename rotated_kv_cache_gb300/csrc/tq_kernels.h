@@ -93,6 +93,7 @@ struct PagedSplit {
     int nch, ru;              // chunks per stage, rows per chunk
     const uint32_t *masks;    // null: causal; else bit j of row t: token t sees new row j of its sequence
     int64_t mask_words;       // words from one token's mask to the next
+    int copies;               // a column's partials stand 2^copies times in a slot (tq_paged_block.cuh)
 };
 
 __host__ __device__ constexpr int gcd_int(int a, int b) { return b == 0 ? a : gcd_int(b, a % b); }

@@ -42,6 +42,15 @@ TQ_DECLARE_PAGED_SPLIT(d64_tree)
 TQ_DECLARE_PAGED_SPLIT(d128_tree)
 TQ_DECLARE_PAGED_SPLIT(d256_tree)
 #undef TQ_DECLARE_PAGED_SPLIT
+#define TQ_DECLARE_PAGED_BLOCK(NAME)                                                                                   \
+    bool paged_block_shape_##NAME(const CacheView &c, PagedShape &sh);                                                 \
+    cudaError_t launch_paged_block_##NAME(const CacheView &c, const PagedSplit &pg, const PagedShape &sh,              \
+                                          const uint16_t *q, int QH, float scale, float *part_o, float *part_ml,       \
+                                          cudaStream_t s);
+TQ_DECLARE_PAGED_BLOCK(d64)
+TQ_DECLARE_PAGED_BLOCK(d128)
+TQ_DECLARE_PAGED_BLOCK(d256)
+#undef TQ_DECLARE_PAGED_BLOCK
 
 namespace {
 
@@ -123,9 +132,12 @@ __global__ void __launch_bounds__(W > 4 ? W * 32 : 128) paged_combine_kernel(con
     // (a unit without a segment, or beyond the slots: starts out of order)
     const bool some = live && len > 0 && unit.first >= 0 && unit.count > 0 && unit.count <= p.pg.slots - unit.first;
     const int64_t first = unit.first;
-    const int segs = some ? unit.count : 0;
+    const int segs = some ? unit.count << p.pg.copies : 0, stride = p.CB >> p.pg.copies;  // partials; columns from one copy to the next
     const int mine = segs > wid ? (segs - wid + W - 1) / W : 0;
-    auto part = [&](int j) { return (first + wid + (int64_t)W * j) * p.CB + col; };
+    auto part = [&](int j) {
+        const int i = wid + W * j;
+        return (first + (i >> p.pg.copies)) * p.CB + (i & ((1 << p.pg.copies) - 1)) * stride + col;
+    };
     // the first rows are under way with their (max, sum) pairs
     constexpr int KF = PER <= 4 ? 4 : 2;
     float v[KF][PER];
@@ -233,6 +245,8 @@ bool generic_shape(const CacheView &c, int64_t cols, bool tree, PagedShape &sh)
 struct PagedPlan {
     PagedShape split;
     bool special;   // the specialised split kernel, else the generic one
+    bool block;     // the block kernel instead
+    int copies;     // log2 of the times that it holds a column
     int64_t per_seq, cols;  // most new tokens of a sequence, and columns of a kv-head, that the split kernels see
     PagedBounds b;
     int64_t slots;
@@ -260,20 +274,66 @@ struct PagedPlan {
 constexpr int64_t kWideColumns = 128;
 constexpr int64_t kWideWork = int64_t(1) << 22;  // rows x kv-heads x columns, by the bounds that the host has
 
+// The block kernel (tq_paged_block.cuh) takes the trees of a call when they have more
+// columns than one pass of the split kernel, and enough rows to fill its
+// pipelines; very many columns are worth the wide kernel's expanded rows.
+// Measured (us), 8 kv-heads unless said, 8-bit keys, 3- or 4-bit values:
+//   head_dim  sequences x rows  columns   block   split   wide
+//      128       8 x 16384         16      92.6    89.2
+//                                  24      95.5   158.8
+//               32 x 28672         64     637    1950
+//                1 x 512           64      16.8    13.7
+//                1 x 2048          64      18.9    19.0
+//               16 x 4352         384     222             298
+//                                 512     292             302
+//                                1024     558 (4-bit keys) 427
+//       64       4 x 8192          24      30.0    32.2
+//               16 x 4352         384     175             188
+//                                 512     231             187
+//      256       2 x 16384         12      42.0    49.3  (4 kv-heads, as below)
+//                                 128      57.1   278.5
+//                2 x 512           32      19.0    14.8
+//                2 x 2048          32      22.4    22.5
+// Keys or values of other widths are cut by run-time shifts, straight from memory:
+//      128       4 x 8192          32      60.1    56.7
+//                                  64      61.3    95.4
+//                                 384     159             164
+constexpr int64_t kBlockWork = int64_t(1) << 20;  // rows x kv-heads x columns, by the bounds that the host has
+
+bool takes_block(const CacheView &c, const PagedBounds &b, int64_t G)
+{
+    const int64_t most = b.max_new * G;  // columns of the largest sequence
+    if (!b.tree || c.d > 256 || (int64_t)c.B * c.H * c.cap >= (int64_t(1) << 31)) return false;  // (its tensor copies count rows in 32 bits)
+    const bool cut = (c.kb == 8 || c.kb == 4) && c.vb <= 4;
+    if (most <= (!cut ? 32 : c.d == 256 ? 8 : 16)) return false;
+    if (c.d <= 128 && most > 384) return false;
+    return b.total_len >= (kBlockWork + c.H * most - 1) / (c.H * most);
+}
+
+bool block_shape(const CacheView &c, PagedShape &sh)
+{
+    return c.d == 64 ? paged_block_shape_d64(c, sh) : c.d == 128 ? paged_block_shape_d128(c, sh) : paged_block_shape_d256(c, sh);
+}
+
 bool paged_plan(const CacheView &c, const PagedBounds &bounds, int QH, PagedPlan &pl)
 {
     const int64_t G = QH / c.H;
     pl.b = bounds;
     const int64_t most = pl.b.max_new * G;  // columns of the largest sequence
     const bool work = most >= kWideColumns && pl.b.total_len >= (kWideWork + c.H * most - 1) / (c.H * most);
-    pl.b.wide = paged_wide_applies(c) && work ? (kWideColumns - 1) / G : INT32_MAX;
+    pl.block = takes_block(c, pl.b, G);
+    pl.b.wide = paged_wide_applies(c) && work && !pl.block ? (kWideColumns - 1) / G : INT32_MAX;
     const bool wide = pl.b.wide != INT32_MAX;
     // new tokens of a sequence that the split kernels see, at most
     pl.per_seq = wide && !paged_wide_spills(c, pl.b, QH) ? (pl.b.wide > 0 ? pl.b.wide : 1) : pl.b.max_new;
     pl.cols = pl.per_seq * G;
     // the specialised kernel where it has the widths (its tensor copies count rows in 32 bits)
     pl.special = attention_supported(c.d, c.kb, c.vb, (int)G) && (int64_t)c.B * c.H * c.cap < (int64_t(1) << 31);
-    if (pl.special)
+    pl.copies = 0;
+    if (pl.block) {
+        if (!block_shape(c, pl.split)) return false;
+        pl.copies = most <= 64 ? (most <= 32 && c.d <= 128 ? 2 : 1) : 0;  // (of shares of 32 rows at least)
+    } else if (pl.special)
         pl.split = pl.b.tree
                        ? (c.d == 64    ? paged_split_shape_d64_tree(c, pl.cols)
                           : c.d == 128 ? paged_split_shape_d128_tree(c, pl.cols)
@@ -317,10 +377,14 @@ cudaError_t launch_paged_attention(const CacheView &c, const PagedView &v, const
     uint8_t *base = static_cast<uint8_t *>(ws);
     const bool wide = pl.b.wide != INT32_MAX;
     PagedSplit pg{v, qs[0], qs[1], reinterpret_cast<PagedUnit *>(base), pl.slots, pl.blocks, pl.b.max_new, pl.b.wide,
-                  wide ? paged_wide_spill(c, pl.b, QH, base + pl.off_wide) : nullptr, 1, 1, masks, mask_words};
+                  wide ? paged_wide_spill(c, pl.b, QH, base + pl.off_wide) : nullptr, 1, 1, masks, mask_words, pl.copies};
     float *part_ml = reinterpret_cast<float *>(base + pl.off_ml), *part_o = reinterpret_cast<float *>(base + pl.off_o);
     auto split = [&]() -> cudaError_t {
         const int64_t cols = pl.cols;
+        if (pl.block) {
+            const auto launch = c.d == 64 ? launch_paged_block_d64 : c.d == 128 ? launch_paged_block_d128 : launch_paged_block_d256;
+            return launch(c, pg, pl.split, q, QH, scale, part_o, part_ml, s);
+        }
         if (pl.special) {
             const auto launch = pl.b.tree
                                     ? (c.d == 64 ? launch_paged_split_d64_tree : c.d == 128 ? launch_paged_split_d128_tree : launch_paged_split_d256_tree)

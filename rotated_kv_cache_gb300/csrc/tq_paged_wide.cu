@@ -52,6 +52,7 @@
 #include "tq_common.cuh"
 #include "tq_kernels.h"
 #include "tq_paged.cuh"
+#include "tq_paged_rows.cuh"
 #include "tq_tcgen05.cuh"
 
 namespace tq {
@@ -65,11 +66,6 @@ constexpr int wPlanThreads = 256;
 // tiles.  A prompt of 8191 tokens, 32 q-heads, with 3 / 4 / 5 / 7 / 9: 498 / 489 /
 // 493 / 502 / 510 us; of 4096 tokens 178 / 173 / 175 / 180 / 180.
 constexpr int wStart = 4;
-constexpr float wTau = 8.0f, wUp = 6.0f;  // lazy raise of R; weights are 2^(s - R + wUp)
-// A product of the operand tiles is below 2^(15 + 14) D <= 2^36, so with a factor
-// up to this the scores are below 2^24, where R's last bit is 1.
-constexpr float wFar = 1.0f / 4096;
-
 // What expand says about a tile.
 struct __align__(16) TileMeta {
     float kf;       // 2^-ek: scores are (q k~) kf
@@ -78,15 +74,6 @@ struct __align__(16) TileMeta {
     uint32_t any;   // bit 0: some value row is not finite; bit 1: every row has exponents of its own (RowMeta)
     uint32_t bad[4];
 };
-
-struct __align__(8) RowMeta {  // of a row of a tile whose rows are of very unlike sizes
-    float kf, e;               // as the tile's
-};
-// A tile gets them where its largest row is larger than its smallest (not zero)
-// by more than this: two f16 terms of a key 2^-16 of the tile's largest still keep
-// 2^-22 of it (the low term's last bit is 2^-38 of the largest), one of a value
-// 2^-24 of it 2^-12.
-constexpr float wSpreadK = 65536.0f, wSpreadV = 16777216.0f;
 
 struct WidePlan {        // device arrays, written by plan
     int32_t *tile0;      // [seqs + 1] scratch tiles before a sequence
@@ -502,96 +489,6 @@ __global__ void __launch_bounds__(256, 4) wide_expand_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------- attend
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
-__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-// A tile whose rows have exponents of their own (their sizes are very unlike, so
-// that one exponent would leave some of them too few of f16's bits): this
-// column's true base-2 scores, value exponents added, in place of the products.
-// The thread goes on with those as with any tile's; the weights' sum, whose terms
-// need each row's value exponent, is taken here at the reference R that it will
-// choose.  Out of line: rare, and its registers are not the common path's.
-// `rows` says which rows the column sees: the first `vis`, or those of a mask.
-struct CausalRows {
-    int vis;
-    __device__ __forceinline__ uint32_t from(int c) const  // of rows c .. c + 31, as bits
-    {
-        const int n = vis - c;
-        return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
-    }
-};
-
-struct TreeRows {
-    const uint32_t *mask;
-    int j0, n;  // the tile's first row among the new ones, new tokens
-    __device__ __forceinline__ uint32_t from(int c) const { return paged_tree_bits(mask, j0 + c, n); }
-};
-
-template <typename Rows>
-__device__ __noinline__ float mixed_tile(uint32_t t_s, const RowMeta *rm, float ie, Rows rows, float R)
-{
-    float mx = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-    for (int c = 0; c < wT; c += 16) {
-        uint32_t x[16];
-        tc_ld16(t_s + c, x);
-        tc_wait_ld();
-        tc_pin(x);
-        const uint32_t seen = rows.from(c);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const RowMeta r = rm[c + j];
-            const float y = fmaf(__uint_as_float(x[j]), fmaxf(ie * r.kf, 1.17549435e-38f), r.e);
-            x[j] = seen >> j & 1u ? __float_as_uint(y) : 0xFF800000u;
-            mx = fmaxf(mx, __uint_as_float(x[j]));
-        }
-        tc_st16(t_s + c, x);
-    }
-    tc_wait_st();
-    if (mx > R + wTau) R = mx;
-    const float add = R == -INFINITY ? 0.0f : wUp - R;
-#pragma unroll 1
-    for (int c = 0; c < wT; c += 16) {
-        uint32_t x[16];
-        tc_ld16(t_s + c, x);
-        tc_wait_ld();
-        tc_pin(x);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)  // weight times 2^-e, |e| <= 100
-            sum = fmaf(tc_ex2(__uint_as_float(x[j]) + add), __int_as_float((127 - (int)rm[c + j].e) << 23), sum);
-    }
-    return sum;
-}
-
-// Scores that may be 2^24 and more: s = x f + e in place of the products x,
-// rounded as R is.  (Taken in one step, x f + (e - R) is exact, and its distance
-// from a rounded R of that size no exponent of a weight.)
-__device__ __noinline__ void far_tile(uint32_t t_s, float f, float e)
-{
-#pragma unroll 1
-    for (int c = 0; c < wT; c += 16) {
-        uint32_t x[16];
-        tc_ld16(t_s + c, x);
-        tc_wait_ld();
-        tc_pin(x);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), f, e));
-        tc_st16(t_s + c, x);
-    }
-    tc_wait_st();
-}
-
 // Tensor memory holds S of both groups (128 columns each; P, f16, overwrites
 // its first half) and O of both.  In one pass over a tile the issuing warp
 // queues O_a += P_a V, S_a = Q_a K(next), then the same for the other group, so
@@ -898,13 +795,13 @@ __global__ void __launch_bounds__(wThreads, 1) wide_attend_kernel(const __grid_c
                 tc_fence_after();
                 float extra = 0.0f;
                 if (!(any & 2u) && __any_sync(0xffffffffu, f > wFar)) {
-                    far_tile(t_s, f, e);
+                    far_tile(t_s, f, e, 0, wT);
                     f = 1.0f;
                     e = 0.0f;
                 }
                 if (any & 2u) {
                     // rows of exponents of their own: true scores now, and the sum of the weights
-                    extra = mixed_tile(t_s, p.row_meta + (mt - p.meta) * wT, ie, rows(), R);
+                    extra = mixed_tile(t_s, p.row_meta + (mt - p.meta) * wT, ie, rows(), R, 0, wT);
                     f = 1.0f;
                     e = lf = 0.0f;
                 } else if (__any_sync(0xffffffffu, vis < wT)) {  // some column does not see the whole tile: its hidden scores become -inf
