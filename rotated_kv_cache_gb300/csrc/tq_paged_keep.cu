@@ -9,6 +9,8 @@
 //
 // A few rows of 200 bytes for each of hundreds of CTAs: bound by the latency of
 // three dependent loads (path, page, row).
+// 32 sequences of up to 5 kept rows, 8 kv-heads: 3.4 us, of which a launch is 2; 256 of up
+// to 12, 4 kv-heads at head_dim 256: 7.2 us.
 #include "tq_common.cuh"
 #include "tq_kernels.h"
 #include "tq_paged.cuh"

@@ -15,16 +15,24 @@
 // p(x) = 0.  When the children are through, the next token is drawn from what is
 // left: the first v whose running sum passes last * sum (where nothing is left, the vocabulary's size).
 //
-// The sums decide which token comes out, so they are kept to 2^-45 or so: a
-// thread adds in pairs of floats (sum and what its roundings left out, the
-// product C r(v) in two parts), whole threads' sums are added in 64 bits.  (64-bit
-// additions for every element would take this chip 64 times as long as 32-bit ones.)
+// The sums decide which token comes out, so they are kept to 2^-45 or so: every
+// addition is one of pairs of floats (sum and what its roundings left out, the
+// product C r(v) in two parts).  64-bit additions would take this chip 64 times as
+// long as 32-bit ones; they are left for the few numbers of a sequence.
 //
-// A cluster of CTAs goes through a row, a run of elements per warp.  The first CTA
-// alone reads the tree and decides; the others are told what to sum, so that
-// no two of them can disagree on how often they meet.  A pass moves the row once:
-// bound by memory for many sequences, by the latency of loads and cluster
-// barriers for few.
+// A cluster of CTAs goes through a row, a run of elements per warp, a run in up to
+// eight pieces with a sum each, so that the one that holds the drawn token is short.
+// The first warp of the first CTA alone reads the tree and decides; all the others are told what
+// to sum, so that no two of them can disagree on how often they meet.  A pass moves
+// the row once: bound by memory for many sequences, by the latency of four
+// dependent loads (tree, its tokens' entries, row, drawn piece) and of the
+// cluster's barriers for few.
+//
+// 16 chains of 5 nodes, 32000 tokens, with draft probabilities: 12.7 us; 64 trees of 8
+// to 32 nodes, 131072 tokens, without: 24.4 us (1.4 TB/s).  With 64-bit sums by every
+// thread of the deciding CTA and 32 KB runs searched element by element they took 32
+// and 76; without the template for drafts, whose registers halve what is under way,
+// 12.7 and 31.  Clusters of 4: 15 and 34; 512 threads: 23 and 85 (fewer CTAs fit).
 #include "tq_common.cuh"
 #include "tq_kernels.h"
 #include "tq_paged.cuh"
@@ -33,11 +41,11 @@ namespace tq {
 namespace {
 
 constexpr int vfThreads = 256, vfWarps = vfThreads / 32;
-constexpr int vfCluster = 8, vfParts = vfWarps * vfCluster;  // warps to a sequence
+constexpr int vfCluster = 8, vfRuns = vfWarps * vfCluster;  // warps to a sequence
+constexpr int vfPieces = 8;                                 // of a run, at most
 
 struct VerifyParams {
     VerifyCall c;
-    int parts;      // warps to a sequence: vfWarps * CTAs of a cluster
 };
 
 // What the CTAs of a cluster are to sum, as the first one says.
@@ -51,13 +59,6 @@ __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t cluster_size()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
 
@@ -89,9 +90,9 @@ __device__ __forceinline__ int64_t cluster_load64(uint32_t a)
     return v;
 }
 
-__device__ __forceinline__ void cluster_store64(uint32_t a, double v)
+__device__ __forceinline__ void cluster_store(uint32_t a, float2 v)
 {
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
 // A probability as it counts: neither negative, NaN nor infinite.
@@ -100,7 +101,7 @@ __device__ __forceinline__ float vf_clean(float x) { return x > 0.0f && x < INFI
 __device__ __forceinline__ float vf_at(const float *row, int64_t v) { return vf_clean(row[v]); }
 __device__ __forceinline__ float vf_at(const uint16_t *row, int64_t v) { return vf_clean(__uint_as_float((uint32_t)row[v] << 16)); }
 
-// A running sum in two floats: s + e.
+// A sum in two floats, s + e.
 struct TwoSum {
     float s = 0.0f, e = 0.0f;
     __device__ __forceinline__ void add(float x)
@@ -109,7 +110,30 @@ struct TwoSum {
         e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z)));
         s = t;
     }
+    __device__ __forceinline__ void add(float x, float rest)
+    {
+        add(x);
+        e = __fadd_rn(e, rest);
+    }
+    __device__ __forceinline__ double value() const { return (double)s + (double)e; }
 };
+
+__device__ __forceinline__ TwoSum warp_total(TwoSum x)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) x.add(__shfl_xor_sync(0xffffffffu, x.s, o), __shfl_xor_sync(0xffffffffu, x.e, o));
+    return x;
+}
+
+__device__ __forceinline__ TwoSum warp_running(TwoSum x, int lane)  // the sum up to each lane
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float s = __shfl_up_sync(0xffffffffu, x.s, o), e = __shfl_up_sync(0xffffffffu, x.e, o);
+        if (lane >= o) x.add(s, e);
+    }
+    return x;
+}
 
 // max(p - C r, 0) in two floats, C = c1 + c2
 struct TwoFloat {
@@ -128,10 +152,10 @@ __device__ __forceinline__ TwoFloat vf_left(float p, float r, float c1, float c2
 // A warp's run of a row: tiles of 32 E elements, counted from the 16-byte
 // boundary at or before the row's start, so that a lane's E elements are one
 // access wherever the row starts.
-template <typename T>
+template <typename T, bool DRAFT>
 struct VerifyRow {
-    static constexpr int E = 16 / sizeof(T);
-    const T *p, *r;  // r null: none
+    static constexpr int E = 16 / sizeof(T), U = (DRAFT ? 8 : 16) / E;  // elements of an access; accesses of a row under way
+    const T *p, *r;  // (r without DRAFT: none)
     int64_t vocab;
     int off;         // elements from the boundary to the row's start
     bool same;       // r starts as far from a boundary as p
@@ -139,16 +163,16 @@ struct VerifyRow {
     __device__ __forceinline__ VerifyRow(const VerifyCall &c, int64_t row)
     {
         p = static_cast<const T *>(c.target) + row * c.target_stride;
-        r = c.draft ? static_cast<const T *>(c.draft) + row * c.draft_stride : nullptr;
+        r = DRAFT ? static_cast<const T *>(c.draft) + row * c.draft_stride : nullptr;
         vocab = c.vocab;
         off = (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
-        same = r && off == (int)((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
+        same = DRAFT && off == (int)((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
     }
-    // tiles of a warp's run, and the run of warp w
-    __device__ __forceinline__ int64_t run(int parts) const
+    // tiles of a piece: a multiple of U of them, vfPieces pieces a warp and vfRuns warps at most
+    __device__ __forceinline__ int piece() const
     {
-        const int64_t tiles = (vocab + off + 32 * E - 1) / (32 * E);
-        return (tiles + parts - 1) / parts;
+        const uint32_t tiles = (uint32_t)(vocab + off + 32 * E - 1) / (32 * E), run = (tiles + vfRuns - 1) / vfRuns;
+        return (int)((run + vfPieces * U - 1) / (vfPieces * U)) * U;
     }
     // the element of a tile that the lane's first one is (may lie before or behind the row)
     __device__ __forceinline__ int64_t first(int64_t tile, int lane) const { return (tile * 32 + lane) * E - off; }
@@ -177,239 +201,284 @@ struct VerifyRow {
     {
 #pragma unroll
         for (int i = 0; i < E; ++i)
-            z[i] = r ? vf_left(vf_clean(x[i]), vf_clean(y[i]), c1, c2) : TwoFloat{vf_clean(x[i]), 0.0f};
+            z[i] = DRAFT ? vf_left(vf_clean(x[i]), vf_clean(y[i]), c1, c2) : TwoFloat{vf_clean(x[i]), 0.0f};
     }
 };
 
-// Sum of what is left over the run of warp `w`.  `gone`: addresses of the first CTA's list of crossed-out tokens.
-template <typename T>
-__device__ __forceinline__ double verify_sum(const VerifyRow<T> &a, int64_t run, int w, double C, uint32_t list, int gone, int lane)
+// Pieces of a row, in order: tiles of a piece, pieces in all and of a warp.
+struct VerifyPieces {
+    int tiles, all, each;
+    template <typename T, bool DRAFT>
+    __device__ __forceinline__ explicit VerifyPieces(const VerifyRow<T, DRAFT> &a)
+    {
+        constexpr int E = VerifyRow<T, DRAFT>::E;
+        const uint32_t n = (uint32_t)(a.vocab + a.off + 32 * E - 1) / (32 * E);
+        tiles = a.piece();
+        all = (int)((n + tiles - 1) / tiles);
+        each = (all + vfRuns - 1) / vfRuns;
+    }
+};
+
+// Elements of crossed-out tokens (a list of `gone` at address `list` of the first CTA; its first 32 in `mine`) become
+// 0 where they are among the lane's, from v[u] on.
+template <int U, int E>
+__device__ __forceinline__ void cross_out(float (&x)[U][E], const int64_t (&v)[U], int64_t lo, int64_t hi, int mine, uint32_t list, int gone,
+                                          int lane)
 {
-    constexpr int E = VerifyRow<T>::E, U = 4;
-    const int64_t t0 = w * run, v_lo = a.first(t0, 0), v_hi = a.first(t0 + run, 0);
+    for (int i0 = 0; i0 < gone; i0 += 32) {
+        const int g = i0 == 0 ? mine : i0 + lane < gone ? cluster_load(list + 4 * (i0 + lane)) : -1;
+        for (uint32_t hit = __ballot_sync(0xffffffffu, g >= lo && g < hi); hit; hit &= hit - 1) {
+            const int t = __shfl_sync(0xffffffffu, g, __ffs(hit) - 1);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (v[u] + i == t) x[u][i] = 0.0f;
+        }
+    }
+}
+
+// What is left in the pieces of warp `w`, a sum each, to the first CTA's `part`.
+template <typename T, bool DRAFT>
+__device__ __forceinline__ void verify_sums(const VerifyRow<T, DRAFT> &a, int w, double C, uint32_t list, int gone, uint32_t part, int lane)
+{
+    constexpr int E = VerifyRow<T, DRAFT>::E, U = VerifyRow<T, DRAFT>::U;
+    const VerifyPieces pc(a);
     const float c1 = (float)C, c2 = (float)(C - (double)c1);
-    TwoSum sum;
-    if (v_lo < a.vocab) {
-        for (int64_t t = t0; t < t0 + run; t += U) {
+    const int mine = lane < gone ? cluster_load(list + 4 * lane) : -1;
+    for (int q = w * pc.each; q < (w + 1) * pc.each && q < pc.all; ++q) {
+        TwoSum sum;
+#pragma unroll 1
+        for (int t = 0; t < pc.tiles; t += U) {
+            const int64_t t0 = (int64_t)q * pc.tiles + t;
             float x[U][E], y[U][E];
+            int64_t v[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t v = t + u < t0 + run ? a.first(t + u, lane) : a.vocab;
-                VerifyRow<T>::load(a.p, v, a.vocab, true, x[u]);
-                if (a.r) VerifyRow<T>::load(a.r, v, a.vocab, a.same, y[u]);
+                v[u] = a.first(t0 + u, lane);
+                VerifyRow<T, DRAFT>::load(a.p, v[u], a.vocab, true, x[u]);
+                if constexpr (DRAFT) VerifyRow<T, DRAFT>::load(a.r, v[u], a.vocab, a.same, y[u]);
             }
+            if (!DRAFT && gone) cross_out(x, v, a.first(t0, 0), a.first(t0 + U, 0), mine, list, gone, lane);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 TwoFloat z[E];
                 a.left(x[u], y[u], c1, c2, z);
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    sum.add(z[i].hi);
-                    sum.e += z[i].lo;
-                }
+                for (int i = 0; i < E; ++i) sum.add(z[i].hi, z[i].lo);
             }
         }
-        // (crossed-out tokens of the run: taken out of the sum of the lane that the list's place falls to)
-        for (int i = lane; i < gone; i += 32) {
-            const int x = cluster_load(list + 4 * i);
-            if (x >= v_lo && x < v_hi) sum.add(-vf_at(a.p, x));
-        }
+        sum = warp_total(sum);
+        if (lane == 0) cluster_store(part + 8 * q, make_float2(sum.s, sum.e));
     }
-    double d = (double)sum.s + (double)sum.e;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    return d > 0.0 ? d : 0.0;
 }
 
-// The first element of warp w's run whose running sum, from `before` on, passes
-// `goal`; the run's last one that is left where roundings leave none.  Whole warps call.
-template <typename T>
-__device__ __forceinline__ int64_t verify_find(const VerifyRow<T> &a, int64_t run, int w, double C, const int *list, int gone,
-                                               double before, double goal, int lane)
+// The first element of piece q whose running sum, from `before` on, passes `goal`; the
+// piece's last one that is left where roundings leave none (-1: none is left).
+template <typename T, bool DRAFT>
+__device__ __forceinline__ int64_t verify_find(const VerifyRow<T, DRAFT> &a, int q, double C, uint32_t list, int gone, double before, double goal,
+                                               int lane)
 {
-    constexpr int E = VerifyRow<T>::E;
+    constexpr int E = VerifyRow<T, DRAFT>::E, U = VerifyRow<T, DRAFT>::U;
+    const VerifyPieces pc(a);
     const float c1 = (float)C, c2 = (float)(C - (double)c1);
+    const int mine = lane < gone ? cluster_load(list + 4 * lane) : -1;
     int64_t found = -1;
-    for (int64_t t = w * run; t < (w + 1) * run; ++t) {
-        const int64_t v = a.first(t, lane);
-        float x[E], y[E];
-        VerifyRow<T>::load(a.p, v, a.vocab, true, x);
-        if (a.r) VerifyRow<T>::load(a.r, v, a.vocab, a.same, y);
-        TwoFloat z[E];
-        a.left(x, y, c1, c2, z);
-        for (int i = 0; i < gone; ++i) {
-            const int64_t k = list[i] - v;
+#pragma unroll 1
+    for (int t = 0; t < pc.tiles; t += U) {
+        const int64_t t0 = (int64_t)q * pc.tiles + t;
+        float x[U][E], y[U][E];
+        int64_t v[U];
 #pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (k == j) z[j] = TwoFloat{0.0f, 0.0f};
+        for (int u = 0; u < U; ++u) {
+            v[u] = a.first(t0 + u, lane);
+            VerifyRow<T, DRAFT>::load(a.p, v[u], a.vocab, true, x[u]);
+            if constexpr (DRAFT) VerifyRow<T, DRAFT>::load(a.r, v[u], a.vocab, a.same, y[u]);
         }
-        double own = 0.0;
-        int last = -1;
+        if (!DRAFT && gone) cross_out(x, v, a.first(t0, 0), a.first(t0 + U, 0), mine, list, gone, lane);
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            own += (double)z[j].hi + (double)z[j].lo;
-            if (z[j].hi > 0.0f) last = j;
-        }
-        double in = own;
+        for (int u = 0; u < U; ++u) {
+            TwoFloat z[E];
+            a.left(x[u], y[u], c1, c2, z);
+            TwoSum own;
+            int last = -1;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double y2 = __shfl_up_sync(0xffffffffu, in, o);
-            if (lane >= o) in += y2;
-        }
-        const uint32_t over = __ballot_sync(0xffffffffu, last >= 0 && before + in > goal);
-        if (over) {
-            const int l = __ffs(over) - 1;
-            double acc = before + (in - own);
-            int pick = last;
-#pragma unroll
-            for (int j = E - 1; j >= 0; --j) {  // the first that passes: from behind
-                double upto = acc;
-#pragma unroll
-                for (int k = 0; k <= j; ++k) upto += (double)z[k].hi + (double)z[k].lo;
-                if (z[j].hi > 0.0f && upto > goal) pick = j;
+            for (int i = 0; i < E; ++i) {
+                own.add(z[i].hi, z[i].lo);
+                if (z[i].hi > 0.0f) last = i;
             }
-            return __shfl_sync(0xffffffffu, v + pick, l);
+            const TwoSum upto = warp_running(own, lane);
+            const uint32_t over = __ballot_sync(0xffffffffu, last >= 0 && before + upto.value() > goal);
+            if (over) {
+                // in the first such lane, element after element
+                double at = before + (upto.value() - own.value());
+                int pick = -1;
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    at += (double)z[i].hi + (double)z[i].lo;
+                    if (pick < 0 && z[i].hi > 0.0f && (at > goal || i == last)) pick = i;
+                }
+                return __shfl_sync(0xffffffffu, v[u] + pick, __ffs(over) - 1);
+            }
+            const uint32_t some = __ballot_sync(0xffffffffu, last >= 0);
+            if (some) found = __shfl_sync(0xffffffffu, v[u] + last, 31 - __clz(some));
+            before += __shfl_sync(0xffffffffu, upto.value(), 31);
         }
-        const uint32_t some = __ballot_sync(0xffffffffu, last >= 0);
-        if (some) found = __shfl_sync(0xffffffffu, v + last, 31 - __clz(some));
-        before += __shfl_sync(0xffffffffu, in, 31);
     }
     return found;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(vfThreads) verify_kernel(const __grid_constant__ VerifyParams p)
+template <typename T, bool DRAFT>
+__global__ void __launch_bounds__(vfThreads, 4) verify_kernel(const __grid_constant__ VerifyParams p)
 {
     extern __shared__ int tree[];  // first CTA: parents, tokens, crossed-out tokens, numbers, p and r of each node's token
     __shared__ VerifyOrder order;
-    __shared__ double part[vfParts];  // first CTA: sums of the sequence's warps
+    __shared__ float2 part[vfRuns * vfPieces];  // first CTA: sums of the sequence's pieces
     pdl_wait_primary();
     pdl_allow_dependents();
     const VerifyCall &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_rank(), ctas = cluster_size();
-    const int s = blockIdx.x / ctas, M = (int)c.max_new;
+    const uint32_t rank = cluster_rank();
+    const int s = blockIdx.x / vfCluster, M = (int)c.max_new;
     const uint32_t order_at = cluster_addr(&order, 0), part_at = cluster_addr(part, 0), gone_at = cluster_addr(tree + 2 * M, 0);
-
-    // one sum over the cluster, of every CTA: order, run, sums to the first CTA
     auto pass = [&](int64_t row, double C, int gone) {
-        const VerifyRow<T> a(c, row);
-        const int w = rank * vfWarps + warp;
-        const double d = verify_sum<T>(a, a.run(p.parts), w, C, gone_at, gone, lane);
-        if (lane == 0) cluster_store64(part_at + 8 * w, d);
+        verify_sums<T, DRAFT>(VerifyRow<T, DRAFT>(c, row), rank * vfWarps + warp, C, gone_at, gone, part_at, lane);
     };
-    if (rank != 0) {
+    int *parent = tree, *token = tree + M, *gone = tree + 2 * M;
+    float *num = reinterpret_cast<float *>(tree + 3 * M), *pp = num + M, *rr = pp + M;
+    int64_t s0 = 0;
+    int n = 0;
+    if (rank == 0) {
+        s0 = c.starts[s];
+        const int64_t s1 = c.starts[s + 1];
+        n = (int)(s1 - s0);
+        if (s0 < 0 || s1 < s0 || s1 > c.total || s1 - s0 > c.max_new) {
+            if (tid == 0) atomicOr(c.err, kErrLength);
+            n = 0;
+        }
+        for (int j = tid; j < n; j += vfThreads) {
+            int up = c.parents[s0 + j];
+            const int x = c.tokens[s0 + j];
+            const float u = c.uniforms[s0 + j];
+            if (up < -1 || up >= j || (j > 0 && (x < 0 || x >= c.vocab))) {
+                atomicOr(c.err, kErrTree);
+                up = -1;  // of no node: never reached
+            }
+            parent[j] = j > 0 ? up : -1;
+            token[j] = x;
+            num[j] = u;
+            if (j > 0 && up >= 0) {
+                pp[j] = vf_at(static_cast<const T *>(c.target) + (s0 + up) * c.target_stride, x);
+                rr[j] = DRAFT ? vf_at(static_cast<const T *>(c.draft) + (s0 + up) * c.draft_stride, x) : 1.0f;
+            }
+        }
+        for (int k = tid; k < M; k += vfThreads) c.path[s * c.path_stride + k] = -1;
+        __syncthreads();
+    }
+    if (rank != 0 || warp != 0) {
+        // told what to sum, until there is nothing more
         for (;;) {
             cluster_sync();  // the order is there
             const int64_t row = cluster_load64(order_at);
             if (row < 0) break;
-            const double C = __longlong_as_double(cluster_load64(order_at + 8));
-            const int gone = cluster_load(order_at + 16);
-            pass(row, C, gone);
+            pass(row, __longlong_as_double(cluster_load64(order_at + 8)), cluster_load(order_at + 16));
             cluster_sync();  // the sums are there
         }
         cluster_sync();  // (the first CTA's memory is read no more)
         return;
     }
 
-    const int64_t s0 = c.starts[s], s1 = c.starts[s + 1];
-    int n = (int)(s1 - s0);
-    if (s0 < 0 || s1 < s0 || s1 > c.total || s1 - s0 > c.max_new) {
-        if (tid == 0) atomicOr(c.err, kErrLength);
-        n = 0;
-    }
-    int *parent = tree, *token = tree + M, *gone = tree + 2 * M;
-    float *num = reinterpret_cast<float *>(tree + 3 * M), *pp = num + M, *rr = pp + M;
-    for (int j = tid; j < n; j += vfThreads) {
-        int up = c.parents[s0 + j];
-        const int x = c.tokens[s0 + j];
-        if (up < -1 || up >= j || (j > 0 && (x < 0 || x >= c.vocab))) {
-            atomicOr(c.err, kErrTree);
-            up = -1;  // of no node: never reached
-        }
-        parent[j] = j > 0 ? up : -1;
-        token[j] = x;
-        num[j] = c.uniforms[s0 + j];
-        if (j > 0 && up >= 0) {
-            pp[j] = vf_at(static_cast<const T *>(c.target) + (s0 + up) * c.target_stride, x);
-            rr[j] = c.draft ? vf_at(static_cast<const T *>(c.draft) + (s0 + up) * c.draft_stride, x) : 1.0f;
-        }
-    }
+    // The deciding warp; every lane walks the tree, to the same end.
     int32_t *path = c.path + s * c.path_stride;
-    for (int k = tid; k < M; k += vfThreads) path[k] = -1;
-    __syncthreads();
-
-    // every thread of the CTA walks the tree, to the same end
-    auto total = [&](int64_t row, double C, int crossed) {
-        if (tid == 0) order = VerifyOrder{row, C, crossed};
+    int cur = 0, kept = n > 0 ? 1 : 0, crossed = 0;
+    double C = 0.0, mass = 1.0;
+    bool summed = false;  // the parts are those of cur and C
+    double mine = 0.0, upto = 0.0;  // sums of the lane's parts, and of those up to it
+    int parts = 0, each = 0;        // pieces, and of a lane
+    auto total = [&](int64_t row) {
+        if (lane == 0) order = VerifyOrder{row, C, crossed};
         cluster_sync();
         pass(row, C, crossed);
         cluster_sync();
-        double sum = 0.0;
-        for (int i = 0; i < p.parts; ++i) sum += part[i];
-        return sum;
-    };
-    int cur = 0, kept = n > 0 ? 1 : 0, crossed = 0;
-    double C = 0.0, mass = 1.0;
-    bool summed = false;  // the sums are those of cur and C
-    if (n > 0 && tid == 0) path[0] = 0;
-    for (int j = 1; j < n; ++j) {
-        if (parent[j] != cur) continue;
-        const double u = num[j], pj = pp[j], rj = rr[j];
-        double here = pj - C * rj;
-        if (!c.draft) {
-            here = pj;
-            for (int i = 0; i < crossed; ++i)
-                if (gone[i] == token[j]) here = 0.0;
+        parts = VerifyPieces(VerifyRow<T, DRAFT>(c, row)).all;
+        each = (parts + 31) / 32;
+        TwoSum x;
+        for (int i = lane * each; i < (lane + 1) * each && i < parts; ++i) x.add(part[i].x, part[i].y);
+        mine = x.value();
+        upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
         }
-        here = here > 0.0 ? here : 0.0;
-        if (u * rj * mass < here) {
-            if (tid == 0) path[kept] = j;
-            ++kept;
-            cur = j;
-            C = 0.0;
-            mass = 1.0;
-            crossed = 0;
-            summed = false;
-        } else if (c.draft) {
-            C += mass;
-            mass = total(s0 + cur, C, 0);
-            summed = true;
-        } else if (here > 0.0) {
-            mass -= here;
-            __syncthreads();  // (the list's readers are done)
-            if (tid == 0) gone[crossed] = token[j];
-            ++crossed;
-            __syncthreads();
+        return __shfl_sync(0xffffffffu, upto, 31);
+    };
+    double sum = 0.0;
+    if (n > 0 && lane == 0) path[0] = 0;
+    for (int j0 = 0; j0 < n; j0 += 32) {
+        int from = j0 == 0 ? 1 : j0;  // nodes before it are done
+        for (;;) {
+            const int at = j0 + lane;
+            const uint32_t kids = __ballot_sync(0xffffffffu, at >= from && at < n && parent[at < n ? at : 0] == cur);
+            if (kids == 0) break;
+            const int j = j0 + __ffs(kids) - 1;
+            from = j + 1;
+            const double u = num[j], rj = rr[j];
+            double here = (double)pp[j] - C * rj;
+            if (!DRAFT) {
+                here = pp[j];
+                for (int i = lane; i < crossed; i += 32)
+                    if (gone[i] == token[j]) here = 0.0;
+                if (__any_sync(0xffffffffu, here == 0.0)) here = 0.0;
+            }
+            here = here > 0.0 ? here : 0.0;
+            if (u * rj * mass < here) {
+                if (lane == 0) path[kept] = j;
+                ++kept;
+                cur = j;
+                C = 0.0;
+                mass = 1.0;
+                crossed = 0;
+                summed = false;
+            } else if (DRAFT) {
+                C += mass;
+                sum = mass = total(s0 + cur);
+                summed = true;
+            } else if (here > 0.0) {
+                mass -= here;
+                if (lane == 0) gone[crossed] = token[j];
+                ++crossed;
+                __syncwarp();
+            }
         }
     }
     int64_t next = -1;
     if (n > 0) {
-        double sum = 0.0;
-        if (!summed) sum = total(s0 + cur, C, crossed);
-        else
-            for (int i = 0; i < p.parts; ++i) sum += part[i];
+        if (!summed) sum = total(s0 + cur);
         next = c.vocab;
-        if (warp == 0 && sum > 0.0) {
+        if (sum > 0.0) {
             const double goal = (double)c.last[s] * sum;
-            // the first warp whose running sum passes the goal, else the last one that has something
-            double before = 0.0, upto = 0.0, from = 0.0;
-            int w = -1;
-            for (int i = 0; i < p.parts; ++i) {
-                before = upto;
-                upto += part[i];
-                if (part[i] > 0.0) {
-                    w = i;
-                    from = before;
-                    if (upto > goal) break;
+            // the first lane whose running sum passes the goal, else the last one that has something; then its part
+            const uint32_t over = __ballot_sync(0xffffffffu, mine > 0.0 && upto > goal), some = __ballot_sync(0xffffffffu, mine > 0.0);
+            const int l = over ? __ffs(over) - 1 : 31 - __clz(some);
+            double before = __shfl_sync(0xffffffffu, upto - mine, l), at = before;
+            int q = -1;
+            for (int i = l * each; i < (l + 1) * each && i < parts; ++i) {
+                const double x = (double)part[i].x + (double)part[i].y;
+                if (x > 0.0) {
+                    q = i;
+                    before = at;
+                    if (at + x > goal) break;
                 }
+                at += x;
             }
-            const VerifyRow<T> a(c, s0 + cur);
-            const int64_t v = verify_find<T>(a, a.run(p.parts), w, C, gone, crossed, from, goal, lane);
-            next = v >= 0 ? v : next;
+            if (q >= 0) {
+                const int64_t v = verify_find<T, DRAFT>(VerifyRow<T, DRAFT>(c, s0 + cur), q, C, gone_at, crossed, before, goal, lane);
+                next = v >= 0 ? v : next;
+            }
         }
     }
-    if (tid == 0) {
+    if (lane == 0) {
         c.kept[s] = kept;
         c.next[s] = (int)next;
         order.row = -1;
@@ -422,10 +491,12 @@ __global__ void __launch_bounds__(vfThreads) verify_kernel(const __grid_constant
 
 cudaError_t launch_verify(const VerifyCall &v, cudaStream_t s)
 {
-    VerifyParams p{v, vfParts};
+    VerifyParams p{v};
     const size_t smem = (size_t)v.max_new * 6 * 4;
     const dim3 grid((unsigned)v.seqs * vfCluster);
-    return launch_dependent_clusters(v.f32 ? verify_kernel<float> : verify_kernel<uint16_t>, grid, vfCluster, dim3(vfThreads), smem, s, p);
+    const auto kern = v.draft ? (v.f32 ? verify_kernel<float, true> : verify_kernel<uint16_t, true>)
+                              : (v.f32 ? verify_kernel<float, false> : verify_kernel<uint16_t, false>);
+    return launch_dependent_clusters(kern, grid, vfCluster, dim3(vfThreads), smem, s, p);
 }
 
 }  // namespace tq
