@@ -589,7 +589,7 @@ tq_status tq_paged_keep(const tq_cache *c, const tq_page_table *t, const int32_t
     tq_status st = check_paged(c, t, starts, total);
     if (st != TQ_OK) return st;
     if (!path || !kept || !lens_out) return TQ_ERR_NULL;
-    if (lens_out == t->seq_lens) return TQ_ERR_SHAPE;  // (read by every CTA of a sequence, written by one)
+    if (lens_out == t->seq_lens || lens_out == kept) return TQ_ERR_SHAPE;  // (read by every CTA of a sequence, written by one)
     if (max_new < 1 || path_stride < max_new) return TQ_ERR_SHAPE;
     if ((int64_t)t->num_seqs * c->num_kv_heads > (int64_t(1) << 30)) return TQ_ERR_SHAPE;
     const tq::PagedView pv = paged_view(c, t, starts, total);
@@ -642,7 +642,8 @@ tq_status tq_rotary(const int32_t *positions, int64_t tokens, int32_t head_dim, 
         }
         if (!aligned16(a.x) || !aligned16(a.out)) return TQ_ERR_ALIGN;
         // outputs apart from one another; in place element for element
-        if ((st[2] < head_dim && tokens > 1) || (st[3] < head_dim && a.heads > 1)) return TQ_ERR_SHAPE;
+        if ((tokens > 1 && st[2] < head_dim) || (a.heads > 1 && st[3] < head_dim)) return TQ_ERR_SHAPE;
+        if (tokens > 1 && a.heads > 1 && st[2] < (a.heads - 1) * st[3] + head_dim && st[3] < (tokens - 1) * st[2] + head_dim) return TQ_ERR_SHAPE;
         if (a.x == a.out && (st[0] != st[2] || st[1] != st[3])) return TQ_ERR_SHAPE;
         r.t[i] = tq::RotaryTensor{a.x, a.out, st[0], st[1], st[2], st[3], a.heads};
     }

@@ -201,6 +201,9 @@ __global__ void __launch_bounds__(plThreads) paged_layout_kernel(const __grid_co
         __syncthreads();
         starts = sh_starts;
     }
+    if (blockIdx.x == 0)  // (a token alone does not see that starts elsewhere fall)
+        for (int i = threadIdx.x; i < p.v.seqs; i += plThreads)
+            if (starts[i] > starts[i + 1]) atomicOr(p.v.err, kErrLength);
     auto sequence = [&](int64_t x) {  // the last sequence that starts at or before x, plus one
         int lo = 0, hi = p.v.seqs + 1;
         while (lo < hi) {
@@ -210,14 +213,14 @@ __global__ void __launch_bounds__(plThreads) paged_layout_kernel(const __grid_co
         }
         return lo;
     };
-    const int32_t *parents = p.parents;  // of token 0
+    int64_t held = INT64_MAX;  // tokens from this one on have their parents in shared memory
     if (p.parents) {
         const int s0 = sequence((int64_t)blockIdx.x * plThreads) - 1;
         const int64_t from = s0 >= 0 && starts[s0] >= 0 ? starts[s0] : 0;
         if (t_last - from < plParents) {
             for (int i = threadIdx.x; i <= t_last - from; i += plThreads) sh_parents[i] = p.parents[from + i];
             __syncthreads();
-            parents = sh_parents - from;
+            held = from;
         }
     }
     if (t >= p.v.total) return;
@@ -258,7 +261,9 @@ __global__ void __launch_bounds__(plThreads) paged_layout_kernel(const __grid_co
                 }
                 bits |= 1u << (j & 31);
             }
-            const int up = parents[t - node + j];
+            // (a sequence of starts out of order may lie before those that the block holds)
+            const int64_t at = t - node + j;
+            const int up = at >= held ? sh_parents[at - held] : p.parents[at];
             if (up < -1 || up >= j) {
                 atomicOr(p.v.err, kErrTree);
                 break;

@@ -337,6 +337,20 @@ def test_layout_of_bad_trees_and_pages(cuda):
     assert pos.tolist()[:6] == [-1] * 6 and slots.tolist()[:6] == [-1] * 6 and masks.tolist() == [[0]] * 6 + [[1], [2], [4]]
 
 
+def test_layout_of_starts_out_of_order(cuda):
+    """Starts that fall: what is read stays within the tokens, the fault is recorded, sequences in order have their places."""
+    seqs, total = 40, 400
+    starts = np.arange(0, 10 * seqs + 1, 10)
+    starts[20], starts[21] = 390, 15
+    pool = cuda.Cache(seqs * 4, 1, 64, 16, k_bits=2, v_bits=2)
+    table = cuda.PageTable(dev(np.arange(seqs * 4).reshape(seqs, 4)), dev([50] * seqs), 64)
+    parents = np.tile(np.arange(-1, 9), seqs)
+    for n in (10, 400):
+        pos, slots, masks = cuda.tq_paged_layout(pool, table, dev(starts), total, parents=dev(parents), max_new=n)
+        assert cuda.tq_device_error() & cuda.TQ_DEVICE_ERR_LENGTH
+        assert pos[:100].tolist() == list(range(40, 50)) * 10 and masks[:100, 0].tolist() == [2 ** (i + 1) - 1 for i in range(10)] * 10
+
+
 # ------------------------------------------------------------------ rotary
 # Bounds: sine and cosine within 2 steps of 2^-24 (what the part left out adds one rounding), the scale and the
 # two products and their sum one each: 6 steps of 2^-24 of (|a| + |b|) scale; then one rounding of the type.

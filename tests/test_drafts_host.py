@@ -71,6 +71,7 @@ def test_layout_and_keep_refusals(tqlib):
     assert keep(path=None) == NULL and keep(kept=None) == NULL and keep(out=None) == NULL
     assert keep(max_new=0) == SHAPE and keep(stride=7) == SHAPE
     assert keep(out=table.seq_lens) == SHAPE  # the table's own lengths
+    assert keep(out=2 * P) == SHAPE  # the counts
 
 
 def test_verify_refusals(tqlib):
@@ -110,6 +111,7 @@ def test_rotary_refusals(tqlib):
     assert rotary(q=tensor(xs=(-512, 128))) == SHAPE
     assert rotary(q=tensor(x=P + 8)) == ALIGN and rotary(q=tensor(xs=(512, 132))) == ALIGN
     assert rotary(q=tensor(os=(0, 128))) == SHAPE and rotary(q=tensor(os=(512, 64))) == SHAPE  # outputs upon one another
+    assert rotary(q=tensor(os=(256, 128))) == SHAPE and rotary(q=tensor(os=(128, 512))) == SHAPE
     assert rotary(q=tensor(out=P, os=(1024, 128))) == SHAPE  # in place with other strides
     assert rotary(tokens=0) == 0
 
