@@ -63,7 +63,7 @@ typedef enum tq_status {
     TQ_ERR_BITS = 3,      /* k_bits not in {2,4,5,8} or v_bits not in {2,3,4,5,8} */
     TQ_ERR_SHAPE = 4,     /* batch/heads/tokens/strides out of range */
     TQ_ERR_CAPACITY = 5,  /* rows beyond the cache capacity */
-    TQ_ERR_ALIGN = 6,     /* pointer or stride not aligned as the call requires (16 or 32 bytes) */
+    TQ_ERR_ALIGN = 6,     /* pointer or stride not aligned as the call requires (16 or 32 bytes, or an element) */
     TQ_ERR_WORKSPACE = 7, /* workspace missing or too small */
     TQ_ERR_CUDA = 8,      /* a CUDA launch or query failed */
     TQ_ERR_UNSUPPORTED = 9, /* valid codec parameters this kernel does not cover */
@@ -441,7 +441,8 @@ TQ_API tq_status tq_paged_tree_attention(const tq_cache *pool, const tq_page_tab
  *              this step (NULL: no starts are wanted), in [0, lens].
  *  lens_out    device int32 [num_seqs]: becomes lens; may be table->seq_lens (in
  *              place), or lens.
- *  starts      device int32 [num_seqs + 1] or NULL: running sums of new_tokens.
+ *  starts      device int32 [num_seqs + 1] or NULL: running sums of new_tokens; none of
+ *              the other tensors.
  *  free_pages  device int32 [free_capacity], read and written.
  *  free_count, free_count_out   device int32; may be the same (in place).
  * table->pages is written.  Where a value is out of range (TQ_DEVICE_ERR_LENGTH), or
@@ -467,6 +468,7 @@ TQ_API tq_status tq_page_table_update(const tq_cache *pool, const tq_page_table 
  *              follow one another, and there are no masks): the parent's index among the sequence's
  *              new tokens, below the token's own, -1 at a root; a parent out of
  *              range is taken for -1 and recorded (TQ_DEVICE_ERR_TREE).
+ * The outputs are none of the inputs, nor of each other.
  * With parents no sequence has more than max_new tokens (one that has is recorded as TQ_DEVICE_ERR_LENGTH).
  * A token behind the last sequence or of a sequence that was recorded has position and slot -1
  * and an empty mask; one that stands before its sequence's first row or in a bad page slot -1.

@@ -64,6 +64,13 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // the fetch and un-rotation kernels move 32-byte words
 bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
+// tensors of `size` bytes an element (a power of two), NULL ones too
+template <typename... P>
+bool aligned_to(uintptr_t size, const P *...x)
+{
+    return ((reinterpret_cast<uintptr_t>(x) | ...) & (size - 1)) == 0;
+}
+
 tq_status check_cache(const tq_cache *c)
 {
     if (!c) return TQ_ERR_NULL;
@@ -491,6 +498,7 @@ tq_status paged_attention(const tq_cache *c, const tq_page_table *t, const int32
     if (total == 0) return TQ_OK;
     if ((st = check_ragged(q, qs)) != TQ_OK) return st;
     if (tree && !masks) return TQ_ERR_NULL;
+    if (tree && (reinterpret_cast<uintptr_t>(masks) & 3) != 0) return TQ_ERR_ALIGN;
     if (tree && (mask_words < 1 || mask_words < ((max_new < total ? max_new : total) + 31) / 32)) return TQ_ERR_SHAPE;
     if (!out) return TQ_ERR_NULL;
     if (!aligned32(out)) return TQ_ERR_ALIGN;
@@ -545,6 +553,10 @@ tq_status tq_page_table_update(const tq_cache *c, const tq_page_table *t, const 
     if ((st = check_table(c, t)) != TQ_OK) return st;
     if (!lens || !lens_out || !free_pages || !free_count || !free_count_out || (starts && !new_tokens)) return TQ_ERR_NULL;
     if (free_capacity < 1 || free_capacity > INT32_MAX) return TQ_ERR_SHAPE;
+    if (!aligned_to(4, t->pages, t->seq_lens, lens, new_tokens, lens_out, starts, free_pages, free_count, free_count_out))
+        return TQ_ERR_ALIGN;
+    // written before the last of these is read
+    if (starts && (starts == lens || starts == new_tokens || starts == lens_out || starts == t->seq_lens)) return TQ_ERR_SHAPE;
     tq::PagedUpdate u{};
     u.pages = const_cast<int32_t *>(t->pages);
     u.lens = t->seq_lens;
@@ -576,6 +588,9 @@ tq_status tq_paged_layout(const tq_cache *c, const tq_page_table *t, const int32
     if (parents && max_new < 1) return TQ_ERR_SHAPE;
     const int64_t most = max_new < total ? max_new : total;
     if (masks && (mask_words < 1 || mask_words < (most + 31) / 32)) return TQ_ERR_SHAPE;
+    if (!aligned_to(4, t->pages, t->seq_lens, starts, parents, positions, masks) || !aligned_to(8, slots)) return TQ_ERR_ALIGN;
+    if (positions && (positions == parents || positions == masks)) return TQ_ERR_SHAPE;
+    if (masks && masks == parents) return TQ_ERR_SHAPE;  // (a token reads the parents of others)
     if (total == 0 || (!positions && !slots && !masks)) return TQ_OK;
     const tq::PagedView pv = paged_view(c, t, starts, total);
     if (!pv.err) return TQ_ERR_CUDA;
@@ -589,6 +604,7 @@ tq_status tq_paged_keep(const tq_cache *c, const tq_page_table *t, const int32_t
     tq_status st = check_paged(c, t, starts, total);
     if (st != TQ_OK) return st;
     if (!path || !kept || !lens_out) return TQ_ERR_NULL;
+    if (!aligned_to(4, t->pages, t->seq_lens, starts, path, kept, lens_out)) return TQ_ERR_ALIGN;
     if (lens_out == t->seq_lens || lens_out == kept) return TQ_ERR_SHAPE;  // (read by every CTA of a sequence, written by one)
     if (max_new < 1 || path_stride < max_new) return TQ_ERR_SHAPE;
     if ((int64_t)t->num_seqs * c->num_kv_heads > (int64_t(1) << 30)) return TQ_ERR_SHAPE;
@@ -610,7 +626,9 @@ tq_status tq_verify_drafts(const int32_t *starts, int32_t num_seqs, int64_t tota
     if (vocab < 1 || vocab > (int64_t(1) << 30)) return TQ_ERR_SHAPE;
     if (target_stride < vocab || (draft && draft_stride < vocab)) return TQ_ERR_SHAPE;
     const uintptr_t size = dt == TQ_F32 ? 4 : 2;
-    if ((reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft)) % size != 0) return TQ_ERR_ALIGN;
+    if (!aligned_to(size, static_cast<const char *>(target), static_cast<const char *>(draft))) return TQ_ERR_ALIGN;
+    if (!aligned_to(4, starts, parents, tokens, uniforms, last, path, kept, next)) return TQ_ERR_ALIGN;
+    if (kept == next || path == kept || path == next) return TQ_ERR_SHAPE;
     tq::VerifyCall v{starts, parents, tokens, total, max_new, vocab, num_seqs, target, draft, target_stride, draft_stride,
                      uniforms, last, path, kept, next, path_stride, dt == TQ_F32, tq::device_error_word()};
     if (!v.err) return TQ_ERR_CUDA;
@@ -627,6 +645,7 @@ tq_status tq_rotary(const int32_t *positions, int64_t tokens, int32_t head_dim, 
     if (dt != TQ_BF16 && dt != TQ_F32) return TQ_ERR_SHAPE;
     if (tokens == 0) return TQ_OK;  // (tensors without tokens may have no address)
     if (!positions || !freqs) return TQ_ERR_NULL;
+    if (!aligned_to(4, positions) || !aligned_to(8, freqs)) return TQ_ERR_ALIGN;
     tq::RotaryCall r{};
     const int64_t unit = dt == TQ_F32 ? 4 : 8;  // elements of 16 bytes
     const tq_rotary_tensor *in[2] = {q, k};

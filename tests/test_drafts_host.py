@@ -31,6 +31,7 @@ def test_tree_attention_refusals(tqlib):
     assert attend(heads=3) == SHAPE and attend(max_new=0) == SHAPE and attend(q=None) == NULL and attend(out=None) == NULL
     assert attend(q=P + 4) == ALIGN and attend(out=P + 8) == ALIGN and attend(qs=(512, 4)) == ALIGN
     assert attend(table=_table(tqlib, max_len=129)) == CAPACITY
+    assert attend(masks=2 * P + 2) == ALIGN
     assert attend(total=0) == 0
     size = L.tq_paged_tree_attention_workspace_bytes
     assert size(REF(pool), REF(table), 3, 4, 1) == 0 and size(REF(pool), REF(table), 4, 4, 0) == 0
@@ -51,6 +52,11 @@ def test_table_update_refusals(tqlib):
     assert update(cap=0) == SHAPE and update(cap=1 << 31) == SHAPE
     assert update(table=_table(tqlib, max_len=129)) == CAPACITY
     assert update(pool=_struct(tqlib, capacity=1 << 31)) == SHAPE
+    for name, at in dict(lens=P, new=2 * P, out=3 * P, starts=4 * P, stack=5 * P, count=6 * P, count_out=7 * P).items():
+        assert update(**{name: at + 2}) == ALIGN, name
+    assert update(table=_table(tqlib, pages=P + 1)) == ALIGN and update(table=_table(tqlib, seq_lens=2 * P + 2)) == ALIGN
+    for at in (P, 2 * P, 3 * P, table.seq_lens):  # what is read after the starts are written, or written over them
+        assert update(lens=P, new=2 * P, out=3 * P, starts=at) == SHAPE
 
 
 def test_layout_and_keep_refusals(tqlib):
@@ -64,6 +70,9 @@ def test_layout_and_keep_refusals(tqlib):
     assert layout(max_new=0) == SHAPE and layout(words=1) == SHAPE and layout(words=0, max_new=1) == SHAPE
     assert layout(total=0) == 0 and layout(pos=None, slots=None, masks=None) == 0
     assert layout(total=-1) == SHAPE
+    assert layout(parents=P + 2) == ALIGN and layout(pos=2 * P + 2) == ALIGN and layout(masks=4 * P + 2) == ALIGN
+    assert layout(slots=3 * P + 4) == ALIGN
+    assert layout(pos=P) == SHAPE and layout(masks=P) == SHAPE and layout(pos=4 * P) == SHAPE  # parents of others are read
 
     def keep(total=40, max_new=8, path=P, stride=8, kept=2 * P, out=3 * P):
         return L.tq_paged_keep(REF(pool), REF(table), 5 * P, total, max_new, path, stride, kept, out, None)
@@ -72,6 +81,7 @@ def test_layout_and_keep_refusals(tqlib):
     assert keep(max_new=0) == SHAPE and keep(stride=7) == SHAPE
     assert keep(out=table.seq_lens) == SHAPE  # the table's own lengths
     assert keep(out=2 * P) == SHAPE  # the counts
+    assert keep(path=P + 2) == ALIGN and keep(kept=2 * P + 1) == ALIGN and keep(out=3 * P + 2) == ALIGN
 
 
 def test_verify_refusals(tqlib):
@@ -91,6 +101,9 @@ def test_verify_refusals(tqlib):
     assert verify(ts=99) == SHAPE and verify(ds=99) == SHAPE
     assert verify(target=4 * P + 2) == ALIGN and verify(draft=5 * P + 2) == ALIGN
     assert verify(target=4 * P + 1, dt=0) == ALIGN
+    for name, at in dict(starts=P, parents=2 * P, tokens=3 * P, u=6 * P, last=7 * P, path=8 * P, kept=9 * P, nxt=10 * P).items():
+        assert verify(**{name: at + 2}) == ALIGN, name
+    assert verify(kept=10 * P) == SHAPE and verify(path=9 * P) == SHAPE and verify(path=10 * P) == SHAPE
 
 
 def test_rotary_refusals(tqlib):
@@ -114,6 +127,7 @@ def test_rotary_refusals(tqlib):
     assert rotary(q=tensor(os=(256, 128))) == SHAPE and rotary(q=tensor(os=(128, 512))) == SHAPE
     assert rotary(q=tensor(out=P, os=(1024, 128))) == SHAPE  # in place with other strides
     assert rotary(tokens=0) == 0
+    assert rotary(pos=3 * P + 2) == ALIGN and rotary(freqs=4 * P + 4) == ALIGN
 
 
 def test_codes_match_the_header(tqlib):
