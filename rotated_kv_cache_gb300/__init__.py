@@ -704,7 +704,7 @@ def tq_paged_layout(pool: Cache, table: PageTable, starts: torch.Tensor, total: 
                     masks: torch.Tensor | None = None, want_positions: bool = True, want_slots: bool = True,
                     want_masks: bool = True, stream=None):
     """(positions int32 [total], slots int64 [total], masks int32 [total][ceil(max_new / 32)]) of the new tokens; with
-    parents (int32 [total], -1 at a root) positions go by the depth in a sequence's tree, without them masks is None."""
+    parents (int32, total of them at least, -1 at a root) positions go by the depth in a sequence's tree, without them masks is None."""
     total = int(total)
     most = words = 0
     if parents is None:
@@ -716,6 +716,8 @@ def tq_paged_layout(pool: Cache, table: PageTable, starts: torch.Tensor, total: 
         most = int(max_new)
         words = masks.shape[1] if masks is not None and masks.dim() == 2 else max(1, (most + 31) // 32)
     s, t = _paged_check(pool, table, starts, parents, positions, slots, masks)
+    if parents is not None and (parents.dim() != 1 or parents.shape[0] < total):
+        raise ValueError("parents must be contiguous int32 [total] (or more)")
     dev = starts.device
     if not want_positions:
         positions = None
@@ -731,7 +733,7 @@ def tq_paged_layout(pool: Cache, table: PageTable, starts: torch.Tensor, total: 
         masks = None
     elif masks is None:
         masks = _empty_on(stream, (total, words), torch.int32, dev)
-    _check(lib().tq_paged_layout(s, t, starts.data_ptr(), total, _i32(parents, (total,), "parents"), most,
+    _check(lib().tq_paged_layout(s, t, starts.data_ptr(), total, None if parents is None else _i32(parents, parents.shape, "parents"), most,
                                  _i32(positions, (total,), "positions"), None if slots is None else slots.data_ptr(),
                                  _i32(masks, (total, words), "masks"), words, _stream(stream)), "tq_paged_layout")
     return positions, slots, masks

@@ -351,6 +351,25 @@ def test_layout_of_starts_out_of_order(cuda):
         assert pos[:100].tolist() == list(range(40, 50)) * 10 and masks[:100, 0].tolist() == [2 ** (i + 1) - 1 for i in range(10)] * 10
 
 
+def test_layout_of_fewer_tokens_than_parents(cuda):
+    """Parents kept for the largest batch: the first `total` count, none of them too; a shorter tensor is refused."""
+    pool = cuda.Cache(8, 1, 64, 16, k_bits=2, v_bits=2)
+    table = cuda.PageTable(dev(np.arange(8).reshape(2, 4)), dev([20, 9]), 64)
+    parents = dev([-1, 0, 0, -1, 0, 7, 7, 7])
+    pos, slots, masks = cuda.tq_paged_layout(pool, table, dev([0, 3, 5]), 5, parents=parents, max_new=3)
+    assert pos.tolist() == [17, 18, 18, 7, 8] and slots.tolist() == [17, 18, 19, 71, 72] and masks.tolist() == [[1], [3], [5], [1], [3]]
+    for few in (parents, parents[:0]):
+        pos, slots, masks = cuda.tq_paged_layout(pool, table, dev([0, 0, 0]), 0, parents=few, max_new=3)
+        assert pos.shape == (0,) and slots.shape == (0,) and masks.shape == (0, 1)
+    assert cuda.tq_device_error() == 0
+    with pytest.raises(ValueError):
+        cuda.tq_paged_layout(pool, table, dev([0, 3, 5]), 5, parents=parents[:4], max_new=3)
+    with pytest.raises(ValueError):
+        cuda.tq_paged_layout(pool, table, dev([0, 3, 5]), 5, parents=parents[::2][:4], max_new=3)
+    with pytest.raises(ValueError):
+        cuda.tq_paged_layout(pool, table, dev([0, 3, 5]), 4, parents=parents.long(), max_new=3)
+
+
 # ------------------------------------------------------------------ rotary
 # Bounds: sine and cosine within 2 steps of 2^-24 (what the part left out adds one rounding), the scale and the
 # two products and their sum one each: 6 steps of 2^-24 of (|a| + |b|) scale; then one rounding of the type.
