@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from pagedtest import ATOL, RTOL, Batch, dequantised
+from pagedtest import ATOL, RTOL, Batch, dequantised, rows_of
 from test_drafts_gpu import check_tree, dev, pack, tree_masks
 
 pytestmark = pytest.mark.gpu
@@ -191,3 +191,64 @@ def test_negative_scale_and_two_streams(cuda):
     torch.cuda.synchronize()
     assert all(torch.equal(x, out) for x in outs)
     assert cuda.tq_device_error() == 0
+
+
+@pytest.mark.parametrize("d,kb,vb,G,new", [(128, 8, 3, 8, 5), (128, 8, 3, 8, 50), (64, 4, 3, 4, 7), (256, 8, 4, 4, 20), (128, 5, 5, 8, 9),
+                                           (512, 8, 3, 2, 6)])
+@pytest.mark.parametrize("bound", [None, BOUND])
+def test_a_workspace_may_hold_anything(cuda, d, kb, vb, G, new, bound):
+    """NaN in all of it, then what another call left there: the same output, with sequences of no rows, of no new
+    tokens, and tokens that see nothing, whose partial sums count for nothing."""
+    lens = [new, 0, 700, 40 + new, 129, 1500]
+    b = Batch(lens, [new, 0, new // 2, 1, 0, new], H=2, d=d, kb=kb, vb=vb, page=64, seed=d, width=-(-BOUND // 64))
+    seen = tree_masks(b, "any")
+    words = -(-new // 32)
+    masks = dev(np.concatenate([pack(np.pad(m, ((0, 0), (0, 32 * words - m.shape[1]))), words) for m in seen]))
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    pages, q = b.pages(cuda, max_len=bound), b.queries(2 * G)
+    need = cuda.tq_paged_tree_attention_workspace_bytes(pool, pages, 2 * G, b.total, new)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    outs = [cuda.tq_paged_tree_attention(pool, pages, b.dev(b.starts), q.cuda(), masks, new, workspace=ws) for _ in range(2)]
+    assert cuda.tq_device_error() == 0 and torch.equal(*outs)
+    check_tree(b, pool, q, outs[0], seen)
+
+
+@pytest.mark.parametrize("d,kb,vb,H,page,rows", [(128, 8, 3, 2, 64, 1 << 26), (64, 4, 2, 1, 16, (1 << 31) + 4096)])
+def test_trees_far_into_a_large_pool(cuda, d, kb, vb, H, page, rows):
+    """Planes of more than 2^32 bytes, and a pool of more than 2^31 rows: trees on every kernel, slots and kept rows at
+    its last pages."""
+    per_row = d * kb // 8 + d * vb // 8 + 3 * (d // 32) * 2
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < rows * per_row + (8 << 30):
+        pytest.skip("not enough device memory")
+    lens, width, G = [300, 17, 0, 200, 64], -(-BOUND // page), 8
+    pages = rows // (H * page)
+    pool = cuda.Cache(pages, H, d, page, k_bits=kb, v_bits=vb)
+    for new, bound in (([2, 1, 0, 1, 2], 320), ([8, 17, 0, 3, 5], BOUND), ([60, 1, 0, 33, 64], BOUND)):  # split, block, wide
+        b = Batch(lens, new, H=H, d=d, kb=kb, vb=vb, page=page, seed=13, spare=0, width=width)
+        b.table = b.table + (pages - b.num_pages)
+        b.fill(cuda, pool)
+        seen = tree_masks(b, "tree")
+        words = -(-max(new) // 32)
+        masks = dev(np.concatenate([pack(np.pad(m, ((0, 0), (0, 32 * words - m.shape[1]))), words) for m in seen]))
+        table, q = b.pages(cuda, max_len=bound), b.queries(H * G)
+        out = cuda.tq_paged_tree_attention(pool, table, b.dev(b.starts), q.cuda(), masks, max(new))
+        check_tree(b, pool, q, out, seen)
+        _, slots, _ = cuda.tq_paged_layout(pool, table, b.dev(b.starts), b.total)
+        at = [int(b.table[s, r // page]) * page + r % page for s, n in enumerate(lens) for r in range(n - new[s], n)]
+        assert slots.tolist() == at
+        before = [rows_of(pool, b.table[s], n) for s, n in enumerate(lens)]
+        path = [list(range(0, n, 2)) for n in new]
+        ids = np.full((5, max(new)), -1, np.int32)
+        for s, x in enumerate(path):
+            ids[s, :len(x)] = x
+        cuda.tq_paged_keep(pool, table, b.dev(b.starts), dev(ids), dev([len(x) for x in path]))
+        for s, (n, x) in enumerate(zip(lens, path)):
+            for got, was in zip(rows_of(pool, b.table[s], n), before[s]):
+                want = was.copy()
+                want[:, n - new[s]:n - new[s] + len(x)] = was[:, [n - new[s] + i for i in x]]
+                assert np.array_equal(got, want), s
+    assert cuda.tq_device_error() == 0
+    del pool
+    torch.cuda.empty_cache()
