@@ -29,7 +29,8 @@
 // cluster's barriers for few.
 //
 // 16 chains of 5 nodes, 32000 tokens, with draft probabilities: 12.7 us; 64 trees of 8
-// to 32 nodes, 131072 tokens, without: 24.4 us (1.4 TB/s).  With 64-bit sums by every
+// to 32 nodes, 131072 tokens, without: 20.7 us (1.6 TB/s; 24.4 with a node's children
+// looked up one after another).  With 64-bit sums by every
 // thread of the deciding CTA and 32 KB runs searched element by element they took 32
 // and 76; without the template for drafts, whose registers halve what is under way,
 // 12.7 and 31.  Clusters of 4: 15 and 34; 512 threads: 23 and 85 (fewer CTAs fit).
@@ -415,41 +416,59 @@ __global__ void __launch_bounds__(vfThreads, 4) verify_kernel(const __grid_const
     };
     double sum = 0.0;
     if (n > 0 && lane == 0) path[0] = 0;
+    auto accept = [&](int j) {
+        if (lane == 0) path[kept] = j;
+        ++kept;
+        cur = j;
+        C = 0.0;
+        mass = 1.0;
+        crossed = 0;
+        summed = false;
+    };
     for (int j0 = 0; j0 < n; j0 += 32) {
-        int from = j0 == 0 ? 1 : j0;  // nodes before it are done
-        for (;;) {
-            const int at = j0 + lane;
-            const uint32_t kids = __ballot_sync(0xffffffffu, at >= from && at < n && parent[at < n ? at : 0] == cur);
-            if (kids == 0) break;
-            const int j = j0 + __ffs(kids) - 1;
-            from = j + 1;
-            const double u = num[j], rj = rr[j];
-            double here = (double)pp[j] - C * rj;
-            if (!DRAFT) {
-                here = pp[j];
-                for (int i = lane; i < crossed; i += 32)
-                    if (gone[i] == token[j]) here = 0.0;
-                if (__any_sync(0xffffffffu, here == 0.0)) here = 0.0;
+        const int at = j0 + lane, up = at < n ? parent[at] : -1;  // (no node's children: -1)
+        uint32_t later = 0xffffffffu;                             // nodes behind the last one tried
+        if constexpr (DRAFT) {
+            for (;;) {
+                const uint32_t kids = __ballot_sync(0xffffffffu, up == cur) & later;
+                if (kids == 0) break;
+                const int j = j0 + __ffs(kids) - 1;
+                later = 0xfffffffeu << (j - j0);
+                const double u = num[j], rj = rr[j], here = (double)pp[j] - C * rj;
+                if (u * rj * mass < (here > 0.0 ? here : 0.0)) {
+                    accept(j);
+                } else {
+                    C += mass;
+                    sum = mass = total(s0 + cur);
+                    summed = true;
+                }
             }
-            here = here > 0.0 ? here : 0.0;
-            if (u * rj * mass < here) {
-                if (lane == 0) path[kept] = j;
-                ++kept;
-                cur = j;
-                C = 0.0;
-                mass = 1.0;
-                crossed = 0;
-                summed = false;
-            } else if (DRAFT) {
-                C += mass;
-                sum = mass = total(s0 + cur);
-                summed = true;
-            } else if (here > 0.0) {
-                mass -= here;
-                if (lane == 0) gone[crossed] = token[j];
-                ++crossed;
-                __syncwarp();
+        } else {
+            // Only tokens with a probability that no earlier child had can be accepted or crossed out: each lane
+            // finds out for its own node, and what is left of the walk is a product and a difference a child.
+            const int x = up >= 0 ? token[at] : -1;
+            const double u = up >= 0 ? num[at] : 0.0f, here = up >= 0 ? pp[at] : 0.0f;
+            bool again = (__match_any_sync(0xffffffffu, up) & __match_any_sync(0xffffffffu, x) & ((1u << lane) - 1)) != 0;
+            for (int i = 0; i < crossed; ++i) again |= up == cur && gone[i] == x;
+            for (;;) {
+                uint32_t kids = __ballot_sync(0xffffffffu, up == cur && here > 0.0 && !again) & later;
+                int j = -1;
+                for (; kids; kids &= kids - 1) {
+                    const int l = __ffs(kids) - 1;
+                    const double p = __shfl_sync(0xffffffffu, here, l);
+                    if (__shfl_sync(0xffffffffu, u, l) * mass < p) {
+                        j = l;
+                        break;
+                    }
+                    mass -= p;
+                    if (lane == l) gone[crossed] = x;
+                    ++crossed;
+                }
+                if (j < 0) break;
+                accept(j0 + j);
+                later = 0xfffffffeu << j;
             }
+            __syncwarp();  // (the next nodes' lanes read what is crossed out)
         }
     }
     int64_t next = -1;
