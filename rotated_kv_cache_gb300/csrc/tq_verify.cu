@@ -21,7 +21,7 @@
 // long as 32-bit ones; they are left for the few numbers of a sequence.
 //
 // A cluster of CTAs goes through a row, a run of elements per warp, a run in up to
-// eight pieces with a sum each, so that the one that holds the drawn token is short.
+// four pieces with a sum each, so that the one that holds the drawn token is short.
 // The first warp of the first CTA alone reads the tree and decides; all the others are told what
 // to sum, so that no two of them can disagree on how often they meet.  A pass moves
 // the row once: bound by memory for many sequences, by the latency of four
@@ -34,6 +34,8 @@
 // thread of the deciding CTA and 32 KB runs searched element by element they took 32
 // and 76; without the template for drafts, whose registers halve what is under way,
 // 12.7 and 31.  Clusters of 4: 15 and 34; 512 threads: 23 and 85 (fewer CTAs fit).
+// 64 chains with draft probabilities, 131072 tokens: 37.5 us (39.9 with eight pieces; a run's lines
+// called to L2 ahead of its loads 43: the arithmetic of pairs bounds it).
 #include "tq_common.cuh"
 #include "tq_kernels.h"
 #include "tq_paged.cuh"
@@ -43,7 +45,7 @@ namespace {
 
 constexpr int vfThreads = 256, vfWarps = vfThreads / 32;
 constexpr int vfCluster = 8, vfRuns = vfWarps * vfCluster;  // warps to a sequence
-constexpr int vfPieces = 8;                                 // of a run, at most
+constexpr int vfPieces = 4;                                 // of a run, at most
 
 struct VerifyParams {
     VerifyCall c;
