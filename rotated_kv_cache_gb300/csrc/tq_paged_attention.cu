@@ -287,6 +287,7 @@ constexpr int64_t kWideWork = int64_t(1) << 22;  // rows x kv-heads x columns, b
 //               16 x 4352         384     222             298
 //                                 512     292             302
 //                                1024     558 (4-bit keys) 427
+// (16 ragged sequences of 500 to 8192 rows, 320 to 512 columns, 4-bit keys: 320 and 264.)
 //       64       4 x 8192          24      30.0    32.2
 //               16 x 4352         384     175             188
 //                                 512     231             187
