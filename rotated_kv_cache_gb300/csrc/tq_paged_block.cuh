@@ -138,18 +138,23 @@ __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((u
 __device__ __forceinline__ uint32_t b_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 __device__ __forceinline__ __half2 b_half2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
 
-// The packed codes and scales of a (row, group of 32 dims) item.  Widths that have
-// no fast path (0) are read where they are converted.
+// The packed codes and scales of a (row, group of 32 dims) item.
 template <int KB, int VB>
 struct BlockItem {
-    uint32_t k[KB ? KB : 1], v[VB ? VB : 1];
+    uint32_t k[KB], v[VB];
     uint16_t s, z, r;  // key scale and zero, value rms
-    int64_t row;      // plane row, -1: none (zeros)
+};
+
+// Of widths that have no fast path (0): the codes are read where they are converted.
+template <>
+struct BlockItem<0, 0> {
+    uint16_t s, z, r;
+    int64_t row;  // plane row, -1: none (zeros)
 };
 
 // An item's scales from memory, of widths whose codes are read where they are converted.
-template <int D, int KB, int VB>
-__device__ __forceinline__ void load_item(const BlockParams &p, int64_t row, int g, BlockItem<KB, VB> &x)
+template <int D>
+__device__ __forceinline__ void load_item(const BlockParams &p, int64_t row, int g, BlockItem<0, 0> &x)
 {
     constexpr int NG = D / 32;
     x.row = row;
@@ -194,7 +199,6 @@ __device__ __forceinline__ void read_item(uint32_t raw, int r, int g, bool live,
     x.z = b_lds16(m + W::OFF_KZ);
     x.r = b_lds16(m + W::OFF_VS);
     if (!live) x.s = x.z = x.r = 0;
-    x.row = live ? 0 : -1;
 }
 
 // Eight key codes of an item, from code 8 c on, as f16 pairs 1024 + (offset) code.
@@ -296,14 +300,28 @@ __device__ __forceinline__ void convert_keys(const BlockParams &p, const BlockIt
         }
     } else {
         const float magic = p.kb == 8 ? 8388736.0f : 8388608.0f;
+        [[maybe_unused]] uint32_t k[KB ? KB : 1];
+        if constexpr (KB != 0)
+#pragma unroll
+            for (int i = 0; i < KB; ++i) k[i] = x.k[i];
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-            uint32_t w0 = 0u, w1 = 0u, hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
-            int sh = 0;
-            if (x.row >= 0) {
+            uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+            bool live = true;  // (scales of a row behind the last are 0: on the fast path)
+            if constexpr (KB == 0) live = x.row >= 0;
+            if (live) {
                 float f[8];
-                code_window(p.k_codes + x.row * (D * p.kb / 8) + g * (4 * p.kb), p.kb, c, w0, w1, sh);
-                key_values<0>(w0, w1, sh, p.kb, s, magic - z, f);
+                if constexpr (KB != 0) {
+                    // codes 8 c .. 8 c + 7 stand in the first words, the others move up (indexed by c they would not stay in registers)
+                    key_values<KB>(k[0], k[KB == 8 ? 1 : 0], 0, KB, s, magic - z, f);
+#pragma unroll
+                    for (int i = 0; i + KB / 4 < KB; ++i) k[i] = k[i + KB / 4];
+                } else {
+                    uint32_t w0, w1;
+                    int sh;
+                    code_window(p.k_codes + x.row * (D * p.kb / 8) + g * (4 * p.kb), p.kb, c, w0, w1, sh);
+                    key_values<0>(w0, w1, sh, p.kb, s, magic - z, f);
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     hi[i] = tc_pack_f16(f[2 * i], f[2 * i + 1]);
@@ -450,7 +468,7 @@ __global__ void __launch_bounds__(nThreads, 1) paged_block_kernel(const __grid_c
                             if ((uint32_t)pg < (uint32_t)p.pg.v.num_pages) row = ((int64_t)pg * p.H + seg.h) * p.pg.v.page + (pos - i * p.pg.v.page);
                             else atomicOr(p.err, kErrPage);
                         }
-                        load_item<D, KB, VB>(p, row, item_group(j), cur[j]);
+                        load_item<D>(p, row, item_group(j), cur[j]);
                     }
                 }
                 // bounds of the tile's finite groups: largest, and smallest of those that are not zero
@@ -852,8 +870,7 @@ auto block_widths(const CacheView &c, F &&f)
     auto with = [&](auto kb) {
         return c.vb == 3   ? f(kb, integral_constant<int, 3>{})
                : c.vb == 4 ? f(kb, integral_constant<int, 4>{})
-               : c.vb == 2 ? f(kb, integral_constant<int, 2>{})
-                           : f(kb, integral_constant<int, 0>{});
+                           : f(kb, integral_constant<int, 2>{});
     };
     // other widths of either by run-time shifts, of both then
     if (c.vb > 4 || (c.kb != 8 && c.kb != 4)) return f(integral_constant<int, 0>{}, integral_constant<int, 0>{});
