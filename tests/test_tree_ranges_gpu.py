@@ -81,3 +81,79 @@ def test_keys_with_an_offset(cuda, d, vb, G, new, kb, offset):
         assert float((z > 896).float().mean()) > 0.25
     check_numbers(b, pool, q, out, seen, lost=d / 16 * 2.0 ** -20)
     assert cuda.tq_device_error() == 0
+
+
+@pytest.mark.parametrize("d,kb,vb,G,new", [(128, 8, 3, 8, 9), (128, 4, 3, 8, 16), (128, 8, 3, 8, 4), (64, 8, 4, 8, 9), (256, 8, 3, 4, 20),
+                                           (128, 2, 5, 8, 9), (256, 4, 2, 4, 4)])
+def test_far_outliers(cuda, d, kb, vb, G, new):
+    """Rows with keys of up to 2^20 (what a half-precision scale of their width holds) that all queries point away from: no
+    weight of theirs is left, and the other rows of their tile keep their precision; rows with values of 2^-14 beside
+    them, and groups far from zero."""
+    b = batch([new + 400, 200], [new, new], d, kb, vb, 64, seed=9)
+    rng = np.random.default_rng(17)
+    way = np.where(np.arange(d) % 2, 1.0, -1.0).astype(np.float32)
+    q = b.queries(2 * G).float()
+    q = q + torch.from_numpy(way) * (4.0 - (q * torch.from_numpy(way)).mean(-1, keepdim=True))
+    q = q.to(torch.bfloat16)
+    top = {8: 20, 4: 18, 2: 16}[kb]
+    for s in range(2):
+        for t, size in ((3, 2.0 ** top), (64, 2.0 ** 14), (150, 2.0 ** (top - 2))):
+            b.k[s][t] = (torch.from_numpy(-size * way) * torch.from_numpy(1 + 0.25 * rng.random((2, 1), np.float32))).to(torch.bfloat16)
+        b.v[s][8:16] = b.v[s][8:16] * 2.0 ** -14
+        b.k[s][20:24, :, 32:64] = torch.from_numpy(2.0 + 2.0 ** -4 * rng.random((4, 2, 32), np.float32)).to(torch.bfloat16)
+    seen = tree_masks(b, "tree")
+    pool, _, out = attend(cuda, b, 2 * G, seen, q=q)
+    if kb == 8:
+        z = zeros_of(b, pool, 0, 1).abs()
+        assert bool((z[20:24] > 896).all()) and bool((z[30:60] < 896).all())
+    check_numbers(b, pool, q, out, seen)
+    assert cuda.tq_device_error() == 0
+
+
+@pytest.mark.parametrize("power", [0, 26, 116])
+@pytest.mark.parametrize("d,kb,G,new", [(128, 8, 8, 3), (128, 8, 8, 6), (128, 8, 8, 9), (128, 4, 8, 40), (64, 4, 8, 3), (64, 8, 8, 9),
+                                        (256, 8, 4, 9), (256, 4, 4, 20), (128, 5, 8, 8)])
+def test_queries_of_any_size(cuda, d, kb, G, new, power):
+    """Finite scores of any size: where they differ by more than what fp32 leaves of them, the rows of the largest share
+    the weight.  (Keys of one of three sizes in the queries' group, so that scores are equal or far apart; a negative
+    query's largest score is the smallest key's.)"""
+    b = batch([400, 90], [new, new], d, kb, 3, 64, seed=4)
+    sign = torch.where(torch.arange(d) % 2 == 0, 1.0, -1.0)
+    for s in range(2):
+        size = torch.ones(len(b.k[s]), 2, d)
+        size[:, :, :32] = 1.0 + (torch.arange(len(b.k[s])) % 3)[:, None, None]
+        b.k[s] = (size * sign).to(torch.bfloat16)
+    q = torch.zeros(2 * new, 2 * G, d)
+    q[:, :, :32] = 4.0 * sign[:32]
+    q[:, 1::2] = -q[:, 1::2]
+    q = (q * 2.0 ** power).to(torch.bfloat16)
+    seen = tree_masks(b, "tree")
+    pool, _, out = attend(cuda, b, 2 * G, seen, q=q)
+    assert cuda.tq_device_error() == 0
+    check_numbers(b, pool, q, out, seen)
+
+
+@pytest.mark.parametrize("d,kb,vb,G,new,bound", [
+    (128, 8, 3, 8, 2, 64), (128, 5, 5, 3, 6, 64), (512, 8, 3, 2, 6, 64), (128, 8, 3, 8, 5, 1 << 14), (128, 4, 3, 8, 33, 1 << 14),
+    (64, 8, 4, 8, 9, 1 << 14), (256, 8, 4, 4, 40, 1 << 14), (128, 5, 5, 8, 12, 1 << 14), (128, 8, 3, 8, 60, 1 << 14), (64, 4, 2, 16, 40, 1 << 14)])
+def test_more_new_tokens_than_rows(cuda, d, kb, vb, G, new, bound):
+    """Lengths below the number of new tokens, on every kernel: those in front stand before the first row, tokens see of
+    the rows that are there what their masks name."""
+    lens = [1, new // 2 + 1, max(1, new - 1), new, new + 1, 0]
+    b = batch(lens, [new] * 5 + [0], d, kb, vb, 16)
+    seen = tree_masks(b, "any")
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    words = -(-new // 32)
+    masks = np.zeros((b.total, words), np.uint32)
+    at = 0
+    for m in seen:
+        for row in m:
+            for j in np.flatnonzero(row):
+                masks[at, j // 32] |= np.uint32(1) << np.uint32(j % 32)
+            at += 1
+    q = b.queries(2 * G)
+    out = cuda.tq_paged_tree_attention(pool, b.pages(cuda, max_len=bound), b.dev(b.starts), q.cuda(),
+                                       torch.from_numpy(masks.view(np.int32)).cuda(), new)
+    assert cuda.tq_device_error() == 0
+    check_numbers(b, pool, q, out, seen)
