@@ -452,6 +452,7 @@ __global__ void __launch_bounds__(vfThreads, 4) verify_kernel(const __grid_const
             const double u = up >= 0 ? num[at] : 0.0f, here = up >= 0 ? pp[at] : 0.0f;
             bool again = (__match_any_sync(0xffffffffu, up) & __match_any_sync(0xffffffffu, x) & ((1u << lane) - 1)) != 0;
             for (int i = 0; i < crossed; ++i) again |= up == cur && gone[i] == x;
+            __syncwarp();  // (from here on gone is written)
             for (;;) {
                 uint32_t kids = __ballot_sync(0xffffffffu, up == cur && here > 0.0 && !again) & later;
                 int j = -1;
@@ -469,6 +470,7 @@ __global__ void __launch_bounds__(vfThreads, 4) verify_kernel(const __grid_const
                 if (j < 0) break;
                 accept(j0 + j);
                 later = 0xfffffffeu << j;
+                __syncwarp();  // (what was crossed out before is written over by other lanes)
             }
             __syncwarp();  // (the next nodes' lanes read what is crossed out)
         }
