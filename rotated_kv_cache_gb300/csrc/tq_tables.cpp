@@ -149,7 +149,8 @@ void rotary_frequencies(int rot, double base, int scaling, double factor, int64_
         freqs[i] = w;
         if (scaling == 1) freqs[i] = w / factor;
         if (scaling == 3) {
-            const double ramp = std::min(std::max((i - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
+            // (hi at 0 or below: the first pair already turns less than `slow` times, and so do all)
+            const double ramp = hi <= 0.0 ? 1.0 : std::min(std::max((i - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
             freqs[i] = w / factor * ramp + w * (1.0 - ramp);
         }
     }

@@ -168,6 +168,14 @@ def test_rotary_frequencies(tqlib, rot, base, factor, original, scaling):
         assert got[0] == plain[0] and abs(got[-1] * factor / plain[-1] - 1) < 1e-13
 
 
+@pytest.mark.parametrize("original,fast,slow", [(4, 32.0, 1.0), (1, 1.0, 1.0), (4096, 3000.0, 2000.0), (6, 2.0, 1.0)])
+def test_yarn_of_pairs_that_all_turn_too_little(tqlib, original, fast, slow):
+    """The first pair turns original / (2 pi) times; where that is below `slow` every pair is divided by the factor."""
+    assert original / (2 * np.pi) < slow
+    got, _ = tqlib.tq_rotary_frequencies(64, 1e4, "yarn", 8.0, original, fast, slow)
+    np.testing.assert_allclose(got, 1e4 ** (-2.0 * np.arange(32) / 64) / 8.0, rtol=1e-14)
+
+
 def test_rotary_frequency_refusals(tqlib):
     bad = lambda *a, **k: pytest.raises((ValueError, tqlib.TQError))  # noqa: E731
     for args in ((3,), (0,), (514,), (64, 1.0), (64, float("nan")), (64, float("inf"))):
