@@ -441,10 +441,11 @@ TQ_API tq_status tq_paged_tree_attention(const tq_cache *pool, const tq_page_tab
  *              this step (NULL: no starts are wanted), in [0, lens].
  *  lens_out    device int32 [num_seqs]: becomes lens; may be table->seq_lens (in
  *              place), or lens.
- *  starts      device int32 [num_seqs + 1] or NULL: running sums of new_tokens; none of
- *              the other tensors.
+ *  starts      device int32 [num_seqs + 1] or NULL: running sums of new_tokens.
  *  free_pages  device int32 [free_capacity], read and written.
  *  free_count, free_count_out   device int32; may be the same (in place).
+ * But for these the outputs share no memory with an input or with one another
+ * (TQ_ERR_SHAPE).
  * table->pages is written.  Where a value is out of range (TQ_DEVICE_ERR_LENGTH), or
  * the pool has fewer pages than are lacking, or the stack no room for those given back
  * or a count out of range (TQ_DEVICE_ERR_FULL), nothing changes: lens_out becomes the
@@ -468,7 +469,7 @@ TQ_API tq_status tq_page_table_update(const tq_cache *pool, const tq_page_table 
  *              follow one another, and there are no masks): the parent's index among the sequence's
  *              new tokens, below the token's own, -1 at a root; a parent out of
  *              range is taken for -1 and recorded (TQ_DEVICE_ERR_TREE).
- * The outputs are none of the inputs, nor of each other.
+ * The outputs share no memory with the inputs, nor with each other (TQ_ERR_SHAPE).
  * With parents no sequence has more than max_new tokens (one that has is recorded as TQ_DEVICE_ERR_LENGTH).
  * A token behind the last sequence or of a sequence that was recorded has position and slot -1
  * and an empty mask; one that stands before its sequence's first row or in a bad page slot -1.
@@ -486,7 +487,7 @@ TQ_API tq_status tq_paged_layout(const tq_cache *pool, const tq_page_table *tabl
  *            <= path_stride.  A sequence where that does not hold keeps its rows and
  *            its length (TQ_DEVICE_ERR_TREE).
  *  lens_out  device int32 [num_seqs], not table->seq_lens (tq_page_table_update takes it
- *            as lens, gives back the pages that are left over and sets the table's).
+ *            as lens, gives back the pages that are left over and sets the table's) nor another input.
  * Sequences must not share pages that hold moved rows.
  */
 TQ_API tq_status tq_paged_keep(const tq_cache *pool, const tq_page_table *table, const int32_t *starts, int64_t total,
@@ -523,6 +524,7 @@ TQ_API tq_status tq_paged_keep(const tq_cache *pool, const tq_page_table *table,
  *  path      device int32 [num_seqs][path_stride]: the accepted nodes, node 0 first,
  *            then -1 up to max_new; kept [num_seqs] their number; next [num_seqs] the next
  *            token (vocab where nothing is left).  A sequence without tokens: 0 kept, next -1.
+ * The outputs share no memory with the inputs, nor with each other (TQ_ERR_SHAPE).
  * max_new <= TQ_MAX_DRAFT, max_new <= path_stride; a sequence of more tokens, or starts out of
  * range, counts as one without (TQ_DEVICE_ERR_LENGTH).  Sums are kept to about 2^-45,
  * products and comparisons in 64 bits.
@@ -536,7 +538,8 @@ TQ_API tq_status tq_verify_drafts(const int32_t *starts, int32_t num_seqs, int64
 /* Queries or keys of ragged tokens, [token][head][head_dim] with head_dim contiguous. */
 typedef struct tq_rotary_tensor {
     const void *x;           /* device, 16-byte aligned */
-    void *out;               /* device, 16-byte aligned; x (in place, with the same strides) or disjoint from it */
+    void *out;               /* device, 16-byte aligned; x (in place, with the same strides) or disjoint from it; disjoint from the
+                                other tensor's x and out */
     int64_t x_strides[2];    /* between tokens and heads, in elements; multiples of 16 bytes */
     int64_t out_strides[2];
     int32_t heads;           /* >= 1 */

@@ -4,6 +4,7 @@
 // excepted, which is documented to synchronise).
 #include <cuda_runtime.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/tq.h"
@@ -69,6 +70,29 @@ template <typename... P>
 bool aligned_to(uintptr_t size, const P *...x)
 {
     return ((reinterpret_cast<uintptr_t>(x) | ...) & (size - 1)) == 0;
+}
+
+// The memory of a tensor: `rows` rows of `n` elements, `stride` elements apart (no tensor, or none of its elements: empty).
+struct Span {
+    uintptr_t at;
+    uint64_t bytes;
+};
+
+template <typename T>
+Span span(const T *x, int64_t n, int64_t rows = 1, int64_t stride = 0)
+{
+    if (!x || rows < 1 || n < 1) return Span{0, 0};
+    constexpr int64_t kMost = int64_t(1) << 56;  // above any memory
+    const int64_t all = rows > 1 && stride > kMost / rows ? kMost : (rows - 1) * stride + n;
+    return Span{reinterpret_cast<uintptr_t>(x), (uint64_t)all * sizeof(T)};
+}
+
+// An output that shares no memory with any of the others.
+bool apart(const Span &a, std::initializer_list<Span> others)
+{
+    for (const Span &b : others)
+        if (a.bytes && b.bytes && a.at < b.at + b.bytes && b.at < a.at + a.bytes) return false;
+    return true;
 }
 
 tq_status check_cache(const tq_cache *c)
@@ -429,6 +453,12 @@ tq_status check_paged_attention(const tq_cache *c, const tq_page_table *t, int32
     return (int64_t)t->num_seqs * c->num_kv_heads > (int64_t(1) << 30) ? TQ_ERR_SHAPE : TQ_OK;
 }
 
+// the table's rows, as far as they are read
+Span table_span(const tq_cache *c, const tq_page_table *t)
+{
+    return span(t->pages, (t->max_len + c->capacity - 1) / c->capacity, t->num_seqs, t->stride);
+}
+
 tq::PagedBounds paged_bounds(const tq_page_table *t, int64_t total, int64_t max_new, bool tree)
 {
     const int64_t all = t->num_seqs * t->max_len;
@@ -555,8 +585,14 @@ tq_status tq_page_table_update(const tq_cache *c, const tq_page_table *t, const 
     if (free_capacity < 1 || free_capacity > INT32_MAX) return TQ_ERR_SHAPE;
     if (!aligned_to(4, t->pages, t->seq_lens, lens, new_tokens, lens_out, starts, free_pages, free_count, free_count_out))
         return TQ_ERR_ALIGN;
-    // written before the last of these is read
-    if (starts && (starts == lens || starts == new_tokens || starts == lens_out || starts == t->seq_lens)) return TQ_ERR_SHAPE;
+    const int64_t S = t->num_seqs;
+    const Span pages = table_span(c, t), old = span(t->seq_lens, S), want = span(lens, S), out = span(lens_out, S),
+               stack = span(free_pages, free_capacity), left = span(free_count_out, 1);
+    // the starts are written before the last of the others is read, pages go both ways between the table and the stack
+    if (!apart(span(starts, S + 1), {pages, old, want, span(new_tokens, S), out, stack, span(free_count, 1), left})) return TQ_ERR_SHAPE;
+    if (!apart(stack, {pages, old, want, span(new_tokens, S), out, span(free_count, 1), left}) || !apart(out, {pages, left})) return TQ_ERR_SHAPE;
+    // a place of its own or the very same one
+    if ((lens_out != lens && !apart(out, {want})) || (lens_out != t->seq_lens && !apart(out, {old}))) return TQ_ERR_SHAPE;
     tq::PagedUpdate u{};
     u.pages = const_cast<int32_t *>(t->pages);
     u.lens = t->seq_lens;
@@ -589,8 +625,13 @@ tq_status tq_paged_layout(const tq_cache *c, const tq_page_table *t, const int32
     const int64_t most = max_new < total ? max_new : total;
     if (masks && (mask_words < 1 || mask_words < (most + 31) / 32)) return TQ_ERR_SHAPE;
     if (!aligned_to(4, t->pages, t->seq_lens, starts, parents, positions, masks) || !aligned_to(8, slots)) return TQ_ERR_ALIGN;
-    if (positions && (positions == parents || positions == masks)) return TQ_ERR_SHAPE;
-    if (masks && masks == parents) return TQ_ERR_SHAPE;  // (a token reads the parents of others)
+    // (a token reads the parents of others)
+    const Span pages = table_span(c, t), lens = span(t->seq_lens, t->num_seqs), first = span(starts, t->num_seqs + (int64_t)1),
+               up = span(parents, total), pos = span(positions, total), slot = span(slots, total),
+               seen = span(masks, mask_words, total, mask_words);
+    if (!apart(pos, {pages, lens, first, up, slot, seen}) || !apart(slot, {pages, lens, first, up, seen}) ||
+        !apart(seen, {pages, lens, first, up}))
+        return TQ_ERR_SHAPE;
     if (total == 0 || (!positions && !slots && !masks)) return TQ_OK;
     const tq::PagedView pv = paged_view(c, t, starts, total);
     if (!pv.err) return TQ_ERR_CUDA;
@@ -605,8 +646,10 @@ tq_status tq_paged_keep(const tq_cache *c, const tq_page_table *t, const int32_t
     if (st != TQ_OK) return st;
     if (!path || !kept || !lens_out) return TQ_ERR_NULL;
     if (!aligned_to(4, t->pages, t->seq_lens, starts, path, kept, lens_out)) return TQ_ERR_ALIGN;
-    if (lens_out == t->seq_lens || lens_out == kept) return TQ_ERR_SHAPE;  // (read by every CTA of a sequence, written by one)
     if (max_new < 1 || path_stride < max_new) return TQ_ERR_SHAPE;
+    const int64_t S = t->num_seqs;  // (read by every CTA of a sequence, written by one)
+    if (!apart(span(lens_out, S), {table_span(c, t), span(t->seq_lens, S), span(starts, S + 1), span(kept, S), span(path, max_new, S, path_stride)}))
+        return TQ_ERR_SHAPE;
     if ((int64_t)t->num_seqs * c->num_kv_heads > (int64_t(1) << 30)) return TQ_ERR_SHAPE;
     const tq::PagedView pv = paged_view(c, t, starts, total);
     if (!pv.err) return TQ_ERR_CUDA;
@@ -628,7 +671,14 @@ tq_status tq_verify_drafts(const int32_t *starts, int32_t num_seqs, int64_t tota
     const uintptr_t size = dt == TQ_F32 ? 4 : 2;
     if (!aligned_to(size, static_cast<const char *>(target), static_cast<const char *>(draft))) return TQ_ERR_ALIGN;
     if (!aligned_to(4, starts, parents, tokens, uniforms, last, path, kept, next)) return TQ_ERR_ALIGN;
-    if (kept == next || path == kept || path == next) return TQ_ERR_SHAPE;
+    const Span way = span(path, max_new, num_seqs, path_stride), many = span(kept, num_seqs), last_one = span(next, num_seqs);
+    if (!apart(way, {many, last_one}) || !apart(many, {last_one})) return TQ_ERR_SHAPE;
+    const int64_t bytes = (int64_t)size;  // (sequences read and write in no order)
+    for (const Span &x : {way, many, last_one})
+        if (!apart(x, {span(starts, num_seqs + (int64_t)1), span(parents, total), span(tokens, total), span(uniforms, total), span(last, num_seqs),
+                       span(static_cast<const char *>(target), vocab * bytes, total, target_stride * bytes),
+                       span(static_cast<const char *>(draft), vocab * bytes, total, draft_stride * bytes)}))
+            return TQ_ERR_SHAPE;
     tq::VerifyCall v{starts, parents, tokens, total, max_new, vocab, num_seqs, target, draft, target_stride, draft_stride,
                      uniforms, last, path, kept, next, path_stride, dt == TQ_F32, tq::device_error_word()};
     if (!v.err) return TQ_ERR_CUDA;
@@ -666,6 +716,7 @@ tq_status tq_rotary(const int32_t *positions, int64_t tokens, int32_t head_dim, 
         if (a.x == a.out && (st[0] != st[2] || st[1] != st[3])) return TQ_ERR_SHAPE;
         r.t[i] = tq::RotaryTensor{a.x, a.out, st[0], st[1], st[2], st[3], a.heads};
     }
+    if (q && k && (q->out == k->x || q->out == k->out || k->out == q->x)) return TQ_ERR_SHAPE;  // one tensor upon the other
     r.pos = positions;
     r.freqs = freqs;
     r.tokens = tokens;

@@ -238,6 +238,66 @@ def test_calls_are_set_up_on_every_device(tqlib, fake, d, kb, vb):  # noqa: F811
         assert set(got.values()) == {0}, (dev, got)
 
 
+def test_outputs_upon_other_tensors_are_refused(tqlib, fake):  # noqa: F811
+    """Whole tensors or their ends: where a call would read what it has written, nothing is launched; tensors side by
+    side, and those that may be the same, are taken."""
+    pool = _struct(tqlib, batch=12)
+    S, total, most = 3, 40, 33
+    table = _table(tqlib, pages=20 * P, seq_lens=21 * P)  # 4 pages a row
+    fake.fake_set_device(0)
+
+    def update(lens=P, new=2 * P, out=3 * P, starts=4 * P, stack=5 * P, count=6 * P, count_out=7 * P):
+        return fake.tq_page_table_update(REF(pool), REF(table), lens, new, out, starts, stack, 12, count, count_out, None)
+
+    for kw in ({}, dict(out=P), dict(out=21 * P), dict(count_out=6 * P), dict(starts=2 * P + 4 * S), dict(starts=P - 4 * (S + 1)),
+               dict(out=P + 4 * S), dict(stack=20 * P + 48), dict(out=2 * P), dict(lens=21 * P, out=21 * P)):
+        assert update(**kw) == 0, kw
+    ends = {P: S, 2 * P: S, 3 * P: S, 5 * P: 12, 6 * P: 1, 7 * P: 1, 20 * P: 12, 21 * P: S}  # words of each
+    for at, n in ends.items():
+        assert update(starts=at) == SHAPE and update(starts=at + 4 * n - 4) == SHAPE and update(starts=at - 4 * S) == SHAPE, at
+        if at not in (5 * P,):
+            assert update(stack=at) == SHAPE and update(stack=at - 44) == SHAPE and update(stack=at + 4 * n - 4) == SHAPE, at
+    assert update(out=P + 4) == SHAPE and update(out=21 * P - 8) == SHAPE  # partly the lengths
+    assert update(out=20 * P + 44) == SHAPE and update(out=7 * P) == SHAPE
+
+    def layout(starts=5 * P, parents=P, pos=2 * P, slots=3 * P, masks=4 * P):
+        return fake.tq_paged_layout(REF(pool), REF(table), starts, total, parents, most, pos, slots, masks, 2, None)
+
+    for kw in ({}, dict(pos=P + 4 * total), dict(slots=2 * P + 4 * total), dict(masks=P - 8 * total), dict(starts=3 * P + 8 * total)):
+        assert layout(**kw) == 0, kw
+    for at, n in {P: total, 5 * P: S + 1, 20 * P: 12, 21 * P: S}.items():
+        for name, size in (("pos", 4 * total), ("slots", 8 * total), ("masks", 8 * total)):
+            for x in (at, (at + 4 * n - 8) // 8 * 8, at - size + 8):
+                assert layout(**{name: x}) == SHAPE, (name, at)
+    assert layout(pos=3 * P + 8) == SHAPE and layout(masks=3 * P + 8 * total - 8) == SHAPE and layout(pos=4 * P + 8 * total - 4) == SHAPE
+
+    def keep(path=P, kept=2 * P, out=3 * P):
+        return fake.tq_paged_keep(REF(pool), REF(table), 5 * P, total, 8, path, 10, kept, out, None)
+
+    for kw in ({}, dict(out=2 * P + 4 * S), dict(out=P + 4 * 28), dict(kept=3 * P + 4 * S)):
+        assert keep(**kw) == 0, kw
+    for x in (P, P + 4 * 27, 2 * P + 8, 2 * P - 8, 5 * P + 12, 20 * P + 44, 21 * P, 21 * P + 8):
+        assert keep(out=x) == SHAPE, hex(x)
+
+    def verify(path=8 * P, kept=9 * P, nxt=10 * P, draft=5 * P):
+        return fake.tq_verify_drafts(P, S, total, 12, 2 * P, 3 * P, 100, 1, 4 * P, 120, draft, 100, 6 * P, 7 * P, path, 12, kept, nxt, None)
+
+    last_row = 4 * (39 * 120 + 99)
+    for kw in ({}, dict(kept=8 * P + 4 * 36, nxt=8 * P + 4 * 39), dict(path=4 * P + last_row + 4), dict(nxt=2 * P + 4 * total), dict(draft=None)):
+        assert verify(**kw) == 0, kw
+    for name, size in (("path", 4 * 36), ("kept", 12), ("nxt", 12)):
+        for at, n in {P: 16, 2 * P: 160, 3 * P: 160, 4 * P: last_row + 4, 5 * P: 4 * 40 * 100, 6 * P: 160, 7 * P: 12}.items():
+            assert verify(**{name: at}) == SHAPE and verify(**{name: at + n - 4}) == SHAPE and verify(**{name: at - size + 4}) == SHAPE, (name, at)
+    assert verify(kept=10 * P + 8) == SHAPE and verify(path=9 * P - 4) == SHAPE and verify(nxt=8 * P + 4 * 35) == SHAPE
+
+    def rotary(x=P, out=2 * P, x2=3 * P, out2=4 * P):
+        q, k = (tqlib._RotaryStruct(a, b, _two(512, 128), _two(512, 128), 4, 0) for a, b in ((x, out), (x2, out2)))
+        return fake.tq_rotary(5 * P, 5, 128, 128, 0, 6 * P, 1.0, 0, REF(q), REF(k), None)
+
+    assert rotary() == 0 and rotary(out=P, out2=3 * P) == 0
+    assert rotary(out=3 * P) == SHAPE and rotary(out2=P) == SHAPE and rotary(out2=2 * P) == SHAPE
+
+
 # ------------------------------------------------------------------ what the kernels rest on
 @pytest.mark.parametrize("seed", range(20))
 def test_what_is_left_after_rejections_has_one_factor(seed):
