@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_drafts_gpu import check_verify
+from test_drafts_gpu import TableModel, check_verify, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,71 @@ def test_verify_rejects_and_accepts_in_turn(cuda, wide, draft, dtype):
     kept = check_verify(cuda, [1 + levels * (wide + 1), 33, 65, 2], 500, draft, dtype, seed=wide, edit=edit)
     assert int(kept[0]) == 1 + levels
     assert cuda.tq_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_of_a_large_vocabulary(cuda, draft, dtype):
+    check_verify(cuda, [5, 1, 9, 0, 2], 131072, draft, dtype, seed=3)
+    check_verify(cuda, [4, 7], 150001, draft, dtype, seed=4, pad=1, stride=5)  # rows at odd offsets
+    assert cuda.tq_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("tokens,d,rot,QH,H", [(4097, 128, 128, 5, 1), (4098, 128, 64, 8, 2), (4099, 64, 64, 3, 3), (5000, 256, 192, 2, 1),
+                                               (4097, 512, 512, 1, 1), (4097, 128, 36, 3, 1)])
+def test_rotary_of_many_tokens(cuda, tokens, d, rot, QH, H, interleaved, dtype):
+    """Several tokens a block, the last block's short; positions below 0 among them.  Bounds as in test_rotary: 6 steps of
+    2^-24 of (|a| + |b|) scale, then one rounding of the type."""
+    assert tokens >= 16 * torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator(device="cuda").manual_seed(tokens + rot)
+    x = torch.randn(tokens, QH + H, d, generator=g, device="cuda").to(dtype)
+    q, k = x[:, :QH], x[:, QH:]
+    pos = torch.randint(0, 1 << 20, (tokens,), generator=g, device="cuda", dtype=torch.int32)
+    pos[[0, 6, tokens // 2, tokens - 2]] = -1
+    live = pos >= 0
+    w = dev(cuda.tq_rotary_frequencies(rot)[0], torch.float64)
+    outs = [torch.full(t.shape, 7.0, dtype=dtype, device="cuda") for t in (q, k)]
+    cuda.tq_rotary(pos, w, q, k, interleaved=interleaved, scale=0.75, q_out=outs[0], k_out=outs[1])
+    t = pos.double()[:, None] * w
+    c, s = torch.cos(t)[:, None] * 0.75, torch.sin(t)[:, None] * 0.75
+    i = (slice(0, rot, 2), slice(1, rot, 2)) if interleaved else (slice(0, rot // 2), slice(rot // 2, rot))
+    for a, b in ((q, outs[0]), (k, outs[1])):
+        y, want = a.double(), a.double()
+        size = torch.zeros_like(y)
+        want[..., i[0]], want[..., i[1]] = y[..., i[0]] * c - y[..., i[1]] * s, y[..., i[0]] * s + y[..., i[1]] * c
+        size[..., i[0]] = size[..., i[1]] = (y[..., i[0]].abs() + y[..., i[1]].abs()) * 0.75
+        bound = torch.finfo(dtype).eps / 2 * want.abs() + 6 * 2.0 ** -24 * size * (1 + torch.finfo(dtype).eps)
+        assert bool(((b.double() - want).abs() <= bound)[live].all())
+        assert bool((b[~live] == 7).all())
+    # in place, both in one tensor
+    y = x.clone()
+    cuda.tq_rotary(pos, w, y[:, :QH], y[:, QH:], interleaved=interleaved, scale=0.75, q_out=y[:, :QH], k_out=y[:, QH:])
+    assert torch.equal(y[live], torch.cat(outs, 1)[live]) and torch.equal(y[~live], x[~live])
+
+
+@pytest.mark.parametrize("seqs,moving", [(1, 1), (5, 3), (40, 40), (1030, 7)])
+def test_long_moves_of_pages(cuda, seqs, moving):
+    """Sequences that gain or give back up to a thousand pages in a call, while others grow by a row."""
+    rng = np.random.default_rng(seqs)
+    page, width = 16, 1100
+    pages = moving * 1000 + seqs + 50
+    m = TableModel(rng, seqs, width, page, pages)
+    pool = cuda.Cache(pages, 1, 64, page, k_bits=2, v_bits=2)
+    table = cuda.PageTable(dev(m.table), dev(m.lens), width * page)
+    free, count = dev(m.free + [-7] * 3), dev([len(m.free)])
+    long = rng.choice(seqs, moving, replace=False)
+    for step, most in enumerate((1000, 0, 1000, 257, 1000, 258, 513, 1, 1000, 0)):
+        want = [min(n + 1, 16) if s not in long else n for s, n in enumerate(m.lens)]
+        for s in long:
+            want[s] = most * page - (int(rng.integers(0, page)) if most else 0) if (s + step) % 3 or step < 2 else want[s]
+        assert m.update(want)
+        cuda.tq_page_table_update(pool, table, dev(want), free, count)
+        assert cuda.tq_device_error() == 0 and table.seq_lens.tolist() == want
+        assert int(count) == len(m.free) and free.tolist()[:len(m.free)] == [int(x) for x in m.free]
+        at = table.pages.cpu().numpy()
+        for s, n in enumerate(m.lens):
+            k = -(-n // page)
+            assert np.array_equal(at[s, :k], m.table[s, :k]), (step, s)
+    assert free.tolist()[pages:] == [-7] * 3
