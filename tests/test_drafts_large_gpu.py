@@ -3,7 +3,9 @@ import numpy as np
 import pytest
 import torch
 
-from test_drafts_gpu import TableModel, check_verify, dev
+from pagedtest import Batch
+from test_drafts_gpu import TableModel, ancestors, check_verify, dev, pack, random_parents, tree_masks
+from test_tree_ranges_gpu import check_numbers
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +105,72 @@ def test_long_moves_of_pages(cuda, seqs, moving):
             k = -(-n // page)
             assert np.array_equal(at[s, :k], m.table[s, :k]), (step, s)
     assert free.tolist()[pages:] == [-7] * 3
+
+
+@pytest.mark.parametrize("seqs,most,big", [(1023, 3, 3), (1024, 3, 3), (2500, 2, 40), (3, 40, 1500), (6, 9, 3100)])
+def test_layout_of_many_sequences_and_large_trees(cuda, seqs, most, big):
+    """More sequences than starts stand on the chip, trees of more nodes than parents do."""
+    rng = np.random.default_rng(seqs)
+    new = [int(x) for x in rng.integers(0, most + 1, seqs)]
+    new[seqs // 2] = big
+    lens = [n + int(x) for n, x in zip(new, rng.integers(0, 40, seqs))]
+    page, width = 16, -(-max(lens) // 16)
+    table = rng.permutation(seqs * width).reshape(seqs, width)
+    pool = cuda.Cache(seqs * width, 1, 64, page, k_bits=2, v_bits=2)
+    pages = cuda.PageTable(dev(table), dev(lens), max(lens))
+    parents = [random_parents(rng, n, wide=3) for n in new]
+    starts, total = np.cumsum([0] + new), sum(new)
+    pos, slots, masks = cuda.tq_paged_layout(pool, pages, dev(starts), total, parents=dev([x for t in parents for x in t]), max_new=big)
+    rows, line, _ = cuda.tq_paged_layout(pool, pages, dev(starts), total)
+    assert cuda.tq_device_error() == 0 and torch.equal(line, slots)
+    want_pos, want_row, want_slot, want_mask = [], [], [], []
+    for s, n in enumerate(new):
+        for i, up in enumerate(ancestors(parents[s])):
+            row = lens[s] - n + i
+            want_pos.append(lens[s] - n + len(up) - 1)
+            want_row.append(row)
+            want_slot.append(int(table[s, row // page]) * page + row % page)
+            seen = np.zeros((1, big), bool)
+            seen[0, up] = True
+            want_mask.append(pack(seen, -(-big // 32))[0])
+    assert pos.tolist() == want_pos and rows.tolist() == want_row and slots.tolist() == want_slot
+    assert np.array_equal(masks.cpu().numpy(), np.stack(want_mask))
+
+
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("shape", ["chain", "star", "any"])
+def test_verify_of_the_largest_trees(cuda, shape, draft):
+    def edit(p, r, tokens, parents, u, last, starts):
+        if shape == "any":
+            return
+        for s, t in enumerate(parents):
+            for i in range(1, len(t)):
+                t[i] = i - 1 if shape == "chain" else 0
+                if shape == "chain":
+                    u[starts[s] + i] = 0.0  # (accepted)
+
+    kept = check_verify(cuda, [1024, 3, 1000], 300, draft, seed=8, edit=edit)
+    assert shape != "chain" or kept.tolist()[0] > 30
+    assert cuda.tq_device_error() == 0
+
+
+@pytest.mark.parametrize("d,kb,vb,H,G,new", [(128, 8, 3, 2, 8, 6), (64, 4, 3, 1, 48, 5), (256, 8, 4, 4, 5, 7), (128, 4, 4, 1, 128, 1)])
+def test_trees_of_many_sequences(cuda, d, kb, vb, H, G, new):
+    """Seventy sequences on the kernel whose rows are dequantised on the chip, odd groups of q-heads, queries within a
+    wider tensor, masks with more words than the tokens need."""
+    rng = np.random.default_rng(G)
+    lens = [int(x) for x in rng.integers(0, 300, 70)]
+    b = Batch(lens, [min(n, int(rng.integers(0, new + 1))) for n in lens], H=H, d=d, kb=kb, vb=vb, page=48, seed=3, width=-(-4096 // 48))
+    b.new[lens.index(max(lens))] = new
+    b.starts = np.concatenate([[0], np.cumsum(b.new)]).astype(np.int32)
+    b.total = int(b.starts[-1])
+    seen = tree_masks(b, "any")
+    masks = np.concatenate([pack(np.pad(m, ((0, 0), (0, 96 - m.shape[1])), constant_values=True), 3) for m in seen])
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    q = b.queries(H * G)
+    wide = torch.full((b.total, H * G + 3, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 2:-1] = q.cuda()
+    out = cuda.tq_paged_tree_attention(pool, b.pages(cuda, max_len=4096), b.dev(b.starts), wide[:, 2:-1], dev(masks), new)
+    assert cuda.tq_device_error() == 0
+    check_numbers(b, pool, q, out, seen)
