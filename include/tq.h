@@ -450,7 +450,9 @@ TQ_API tq_status tq_paged_tree_attention(const tq_cache *pool, const tq_page_tab
  * the pool has fewer pages than are lacking, or the stack no room for those given back
  * or a count out of range (TQ_DEVICE_ERR_FULL), nothing changes: lens_out becomes the
  * old lengths, free_count_out the old count, starts all 0.  Page numbers given
- * back that are outside the pool are recorded (TQ_DEVICE_ERR_PAGE) and pushed.
+ * back that are outside the pool are recorded (TQ_DEVICE_ERR_PAGE) and pushed.  Owners
+ * of a page are not counted: one that two sequences share goes to the stack once for each
+ * that gives it back, so those tables are the caller's to keep.
  */
 TQ_API tq_status tq_page_table_update(const tq_cache *pool, const tq_page_table *table, const int32_t *lens,
                                       const int32_t *new_tokens, int32_t *lens_out, int32_t *starts, int32_t *free_pages,
@@ -513,7 +515,9 @@ TQ_API tq_status tq_paged_keep(const tq_cache *pool, const tq_page_table *table,
  * crossed out: M -= p(x), p(x) = 0.  When no child is accepted, the next token is the
  * first v where the running sum of what is left, max(p - C r, 0) or p without the
  * crossed-out tokens, is above last[s] times its sum.  The tokens then follow the
- * target's distribution.
+ * target's distribution, where rows sum to 1: tests compare what is left with M = 1 at
+ * first, whatever a row sums to, and only the last draw goes by the real sum.  Rows rounded to
+ * bf16 miss 1 by up to 2^-8, and the distribution is off by as much.
  *  target, draft   device fp32 or bf16 (dtype), rows of `vocab` probabilities,
  *            target_stride and draft_stride elements apart, aligned to their elements.
  *            Values that are negative or not finite count as 0.
@@ -551,8 +555,9 @@ typedef struct tq_rotary_tensor {
  *   scale * (a cos t - b sin t, a sin t + b cos t),  t = positions[token] * freqs[pair],
  * the pairs being elements (2 i, 2 i + 1) when interleaved, else (i, i + rot_dim / 2);
  * the elements from rot_dim on are copied.  One call turns queries and keys (either
- * may be NULL).  A token whose position is negative is left as it was.  Angles are
- * reduced in 64 bits, the rest is fp32, rounded once.
+ * may be NULL).  The output rows of a token whose position is negative (padding of
+ * tq_paged_layout) are not written: in place they keep the vectors, in a tensor of their own
+ * whatever it held.  Angles are reduced in 64 bits, the rest is fp32, rounded once.
  *  positions device int32 [tokens] (tq_paged_layout's); freqs device binary64 [rot_dim / 2].
  *  head_dim  one of the codec's; rot_dim even, 2 .. head_dim.
  */

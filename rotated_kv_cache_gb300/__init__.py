@@ -832,8 +832,9 @@ def _rotary_tensor(x: torch.Tensor, out: torch.Tensor | None, tokens: int, d: in
 def tq_rotary(positions: torch.Tensor, freqs: torch.Tensor, q: torch.Tensor | None, k: torch.Tensor | None = None,
               interleaved: bool = False, scale: float = 1.0, q_out: torch.Tensor | None = None,
               k_out: torch.Tensor | None = None, stream=None):
-    """(q, k) turned by positions (int32 [tokens], below 0: left as it was) times freqs (float64 [rot_dim / 2]); q and k bf16
-    or fp32 [tokens][heads][d], any token and head strides, either None; q_out=q turns in place."""
+    """(q, k) turned by positions (int32 [tokens]) times freqs (float64 [rot_dim / 2]); q and k bf16 or fp32
+    [tokens][heads][d], any token and head strides, either None; q_out=q turns in place.  Rows of a position below 0 are
+    not written: a new output holds nothing there, a given one what it held."""
     some = k if q is None else q
     if some is None:
         raise ValueError("give q or k")

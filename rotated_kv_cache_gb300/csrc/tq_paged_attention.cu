@@ -280,21 +280,32 @@ constexpr int64_t kWideWork = int64_t(1) << 22;  // rows x kv-heads x columns, b
 // Measured (us), 8 kv-heads unless said, 8-bit keys, 3- or 4-bit values:
 //   head_dim  sequences x rows  columns   block   split   wide
 //      128       8 x 16384         16      92.6    89.2
-//                                  24      95.5   158.8
-//               32 x 28672         64     637    1950
+//                                  24      92.7   158.8
+//               32 x 28672         64     624    1950
 //                1 x 512           64      16.8    13.7
-//                1 x 2048          64      18.9    19.0
-//               16 x 4352         384     222             298
+//                1 x 2048          64      18.5    19.0
+//               16 x 4352         384     218             298
 //                                 512     292             302
 //                                1024     558 (4-bit keys) 427
-// (16 ragged sequences of 500 to 8192 rows, 320 to 512 columns, 4-bit keys: 320 and 264.)
-//       64       4 x 8192          24      30.0    32.2
-//               16 x 4352         384     175             188
+//       64       4 x 8192          24      29.4    32.2
+//               16 x 4352         384     174             188
 //                                 512     231             187
-//      256       2 x 16384         12      42.0    49.3  (4 kv-heads, as below)
-//                                 128      57.1   278.5
+//      256       2 x 16384         12      41.3    49.3  (4 kv-heads, as below)
+//                                 128      56.4   278.5
 //                2 x 512           32      19.0    14.8
 //                2 x 2048          32      22.4    22.5
+// Ragged sequences, with the limit on the largest one's columns (4-bit keys; with 8-bit ones the wide kernel
+// takes 5 to 25 us more):
+//      128      16 x 500..8192   80..128  100             310
+//                               200..320  197             233
+//                               240..384  213             234
+//                                 8..384  140             241
+//                               320..512  320             262
+//                8 x 500..32768 240..384  295             360
+//               32 x 100..8192   32..384  400             449
+//       64      16 x 500..8192  160..256  135             131
+//                               240..384  157             166
+//                               320..512  237             185
 // Keys or values of other widths are cut by run-time shifts, straight from memory:
 //      128       4 x 8192          32      60.1    56.7
 //                                  64      61.3    95.4

@@ -31,9 +31,10 @@
 // out of tensor memory every nFlush tiles and summed in fp32.
 //
 // Measured: 32 sequences of 28672 rows, 8 kv-heads, head_dim 128, 8-bit keys and
-// 3-bit values, 8 new tokens of 64 q-heads: 637 us (2.3 TB/s of packed rows; the
-// split kernel 1950), with 16 tokens 760 (2300 by expanded rows).  A tile of 128
-// rows takes 3100 cycles, of which the tensor pipe works 1560 (three products a
+// 3-bit values, 8 new tokens of 64 q-heads: 624 us (2.4 TB/s of packed rows; the
+// split kernel 1950), with 16 tokens 749 (2300 by expanded rows); with one group of
+// four beyond |z| = 896 in every row 909 and 956 (head_dim 64 and 256: 9 to 10 %
+// more).  A tile of 128 rows takes 3100 cycles, of which the tensor pipe works 1560 (three products a
 // row, lanes of 64 columns idle); the rows' 16 warps and the softmax's four share
 // the issue slots, and their chains of dependent instructions take the time.
 // Steps: loads kept apart from arithmetic on them and rows by bulk copies instead
