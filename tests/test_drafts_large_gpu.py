@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from pagedtest import Batch
+from pagedtest import ATOL, RTOL, Batch, dequantised
 from test_drafts_gpu import TableModel, ancestors, check_verify, dev, pack, random_parents, tree_masks
 from test_tree_ranges_gpu import check_numbers
 
@@ -174,3 +174,34 @@ def test_trees_of_many_sequences(cuda, d, kb, vb, H, G, new):
     out = cuda.tq_paged_tree_attention(pool, b.pages(cuda, max_len=4096), b.dev(b.starts), wide[:, 2:-1], dev(masks), new)
     assert cuda.tq_device_error() == 0
     check_numbers(b, pool, q, out, seen)
+
+
+def test_large_trees_that_find_no_room_for_their_rows(cuda):
+    """Trees of 512 columns over three sequences whose expanded rows pass what the workspace has for them (8 GiB): the last
+    one's go to the kernel without.  One prefix of 512 rows, repeated; the plain implementation counts each row."""
+    S, H, G, d, P, n, new = 3, 8, 8, 128, 128, 1 << 19, 64
+    b = Batch([512], [0], H=H, d=d, kb=8, vb=3, page=P, spare=0, seed=6)
+    pool = b.pool(cuda)
+    b.fill(cuda, pool)
+    lens = [n - 41 * s for s in range(S)]
+    pages = cuda.PageTable(b.dev(np.tile(b.table[0, :4], (S, n // 512)).astype(np.int32)), b.dev(np.array(lens, np.int32)), n)
+    need = cuda.tq_paged_tree_attention_workspace_bytes(pool, pages, H * G, S * new, new)
+    assert (8 << 30) < need < S * n * H * 6 * d
+    rng = np.random.default_rng(4)
+    masks = rng.integers(-(1 << 31), 1 << 31, (S * new, 2)).astype(np.int32)
+    q = b.queries(H * G, total=S * new)
+    out = cuda.tq_paged_tree_attention(pool, pages, dev(np.arange(0, S * new + 1, new)), q.cuda(), dev(masks), new).cpu().double()
+    assert cuda.tq_device_error() == 0
+    torch.cuda.empty_cache()
+    k, v = (torch.from_numpy(x).double() for x in dequantised(pool, b.table[0], 512))
+    for s in range(S):
+        before = lens[s] - new
+        for i in (0, 31, new - 1):
+            times = torch.tensor([(before - r + 511) // 512 for r in range(512)], dtype=torch.float64)
+            for j in range(new):
+                if masks[s * new + i, j // 32] >> (j % 32) & 1:
+                    times[(before + j) % 512] += 1
+            x = torch.einsum("hgd,hnd->hgn", q[s * new + i].double().view(H, G, d), k) * d ** -0.5
+            p = torch.exp(x - x.amax(-1, keepdim=True)) * times
+            want = torch.einsum("hgn,hnd->hgd", p / p.sum(-1, keepdim=True), v).reshape(H * G, d)
+            assert float(((out[s * new + i] - want).abs() - RTOL * want.abs()).max()) <= ATOL, (s, i)
